@@ -22,7 +22,8 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = _build.LIB
 
 MOE_OK, MOE_ERR_INVALID, MOE_ERR_CAPACITY, MOE_ERR_CUDA, MOE_ERR_STATE = range(5)
-MOE_BF16, MOE_F32 = 0, 1
+MOE_BF16, MOE_F32, MOE_E4M3 = 0, 1, 2
+MOE_ACT_SILU, MOE_ACT_GELU = 0, 1
 MOE_SCORE_SOFTMAX, MOE_SCORE_SIGMOID = 0, 1
 MOE_DEVERR_BAD_EXPERT, MOE_DEVERR_DUP_EXPERT, MOE_DEVERR_NONFINITE, MOE_DEVERR_TIMEOUT = 1, 2, 4, 8
 MOE_DEVERR_INTERNAL, MOE_DEVERR_BAD_LAYOUT = 16, 32
@@ -34,9 +35,11 @@ EXPORTS = ("moe_status_string", "moe_workspace_bytes", "moe_handle_create", "moe
            "moe_scale_rows_bwd", "moe_read_device_status", "moe_clear_device_status",
            "moe_dispatch_layout_static", "moe_route_bwd", "moe_expand", "moe_combine_partial",
            "moe_combine_reduce", "moe_w2_absorbed", "moe_dispatch_layout_launches",
-           "moe_dispatch_bwd_route", "moe_dispatch_bwd_route_launches", "moe_set_wait_limit")
+           "moe_dispatch_bwd_route", "moe_dispatch_bwd_route_launches", "moe_set_wait_limit",
+           "moe_act_rows", "moe_act_rows_bwd", "moe_layer_workspace_bytes", "moe_layer")
 MOE_LAYOUT_STATIC_COUNTERS = 65536
 MOE_LAYOUT_TILE_TOKENS = 512
+MOE_LAYER_MAX_TOKENS, MOE_LAYER_MAX_SHARED, MOE_LAYER_MAX_WIDTH = 128, 4, 65536
 
 
 class MoeConfig(ctypes.Structure):
@@ -53,6 +56,12 @@ class MoeLayout(ctypes.Structure):
         "cnt_e", "off_e", "cnt_send_r", "off_send_r", "cnt_recv_r", "off_recv_r", "pos",
         "recv_token", "recv_k", "send_token", "send_row_of", "recv_send_row", "S")] + [
         ("num_tokens", ctypes.c_int32), ("pad_align", ctypes.c_int32)]
+
+
+class MoeLayerArgs(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in (
+        "d_x", "d_logits", "d_bias", "d_live", "d_w13", "d_w2", "d_s13", "d_s2", "d_out", "d_idx",
+        "d_w")] + [(n, ctypes.c_int32) for n in ("H", "I", "num_shared", "weight_dtype", "act")]
 
 
 class MoeError(RuntimeError):
@@ -99,6 +108,10 @@ def lib():
             "moe_dispatch_bwd_route": ([P, P, i32, i32, P, P, P, P, P, P], st),
             "moe_dispatch_bwd_route_launches": ([P, P], st),
             "moe_set_wait_limit": ([P, ctypes.c_uint64], st),
+            "moe_act_rows": ([P, P, i32, i32, i32, P, ctypes.c_double, P, P, P], st),
+            "moe_act_rows_bwd": ([P, P, P, i32, i32, i32, P, ctypes.c_double, P, P, P, P], st),
+            "moe_layer_workspace_bytes": ([P, i32, i32, i32], sz),
+            "moe_layer": ([P, P, i32, P, sz, P], st),
         }
         for name, (args, res) in sigs.items():
             f = getattr(L, name)
@@ -397,6 +410,85 @@ def moe_w2_absorbed(h, hrows, recv_w, w2, y, stream=None):
           _stream(stream, d))
 
 
+def _act(act):
+    return {"silu": MOE_ACT_SILU, "gelu": MOE_ACT_GELU}[act] if isinstance(act, str) else int(act)
+
+
+def moe_act_rows(h, gu, recv_w, hs, act="silu", p=0.0, rng=None, stream=None):
+    """hs = recv_w * dropout(act(gate) * up) per receive row, gu = [gate, up];
+    recv_w None: 1.  rng: int64 [2] CUDA tensor (seed, offset), needed if p > 0."""
+    I = hs.shape[1]
+    d = h.device
+    _req(gu, hs.dtype, (h.recv_rows, 2 * I), "gu", d)
+    _req(recv_w, torch.float32, (h.recv_rows,), "recv_w", d)
+    _req(hs, None, (h.recv_rows, I), "hs", d)
+    _req(rng, torch.int64, (2,), "rng", d)
+    _call(h, "moe_act_rows", h.ptr, _ptr(gu), I, _row_dtype(hs), _act(act), _ptr(recv_w), float(p),
+          _ptr(rng), _ptr(hs), _stream(stream, d))
+
+
+def moe_act_rows_bwd(h, ghs, gu, recv_w, ggu, gw=None, act="silu", p=0.0, rng=None, stream=None):
+    """Backward of moe_act_rows: ggu (may be gu) and, with recv_w, the score
+    gradient gw [T, K] (None: not computed)."""
+    I = ghs.shape[1]
+    d = h.device
+    _req(ghs, None, (h.recv_rows, I), "ghs", d)
+    _req(gu, ghs.dtype, (h.recv_rows, 2 * I), "gu", d)
+    _req(recv_w, torch.float32, (h.recv_rows,), "recv_w", d)
+    _req(ggu, ghs.dtype, (h.recv_rows, 2 * I), "ggu", d)
+    _req(gw, torch.float32, (h.T, h.K), "gw", d)
+    _req(rng, torch.int64, (2,), "rng", d)
+    _call(h, "moe_act_rows_bwd", h.ptr, _ptr(ghs), _ptr(gu), I, _row_dtype(ghs), _act(act),
+          _ptr(recv_w), float(p), _ptr(rng), _ptr(ggu), _ptr(gw), _stream(stream, d))
+
+
+def moe_layer_workspace_bytes(cfg, H, I, num_shared=0):
+    return lib().moe_layer_workspace_bytes(ctypes.byref(cfg), H, I, num_shared)
+
+
+def layer_workspace(h, H, I, num_shared=0):
+    """Workspace tensor for moe_layer on this handle (one per overlapping call)."""
+    n = moe_layer_workspace_bytes(h.cfg, H, I, num_shared)
+    if n == 0:
+        raise MoeError("moe_layer_workspace_bytes", MOE_ERR_INVALID)
+    return torch.empty(n, dtype=torch.uint8, device=h.device)
+
+
+def moe_layer(h, x, logits, w13, w2, out, idx, w, workspace, bias=None, s13=None, s2=None,
+              live=None, act="silu", num_shared=0, stream=None):
+    """A whole MoE layer for a few tokens: out [T, H], idx and w [T, K] (outputs;
+    inputs when logits is None).  Weights bf16, or float8_e4m3fn with the fp32
+    scales s13 and s2 of their 128 x 128 blocks; the last num_shared experts
+    are shared.  live: int32 [1] CUDA tensor, the tokens to compute."""
+    T, H = x.shape
+    I = w2.shape[2]
+    d = h.device
+    n = h.E + num_shared
+    wt = w13.dtype
+    if wt == torch.bfloat16:
+        wd = MOE_BF16
+    elif wt == torch.float8_e4m3fn:
+        wd = MOE_E4M3
+    else:
+        raise TypeError("weights must be bfloat16 or float8_e4m3fn, got %s" % wt)
+    _req(x, torch.bfloat16, (T, H), "x", d)
+    _req(logits, torch.float32, (T, h.E), "logits", d)
+    _req(bias, torch.float32, (h.E,), "bias", d)
+    _req(live, torch.int32, (1,), "live", d)
+    _req(w13, wt, (n, 2 * I, H), "w13", d)
+    _req(w2, wt, (n, H, I), "w2", d)
+    _req(s13, torch.float32, (n, -(-2 * I // 128), -(-H // 128)), "s13", d)
+    _req(s2, torch.float32, (n, -(-H // 128), -(-I // 128)), "s2", d)
+    _req(out, torch.bfloat16, (T, H), "out", d)
+    _req(idx, torch.int32, (T, h.K), "idx", d)
+    _req(w, torch.float32, (T, h.K), "w", d)
+    _req(workspace, torch.uint8, None, "workspace", d)
+    a = MoeLayerArgs(_ptr(x), _ptr(logits), _ptr(bias), _ptr(live), _ptr(w13), _ptr(w2), _ptr(s13),
+                     _ptr(s2), _ptr(out), _ptr(idx), _ptr(w), H, I, num_shared, wd, _act(act))
+    _call(h, "moe_layer", h.ptr, ctypes.byref(a), T, _ptr(workspace), workspace.numel(),
+          _stream(stream, d))
+
+
 def moe_dispatch_layout_launches(h, T):
     """Kernel launches moe_dispatch_layout makes for T tokens (1 or 2)."""
     n = ctypes.c_int32(0)
@@ -550,6 +642,36 @@ class MoeRouter:
         hs = torch.empty_like(hrows)
         moe_scale_rows(self.h, hrows, recv_w, hs, stream)
         return hs
+
+    def act_rows(self, gu, recv_w=None, act="silu", p=0.0, rng=None, stream=None):
+        """Gated activation of [rows, 2I] gate/up rows with the routed score
+        and dropout."""
+        hs = torch.empty(gu.shape[0], gu.shape[1] // 2, dtype=gu.dtype, device=gu.device)
+        moe_act_rows(self.h, gu, recv_w, hs, act, p, rng, stream)
+        return hs
+
+    def act_rows_bwd(self, ghs, gu, recv_w=None, act="silu", p=0.0, rng=None, stream=None):
+        """(ggu, gw); gw is None without recv_w."""
+        ggu = torch.empty_like(gu)
+        gw = torch.empty(max(self.h.T, 0), self.h.K, dtype=torch.float32, device=gu.device) \
+            if recv_w is not None else None
+        moe_act_rows_bwd(self.h, ghs, gu, recv_w, ggu, gw, act, p, rng, stream)
+        return ggu, gw
+
+    def layer(self, x, logits, w13, w2, bias=None, s13=None, s2=None, live=None, act="silu",
+              num_shared=0, stream=None):
+        """A whole MoE layer for a few tokens: (out, idx, w).  With `live`, rows
+        behind the live tokens are 0 (idx: -1)."""
+        T, H = x.shape
+        make = torch.empty if live is None else torch.zeros
+        out = make(T, H, dtype=torch.bfloat16, device=x.device)
+        idx = torch.full((T, self.h.K), -1, dtype=torch.int32, device=x.device) if live is not None \
+            else torch.empty(T, self.h.K, dtype=torch.int32, device=x.device)
+        w = make(T, self.h.K, dtype=torch.float32, device=x.device)
+        ws = layer_workspace(self.h, H, w2.shape[2], num_shared)
+        moe_layer(self.h, x, logits, w13, w2, out, idx, w, ws, bias, s13, s2, live, act,
+                  num_shared, stream)
+        return out, idx, w
 
     def w2_absorbed(self, hrows, recv_w, w2, stream=None):
         y = torch.empty(hrows.shape[0], w2.shape[1], dtype=torch.bfloat16, device=hrows.device)

@@ -102,6 +102,27 @@ moe_status from_cuda(cudaError_t e) { return e == cudaSuccess ? MOE_OK : MOE_ERR
 
 cudaStream_t as_stream(void* s) { return static_cast<cudaStream_t>(s); }
 
+// Arguments the activation and its backward share.  Rows of 2I elements, so
+// I is held to half the range.
+bool act_args_ok(int32_t I, int32_t act, double p, const int64_t* rng) {
+  if (I > INT32_MAX / 2) return false;
+  if (act != MOE_ACT_SILU && act != MOE_ACT_GELU) return false;
+  if (!(p >= 0.0 && p < 1.0) || moe::dropped_of(p) >= 65536u) return false;
+  return moe::dropped_of(p) == 0 || (rng && aligned(rng, 8));
+}
+
+int32_t layer_tokens(const moe_config* c) {
+  return c->max_tokens < MOE_LAYER_MAX_TOKENS ? c->max_tokens : MOE_LAYER_MAX_TOKENS;
+}
+
+bool layer_sizes_ok(const moe_config* c, int32_t H, int32_t I, int32_t num_shared,
+                    int32_t weight_dtype) {
+  const int32_t step = weight_dtype == MOE_E4M3 ? 16 : 8;
+  if (H < 1 || I < 1 || H > MOE_LAYER_MAX_WIDTH || I > MOE_LAYER_MAX_WIDTH) return false;
+  if (H % step || I % step) return false;
+  return num_shared >= 0 && num_shared <= MOE_LAYER_MAX_SHARED && c->num_experts >= 1;
+}
+
 // Every launch goes to the current device, and every pointer a call gets must
 // live on the handle's device: a call made while another device is current
 // is refused before anything is launched.
@@ -398,6 +419,66 @@ moe_status moe_w2_absorbed(const moe_handle* h, const void* d_h, int32_t I, cons
   if (!aligned(d_h, 16) || !aligned(d_w2, 16) || !aligned(d_y, 16)) return MOE_ERR_INVALID;
   if (!d_recv_w || !aligned(d_recv_w, 4)) return MOE_ERR_INVALID;
   return from_cuda(moe::launch_w2_absorbed(h, d_h, I, d_recv_w, d_w2, H, d_y, as_stream(stream)));
+}
+
+moe_status moe_act_rows(const moe_handle* h, const void* d_gu, int32_t I, int32_t dtype,
+                        int32_t act, const float* d_recv_w, double drop_p, const int64_t* d_rng,
+                        void* d_hs, void* stream) {
+  if (!h) return MOE_ERR_INVALID;
+  if (!on_handle_device(h)) return MOE_ERR_INVALID;
+  if (!act_args_ok(I, act, drop_p, d_rng)) return MOE_ERR_INVALID;
+  if (h->T < 0) return MOE_ERR_STATE;
+  if (h->T == 0) return empty_rows_ok(I, dtype) ? MOE_OK : MOE_ERR_INVALID;
+  if (!row_ok(d_gu, I, dtype) || !row_ok(d_hs, I, dtype)) return MOE_ERR_INVALID;
+  if (!aligned(d_recv_w, 4)) return MOE_ERR_INVALID;
+  return from_cuda(moe::launch_act_rows(h, d_gu, I, dtype, act, d_recv_w, drop_p, d_rng, d_hs,
+                                        as_stream(stream)));
+}
+
+moe_status moe_act_rows_bwd(const moe_handle* h, const void* d_ghs, const void* d_gu, int32_t I,
+                            int32_t dtype, int32_t act, const float* d_recv_w, double drop_p,
+                            const int64_t* d_rng, void* d_ggu, float* d_gw, void* stream) {
+  if (!h) return MOE_ERR_INVALID;
+  if (!on_handle_device(h)) return MOE_ERR_INVALID;
+  if (!act_args_ok(I, act, drop_p, d_rng)) return MOE_ERR_INVALID;
+  if (d_gw && !d_recv_w) return MOE_ERR_INVALID;
+  if (h->T < 0) return MOE_ERR_STATE;
+  if (h->T == 0) return empty_rows_ok(I, dtype) ? MOE_OK : MOE_ERR_INVALID;
+  if (!row_ok(d_ghs, I, dtype) || !row_ok(d_gu, I, dtype) || !row_ok(d_ggu, I, dtype))
+    return MOE_ERR_INVALID;
+  if (!aligned(d_recv_w, 4) || !aligned(d_gw, 4)) return MOE_ERR_INVALID;
+  return from_cuda(moe::launch_act_rows_bwd(h, d_ghs, d_gu, I, dtype, act, d_recv_w, drop_p, d_rng,
+                                            d_ggu, d_gw, as_stream(stream)));
+}
+
+size_t moe_layer_workspace_bytes(const moe_config* c, int32_t H, int32_t I, int32_t num_shared) {
+  if (!config_valid(c) || !layer_sizes_ok(c, H, I, num_shared, MOE_BF16)) return 0;
+  return moe::layer_plan(layer_tokens(c), c->top_k, num_shared, H, I).total;
+}
+
+moe_status moe_layer(const moe_handle* h, const moe_layer_args* q, int32_t T, void* d_workspace,
+                     size_t workspace_bytes, void* stream) {
+  if (!h || !q || T < 0) return MOE_ERR_INVALID;
+  if (!on_handle_device(h)) return MOE_ERR_INVALID;
+  if (q->weight_dtype != MOE_BF16 && q->weight_dtype != MOE_E4M3) return MOE_ERR_INVALID;
+  if (q->act != MOE_ACT_SILU && q->act != MOE_ACT_GELU) return MOE_ERR_INVALID;
+  if (!layer_sizes_ok(&h->cfg, q->H, q->I, q->num_shared, q->weight_dtype)) return MOE_ERR_INVALID;
+  if (T > layer_tokens(&h->cfg)) return MOE_ERR_CAPACITY;
+  if (q->d_bias && (!q->d_logits || h->cfg.score_fn != MOE_SCORE_SIGMOID)) return MOE_ERR_INVALID;
+  const bool e4m3 = q->weight_dtype == MOE_E4M3;
+  if ((q->d_s13 != nullptr) != e4m3 || (q->d_s2 != nullptr) != e4m3) return MOE_ERR_INVALID;
+  if (T == 0) return MOE_OK;
+  if (!q->d_x || !q->d_w13 || !q->d_w2 || !q->d_out || !q->d_idx || !q->d_w) return MOE_ERR_INVALID;
+  if (!aligned(q->d_x, 16) || !aligned(q->d_w13, 16) || !aligned(q->d_w2, 16) ||
+      !aligned(q->d_out, 16))
+    return MOE_ERR_INVALID;
+  if (!aligned(q->d_logits, 4) || !aligned(q->d_bias, 4) || !aligned(q->d_live, 4) ||
+      !aligned(q->d_s13, 4) || !aligned(q->d_s2, 4) || !aligned(q->d_idx, 4) || !aligned(q->d_w, 4))
+    return MOE_ERR_INVALID;
+  if (!d_workspace || !aligned(d_workspace, kAlign) ||
+      workspace_bytes < moe::layer_plan(T, h->cfg.top_k, q->num_shared, q->H, q->I).total)
+    return MOE_ERR_INVALID;
+  return from_cuda(moe::launch_layer(h, *q, T, d_workspace, as_stream(stream)));
 }
 
 moe_status moe_read_device_status(const moe_handle* h, uint32_t* host_flags) {

@@ -41,7 +41,8 @@ namespace moe {
 int resident_blocks(const void* kernel, int threads, size_t smem);
 
 cudaError_t launch_route_topk(const moe_handle* h, const float* logits, const float* bias, int T,
-                              int32_t* idx, float* w, cudaStream_t s);
+                              int32_t* idx, float* w, cudaStream_t s,
+                              const int32_t* live = nullptr);
 
 cudaError_t launch_route_bwd(const moe_handle* h, const float* logits, const int32_t* idx,
                              const float* gw, int T, float* glogits, cudaStream_t s);
@@ -91,6 +92,26 @@ cudaError_t launch_scale_rows(const moe_handle* h, const void* hrows, int I, int
 cudaError_t launch_scale_rows_bwd(const moe_handle* h, const void* ghs, const void* hrows, int I,
                                   int dtype, const float* recv_w, void* gh, float* gw,
                                   cudaStream_t s);
+
+// 16-bit values dropped at probability p: p * 2^16 to the nearest
+uint32_t dropped_of(double p);
+
+cudaError_t launch_act_rows(const moe_handle* h, const void* gu, int I, int dtype, int act,
+                            const float* rw, double p, const int64_t* rng, void* hs,
+                            cudaStream_t s);
+
+cudaError_t launch_act_rows_bwd(const moe_handle* h, const void* ghs, const void* gu, int I,
+                                int dtype, int act, const float* rw, double p, const int64_t* rng,
+                                void* ggu, float* gw, cudaStream_t s);
+
+// Workspace of the few-token layer for T tokens, K + S experts a token: byte
+// offsets of the activations, the fp32 output rows and the tile counters.
+struct LayerPlan {
+  size_t a, y, done, total;
+};
+LayerPlan layer_plan(int T, int K, int S, int H, int I);
+cudaError_t launch_layer(const moe_handle* h, const moe_layer_args& q, int T, void* workspace,
+                         cudaStream_t s);
 
 int layout_launches(const moe_config& c, int T);
 cudaError_t prepare_w2_kernel();

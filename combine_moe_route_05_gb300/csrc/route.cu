@@ -67,8 +67,14 @@ struct RouteArgs {
   int scale_ff_ok;  // scale is 0 or within [2^-60, 2^60] in magnitude, exact to 2^-48 as FF
   int32_t* idx;
   float* w;
+  const int32_t* live;  // rows at and behind *live are neither read nor written (NULL: all T)
   uint32_t* flags;
 };
+
+// The tokens to route: T, or the device's count of live ones.
+__device__ __forceinline__ int live_tokens(const RouteArgs& a) {
+  return a.live ? min(max(*a.live, 0), a.T) : a.T;
+}
 
 template <typename V>
 __device__ __forceinline__ bool ranks_before(V kv, int e, V bv, int bi) {
@@ -867,6 +873,7 @@ __device__ __forceinline__ void warp_route_tokens(const RouteArgs& a, int t0, in
 template <int VPL, bool SIGMOID>
 __global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(RouteArgs a) {
   grid_dependency_wait();
+  const int T = live_tokens(a);
   extern __shared__ double route_smem[];
   __shared__ int2 cand_lists[kRouteWarps][32];
   double* wkeys = route_smem + (threadIdx.x >> 5) * a.E;
@@ -878,9 +885,9 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(RouteArgs a) {
   // within one
   const int W = gridDim.x * kRouteWarps;
   const int wid = blockIdx.x * kRouteWarps + (threadIdx.x >> 5);
-  for (int i0 = 0; wid + i0 * W < a.T; i0 += TB) {
+  for (int i0 = 0; wid + i0 * W < T; i0 += TB) {
     const int t0 = wid + i0 * W;
-    const int count = min(TB, (a.T - t0 + W - 1) / W);
+    const int count = min(TB, (T - t0 + W - 1) / W);
     warp_route_tokens<VPL, SIGMOID>(a, t0, W, count, lane, wkeys, list);
   }
 }
@@ -987,6 +994,7 @@ __device__ __forceinline__ int word_expert(uint32_t w) { return 255 - static_cas
 template <int EP, bool SIGMOID>
 __global__ void __launch_bounds__(kTeamWarps * 32) route_team_kernel(RouteArgs a) {
   grid_dependency_wait();
+  const int T = live_tokens(a);
   extern __shared__ double route_smem[];  // the fallback's fp64 keys: E per warp (sigmoid)
   __shared__ int2 cand_lists[kTeamWarps][32];
   __shared__ __align__(16) float bias_s[256];
@@ -1038,9 +1046,9 @@ __global__ void __launch_bounds__(kTeamWarps * 32) route_team_kernel(RouteArgs a
   const int n_list = a.K < n_elig ? a.K + 1 : a.K;
 
   const int stride = gridDim.x * kTeamWarps * (32 / kTeam);
-  for (int t0 = (blockIdx.x * kTeamWarps + warp) * (32 / kTeam); t0 < a.T; t0 += stride) {
+  for (int t0 = (blockIdx.x * kTeamWarps + warp) * (32 / kTeam); t0 < T; t0 += stride) {
     const int t = t0 + lane / kTeam;
-    const bool active = t < a.T;
+    const bool active = t < T;
     const float* row = a.logits + static_cast<size_t>(active ? t : t0) * a.E;
     float kx[EP];
 #pragma unroll
@@ -1311,7 +1319,7 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_bwd_full_softmax_kerne
 }  // namespace
 
 cudaError_t launch_route_topk(const moe_handle* h, const float* logits, const float* bias, int T,
-                              int32_t* idx, float* w, cudaStream_t s) {
+                              int32_t* idx, float* w, cudaStream_t s, const int32_t* live) {
   const moe_config& c = h->cfg;
   RouteArgs a;
   a.logits = logits;
@@ -1333,6 +1341,7 @@ cudaError_t launch_route_topk(const moe_handle* h, const float* logits, const fl
   }
   a.idx = idx;
   a.w = w;
+  a.live = live;
   a.flags = h->flags;
   if (T == 0) return cudaSuccess;
 

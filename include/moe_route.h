@@ -62,7 +62,11 @@ typedef enum moe_status {
   MOE_ERR_STATE = 4     /* a row operation called before moe_dispatch_layout */
 } moe_status;
 
-typedef enum moe_dtype { MOE_BF16 = 0, MOE_F32 = 1 } moe_dtype;
+typedef enum moe_dtype { MOE_BF16 = 0, MOE_F32 = 1, MOE_E4M3 = 2 /* moe_layer weights only */ } moe_dtype;
+
+/* Gate activations g * sigmoid(c(g)): c = g, or GELU in its tanh form,
+   c = 2 sqrt(2/pi) (g + 0.044715 g^3). */
+typedef enum moe_act { MOE_ACT_SILU = 0, MOE_ACT_GELU = 1 } moe_act;
 
 typedef enum moe_score_fn { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 } moe_score_fn;
 
@@ -405,6 +409,110 @@ moe_status moe_scale_rows_bwd(const moe_handle* h, const void* d_ghs, const void
  */
 moe_status moe_w2_absorbed(const moe_handle* h, const void* d_h, int32_t I, const float* d_recv_w,
                            const void* d_w2, int32_t H, void* d_y, void* stream);
+
+/*
+ * Gated expert activation with dropout and the routed score, between the
+ * gate/up grouped GEMM and W2.  The pages have the score absorption
+ * ([Titan-absorb] "Implementation": scores applied in fp32 to the W2 input);
+ * the activation in front of it and its dropout have no counterpart there.
+ * For every receive row r of an entry (t,k) in the current layout:
+ *   d_hs[r,i] = round( s_r * m(r,i) * a(g) * u ),   g = d_gu[r, i],
+ *                                                   u = d_gu[r, I + i],
+ * a = the gate activation `act` (moe_act), s_r = d_recv_w[r] (1 if d_recv_w
+ * is NULL: scores applied at the combine), fp32 products, one rounding.
+ * m is 0 for a dropped element and 2^16 / (2^16 - D) for a kept one, where
+ * D = drop_p * 2^16 rounded to the nearest integer (ties to even): the
+ * probability is D / 2^16.  The mask is a function of d_rng and the entry and
+ * is never stored: element i of entry n = t*K + k is dropped when its 16 bits
+ * are below D; they are half i % 2 (0: low) of word (i % 8) / 2 of
+ * Philox4x32-10 with counter (i / 8, n, offset low, offset high) and key (seed
+ * low, seed high), {seed, offset} = d_rng[0..1] as unsigned 64-bit values.  So
+ * the mask does not depend on the layout's rows, padding, or the row dtype.
+ *   d_gu     [RR, 2I] gate then up;  d_hs [RR, I];  RR receive rows
+ *   d_rng    int64[2] on the DEVICE, read when the call runs: a captured graph
+ *            draws a new mask when d_rng is advanced before each replay (keep
+ *            the pair of each step for its backward).  NULL if drop_p = 0.
+ * A dropped element is 0 whatever its inputs hold, and so is a pad row; rows
+ * behind the last segment are not written.  0 <= drop_p < 1 and D < 2^16.
+ */
+moe_status moe_act_rows(const moe_handle* h, const void* d_gu, int32_t I, int32_t dtype,
+                        int32_t act, const float* d_recv_w, double drop_p, const int64_t* d_rng,
+                        void* d_hs, void* stream);
+
+/*
+ * Backward of moe_act_rows with the mask drawn again (the same layout, d_gu,
+ * d_recv_w, drop_p and values at d_rng as in the forward):
+ *   d_ggu[r, i]     = round( d_ghs[r,i] * s_r * m * u * a'(g) )
+ *   d_ggu[r, I + i] = round( d_ghs[r,i] * s_r * m * a(g) )
+ *   d_gw[t,k]       = sum_i d_ghs[r,i] * m * a(g) * u   (fp32; 0 for a dropped
+ *                     entry; not computed if d_gw is NULL; needs d_recv_w)
+ * d_ggu may be d_gu (in place).  Pad rows of d_ggu are 0.
+ */
+moe_status moe_act_rows_bwd(const moe_handle* h, const void* d_ghs, const void* d_gu, int32_t I,
+                            int32_t dtype, int32_t act, const float* d_recv_w, double drop_p,
+                            const int64_t* d_rng, void* d_ggu, float* d_gw, void* stream);
+
+/*
+ * A whole MoE layer for a few tokens (a decode batch), without a dispatch
+ * layout: routing, the experts and the weighted sum, reading the weights of
+ * each reached expert once.  The layer is that of the separate calls
+ * (moe_route_topk, gate/up GEMM, moe_act_rows, W2, moe_combine):
+ *   a[t,k,i] = round_bf16( act(<w13_e[i], x_t>) * <w13_e[I + i], x_t> )
+ *   out[t]   = round_bf16( sum_k w[t,k] <w2_e, a[t,k]> + sum_j <w2_(E+j), a[t,K+j]> )
+ * with e = idx[t,k]; fp32 sums; a is rounded to bf16 because it is the operand
+ * of the second product.  Deterministic: the same inputs give the same bits.
+ *   d_x [T,H] bf16;  d_out [T,H] bf16 (may be d_x: in place)
+ *   d_logits [T,E] fp32 and d_bias [E] or NULL as in moe_route_topk, which
+ *     fills d_idx [T,K] int32 and d_w [T,K] fp32.  d_logits NULL: the caller's
+ *     d_idx and d_w are used; an entry of -1 is no expert, any other index
+ *     outside [0,E) is dropped and flagged (MOE_DEVERR_BAD_EXPERT), and so is
+ *     a token's repeated expert (MOE_DEVERR_DUP_EXPERT).  A token without
+ *     experts gets a zero row (plus the shared experts).
+ *   d_live  int32[1] on the device or NULL: only the first *d_live tokens
+ *     (clamped to [0,T]) are computed; what lies behind them in d_x and d_logits is
+ *     not read, and in d_idx, d_w and d_out not written (a captured batch
+ *     whose last places are empty).
+ *   d_w13 [E+S, 2I, H] (I gate rows, then I up rows), d_w2 [E+S, H, I]: the
+ *     last S = num_shared experts are shared: every token takes them, weight 1.
+ *   weight_dtype MOE_BF16 (d_s13, d_s2 NULL), or MOE_E4M3 with fp32 scales of
+ *     128 x 128 blocks: d_s13 [E+S, ceil(2I/128), ceil(H/128)], d_s2 [E+S,
+ *     ceil(H/128), ceil(I/128)]; a weight is its e4m3 value times its scale.
+ * H and I are multiples of 8 (MOE_E4M3: 16), at most MOE_LAYER_MAX_WIDTH.
+ * T > min(max_tokens, MOE_LAYER_MAX_TOKENS) is MOE_ERR_CAPACITY: larger batches
+ * go through the dispatch.  The handle gives the routing configuration and
+ * the status word; its layout is neither read nor changed.
+ * d_workspace: moe_layer_workspace_bytes(c, H, I, S) bytes, 256-byte aligned,
+ * free after the call's work; calls that may overlap on the GPU need one each.
+ */
+#define MOE_LAYER_MAX_TOKENS 128
+#define MOE_LAYER_MAX_SHARED 4
+#define MOE_LAYER_MAX_WIDTH 65536
+
+typedef struct moe_layer_args {
+  const void* d_x;
+  const float* d_logits;
+  const float* d_bias;
+  const int32_t* d_live;
+  const void* d_w13;
+  const void* d_w2;
+  const float* d_s13;
+  const float* d_s2;
+  void* d_out;
+  int32_t* d_idx;
+  float* d_w;
+  int32_t H;
+  int32_t I;
+  int32_t num_shared;
+  int32_t weight_dtype; /* MOE_BF16 or MOE_E4M3 */
+  int32_t act;          /* moe_act */
+} moe_layer_args;
+
+/* Workspace of moe_layer for up to min(max_tokens, MOE_LAYER_MAX_TOKENS)
+ * tokens; 0 if the configuration or a size is invalid. */
+size_t moe_layer_workspace_bytes(const moe_config* c, int32_t H, int32_t I, int32_t num_shared);
+
+moe_status moe_layer(const moe_handle* h, const moe_layer_args* args, int32_t T, void* d_workspace,
+                     size_t workspace_bytes, void* stream);
 
 /*
  * Copies the device status word to *host_flags (MOE_DEVERR_* bits).  This

@@ -1,0 +1,360 @@
+"""The few-token MoE layer on the GPU against its fp64 definition, within the
+element-wise bound that tests/expert_ref.py derives; its routing against the
+oracle; and the calls around it (padded batches, given routes, graphs, streams,
+in place, the separate calls of the same layer)."""
+import ctypes
+
+import numpy as np
+import pytest
+import torch
+
+import combine_moe_route_05_gb300 as moe
+import oracle
+from tests import expert_ref as ref
+from tests.gpu_util import dev, to_dev, to_host
+
+pytestmark = pytest.mark.gpu
+
+
+def weights(g, n, I, H, e4m3):
+    """(w13, w2, s13, s2) on the device, and their fp64 values."""
+    out, scales, vals = [], [], []
+    for shape, fan in (((n, 2 * I, H), H), ((n, H, I), I)):
+        if not e4m3:
+            t = torch.from_numpy(g.standard_normal(shape).astype(np.float32) * fan ** -0.5).to(dev(), torch.bfloat16)
+            out.append(t)
+            scales.append(None)
+            vals.append(t.double().cpu().numpy())
+            continue
+        q = torch.from_numpy((g.standard_normal(shape) * 100).clip(-448, 448).astype(np.float32)).to(torch.float8_e4m3fn)
+        s = ((g.random((n, -(-shape[1] // 128), -(-shape[2] // 128))) + 0.5) * 0.01 * fan ** -0.5).astype(np.float32)
+        big = np.repeat(np.repeat(s, 128, 1), 128, 2)[:, :shape[1], :shape[2]]
+        out.append(q.to(dev()))
+        scales.append(torch.from_numpy(s).to(dev()))
+        vals.append(q.double().numpy() * big)
+    return out + scales, vals
+
+
+class Problem:
+    def __init__(self, T, E, K, H, I, shared=0, e4m3=False, act="silu", score="softmax", groups=1,
+                 top_groups=1, group_top=1, scale=1.0, renorm=True, seed=0, max_tokens=None):
+        g = np.random.default_rng(seed)
+        self.T, self.E, self.K, self.H, self.I, self.S, self.act = T, E, K, H, I, shared, act
+        self.r = moe.MoeRouter(E, K, 1, max_tokens or T, score_fn=score, num_groups=groups,
+                               topk_groups=top_groups, group_score_topk=group_top, renorm=renorm,
+                               route_scale=scale)
+        (self.w13, self.w2, self.s13, self.s2), (self.v13, self.v2) = weights(g, E + shared, I, H, e4m3)
+        self.x = torch.from_numpy(g.standard_normal((T, H)).astype(np.float32)).to(dev(), torch.bfloat16)
+        self.logits = g.standard_normal((T, E)).astype(np.float32)
+        self.bias = (g.standard_normal(E) * 0.01).astype(np.float32) if score == "sigmoid" else None
+        if score == "sigmoid":
+            self.route = oracle.route_sigmoid_grouped(self.logits, self.bias, K, groups, top_groups,
+                                                      group_top, renorm, scale) if T else None
+        else:
+            self.route = oracle.route_softmax(self.logits, K, renorm, scale) if T else None
+        self.ws = moe.layer_workspace(self.r.h, H, I, shared)
+        # sentinels in the outputs, and in the workspace what an earlier call may leave
+        self.ws.fill_(0xff)
+        self.out = torch.full((T, H), 7.0, dtype=torch.bfloat16, device=dev())
+        self.idx = torch.full((T, K), -9, dtype=torch.int32, device=dev())
+        self.w = torch.full((T, K), -9.0, device=dev())
+
+    def call(self, logits=True, x=None, out=None, live=None, ws=None, stream=None):
+        moe.moe_layer(self.r.h, self.x if x is None else x,
+                      to_dev(self.logits) if logits is True else logits, self.w13, self.w2,
+                      self.out if out is None else out, self.idx, self.w,
+                      self.ws if ws is None else ws, bias=to_dev(self.bias) if logits is not None else None,
+                      s13=self.s13, s2=self.s2, live=live, act=self.act, num_shared=self.S,
+                      stream=stream)
+
+    def want(self, idx, w, tokens=None):
+        n = self.T if tokens is None else tokens
+        x = self.x[:n].double().cpu().numpy()
+        return ref.layer(x, idx[:n], w[:n], self.v13, self.v2, self.S, self.E, self.act)
+
+    def check(self, tokens=None, out=None, flags=0):
+        n = self.T if tokens is None else tokens
+        torch.cuda.synchronize()
+        assert moe.moe_read_device_status(self.r.h) == flags
+        idx, w = to_host(self.idx), to_host(self.w)
+        want, bound = self.want(idx, w, n)
+        got = (self.out if out is None else out).double().cpu().numpy()
+        bad = ~(np.abs(got[:n] - want) <= bound)
+        assert not bad.any(), "%d of %d out of bound: worst %.3g, bound %.3g" % (
+            bad.sum(), bad.size, np.abs(got[:n] - want)[bad].max(), bound[bad].max())
+        return idx, w, got
+
+    def check_route(self, n=None):
+        n = self.T if n is None else n
+        oi, ow = self.route
+        assert np.array_equal(to_host(self.idx)[:n], oi[:n])
+        assert np.abs(to_host(self.w)[:n].view(np.int32) - ow[:n].view(np.int32)).max() <= 1
+
+
+CASES = [
+    dict(T=1, E=4, K=1, H=8, I=8),
+    dict(T=1, E=8, K=2, H=256, I=64),
+    dict(T=2, E=13, K=3, H=264, I=72, act="gelu"),
+    dict(T=3, E=16, K=16, H=136, I=200),
+    dict(T=7, E=60, K=6, H=1000, I=360, act="gelu", shared=2),
+    dict(T=9, E=512, K=8, H=64, I=40),
+    dict(T=16, E=32, K=4, H=2048, I=96, shared=1),
+    dict(T=33, E=8, K=2, H=120, I=136, renorm=False),
+    dict(T=64, E=4, K=4, H=72, I=64, shared=4),
+    dict(T=128, E=8, K=2, H=200, I=48),
+    dict(T=127, E=3, K=1, H=48, I=1024),
+    dict(T=5, E=32, K=4, H=512, I=256, score="sigmoid", groups=8, top_groups=4, group_top=2, scale=2.5),
+    dict(T=1, E=8, K=2, H=16, I=16, e4m3=True),
+    dict(T=4, E=16, K=3, H=400, I=176, e4m3=True, shared=1),     # blocks cut at 2I, H and I
+    dict(T=20, E=6, K=2, H=128, I=336, e4m3=True, act="gelu"),
+    dict(T=70, E=4, K=2, H=272, I=128, e4m3=True, score="sigmoid", scale=0.5),
+]
+
+
+@pytest.mark.parametrize("kw", CASES, ids=lambda k: "-".join("%s" % v for v in k.values()))
+def test_layer(kw):
+    p = Problem(**kw)
+    p.call()
+    p.check()
+    p.check_route()
+    first = p.out.clone()
+    p.call()   # the same workspace again: the same bits
+    assert torch.equal(p.out, first)
+
+
+@pytest.mark.parametrize("live", [0, 1, 5, 12, 13, -4, 1000])
+@pytest.mark.parametrize("shared", [0, 1])
+def test_live_tokens(live, shared):
+    """Places behind the live tokens: x and logits hold NaN, outputs keep theirs."""
+    p = Problem(T=13, E=12, K=3, H=96, I=64, shared=shared, max_tokens=40)
+    n = min(max(live, 0), 13)
+    p.logits[n:] = np.nan
+    p.x[n:] = float("nan")
+    p.call(live=torch.tensor([live], dtype=torch.int32, device=dev()))
+    idx, w, got = p.check(n)
+    if n:
+        p.check_route(n)
+    assert (idx[n:] == -9).all() and (w[n:] == -9.0).all() and (got[n:] == 7.0).all()
+
+
+def test_given_routes_with_empty_tokens():
+    """Routes of the caller's own: no expert (-1), out of range, repeated."""
+    p = Problem(T=11, E=6, K=3, H=88, I=48)
+    idx = np.argsort(np.random.default_rng(1).random((11, 6)), axis=1)[:, :3].astype(np.int32)
+    idx[2] = -1
+    idx[5, 1] = -1
+    p.idx.copy_(to_dev(idx))
+    p.w.copy_(torch.rand(11, 3, device=dev()))
+    p.call(logits=None)
+    i2, _, got = p.check()
+    assert np.array_equal(i2, idx) and (got[2] == 0).all()
+    idx[7] = [4, 9, -2]
+    idx[8] = [1, 1, 1]
+    p.idx.copy_(to_dev(idx))
+    p.call(logits=None)
+    p.check(flags=moe.MOE_DEVERR_BAD_EXPERT | moe.MOE_DEVERR_DUP_EXPERT)
+
+
+@pytest.mark.parametrize("shared", [0, 2])
+def test_no_token_has_an_expert(shared):
+    p = Problem(T=6, E=4, K=2, H=40, I=32, shared=shared)
+    p.idx.fill_(-1)
+    p.w.fill_(1.0)
+    p.call(logits=None)
+    _, _, got = p.check()
+    assert shared or (got == 0).all()
+
+
+@pytest.mark.parametrize("T", [8, 9, 31, 32, 33, 64, 100, 128])
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_all_tokens_on_the_same_experts(T, e4m3):
+    p = Problem(T=T, E=16, K=2, H=144, I=48, e4m3=e4m3)
+    p.logits[:, [3, 15]] += 50.0
+    p.call()
+    idx, _, _ = p.check()
+    assert set(idx.reshape(-1)) == {3, 15}
+
+
+def test_a_bad_token_stays_its_own():
+    """NaN and infinity in one token's row, and a non-finite logit of another."""
+    p = Problem(T=10, E=8, K=2, H=64, I=32)
+    p.call()
+    want = p.out.clone()
+    p.x[4, 7] = float("nan")
+    p.x[6, 0] = float("inf")
+    p.logits[8, 3] = np.nan
+    p.call()
+    torch.cuda.synchronize()
+    assert moe.moe_read_device_status(p.r.h) == moe.MOE_DEVERR_NONFINITE
+    keep = [t for t in range(10) if t not in (4, 6, 8)]
+    assert torch.equal(p.out[keep], want[keep])
+    assert p.out[4].isnan().any() and not p.out[6].isfinite().all()
+
+
+def test_e4m3_codes_read_as_their_values():
+    """Every finite e4m3 code, subnormals among them, as a W2 weight: with one
+    expert, I = 16 and a one-hot activation, out is scale * code * a, one
+    rounding each for a (exact here) and out."""
+    H, I = 256, 16
+    r = moe.MoeRouter(1, 1, 1, 1)
+    codes = torch.arange(256, dtype=torch.uint8)
+    codes[0x7f] = codes[0xff] = 0
+    w2 = codes.view(torch.float8_e4m3fn).reshape(1, H, 1).repeat(1, 1, I).contiguous().to(dev())
+    w13 = torch.zeros(1, 2 * I, 16 * 16, dtype=torch.float8_e4m3fn, device=dev())
+    w13 = torch.zeros(1, 2 * I, H, dtype=torch.uint8, device=dev())
+    one = torch.tensor([1.0]).to(torch.float8_e4m3fn).view(torch.uint8).item()
+    w13[0, 3, 0] = one          # gate 3 = x0
+    w13[0, I + 3, 1] = one      # up 3 = x1
+    w13 = w13.view(torch.float8_e4m3fn)
+    s13 = torch.ones(1, 1, 2, device=dev())
+    s2 = torch.full((1, 2, 1), 0.25, device=dev())
+    x = torch.zeros(1, H, dtype=torch.bfloat16, device=dev())
+    x[0, 0], x[0, 1] = 64.0, 0.03125   # silu(64) = 64 to 28 digits: a = 2
+    out, _, _ = r.layer(x, torch.zeros(1, 1, device=dev()), w13, w2, s13=s13, s2=s2)
+    want = codes.view(torch.float8_e4m3fn).float() * 0.5
+    assert torch.equal(out.float().cpu()[0], want)
+
+
+def test_same_layer_as_the_separate_calls():
+    """Routing, layout, dispatch, gate/up products, activation with the score
+    absorbed, the W2 GEMM and the plain combine, against the layer; the handle
+    keeps its layout across the layer call."""
+    T, E, K, H, I = 48, 16, 4, 512, 192
+    p = Problem(T=T, E=E, K=K, H=H, I=I)
+    r = p.r
+    logits = to_dev(p.logits)
+    idx, w = r.route(logits)
+    lay = {k: v.clone() for k, v in r.layout(idx).items()}
+    p.call()
+    for k, v in moe.layout_tensors(r.h).items():
+        assert torch.equal(v, lay[k]), k
+    recv, recv_w, _ = r.dispatch(p.x, w)
+    off = lay["off_e"].tolist()
+    gu = torch.cat([recv[a:b].float() @ p.w13[e].float().T for e, (a, b) in enumerate(zip(off, off[1:]))]).to(torch.bfloat16)
+    y = r.w2_absorbed(r.act_rows(gu), recv_w, p.w2)
+    sep = r.combine(y).double().cpu().numpy()
+    _, _, got = p.check()
+    # the separate calls round gate/up (2), the activation (1), its product with
+    # the score (1) and the expert rows (1) to bf16: five roundings more, each
+    # half a step of a term; the terms add up to at most sum |w| |w2| |a|
+    want, bound = p.want(to_host(idx), to_host(w))
+    assert (np.abs(sep - want) <= 7 * bound).all()
+    assert (np.abs(got - want) <= bound).all()
+
+
+def test_in_place_output():
+    p = Problem(T=12, E=8, K=2, H=160, I=64, shared=1)
+    p.call()
+    want = p.out.clone()
+    x = p.x.clone()
+    p.call(x=x, out=x)
+    assert torch.equal(x, want)
+
+
+def test_captured_graph_replays_with_new_inputs():
+    p = Problem(T=24, E=12, K=2, H=128, I=96, shared=1)
+    logits = to_dev(p.logits)
+    live = torch.tensor([24], dtype=torch.int32, device=dev())
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        p.call(logits=logits, live=live)
+    s.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=s):
+        p.call(logits=logits, live=live)
+        p.call(logits=logits, live=live)   # back to back on one workspace
+    for step, n in ((0, 24), (1, 9), (2, 17)):
+        g = torch.Generator().manual_seed(step)
+        p.logits[:] = torch.randn(24, 12, generator=g).numpy()
+        p.x.copy_(torch.randn(24, 128, generator=g).to(torch.bfloat16))
+        logits.copy_(to_dev(p.logits))
+        live.fill_(n)
+        p.out.fill_(7.0)
+        graph.replay()
+        _, _, got = p.check(n)
+        assert (got[n:] == 7.0).all()
+
+
+def test_two_streams_with_a_workspace_each():
+    ps = [Problem(T=32, E=8, K=2, H=256, I=128, seed=s) for s in (1, 2)]
+    streams = [torch.cuda.Stream() for _ in ps]
+    logits = [to_dev(p.logits) for p in ps]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for p, s, l in zip(ps, streams, logits):
+            p.call(logits=l, stream=s)
+    for p in ps:
+        p.check()
+
+
+def test_binding_method_with_and_without_live():
+    p = Problem(T=9, E=8, K=2, H=64, I=32)
+    out, idx, w = p.r.layer(p.x, to_dev(p.logits), p.w13, p.w2)
+    p.call()
+    assert torch.equal(out, p.out) and torch.equal(idx, p.idx) and torch.equal(w, p.w)
+    out, idx, w = p.r.layer(p.x, to_dev(p.logits), p.w13, p.w2,
+                            live=torch.tensor([4], dtype=torch.int32, device=dev()))
+    assert torch.equal(out[:4], p.out[:4]) and (out[4:] == 0).all() and (idx[4:] == -1).all()
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(H=60), moe.MOE_ERR_INVALID),
+    (dict(I=36), moe.MOE_ERR_INVALID),
+    (dict(num_shared=5), moe.MOE_ERR_INVALID),
+    (dict(act=7), moe.MOE_ERR_INVALID),
+    (dict(weight_dtype=1), moe.MOE_ERR_INVALID),
+    (dict(weight_dtype=2), moe.MOE_ERR_INVALID),          # e4m3 without scales
+    (dict(d_s13=0x1000, d_s2=0x1000), moe.MOE_ERR_INVALID),  # bf16 with scales
+    (dict(d_x=None), moe.MOE_ERR_INVALID),
+    (dict(d_x=0x1008), moe.MOE_ERR_INVALID),
+    (dict(d_w13=None), moe.MOE_ERR_INVALID),
+    (dict(d_idx=None), moe.MOE_ERR_INVALID),
+    (dict(d_w=0x1002), moe.MOE_ERR_INVALID),
+    (dict(d_bias=0x1000), moe.MOE_ERR_INVALID),           # bias with softmax scores
+    (dict(T=17), moe.MOE_ERR_CAPACITY),
+    (dict(T=-1), moe.MOE_ERR_INVALID),
+    (dict(ws=0x1010), moe.MOE_ERR_INVALID),
+    (dict(ws=None), moe.MOE_ERR_INVALID),
+    (dict(ws_bytes=1000), moe.MOE_ERR_INVALID),
+    (dict(T=0), moe.MOE_OK),
+])
+def test_refusals(kw, status):
+    """Host checks of the C entry point (addresses that no kernel gets)."""
+    h = moe.Handle(moe.make_config(8, 2, 1, 16))
+    f = dict(d_x=0x1000, d_logits=0x1000, d_w13=0x1000, d_w2=0x1000, d_out=0x1000, d_idx=0x1000,
+             d_w=0x1000, H=64, I=32)
+    c = dict(T=16, ws=0x1000, ws_bytes=1 << 24)
+    for k, v in kw.items():
+        (c if k in c else f)[k] = v
+    a = moe.MoeLayerArgs(**f)
+    assert moe.lib().moe_layer(h.ptr, ctypes.byref(a), c["T"], c["ws"], c["ws_bytes"], None) == status
+
+
+def test_more_than_the_layer_takes():
+    r = moe.MoeRouter(8, 2, 1, 4096)
+    assert moe.moe_layer_workspace_bytes(r.h.cfg, 64, 32) == \
+        moe.moe_layer_workspace_bytes(moe.make_config(8, 2, 1, 128), 64, 32)
+    x = torch.zeros(129, 64, dtype=torch.bfloat16, device=dev())
+    with pytest.raises(moe.MoeError) as e:
+        r.layer(x, torch.zeros(129, 8, device=dev()),
+                torch.zeros(8, 64, 64, dtype=torch.bfloat16, device=dev()),
+                torch.zeros(8, 64, 32, dtype=torch.bfloat16, device=dev()))
+    assert e.value.status == moe.MOE_ERR_CAPACITY
+
+
+def test_weights_past_32_bit_offsets():
+    """Expert 40 of 41 begins past 2^31 elements of w13 (4.7 GB)."""
+    E, H, I = 41, 7168, 4096
+    r = moe.MoeRouter(E, 1, 1, 1)
+    w13 = torch.zeros(E, 2 * I, H, dtype=torch.bfloat16, device=dev())
+    w2 = torch.zeros(E, H, I, dtype=torch.bfloat16, device=dev())
+    w13[40, 5, 11] = 1.0
+    w13[40, I + 5, 12] = 1.0
+    w2[40, 7000, 5] = 1.0
+    x = torch.zeros(1, H, dtype=torch.bfloat16, device=dev())
+    x[0, 11], x[0, 12] = 64.0, 0.5
+    logits = torch.zeros(1, E, device=dev())
+    logits[0, 40] = 5.0
+    out, idx, _ = r.layer(x, logits, w13, w2)
+    assert idx.item() == 40 and out[0, 7000].item() == 32.0 and out.abs().sum().item() == 32.0
