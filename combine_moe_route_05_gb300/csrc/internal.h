@@ -105,9 +105,9 @@ cudaError_t launch_act_rows_bwd(const moe_handle* h, const void* ghs, const void
                                 void* ggu, float* gw, cudaStream_t s);
 
 // Workspace of the few-token layer for T tokens, K + S experts a token: byte
-// offsets of the activations, the fp32 output rows and the tile counters.
+// offsets of the activations, the fp32 output rows and the tokens' entry masks.
 struct LayerPlan {
-  size_t a, y, done, total;
+  size_t a, y, kept, total;
 };
 LayerPlan layer_plan(int T, int K, int S, int H, int I);
 cudaError_t launch_layer(const moe_handle* h, const moe_layer_args& q, int T, void* workspace,

@@ -37,7 +37,6 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kMaxEntries = MOE_LAYER_MAX_TOKENS * (MOE_MAX_TOPK + MOE_LAYER_MAX_SHARED);
 constexpr int kMaxExperts = MOE_MAX_EXPERTS + MOE_LAYER_MAX_SHARED;
 constexpr unsigned kFull = 0xffffffffu;
 constexpr uint16_t kNone = 0xffff;
@@ -51,50 +50,80 @@ struct LayerArgs {
   const uint8_t* w2;     // [E + S, H, I]
   const float* s13;      // block scales of e4m3 weights
   const float* s2;
-  __nv_bfloat16* a;      // [T (K + S), I]
+  __nv_bfloat16* a;      // [2][T (K + S), I]: high and low parts
   float* y;              // [T (K + S), H]
-  int32_t* done;         // finished experts per output tile
+  uint32_t* kept;        // [T] bit k: entry (t, k) has an expert
   __nv_bfloat16* out;    // [T, H]
   int T, K, S, E, H, I;
+  int act;
   uint32_t* flags;
 };
 
-// The entries (t, k) grouped by expert; entry t (K + S) + k, shared expert j
-// as k = K + j.
+// ---------------------------------------------------------------------------
+// entries (t, k) grouped by expert
+
+// Shared-memory tables of a block.  Entry n = t (K + S) + k, the shared expert
+// j as k = K + j; experts are numbered shared first, so that their many
+// tokens do not come last.
 struct Groups {
-  uint16_t order[kMaxEntries];  // entries, grouped
-  uint16_t rank[kMaxEntries];   // place within its expert, kNone: dropped
-  int cnt[kMaxExperts];
-  int start[kMaxExperts];
-  uint16_t slot_expert[kMaxExperts];  // experts with entries
-  int warp_sum[kWarps];
-  int nslots;
-  int tokens;
+  uint16_t* order;        // entries, grouped
+  uint16_t* rank;         // an entry's place within its expert, kNone: dropped
+  uint16_t* slot_expert;  // experts with entries
+  int* cnt;               // per expert
+  int* start;
+  int* head;              // warp sums, number of slots
+  int tokens, nslots;
 };
 
-__device__ __forceinline__ int expert_of(const LayerArgs& a, int entry) {
-  const int k = entry % (a.K + a.S);
-  return k < a.K ? __ldg(a.idx + entry / (a.K + a.S) * a.K + k) : a.E + k - a.K;
+__host__ __device__ constexpr size_t up16(size_t b) { return (b + 15) / 16 * 16; }
+
+__host__ __device__ constexpr size_t groups_bytes(int T, int KS, int n_exp) {
+  return 2 * up16(2ull * T * KS) + up16(2ull * n_exp) + 2 * up16(4ull * n_exp) + 64;
 }
 
-__device__ void group_entries(const LayerArgs& a, Groups& g) {
+__device__ __forceinline__ int expert_of(const LayerArgs& a, int entry) {
+  const int t = entry / (a.K + a.S), k = entry - t * (a.K + a.S);
+  if (k >= a.K) return k - a.K;
+  const int e = __ldcg(a.idx + t * a.K + k);
+  return static_cast<unsigned>(e) < static_cast<unsigned>(a.E) ? e + a.S : e == -1 ? -1 : -2;
+}
+
+__device__ void group_entries(const LayerArgs& a, Groups& g, uint8_t* smem) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int n_exp = a.E + a.S;
+  const int n_exp = a.E + a.S, KS = a.K + a.S;
+  g.order = reinterpret_cast<uint16_t*>(smem);
+  smem += up16(2ull * a.T * KS);
+  g.rank = reinterpret_cast<uint16_t*>(smem);
+  smem += up16(2ull * a.T * KS);
+  g.slot_expert = reinterpret_cast<uint16_t*>(smem);
+  smem += up16(2ull * n_exp);
+  g.cnt = reinterpret_cast<int*>(smem);
+  smem += up16(4ull * n_exp);
+  g.start = reinterpret_cast<int*>(smem);
+  smem += up16(4ull * n_exp);
+  g.head = reinterpret_cast<int*>(smem);
+
   for (int e = tid; e < n_exp; e += kThreads) g.cnt[e] = 0;
-  const int tokens = a.live ? min(max(*a.live, 0), a.T) : a.T;
-  const int n = tokens * (a.K + a.S);
-  __syncthreads();
+  g.tokens = a.live ? min(max(__ldcg(a.live), 0), a.T) : a.T;
+  const int n = g.tokens * KS;
+  // an entry's expert, checked, in `order` until the entries are placed
   for (int i = tid; i < n; i += kThreads) {
     const int e = expert_of(a, i);
-    const int k = i % (a.K + a.S);
-    bool ok = static_cast<unsigned>(e) < static_cast<unsigned>(n_exp) && (k >= a.K || e < a.E);
-    uint32_t bad = ok || e == -1 ? 0u : MOE_DEVERR_BAD_EXPERT;
-    for (int j = 0; j < min(k, a.K) && ok && k < a.K; ++j)
-      if (expert_of(a, i - k + j) == e) {
+    if (e == -2 && blockIdx.x == 0) raise_flag(a.flags, MOE_DEVERR_BAD_EXPERT);
+    g.order[i] = e >= 0 ? static_cast<uint16_t>(e) : kNone;
+  }
+  __syncthreads();
+  for (int i = tid; i < n; i += kThreads) {
+    const uint16_t e = g.order[i];
+    bool ok = e != kNone;
+    if (ok && e >= a.S) {  // a repeated expert of the token counts once
+      bool seen = false;
+      for (int j = i / KS * KS; j < i; ++j) seen |= g.order[j] == e;
+      if (seen) {
         ok = false;
-        bad = MOE_DEVERR_DUP_EXPERT;
+        if (blockIdx.x == 0) raise_flag(a.flags, MOE_DEVERR_DUP_EXPERT);
       }
-    if (bad && blockIdx.x == 0) raise_flag(a.flags, bad);
+    }
     g.rank[i] = ok ? static_cast<uint16_t>(atomicAdd(&g.cnt[e], 1)) : kNone;
   }
   __syncthreads();
@@ -114,10 +143,16 @@ __device__ void group_entries(const LayerArgs& a, Groups& g) {
     const int v = __shfl_up_sync(kFull, inc, off);
     if (lane >= off) inc += v;
   }
-  if (lane == 31) g.warp_sum[warp] = inc;
+  if (lane == 31) g.head[warp] = inc;
+  // the entries' experts, before `order` takes the entries
+  constexpr int kMine = MOE_LAYER_MAX_TOKENS * (MOE_MAX_TOPK + MOE_LAYER_MAX_SHARED) / kThreads;
+  uint16_t mine[kMine];
+#pragma unroll
+  for (int j = 0; j < kMine; ++j)
+    if (tid + j * kThreads < n) mine[j] = g.order[tid + j * kThreads];
   __syncthreads();
   int base = inc - sum;
-  for (int wv = 0; wv < warp; ++wv) base += g.warp_sum[wv];
+  for (int wv = 0; wv < warp; ++wv) base += g.head[wv];
 #pragma unroll
   for (int j = 0; j < kPer; ++j) {
     const int e = tid * kPer + j;
@@ -127,15 +162,19 @@ __device__ void group_entries(const LayerArgs& a, Groups& g) {
       if (g.cnt[e]) g.slot_expert[at >> 16] = static_cast<uint16_t>(e);
     }
   }
-  if (tid == kThreads - 1) {
-    g.nslots = (base + sum) >> 16;
-    g.tokens = tokens;
-  }
+  if (tid == kThreads - 1) g.head[kWarps] = (base + sum) >> 16;
   __syncthreads();
-  for (int i = tid; i < n; i += kThreads)
-    if (g.rank[i] != kNone) g.order[g.start[expert_of(a, i)] + g.rank[i]] = static_cast<uint16_t>(i);
+#pragma unroll
+  for (int j = 0; j < kMine; ++j) {
+    const int i = tid + j * kThreads;
+    if (i < n && g.rank[i] != kNone) g.order[g.start[mine[j]] + g.rank[i]] = static_cast<uint16_t>(i);
+  }
+  g.nslots = g.head[kWarps];
   __syncthreads();
 }
+
+// ---------------------------------------------------------------------------
+// matrix products on lane-private queues
 
 __device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                          uint32_t a3, uint32_t b0, uint32_t b1) {
@@ -155,94 +194,259 @@ __device__ __forceinline__ uint32_t bf16x2_of_e4m3x2(uint32_t two) {
   return *reinterpret_cast<const uint32_t*>(&b);
 }
 
-// acc[nt] += 16 weight rows x 8 columns over this warp's share of k.
-// row0 / row1: the lane's weight rows (lane / 4 and lane / 4 + 8); col[nt]: the
-// lane's token row of tile nt or NULL; sc0 / sc1: block scales of the rows'
-// 128-row block (e4m3).  Steps of 32 (e4m3: 64) k are dealt out to the warps.
-template <int NT, bool FP8>
-__device__ __forceinline__ void dot_rows(float (&acc)[NT][4], const uint8_t* row0,
-                                         const uint8_t* row1, const uint8_t* const (&col)[NT],
-                                         const float* sc0, const float* sc1, int kd, int warp) {
-  constexpr int kStep = FP8 ? 64 : 32;
-  constexpr int U = NT == 1 ? 4 : 2;
-  constexpr int X = FP8 ? 2 : 1;  // 16-byte token vectors per weight vector
-  const int t = threadIdx.x & 3;
-  const Vec16 zero{};
-  for (int s0 = warp; s0 * kStep < kd; s0 += kWarps * U) {
-    Vec16 w0[U], w1[U], xv[U][NT][X];
+// Asynchronous copies of 16 and 4 bytes into shared memory; !valid writes
+// zeros and reads nothing.  Weights pass by L1, tokens are kept in it.
+__device__ __forceinline__ void copy16_stream(uint32_t dst, const void* src, bool valid) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
+               "r"(valid ? 16 : 0)
+               : "memory");
+}
+__device__ __forceinline__ void copy16_keep(uint32_t dst, const void* src, bool valid) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
+               "r"(valid ? 16 : 0)
+               : "memory");
+}
+__device__ __forceinline__ void copy4(uint32_t dst, const void* src, bool valid) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src),
+               "r"(valid ? 4 : 0)
+               : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copies_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ Vec16 lds16(uint32_t p) {
+  Vec16 v;
+  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(v.u[0]), "=r"(v.u[1]), "=r"(v.u[2]), "=r"(v.u[3])
+               : "r"(p)
+               : "memory");
+  return v;
+}
+__device__ __forceinline__ float lds4(uint32_t p) {
+  float v;
+  asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(p) : "memory");
+  return v;
+}
+
+// Shape of a kernel: MT tiles of 16 weight rows by NT tiles of 8 tokens,
+// STEPS steps of 64 bytes of a weight row per stage of the queue.
+template <int MT_, int NT_, int STEPS_, int STAGES_, bool FP8_, bool UP_>
+struct Shape {
+  static constexpr int MT = MT_, NT = NT_, kSteps = STEPS_, kStages = STAGES_;
+  static constexpr bool FP8 = FP8_, UP = UP_;
+  static constexpr int kRows = UP ? 8 * MT : 16 * MT;     // outputs of a tile
+  static constexpr int kParts = UP ? 1 : 2;               // x; high and low part of a
+  static constexpr int kVec = FP8 ? 2 : 1;                // token vectors beside a weight vector
+  static constexpr int kSlots = 2 * MT + NT * kVec * kParts;
+  static constexpr int kStepBytes = kThreads * (16 * kSlots + (FP8 ? 8 * MT : 0));
+  static constexpr int kStageBytes = kSteps * kStepBytes;
+  static constexpr size_t kRedBytes = static_cast<size_t>(kWarps) * MT * NT * 4 * 32 * 4;
+  static_assert(kStages * kStageBytes + kRedBytes +
+                        groups_bytes(MOE_LAYER_MAX_TOKENS, MOE_MAX_TOPK + MOE_LAYER_MAX_SHARED,
+                                     kMaxExperts) <= 227 * 1024, "shared memory budget");
+  static size_t smem(const LayerArgs& a) {
+    return kStages * kStageBytes + kRedBytes + groups_bytes(a.T, a.K + a.S, a.E + a.S);
+  }
+};
+
+// Tile `tile` of the outputs for tokens [c0, c0 + 8 NT) of the expert in slot
+// `slot`; q = slot * tiles + tile.
+struct Job {
+  int q, slot, tile, c0;
+};
+
+template <typename S>
+struct Kernel {
+  const LayerArgs& a;
+  const Groups& g;
+  uint32_t fifo;  // shared-memory address of this thread's queue
+  int tiles, kd, stages, nq;
+  int lane, warp;
+  int team;       // warps that share a job and split its k
+  int first_q, stride_q, part;
+
+  __device__ Kernel(const LayerArgs& args, const Groups& groups, uint8_t* smem)
+      : a(args), g(groups), lane(threadIdx.x & 31), warp(threadIdx.x >> 5) {
+    fifo = smem_addr(smem) + threadIdx.x * 16;
+    kd = S::UP ? a.H : a.I;
+    tiles = ((S::UP ? a.I : a.H) + S::kRows - 1) / S::kRows;
+    constexpr int kPer = S::kSteps * (S::FP8 ? 64 : 32);
+    stages = (kd + kPer - 1) / kPer;
+    nq = g.nslots * tiles;
+    team = 1;
+    while (team < kWarps && nq * team < 4 * kWarps * static_cast<int>(gridDim.x) && team < stages) team *= 2;
+    first_q = blockIdx.x + gridDim.x * (warp / team);
+    stride_q = gridDim.x * (kWarps / team);
+    part = warp % team;
+  }
+
+  __device__ __forceinline__ bool valid(const Job& j) const { return j.q < nq; }
+  __device__ __forceinline__ Job at(int q) const {
+    const int slot = q / tiles;
+    return Job{q, slot, q - slot * tiles, 0};
+  }
+  __device__ __forceinline__ Job next(Job j) const {
+    j.c0 += 8 * S::NT;
+    return j.c0 < g.cnt[g.slot_expert[j.slot]] ? j : at(j.q + stride_q);
+  }
+
+  // Where the next copies of this warp come from.
+  struct Cursor {
+    Job j;
+    int stage;
+    const uint8_t* row;   // the lane's first weight row
+    const float* scale;   // its block scales
+    int col[S::NT];       // the lane's entry (up: token) per token tile, -1: none
+    int first_row;
+  };
+
+  __device__ __forceinline__ void open(Cursor& c) const {
+    if (!valid(c.j)) return;
+    const int p = g.slot_expert[c.j.slot];
+    const int e = p < a.S ? a.E + p : p - a.S;
+    constexpr int kEb = S::FP8 ? 1 : 2;
+    c.first_row = c.j.tile * S::kRows;
+    const int rows = S::UP ? 2 * a.I : a.H;
+    c.row = (S::UP ? a.w13 : a.w2) +
+            (static_cast<int64_t>(e) * rows + c.first_row + (lane >> 2)) * kd * kEb;
+    if (S::FP8)
+      c.scale = (S::UP ? a.s13 : a.s2) +
+                static_cast<int64_t>(e) * ((rows + 127) / 128) * ((kd + 127) / 128);
+    const int cnt = g.cnt[p], at = g.start[p];
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int o = (s0 + u * kWarps) * kStep + t * (kStep / 4);
-      w0[u] = o < kd ? ld_stream(row0 + static_cast<int64_t>(o) * (FP8 ? 1 : 2)) : zero;
-      w1[u] = o < kd ? ld_stream(row1 + static_cast<int64_t>(o) * (FP8 ? 1 : 2)) : zero;
+    for (int nt = 0; nt < S::NT; ++nt) {
+      const int n = c.j.c0 + nt * 8 + (lane >> 2);
+      c.col[nt] = n < cnt ? (S::UP ? g.order[at + n] / (a.K + a.S) : g.order[at + n]) : -1;
     }
+  }
+  __device__ __forceinline__ Cursor begin() const {
+    Cursor c;
+    c.j = at(first_q);
+    c.stage = part;
+    if (part >= stages) c.j.q = nq;  // more warps than stages
+    open(c);
+    return c;
+  }
+  __device__ __forceinline__ void advance(Cursor& c) const {
+    c.stage += team;
+    if (c.stage < stages) return;
+    c.stage = part;
+    c.j = next(c.j);
+    open(c);
+  }
+
+  __device__ __forceinline__ void copy_weights(const Cursor& c, int slot) const {
+    if (!valid(c.j)) return;
+    constexpr int kEb = S::FP8 ? 1 : 2;
+    const int64_t half = static_cast<int64_t>(S::UP ? a.I : 8) * kd * kEb;
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int o = (s0 + u * kWarps) * kStep + t * (kStep / 4);
+    for (int st = 0; st < S::kSteps; ++st) {
+      const uint32_t dst = fifo + slot * S::kStageBytes + st * S::kStepBytes;
+      const int step = c.stage * S::kSteps + st;
+      const int o = step * 64 + (lane & 3) * 16;
+      const bool in = o < kd * kEb;
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int v = 0; v < X; ++v)
-          xv[u][nt][v] = o < kd && col[nt] ? ld_vec(col[nt] + o * 2 + v * 16) : zero;
-    }
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      if (!FP8) {
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int q = 0; q < 4; q += 2)
-            mma_bf16(acc[nt], w0[u].u[q], w1[u].u[q], w0[u].u[q + 1], w1[u].u[q + 1],
-                     xv[u][nt][0].u[q], xv[u][nt][0].u[q + 1]);
-      } else {
-        const int s = s0 + u * kWarps;
-        if (s * kStep >= kd) continue;
-        const float f0 = __ldg(sc0 + s / 2), f1 = __ldg(sc1 + s / 2);
-        float part[NT][4];
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int j = 0; j < 4; ++j) part[nt][j] = 0.0f;
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const uint32_t a0 = bf16x2_of_e4m3x2(w0[u].u[q]), a2 = bf16x2_of_e4m3x2(w0[u].u[q] >> 16);
-          const uint32_t a1 = bf16x2_of_e4m3x2(w1[u].u[q]), a3 = bf16x2_of_e4m3x2(w1[u].u[q] >> 16);
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-            mma_bf16(part[nt], a0, a1, a2, a3, xv[u][nt][q / 2].u[q % 2 * 2],
-                     xv[u][nt][q / 2].u[q % 2 * 2 + 1]);
-        }
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          acc[nt][0] = fmaf(f0, part[nt][0], acc[nt][0]);
-          acc[nt][1] = fmaf(f0, part[nt][1], acc[nt][1]);
-          acc[nt][2] = fmaf(f1, part[nt][2], acc[nt][2]);
-          acc[nt][3] = fmaf(f1, part[nt][3], acc[nt][3]);
+      for (int mt = 0; mt < S::MT; ++mt) {
+        const int r = c.first_row + mt * (S::UP ? 8 : 16);  // outputs are whole 8-row groups
+        const uint8_t* p = c.row + static_cast<int64_t>(mt * (S::UP ? 8 : 16)) * kd * kEb + o;
+        const bool row_ok = r < (S::UP ? a.I : a.H);
+        const bool ok0 = in && row_ok;
+        const bool ok1 = S::UP ? ok0 : in && r + 8 < a.H;
+        copy16_stream(dst + (2 * mt) * kThreads * 16, ok0 ? p : c.row, ok0);
+        copy16_stream(dst + (2 * mt + 1) * kThreads * 16, ok1 ? p + half : c.row, ok1);
+        if (S::FP8) {
+          const int kb = (kd + 127) / 128;
+          const bool ok = row_ok && step * 64 < kd;
+          const float* s0 = c.scale + static_cast<int64_t>(r / 128) * kb + step / 2;
+          const float* s1 = S::UP ? c.scale + static_cast<int64_t>((a.I + r) / 128) * kb + step / 2 : s0;
+          const uint32_t sd = dst - threadIdx.x * 16 + S::kSlots * kThreads * 16 +
+                              (mt * kThreads + threadIdx.x) * 8;
+          // also where this lane's bytes lie behind the row's end: the scale
+          // is for the sums it receives
+          copy4(sd, ok ? s0 : c.scale, ok);
+          copy4(sd + 4, ok ? s1 : c.scale, ok);
         }
       }
     }
   }
-}
-
-// The warps' partial sums added in warp order; warp nt returns true with tile
-// nt's sums in acc.
-template <int NT>
-__device__ __forceinline__ bool sum_warps(float (&acc)[NT][4], float (&sum)[4], float* red,
-                                          int warp, int lane) {
-  __syncthreads();
+  __device__ __forceinline__ void copy_tokens(const Cursor& c, int slot) const {
+    if (!valid(c.j)) return;
+    const uint8_t* src = S::UP ? a.x : reinterpret_cast<const uint8_t*>(a.a);
+    const int64_t low = static_cast<int64_t>(a.T) * (a.K + a.S) * kd * 2;
 #pragma unroll
-  for (int nt = 0; nt < NT; ++nt)
+    for (int st = 0; st < S::kSteps; ++st) {
+      const uint32_t dst = fifo + slot * S::kStageBytes + st * S::kStepBytes +
+                           2 * S::MT * kThreads * 16;
+      // bytes of a bf16 row
+      const int o = ((c.stage * S::kSteps + st) * 64 + (lane & 3) * 16) * (S::FP8 ? 2 : 1);
+      const bool in = o < kd * 2;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) red[((warp * NT + nt) * 4 + j) * 32 + lane] = acc[nt][j];
-  __syncthreads();
-  if (warp >= NT) return false;
+      for (int nt = 0; nt < S::NT; ++nt) {
+        const bool ok = in && c.col[nt] >= 0;
+        const uint8_t* p = ok ? src + static_cast<int64_t>(c.col[nt]) * kd * 2 + o : src;
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    sum[j] = 0.0f;
-    for (int wv = 0; wv < kWarps; ++wv) sum[j] += red[((wv * NT + warp) * 4 + j) * 32 + lane];
+        for (int h = 0; h < S::kParts; ++h)
+#pragma unroll
+          for (int v = 0; v < S::kVec; ++v)
+            copy16_keep(dst + ((nt * S::kParts + h) * S::kVec + v) * kThreads * 16,
+                        ok ? p + h * low + v * 16 : src, ok);
+      }
+    }
   }
-  return true;
-}
+
+  // acc += the products of one step of the queue's slot.
+  __device__ __forceinline__ void products(float (&acc)[S::MT][S::NT][4], int slot, int step) const {
+    const uint32_t at = fifo + slot * S::kStageBytes + step * S::kStepBytes;
+    Vec16 b[S::NT][S::kParts][S::kVec];
+#pragma unroll
+    for (int nt = 0; nt < S::NT; ++nt)
+#pragma unroll
+      for (int h = 0; h < S::kParts; ++h)
+#pragma unroll
+        for (int v = 0; v < S::kVec; ++v)
+          b[nt][h][v] = lds16(at + (2 * S::MT + (nt * S::kParts + h) * S::kVec + v) * kThreads * 16);
+#pragma unroll
+    for (int mt = 0; mt < S::MT; ++mt) {
+      const Vec16 w0 = lds16(at + (2 * mt) * kThreads * 16);
+      const Vec16 w1 = lds16(at + (2 * mt + 1) * kThreads * 16);
+      if (!S::FP8) {
+#pragma unroll
+        for (int q = 0; q < 4; q += 2)
+#pragma unroll
+          for (int nt = 0; nt < S::NT; ++nt)
+#pragma unroll
+            for (int h = 0; h < S::kParts; ++h)
+              mma_bf16(acc[mt][nt], w0.u[q], w1.u[q], w0.u[q + 1], w1.u[q + 1], b[nt][h][0].u[q],
+                       b[nt][h][0].u[q + 1]);
+      } else {
+        const uint32_t sd = at - threadIdx.x * 16 + S::kSlots * kThreads * 16 +
+                            (mt * kThreads + threadIdx.x) * 8;
+        const float f0 = lds4(sd), f1 = lds4(sd + 4);
+        float sum[S::NT][4] = {};
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const uint32_t a0 = bf16x2_of_e4m3x2(w0.u[q]), a2 = bf16x2_of_e4m3x2(w0.u[q] >> 16);
+          const uint32_t a1 = bf16x2_of_e4m3x2(w1.u[q]), a3 = bf16x2_of_e4m3x2(w1.u[q] >> 16);
+#pragma unroll
+          for (int nt = 0; nt < S::NT; ++nt)
+#pragma unroll
+            for (int h = 0; h < S::kParts; ++h)
+              mma_bf16(sum[nt], a0, a1, a2, a3, b[nt][h][q / 2].u[q % 2 * 2],
+                       b[nt][h][q / 2].u[q % 2 * 2 + 1]);
+        }
+#pragma unroll
+        for (int nt = 0; nt < S::NT; ++nt) {
+          acc[mt][nt][0] = fmaf(f0, sum[nt][0], acc[mt][nt][0]);
+          acc[mt][nt][1] = fmaf(f0, sum[nt][1], acc[mt][nt][1]);
+          acc[mt][nt][2] = fmaf(f1, sum[nt][2], acc[mt][nt][2]);
+          acc[mt][nt][3] = fmaf(f1, sum[nt][3], acc[mt][nt][3]);
+        }
+      }
+    }
+  }
+};
 
 __device__ __forceinline__ float act_value(float g, int act) {
   const float c = act == MOE_ACT_GELU
@@ -250,134 +454,169 @@ __device__ __forceinline__ float act_value(float g, int act) {
   return c < -80.0f ? g * 0.0f : g * __fdividef(1.0f, 1.0f + __expf(-c));
 }
 
-constexpr int kNT = 4;  // column tiles of 8 tokens handled at once
-
-// One unit: 16 weight rows of one expert against its tokens, kNT * 8 at a
-// time; store(sum, token column, lane row) takes the results.
-template <bool FP8, typename Col, typename Store>
-__device__ __forceinline__ void unit_products(const Groups& g, int e, const uint8_t* row0,
-                                              const uint8_t* row1, const float* sc0,
-                                              const float* sc1, int kd, float* red, Col col_of,
-                                              Store store) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int cnt = g.cnt[e], start = g.start[e];
-  for (int c0 = 0; c0 < cnt;) {
-    auto pass = [&](auto tiles) {
-      constexpr int NT = decltype(tiles)::value;
-      float acc[NT][4] = {}, sum[4];
-      const uint8_t* col[NT];
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        const int c = c0 + nt * 8 + (lane >> 2);
-        col[nt] = c < cnt ? col_of(g.order[start + c]) : nullptr;
-      }
-      dot_rows<NT, FP8>(acc, row0, row1, col, sc0, sc1, kd, warp);
-      if (sum_warps<NT>(acc, sum, red, warp, lane)) {
-        const int c = c0 + warp * 8 + 2 * (lane & 3);
-        if (c < cnt) store(g.order[start + c], sum[0], sum[2]);
-        if (c + 1 < cnt) store(g.order[start + c + 1], sum[1], sum[3]);
-      }
-      c0 += NT * 8;
-    };
-    if (cnt - c0 <= 8) pass(std::integral_constant<int, 1>{});
-    else if (cnt - c0 <= 16) pass(std::integral_constant<int, 2>{});
-    else pass(std::integral_constant<int, kNT>{});
-  }
+__device__ __forceinline__ void team_sync(int id, int threads) {
+  asm volatile("bar.sync %0, %1;" ::"r"(id + 1), "r"(threads) : "memory");
 }
 
-template <bool FP8>
-__global__ void __launch_bounds__(kThreads, 2) layer_up_kernel(LayerArgs a, int act) {
-  grid_dependency_wait();
-  __shared__ Groups g;
-  __shared__ float red[kWarps * kNT * 4 * 32];
-  group_entries(a, g);
-  const int lane = threadIdx.x & 31;
-  const int tiles2 = (a.H + 15) / 16;
-  for (int i = blockIdx.x * kThreads + threadIdx.x; i < tiles2; i += gridDim.x * kThreads) a.done[i] = 0;
-  const int tiles = a.I / 8;
-  const int units = g.nslots * tiles;
-  const int KS = a.K + a.S;
-  constexpr int kEb = FP8 ? 1 : 2;
-  const int u0 = static_cast<int>(static_cast<int64_t>(units) * blockIdx.x / gridDim.x);
-  const int u1 = static_cast<int>(static_cast<int64_t>(units) * (blockIdx.x + 1) / gridDim.x);
-  for (int u = u0; u < u1; ++u) {
-    const int e = g.slot_expert[u / tiles], i0 = u % tiles * 8;
-    const int64_t base = static_cast<int64_t>(e) * 2 * a.I;
-    const uint8_t* row0 = a.w13 + (base + i0 + (lane >> 2)) * a.H * kEb;
-    const uint8_t* row1 = row0 + static_cast<int64_t>(a.I) * a.H * kEb;
-    const int kb = (a.H + 127) / 128, rb = (2 * a.I + 127) / 128;
-    const float* sc = a.s13 + static_cast<int64_t>(e) * rb * kb;
-    unit_products<FP8>(
-        g, e, row0, row1, sc + static_cast<int64_t>(i0 / 128) * kb,
-        sc + static_cast<int64_t>((a.I + i0) / 128) * kb, a.H, red,
-        [&](int entry) { return a.x + static_cast<int64_t>(entry / KS) * a.H * 2; },
-        [&](int entry, float gate, float up) {
-          a.a[static_cast<int64_t>(entry) * a.I + i0 + (lane >> 2)] =
-              __float2bfloat16_rn(act_value(gate, act) * up);
-        });
+template <typename S>
+__global__ void __launch_bounds__(kThreads, S::MT * S::NT == 1 ? 2 : 1) layer_kernel(LayerArgs a) {
+  extern __shared__ __align__(16) uint8_t smem[];
+  if (S::UP) {
+    // what this grid reads of earlier ones is complete from here on; the down
+    // grid starts behind this point, so it may read all but this grid's `a`
+    asm volatile("griddepcontrol.wait;\n\tgriddepcontrol.launch_dependents;" ::: "memory");
   }
-}
-
-template <bool FP8>
-__global__ void __launch_bounds__(kThreads, 2) layer_down_kernel(LayerArgs a) {
-  grid_dependency_wait();
-  __shared__ Groups g;
-  __shared__ float red[kWarps * kNT * 4 * 32];
-  __shared__ int last;
-  group_entries(a, g);
-  const int lane = threadIdx.x & 31;
-  const int tiles = (a.H + 15) / 16;
-  const int units = g.nslots * tiles;
+  float* red = reinterpret_cast<float*>(smem + S::kStages * S::kStageBytes);
+  Groups g;
+  group_entries(a, g, smem + S::kStages * S::kStageBytes + S::kRedBytes);
+  const Kernel<S> k(a, g, smem);
+  const int lane = k.lane, warp = k.warp;
   const int KS = a.K + a.S;
-  constexpr int kEb = FP8 ? 1 : 2;
-  if (units == 0) {  // no expert reached: zero rows
-    const int64_t n = static_cast<int64_t>(g.tokens) * a.H;
-    for (int64_t i = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x; i < n;
-         i += static_cast<int64_t>(gridDim.x) * kThreads)
-      a.out[i] = __float2bfloat16_rn(0.0f);
-    return;
-  }
-  const int u0 = static_cast<int>(static_cast<int64_t>(units) * blockIdx.x / gridDim.x);
-  const int u1 = static_cast<int>(static_cast<int64_t>(units) * (blockIdx.x + 1) / gridDim.x);
-  for (int u = u0; u < u1; ++u) {
-    const int e = g.slot_expert[u / tiles], n0 = u % tiles * 16;
-    const int r0 = n0 + (lane >> 2);
-    const bool second = r0 + 8 < a.H;  // H is a multiple of 8
-    const uint8_t* row0 = a.w2 + (static_cast<int64_t>(e) * a.H + r0) * a.I * kEb;
-    const uint8_t* row1 = second ? row0 + static_cast<int64_t>(8) * a.I * kEb : row0;
-    const int kb = (a.I + 127) / 128, rb = (a.H + 127) / 128;
-    const float* sc = a.s2 + (static_cast<int64_t>(e) * rb + n0 / 128) * kb;
-    unit_products<FP8>(
-        g, e, row0, row1, sc, sc, a.I, red,
-        [&](int entry) {
-          return reinterpret_cast<const uint8_t*>(a.a + static_cast<int64_t>(entry) * a.I);
-        },
-        [&](int entry, float lo, float hi) {
-          float* y = a.y + static_cast<int64_t>(entry) * a.H + r0;
-          y[0] = lo;
-          if (second) y[8] = hi;
-        });
-    // the last expert's block of this tile adds the experts' rows
-    __threadfence();
-    __syncthreads();
-    if (threadIdx.x == 0) last = atomicAdd(a.done + u % tiles, 1) == g.nslots - 1;
-    __syncthreads();
-    if (last) {
-      __threadfence();
-      const int width = min(16, a.H - n0);
-      for (int i = threadIdx.x; i < g.tokens * 16; i += kThreads) {
-        const int t = i / 16, n = i % 16;
-        if (n >= width) continue;
-        float v = 0.0f;
-        for (int k = 0; k < KS; ++k) {
-          if (g.rank[t * KS + k] == kNone) continue;
-          const float yv = __ldcg(a.y + static_cast<int64_t>(t * KS + k) * a.H + n0 + n);
-          v = fmaf(k < a.K ? __ldg(a.w + t * a.K + k) : 1.0f, yv, v);
-        }
-        a.out[static_cast<int64_t>(t) * a.H + n0 + n] = __float2bfloat16_rn(v);
-      }
+  if (S::UP && blockIdx.x == 0) {
+    for (int t = threadIdx.x; t < g.tokens; t += kThreads) {
+      uint32_t kept = 0;
+      for (int kk = 0; kk < KS; ++kk) kept |= (g.rank[t * KS + kk] != kNone ? 1u : 0u) << kk;
+      a.kept[t] = kept;
     }
   }
+
+  typename Kernel<S>::Cursor next = k.begin();
+  {
+    typename Kernel<S>::Cursor c = next;
+#pragma unroll
+    for (int s = 0; s < S::kStages; ++s) {
+      k.copy_weights(c, s);
+      if (k.valid(c.j)) k.advance(c);
+    }
+  }
+  if (!S::UP) asm volatile("griddepcontrol.wait;\n\tgriddepcontrol.launch_dependents;" ::: "memory");
+#pragma unroll
+  for (int s = 0; s < S::kStages; ++s) {
+    k.copy_tokens(next, s);
+    copies_commit();
+    if (k.valid(next.j)) k.advance(next);
+  }
+
+  int slot = 0;
+  for (Job j = k.at(k.first_q); k.valid(j); j = k.next(j)) {
+    float acc[S::MT][S::NT][4] = {};
+    for (int st = k.part; st < k.stages; st += k.team) {
+      copies_wait<S::kStages - 1>();
+#pragma unroll
+      for (int i = 0; i < S::kSteps; ++i) k.products(acc, slot, i);
+      // the products have read the slot; its next contents
+      k.copy_weights(next, slot);
+      k.copy_tokens(next, slot);
+      copies_commit();
+      if (k.valid(next.j)) k.advance(next);
+      slot = slot + 1 == S::kStages ? 0 : slot + 1;
+    }
+    if (k.team > 1) {  // the team's partial sums, added in warp order
+      const int id = warp / k.team;
+      team_sync(id, k.team * 32);
+#pragma unroll
+      for (int mt = 0; mt < S::MT; ++mt)
+#pragma unroll
+        for (int nt = 0; nt < S::NT; ++nt)
+#pragma unroll
+          for (int r = 0; r < 4; ++r)
+            red[((warp * S::MT * S::NT + mt * S::NT + nt) * 4 + r) * 32 + lane] = acc[mt][nt][r];
+      team_sync(id, k.team * 32);
+    }
+    const int p = g.slot_expert[j.slot];
+    const int cnt = g.cnt[p], at = g.start[p], r0 = j.tile * S::kRows;
+#pragma unroll
+    for (int mt = 0; mt < S::MT; ++mt)
+#pragma unroll
+      for (int nt = 0; nt < S::NT; ++nt) {
+        const int tile = mt * S::NT + nt;
+        if (tile % k.team != k.part) continue;
+        float v[4];
+        if (k.team > 1) {
+#pragma unroll
+          for (int r = 0; r < 4; ++r) v[r] = 0.0f;
+          for (int wv = warp - k.part; wv < warp - k.part + k.team; ++wv)
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+              v[r] += red[((wv * S::MT * S::NT + tile) * 4 + r) * 32 + lane];
+        } else {
+#pragma unroll
+          for (int r = 0; r < 4; ++r) v[r] = acc[mt][nt][r];
+        }
+        const int n = j.c0 + nt * 8 + 2 * (lane & 3);
+        const int row = r0 + mt * (S::UP ? 8 : 16) + (lane >> 2);
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          if (n + c >= cnt) continue;
+          const int entry = g.order[at + n + c];
+          if (S::UP) {
+            if (row >= a.I) continue;
+            const float h = act_value(v[c], a.act) * v[2 + c];
+            const __nv_bfloat16 hi = __float2bfloat16_rn(h);
+            const float rest = h - __bfloat162float(hi);
+            __nv_bfloat16* dst = a.a + static_cast<int64_t>(entry) * a.I + row;
+            dst[0] = hi;
+            dst[static_cast<int64_t>(a.T) * KS * a.I] =
+                __float2bfloat16_rn(isfinite(rest) ? rest : 0.0f);
+          } else {
+            float* y = a.y + static_cast<int64_t>(entry) * a.H + row;
+            if (row < a.H) y[0] = v[c];
+            if (row + 8 < a.H) y[8] = v[2 + c];
+          }
+        }
+      }
+  }
+}
+
+// out[t] = round(sum over the token's entries of weight * y), in k order; a
+// thread per 4 columns of a token.
+__global__ void __launch_bounds__(kThreads) layer_combine_kernel(LayerArgs a) {
+  grid_dependency_wait();
+  const int KS = a.K + a.S;
+  const int tokens = a.live ? min(max(__ldg(a.live), 0), a.T) : a.T;
+  const int per = a.H / 4;
+  const int i = blockIdx.x * kThreads + threadIdx.x;
+  const int t = i / per, col = (i - t * per) * 4;
+  if (t >= tokens) return;
+  const uint32_t kept = __ldg(a.kept + t);
+  float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  const float* y = a.y + static_cast<int64_t>(t) * KS * a.H + col;
+#pragma unroll 4
+  for (int k = 0; k < KS; ++k) {
+    if (!((kept >> k) & 1u)) continue;
+    const float w = k < a.K ? __ldg(a.w + t * a.K + k) : 1.0f;
+    const float4 f = __ldg(reinterpret_cast<const float4*>(y + static_cast<int64_t>(k) * a.H));
+    v.x = fmaf(w, f.x, v.x);
+    v.y = fmaf(w, f.y, v.y);
+    v.z = fmaf(w, f.z, v.z);
+    v.w = fmaf(w, f.w, v.w);
+  }
+  const __nv_bfloat162 lo = __floats2bfloat162_rn(v.x, v.y), hi = __floats2bfloat162_rn(v.z, v.w);
+  uint2 o;
+  o.x = *reinterpret_cast<const uint32_t*>(&lo);
+  o.y = *reinterpret_cast<const uint32_t*>(&hi);
+  *reinterpret_cast<uint2*>(a.out + static_cast<int64_t>(t) * a.H + col) = o;
+}
+
+cudaError_t launch_combine_layer(const LayerArgs& a, cudaStream_t s) {
+  const long long n = static_cast<long long>(a.T) * (a.H / 4);
+  return launch_chained(layer_combine_kernel, dim3(static_cast<unsigned>((n + kThreads - 1) / kThreads)),
+                        dim3(kThreads), 0, s, false, a);
+}
+
+constexpr size_t kUpSmem = 116 * 1024;
+
+template <typename S>
+cudaError_t launch_shape(const moe_handle* h, const LayerArgs& a, cudaStream_t s) {
+  auto k = layer_kernel<S>;
+  // over half an SM's shared memory, so that every SM gets one block of the
+  // up grid, whatever still runs there when the grid is scheduled
+  const size_t smem = S::UP && S::smem(a) < kUpSmem ? kUpSmem : S::smem(a);
+  // per device and cheap: no state to keep
+  const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             static_cast<int>(smem));
+  if (e != cudaSuccess) return e;
+  return launch_chained(k, dim3(h->num_sms), dim3(kThreads), smem, s, false, a);
 }
 
 }  // namespace
@@ -387,9 +626,9 @@ LayerPlan layer_plan(int T, int K, int S, int H, int I) {
   const size_t entries = static_cast<size_t>(T) * (K + S);
   LayerPlan p;
   p.a = 0;
-  p.y = up(entries * I * sizeof(__nv_bfloat16));
-  p.done = p.y + up(entries * H * sizeof(float));
-  p.total = p.done + up(static_cast<size_t>((H + 15) / 16) * sizeof(int32_t));
+  p.y = up(2 * entries * I * sizeof(__nv_bfloat16));
+  p.kept = p.y + up(entries * H * sizeof(float));
+  p.total = p.kept + up(static_cast<size_t>(T) * sizeof(uint32_t));
   return p;
 }
 
@@ -414,7 +653,7 @@ cudaError_t launch_layer(const moe_handle* h, const moe_layer_args& q, int T, vo
   a.s2 = q.d_s2;
   a.a = reinterpret_cast<__nv_bfloat16*>(ws + p.a);
   a.y = reinterpret_cast<float*>(ws + p.y);
-  a.done = reinterpret_cast<int32_t*>(ws + p.done);
+  a.kept = reinterpret_cast<uint32_t*>(ws + p.kept);
   a.out = static_cast<__nv_bfloat16*>(q.d_out);
   a.T = T;
   a.K = K;
@@ -422,14 +661,25 @@ cudaError_t launch_layer(const moe_handle* h, const moe_layer_args& q, int T, vo
   a.E = h->cfg.num_experts;
   a.H = q.H;
   a.I = q.I;
+  a.act = q.act;
   a.flags = h->flags;
   const bool fp8 = q.weight_dtype == MOE_E4M3;
-  const dim3 grid(2 * h->num_sms), block(kThreads);
-  cudaError_t e = fp8 ? launch_chained(layer_up_kernel<true>, grid, block, 0, s, false, a, q.act)
-                      : launch_chained(layer_up_kernel<false>, grid, block, 0, s, false, a, q.act);
-  if (e != cudaSuccess) return e;
-  return fp8 ? launch_chained(layer_down_kernel<true>, grid, block, 0, s, false, a)
-             : launch_chained(layer_down_kernel<false>, grid, block, 0, s, false, a);
+  const bool many = static_cast<int64_t>(T) * K > 6 * static_cast<int64_t>(a.E);
+  cudaError_t e;
+  if (many) {
+    e = fp8 ? launch_shape<Shape<2, 4, 1, 3, true, true>>(h, a, s)
+            : launch_shape<Shape<2, 4, 1, 5, false, true>>(h, a, s);
+    if (e != cudaSuccess) return e;
+    e = fp8 ? launch_shape<Shape<2, 4, 1, 2, true, false>>(h, a, s)
+            : launch_shape<Shape<2, 4, 1, 3, false, false>>(h, a, s);
+  } else {
+    e = fp8 ? launch_shape<Shape<1, 1, 2, 3, true, true>>(h, a, s)
+            : launch_shape<Shape<1, 1, 2, 4, false, true>>(h, a, s);
+    if (e != cudaSuccess) return e;
+    e = fp8 ? launch_shape<Shape<1, 1, 1, 4, true, false>>(h, a, s)
+            : launch_shape<Shape<1, 1, 2, 3, false, false>>(h, a, s);
+  }
+  return e != cudaSuccess ? e : launch_combine_layer(a, s);
 }
 
 }  // namespace moe
