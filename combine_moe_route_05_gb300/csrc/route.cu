@@ -68,11 +68,14 @@ struct RouteArgs {
   int32_t* idx;
   float* w;
   const int32_t* live;  // rows at and behind *live are neither read nor written (NULL: all T)
+  uint32_t* zeroed;     // barrier counters of the kernel behind this one, or NULL
   uint32_t* flags;
 };
 
-// The tokens to route: T, or the device's count of live ones.
+// The tokens to route: T, or the device's count of live ones.  Called once, at
+// the start: also clears the counters of the kernel behind this one.
 __device__ __forceinline__ int live_tokens(const RouteArgs& a) {
+  if (a.zeroed && blockIdx.x == 0 && threadIdx.x < kLayerCounters) a.zeroed[threadIdx.x] = 0;
   return a.live ? min(max(*a.live, 0), a.T) : a.T;
 }
 
@@ -1319,7 +1322,8 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_bwd_full_softmax_kerne
 }  // namespace
 
 cudaError_t launch_route_topk(const moe_handle* h, const float* logits, const float* bias, int T,
-                              int32_t* idx, float* w, cudaStream_t s, const int32_t* live) {
+                              int32_t* idx, float* w, cudaStream_t s, const int32_t* live,
+                              uint32_t* zeroed) {
   const moe_config& c = h->cfg;
   RouteArgs a;
   a.logits = logits;
@@ -1342,6 +1346,7 @@ cudaError_t launch_route_topk(const moe_handle* h, const float* logits, const fl
   a.idx = idx;
   a.w = w;
   a.live = live;
+  a.zeroed = zeroed;
   a.flags = h->flags;
   if (T == 0) return cudaSuccess;
 
