@@ -42,7 +42,7 @@ int resident_blocks(const void* kernel, int threads, size_t smem);
 
 // live: device count of tokens to route (NULL: all T); zeroed: kLayerCounters
 // words that the kernel clears for the kernel behind it, or NULL
-constexpr int kLayerCounters = 3;
+constexpr int kLayerCounters = 4;
 cudaError_t launch_route_topk(const moe_handle* h, const float* logits, const float* bias, int T,
                               int32_t* idx, float* w, cudaStream_t s,
                               const int32_t* live = nullptr, uint32_t* zeroed = nullptr);
@@ -111,7 +111,7 @@ cudaError_t launch_act_rows_bwd(const moe_handle* h, const void* ghs, const void
 // offsets of the activations, the fp32 output rows, the fp16 tokens and their
 // factors, the activations' maxima and the barrier counters.
 struct LayerPlan {
-  size_t a, y, x16, xscale, amax, arrived, total;
+  size_t a, a32, y, x16, xscale, amax, arrived, total;
 };
 LayerPlan layer_plan(int T, int K, int S, int H, int I);
 cudaError_t launch_layer(const moe_handle* h, const moe_layer_args& q, int T, void* workspace,

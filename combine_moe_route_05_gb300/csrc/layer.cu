@@ -46,13 +46,10 @@
 namespace moe {
 namespace {
 
-constexpr int kThreads = 512;
-constexpr int kWarps = kThreads / 32;
 constexpr int kMaxEntries = MOE_LAYER_MAX_TOKENS * (MOE_MAX_TOPK + MOE_LAYER_MAX_SHARED);
 constexpr int kMaxExperts = MOE_MAX_EXPERTS + MOE_LAYER_MAX_SHARED;
 constexpr unsigned kFull = 0xffffffffu;
 constexpr uint16_t kNone = 0xffff;
-constexpr int kSlotBytes = kThreads * 16;  // 16 bytes per lane
 constexpr int kQueueBytes = 192 * 1024;
 
 struct LayerArgs {
@@ -66,8 +63,8 @@ struct LayerArgs {
   const float* s2;
   __half* x16;           // [T, H] scaled x (e4m3)
   float* xscale;         // [T] 1 / its factor (e4m3)
-  uint8_t* a;            // bf16 weights: bf16 [2][T (K + S), I], high and low part;
-                         // e4m3: fp32 [T (K + S), I]
+  uint8_t* a;            // bf16 [2][T (K + S), I], high and low part; e4m3: fp16, scaled
+  float* a32;            // [T (K + S), I] (e4m3)
   uint32_t* amax;        // [T (K + S)] bits of the largest |a| of an entry (e4m3)
   float* y;              // [T (K + S), H]
   uint32_t* arrived;     // blocks that reached each grid barrier, zero at the start
@@ -96,9 +93,11 @@ struct Groups {
 
 __host__ __device__ constexpr size_t up16(size_t b) { return (b + 15) / 16 * 16; }
 
+constexpr int kMaxWarps = 16;
+
 __host__ __device__ constexpr size_t groups_bytes(int T, int KS, int n_exp) {
   return 2 * up16(2ull * T * KS) + up16(2ull * n_exp) + 2 * up16(4ull * n_exp) +
-         up16(4ull * (kWarps + 1));
+         up16(4ull * (kMaxWarps + 1));
 }
 
 __device__ __forceinline__ int expert_of(const LayerArgs& a, int entry) {
@@ -108,7 +107,8 @@ __device__ __forceinline__ int expert_of(const LayerArgs& a, int entry) {
   return static_cast<unsigned>(e) < static_cast<unsigned>(a.E) ? e + a.S : e == -1 ? -1 : -2;
 }
 
-__device__ void group_entries(const LayerArgs& a, Groups& g, uint8_t* smem) {
+template <int kThreads>
+__device__ __forceinline__ void group_entries(const LayerArgs& a, Groups& g, uint8_t* smem) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int n_exp = a.E + a.S, KS = a.K + a.S;
   g.order = reinterpret_cast<uint16_t*>(smem);
@@ -182,14 +182,14 @@ __device__ void group_entries(const LayerArgs& a, Groups& g, uint8_t* smem) {
       if (g.cnt[e]) g.slot_expert[at >> 16] = static_cast<uint16_t>(e);
     }
   }
-  if (tid == kThreads - 1) g.head[kWarps] = (base + sum) >> 16;
+  if (tid == kThreads - 1) g.head[kMaxWarps] = (base + sum) >> 16;
   __syncthreads();
 #pragma unroll
   for (int j = 0; j < kMine; ++j) {
     const int i = tid + j * kThreads;
     if (i < n && g.rank[i] != kNone) g.order[g.start[mine[j]] + g.rank[i]] = static_cast<uint16_t>(i);
   }
-  g.nslots = g.head[kWarps];
+  g.nslots = g.head[kMaxWarps];
   __syncthreads();
 }
 
@@ -202,13 +202,19 @@ __device__ __forceinline__ unsigned long long global_ns() {
   return t;
 }
 
-// Waits until every block of the grid has come here; false, with the status
-// bit set, after the handle's limit.
-__device__ __forceinline__ bool grid_barrier(const LayerArgs& a, uint32_t* arrived, int* ok) {
+// This block is done with what the others wait for.
+__device__ __forceinline__ void grid_arrive(uint32_t* arrived) {
   __syncthreads();
   if (threadIdx.x == 0) {
     __threadfence();
     atomicAdd(arrived, 1u);
+  }
+}
+
+// Waits until every block of the grid has arrived; false, with the status bit
+// set, after the handle's limit.
+__device__ __forceinline__ bool grid_wait(const LayerArgs& a, uint32_t* arrived, int* ok) {
+  if (threadIdx.x == 0) {
     const unsigned long long t0 = global_ns();
     bool done = true;
     for (;;) {
@@ -231,17 +237,20 @@ __device__ __forceinline__ bool grid_barrier(const LayerArgs& a, uint32_t* arriv
 // ---------------------------------------------------------------------------
 // copies and products
 
-// Asynchronous copies of 16 bytes into shared memory; !valid writes zeros and
-// reads nothing.  Weights pass by L1, tokens are kept in it.
+// Asynchronous copies of 16 bytes into shared memory; where !valid, zeros are
+// written and nothing is read.  Weights pass by L1, tokens are kept in it.
 __device__ __forceinline__ void copy16_stream(uint32_t dst, const void* src, bool valid) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
                "r"(valid ? 16 : 0)
                : "memory");
 }
-__device__ __forceinline__ void copy16_keep(uint32_t dst, const void* src, bool valid) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
-               "r"(valid ? 16 : 0)
-               : "memory");
+// Nothing at all where !any (predicated, since the lanes of a warp differ).
+__device__ __forceinline__ void copy16_keep(uint32_t dst, const void* src, bool valid, bool any) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.s32 p, %3, 0;\n\t"
+      "@p cp.async.ca.shared.global [%0], [%1], 16, %2;\n\t}" ::"r"(dst),
+      "l"(src), "r"(valid ? 16 : 0), "r"(static_cast<int>(any))
+      : "memory");
 }
 __device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -255,6 +264,16 @@ __device__ __forceinline__ Vec16 lds16(uint32_t p) {
                : "r"(p)
                : "memory");
   return v;
+}
+
+// 16 bytes of shared memory where `any`; else v keeps what it holds.
+__device__ __forceinline__ void lds16_if(Vec16& v, uint32_t p, bool any) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.s32 p, %5, 0;\n\t"
+      "@p ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];\n\t}"
+      : "+r"(v.u[0]), "+r"(v.u[1]), "+r"(v.u[2]), "+r"(v.u[3])
+      : "r"(p), "r"(static_cast<int>(any))
+      : "memory");
 }
 
 template <bool F16>
@@ -301,21 +320,24 @@ __device__ __forceinline__ float act_value(float g, int act) {
   return c < -80.0f ? g * 0.0f : g * __fdividef(1.0f, 1.0f + __expf(-c));
 }
 
-// MT tiles of 16 weight rows by NT tiles of 8 tokens a job.
-template <int MT_, int NT_, bool FP8_>
+// MT tiles of 16 weight rows by NT tiles of 8 tokens a job; a stage of the
+// queue holds STEPS steps of 64 bytes of each weight row.
+template <int THREADS_, int MT_, int NT_, int STEPS_, bool FP8_>
 struct Shape {
-  static constexpr int MT = MT_, NT = NT_;
+  static constexpr int kThreads = THREADS_, kWarps = THREADS_ / 32;
+  static constexpr int MT = MT_, NT = NT_, kSteps = STEPS_;
   static constexpr bool FP8 = FP8_;
-  // token vectors beside a weight vector: x, or a's two bf16 parts or fp32
-  static constexpr int kVecUp = FP8 ? 2 : 1, kVecDown = FP8 ? 4 : 2;
-  static constexpr int kSlotsUp = 2 * MT + NT * kVecUp, kSlotsDown = 2 * MT + NT * kVecDown;
-  static constexpr int kStagesUp = kQueueBytes / (kSlotsUp * kSlotBytes);
-  static constexpr int kStagesDown = kQueueBytes / (kSlotsDown * kSlotBytes);
-  static constexpr size_t kRedBytes = static_cast<size_t>(kWarps) * MT * NT * 4 * 32 * 4;
+  static constexpr int kSlotBytes = kThreads * 16;  // 16 bytes per lane
+  // token vectors beside a weight vector: x, or a's two parts; fp16 in e4m3
+  static constexpr int kVecUp = FP8 ? 2 : 1, kVecDown = 2;
+  static constexpr int kStageUp = kSteps * (2 * MT + NT * kVecUp) * kSlotBytes;
+  static constexpr int kStageDown = kSteps * (2 * MT + NT * kVecDown) * kSlotBytes;
+  static constexpr size_t kRedBytes = static_cast<size_t>(kWarps) * NT * 4 * 32 * 4;
   static constexpr size_t smem(int T, int KS, int n_exp) {
-    return kQueueBytes + kRedBytes + groups_bytes(T, KS, n_exp) + (FP8 ? up16(4ull * T * KS) : 0);
+    return kQueueBytes + kRedBytes + groups_bytes(T, KS, n_exp);
   }
-  static_assert(kStagesUp >= 2 && kStagesDown >= 2, "queue");
+  static_assert(kWarps <= kMaxWarps && 2 * kStageUp <= kQueueBytes && 2 * kStageDown <= kQueueBytes,
+                "queue");
   static_assert(smem(MOE_LAYER_MAX_TOKENS, MOE_MAX_TOPK + MOE_LAYER_MAX_SHARED, kMaxExperts) <=
                     227 * 1024, "shared memory budget");
 };
@@ -327,46 +349,39 @@ struct Job {
 };
 
 // The products of one phase (up or down) for one thread.
-template <typename S>
+template <typename S, bool UP>
 struct Phase {
+  static constexpr int MT = S::MT, NT = S::NT, kWarps = S::kWarps;
+  static constexpr bool FP8 = S::FP8;
+  static constexpr int kEb = FP8 ? 1 : 2;
+  static constexpr int kRowBytes = 64 * S::kSteps;      // of a weight row in a stage
+  static constexpr int kVec = UP ? S::kVecUp : S::kVecDown;
+  static constexpr int kStageBytes = UP ? S::kStageUp : S::kStageDown;
+  static constexpr int kStages = kQueueBytes / kStageBytes;
+  static constexpr int kStepSlots = 2 * MT + NT * kVec;
+  static constexpr int kRows = UP ? 8 : 16;  // outputs that 16 weight rows give
+
   const LayerArgs& a;
   const Groups& g;
-  bool up;
-  uint32_t queue;   // shared-memory address of this lane's queue
-  int tiles, kd, steps, nq;
-  int rows;         // outputs a tile of 16 weight rows gives: 8 (up) or 16
-  int limit;        // outputs in all
+  uint32_t queue;  // shared-memory address of this lane's queue
+  int kd, tiles, limit, stages, nq;
   int lane, warp, team, part, first_q, stride_q;
-  int stage_bytes;
-  int64_t half;     // bytes from a lane's first weight row to its second
-  const uint8_t* weights;
-  const float* scales;
-  int scale_rows, scale_cols;
-  static constexpr int kEb = S::FP8 ? 1 : 2;
-  static constexpr int kStep = 64 / kEb;  // k of a step: 64 bytes of a weight row
 
-  __device__ __forceinline__ Phase(const LayerArgs& args, const Groups& groups, uint8_t* smem,
-                                   bool is_up)
-      : a(args), g(groups), up(is_up), lane(threadIdx.x & 31), warp(threadIdx.x >> 5) {
+  __device__ __forceinline__ Phase(const LayerArgs& args, const Groups& groups, uint8_t* smem)
+      : a(args), g(groups), lane(threadIdx.x & 31), warp(threadIdx.x >> 5) {
     queue = smem_addr(smem) + threadIdx.x * 16;
-    kd = up ? a.H : a.I;
-    rows = up ? 8 : 16;
-    limit = up ? a.I : a.H;
-    tiles = (limit + rows * S::MT - 1) / (rows * S::MT);
-    steps = (kd + kStep - 1) / kStep;
+    kd = UP ? a.H : a.I;
+    limit = UP ? a.I : a.H;
+    tiles = (limit + kRows * MT - 1) / (kRows * MT);
+    stages = (kd * kEb + kRowBytes - 1) / kRowBytes;
     nq = g.nslots * tiles;
-    stage_bytes = (up ? S::kSlotsUp : S::kSlotsDown) * kSlotBytes;
-    half = static_cast<int64_t>(up ? a.I : 8) * kd * kEb;
-    weights = up ? a.w13 : a.w2;
-    scales = up ? a.s13 : a.s2;
-    scale_rows = ((up ? 2 * a.I : a.H) + 127) / 128;
-    scale_cols = (kd + 127) / 128;
-    // rounds of jobs over the grid, in units of a one-warp job
+    // the team size with the fewest rounds of jobs over the grid, in units of
+    // a one-warp job
     team = 1;
     const int warps = kWarps * gridDim.x;
     float best = 0.0f;
 #pragma unroll 1
-    for (int n = 1; n <= 8 && n <= steps; n *= 2) {
+    for (int n = 1; n <= 8 && n <= stages; n *= 2) {
       const float cost = static_cast<float>((nq * n + warps - 1) / warps) / n;
       if (n == 1 || cost < best) {
         best = cost;
@@ -384,187 +399,171 @@ struct Phase {
     return Job{q, slot, q - slot * tiles, 0};
   }
   __device__ __forceinline__ Job next(const Job& j) const {
-    if (j.c0 + 8 * S::NT < g.cnt[g.slot_expert[j.slot]])
-      return Job{j.q, j.slot, j.tile, j.c0 + 8 * S::NT};
+    if (j.c0 + 8 * NT < g.cnt[g.slot_expert[j.slot]]) return Job{j.q, j.slot, j.tile, j.c0 + 8 * NT};
     return at(j.q + stride_q);
   }
+  // Whether tile mt of the job has outputs, and a second half (down).
+  __device__ __forceinline__ bool has_rows(const Job& j, int mt) const {
+    return MT == 1 || (j.tile * MT + mt) * kRows < limit;
+  }
 
-  // Where the next copies of this warp come from.
+  // Where this lane's next copies come from.
   struct Cursor {
     Job j;
-    int step;
-    const uint8_t* row;        // the lane's first weight row
-    const uint8_t* col[S::NT]; // its token's values per token tile, NULL: none
+    int o;                  // byte of the weight rows, of the lane's 16
+    const uint8_t* row;     // the lane's first weight row, from byte o on
+    int64_t half;           // from it to the lane's second row
+    const uint8_t* col[NT]; // its token's values per token tile, NULL: none
   };
 
   __device__ __forceinline__ void open(Cursor& c) const {
     if (!valid(c.j)) return;
     const int p = g.slot_expert[c.j.slot];
     const int e = p < a.S ? a.E + p : p - a.S;
-    c.row = weights + (static_cast<int64_t>(e) * (up ? 2 * a.I : a.H) + c.j.tile * rows * S::MT +
-                       (lane >> 2)) * kd * kEb;
+    const int r0 = c.j.tile * kRows * MT;
+    c.o = part * kRowBytes + (lane & 3) * 16;
+    c.row = (UP ? a.w13 : a.w2) +
+            (static_cast<int64_t>(e) * (UP ? 2 * a.I : a.H) + r0 + (lane >> 2)) * kd * kEb + c.o;
+    // the last tile of the down products may have no second half: it reads
+    // the first again, and its results go nowhere
+    c.half = static_cast<int64_t>(UP ? a.I : MT == 1 && r0 + 8 >= limit ? 0 : 8) * kd * kEb;
     const int cnt = g.cnt[p], at = g.start[p];
+    const uint8_t* src = UP ? (FP8 ? reinterpret_cast<const uint8_t*>(a.x16) : a.x) : a.a;
 #pragma unroll
-    for (int nt = 0; nt < S::NT; ++nt) {
+    for (int nt = 0; nt < NT; ++nt) {
       const int n = c.j.c0 + nt * 8 + (lane >> 2);
       c.col[nt] = nullptr;
-      if (n >= cnt) continue;
-      const int entry = g.order[at + n];
-      if (up)
-        c.col[nt] = (S::FP8 ? reinterpret_cast<const uint8_t*>(a.x16) : a.x) +
-                    static_cast<int64_t>(entry / (a.K + a.S)) * kd * 2;
-      else
-        c.col[nt] = a.a + static_cast<int64_t>(entry) * kd * (S::FP8 ? 4 : 2);
+      if (n < cnt) {
+        const int entry = g.order[at + n];
+        c.col[nt] = src + static_cast<int64_t>(UP ? entry / (a.K + a.S) : entry) * kd * 2 + c.o * (2 / kEb);
+      }
     }
   }
   __device__ __forceinline__ Cursor begin() const {
     Cursor c;
     c.j = at(first_q);
-    c.step = part;
     open(c);
     return c;
   }
   __device__ __forceinline__ void advance(Cursor& c) const {
-    if (!valid(c.j)) return;
-    c.step += team;
-    if (c.step < steps) return;
-    c.step = part;
+    const int step = team * kRowBytes;
+    c.o += step;
+    if (c.o - (lane & 3) * 16 < kd * kEb) {
+      c.row += step;
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+        if (c.col[nt]) c.col[nt] += step * (2 / kEb);
+      return;
+    }
     c.j = next(c.j);
     open(c);
   }
 
-  __device__ __forceinline__ void copy_weights(const Cursor& c, int stage) const {
-    if (!valid(c.j)) return;
-    const uint32_t dst = queue + stage * stage_bytes;
-    const int o = c.step * 64 + (lane & 3) * 16;
-    const bool in = o < kd * kEb;
+  __device__ __forceinline__ void copy_weights(const Cursor& c, uint32_t dst) const {
 #pragma unroll
-    for (int mt = 0; mt < S::MT; ++mt) {
-      const int r = (c.j.tile * S::MT + mt) * rows;  // outputs come in whole eights
-      const uint8_t* p = c.row + static_cast<int64_t>(mt * rows) * kd * kEb + o;
-      const bool ok0 = in && r < limit, ok1 = ok0 && (up || r + 8 < limit);
-      copy16_stream(dst + (2 * mt) * kSlotBytes, ok0 ? p : c.row, ok0);
-      copy16_stream(dst + (2 * mt + 1) * kSlotBytes, ok1 ? p + half : c.row, ok1);
+    for (int st = 0; st < S::kSteps; ++st) {
+      const bool in = c.o + st * 64 < kd * kEb;
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt) {
+        const uint32_t d = dst + (st * kStepSlots + 2 * mt) * S::kSlotBytes;
+        // a tile without outputs reads the first again
+        const bool rows = has_rows(c.j, mt);
+        const bool second = UP || MT == 1 || (c.j.tile * MT + mt) * 16 + 8 < limit;
+        const uint8_t* p = c.row + (rows ? static_cast<int64_t>(mt * kRows) * kd * kEb : 0);
+        copy16_stream(d, p + st * 64, in);
+        copy16_stream(d + S::kSlotBytes, p + (second ? c.half : 0) + st * 64, in);
+      }
     }
   }
-  __device__ __forceinline__ void copy_tokens(const Cursor& c, int stage) const {
-    if (!valid(c.j)) return;
-    const uint32_t dst = queue + stage * stage_bytes + 2 * S::MT * kSlotBytes;
-    const int k = c.step * kStep + (lane & 3) * (16 / kEb);
-    const bool in = k < kd;
-    const int bytes = k * (S::FP8 && !up ? 4 : 2);
+  __device__ __forceinline__ void copy_tokens(const Cursor& c, uint32_t dst) const {
     // the second vector: the next 16 bytes, or a's low part
-    const int64_t second = S::FP8 ? 16 : static_cast<int64_t>(a.T) * (a.K + a.S) * kd * 2;
+    const int64_t second = FP8 ? 16 : static_cast<int64_t>(a.T) * (a.K + a.S) * kd * 2;
 #pragma unroll
-    for (int nt = 0; nt < S::NT; ++nt) {
-      const bool ok = in && c.col[nt];
-      const uint8_t* p = ok ? c.col[nt] + bytes : weights;
-      const uint32_t d = dst + nt * (up ? S::kVecUp : S::kVecDown) * kSlotBytes;
-      copy16_keep(d, p, ok);
-      if (S::FP8 || !up) copy16_keep(d + kSlotBytes, ok ? p + second : p, ok);
-      if (S::FP8 && !up) {
-        copy16_keep(d + 2 * kSlotBytes, ok ? p + 32 : p, ok);
-        copy16_keep(d + 3 * kSlotBytes, ok ? p + 48 : p, ok);
+    for (int st = 0; st < S::kSteps; ++st) {
+      const bool in = c.o + st * 64 < kd * kEb;
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        const bool any = c.col[nt] != nullptr;
+        const uint32_t d = dst + (st * kStepSlots + 2 * MT + nt * kVec) * S::kSlotBytes;
+        copy16_keep(d, c.col[nt] + st * (128 / kEb), in, any);
+        if (kVec == 2) copy16_keep(d + S::kSlotBytes, c.col[nt] + second + st * (128 / kEb), in, any);
       }
     }
   }
 
-  // acc += the products of one step.  factor[nt]: what brings the lane's
-  // entry to fp16; sc0 / sc1: block scales of the lane's accumulator rows.
-  __device__ __forceinline__ void products(float (&acc)[S::MT][S::NT][4], int stage,
-                                           const float (&factor)[S::NT],
-                                           const float (&sc)[S::MT][2]) const {
-    const uint32_t at = queue + stage * stage_bytes;
-    constexpr int kWords = S::FP8 ? 8 : 4;  // operand words of the lane's token
-    uint32_t b[S::NT][S::FP8 ? 1 : 2][kWords];
+  // acc += the products of one stage.  has: bit nt: the lane has a token in
+  // tile nt (without one its operand registers and columns mean nothing);
+  // sc: block scales of the lane's accumulator rows.
+  __device__ __forceinline__ void products(float (&acc)[MT][NT][4], uint32_t at, uint32_t has,
+                                           const float (&sc)[MT][2]) const {
+    float sum[FP8 ? MT : 1][NT][4] = {};
 #pragma unroll
-    for (int nt = 0; nt < S::NT; ++nt) {
-      const uint32_t d = at + (2 * S::MT + nt * (up ? S::kVecUp : S::kVecDown)) * kSlotBytes;
-      if (!S::FP8) {
-        const Vec16 hi = lds16(d);
+    for (int st = 0; st < S::kSteps; ++st) {
+      const uint32_t from = at + st * kStepSlots * S::kSlotBytes;
+      Vec16 b[NT][kVec];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) b[nt][0][i] = hi.u[i];
-        if (!up) {
-          const Vec16 lo = lds16(d + kSlotBytes);
+      for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) b[nt][S::FP8 ? 0 : 1][i] = lo.u[i];
-        }
-      } else if (up) {
+        for (int v = 0; v < kVec; ++v)
+          lds16_if(b[nt][v], from + (2 * MT + nt * kVec + v) * S::kSlotBytes, (has >> nt) & 1u);
 #pragma unroll
-        for (int v = 0; v < 2; ++v) {
-          const Vec16 x = lds16(d + v * kSlotBytes);
+      for (int mt = 0; mt < MT; ++mt) {
+        const Vec16 w0 = lds16(from + (2 * mt) * S::kSlotBytes);
+        const Vec16 w1 = lds16(from + (2 * mt + 1) * S::kSlotBytes);
+        if (!FP8) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) b[nt][0][(v * 4 + i) % kWords] = x.u[i];
-        }
-      } else {
+          for (int q = 0; q < 4; q += 2)
 #pragma unroll
-        for (int v = 0; v < 4; ++v) {
-          const Vec16 f = lds16(d + v * kSlotBytes);
+            for (int v = 0; v < kVec; ++v)
 #pragma unroll
-          for (int i = 0; i < 2; ++i)
-            b[nt][0][(v * 2 + i) % kWords] = f16x2(__uint_as_float(f.u[2 * i]) * factor[nt],
-                                                   __uint_as_float(f.u[2 * i + 1]) * factor[nt]);
+              for (int nt = 0; nt < NT; ++nt)
+                mma<false>(acc[mt][nt], w0.u[q], w1.u[q], w0.u[q + 1], w1.u[q + 1], b[nt][v].u[q],
+                           b[nt][v].u[q + 1]);
+        } else {
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            uint32_t a0, a1, a2, a3;
+            f16_of_e4m3(w0.u[q], a0, a2);
+            f16_of_e4m3(w1.u[q], a1, a3);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+              mma<true>(sum[FP8 ? mt : 0][nt], a0, a1, a2, a3, b[nt][(q / 2) % kVec].u[q % 2 * 2],
+                        b[nt][(q / 2) % kVec].u[q % 2 * 2 + 1]);
+          }
         }
       }
     }
+    if (FP8) {
 #pragma unroll
-    for (int mt = 0; mt < S::MT; ++mt) {
-      const Vec16 w0 = lds16(at + (2 * mt) * kSlotBytes);
-      const Vec16 w1 = lds16(at + (2 * mt + 1) * kSlotBytes);
-      if (!S::FP8) {
+      for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-        for (int q = 0; q < 4; q += 2)
+        for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int nt = 0; nt < S::NT; ++nt) {
-            mma<false>(acc[mt][nt], w0.u[q], w1.u[q], w0.u[q + 1], w1.u[q + 1], b[nt][0][q],
-                       b[nt][0][q + 1]);
-            if (!up)
-              mma<false>(acc[mt][nt], w0.u[q], w1.u[q], w0.u[q + 1], w1.u[q + 1],
-                         b[nt][S::FP8 ? 0 : 1][q], b[nt][S::FP8 ? 0 : 1][q + 1]);
-          }
-      } else {
-        float sum[S::NT][4] = {};
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          uint32_t a0, a1, a2, a3;
-          f16_of_e4m3(w0.u[q], a0, a2);
-          f16_of_e4m3(w1.u[q], a1, a3);
-#pragma unroll
-          for (int nt = 0; nt < S::NT; ++nt)
-            mma<true>(sum[nt], a0, a1, a2, a3, b[nt][0][(2 * q) % kWords],
-                      b[nt][0][(2 * q + 1) % kWords]);
-        }
-#pragma unroll
-        for (int nt = 0; nt < S::NT; ++nt) {
-          acc[mt][nt][0] = fmaf(sc[mt][0], sum[nt][0], acc[mt][nt][0]);
-          acc[mt][nt][1] = fmaf(sc[mt][0], sum[nt][1], acc[mt][nt][1]);
-          acc[mt][nt][2] = fmaf(sc[mt][1], sum[nt][2], acc[mt][nt][2]);
-          acc[mt][nt][3] = fmaf(sc[mt][1], sum[nt][3], acc[mt][nt][3]);
-        }
-      }
+          for (int r = 0; r < 4; ++r)
+            acc[mt][nt][r] = fmaf(sc[mt][r / 2], sum[FP8 ? mt : 0][nt][r], acc[mt][nt][r]);
     }
   }
 
   // One result pair of entry `entry`: up: gate and up of output `row`; down:
   // outputs row and row + 8.
-  __device__ __forceinline__ void store(int entry, int row, float v0, float v1,
-                                        const float* inverse) const {
+  __device__ __forceinline__ void store(int entry, int row, float v0, float v1) const {
     if (row >= limit) return;
     const int KS = a.K + a.S;
-    if (!up) {
-      if (S::FP8) {
-        v0 *= inverse[entry];
-        v1 *= inverse[entry];
+    if (!UP) {
+      if (FP8) {
+        const float f = 1.0f / f16_factor(__ldcg(a.amax + entry));
+        v0 *= f;
+        v1 *= f;
       }
       float* y = a.y + static_cast<int64_t>(entry) * a.H + row;
       y[0] = v0;
       if (row + 8 < limit) y[8] = v1;
       return;
     }
-    if (S::FP8) {
+    if (FP8) {
       const float f = __ldcg(a.xscale + entry / KS);
       const float h = act_value(v0 * f, a.act) * (v1 * f);
-      reinterpret_cast<float*>(a.a)[static_cast<int64_t>(entry) * a.I + row] = h;
+      a.a32[static_cast<int64_t>(entry) * a.I + row] = h;
       // a maximum does not depend on the order
       atomicMax(a.amax + entry, __float_as_uint(h) & 0x7fffffffu);
     } else {
@@ -576,14 +575,122 @@ struct Phase {
       dst[static_cast<int64_t>(a.T) * KS * a.I] = __float2bfloat16_rn(isfinite(rest) ? rest : 0.0f);
     }
   }
+
+  static __device__ __forceinline__ void team_sync(int id, int threads) {
+    asm volatile("bar.sync %0, %1;" ::"r"(id + 1), "r"(threads) : "memory");
+  }
+
+  // The first stages' weights.
+  __device__ __forceinline__ void start(Cursor c) const {
+#pragma unroll 1
+    for (int s = 0; s < kStages && valid(c.j); ++s) {
+      copy_weights(c, queue + s * kStageBytes);
+      advance(c);
+    }
+  }
+
+  // Everything else.
+  __device__ __forceinline__ void run(Cursor& next_copy, float* red) const {
+#pragma unroll 1
+    for (int s = 0; s < kStages; ++s) {
+      if (valid(next_copy.j)) {
+        copy_tokens(next_copy, queue + s * kStageBytes);
+        advance(next_copy);
+      }
+      copies_commit();
+    }
+    uint32_t at = queue;
+#pragma unroll 1
+    for (Job j = this->at(first_q); valid(j); j = next(j)) {
+      const int p = g.slot_expert[j.slot];
+      const int cnt = g.cnt[p], begin = g.start[p];
+      uint32_t has = 0;
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) has |= (j.c0 + nt * 8 + (lane >> 2) < cnt ? 1u : 0u) << nt;
+      const float* scale[MT][2] = {};
+      float held[MT][2] = {}, sc[MT][2] = {};
+      const int scale_cols = (kd + 127) / 128;
+      if (FP8) {
+        const int e = p < a.S ? a.E + p : p - a.S;
+        const float* base = (UP ? a.s13 : a.s2) +
+                            static_cast<int64_t>(e) * (((UP ? 2 * a.I : a.H) + 127) / 128) * scale_cols;
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+          const int r = min((j.tile * MT + mt) * kRows, limit - 8);
+          scale[mt][0] = base + static_cast<int64_t>(r / 128) * scale_cols;
+          scale[mt][1] = UP ? base + static_cast<int64_t>((a.I + r) / 128) * scale_cols : scale[mt][0];
+        }
+      }
+      float acc[MT][NT][4] = {};
+      int window = -1;  // the 32 k blocks whose scales the lanes hold
+#pragma unroll 1
+      for (int st = part; st < stages; st += team) {
+        if (FP8) {
+          const int block = st * S::kSteps / 2;
+          if (block / 32 != window) {
+            window = block / 32;
+            const int b = min(window * 32 + lane, scale_cols - 1);
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) {
+              held[mt][0] = __ldg(scale[mt][0] + b);
+              if (UP) held[mt][1] = __ldg(scale[mt][1] + b);
+            }
+          }
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt) {
+            sc[mt][0] = __shfl_sync(kFull, held[mt][0], block % 32);
+            sc[mt][1] = UP ? __shfl_sync(kFull, held[mt][1], block % 32) : sc[mt][0];
+          }
+        }
+        copies_wait<kStages - 1>();
+        products(acc, at, has, sc);
+        // the products have read the stage; its next contents
+        if (valid(next_copy.j)) {
+          copy_weights(next_copy, at);
+          copy_tokens(next_copy, at);
+          advance(next_copy);
+        }
+        copies_commit();
+        at = at + kStageBytes == queue + kStages * kStageBytes ? queue : at + kStageBytes;
+      }
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt) {
+        if (team > 1) {  // the team's partial sums, added in warp order
+          const int id = warp / team;
+          team_sync(id, team * 32);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+              red[((warp * NT + nt) * 4 + r) * 32 + lane] = acc[mt][nt][r];
+          team_sync(id, team * 32);
+        }
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          if ((mt * NT + nt) % team != part) continue;
+          float (&v)[4] = acc[mt][nt];
+          if (team > 1) {
+#pragma unroll
+            for (int r = 0; r < 4; ++r) v[r] = 0.0f;
+#pragma unroll 2
+            for (int wv = warp - part; wv < warp - part + team; ++wv)
+#pragma unroll
+              for (int r = 0; r < 4; ++r) v[r] += red[((wv * NT + nt) * 4 + r) * 32 + lane];
+          }
+          const int n = j.c0 + nt * 8 + 2 * (lane & 3);
+          const int row = (j.tile * MT + mt) * kRows + (lane >> 2);
+          if (n < cnt) store(g.order[begin + n], row, v[0], v[2]);
+          if (n + 1 < cnt) store(g.order[begin + n + 1], row, v[1], v[3]);
+        }
+      }
+    }
+    copies_wait<0>();
+  }
 };
 
-__device__ __forceinline__ void team_sync(int id, int threads) {
-  asm volatile("bar.sync %0, %1;" ::"r"(id + 1), "r"(threads) : "memory");
-}
-
 // fp16 copies of x and their factors: a block per token.
-__device__ void scale_tokens(const LayerArgs& a, int tokens, float* red) {
+template <int kThreads>
+__device__ __forceinline__ void scale_tokens(const LayerArgs& a, int tokens, uint32_t* red) {
   for (int t = blockIdx.x; t < tokens; t += gridDim.x) {
     const uint8_t* row = a.x + static_cast<int64_t>(t) * a.H * 2;
     uint32_t m = 0;  // the largest |x|, as bits of a bf16 in the high half
@@ -594,10 +701,10 @@ __device__ void scale_tokens(const LayerArgs& a, int tokens, float* red) {
         m = max(m, max(x.u[i] & 0x7fff0000u, (x.u[i] << 16) & 0x7fff0000u));
     }
     m = __reduce_max_sync(kFull, m);
-    if ((threadIdx.x & 31) == 0) reinterpret_cast<uint32_t*>(red)[threadIdx.x >> 5] = m;
+    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = m;
     __syncthreads();
 #pragma unroll
-    for (int i = 0; i < kWarps; ++i) m = max(m, reinterpret_cast<uint32_t*>(red)[i]);
+    for (int i = 0; i < kThreads / 32; ++i) m = max(m, red[i]);
     __syncthreads();
     const float f = f16_factor(m);
     uint8_t* dst = reinterpret_cast<uint8_t*>(a.x16) + static_cast<int64_t>(t) * a.H * 2;
@@ -614,145 +721,70 @@ __device__ void scale_tokens(const LayerArgs& a, int tokens, float* red) {
   }
 }
 
+// fp16 copies of the activations, their factors from the entries' maxima.
+template <int kThreads>
+__device__ __forceinline__ void scale_activations(const LayerArgs& a, const Groups& g) {
+  const int per = a.I / 8;
+  const int64_t n = static_cast<int64_t>(g.tokens) * (a.K + a.S) * per;
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x; i < n;
+       i += static_cast<int64_t>(gridDim.x) * kThreads) {
+    const int entry = static_cast<int>(i / per);
+    if (g.rank[entry] == kNone) continue;
+    const float f = f16_factor(__ldcg(a.amax + entry));
+    const float4* src = reinterpret_cast<const float4*>(a.a32) + 2 * i;
+    const float4 lo = __ldcg(src), hi = __ldcg(src + 1);
+    const Vec16 o{f16x2(lo.x * f, lo.y * f), f16x2(lo.z * f, lo.w * f), f16x2(hi.x * f, hi.y * f),
+                  f16x2(hi.z * f, hi.w * f)};
+    st_vec(a.a + i * 16, o);
+  }
+}
+
 template <typename S>
-__global__ void __launch_bounds__(kThreads, 1) layer_kernel(LayerArgs a) {
+__global__ void __launch_bounds__(S::kThreads, 1) layer_kernel(LayerArgs a) {
+  constexpr int kThreads = S::kThreads;
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ int ok;
   grid_dependency_wait();
   float* red = reinterpret_cast<float*>(smem + kQueueBytes);
-  uint8_t* tables = smem + kQueueBytes + S::kRedBytes;
-  float* inverse = reinterpret_cast<float*>(tables + groups_bytes(a.T, a.K + a.S, a.E + a.S));
   Groups g;
-  group_entries(a, g, tables);
+  group_entries<kThreads>(a, g, smem + kQueueBytes + S::kRedBytes);
   const int KS = a.K + a.S;
-  if (S::FP8) scale_tokens(a, g.tokens, red);
-
-#pragma unroll 1
-  for (int ph = 0; ph < 2; ++ph) {
-    const Phase<S> k(a, g, smem, ph == 0);
-    const int lane = k.lane, warp = k.warp;
-    const int stages = k.up ? S::kStagesUp : S::kStagesDown;
-    typename Phase<S>::Cursor next = k.begin();
-    {
-      typename Phase<S>::Cursor c = next;
-#pragma unroll 1
-      for (int s = 0; s < stages; ++s) {
-        k.copy_weights(c, s);
-        k.advance(c);
-      }
-    }
-    // what the tokens' side reads was written by other blocks
-    if ((S::FP8 || !k.up) && !grid_barrier(a, a.arrived + ph, &ok)) {
+  uint32_t* arrived = a.arrived;  // of the next barrier
+  if (S::FP8) {
+    scale_tokens<kThreads>(a, g.tokens, reinterpret_cast<uint32_t*>(red));
+    grid_arrive(arrived);
+  }
+  {
+    const Phase<S, true> up(a, g, smem);
+    typename Phase<S, true>::Cursor c = up.begin();
+    up.start(c);
+    if (S::FP8 && !grid_wait(a, arrived++, &ok)) {
       copies_wait<0>();
       return;
     }
-    if (S::FP8 && !k.up) {
-      for (int i = threadIdx.x; i < g.tokens * KS; i += kThreads)
-        inverse[i] = 1.0f / f16_factor(__ldcg(a.amax + i));
-      __syncthreads();
-    }
-#pragma unroll 1
-    for (int s = 0; s < stages; ++s) {
-      k.copy_tokens(next, s);
-      copies_commit();
-      k.advance(next);
-    }
-
-    int stage = 0;
-#pragma unroll 1
-    for (Job j = k.at(k.first_q); k.valid(j); j = k.next(j)) {
-      const int p = g.slot_expert[j.slot];
-      const int cnt = g.cnt[p], at = g.start[p];
-      float factor[S::NT] = {};
-      const float* scale[S::MT][2] = {};
-      float held[S::MT][2] = {}, sc[S::MT][2] = {};
-      if (S::FP8) {
-        const int e = p < a.S ? a.E + p : p - a.S;
-        const float* base = k.scales + static_cast<int64_t>(e) * k.scale_rows * k.scale_cols;
-#pragma unroll
-        for (int mt = 0; mt < S::MT; ++mt) {
-          const int r = min((j.tile * S::MT + mt) * k.rows, k.limit - 8);
-          scale[mt][0] = base + static_cast<int64_t>(r / 128) * k.scale_cols;
-          scale[mt][1] = k.up ? base + static_cast<int64_t>((a.I + r) / 128) * k.scale_cols : scale[mt][0];
-        }
-        if (!k.up) {
-#pragma unroll
-          for (int nt = 0; nt < S::NT; ++nt) {
-            const int n = j.c0 + nt * 8 + (lane >> 2);
-            factor[nt] = n < cnt ? 1.0f / inverse[g.order[at + n]] : 0.0f;
-          }
-        }
-      }
-      float acc[S::MT][S::NT][4] = {};
-      int window = -1;  // the 32 k blocks whose scales the lanes hold
-#pragma unroll 1
-      for (int step = k.part; step < k.steps; step += k.team) {
-        if (S::FP8) {
-          const int block = step / 2;
-          if (block / 32 != window) {
-            window = block / 32;
-            const int b = min(window * 32 + lane, k.scale_cols - 1);
-#pragma unroll
-            for (int mt = 0; mt < S::MT; ++mt) {
-              held[mt][0] = __ldg(scale[mt][0] + b);
-              held[mt][1] = __ldg(scale[mt][1] + b);
-            }
-          }
-#pragma unroll
-          for (int mt = 0; mt < S::MT; ++mt) {
-            sc[mt][0] = __shfl_sync(kFull, held[mt][0], block % 32);
-            sc[mt][1] = __shfl_sync(kFull, held[mt][1], block % 32);
-          }
-        }
-        if (k.up) copies_wait<S::kStagesUp - 1>();
-        else copies_wait<S::kStagesDown - 1>();
-        k.products(acc, stage, factor, sc);
-        // the products have read the stage; its next contents
-        k.copy_weights(next, stage);
-        k.copy_tokens(next, stage);
-        copies_commit();
-        k.advance(next);
-        stage = stage + 1 == stages ? 0 : stage + 1;
-      }
-      if (k.team > 1) {  // the team's partial sums, added in warp order
-        const int id = warp / k.team;
-        team_sync(id, k.team * 32);
-#pragma unroll
-        for (int mt = 0; mt < S::MT; ++mt)
-#pragma unroll
-          for (int nt = 0; nt < S::NT; ++nt)
-#pragma unroll
-            for (int r = 0; r < 4; ++r)
-              red[((warp * S::MT * S::NT + mt * S::NT + nt) * 4 + r) * 32 + lane] = acc[mt][nt][r];
-        team_sync(id, k.team * 32);
-      }
-#pragma unroll
-      for (int mt = 0; mt < S::MT; ++mt)
-#pragma unroll
-        for (int nt = 0; nt < S::NT; ++nt) {
-          const int tile = mt * S::NT + nt;
-          if (tile % k.team != k.part) continue;
-          float (&v)[4] = acc[mt][nt];
-          if (k.team > 1) {
-#pragma unroll
-            for (int r = 0; r < 4; ++r) v[r] = 0.0f;
-#pragma unroll 2
-            for (int wv = warp - k.part; wv < warp - k.part + k.team; ++wv)
-#pragma unroll
-              for (int r = 0; r < 4; ++r)
-                v[r] += red[((wv * S::MT * S::NT + tile) * 4 + r) * 32 + lane];
-          }
-          const int n = j.c0 + nt * 8 + 2 * (lane & 3);
-          const int row = (j.tile * S::MT + mt) * k.rows + (lane >> 2);
-          if (n < cnt) k.store(g.order[at + n], row, v[0], v[2], inverse);
-          if (n + 1 < cnt) k.store(g.order[at + n + 1], row, v[1], v[3], inverse);
-        }
-    }
-    copies_wait<0>();
+    up.run(c, red);
   }
+  grid_arrive(arrived);
+  {
+    const Phase<S, false> down(a, g, smem);
+    typename Phase<S, false>::Cursor c = down.begin();
+    down.start(c);
+    bool done = grid_wait(a, arrived++, &ok);
+    if (S::FP8 && done) {
+      scale_activations<kThreads>(a, g);
+      grid_arrive(arrived);
+      done = grid_wait(a, arrived++, &ok);
+    }
+    if (!done) {
+      copies_wait<0>();
+      return;
+    }
+    down.run(c, red);
+  }
+  grid_arrive(arrived);
+  if (!grid_wait(a, arrived, &ok)) return;
 
   // the entries' rows summed per token, a thread per 4 columns
-  if (!grid_barrier(a, a.arrived + 2, &ok)) return;
   const int per = a.H / 4;
   const int64_t n = static_cast<int64_t>(g.tokens) * per;
   for (int64_t i = (static_cast<int64_t>(threadIdx.x >> 5) * gridDim.x + blockIdx.x) * 32 + (threadIdx.x & 31);
@@ -792,7 +824,7 @@ cudaError_t launch_shape(const moe_handle* h, const LayerArgs& a, cudaStream_t s
   const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                              static_cast<int>(smem));
   if (e != cudaSuccess) return e;
-  return launch_chained(k, dim3(h->num_sms), dim3(kThreads), smem, s, true, a);
+  return launch_chained(k, dim3(h->num_sms), dim3(S::kThreads), smem, s, true, a);
 }
 
 }  // namespace
@@ -802,7 +834,8 @@ LayerPlan layer_plan(int T, int K, int S, int H, int I) {
   const size_t entries = static_cast<size_t>(T) * (K + S);
   LayerPlan p;
   p.a = 0;
-  p.y = up(entries * I * sizeof(float));
+  p.a32 = up(2 * entries * I * sizeof(__nv_bfloat16));
+  p.y = p.a32 + up(entries * I * sizeof(float));
   p.x16 = p.y + up(entries * H * sizeof(float));
   p.xscale = p.x16 + up(static_cast<size_t>(T) * H * sizeof(__half));
   p.amax = p.xscale + up(static_cast<size_t>(T) * sizeof(float));
@@ -834,6 +867,7 @@ cudaError_t launch_layer(const moe_handle* h, const moe_layer_args& q, int T, vo
   a.x16 = reinterpret_cast<__half*>(ws + p.x16);
   a.xscale = reinterpret_cast<float*>(ws + p.xscale);
   a.a = ws + p.a;
+  a.a32 = reinterpret_cast<float*>(ws + p.a32);
   a.amax = reinterpret_cast<uint32_t*>(ws + p.amax);
   a.y = reinterpret_cast<float*>(ws + p.y);
   a.arrived = arrived;
@@ -847,8 +881,13 @@ cudaError_t launch_layer(const moe_handle* h, const moe_layer_args& q, int T, vo
   a.act = q.act;
   a.wait_ns = h->wait_ns;
   a.flags = h->flags;
-  return q.weight_dtype == MOE_E4M3 ? launch_shape<Shape<1, 1, true>>(h, a, s)
-                                    : launch_shape<Shape<1, 1, false>>(h, a, s);
+  // few: 8 tokens an expert and less in the mean
+  const bool many = static_cast<int64_t>(T) * K > 6 * static_cast<int64_t>(a.E);
+  if (q.weight_dtype == MOE_E4M3)
+    return many ? launch_shape<Shape<256, 4, 4, 1, true>>(h, a, s)
+                : launch_shape<Shape<512, 1, 1, 2, true>>(h, a, s);
+  return many ? launch_shape<Shape<256, 4, 4, 1, false>>(h, a, s)
+              : launch_shape<Shape<512, 1, 1, 2, false>>(h, a, s);
 }
 
 }  // namespace moe
