@@ -280,14 +280,12 @@ template <bool F16>
 __device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                     uint32_t a3, uint32_t b0, uint32_t b1) {
   if (F16)
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
         "{%0,%1,%2,%3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
   else
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
         "{%8,%9}, {%0,%1,%2,%3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
@@ -491,34 +489,56 @@ struct Phase {
     }
   }
 
-  // acc += the products of one stage.  has: bit nt: the lane has a token in
-  // tile nt (without one its operand registers and columns mean nothing);
-  // sc: block scales of the lane's accumulator rows.
-  __device__ __forceinline__ void products(float (&acc)[MT][NT][4], uint32_t at, uint32_t has,
-                                           const float (&sc)[MT][2]) const {
-    float sum[FP8 ? MT : 1][NT][4] = {};
+  // One stage's operands.
+  struct Operands {
+    Vec16 w[S::kSteps][MT][2];
+    Vec16 x[S::kSteps][NT][kVec];
+  };
+
+  // has: bit nt: the lane has a token in tile nt (without one its operand
+  // registers, and the columns of its sums, mean nothing).
+  __device__ __forceinline__ void load(Operands& v, uint32_t at, uint32_t has) const {
 #pragma unroll
     for (int st = 0; st < S::kSteps; ++st) {
       const uint32_t from = at + st * kStepSlots * S::kSlotBytes;
-      Vec16 b[NT][kVec];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int v = 0; v < kVec; ++v)
-          lds16_if(b[nt][v], from + (2 * MT + nt * kVec + v) * S::kSlotBytes, (has >> nt) & 1u);
+        for (int i = 0; i < kVec; ++i)
+          lds16_if(v.x[st][nt][i], from + (2 * MT + nt * kVec + i) * S::kSlotBytes, (has >> nt) & 1u);
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt) {
-        const Vec16 w0 = lds16(from + (2 * mt) * S::kSlotBytes);
-        const Vec16 w1 = lds16(from + (2 * mt + 1) * S::kSlotBytes);
+        v.w[st][mt][0] = lds16(from + (2 * mt) * S::kSlotBytes);
+        v.w[st][mt][1] = lds16(from + (2 * mt + 1) * S::kSlotBytes);
+      }
+    }
+  }
+
+  // Sums that run beside each other, so that a product need not wait for the
+  // one before it; added at the end of a job (bf16) or a stage (e4m3).
+  static constexpr int kChains = MT * NT == 1 ? 4 : 1;
+
+  // acc += the products of one stage; sc: block scales of the lane's
+  // accumulator rows.
+  __device__ __forceinline__ void multiply(float (&acc)[kChains][MT][NT][4], const Operands& v,
+                                           const float (&sc)[MT][2]) const {
+    float sum[FP8 ? kChains : 1][FP8 ? MT : 1][NT][4] = {};
+#pragma unroll
+    for (int st = 0; st < S::kSteps; ++st) {
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt) {
+        const Vec16& w0 = v.w[st][mt][0];
+        const Vec16& w1 = v.w[st][mt][1];
         if (!FP8) {
 #pragma unroll
           for (int q = 0; q < 4; q += 2)
 #pragma unroll
-            for (int v = 0; v < kVec; ++v)
+            for (int i = 0; i < kVec; ++i)
 #pragma unroll
               for (int nt = 0; nt < NT; ++nt)
-                mma<false>(acc[mt][nt], w0.u[q], w1.u[q], w0.u[q + 1], w1.u[q + 1], b[nt][v].u[q],
-                           b[nt][v].u[q + 1]);
+                mma<false>(acc[(q / 2 * kVec + i + st * (kVec == 1 ? 2 : 0)) % kChains][mt][nt], w0.u[q],
+                           w1.u[q], w0.u[q + 1], w1.u[q + 1], v.x[st][nt][i].u[q],
+                           v.x[st][nt][i].u[q + 1]);
         } else {
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
@@ -527,8 +547,9 @@ struct Phase {
             f16_of_e4m3(w1.u[q], a1, a3);
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
-              mma<true>(sum[FP8 ? mt : 0][nt], a0, a1, a2, a3, b[nt][(q / 2) % kVec].u[q % 2 * 2],
-                        b[nt][(q / 2) % kVec].u[q % 2 * 2 + 1]);
+              mma<true>(sum[FP8 ? q % kChains : 0][FP8 ? mt : 0][nt], a0, a1, a2, a3,
+                        v.x[st][nt][(q / 2) % kVec].u[q % 2 * 2],
+                        v.x[st][nt][(q / 2) % kVec].u[q % 2 * 2 + 1]);
           }
         }
       }
@@ -539,8 +560,12 @@ struct Phase {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int r = 0; r < 4; ++r)
-            acc[mt][nt][r] = fmaf(sc[mt][r / 2], sum[FP8 ? mt : 0][nt][r], acc[mt][nt][r]);
+          for (int r = 0; r < 4; ++r) {
+            float t = sum[0][FP8 ? mt : 0][nt][r];
+#pragma unroll
+            for (int c = 1; c < (FP8 ? kChains : 1); ++c) t += sum[c][FP8 ? mt : 0][nt][r];
+            acc[0][mt][nt][r] = fmaf(sc[mt][r / 2], t, acc[0][mt][nt][r]);
+          }
     }
   }
 
@@ -583,7 +608,7 @@ struct Phase {
   // The first stages' weights.
   __device__ __forceinline__ void start(Cursor c) const {
 #pragma unroll 1
-    for (int s = 0; s < kStages && valid(c.j); ++s) {
+    for (int s = 0; s < kStages - 1 && valid(c.j); ++s) {
       copy_weights(c, queue + s * kStageBytes);
       advance(c);
     }
@@ -592,14 +617,15 @@ struct Phase {
   // Everything else.
   __device__ __forceinline__ void run(Cursor& next_copy, float* red) const {
 #pragma unroll 1
-    for (int s = 0; s < kStages; ++s) {
+    for (int s = 0; s < kStages - 1; ++s) {
       if (valid(next_copy.j)) {
         copy_tokens(next_copy, queue + s * kStageBytes);
         advance(next_copy);
       }
       copies_commit();
     }
-    uint32_t at = queue;
+    uint32_t at = queue, to = queue + (kStages - 1) * kStageBytes;
+    constexpr uint32_t kEnd = kStages * kStageBytes;
 #pragma unroll 1
     for (Job j = this->at(first_q); valid(j); j = next(j)) {
       const int p = g.slot_expert[j.slot];
@@ -621,7 +647,7 @@ struct Phase {
           scale[mt][1] = UP ? base + static_cast<int64_t>((a.I + r) / 128) * scale_cols : scale[mt][0];
         }
       }
-      float acc[MT][NT][4] = {};
+      float acc[kChains][MT][NT][4] = {};
       int window = -1;  // the 32 k blocks whose scales the lanes hold
 #pragma unroll 1
       for (int st = part; st < stages; st += team) {
@@ -642,16 +668,25 @@ struct Phase {
             sc[mt][1] = UP ? __shfl_sync(kFull, held[mt][1], block % 32) : sc[mt][0];
           }
         }
-        copies_wait<kStages - 1>();
-        products(acc, at, has, sc);
-        // the products have read the stage; its next contents
+        copies_wait<kStages - 2>();
+        Operands v;
+        load(v, at, has);
+        // the stage before this one has been multiplied: its slot is free
         if (valid(next_copy.j)) {
-          copy_weights(next_copy, at);
-          copy_tokens(next_copy, at);
+          copy_weights(next_copy, to);
+          copy_tokens(next_copy, to);
           advance(next_copy);
         }
         copies_commit();
-        at = at + kStageBytes == queue + kStages * kStageBytes ? queue : at + kStageBytes;
+        multiply(acc, v, sc);
+        to = at;
+        at = at + kStageBytes == queue + kEnd ? queue : at + kStageBytes;
+      }
+      if (!FP8) {
+#pragma unroll
+        for (int c = 1; c < kChains; ++c)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) acc[0][0][0][r] += acc[c][0][0][r];
       }
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt) {
@@ -662,13 +697,13 @@ struct Phase {
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int r = 0; r < 4; ++r)
-              red[((warp * NT + nt) * 4 + r) * 32 + lane] = acc[mt][nt][r];
+              red[((warp * NT + nt) * 4 + r) * 32 + lane] = acc[0][mt][nt][r];
           team_sync(id, team * 32);
         }
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
           if ((mt * NT + nt) % team != part) continue;
-          float (&v)[4] = acc[mt][nt];
+          float (&v)[4] = acc[0][mt][nt];
           if (team > 1) {
 #pragma unroll
             for (int r = 0; r < 4; ++r) v[r] = 0.0f;
