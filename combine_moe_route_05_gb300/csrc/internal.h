@@ -42,7 +42,7 @@ int resident_blocks(const void* kernel, int threads, size_t smem);
 
 // live: device count of tokens to route (NULL: all T); zeroed: kLayerCounters
 // words that the kernel clears for the kernel behind it, or NULL
-constexpr int kLayerCounters = 4;
+constexpr int kLayerCounters = 6;
 cudaError_t launch_route_topk(const moe_handle* h, const float* logits, const float* bias, int T,
                               int32_t* idx, float* w, cudaStream_t s,
                               const int32_t* live = nullptr, uint32_t* zeroed = nullptr);
