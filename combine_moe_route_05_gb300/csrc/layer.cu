@@ -94,7 +94,7 @@ struct Groups {
 
 __host__ __device__ constexpr size_t up16(size_t b) { return (b + 15) / 16 * 16; }
 
-constexpr int kMaxWarps = 18;
+constexpr int kMaxWarps = 20;
 
 __host__ __device__ constexpr size_t groups_bytes(int T, int KS, int n_exp) {
   return 2 * up16(2ull * T * KS) + up16(2ull * n_exp) + 2 * up16(4ull * n_exp) +
@@ -314,14 +314,14 @@ __device__ __forceinline__ float act_value(float g, int act) {
 // GROUPS groups of a block; in each, WK x WM consumer warps: WK split the k of
 // a stage, WM the MT WM tiles of 16 weight rows of a job, by NT tiles of 8
 // tokens.  A stage holds STEPS steps of 64 bytes of a weight row per warp.
-template <int GROUPS_, int WK_, int WM_, int MT_, int NT_, int STEPS_, bool FP8_>
+template <int GROUPS_, int COPIERS_, int WK_, int WM_, int MT_, int NT_, int STEPS_, bool FP8_>
 struct Shape {
-  static constexpr int kGroups = GROUPS_, WK = WK_, WM = WM_, MT = MT_, NT = NT_, kSteps = STEPS_;
+  static constexpr int kGroups = GROUPS_, kProducers = 1 + COPIERS_, WK = WK_, WM = WM_, MT = MT_, NT = NT_, kSteps = STEPS_;
   static constexpr bool FP8 = FP8_;
   static constexpr int kEb = FP8 ? 1 : 2;
   static constexpr int kTiles = WM * MT;                 // of 16 weight rows
   static constexpr int kConsumers = WK * WM;             // warps of a group
-  static constexpr int kThreads = kGroups * (kConsumers + 1) * 32;
+  static constexpr int kThreads = kGroups * (kConsumers + kProducers) * 32;
   static constexpr int kRowBytes = WK * kSteps * 64;     // of a weight row in a stage, at most
   static constexpr int kScales = FP8 ? kTiles * 2 * (kRowBytes / 128) : 0;
   static constexpr int kRed = kTiles * NT == 1 ? 2 : 1;  // buffers of partial sums
@@ -339,9 +339,11 @@ struct Stage {
   int slot, tile, c0;
   int bytes;  // of a weight row
   int tokens;
-  int last;   // 1: the job's last stage, -1: no more jobs
+  int what;   // kLast, kHeld, and from bit 2 on the stage's place in its rows; -1: no more jobs
   int taken;  // bytes of the ring, with what a wrap skipped
 };
+constexpr int kLast = 1;  // the job's last stage
+constexpr int kHeld = 2;  // its tokens come later
 
 // A group's shared memory.
 template <typename S>
@@ -349,7 +351,7 @@ struct Ring {
   uint32_t base;  // the ring itself
   int size;
   Stage* stage;
-  uint64_t *full, *empty;          // per stage
+  uint64_t *full, *empty, *go;     // per stage
   uint64_t *red_full, *red_empty;  // per buffer of partial sums
   float* scales;  // [stage][tile][2][block] (e4m3)
   float* red;
@@ -357,7 +359,7 @@ struct Ring {
 
 template <typename S>
 constexpr size_t group_bytes(int ring) {
-  return static_cast<size_t>(ring) + S::kRedBytes + S::kStages * (sizeof(Stage) + 16 + 4 * S::kScales) + 32;
+  return static_cast<size_t>(ring) + S::kRedBytes + S::kStages * (sizeof(Stage) + 24 + 4 * S::kScales) + 32;
 }
 template <typename S>
 constexpr int ring_bytes(int T, int KS, int n_exp) {
@@ -425,22 +427,26 @@ struct Phase {
                  block);
   }
 
-  __device__ __forceinline__ void copy_weights(const Place& p, int off, int bytes, uint64_t* bar, int lane) const {
+  // This issuer's share of a stage's weight rows (of kProducers issuers: one
+  // warp issues a copy in about 41 ns, which is 25 GB/s at 1 KB).
+  __device__ __forceinline__ void copy_weights(const Place& p, int off, int bytes, uint64_t* bar, int issuer,
+                                               int lane) const {
     const uint8_t* base = (UP ? a.w13 : a.w2) +
                           static_cast<int64_t>(expert(p.slot)) * (UP ? 2 * a.I : a.H) * kd * kEb +
                           static_cast<int64_t>(p.st) * row_bytes;
-    for (int r = lane; r < 16 * S::kTiles; r += 32) {
+    for (int r = issuer + lane * S::kProducers; r < 16 * S::kTiles; r += 32 * S::kProducers) {
       const int out = (p.tile * S::kTiles + r / 16) * kRows + (UP ? r % 8 : r % 16);
       if (out >= limit) continue;
       const int row = UP && r % 16 >= 8 ? a.I + out : out;
       copy_bulk(ring.base + off + r * pitch, base + static_cast<int64_t>(row) * kd * kEb, bytes, bar);
     }
   }
+  // The token rows `first`, first + step, ... of a stage.
   __device__ __forceinline__ void copy_tokens(const Place& p, int off, int bytes, int tokens, uint64_t* bar,
-                                              int lane) const {
+                                              int first, int step) const {
     const uint8_t* src = UP ? (FP8 ? reinterpret_cast<const uint8_t*>(a.x16) : a.x) : a.a;
     const int begin = g.start[g.slot_expert[p.slot]] + p.c0;
-    for (int i = lane; i < tokens * kParts; i += 32) {
+    for (int i = first; i < tokens * kParts; i += step) {
       const int n = kParts == 2 && i >= tokens ? i - tokens : i;
       const int entry = g.order[begin + n];
       const int64_t row = UP ? entry / (a.K + a.S) : entry + (i >= tokens ? static_cast<int64_t>(a.T) * (a.K + a.S) : 0);
@@ -503,12 +509,13 @@ struct Phase {
         rows += UP ? 2 * left : left;
       }
       if (lane == 0) {
-        ring.stage[s] = Stage{off, p.slot, p.tile, p.c0, bytes, tokens, p.st + 1 == stages, need};
+        ring.stage[s] = Stage{off, p.slot, p.tile, p.c0, bytes, tokens, p.st * 4 + (p.st + 1 == stages ? kLast : 0) + (barrier ? kHeld : 0), need};
         mbar_arrive_expect_tx(ring.full + s, rows * bytes + tokens * kParts * bytes * (2 / kEb));
+        mbar_arrive(ring.go + s);
       }
       __syncwarp();
-      copy_weights(p, off, bytes, ring.full + s, lane);
-      if (!barrier) copy_tokens(p, off, bytes, tokens, ring.full + s, lane);
+      copy_weights(p, off, bytes, ring.full + s, 0, lane);
+      if (!barrier) copy_tokens(p, off, bytes, tokens, ring.full + s, lane * S::kProducers, 32 * S::kProducers);
       off += size;
       used += need;
       ++head;
@@ -522,6 +529,7 @@ struct Phase {
     if (lane == 0) {
       ring.stage[head % S::kStages] = Stage{0, 0, 0, 0, 0, 0, -1, 0};
       mbar_arrive(ring.full + head % S::kStages);
+      mbar_arrive(ring.go + head % S::kStages);
     }
     __syncwarp();
     ++head;
@@ -543,9 +551,29 @@ struct Phase {
     fence_bulk();
     for (int h = from; h < to; ++h, ++p.st) {
       const Stage& st = ring.stage[h % S::kStages];
-      copy_tokens(p, st.off, st.bytes, st.tokens, ring.full + h % S::kStages, lane);
+      copy_tokens(p, st.off, st.bytes, st.tokens, ring.full + h % S::kStages, lane, 32);
     }
     return true;
+  }
+  // A copier: its share of every stage that the producer announces.
+  __device__ __forceinline__ bool assist(int& head, int issuer, int lane) const {
+    bool fenced = false;
+#pragma unroll 1
+    for (;; ++head) {
+      const int s = head % S::kStages;
+      if (!__all_sync(kFull, ring_wait(a, ring.go + s, (head / S::kStages) & 1))) return false;
+      const Stage st = ring.stage[s];
+      if (st.what < 0) {
+        ++head;
+        return true;
+      }
+      const Place p{0, st.slot, st.tile, st.c0, st.what >> 2};
+      copy_weights(p, st.off, st.bytes, ring.full + s, issuer, lane);
+      if (st.what & kHeld) continue;
+      if (!fenced) fence_bulk();  // behind the producer's grid barrier
+      fenced = true;
+      copy_tokens(p, st.off, st.bytes, st.tokens, ring.full + s, issuer + lane * S::kProducers, 32 * S::kProducers);
+    }
   }
 
   // ------------------------------------------------------------- consumers
@@ -601,7 +629,7 @@ struct Phase {
       if (!__all_sync(kFull, ring_wait(a, ring.full + i, (done.stages / S::kStages) & 1))) return false;
       ++done.stages;
       const Stage st = ring.stage[i];
-      if (st.last < 0) {
+      if (st.what < 0) {
         __syncwarp();
         if (lane == 0) mbar_arrive(ring.empty + i);
         return true;
@@ -635,7 +663,7 @@ struct Phase {
       __syncwarp();
       if (lane == 0) mbar_arrive(ring.empty + i);
       multiply(acc, w, x, sc);
-      if (st.last && !finish(acc, st, warp, lane, done.sums)) return false;
+      if ((st.what & kLast) && !finish(acc, st, warp, lane, done.sums)) return false;
     }
   }
 
@@ -828,7 +856,8 @@ __global__ void __launch_bounds__(S::kThreads, 1) layer_kernel(LayerArgs a, int 
   const int KS = a.K + a.S;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const bool producer = warp >= S::kGroups * S::kConsumers;
-  const int group = producer ? warp - S::kGroups * S::kConsumers : warp / S::kConsumers;
+  const int issuer = producer ? (warp - S::kGroups * S::kConsumers) % S::kProducers : 0;
+  const int group = producer ? (warp - S::kGroups * S::kConsumers) / S::kProducers : warp / S::kConsumers;
   Ring<S> ring;
   {
     uint8_t* p = smem + group * static_cast<size_t>(ring_size);
@@ -841,12 +870,14 @@ __global__ void __launch_bounds__(S::kThreads, 1) layer_kernel(LayerArgs a, int 
     p += S::kStages * sizeof(Stage);
     ring.full = reinterpret_cast<uint64_t*>(p);
     ring.empty = ring.full + S::kStages;
-    ring.red_full = ring.empty + S::kStages;
+    ring.go = ring.empty + S::kStages;
+    ring.red_full = ring.go + S::kStages;
     ring.red_empty = ring.red_full + 2;
     ring.scales = reinterpret_cast<float*>(ring.red_empty + 2);
   }
-  if (producer) {
+  if (producer && issuer == 0) {
     if (lane < S::kStages) {
+      mbar_init(ring.go + lane, 1);
       mbar_init(ring.full + lane, 1);
       mbar_init(ring.empty + lane, S::kConsumers);
     }
@@ -882,6 +913,10 @@ __global__ void __launch_bounds__(S::kThreads, 1) layer_kernel(LayerArgs a, int 
     const int first = blockIdx.x + gridDim.x * group;
     int head = 0, tail = 0, off = 0, used = 0;
     fence_bulk();
+    if (issuer > 0) {
+      if ((!up.assist(head, issuer, lane) || !down.assist(head, issuer, lane)) && lane == 0) failed = 1;
+      return;
+    }
     if (!up.produce(head, tail, off, used, taken, first, S::FP8 ? a.arrived : nullptr, lane) ||
         !down.produce(head, tail, off, used, taken + 1, first, after_scale, lane)) {
       // what is still in flight lands before the block may end
@@ -1008,10 +1043,10 @@ cudaError_t launch_layer(const moe_handle* h, const moe_layer_args& q, int T, vo
   // few: 8 tokens an expert and less in the mean
   const bool many = static_cast<int64_t>(T) * K > 6 * static_cast<int64_t>(a.E);
   if (q.weight_dtype == MOE_E4M3)
-    return many ? launch_shape<Shape<1, 8, 1, 4, 2, 1, true>>(h, a, s)
-                : launch_shape<Shape<2, 8, 1, 1, 1, 2, true>>(h, a, s);
-  return many ? launch_shape<Shape<1, 8, 1, 4, 4, 1, false>>(h, a, s)
-              : launch_shape<Shape<2, 8, 1, 1, 1, 2, false>>(h, a, s);
+    return many ? launch_shape<Shape<1, 3, 8, 1, 4, 2, 1, true>>(h, a, s)
+                : launch_shape<Shape<2, 1, 8, 1, 1, 1, 2, true>>(h, a, s);
+  return many ? launch_shape<Shape<1, 3, 8, 1, 4, 4, 1, false>>(h, a, s)
+              : launch_shape<Shape<2, 1, 8, 1, 1, 1, 2, false>>(h, a, s);
 }
 
 }  // namespace moe
