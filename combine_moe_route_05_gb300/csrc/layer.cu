@@ -15,18 +15,18 @@
 // 8..15 the up rows of the same outputs: a lane's accumulators then hold gate
 // and up of one output and the activation needs no exchange.
 //
-// A block has one or two groups: a producer warp that copies weight rows (and
-// the expert's token rows beside them) into the group's ring in shared memory
-// with bulk copies, and consumer warps that split each stage's k.  A job is one
-// expert and one tile of outputs.  The producer runs several stages ahead and
-// across the ends of jobs, so the stream of weights has no gaps; it takes its
-// jobs from a counter, because the SMs do not all get the same share of the
-// memory's rate (by up to a quarter on the largest layers), and a stage takes
-// only the room that its tokens need.
+// Every lane copies what it will itself multiply into a queue of its own in
+// shared memory (cp.async), several steps ahead and across the ends of jobs,
+// so the stream of weights has no gaps and the queue needs no barrier.  A job
+// is one expert and one tile of outputs; a team of 1, 2, 4 or 8 warps, as many
+// as make the jobs fill the grid evenly, splits its k and adds its partial
+// sums in warp order.  Jobs go round over the blocks, expert by expert, so
+// that neighbouring blocks read neighbouring rows and the experts with many
+// tokens spread over all blocks.
 //
 // The three parts are one cooperative kernel, with grid-wide barriers between
-// them (bounded waits): the ring takes the first W2 rows before it waits for
-// the up products.  Results do not depend on which block takes which job.
+// them (bounded waits): the queue takes the first W2 rows before it waits for
+// the up products.  Results do not depend on the order of blocks or warps.
 //
 // Precision: products and sums are fp32.  bf16 weights: x is taken as it is,
 // and a as the sum of two bf16 numbers (16 bits), which costs a second
@@ -50,7 +50,9 @@ constexpr int kMaxEntries = MOE_LAYER_MAX_TOKENS * (MOE_MAX_TOPK + MOE_LAYER_MAX
 constexpr int kMaxExperts = MOE_MAX_EXPERTS + MOE_LAYER_MAX_SHARED;
 constexpr unsigned kFull = 0xffffffffu;
 constexpr uint16_t kNone = 0xffff;
-constexpr int kBarriers = 4;  // grid barriers of a call
+constexpr int kBarriers = 4;  // grid barriers of a call, at most
+constexpr int kTickets = 16;  // of a team's coming jobs
+constexpr int kQueueBytes = 192 * 1024;
 
 struct LayerArgs {
   const uint8_t* x;      // [T, H] bf16
@@ -68,7 +70,7 @@ struct LayerArgs {
   uint32_t* amax;        // [T (K + S)] bits of the largest |a| of an entry (e4m3)
   float* y;              // [T (K + S), H]
   uint32_t* arrived;     // blocks that reached each grid barrier (kBarriers), then the
-                         // jobs taken of each phase; zero at the start
+                         // jobs given out in each phase; zero at the start
   __nv_bfloat16* out;    // [T, H]
   int T, K, S, E, H, I;
   int act;
@@ -94,7 +96,7 @@ struct Groups {
 
 __host__ __device__ constexpr size_t up16(size_t b) { return (b + 15) / 16 * 16; }
 
-constexpr int kMaxWarps = 20;
+constexpr int kMaxWarps = 16;
 
 __host__ __device__ constexpr size_t groups_bytes(int T, int KS, int n_exp) {
   return 2 * up16(2ull * T * KS) + up16(2ull * n_exp) + 2 * up16(4ull * n_exp) +
@@ -166,7 +168,7 @@ __device__ __forceinline__ void group_entries(const LayerArgs& a, Groups& g, uin
   }
   if (lane == 31) g.head[warp] = inc;
   // the entries' experts, before `order` takes the entries
-  constexpr int kMine = (kMaxEntries + kThreads - 1) / kThreads;
+  constexpr int kMine = kMaxEntries / kThreads;
   uint16_t mine[kMine];
 #pragma unroll
   for (int j = 0; j < kMine; ++j)
@@ -203,69 +205,88 @@ __device__ __forceinline__ unsigned long long global_ns() {
   return t;
 }
 
+// This block is done with what the others wait for.
+__device__ __forceinline__ void grid_arrive(uint32_t* arrived) {
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    __threadfence();
+    atomicAdd(arrived, 1u);
+  }
+}
+
 // Waits until every block of the grid has arrived; false, with the status bit
-// set, after the handle's limit.  One thread.
-__device__ __forceinline__ bool grid_wait(const LayerArgs& a, const uint32_t* arrived) {
-  const unsigned long long t0 = global_ns();
-  for (;;) {
-    uint32_t n;
-    asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(n) : "l"(arrived) : "memory");
-    if (n >= gridDim.x) break;
-    if (global_ns() - t0 > a.wait_ns) {
-      raise_flag(a.flags, MOE_DEVERR_TIMEOUT);
-      return false;
-    }
-  }
-  __threadfence();
-  return true;
-}
-
-// Waits for a phase of a shared-memory barrier; false, with the status bit
 // set, after the handle's limit.
-__device__ __forceinline__ bool ring_wait(const LayerArgs& a, uint64_t* bar, uint32_t parity) {
-  if (mbar_try_wait(bar, parity)) return true;
-  const unsigned long long t0 = global_ns();
-  for (;;) {
-    if (mbar_try_wait(bar, parity)) return true;
-    if (global_ns() - t0 > a.wait_ns) {
-      raise_flag(a.flags, MOE_DEVERR_TIMEOUT);
-      return false;
+__device__ __forceinline__ bool grid_wait(const LayerArgs& a, uint32_t* arrived, int* ok) {
+  if (threadIdx.x == 0) {
+    const unsigned long long t0 = global_ns();
+    bool done = true;
+    for (;;) {
+      uint32_t n;
+      asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(n) : "l"(arrived) : "memory");
+      if (n >= gridDim.x) break;
+      if (global_ns() - t0 > a.wait_ns) {
+        raise_flag(a.flags, MOE_DEVERR_TIMEOUT);
+        done = false;
+        break;
+      }
     }
+    __threadfence();
+    *ok = done;
   }
-}
-
-__device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
-  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(bar)) : "memory");
-}
-
-__device__ __forceinline__ void named_sync(int id, int threads) {
-  asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+  __syncthreads();
+  return *ok != 0;
 }
 
 // ---------------------------------------------------------------------------
 // copies and products
 
-// A bulk copy of `bytes` (16-byte aligned, a multiple of 16) into shared
-// memory, reported to `bar`.
-__device__ __forceinline__ void copy_bulk(uint32_t dst, const void* src, uint32_t bytes, uint64_t* bar) {
+// Asynchronous copies of 16 bytes into shared memory; where !valid, zeros are
+// written and nothing is read.  Weights pass by L1, tokens are kept in it.
+__device__ __forceinline__ void copy16_stream(uint32_t dst, const void* src, bool valid) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
+               "r"(valid ? 16 : 0)
+               : "memory");
+}
+// Nothing at all where !any (predicated, since the lanes of a warp differ).
+__device__ __forceinline__ void copy16_keep(uint32_t dst, const void* src, bool valid, bool any) {
   asm volatile(
-      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
-      "l"(src), "r"(bytes), "r"(smem_addr(bar))
+      "{\n\t.reg .pred p;\n\tsetp.ne.s32 p, %3, 0;\n\t"
+      "@p cp.async.ca.shared.global [%0], [%1], 16, %2;\n\t}" ::"r"(dst),
+      "l"(src), "r"(valid ? 16 : 0), "r"(static_cast<int>(any))
       : "memory");
 }
-// Orders what this thread has seen of global memory before its bulk copies.
-__device__ __forceinline__ void fence_bulk() { asm volatile("fence.proxy.async;" ::: "memory"); }
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copies_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ Vec16 lds16(uint32_t p) {
+  Vec16 v;
+  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(v.u[0]), "=r"(v.u[1]), "=r"(v.u[2]), "=r"(v.u[3])
+               : "r"(p)
+               : "memory");
+  return v;
+}
 
-// 16 bytes of shared memory, zeros where !valid.  Predicated: the lanes of a
-// warp differ.
-__device__ __forceinline__ Vec16 lds16_if(uint32_t p, bool valid) {
-  Vec16 v{};
+// 4 bytes of an asynchronous copy.
+__device__ __forceinline__ void copy4(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+
+// 16 bytes of shared memory where `any`; else v keeps what it holds.
+__device__ __forceinline__ void lds16_if(Vec16& v, uint32_t p, bool any) {
   asm volatile(
       "{\n\t.reg .pred p;\n\tsetp.ne.s32 p, %5, 0;\n\t"
       "@p ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];\n\t}"
       : "+r"(v.u[0]), "+r"(v.u[1]), "+r"(v.u[2]), "+r"(v.u[3])
-      : "r"(p), "r"(static_cast<int>(valid))
+      : "r"(p), "r"(static_cast<int>(any))
       : "memory");
+}
+
+__device__ __forceinline__ float lds4(uint32_t p) {
+  float v;
+  asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(p) : "memory");
   return v;
 }
 
@@ -273,12 +294,12 @@ template <bool F16>
 __device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                     uint32_t a3, uint32_t b0, uint32_t b1) {
   if (F16)
-    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
         "{%0,%1,%2,%3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
   else
-    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
         "{%8,%9}, {%0,%1,%2,%3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
@@ -311,304 +332,253 @@ __device__ __forceinline__ float act_value(float g, int act) {
   return c < -80.0f ? g * 0.0f : g * __fdividef(1.0f, 1.0f + __expf(-c));
 }
 
-// GROUPS groups of a block; in each, WK x WM consumer warps: WK split the k of
-// a stage, WM the MT WM tiles of 16 weight rows of a job, by NT tiles of 8
-// tokens.  A stage holds STEPS steps of 64 bytes of a weight row per warp.
-template <int GROUPS_, int COPIERS_, int WK_, int WM_, int MT_, int NT_, int STEPS_, bool FP8_>
+// MT tiles of 16 weight rows by NT tiles of up to 8 tokens a job; a stage of
+// the queue holds STEPS steps of 64 bytes of each weight row.
+template <int THREADS_, int MT_, int NT_, int STEPS_, bool FP8_, bool PACKED_>
 struct Shape {
-  static constexpr int kGroups = GROUPS_, kProducers = 1 + COPIERS_, WK = WK_, WM = WM_, MT = MT_, NT = NT_, kSteps = STEPS_;
-  static constexpr bool FP8 = FP8_;
-  static constexpr int kEb = FP8 ? 1 : 2;
-  static constexpr int kTiles = WM * MT;                 // of 16 weight rows
-  static constexpr int kConsumers = WK * WM;             // warps of a group
-  static constexpr int kThreads = kGroups * (kConsumers + kProducers) * 32;
-  static constexpr int kRowBytes = WK * kSteps * 64;     // of a weight row in a stage, at most
-  static constexpr int kScales = FP8 ? kTiles * 2 * (kRowBytes / 128) : 0;
-  static constexpr int kRed = kTiles * NT == 1 ? 2 : 1;  // buffers of partial sums
-  static constexpr int kRedBytes = kRed * kConsumers * NT * 4 * 32 * 4;  // of a group
-  static constexpr int kStages = 16;                     // at most in a ring
-  static constexpr int kReducers = WM * NT;              // warps that add a buffer's sums
-  static_assert(kRowBytes % 128 == 0 && kScales <= 32 && kGroups * kConsumers <= 16 && NT <= WK, "shape");
-  // the largest stage: two of them have to fit the smallest ring
-  static constexpr int kStageBytes =
-      16 * kTiles * (kRowBytes + 64) + 8 * NT * 2 * (kRowBytes + 64);
+  static constexpr int kThreads = THREADS_, kWarps = THREADS_ / 32;
+  static constexpr int MT = MT_, NT = NT_, kSteps = STEPS_;
+  static constexpr bool FP8 = FP8_, kPacked = PACKED_;
+  static_assert(!kPacked || MT * NT == 1, "packed");
+  static constexpr int kSlotBytes = kThreads * 16;  // 16 bytes per lane
+  static constexpr int kRed = MT * NT == 1 ? 2 : 1;  // buffers of partial sums
+  static constexpr int kRedFloats = kWarps * NT * 4 * 32;
+  static constexpr int kMaxStages = 8;
+  // behind the queue: partial sums, tickets, block scales of the stages
+  static constexpr int kRedBytes = kRed * kRedFloats * 4;
+  static constexpr int kTicketBytes = kWarps * kTickets * 4;
+  static constexpr int kScaleBytes = FP8 ? kWarps * kMaxStages * 2 * MT * 4 : 0;
+  static constexpr size_t kFixedBytes = kQueueBytes + kRedBytes + kTicketBytes + kScaleBytes;
+  static constexpr size_t smem(int T, int KS, int n_exp) { return kFixedBytes + groups_bytes(T, KS, n_exp); }
+  static_assert(kWarps <= kMaxWarps, "warps");
+  static_assert(smem(MOE_LAYER_MAX_TOKENS, MOE_MAX_TOPK + MOE_LAYER_MAX_SHARED, kMaxExperts) <=
+                    227 * 1024, "shared memory budget");
 };
 
-struct Stage {
-  int off;    // of the weight rows in the ring
-  int slot, tile, c0;
-  int bytes;  // of a weight row
-  int tokens;
-  int what;   // kLast, kHeld, and from bit 2 on the stage's place in its rows; -1: no more jobs
-  int taken;  // bytes of the ring, with what a wrap skipped
-};
-constexpr int kLast = 1;  // the job's last stage
-constexpr int kHeld = 2;  // its tokens come later
-
-// A group's shared memory.
-template <typename S>
-struct Ring {
-  uint32_t base;  // the ring itself
-  int size;
-  Stage* stage;
-  uint64_t *full, *empty, *go;     // per stage
-  uint64_t *red_full, *red_empty;  // per buffer of partial sums
-  float* scales;  // [stage][tile][2][block] (e4m3)
-  float* red;
+// Tokens [c0, c0 + kTokens) of the expert in slot `slot`, output tile `tile`;
+// q = slot * tiles + tile, i its place in the team's sequence.
+struct Job {
+  int i, q, slot, tile, c0;
 };
 
-template <typename S>
-constexpr size_t group_bytes(int ring) {
-  return static_cast<size_t>(ring) + S::kRedBytes + S::kStages * (sizeof(Stage) + 24 + 4 * S::kScales) + 32;
-}
-template <typename S>
-constexpr int ring_bytes(int T, int KS, int n_exp) {
-  const size_t rest = 1024 + groups_bytes(T, KS, n_exp) + S::kGroups * group_bytes<S>(0);
-  return static_cast<int>((227 * 1024 - rest) / S::kGroups / 128 * 128);
-}
-
-// What the warps of a group have passed of its barriers, over both phases.
-struct Progress {
-  int stages = 0, sums = 0;
-};
-
-// One phase (up or down) of one group.
+// The products of one phase (up or down) for one thread.
 template <typename S, bool UP>
 struct Phase {
-  static constexpr int MT = S::MT, NT = S::NT, kEb = S::kEb;
+  static constexpr int MT = S::MT, NT = S::NT, kWarps = S::kWarps;
   static constexpr bool FP8 = S::FP8;
-  static constexpr int kVec = UP ? (FP8 ? 2 : 1) : 2;    // token vectors beside a weight vector
-  static constexpr int kParts = FP8 || UP ? 1 : 2;       // rows of a token: x; a's two parts
-  static constexpr int kRows = UP ? 8 : 16;              // outputs of 16 weight rows
-  static constexpr int kBlocks = S::kRowBytes / 128;     // block scales along a stage's rows
+  static constexpr int kEb = FP8 ? 1 : 2;
+  static constexpr int kRowBytes = 64 * S::kSteps;  // of a weight row in a stage
+  static constexpr int kRows = UP ? 8 : 16;         // outputs that 16 weight rows give
+  // token vectors beside a weight vector: x, or a's two parts; fp16 in e4m3
+  static constexpr int kVec = UP && !FP8 ? 1 : 2;
+  // Packed: 4 tokens to a tile, whose two vectors share the places of one, so
+  // that more of the queue holds weights.  bf16: columns 4..7 take the low parts
+  // of columns 0..3 (one product for both, added at the end); e4m3: the second
+  // vector lies in the places of the lanes without a token.
+  static constexpr bool kPacked = S::kPacked && kVec == 2;
+  static constexpr bool kLowColumns = kPacked && !FP8;
+  static constexpr int kTokens = kPacked ? 4 : 8 * NT;  // of a job
+  static constexpr int kSlots = kPacked ? 1 : kVec;     // per token tile
+  static constexpr int kLoads = kLowColumns ? 1 : kVec; // vectors a lane multiplies
+  static constexpr int kStepSlots = 2 * MT + NT * kSlots;
+  static constexpr int kStageBytes = S::kSteps * kStepSlots * S::kSlotBytes;
+  static constexpr int kStages = kQueueBytes / kStageBytes < S::kMaxStages ? kQueueBytes / kStageBytes
+                                                                          : S::kMaxStages;
+  static_assert(kStages >= 3, "queue");
 
   const LayerArgs& a;
   const Groups& g;
-  const Ring<S>& ring;
-  int kd, limit, tiles, stages, nq;
-  int row_bytes;           // of a weight row in a stage
-  int pitch, token_pitch;  // of rows in the ring, free of bank conflicts
+  uint32_t queue;   // shared-memory address of this lane's queue
+  uint32_t scales;  // of the warp's block scales
+  int kd, tiles, limit, stages, nq;
+  int lane, warp, team, part, first_q, stride_q;
+  int fixed;       // jobs of a team that are dealt out beforehand
+  int* tickets;    // the team's others
+  uint32_t* given;
 
-  __device__ __forceinline__ Phase(const LayerArgs& args, const Groups& groups, const Ring<S>& r)
-      : a(args), g(groups), ring(r) {
+  __device__ __forceinline__ Phase(const LayerArgs& args, const Groups& groups, uint8_t* smem)
+      : a(args), g(groups), lane(threadIdx.x & 31), warp(threadIdx.x >> 5) {
+    queue = smem_addr(smem) + threadIdx.x * 16;
+    scales = smem_addr(smem) + kQueueBytes + S::kRedBytes + S::kTicketBytes + warp * S::kMaxStages * 2 * MT * 4;
     kd = UP ? a.H : a.I;
     limit = UP ? a.I : a.H;
-    tiles = (limit + kRows * S::kTiles - 1) / (kRows * S::kTiles);
-    stages = (kd * kEb + S::kRowBytes - 1) / S::kRowBytes;
-    row_bytes = ((kd * kEb + stages - 1) / stages + 127) / 128 * 128;
-    pitch = row_bytes + 64;
-    token_pitch = FP8 ? 2 * row_bytes + 16 : pitch;
+    tiles = (limit + kRows * MT - 1) / (kRows * MT);
+    stages = (kd * kEb + kRowBytes - 1) / kRowBytes;
     nq = g.nslots * tiles;
-  }
-  __device__ __forceinline__ int expert(int slot) const {
-    const int p = g.slot_expert[slot];
-    return p < a.S ? a.E + p : p - a.S;
+    // Many jobs: teams of 8 (fewer where that leaves a warp less than four
+    // stages of a job), which makes jobs short enough to even out at the end
+    // what the SMs differ in speed.  Few: the team size with the fewest rounds
+    // over the grid, in units of a one-warp job.
+    const int warps = kWarps * gridDim.x;
+    team = 1;
+    if (nq >= warps / 8 * 6) {
+      while (team < 8 && 8 * team <= stages) team *= 2;
+    } else {
+      float best = 0.0f;
+#pragma unroll 1
+      for (int n = 1; n <= 8 && n <= stages; n *= 2) {
+        const float cost = static_cast<float>((nq * n + warps - 1) / warps) / n;
+        if (n == 1 || cost < best) {
+          best = cost;
+          team = n;
+        }
+      }
+    }
+    first_q = blockIdx.x + gridDim.x * (warp / team);
+    stride_q = gridDim.x * (kWarps / team);
+    part = warp % team;
+    // the copies of a warp run at most (per - 1 + kStages) / per jobs ahead,
+    // and a ticket is there from the second job behind its request on
+    const int per = stages / team;
+    fixed = (per - 1 + kStages) / per + 1;
+    tickets = reinterpret_cast<int*>(smem + kQueueBytes + S::kRedBytes) + warp / team * kTickets;
+    given = a.arrived + kBarriers + (UP ? 0 : 1);
   }
 
-  // ------------------------------------------------------------- producer
-  struct Place {
-    int q, slot, tile, c0, st;
-  };
-  __device__ __forceinline__ Place at(int q) const {
+  __device__ __forceinline__ bool valid(const Job& j) const { return j.q < nq; }
+  __device__ __forceinline__ Job at(int i) const {
+    const int q = i < fixed ? first_q + i * stride_q : tickets[i % kTickets];
     const int slot = q / tiles;
-    return Place{q, slot, q - slot * tiles, 0, 0};
+    return Job{i, q, slot, q - slot * tiles, 0};
   }
-  __device__ __forceinline__ bool valid(const Place& p) const { return p.q < nq; }
-
-  // The block scales of a stage, one per lane.
-  __device__ __forceinline__ float scale_of(const Place& p, int lane) const {
-    if (!FP8 || !valid(p) || lane >= S::kScales) return 0.0f;
-    const int cols = (kd + 127) / 128;
-    const int block = min(p.st * (row_bytes / 128) + lane % kBlocks, cols - 1);
-    const int h = lane / kBlocks % 2, mt = lane / kBlocks / 2;
-    const int r = min((p.tile * S::kTiles + mt) * kRows, limit - 8) + (UP && h ? a.I : 0);
-    return __ldg((UP ? a.s13 : a.s2) +
-                 (static_cast<int64_t>(expert(p.slot)) * (((UP ? 2 * a.I : a.H) + 127) / 128) + r / 128) * cols +
-                 block);
+  __device__ __forceinline__ Job next(const Job& j) const {
+    if (j.c0 + kTokens < g.cnt[g.slot_expert[j.slot]]) return Job{j.i, j.q, j.slot, j.tile, j.c0 + kTokens};
+    return at(j.i + 1);
+  }
+  // Whether tile mt of the job has outputs.
+  __device__ __forceinline__ bool has_rows(const Job& j, int mt) const {
+    return MT == 1 || (j.tile * MT + mt) * kRows < limit;
+  }
+  // The token (of the job) that this lane's operand holds in tile nt.
+  __device__ __forceinline__ int lane_token(int nt) const {
+    return kLowColumns ? (lane >> 2) & 3 : kPacked && lane >= 16 ? kTokens : nt * 8 + (lane >> 2);
   }
 
-  // This issuer's share of a stage's weight rows (of kProducers issuers: one
-  // warp issues a copy in about 41 ns, which is 25 GB/s at 1 KB).
-  __device__ __forceinline__ void copy_weights(const Place& p, int off, int bytes, uint64_t* bar, int issuer,
-                                               int lane) const {
-    const uint8_t* base = (UP ? a.w13 : a.w2) +
-                          static_cast<int64_t>(expert(p.slot)) * (UP ? 2 * a.I : a.H) * kd * kEb +
-                          static_cast<int64_t>(p.st) * row_bytes;
-    for (int r = issuer + lane * S::kProducers; r < 16 * S::kTiles; r += 32 * S::kProducers) {
-      const int out = (p.tile * S::kTiles + r / 16) * kRows + (UP ? r % 8 : r % 16);
-      if (out >= limit) continue;
-      const int row = UP && r % 16 >= 8 ? a.I + out : out;
-      copy_bulk(ring.base + off + r * pitch, base + static_cast<int64_t>(row) * kd * kEb, bytes, bar);
+  // Where this lane's next copies come from.
+  struct Cursor {
+    Job j;
+    int o;                  // byte of the weight rows, of the lane's 16
+    const uint8_t* row;     // the lane's first weight row, from byte o on
+    int64_t half;           // from it to the lane's second row
+    const uint8_t* col[NT]; // its token's values per token tile, NULL: none
+    const float* scale;     // the block scales' row of lanes 0 .. 2 MT - 1
+  };
+
+  __device__ __forceinline__ void open(Cursor& c) const {
+    if (!valid(c.j)) return;
+    const int p = g.slot_expert[c.j.slot];
+    const int e = p < a.S ? a.E + p : p - a.S;
+    const int r0 = c.j.tile * kRows * MT;
+    const int64_t all_rows = UP ? 2 * a.I : a.H;
+    c.o = part * kRowBytes + (lane & 3) * 16;
+    c.row = (UP ? a.w13 : a.w2) + (e * all_rows + r0 + (lane >> 2)) * kd * kEb + c.o;
+    // the last tile of the down products may have no second half: it reads
+    // the first again, and its results go nowhere
+    c.half = static_cast<int64_t>(UP ? a.I : MT == 1 && r0 + 8 >= limit ? 0 : 8) * kd * kEb;
+    if (FP8 && lane < 2 * MT) {
+      const int r = min(r0 + lane / 2 * kRows, limit - 8) + (UP && lane % 2 ? a.I : 0);
+      c.scale = (UP ? a.s13 : a.s2) + (e * ((all_rows + 127) / 128) + r / 128) * ((kd + 127) / 128);
     }
-  }
-  // The token rows `first`, first + step, ... of a stage.
-  __device__ __forceinline__ void copy_tokens(const Place& p, int off, int bytes, int tokens, uint64_t* bar,
-                                              int first, int step) const {
+    const int cnt = g.cnt[p], at = g.start[p];
     const uint8_t* src = UP ? (FP8 ? reinterpret_cast<const uint8_t*>(a.x16) : a.x) : a.a;
-    const int begin = g.start[g.slot_expert[p.slot]] + p.c0;
-    for (int i = first; i < tokens * kParts; i += step) {
-      const int n = kParts == 2 && i >= tokens ? i - tokens : i;
-      const int entry = g.order[begin + n];
-      const int64_t row = UP ? entry / (a.K + a.S) : entry + (i >= tokens ? static_cast<int64_t>(a.T) * (a.K + a.S) : 0);
-      copy_bulk(ring.base + off + 16 * S::kTiles * pitch + i * token_pitch,
-                src + row * kd * 2 + static_cast<int64_t>(p.st) * row_bytes * (2 / kEb), bytes * (2 / kEb), bar);
-    }
-  }
-
-  // Issues every stage of this group's jobs.  `head` counts the stages of both
-  // phases; the consumers release them in order.  barrier: the grid barrier
-  // behind which the tokens' side is complete (NULL: it is).
-  __device__ __forceinline__ bool produce(int& head, int& tail, int& off, int& used, uint32_t* taken, int first,
-                                          const uint32_t* barrier, int lane) const {
-    Place p = at(first);
-    int ticket = 0;
-    if (lane == 0) ticket = atomicAdd(taken, 1u);
-    float scale = scale_of(p, lane);
-    Place held = p;            // stages from here to p wait for their tokens
-    const int held_head = head;
-#pragma unroll 1
-    while (valid(p)) {
-      const int cnt = g.cnt[g.slot_expert[p.slot]];
-      const int tokens = min(cnt - p.c0, 8 * NT);
-      const int bytes = min(row_bytes, kd * kEb - p.st * row_bytes);
-      const int size = 16 * S::kTiles * pitch + (tokens * kParts * token_pitch + 127) / 128 * 128;
-      const bool wrap = off + size > ring.size;
-      const int need = size + (wrap ? ring.size - off : 0);
-      // the held stages' tokens, when their job ends or the ring has nothing
-      // older to release
-      if (barrier && (p.q != held.q || p.c0 != held.c0)) {
-        if (!release(held, held_head, head, barrier, lane)) return false;
-        barrier = nullptr;
-      }
-      while (used + need > ring.size || head - tail == S::kStages) {
-        if (barrier && tail >= held_head) {
-          if (!release(held, held_head, head, barrier, lane)) return false;
-          barrier = nullptr;
-        }
-        if (!retire(tail, used)) return false;
-      }
-      if (wrap) off = 0;
-      const int s = head % S::kStages;
-      // the place behind this one, and its scales
-      Place n = p;
-      if (++n.st == stages) {
-        n.st = 0;
-        n.c0 += 8 * NT;
-        if (n.c0 >= cnt) {
-          n = at(static_cast<int>(gridDim.x) * S::kGroups + __shfl_sync(kFull, ticket, 0));
-          if (lane == 0 && valid(n)) ticket = atomicAdd(taken, 1u);
-        }
-      }
-      const float next_scale = scale_of(n, lane);
-      if (FP8 && lane < S::kScales) ring.scales[s * S::kScales + lane] = scale;
-      __syncwarp();
-      int rows = 0;  // weight rows that are copied
+    if (kLowColumns && lane >= 16) src += static_cast<int64_t>(a.T) * (a.K + a.S) * kd * 2;
 #pragma unroll
-      for (int mt = 0; mt < S::kTiles; ++mt) {
-        const int left = min(max(limit - (p.tile * S::kTiles + mt) * kRows, 0), kRows);
-        rows += UP ? 2 * left : left;
+    for (int nt = 0; nt < NT; ++nt) {
+      const int n = c.j.c0 + lane_token(nt);
+      c.col[nt] = nullptr;
+      if (n < min(cnt, c.j.c0 + kTokens)) {
+        const int entry = g.order[at + n];
+        c.col[nt] = src + static_cast<int64_t>(UP ? entry / (a.K + a.S) : entry) * kd * 2 + c.o * (2 / kEb);
       }
-      if (lane == 0) {
-        ring.stage[s] = Stage{off, p.slot, p.tile, p.c0, bytes, tokens, p.st * 4 + (p.st + 1 == stages ? kLast : 0) + (barrier ? kHeld : 0), need};
-        mbar_arrive_expect_tx(ring.full + s, rows * bytes + tokens * kParts * bytes * (2 / kEb));
-        mbar_arrive(ring.go + s);
-      }
-      __syncwarp();
-      copy_weights(p, off, bytes, ring.full + s, 0, lane);
-      if (!barrier) copy_tokens(p, off, bytes, tokens, ring.full + s, lane * S::kProducers, 32 * S::kProducers);
-      off += size;
-      used += need;
-      ++head;
-      p = n;
-      scale = next_scale;
-    }
-    if (barrier && head != held_head && !release(held, held_head, head, barrier, lane)) return false;
-    // the end of this phase: a stage without copies
-    while (head - tail == S::kStages)
-      if (!retire(tail, used)) return false;
-    if (lane == 0) {
-      ring.stage[head % S::kStages] = Stage{0, 0, 0, 0, 0, 0, -1, 0};
-      mbar_arrive(ring.full + head % S::kStages);
-      mbar_arrive(ring.go + head % S::kStages);
-    }
-    __syncwarp();
-    ++head;
-    return true;
-  }
-  // Waits until the consumers have released the oldest stage.
-  __device__ __forceinline__ bool retire(int& tail, int& used) const {
-    const int s = tail % S::kStages;
-    if (!__all_sync(kFull, ring_wait(a, ring.empty + s, (tail / S::kStages) & 1))) return false;
-    used -= ring.stage[s].taken;
-    ++tail;
-    return true;
-  }
-  // The token rows of the stages held back since `p` (all of one job).
-  __device__ __forceinline__ bool release(Place p, int from, int to, const uint32_t* barrier, int lane) const {
-    bool ok = true;
-    if (lane == 0) ok = grid_wait(a, barrier);
-    if (!__all_sync(kFull, ok)) return false;
-    fence_bulk();
-    for (int h = from; h < to; ++h, ++p.st) {
-      const Stage& st = ring.stage[h % S::kStages];
-      copy_tokens(p, st.off, st.bytes, st.tokens, ring.full + h % S::kStages, lane, 32);
-    }
-    return true;
-  }
-  // A copier: its share of every stage that the producer announces.
-  __device__ __forceinline__ bool assist(int& head, int issuer, int lane) const {
-    bool fenced = false;
-#pragma unroll 1
-    for (;; ++head) {
-      const int s = head % S::kStages;
-      if (!__all_sync(kFull, ring_wait(a, ring.go + s, (head / S::kStages) & 1))) return false;
-      const Stage st = ring.stage[s];
-      if (st.what < 0) {
-        ++head;
-        return true;
-      }
-      const Place p{0, st.slot, st.tile, st.c0, st.what >> 2};
-      copy_weights(p, st.off, st.bytes, ring.full + s, issuer, lane);
-      if (st.what & kHeld) continue;
-      if (!fenced) fence_bulk();  // behind the producer's grid barrier
-      fenced = true;
-      copy_tokens(p, st.off, st.bytes, st.tokens, ring.full + s, issuer + lane * S::kProducers, 32 * S::kProducers);
     }
   }
-
-  // ------------------------------------------------------------- consumers
-
-  // What undoes an entry's factor (e4m3).
-  __device__ __forceinline__ float inverse(int entry) const {
-    return UP ? __ldcg(a.xscale + entry / (a.K + a.S)) : 1.0f / f16_factor(__ldcg(a.amax + entry));
+  __device__ __forceinline__ Cursor begin() const {
+    Cursor c;
+    c.j = at(0);
+    open(c);
+    return c;
   }
-
-  // One result pair of entry `entry`, f its inverse(): up: gate and up of
-  // output `row`; down: outputs row and row + 8.
-  __device__ __forceinline__ void store(int entry, int row, float v0, float v1, float f) const {
-    if (row >= limit) return;
-    const int KS = a.K + a.S;
-    if (FP8) {
-      v0 *= f;
-      v1 *= f;
-    }
-    if (!UP) {
-      float* y = a.y + static_cast<int64_t>(entry) * a.H + row;
-      y[0] = v0;
-      if (row + 8 < limit) y[8] = v1;
+  __device__ __forceinline__ void advance(Cursor& c) const {
+    const int step = team * kRowBytes;
+    c.o += step;
+    if (c.o - (lane & 3) * 16 < kd * kEb) {
+      c.row += step;
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+        if (c.col[nt]) c.col[nt] += step * (2 / kEb);
       return;
     }
-    const float h = act_value(v0, a.act) * v1;
+    c.j = next(c.j);
+    open(c);
+  }
+
+  __device__ __forceinline__ void copy_weights(const Cursor& c, uint32_t dst) const {
+#pragma unroll
+    for (int st = 0; st < S::kSteps; ++st) {
+      const bool in = c.o + st * 64 < kd * kEb;
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt) {
+        const uint32_t d = dst + (st * kStepSlots + 2 * mt) * S::kSlotBytes;
+        // a tile without outputs reads the first again
+        const bool rows = has_rows(c.j, mt);
+        const bool second = UP || MT == 1 || (c.j.tile * MT + mt) * 16 + 8 < limit;
+        const uint8_t* p = c.row + (rows ? static_cast<int64_t>(mt * kRows) * kd * kEb : 0);
+        copy16_stream(d, p + st * 64, in);
+        copy16_stream(d + S::kSlotBytes, p + (second ? c.half : 0) + st * 64, in);
+      }
+    }
+    if (FP8 && lane < 2 * MT)
+      copy4(scales + ((dst - queue) / kStageBytes * 2 * MT + lane) * 4, c.scale + (c.o - lane % 4 * 16) / 128);
+  }
+  __device__ __forceinline__ void copy_tokens(const Cursor& c, uint32_t dst) const {
+    // the second vector: the next 16 bytes, or a's low part
+    const int64_t second = FP8 ? 16 : static_cast<int64_t>(a.T) * (a.K + a.S) * kd * 2;
+#pragma unroll
+    for (int st = 0; st < S::kSteps; ++st) {
+      const bool in = c.o + st * 64 < kd * kEb;
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        const bool any = c.col[nt] != nullptr;
+        const uint32_t d = dst + (st * kStepSlots + 2 * MT + nt * kSlots) * S::kSlotBytes;
+#pragma unroll
+        for (int v = 0; v < kLoads; ++v)
+          copy16_keep(d + v * (kPacked ? 256 : S::kSlotBytes), c.col[nt] + v * second + st * (128 / kEb), in, any);
+      }
+    }
+  }
+
+  // One stage's operands.
+  struct Operands {
+    Vec16 w[S::kSteps][MT][2];
+    Vec16 x[S::kSteps][NT][kLoads];
+    float sc[MT][2];  // block scales of the lane's accumulator rows
+  };
+
+  // has: bit nt: the lane has a token in tile nt (without one its operand
+  // registers, and the columns of its sums, mean nothing).
+  __device__ __forceinline__ void load(Operands& v, uint32_t at, uint32_t has) const {
+#pragma unroll
+    for (int st = 0; st < S::kSteps; ++st) {
+      const uint32_t from = at + st * kStepSlots * S::kSlotBytes;
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i)
+          lds16_if(v.x[st][nt][i],
+                   from + (2 * MT + nt * kSlots) * S::kSlotBytes + i * (kPacked ? 256 : S::kSlotBytes),
+                   (has >> nt) & 1u);
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt) {
+        v.w[st][mt][0] = lds16(from + (2 * mt) * S::kSlotBytes);
+        v.w[st][mt][1] = lds16(from + (2 * mt + 1) * S::kSlotBytes);
+      }
+    }
     if (FP8) {
-      a.a32[static_cast<int64_t>(entry) * a.I + row] = h;
-      // a maximum does not depend on the order
-      atomicMax(a.amax + entry, __float_as_uint(h) & 0x7fffffffu);
-    } else {
-      const __nv_bfloat16 hi = __float2bfloat16_rn(h);
-      const float rest = h - __bfloat162float(hi);
-      __nv_bfloat16* dst = reinterpret_cast<__nv_bfloat16*>(a.a) + static_cast<int64_t>(entry) * a.I + row;
-      dst[0] = hi;
-      dst[static_cast<int64_t>(a.T) * KS * a.I] = __float2bfloat16_rn(isfinite(rest) ? rest : 0.0f);
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          v.sc[mt][h] = lds4(scales + ((at - queue) / kStageBytes * 2 * MT + mt * 2 + h) * 4);
     }
   }
 
@@ -616,77 +586,24 @@ struct Phase {
   // one before it; added at the end of a job (bf16) or a stage (e4m3).
   static constexpr int kChains = MT * NT == 1 ? 4 : 1;
 
-  // The group's stages until the phase ends.  warp: of the group's consumers.
-  __device__ __forceinline__ bool consume(Progress& done, int warp, int lane) const {
-    const int kp = warp % S::WK, mh = warp / S::WK;
-    const uint32_t lane_row = (mh * MT * 16 + (lane >> 2)) * pitch + kp * S::kSteps * 64 + (lane & 3) * 16;
-    const uint32_t lane_token = 16 * S::kTiles * pitch + (lane >> 2) * token_pitch +
-                                (kp * S::kSteps * 64 + (lane & 3) * 16) * (2 / kEb);
-    float acc[kChains][MT][NT][4] = {};
-#pragma unroll 1
-    for (;;) {
-      const int i = done.stages % S::kStages;
-      if (!__all_sync(kFull, ring_wait(a, ring.full + i, (done.stages / S::kStages) & 1))) return false;
-      ++done.stages;
-      const Stage st = ring.stage[i];
-      if (st.what < 0) {
-        __syncwarp();
-        if (lane == 0) mbar_arrive(ring.empty + i);
-        return true;
-      }
-      Vec16 w[S::kSteps][MT][2], x[S::kSteps][NT][kVec];
-      float sc[MT][2] = {};
-#pragma unroll
-      for (int e = 0; e < S::kSteps; ++e) {
-        const bool in = (kp * S::kSteps + e) * 64 + (lane & 3) * 16 < st.bytes;
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          const bool any = in && nt * 8 + (lane >> 2) < st.tokens;
-          const uint32_t from = ring.base + st.off + lane_token + nt * 8 * token_pitch + e * 64 * (2 / kEb);
-#pragma unroll
-          for (int v = 0; v < kVec; ++v)
-            x[e][nt][v] = lds16_if(from + (kParts == 2 ? v * st.tokens * token_pitch : v * 16), any);
-        }
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-          for (int h = 0; h < 2; ++h)
-            w[e][mt][h] = lds16_if(ring.base + st.off + lane_row + (mt * 16 + h * 8) * pitch + e * 64, in);
-      }
-      if (FP8) {
-        const float* from = ring.scales + i * S::kScales + kp * S::kSteps / 2;
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-          for (int h = 0; h < 2; ++h) sc[mt][h] = from[((mh * MT + mt) * 2 + h) * kBlocks];
-      }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(ring.empty + i);
-      multiply(acc, w, x, sc);
-      if ((st.what & kLast) && !finish(acc, st, warp, lane, done.sums)) return false;
-    }
-  }
-
   // acc += the products of one stage.
-  __device__ __forceinline__ void multiply(float (&acc)[kChains][MT][NT][4], const Vec16 (&w)[S::kSteps][MT][2],
-                                           const Vec16 (&x)[S::kSteps][NT][kVec],
-                                           const float (&sc)[MT][2]) const {
+  __device__ __forceinline__ void multiply(float (&acc)[kChains][MT][NT][4], const Operands& v) const {
     float sum[FP8 ? kChains : 1][FP8 ? MT : 1][NT][4] = {};
 #pragma unroll
-    for (int e = 0; e < S::kSteps; ++e) {
+    for (int st = 0; st < S::kSteps; ++st) {
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt) {
-        const Vec16& w0 = w[e][mt][0];
-        const Vec16& w1 = w[e][mt][1];
+        const Vec16& w0 = v.w[st][mt][0];
+        const Vec16& w1 = v.w[st][mt][1];
         if (!FP8) {
 #pragma unroll
           for (int q = 0; q < 4; q += 2)
 #pragma unroll
-            for (int v = 0; v < kVec; ++v)
+            for (int i = 0; i < kLoads; ++i)
 #pragma unroll
               for (int nt = 0; nt < NT; ++nt)
-                mma<false>(acc[(q / 2 * kVec + v + e * (kVec == 1 ? 2 : 0)) % kChains][mt][nt], w0.u[q],
-                           w1.u[q], w0.u[q + 1], w1.u[q + 1], x[e][nt][v].u[q], x[e][nt][v].u[q + 1]);
+                mma<false>(acc[(q / 2 + st * 2) % kChains][mt][nt], w0.u[q], w1.u[q], w0.u[q + 1],
+                           w1.u[q + 1], v.x[st][nt][i].u[q], v.x[st][nt][i].u[q + 1]);
         } else {
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
@@ -696,7 +613,8 @@ struct Phase {
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
               mma<true>(sum[FP8 ? q % kChains : 0][FP8 ? mt : 0][nt], a0, a1, a2, a3,
-                        x[e][nt][(q / 2) % kVec].u[q % 2 * 2], x[e][nt][(q / 2) % kVec].u[q % 2 * 2 + 1]);
+                        v.x[st][nt][(q / 2) % kLoads].u[q % 2 * 2],
+                        v.x[st][nt][(q / 2) % kLoads].u[q % 2 * 2 + 1]);
           }
         }
       }
@@ -711,67 +629,169 @@ struct Phase {
             float t = sum[0][FP8 ? mt : 0][nt][r];
 #pragma unroll
             for (int c = 1; c < (FP8 ? kChains : 1); ++c) t += sum[c][FP8 ? mt : 0][nt][r];
-            acc[0][mt][nt][r] = fmaf(sc[mt][r / 2], t, acc[0][mt][nt][r]);
+            acc[0][mt][nt][r] = fmaf(v.sc[mt][r / 2], t, acc[0][mt][nt][r]);
           }
     }
   }
 
-  // The end of a job: the WK warps' sums are added in warp order by one of
-  // them (another one each time) and stored; acc is cleared.
-  __device__ __forceinline__ bool finish(float (&acc)[kChains][MT][NT][4], const Stage& st, int warp, int lane,
-                                         int& sums) const {
-    const int kp = warp % S::WK, mh = warp / S::WK;
-    const int begin = g.start[g.slot_expert[st.slot]] + st.c0;
-    if (!FP8) {
-#pragma unroll
-      for (int c = 1; c < kChains; ++c)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) acc[0][0][0][r] += acc[c][0][0][r];
-    }
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt, ++sums) {
-      const int buf = sums % S::kRed, use = sums / S::kRed;
-      float* red = ring.red + buf * (S::kRedBytes / S::kRed / 4);
-      if (use > 0 && !__all_sync(kFull, ring_wait(a, ring.red_empty + buf, (use - 1) & 1))) return false;
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) red[((warp * NT + nt) * 4 + r) * 32 + lane] = acc[0][mt][nt][r];
-      __syncwarp();
-      if (lane == 0) mbar_arrive(ring.red_full + buf);
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        if ((nt + sums) % S::WK != kp) continue;
-        if (!__all_sync(kFull, ring_wait(a, ring.red_full + buf, use & 1))) return false;
-        const float* from = red + (mh * S::WK * NT + nt) * 4 * 32 + lane;
-        float v[4];
-#pragma unroll
-        for (int r = 0; r < 4; ++r) v[r] = from[r * 32];
-#pragma unroll
-        for (int i = 1; i < S::WK; ++i)
-#pragma unroll
-          for (int r = 0; r < 4; ++r) v[r] += from[(i * NT * 4 + r) * 32];
-        __syncwarp();
-        if (lane == 0) mbar_arrive(ring.red_empty + buf);
-        const int n = nt * 8 + 2 * (lane & 3);
-        const int row = (st.tile * S::kTiles + mh * MT + mt) * kRows + (lane >> 2);
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-          if (n + i < st.tokens) {
-            const int entry = g.order[begin + n + i];
-            store(entry, row, v[i], v[2 + i], FP8 ? inverse(entry) : 1.0f);
-          }
+  // What undoes an entry's factor (e4m3): loaded at a job's start, worked out
+  // at its end.
+  __device__ __forceinline__ uint32_t held_factor(int entry) const {
+    return UP ? __ldcg(reinterpret_cast<const uint32_t*>(a.xscale) + entry / (a.K + a.S)) : __ldcg(a.amax + entry);
+  }
+  static __device__ __forceinline__ float inverse(uint32_t held) {
+    return UP ? __uint_as_float(held) : 1.0f / f16_factor(held);
+  }
+
+  // One result pair of entry `entry`, f its inverse(): up: gate and up of output `row`; down:
+  // outputs row and row + 8.
+  __device__ __forceinline__ void store(int entry, int row, float v0, float v1, float f) const {
+    if (row >= limit) return;
+    const int KS = a.K + a.S;
+    if (!UP) {
+      if (FP8) {
+        v0 *= f;
+        v1 *= f;
       }
+      float* y = a.y + static_cast<int64_t>(entry) * a.H + row;
+      y[0] = v0;
+      if (row + 8 < limit) y[8] = v1;
+      return;
     }
+    if (FP8) {
+      const float h = act_value(v0 * f, a.act) * (v1 * f);
+      a.a32[static_cast<int64_t>(entry) * a.I + row] = h;
+      // a maximum does not depend on the order
+      atomicMax(a.amax + entry, __float_as_uint(h) & 0x7fffffffu);
+    } else {
+      const float h = act_value(v0, a.act) * v1;
+      const __nv_bfloat16 hi = __float2bfloat16_rn(h);
+      const float rest = h - __bfloat162float(hi);
+      __nv_bfloat16* dst = reinterpret_cast<__nv_bfloat16*>(a.a) + static_cast<int64_t>(entry) * a.I + row;
+      dst[0] = hi;
+      dst[static_cast<int64_t>(a.T) * KS * a.I] = __float2bfloat16_rn(isfinite(rest) ? rest : 0.0f);
+    }
+  }
+
+  __device__ __forceinline__ void sync_team() const {
+    if (team == 1) __syncwarp();
+    else asm volatile("bar.sync %0, %1;" ::"r"(warp / team + 1), "r"(team * 32) : "memory");
+  }
+
+  // The first stages' weights.
+  __device__ __forceinline__ void start(Cursor c) const {
+#pragma unroll 1
+    for (int s = 0; s < kStages - 1 && valid(c.j); ++s) {
+      copy_weights(c, queue + s * kStageBytes);
+      advance(c);
+    }
+  }
+
+  // Everything else.
+  __device__ __forceinline__ void run(Cursor& c, float* red) const {
+#pragma unroll 1
+    for (int s = 0; s < kStages - 1; ++s) {
+      if (valid(c.j)) {
+        copy_tokens(c, queue + s * kStageBytes);
+        advance(c);
+      }
+      copies_commit();
+    }
+    const bool leader = part == 0 && lane == 0;
+    int ticket = 0, sums = 0;
+    if (leader) ticket = static_cast<int>(atomicAdd(given, 1u));
+    uint32_t from = queue, to = queue + (kStages - 1) * kStageBytes;
+    Job j = at(0);
+#pragma unroll 1
+    while (valid(j)) {
+      const int p = g.slot_expert[j.slot];
+      const int cnt = min(g.cnt[p] - j.c0, kTokens), begin = g.start[p] + j.c0;
+      uint32_t has = 0;
 #pragma unroll
-    for (int c = 0; c < kChains; ++c)
-#pragma unroll
-      for (int mt = 0; mt < MT; ++mt)
+      for (int nt = 0; nt < NT; ++nt) has |= (lane_token(nt) < cnt ? 1u : 0u) << nt;
+      uint32_t f[NT][2] = {};
+      if (FP8) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int r = 0; r < 4; ++r) acc[c][mt][nt][r] = 0.0f;
-    return true;
+          for (int i = 0; i < 2; ++i) {
+            const int n = nt * 8 + 2 * (lane & 3) + i;
+            if (n < cnt) f[nt][i] = held_factor(g.order[begin + n]);
+          }
+      }
+      float acc[kChains][MT][NT][4] = {};
+#pragma unroll 1
+      for (int st = part; st < stages; st += team) {
+        copies_wait<kStages - 2>();
+        // the scales are other lanes' copies; and nobody still reads the slot
+        // that is filled next
+        if (FP8) __syncwarp();
+        Operands v;
+        load(v, from, has);
+        // the stage before this one has been multiplied: its slot is free
+        if (valid(c.j)) {
+          copy_weights(c, to);
+          copy_tokens(c, to);
+          advance(c);
+        }
+        copies_commit();
+        multiply(acc, v);
+        to = from;
+        from = from + kStageBytes == queue + kStages * kStageBytes ? queue : from + kStageBytes;
+      }
+      if (!FP8) {
+#pragma unroll
+        for (int i = 1; i < kChains; ++i)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) acc[0][0][0][r] += acc[i][0][0][r];
+      }
+      // the ticket that was asked for at the last job's end
+      const bool ends = j.c0 + kTokens >= g.cnt[p];
+      if (leader && ends) tickets[(fixed + j.i) % kTickets] = fixed * stride_q + ticket;
+      // The team's partial sums, added in warp order by one of its warps.  With
+      // two buffers, whoever writes one has passed the sync behind the reads
+      // of its last contents.
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt, ++sums) {
+        float* buf = red + sums % S::kRed * S::kRedFloats;
+        if (team > 1) {
+          if (S::kRed == 1) sync_team();
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+              buf[((warp * NT + nt) * 4 + r) * 32 + lane] = acc[0][mt][nt][r];
+        }
+        sync_team();
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          if ((sums + nt) % team != part) continue;
+          float (&v)[4] = acc[0][mt][nt];
+          if (team > 1) {
+            const float* at = buf + ((warp - part) * NT + nt) * 4 * 32 + lane;
+#pragma unroll
+            for (int r = 0; r < 4; ++r) v[r] = at[r * 32] + at[(NT * 4 + r) * 32];
+#pragma unroll
+            for (int i = 2; i < 8; ++i)
+              if (i < team) {
+#pragma unroll
+                for (int r = 0; r < 4; ++r) v[r] += at[(i * NT * 4 + r) * 32];
+              }
+          }
+          if (kLowColumns) {  // columns n and n + 4
+#pragma unroll
+            for (int r = 0; r < 4; ++r) v[r] += __shfl_xor_sync(kFull, v[r], 2);
+          }
+          const int n = nt * 8 + 2 * (lane & 3);
+          const int row = (j.tile * MT + mt) * kRows + (lane >> 2);
+          if (n < cnt) store(g.order[begin + n], row, v[0], v[2], inverse(f[nt][0]));
+          if (n + 1 < cnt) store(g.order[begin + n + 1], row, v[1], v[3], inverse(f[nt][1]));
+        }
+      }
+      if (leader && ends) ticket = static_cast<int>(atomicAdd(given, 1u));
+      j = next(j);
+    }
+    copies_wait<0>();
   }
 };
 
@@ -826,124 +846,56 @@ __device__ __forceinline__ void scale_activations(const LayerArgs& a, const Grou
   }
 }
 
-// A grid barrier for a block's consumers: all their writes before it, and the
-// other blocks' after it, seen by every one of them.  A block in which a wait
-// gave up does not arrive, so that no block goes on.
-template <int kConsumerThreads>
-__device__ __forceinline__ void consumers_arrive(uint32_t* arrived, const int* failed) {
-  __threadfence();
-  fence_bulk();
-  named_sync(1, kConsumerThreads);
-  if (threadIdx.x == 0 && !*failed) {
-    __threadfence();
-    atomicAdd(arrived, 1u);
-  }
-}
-template <int kConsumerThreads>
-__device__ __forceinline__ bool consumers_wait(const LayerArgs& a, const uint32_t* arrived, volatile int* failed) {
-  if (threadIdx.x == 0 && !*failed && !grid_wait(a, arrived)) *failed = 1;
-  named_sync(1, kConsumerThreads);
-  const bool done = !*failed;
-  named_sync(1, kConsumerThreads);
-  return done;
-}
-
 template <typename S>
-__global__ void __launch_bounds__(S::kThreads, 1) layer_kernel(LayerArgs a, int ring_size) {
-  constexpr int kConsumerThreads = S::kGroups * S::kConsumers * 32;
-  extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ int failed;  // a wait of this block gave up
-  const int KS = a.K + a.S;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const bool producer = warp >= S::kGroups * S::kConsumers;
-  const int issuer = producer ? (warp - S::kGroups * S::kConsumers) % S::kProducers : 0;
-  const int group = producer ? (warp - S::kGroups * S::kConsumers) / S::kProducers : warp / S::kConsumers;
-  Ring<S> ring;
-  {
-    uint8_t* p = smem + group * static_cast<size_t>(ring_size);
-    ring.base = smem_addr(p);
-    ring.size = ring_size;
-    p = smem + S::kGroups * static_cast<size_t>(ring_size) + group * group_bytes<S>(0);
-    ring.red = reinterpret_cast<float*>(p);
-    p += S::kRedBytes;
-    ring.stage = reinterpret_cast<Stage*>(p);
-    p += S::kStages * sizeof(Stage);
-    ring.full = reinterpret_cast<uint64_t*>(p);
-    ring.empty = ring.full + S::kStages;
-    ring.go = ring.empty + S::kStages;
-    ring.red_full = ring.go + S::kStages;
-    ring.red_empty = ring.red_full + 2;
-    ring.scales = reinterpret_cast<float*>(ring.red_empty + 2);
-  }
-  if (producer && issuer == 0) {
-    if (lane < S::kStages) {
-      mbar_init(ring.go + lane, 1);
-      mbar_init(ring.full + lane, 1);
-      mbar_init(ring.empty + lane, S::kConsumers);
-    }
-    if (lane < S::kRed) {
-      mbar_init(ring.red_full + lane, S::kConsumers);
-      mbar_init(ring.red_empty + lane, S::kReducers);
-    }
-    fence_mbar_init();
-  }
-  if (threadIdx.x == 0) failed = 0;
+__global__ void __launch_bounds__(S::kThreads, 1) layer_kernel(LayerArgs a) {
+  constexpr int kThreads = S::kThreads;
+  extern __shared__ __align__(16) uint8_t smem[];
+  __shared__ int ok;
   grid_dependency_wait();
+  float* red = reinterpret_cast<float*>(smem + kQueueBytes);
   Groups g;
-  group_entries<S::kThreads>(a, g, smem + S::kGroups * group_bytes<S>(ring_size));
-
-  // grid barriers: x16 (e4m3), a, a as fp16 (e4m3), y
-  uint32_t* after_up = a.arrived + 1;
-  uint32_t* after_scale = S::FP8 ? a.arrived + 2 : after_up;
-  uint32_t* after_down = a.arrived + 3;
-  uint32_t* taken = a.arrived + kBarriers;
+  group_entries<kThreads>(a, g, smem + S::kFixedBytes);
+  const int KS = a.K + a.S;
+  uint32_t* arrived = a.arrived;  // of the next barrier
   if (S::FP8) {
-    scale_tokens<S::kThreads>(a, g.tokens, reinterpret_cast<uint32_t*>(smem + S::kGroups * static_cast<size_t>(ring_size)));
-    __threadfence();
-    fence_bulk();
-    __syncthreads();
-    if (threadIdx.x == 0) {
-      __threadfence();
-      atomicAdd(a.arrived, 1u);
-    }
+    scale_tokens<kThreads>(a, g.tokens, reinterpret_cast<uint32_t*>(red));
+    grid_arrive(arrived);
   }
-  const Phase<S, true> up(a, g, ring);
-  const Phase<S, false> down(a, g, ring);
-  if (producer) {
-    const int first = blockIdx.x + gridDim.x * group;
-    int head = 0, tail = 0, off = 0, used = 0;
-    fence_bulk();
-    if (issuer > 0) {
-      if ((!up.assist(head, issuer, lane) || !down.assist(head, issuer, lane)) && lane == 0) failed = 1;
+  {
+    const Phase<S, true> up(a, g, smem);
+    typename Phase<S, true>::Cursor c = up.begin();
+    up.start(c);
+    if (S::FP8 && !grid_wait(a, arrived++, &ok)) {
+      copies_wait<0>();
       return;
     }
-    if (!up.produce(head, tail, off, used, taken, first, S::FP8 ? a.arrived : nullptr, lane) ||
-        !down.produce(head, tail, off, used, taken + 1, first, after_scale, lane)) {
-      // what is still in flight lands before the block may end
-      if (lane == 0) failed = 1;
-      for (; tail < head; ++tail) ring_wait(a, ring.full + tail % S::kStages, (tail / S::kStages) & 1);
+    up.run(c, red);
+  }
+  grid_arrive(arrived);
+  {
+    const Phase<S, false> down(a, g, smem);
+    typename Phase<S, false>::Cursor c = down.begin();
+    down.start(c);
+    bool done = grid_wait(a, arrived++, &ok);
+    if (S::FP8 && done) {
+      scale_activations<kThreads>(a, g);
+      grid_arrive(arrived);
+      done = grid_wait(a, arrived++, &ok);
     }
-    return;
+    if (!done) {
+      copies_wait<0>();
+      return;
+    }
+    down.run(c, red);
   }
-  Progress done;
-  bool ok = up.consume(done, warp % S::kConsumers, lane);
-  if (!ok && lane == 0) failed = 1;
-  consumers_arrive<kConsumerThreads>(after_up, &failed);
-  if (S::FP8) {
-    ok = consumers_wait<kConsumerThreads>(a, after_up, &failed);
-    if (ok) scale_activations<kConsumerThreads>(a, g);
-    consumers_arrive<kConsumerThreads>(after_scale, &failed);
-  }
-  ok = ok && down.consume(done, warp % S::kConsumers, lane);
-  if (!ok && lane == 0) failed = 1;
-  consumers_arrive<kConsumerThreads>(after_down, &failed);
-  if (!consumers_wait<kConsumerThreads>(a, after_down, &failed)) return;
+  grid_arrive(arrived);
+  if (!grid_wait(a, arrived, &ok)) return;
 
   // the entries' rows summed per token, a thread per 4 columns
   const int per = a.H / 4;
   const int64_t n = static_cast<int64_t>(g.tokens) * per;
   for (int64_t i = (static_cast<int64_t>(threadIdx.x >> 5) * gridDim.x + blockIdx.x) * 32 + (threadIdx.x & 31);
-       i < n; i += static_cast<int64_t>(gridDim.x) * kConsumerThreads) {
+       i < n; i += static_cast<int64_t>(gridDim.x) * kThreads) {
     const int t = static_cast<int>(i / per), col = static_cast<int>(i - static_cast<int64_t>(t) * per) * 4;
     float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     const float* y = a.y + static_cast<int64_t>(t) * KS * a.H + col;
@@ -973,17 +925,13 @@ __global__ void layer_start_kernel(uint32_t* arrived) {
 
 template <typename S>
 cudaError_t launch_shape(const moe_handle* h, const LayerArgs& a, cudaStream_t s) {
-  static_assert(2 * S::kStageBytes <= ring_bytes<S>(MOE_LAYER_MAX_TOKENS, MOE_MAX_TOPK + MOE_LAYER_MAX_SHARED,
-                                                    kMaxExperts),
-                "ring");
   auto k = layer_kernel<S>;
-  const int ring = ring_bytes<S>(a.T, a.K + a.S, a.E + a.S);
-  const size_t smem = S::kGroups * group_bytes<S>(ring) + groups_bytes(a.T, a.K + a.S, a.E + a.S);
+  const size_t smem = S::smem(a.T, a.K + a.S, a.E + a.S);
   // per device and cheap: no state to keep
   const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                              static_cast<int>(smem));
   if (e != cudaSuccess) return e;
-  return launch_chained(k, dim3(h->num_sms), dim3(S::kThreads), smem, s, true, a, ring);
+  return launch_chained(k, dim3(h->num_sms), dim3(S::kThreads), smem, s, true, a);
 }
 
 }  // namespace
@@ -1040,13 +988,15 @@ cudaError_t launch_layer(const moe_handle* h, const moe_layer_args& q, int T, vo
   a.act = q.act;
   a.wait_ns = h->wait_ns;
   a.flags = h->flags;
-  // few: 8 tokens an expert and less in the mean
-  const bool many = static_cast<int64_t>(T) * K > 6 * static_cast<int64_t>(a.E);
+  // few: 6 tokens an expert and less in the mean; packed: 2 and less
+  const int64_t entries = static_cast<int64_t>(T) * K;
   if (q.weight_dtype == MOE_E4M3)
-    return many ? launch_shape<Shape<1, 3, 8, 1, 4, 2, 1, true>>(h, a, s)
-                : launch_shape<Shape<2, 1, 8, 1, 1, 1, 2, true>>(h, a, s);
-  return many ? launch_shape<Shape<1, 3, 8, 1, 4, 4, 1, false>>(h, a, s)
-              : launch_shape<Shape<2, 1, 8, 1, 1, 1, 2, false>>(h, a, s);
+    return entries > 6 * a.E   ? launch_shape<Shape<256, 4, 2, 1, true, false>>(h, a, s)
+           : entries > 2 * a.E ? launch_shape<Shape<512, 1, 1, 2, true, false>>(h, a, s)
+                               : launch_shape<Shape<512, 1, 1, 2, true, true>>(h, a, s);
+  return entries > 6 * a.E   ? launch_shape<Shape<256, 4, 4, 1, false, false>>(h, a, s)
+         : entries > 2 * a.E ? launch_shape<Shape<512, 1, 1, 2, false, false>>(h, a, s)
+                             : launch_shape<Shape<512, 1, 1, 2, false, true>>(h, a, s);
 }
 
 }  // namespace moe
