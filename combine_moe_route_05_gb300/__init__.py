@@ -72,6 +72,12 @@ class MoeError(RuntimeError):
 
 _lib = None
 
+# the current stream's raw handle and the current device without the Python
+# objects around them (a third of a small call's host time)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+
 
 def lib():
     """The loaded CUDA library (raises if it is not built or cannot load)."""
@@ -138,7 +144,9 @@ def _stream(stream, device=None):
     """The raw handle of `stream`, else of the current stream of `device` (the
     handle's device; the current device when None)."""
     if stream is None:
-        return torch.cuda.current_stream(device).cuda_stream
+        if device is None:
+            return torch.cuda.current_stream().cuda_stream
+        return _raw_stream(device.index)
     if device is not None and stream.device != device:
         raise ValueError("stream is on %s, the handle on %s" % (stream.device, device))
     return stream.cuda_stream
@@ -147,8 +155,8 @@ def _stream(stream, device=None):
 def _call(h, fn, *args):
     """Library function `fn` called with the handle's device current (the
     library refuses a call made while another device is current)."""
-    f = getattr(lib(), fn)
-    if torch.cuda.current_device() != h.device.index:
+    f = getattr(_lib or lib(), fn)
+    if _current_device() != h.device.index:
         with torch.cuda.device(h.device):
             _check(fn, f(*args))
     else:
@@ -165,6 +173,10 @@ def _row_dtype(t):
 
 def _req(t, dtype=None, shape=None, name="tensor", device=None):
     if t is None:
+        return
+    # the usual case first: these checks are most of a small call's host time
+    if dtype is not None and t.dtype == dtype and t.device == device and t.shape == shape \
+            and t.is_contiguous():
         return
     if shape is not None and any(d < 0 for d in shape):
         shape = None  # no layout yet: the library itself reports MOE_ERR_STATE
