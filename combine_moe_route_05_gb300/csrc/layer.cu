@@ -15,8 +15,8 @@
 // 8..15 the up rows of the same outputs: a lane's accumulators then hold gate
 // and up of one output and the activation needs no exchange.
 //
-// Every lane copies what it will itself multiply into a queue of its own in
-// shared memory (cp.async), several steps ahead and across the ends of jobs,
+// Every warp copies what it will itself multiply into a queue of its own in
+// shared memory (cp.async), several stages ahead and across the ends of jobs,
 // so the stream of weights has no gaps and the queue needs no barrier.  A job
 // is one expert and one tile of outputs; a team of 1, 2, 4 or 8 warps, as many
 // as make the jobs fill the grid evenly, splits its k and adds its partial
@@ -52,7 +52,6 @@ constexpr unsigned kFull = 0xffffffffu;
 constexpr uint16_t kNone = 0xffff;
 constexpr int kBarriers = 4;  // grid barriers of a call, at most
 constexpr int kTickets = 16;  // of a team's coming jobs
-constexpr int kQueueBytes = 192 * 1024;
 
 struct LayerArgs {
   const uint8_t* x;      // [T, H] bf16
@@ -334,13 +333,16 @@ __device__ __forceinline__ float act_value(float g, int act) {
 
 // MT tiles of 16 weight rows by NT tiles of up to 8 tokens a job; a stage of
 // the queue holds STEPS steps of 64 bytes of each weight row.
-template <int THREADS_, int MT_, int NT_, int STEPS_, bool FP8_, bool PACKED_>
+template <int THREADS_, int MT_, int NT_, int STEPS_, int QUEUE_KB_, bool FP8_, bool PACKED_>
 struct Shape {
+  static constexpr int kQueueBytes = QUEUE_KB_ * 1024;
   static constexpr int kThreads = THREADS_, kWarps = THREADS_ / 32;
   static constexpr int MT = MT_, NT = NT_, kSteps = STEPS_;
   static constexpr bool FP8 = FP8_, kPacked = PACKED_;
+  // a in two bf16 parts; with many tokens in one, whose copies and products
+  // would bound the down phase twice over
+  static constexpr bool kSplit = MT * NT == 1;
   static_assert(!kPacked || MT * NT == 1, "packed");
-  static constexpr int kSlotBytes = kThreads * 16;  // 16 bytes per lane
   static constexpr int kRed = MT * NT == 1 ? 2 : 1;  // buffers of partial sums
   static constexpr int kRedFloats = kWarps * NT * 4 * 32;
   static constexpr int kMaxStages = 8;
@@ -369,26 +371,31 @@ struct Phase {
   static constexpr int kEb = FP8 ? 1 : 2;
   static constexpr int kRowBytes = 64 * S::kSteps;  // of a weight row in a stage
   static constexpr int kRows = UP ? 8 : 16;         // outputs that 16 weight rows give
-  // token vectors beside a weight vector: x, or a's two parts; fp16 in e4m3
-  static constexpr int kVec = UP && !FP8 ? 1 : 2;
-  // Packed: 4 tokens to a tile, whose two vectors share the places of one, so
-  // that more of the queue holds weights.  bf16: columns 4..7 take the low parts
-  // of columns 0..3 (one product for both, added at the end); e4m3: the second
-  // vector lies in the places of the lanes without a token.
-  static constexpr bool kPacked = S::kPacked && kVec == 2;
+  // Packed: 4 tokens to a tile, so that more of the queue holds weights.
+  // bf16: rows (and columns) 4..7 of the tile are the low parts of rows 0..3,
+  // one product for both, added at the end.
+  static constexpr bool kPacked = S::kPacked && (FP8 || !UP);
   static constexpr bool kLowColumns = kPacked && !FP8;
-  static constexpr int kTokens = kPacked ? 4 : 8 * NT;  // of a job
-  static constexpr int kSlots = kPacked ? 1 : kVec;     // per token tile
-  static constexpr int kLoads = kLowColumns ? 1 : kVec; // vectors a lane multiplies
-  static constexpr int kStepSlots = 2 * MT + NT * kSlots;
-  static constexpr int kStageBytes = S::kSteps * kStepSlots * S::kSlotBytes;
-  static constexpr int kStages = kQueueBytes / kStageBytes < S::kMaxStages ? kQueueBytes / kStageBytes
-                                                                          : S::kMaxStages;
+  static constexpr int kTokens = kPacked ? 4 : 8 * NT;      // of a job
+  static constexpr bool kLowRows = !UP && !FP8 && S::kSplit && !kPacked;  // behind the tiles
+  static constexpr int kTokenRows = kPacked && FP8 ? 4 : NT * 8 * (kLowRows ? 2 : 1);
+  static constexpr int kTokenBytes = kRowBytes * 2 / kEb;   // of a token row in a stage
+  static constexpr int kLoads = FP8 || kLowRows ? 2 : 1;    // 16-byte vectors of a lane and step
+  // lanes along a row, and rows, of one copy instruction
+  static constexpr int kAcross = kRowBytes / 16, kDown = 32 / kAcross;
+  static constexpr int kTokenAcross = kTokenBytes / 16, kTokenDown = 32 / kTokenAcross;
+  static constexpr int kTokenCopies = kTokenRows / kTokenDown;
+  static constexpr int kWeightBytes = MT * 16 * kRowBytes;  // of a warp's stage
+  static constexpr int kWarpBytes = kWeightBytes + kTokenRows * kTokenBytes;
+  static constexpr int kStageBytes = kWarps * kWarpBytes;
+  static constexpr int kStages = S::kQueueBytes / kStageBytes < S::kMaxStages ? S::kQueueBytes / kStageBytes
+                                                                              : S::kMaxStages;
+  static_assert(kTokenRows % kTokenDown == 0 && 8 % kDown == 0, "copies");
   static_assert(kStages >= 3, "queue");
 
   const LayerArgs& a;
   const Groups& g;
-  uint32_t queue;   // shared-memory address of this lane's queue
+  uint32_t queue;   // shared-memory address of this warp's queue
   uint32_t scales;  // of the warp's block scales
   int kd, tiles, limit, stages, nq;
   int lane, warp, team, part, first_q, stride_q;
@@ -398,8 +405,8 @@ struct Phase {
 
   __device__ __forceinline__ Phase(const LayerArgs& args, const Groups& groups, uint8_t* smem)
       : a(args), g(groups), lane(threadIdx.x & 31), warp(threadIdx.x >> 5) {
-    queue = smem_addr(smem) + threadIdx.x * 16;
-    scales = smem_addr(smem) + kQueueBytes + S::kRedBytes + S::kTicketBytes + warp * S::kMaxStages * 2 * MT * 4;
+    queue = smem_addr(smem) + warp * kWarpBytes;
+    scales = smem_addr(smem) + S::kQueueBytes + S::kRedBytes + S::kTicketBytes + warp * S::kMaxStages * 2 * MT * 4;
     kd = UP ? a.H : a.I;
     limit = UP ? a.I : a.H;
     tiles = (limit + kRows * MT - 1) / (kRows * MT);
@@ -431,7 +438,7 @@ struct Phase {
     // and a ticket is there from the second job behind its request on
     const int per = stages / team;
     fixed = (per - 1 + kStages) / per + 1;
-    tickets = reinterpret_cast<int*>(smem + kQueueBytes + S::kRedBytes) + warp / team * kTickets;
+    tickets = reinterpret_cast<int*>(smem + S::kQueueBytes + S::kRedBytes) + warp / team * kTickets;
     given = a.arrived + kBarriers + (UP ? 0 : 1);
   }
 
@@ -449,18 +456,24 @@ struct Phase {
   __device__ __forceinline__ bool has_rows(const Job& j, int mt) const {
     return MT == 1 || (j.tile * MT + mt) * kRows < limit;
   }
-  // The token (of the job) that this lane's operand holds in tile nt.
-  __device__ __forceinline__ int lane_token(int nt) const {
-    return kLowColumns ? (lane >> 2) & 3 : kPacked && lane >= 16 ? kTokens : nt * 8 + (lane >> 2);
+  // Places of 16-byte units in a row, so that the 8 lanes of a shared-memory
+  // access (two rows, 4 lanes each) meet no bank twice.
+  static __device__ __forceinline__ int weight_unit(int row, int unit) {
+    return S::kSteps == 2 ? unit ^ ((row & 1) << 2) : unit;
+  }
+  static __device__ __forceinline__ int token_unit(int row, int unit) {
+    return FP8 ? unit ^ (row & 1) : weight_unit(row, unit);
   }
 
-  // Where this lane's next copies come from.
+  // Where this warp's next copies come from.  A copy instruction takes kDown
+  // rows of kRowBytes: whole 128-byte lines of few rows (16 rows by 64 bytes
+  // an instruction took 49 GB/s an SM from L2, lines 75).
   struct Cursor {
     Job j;
-    int o;                  // byte of the weight rows, of the lane's 16
-    const uint8_t* row;     // the lane's first weight row, from byte o on
-    int64_t half;           // from it to the lane's second row
-    const uint8_t* col[NT]; // its token's values per token tile, NULL: none
+    int o;                  // byte of the weight rows
+    const uint8_t* row;     // this lane's place in the first kDown rows, from byte o on
+    int64_t half;           // from rows 0..7 of a tile to rows 8..15
+    int col[kTokenCopies];  // the row of x or a that this lane copies from, -1: none
     const float* scale;     // the block scales' row of lanes 0 .. 2 MT - 1
   };
 
@@ -470,8 +483,8 @@ struct Phase {
     const int e = p < a.S ? a.E + p : p - a.S;
     const int r0 = c.j.tile * kRows * MT;
     const int64_t all_rows = UP ? 2 * a.I : a.H;
-    c.o = part * kRowBytes + (lane & 3) * 16;
-    c.row = (UP ? a.w13 : a.w2) + (e * all_rows + r0 + (lane >> 2)) * kd * kEb + c.o;
+    c.o = part * kRowBytes;
+    c.row = (UP ? a.w13 : a.w2) + (e * all_rows + r0 + lane / kAcross) * kd * kEb + c.o + lane % kAcross * 16;
     // the last tile of the down products may have no second half: it reads
     // the first again, and its results go nowhere
     c.half = static_cast<int64_t>(UP ? a.I : MT == 1 && r0 + 8 >= limit ? 0 : 8) * kd * kEb;
@@ -479,16 +492,16 @@ struct Phase {
       const int r = min(r0 + lane / 2 * kRows, limit - 8) + (UP && lane % 2 ? a.I : 0);
       c.scale = (UP ? a.s13 : a.s2) + (e * ((all_rows + 127) / 128) + r / 128) * ((kd + 127) / 128);
     }
-    const int cnt = g.cnt[p], at = g.start[p];
-    const uint8_t* src = UP ? (FP8 ? reinterpret_cast<const uint8_t*>(a.x16) : a.x) : a.a;
-    if (kLowColumns && lane >= 16) src += static_cast<int64_t>(a.T) * (a.K + a.S) * kd * 2;
+    const int cnt = min(g.cnt[p] - c.j.c0, kTokens), begin = g.start[p] + c.j.c0;
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      const int n = c.j.c0 + lane_token(nt);
-      c.col[nt] = nullptr;
-      if (n < min(cnt, c.j.c0 + kTokens)) {
-        const int entry = g.order[at + n];
-        c.col[nt] = src + static_cast<int64_t>(UP ? entry / (a.K + a.S) : entry) * kd * 2 + c.o * (2 / kEb);
+    for (int i = 0; i < kTokenCopies; ++i) {
+      const int row = i * kTokenDown + lane / kTokenAcross;
+      const bool low = kLowColumns ? row >= 4 : kLowRows && row >= NT * 8;
+      const int n = kLowColumns ? row & 3 : low ? row - NT * 8 : row;
+      c.col[i] = -1;
+      if (n < cnt) {
+        const int entry = g.order[begin + n];
+        c.col[i] = (UP ? entry / (a.K + a.S) : entry) + (low ? a.T * (a.K + a.S) : 0);
       }
     }
   }
@@ -501,50 +514,50 @@ struct Phase {
   __device__ __forceinline__ void advance(Cursor& c) const {
     const int step = team * kRowBytes;
     c.o += step;
-    if (c.o - (lane & 3) * 16 < kd * kEb) {
-      c.row += step;
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-        if (c.col[nt]) c.col[nt] += step * (2 / kEb);
-      return;
-    }
+    c.row += step;
+    if (c.o < kd * kEb) return;
     c.j = next(c.j);
     open(c);
   }
 
   __device__ __forceinline__ void copy_weights(const Cursor& c, uint32_t dst) const {
+    const bool in = c.o + lane % kAcross * 16 < kd * kEb;
+    const int64_t down = static_cast<int64_t>(kDown) * kd * kEb;
 #pragma unroll
-    for (int st = 0; st < S::kSteps; ++st) {
-      const bool in = c.o + st * 64 < kd * kEb;
+    for (int mt = 0; mt < MT; ++mt) {
+      // a tile (or its second half) without outputs reads the first again
+      const bool rows = has_rows(c.j, mt);
+      const bool second = UP || MT == 1 || (c.j.tile * MT + mt) * 16 + 8 < limit;
+      const uint8_t* tile = c.row + (rows ? static_cast<int64_t>(mt * kRows) * kd * kEb : 0);
 #pragma unroll
-      for (int mt = 0; mt < MT; ++mt) {
-        const uint32_t d = dst + (st * kStepSlots + 2 * mt) * S::kSlotBytes;
-        // a tile without outputs reads the first again
-        const bool rows = has_rows(c.j, mt);
-        const bool second = UP || MT == 1 || (c.j.tile * MT + mt) * 16 + 8 < limit;
-        const uint8_t* p = c.row + (rows ? static_cast<int64_t>(mt * kRows) * kd * kEb : 0);
-        copy16_stream(d, p + st * 64, in);
-        copy16_stream(d + S::kSlotBytes, p + (second ? c.half : 0) + st * 64, in);
+      for (int h = 0; h < 2; ++h) {
+        const uint8_t* p = tile + (h && second ? c.half : 0);
+#pragma unroll
+        for (int i = 0; i < 8 / kDown; ++i) {
+          const int row = h * 8 + i * kDown + lane / kAcross;
+          copy16_stream(dst + (mt * 16 + row) * kRowBytes + weight_unit(row, lane % kAcross) * 16,
+                        p + i * down, in);
+        }
       }
     }
     if (FP8 && lane < 2 * MT)
-      copy4(scales + ((dst - queue) / kStageBytes * 2 * MT + lane) * 4, c.scale + (c.o - lane % 4 * 16) / 128);
+      copy4(scales + ((dst - queue) / kStageBytes * 2 * MT + lane) * 4, c.scale + c.o / 128);
   }
   __device__ __forceinline__ void copy_tokens(const Cursor& c, uint32_t dst) const {
-    // the second vector: the next 16 bytes, or a's low part
-    const int64_t second = FP8 ? 16 : static_cast<int64_t>(a.T) * (a.K + a.S) * kd * 2;
+    const uint8_t* src = UP ? (FP8 ? reinterpret_cast<const uint8_t*>(a.x16) : a.x) : a.a;
+    const int o = c.o * (2 / kEb) + lane % kTokenAcross * 16;
+    const bool in = o < kd * 2;
 #pragma unroll
-    for (int st = 0; st < S::kSteps; ++st) {
-      const bool in = c.o + st * 64 < kd * kEb;
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        const bool any = c.col[nt] != nullptr;
-        const uint32_t d = dst + (st * kStepSlots + 2 * MT + nt * kSlots) * S::kSlotBytes;
-#pragma unroll
-        for (int v = 0; v < kLoads; ++v)
-          copy16_keep(d + v * (kPacked ? 256 : S::kSlotBytes), c.col[nt] + v * second + st * (128 / kEb), in, any);
-      }
+    for (int i = 0; i < kTokenCopies; ++i) {
+      const int row = i * kTokenDown + lane / kTokenAcross;
+      copy16_keep(dst + kWeightBytes + row * kTokenBytes + token_unit(row, lane % kTokenAcross) * 16,
+                  src + static_cast<int64_t>(c.col[i]) * kd * 2 + o, in, c.col[i] >= 0);
     }
+  }
+
+  // The token (of the job) that this lane's operand holds in tile nt.
+  __device__ __forceinline__ int lane_token(int nt) const {
+    return kLowColumns ? (lane >> 2) & 3 : nt * 8 + (lane >> 2);
   }
 
   // One stage's operands.
@@ -557,21 +570,23 @@ struct Phase {
   // has: bit nt: the lane has a token in tile nt (without one its operand
   // registers, and the columns of its sums, mean nothing).
   __device__ __forceinline__ void load(Operands& v, uint32_t at, uint32_t has) const {
+    const int row = lane >> 2, t = lane & 3;
 #pragma unroll
     for (int st = 0; st < S::kSteps; ++st) {
-      const uint32_t from = at + st * kStepSlots * S::kSlotBytes;
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int i = 0; i < kLoads; ++i)
+        for (int i = 0; i < kLoads; ++i) {
+          const int r = nt * 8 + row + (kLowRows ? i * NT * 8 : 0);
           lds16_if(v.x[st][nt][i],
-                   from + (2 * MT + nt * kSlots) * S::kSlotBytes + i * (kPacked ? 256 : S::kSlotBytes),
+                   at + kWeightBytes + r * kTokenBytes + token_unit(row, FP8 ? st * 8 + t * 2 + i : st * 4 + t) * 16,
                    (has >> nt) & 1u);
+        }
 #pragma unroll
-      for (int mt = 0; mt < MT; ++mt) {
-        v.w[st][mt][0] = lds16(from + (2 * mt) * S::kSlotBytes);
-        v.w[st][mt][1] = lds16(from + (2 * mt + 1) * S::kSlotBytes);
-      }
+      for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          v.w[st][mt][h] = lds16(at + (mt * 16 + h * 8 + row) * kRowBytes + weight_unit(row, st * 4 + t) * 16);
     }
     if (FP8) {
 #pragma unroll
@@ -588,11 +603,11 @@ struct Phase {
 
   // acc += the products of one stage.
   __device__ __forceinline__ void multiply(float (&acc)[kChains][MT][NT][4], const Operands& v) const {
-    float sum[FP8 ? kChains : 1][FP8 ? MT : 1][NT][4] = {};
 #pragma unroll
-    for (int st = 0; st < S::kSteps; ++st) {
+    for (int mt = 0; mt < MT; ++mt) {
+      float sum[FP8 ? kChains : 1][NT][4] = {};
 #pragma unroll
-      for (int mt = 0; mt < MT; ++mt) {
+      for (int st = 0; st < S::kSteps; ++st) {
         const Vec16& w0 = v.w[st][mt][0];
         const Vec16& w1 = v.w[st][mt][1];
         if (!FP8) {
@@ -612,25 +627,23 @@ struct Phase {
             f16_of_e4m3(w1.u[q], a1, a3);
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
-              mma<true>(sum[FP8 ? q % kChains : 0][FP8 ? mt : 0][nt], a0, a1, a2, a3,
+              mma<true>(sum[FP8 ? q % kChains : 0][nt], a0, a1, a2, a3,
                         v.x[st][nt][(q / 2) % kLoads].u[q % 2 * 2],
                         v.x[st][nt][(q / 2) % kLoads].u[q % 2 * 2 + 1]);
           }
         }
       }
-    }
-    if (FP8) {
-#pragma unroll
-      for (int mt = 0; mt < MT; ++mt)
+      if (FP8) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int r = 0; r < 4; ++r) {
-            float t = sum[0][FP8 ? mt : 0][nt][r];
+            float t = sum[0][nt][r];
 #pragma unroll
-            for (int c = 1; c < (FP8 ? kChains : 1); ++c) t += sum[c][FP8 ? mt : 0][nt][r];
+            for (int c = 1; c < (FP8 ? kChains : 1); ++c) t += sum[c][nt][r];
             acc[0][mt][nt][r] = fmaf(v.sc[mt][r / 2], t, acc[0][mt][nt][r]);
           }
+      }
     }
   }
 
@@ -669,7 +682,8 @@ struct Phase {
       const float rest = h - __bfloat162float(hi);
       __nv_bfloat16* dst = reinterpret_cast<__nv_bfloat16*>(a.a) + static_cast<int64_t>(entry) * a.I + row;
       dst[0] = hi;
-      dst[static_cast<int64_t>(a.T) * KS * a.I] = __float2bfloat16_rn(isfinite(rest) ? rest : 0.0f);
+      if (S::kSplit)
+        dst[static_cast<int64_t>(a.T) * KS * a.I] = __float2bfloat16_rn(isfinite(rest) ? rest : 0.0f);
     }
   }
 
@@ -678,25 +692,25 @@ struct Phase {
     else asm volatile("bar.sync %0, %1;" ::"r"(warp / team + 1), "r"(team * 32) : "memory");
   }
 
-  // The first stages' weights.
-  __device__ __forceinline__ void start(Cursor c) const {
+  // The first stages: all of them, or the weights alone while the tokens are
+  // not there yet (c is then left where it was).
+  template <bool WEIGHTS, bool TOKENS>
+  __device__ __forceinline__ void start(Cursor& from) const {
+    Cursor c = from;
 #pragma unroll 1
-    for (int s = 0; s < kStages - 1 && valid(c.j); ++s) {
-      copy_weights(c, queue + s * kStageBytes);
-      advance(c);
+    for (int s = 0; s < kStages - 1; ++s) {
+      if (valid(c.j)) {
+        if (WEIGHTS) copy_weights(c, queue + s * kStageBytes);
+        if (TOKENS) copy_tokens(c, queue + s * kStageBytes);
+        advance(c);
+      }
+      if (TOKENS) copies_commit();
     }
+    if (TOKENS) from = c;
   }
 
   // Everything else.
   __device__ __forceinline__ void run(Cursor& c, float* red) const {
-#pragma unroll 1
-    for (int s = 0; s < kStages - 1; ++s) {
-      if (valid(c.j)) {
-        copy_tokens(c, queue + s * kStageBytes);
-        advance(c);
-      }
-      copies_commit();
-    }
     const bool leader = part == 0 && lane == 0;
     int ticket = 0, sums = 0;
     if (leader) ticket = static_cast<int>(atomicAdd(given, 1u));
@@ -723,9 +737,9 @@ struct Phase {
 #pragma unroll 1
       for (int st = part; st < stages; st += team) {
         copies_wait<kStages - 2>();
-        // the scales are other lanes' copies; and nobody still reads the slot
-        // that is filled next
-        if (FP8) __syncwarp();
+        // the lanes' copies are there for one another, and no lane still
+        // reads the slot that is filled next
+        __syncwarp();
         Operands v;
         load(v, from, has);
         // the stage before this one has been multiplied: its slot is free
@@ -852,7 +866,7 @@ __global__ void __launch_bounds__(S::kThreads, 1) layer_kernel(LayerArgs a) {
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ int ok;
   grid_dependency_wait();
-  float* red = reinterpret_cast<float*>(smem + kQueueBytes);
+  float* red = reinterpret_cast<float*>(smem + S::kQueueBytes);
   Groups g;
   group_entries<kThreads>(a, g, smem + S::kFixedBytes);
   const int KS = a.K + a.S;
@@ -864,10 +878,15 @@ __global__ void __launch_bounds__(S::kThreads, 1) layer_kernel(LayerArgs a) {
   {
     const Phase<S, true> up(a, g, smem);
     typename Phase<S, true>::Cursor c = up.begin();
-    up.start(c);
-    if (S::FP8 && !grid_wait(a, arrived++, &ok)) {
-      copies_wait<0>();
-      return;
+    if (S::FP8) {
+      up.template start<true, false>(c);
+      if (!grid_wait(a, arrived++, &ok)) {
+        copies_wait<0>();
+        return;
+      }
+      up.template start<false, true>(c);
+    } else {
+      up.template start<true, true>(c);
     }
     up.run(c, red);
   }
@@ -875,7 +894,7 @@ __global__ void __launch_bounds__(S::kThreads, 1) layer_kernel(LayerArgs a) {
   {
     const Phase<S, false> down(a, g, smem);
     typename Phase<S, false>::Cursor c = down.begin();
-    down.start(c);
+    down.template start<true, false>(c);
     bool done = grid_wait(a, arrived++, &ok);
     if (S::FP8 && done) {
       scale_activations<kThreads>(a, g);
@@ -886,6 +905,7 @@ __global__ void __launch_bounds__(S::kThreads, 1) layer_kernel(LayerArgs a) {
       copies_wait<0>();
       return;
     }
+    down.template start<false, true>(c);
     down.run(c, red);
   }
   grid_arrive(arrived);
@@ -991,12 +1011,12 @@ cudaError_t launch_layer(const moe_handle* h, const moe_layer_args& q, int T, vo
   // few: 6 tokens an expert and less in the mean; packed: 2 and less
   const int64_t entries = static_cast<int64_t>(T) * K;
   if (q.weight_dtype == MOE_E4M3)
-    return entries > 6 * a.E   ? launch_shape<Shape<256, 4, 2, 1, true, false>>(h, a, s)
-           : entries > 2 * a.E ? launch_shape<Shape<512, 1, 1, 2, true, false>>(h, a, s)
-                               : launch_shape<Shape<512, 1, 1, 2, true, true>>(h, a, s);
-  return entries > 6 * a.E   ? launch_shape<Shape<256, 4, 4, 1, false, false>>(h, a, s)
-         : entries > 2 * a.E ? launch_shape<Shape<512, 1, 1, 2, false, false>>(h, a, s)
-                             : launch_shape<Shape<512, 1, 1, 2, false, true>>(h, a, s);
+    return entries > 6 * a.E   ? launch_shape<Shape<256, 4, 4, 1, 192, true, false>>(h, a, s)
+           : entries > 2 * a.E ? launch_shape<Shape<512, 1, 1, 2, 192, true, false>>(h, a, s)
+                               : launch_shape<Shape<512, 1, 1, 2, 192, true, true>>(h, a, s);
+  return entries > 6 * a.E   ? launch_shape<Shape<256, 4, 6, 1, 168, false, false>>(h, a, s)
+         : entries > 2 * a.E ? launch_shape<Shape<512, 1, 1, 2, 192, false, false>>(h, a, s)
+                             : launch_shape<Shape<512, 1, 1, 2, 192, false, true>>(h, a, s);
 }
 
 }  // namespace moe
