@@ -125,6 +125,43 @@ __device__ __forceinline__ void group_entries(const LayerArgs& a, Groups& g, uin
   smem += up16(4ull * n_exp);
   g.head = reinterpret_cast<int*>(smem);
 
+  if (a.T * KS <= 32) {  // a warp's worth: without the tables of all experts
+    g.tokens = a.live ? min(max(__ldcg(a.live), 0), a.T) : a.T;
+    if (warp == 0) {
+      const bool mine = lane < g.tokens * KS;
+      int e = mine ? expert_of(a, lane) : -1;
+      if (e == -2 && blockIdx.x == 0) raise_flag(a.flags, MOE_DEVERR_BAD_EXPERT);
+      // the lanes of the same expert; a token's second one is dropped
+      uint32_t same = __match_any_sync(kFull, e);
+      const uint32_t token = ((1u << KS) - 1u) << (lane / KS * KS);
+      const bool twice = e >= a.S && (same & token & lanemask_lt()) != 0;
+      if (twice && blockIdx.x == 0) raise_flag(a.flags, MOE_DEVERR_DUP_EXPERT);
+      const bool ok = e >= 0 && !twice;
+      const uint32_t good = __ballot_sync(kFull, ok);
+      same &= good;
+      const int rank = __popc(same & lanemask_lt()), cnt = __popc(same);
+      const bool first = ok && rank == 0;
+      const uint32_t firsts = __ballot_sync(kFull, first);
+      int start = first ? cnt : 0;  // of the experts in order of their first entry
+#pragma unroll
+      for (int off = 1; off < 32; off <<= 1) {
+        const int v = __shfl_up_sync(kFull, start, off);
+        if (lane >= off) start += v;
+      }
+      start = __shfl_sync(kFull, start - cnt, ok ? __ffs(same) - 1 : 0);
+      if (mine) g.rank[lane] = ok ? static_cast<uint16_t>(rank) : kNone;
+      if (ok) g.order[start + rank] = static_cast<uint16_t>(lane);
+      if (first) {
+        g.slot_expert[__popc(firsts & lanemask_lt())] = static_cast<uint16_t>(e);
+        g.cnt[e] = cnt;
+        g.start[e] = start;
+      }
+      if (lane == 0) g.head[kMaxWarps] = __popc(firsts);
+    }
+    __syncthreads();
+    g.nslots = g.head[kMaxWarps];
+    return;
+  }
   for (int e = tid; e < n_exp; e += kThreads) g.cnt[e] = 0;
   g.tokens = a.live ? min(max(__ldcg(a.live), 0), a.T) : a.T;
   const int n = g.tokens * KS;
@@ -390,13 +427,17 @@ struct Phase {
   static constexpr int kStageBytes = kWarps * kWarpBytes;
   static constexpr int kStages = S::kQueueBytes / kStageBytes < S::kMaxStages ? S::kQueueBytes / kStageBytes
                                                                               : S::kMaxStages;
-  static_assert(kTokenRows % kTokenDown == 0 && 8 % kDown == 0, "copies");
+  // an instruction's rows begin at an even one, and weights end on 128 bytes
+  static_assert(kTokenRows % kTokenDown == 0 && 8 % kDown == 0 && kDown % 2 == 0 && kTokenDown % 2 == 0 &&
+                    kWeightBytes % 128 == 0, "copies");
   static_assert(kStages >= 3, "queue");
 
   const LayerArgs& a;
   const Groups& g;
   uint32_t queue;   // shared-memory address of this warp's queue
   uint32_t scales;  // of the warp's block scales
+  // this lane's places in a stage: where it copies to and loads from
+  uint32_t copy_weight, copy_token, load_weight, load_token;
   int kd, tiles, limit, stages, nq;
   int lane, warp, team, part, first_q, stride_q;
   int fixed;       // jobs of a team that are dealt out beforehand
@@ -407,6 +448,13 @@ struct Phase {
       : a(args), g(groups), lane(threadIdx.x & 31), warp(threadIdx.x >> 5) {
     queue = smem_addr(smem) + warp * kWarpBytes;
     scales = smem_addr(smem) + S::kQueueBytes + S::kRedBytes + S::kTicketBytes + warp * S::kMaxStages * 2 * MT * 4;
+    {
+      const int row = lane / kAcross, token = lane / kTokenAcross, odd = (lane >> 2) & 1;
+      copy_weight = row * kRowBytes + ((lane % kAcross * 16) ^ (row % 2 * kTurn));
+      copy_token = kWeightBytes + token * kTokenBytes + ((lane % kTokenAcross * 16) ^ (token % 2 * kTokenTurn));
+      load_weight = (lane >> 2) * kRowBytes + (((lane & 3) * 16) ^ (odd * kTurn));
+      load_token = kWeightBytes + (lane >> 2) * kTokenBytes + (((lane & 3) * (FP8 ? 32 : 16)) ^ (odd * kTokenTurn));
+    }
     kd = UP ? a.H : a.I;
     limit = UP ? a.I : a.H;
     tiles = (limit + kRows * MT - 1) / (kRows * MT);
@@ -456,14 +504,10 @@ struct Phase {
   __device__ __forceinline__ bool has_rows(const Job& j, int mt) const {
     return MT == 1 || (j.tile * MT + mt) * kRows < limit;
   }
-  // Places of 16-byte units in a row, so that the 8 lanes of a shared-memory
-  // access (two rows, 4 lanes each) meet no bank twice.
-  static __device__ __forceinline__ int weight_unit(int row, int unit) {
-    return S::kSteps == 2 ? unit ^ ((row & 1) << 2) : unit;
-  }
-  static __device__ __forceinline__ int token_unit(int row, int unit) {
-    return FP8 ? unit ^ (row & 1) : weight_unit(row, unit);
-  }
+  // Odd rows have two halves of their 16-byte units changed over (bit 2 of a
+  // unit's number, e4m3 tokens: bit 0), so that the 8 lanes of a shared-memory
+  // access, 4 each of two rows, meet no bank twice.
+  static constexpr int kTurn = S::kSteps == 2 ? 64 : 0, kTokenTurn = FP8 ? 16 : kTurn;
 
   // Where this warp's next copies come from.  A copy instruction takes kDown
   // rows of kRowBytes: whole 128-byte lines of few rows (16 rows by 64 bytes
@@ -473,7 +517,8 @@ struct Phase {
     int o;                  // byte of the weight rows
     const uint8_t* row;     // this lane's place in the first kDown rows, from byte o on
     int64_t half;           // from rows 0..7 of a tile to rows 8..15
-    int col[kTokenCopies];  // the row of x or a that this lane copies from, -1: none
+    const uint8_t* col[kTokenCopies];  // this lane's places in rows of x or a
+    uint32_t have;          // bit i: there is a row in col[i]
     const float* scale;     // the block scales' row of lanes 0 .. 2 MT - 1
   };
 
@@ -493,15 +538,19 @@ struct Phase {
       c.scale = (UP ? a.s13 : a.s2) + (e * ((all_rows + 127) / 128) + r / 128) * ((kd + 127) / 128);
     }
     const int cnt = min(g.cnt[p] - c.j.c0, kTokens), begin = g.start[p] + c.j.c0;
+    const uint8_t* src = UP ? (FP8 ? reinterpret_cast<const uint8_t*>(a.x16) : a.x) : a.a;
+    src += c.o * (2 / kEb) + lane % kTokenAcross * 16;
+    c.have = 0;
 #pragma unroll
     for (int i = 0; i < kTokenCopies; ++i) {
       const int row = i * kTokenDown + lane / kTokenAcross;
       const bool low = kLowColumns ? row >= 4 : kLowRows && row >= NT * 8;
       const int n = kLowColumns ? row & 3 : low ? row - NT * 8 : row;
-      c.col[i] = -1;
+      c.col[i] = src;
       if (n < cnt) {
         const int entry = g.order[begin + n];
-        c.col[i] = (UP ? entry / (a.K + a.S) : entry) + (low ? a.T * (a.K + a.S) : 0);
+        c.col[i] += static_cast<int64_t>((UP ? entry / (a.K + a.S) : entry) + (low ? a.T * (a.K + a.S) : 0)) * kd * 2;
+        c.have |= 1u << i;
       }
     }
   }
@@ -514,8 +563,12 @@ struct Phase {
   __device__ __forceinline__ void advance(Cursor& c) const {
     const int step = team * kRowBytes;
     c.o += step;
-    c.row += step;
-    if (c.o < kd * kEb) return;
+    if (c.o < kd * kEb) {
+      c.row += step;
+#pragma unroll
+      for (int i = 0; i < kTokenCopies; ++i) c.col[i] += step * (2 / kEb);
+      return;
+    }
     c.j = next(c.j);
     open(c);
   }
@@ -523,6 +576,7 @@ struct Phase {
   __device__ __forceinline__ void copy_weights(const Cursor& c, uint32_t dst) const {
     const bool in = c.o + lane % kAcross * 16 < kd * kEb;
     const int64_t down = static_cast<int64_t>(kDown) * kd * kEb;
+    dst += copy_weight;
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) {
       // a tile (or its second half) without outputs reads the first again
@@ -533,26 +587,19 @@ struct Phase {
       for (int h = 0; h < 2; ++h) {
         const uint8_t* p = tile + (h && second ? c.half : 0);
 #pragma unroll
-        for (int i = 0; i < 8 / kDown; ++i) {
-          const int row = h * 8 + i * kDown + lane / kAcross;
-          copy16_stream(dst + (mt * 16 + row) * kRowBytes + weight_unit(row, lane % kAcross) * 16,
-                        p + i * down, in);
-        }
+        for (int i = 0; i < 8 / kDown; ++i)
+          copy16_stream(dst + (mt * 16 + h * 8 + i * kDown) * kRowBytes, p + i * down, in);
       }
     }
     if (FP8 && lane < 2 * MT)
-      copy4(scales + ((dst - queue) / kStageBytes * 2 * MT + lane) * 4, c.scale + c.o / 128);
+      copy4(scales + ((dst - copy_weight - queue) / kStageBytes * 2 * MT + lane) * 4, c.scale + c.o / 128);
   }
   __device__ __forceinline__ void copy_tokens(const Cursor& c, uint32_t dst) const {
-    const uint8_t* src = UP ? (FP8 ? reinterpret_cast<const uint8_t*>(a.x16) : a.x) : a.a;
-    const int o = c.o * (2 / kEb) + lane % kTokenAcross * 16;
-    const bool in = o < kd * 2;
+    const bool in = c.o * (2 / kEb) + lane % kTokenAcross * 16 < kd * 2;
+    dst += copy_token;
 #pragma unroll
-    for (int i = 0; i < kTokenCopies; ++i) {
-      const int row = i * kTokenDown + lane / kTokenAcross;
-      copy16_keep(dst + kWeightBytes + row * kTokenBytes + token_unit(row, lane % kTokenAcross) * 16,
-                  src + static_cast<int64_t>(c.col[i]) * kd * 2 + o, in, c.col[i] >= 0);
-    }
+    for (int i = 0; i < kTokenCopies; ++i)
+      copy16_keep(dst + i * kTokenDown * kTokenBytes, c.col[i], in, (c.have >> i) & 1u);
   }
 
   // The token (of the job) that this lane's operand holds in tile nt.
@@ -570,23 +617,20 @@ struct Phase {
   // has: bit nt: the lane has a token in tile nt (without one its operand
   // registers, and the columns of its sums, mean nothing).
   __device__ __forceinline__ void load(Operands& v, uint32_t at, uint32_t has) const {
-    const int row = lane >> 2, t = lane & 3;
 #pragma unroll
     for (int st = 0; st < S::kSteps; ++st) {
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int i = 0; i < kLoads; ++i) {
-          const int r = nt * 8 + row + (kLowRows ? i * NT * 8 : 0);
-          lds16_if(v.x[st][nt][i],
-                   at + kWeightBytes + r * kTokenBytes + token_unit(row, FP8 ? st * 8 + t * 2 + i : st * 4 + t) * 16,
-                   (has >> nt) & 1u);
+          const uint32_t from = FP8 ? (load_token ^ (i * kTokenTurn)) + st * 128 : load_token ^ (st * kTokenTurn);
+          lds16_if(v.x[st][nt][i], at + from + (nt * 8 + (kLowRows ? i * NT * 8 : 0)) * kTokenBytes, (has >> nt) & 1u);
         }
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
         for (int h = 0; h < 2; ++h)
-          v.w[st][mt][h] = lds16(at + (mt * 16 + h * 8 + row) * kRowBytes + weight_unit(row, st * 4 + t) * 16);
+          v.w[st][mt][h] = lds16(at + (load_weight ^ (st * kTurn)) + (mt * 16 + h * 8) * kRowBytes);
     }
     if (FP8) {
 #pragma unroll
@@ -599,7 +643,7 @@ struct Phase {
 
   // Sums that run beside each other, so that a product need not wait for the
   // one before it; added at the end of a job (bf16) or a stage (e4m3).
-  static constexpr int kChains = MT * NT == 1 ? 4 : 1;
+  static constexpr int kChains = MT * NT > 1 ? 1 : FP8 ? 2 : 4;
 
   // acc += the products of one stage.
   __device__ __forceinline__ void multiply(float (&acc)[kChains][MT][NT][4], const Operands& v) const {
@@ -919,11 +963,12 @@ __global__ void __launch_bounds__(S::kThreads, 1) layer_kernel(LayerArgs a) {
     const int t = static_cast<int>(i / per), col = static_cast<int>(i - static_cast<int64_t>(t) * per) * 4;
     float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     const float* y = a.y + static_cast<int64_t>(t) * KS * a.H + col;
-#pragma unroll 4
+#pragma unroll 8
     for (int kk = 0; kk < KS; ++kk) {
-      if (g.rank[t * KS + kk] == kNone) continue;
-      const float w = kk < a.K ? __ldg(a.w + t * a.K + kk) : 1.0f;
-      const float4 f = __ldcg(reinterpret_cast<const float4*>(y + static_cast<int64_t>(kk) * a.H));
+      const bool kept = g.rank[t * KS + kk] != kNone;
+      const float w = kept && kk < a.K ? __ldg(a.w + t * a.K + kk) : 1.0f;
+      float4 f = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      if (kept) f = __ldcg(reinterpret_cast<const float4*>(y + static_cast<int64_t>(kk) * a.H));
       v.x = fmaf(w, f.x, v.x);
       v.y = fmaf(w, f.y, v.y);
       v.z = fmaf(w, f.z, v.z);
