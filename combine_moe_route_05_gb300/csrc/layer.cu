@@ -368,20 +368,25 @@ __device__ __forceinline__ float act_value(float g, int act) {
   return c < -80.0f ? g * 0.0f : g * __fdividef(1.0f, 1.0f + __expf(-c));
 }
 
-// MT tiles of 16 weight rows by NT tiles of up to 8 tokens a job; a stage of
-// the queue holds STEPS steps of 64 bytes of each weight row.
-template <int THREADS_, int MT_, int NT_, int STEPS_, int QUEUE_KB_, bool FP8_, bool PACKED_>
+// A unit of WM warps shares a part of a job's k and its token rows; each warp
+// has MT tiles of 16 weight rows by NT tiles of up to 8 tokens.  A stage of the
+// queue holds STEPS steps of 64 bytes of each row.
+template <int THREADS_, int WM_, int MT_, int NT_, int STEPS_, int QUEUE_KB_, bool FP8_, bool PACKED_>
 struct Shape {
   static constexpr int kQueueBytes = QUEUE_KB_ * 1024;
   static constexpr int kThreads = THREADS_, kWarps = THREADS_ / 32;
-  static constexpr int MT = MT_, NT = NT_, kSteps = STEPS_;
+  static constexpr int WM = WM_, MT = MT_, NT = NT_, kSteps = STEPS_;
+  static constexpr int kTiles = WM * MT, kUnits = kWarps / WM;
+  static constexpr int kMaxTeam = kUnits < 8 ? kUnits : 8;
   static constexpr bool FP8 = FP8_, kPacked = PACKED_;
   // a in two bf16 parts; with many tokens in one, whose copies and products
   // would bound the down phase twice over
-  static constexpr bool kSplit = MT * NT == 1;
+  static constexpr bool kSplit = NT == 1;
   static_assert(!kPacked || MT * NT == 1, "packed");
   static constexpr int kRed = MT * NT == 1 ? 2 : 1;  // buffers of partial sums
-  static constexpr int kRedFloats = kWarps * NT * 4 * 32;
+  static constexpr int kAtOnce = NT > 1 ? 2 : 1;     // token tiles in a buffer
+  static_assert(NT % kAtOnce == 0, "sums");
+  static constexpr int kRedFloats = kWarps * kAtOnce * 4 * 32;
   static constexpr int kMaxStages = 8;
   // behind the queue: partial sums, tickets, block scales of the stages
   static constexpr int kRedBytes = kRed * kRedFloats * 4;
@@ -403,7 +408,8 @@ struct Job {
 // The products of one phase (up or down) for one thread.
 template <typename S, bool UP>
 struct Phase {
-  static constexpr int MT = S::MT, NT = S::NT, kWarps = S::kWarps;
+  static constexpr int WM = S::WM, MT = S::MT, NT = S::NT, kTiles = S::kTiles, kUnits = S::kUnits;
+  static constexpr int kAtOnce = S::kAtOnce;
   static constexpr bool FP8 = S::FP8;
   static constexpr int kEb = FP8 ? 1 : 2;
   static constexpr int kRowBytes = 64 * S::kSteps;  // of a weight row in a stage
@@ -421,72 +427,75 @@ struct Phase {
   // lanes along a row, and rows, of one copy instruction
   static constexpr int kAcross = kRowBytes / 16, kDown = 32 / kAcross;
   static constexpr int kTokenAcross = kTokenBytes / 16, kTokenDown = 32 / kTokenAcross;
-  static constexpr int kTokenCopies = kTokenRows / kTokenDown;
-  static constexpr int kWeightBytes = MT * 16 * kRowBytes;  // of a warp's stage
-  static constexpr int kWarpBytes = kWeightBytes + kTokenRows * kTokenBytes;
-  static constexpr int kStageBytes = kWarps * kWarpBytes;
+  static constexpr int kTokenCopies = kTokenRows / kTokenDown / WM;
+  static constexpr int kWeightBytes = kTiles * 16 * kRowBytes;  // of a unit's stage
+  static constexpr int kUnitBytes = kWeightBytes + kTokenRows * kTokenBytes;
+  static constexpr int kStageBytes = kUnits * kUnitBytes;
   static constexpr int kStages = S::kQueueBytes / kStageBytes < S::kMaxStages ? S::kQueueBytes / kStageBytes
                                                                               : S::kMaxStages;
   // an instruction's rows begin at an even one, and weights end on 128 bytes
-  static_assert(kTokenRows % kTokenDown == 0 && 8 % kDown == 0 && kDown % 2 == 0 && kTokenDown % 2 == 0 &&
+  static_assert(kTokenRows % (kTokenDown * WM) == 0 && 8 % kDown == 0 && kDown % 2 == 0 && kTokenDown % 2 == 0 &&
                     kWeightBytes % 128 == 0, "copies");
   static_assert(kStages >= 3, "queue");
 
   const LayerArgs& a;
   const Groups& g;
-  uint32_t queue;   // shared-memory address of this warp's queue
+  uint32_t queue;   // shared-memory address of this unit's queue
   uint32_t scales;  // of the warp's block scales
   // this lane's places in a stage: where it copies to and loads from
   uint32_t copy_weight, copy_token, load_weight, load_token;
   int kd, tiles, limit, stages, nq;
-  int lane, warp, team, part, first_q, stride_q;
+  int lane, warp, unit, mine;  // mine: the warp's first row tile in its unit
+  int team, part, first_q, stride_q;  // units that split a job's k
   int fixed;       // jobs of a team that are dealt out beforehand
   int* tickets;    // the team's others
   uint32_t* given;
 
   __device__ __forceinline__ Phase(const LayerArgs& args, const Groups& groups, uint8_t* smem)
       : a(args), g(groups), lane(threadIdx.x & 31), warp(threadIdx.x >> 5) {
-    queue = smem_addr(smem) + warp * kWarpBytes;
+    unit = warp / WM;
+    mine = warp % WM * MT;
+    queue = smem_addr(smem) + unit * kUnitBytes;
     scales = smem_addr(smem) + S::kQueueBytes + S::kRedBytes + S::kTicketBytes + warp * S::kMaxStages * 2 * MT * 4;
     {
       const int row = lane / kAcross, token = lane / kTokenAcross, odd = (lane >> 2) & 1;
-      copy_weight = row * kRowBytes + ((lane % kAcross * 16) ^ (row % 2 * kTurn));
-      copy_token = kWeightBytes + token * kTokenBytes + ((lane % kTokenAcross * 16) ^ (token % 2 * kTokenTurn));
-      load_weight = (lane >> 2) * kRowBytes + (((lane & 3) * 16) ^ (odd * kTurn));
+      copy_weight = (mine * 16 + row) * kRowBytes + ((lane % kAcross * 16) ^ (row % 2 * kTurn));
+      copy_token = kWeightBytes + (warp % WM * kTokenCopies * kTokenDown + token) * kTokenBytes + ((lane % kTokenAcross * 16) ^ (token % 2 * kTokenTurn));
+      load_weight = (mine * 16 + (lane >> 2)) * kRowBytes + (((lane & 3) * 16) ^ (odd * kTurn));
       load_token = kWeightBytes + (lane >> 2) * kTokenBytes + (((lane & 3) * (FP8 ? 32 : 16)) ^ (odd * kTokenTurn));
     }
     kd = UP ? a.H : a.I;
     limit = UP ? a.I : a.H;
-    tiles = (limit + kRows * MT - 1) / (kRows * MT);
+    tiles = (limit + kRows * kTiles - 1) / (kRows * kTiles);
     stages = (kd * kEb + kRowBytes - 1) / kRowBytes;
     nq = g.nslots * tiles;
-    // Many jobs: teams of 8 (fewer where that leaves a warp less than four
-    // stages of a job), which makes jobs short enough to even out at the end
-    // what the SMs differ in speed.  Few: the team size with the fewest rounds
-    // over the grid, in units of a one-warp job.
-    const int warps = kWarps * gridDim.x;
+    // Many jobs: teams of up to 8 units (fewer where that leaves a unit less than
+    // four stages of a job), which makes jobs short enough to even out at the
+    // end what the SMs differ in speed.  Few: the team size with the fewest
+    // rounds over the grid, in units of a job of one.
+    const int units = kUnits * gridDim.x;
     team = 1;
-    if (nq >= warps / 8 * 6) {
-      while (team < 8 && 8 * team <= stages) team *= 2;
+    if (nq >= units / S::kMaxTeam * 6) {
+      while (team < S::kMaxTeam && 8 * team <= stages) team *= 2;
     } else {
       float best = 0.0f;
 #pragma unroll 1
-      for (int n = 1; n <= 8 && n <= stages; n *= 2) {
-        const float cost = static_cast<float>((nq * n + warps - 1) / warps) / n;
+      for (int n = 1; n <= S::kMaxTeam && n <= stages; n *= 2) {
+        const float cost = static_cast<float>((nq * n + units - 1) / units) / n;
         if (n == 1 || cost < best) {
           best = cost;
           team = n;
         }
       }
     }
-    first_q = blockIdx.x + gridDim.x * (warp / team);
-    stride_q = gridDim.x * (kWarps / team);
-    part = warp % team;
+    first_q = blockIdx.x + gridDim.x * (unit / team);
+    stride_q = gridDim.x * (kUnits / team);
+    part = unit % team;
     // the copies of a warp run at most (per - 1 + kStages) / per jobs ahead,
     // and a ticket is there from the second job behind its request on
     const int per = stages / team;
     fixed = (per - 1 + kStages) / per + 1;
-    tickets = reinterpret_cast<int*>(smem + S::kQueueBytes + S::kRedBytes) + warp / team * kTickets;
+    tickets = reinterpret_cast<int*>(smem + S::kQueueBytes + S::kRedBytes) + unit / team * kTickets;
     given = a.arrived + kBarriers + (UP ? 0 : 1);
   }
 
@@ -500,9 +509,12 @@ struct Phase {
     if (j.c0 + kTokens < g.cnt[g.slot_expert[j.slot]]) return Job{j.i, j.q, j.slot, j.tile, j.c0 + kTokens};
     return at(j.i + 1);
   }
-  // Whether tile mt of the job has outputs.
+  // The first output of the warp's tile mt, and whether there is one.
+  __device__ __forceinline__ int first_row(const Job& j, int mt) const {
+    return (j.tile * kTiles + mine + mt) * kRows;
+  }
   __device__ __forceinline__ bool has_rows(const Job& j, int mt) const {
-    return MT == 1 || (j.tile * MT + mt) * kRows < limit;
+    return kTiles == 1 || first_row(j, mt) < limit;
   }
   // Odd rows have two halves of their 16-byte units changed over (bit 2 of a
   // unit's number, e4m3 tokens: bit 0), so that the 8 lanes of a shared-memory
@@ -526,13 +538,13 @@ struct Phase {
     if (!valid(c.j)) return;
     const int p = g.slot_expert[c.j.slot];
     const int e = p < a.S ? a.E + p : p - a.S;
-    const int r0 = c.j.tile * kRows * MT;
+    const int r0 = has_rows(c.j, 0) ? first_row(c.j, 0) : 0;  // of no outputs: any rows
     const int64_t all_rows = UP ? 2 * a.I : a.H;
     c.o = part * kRowBytes;
     c.row = (UP ? a.w13 : a.w2) + (e * all_rows + r0 + lane / kAcross) * kd * kEb + c.o + lane % kAcross * 16;
     // the last tile of the down products may have no second half: it reads
     // the first again, and its results go nowhere
-    c.half = static_cast<int64_t>(UP ? a.I : MT == 1 && r0 + 8 >= limit ? 0 : 8) * kd * kEb;
+    c.half = static_cast<int64_t>(UP ? a.I : kTiles == 1 && r0 + 8 >= limit ? 0 : 8) * kd * kEb;
     if (FP8 && lane < 2 * MT) {
       const int r = min(r0 + lane / 2 * kRows, limit - 8) + (UP && lane % 2 ? a.I : 0);
       c.scale = (UP ? a.s13 : a.s2) + (e * ((all_rows + 127) / 128) + r / 128) * ((kd + 127) / 128);
@@ -543,7 +555,7 @@ struct Phase {
     c.have = 0;
 #pragma unroll
     for (int i = 0; i < kTokenCopies; ++i) {
-      const int row = i * kTokenDown + lane / kTokenAcross;
+      const int row = (warp % WM * kTokenCopies + i) * kTokenDown + lane / kTokenAcross;
       const bool low = kLowColumns ? row >= 4 : kLowRows && row >= NT * 8;
       const int n = kLowColumns ? row & 3 : low ? row - NT * 8 : row;
       c.col[i] = src;
@@ -581,7 +593,7 @@ struct Phase {
     for (int mt = 0; mt < MT; ++mt) {
       // a tile (or its second half) without outputs reads the first again
       const bool rows = has_rows(c.j, mt);
-      const bool second = UP || MT == 1 || (c.j.tile * MT + mt) * 16 + 8 < limit;
+      const bool second = UP || kTiles == 1 || first_row(c.j, mt) + 8 < limit;
       const uint8_t* tile = c.row + (rows ? static_cast<int64_t>(mt * kRows) * kd * kEb : 0);
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
@@ -732,8 +744,14 @@ struct Phase {
   }
 
   __device__ __forceinline__ void sync_team() const {
-    if (team == 1) __syncwarp();
-    else asm volatile("bar.sync %0, %1;" ::"r"(warp / team + 1), "r"(team * 32) : "memory");
+    if (team == 1) sync_unit();
+    else asm volatile("bar.sync %0, %1;" ::"r"(unit / team + 1), "r"(team * WM * 32) : "memory");
+  }
+  // Barriers 1 .. 8 are the teams', 8 .. 15 the units' (of two warps: at most
+  // 8 units, whose teams of two and more take 1 .. 4).
+  __device__ __forceinline__ void sync_unit() const {
+    if (WM == 1) __syncwarp();
+    else asm volatile("bar.sync %0, %1;" ::"r"(unit + 8), "r"(WM * 32) : "memory");
   }
 
   // The first stages: all of them, or the weights alone while the tokens are
@@ -755,7 +773,7 @@ struct Phase {
 
   // Everything else.
   __device__ __forceinline__ void run(Cursor& c, float* red) const {
-    const bool leader = part == 0 && lane == 0;
+    const bool leader = part == 0 && warp % WM == 0 && lane == 0;
     int ticket = 0, sums = 0;
     if (leader) ticket = static_cast<int>(atomicAdd(given, 1u));
     uint32_t from = queue, to = queue + (kStages - 1) * kStageBytes;
@@ -783,7 +801,7 @@ struct Phase {
         copies_wait<kStages - 2>();
         // the lanes' copies are there for one another, and no lane still
         // reads the slot that is filled next
-        __syncwarp();
+        sync_unit();
         Operands v;
         load(v, from, has);
         // the stage before this one has been multiplied: its slot is free
@@ -810,40 +828,44 @@ struct Phase {
       // two buffers, whoever writes one has passed the sync behind the reads
       // of its last contents.
 #pragma unroll
-      for (int mt = 0; mt < MT; ++mt, ++sums) {
-        float* buf = red + sums % S::kRed * S::kRedFloats;
-        if (team > 1) {
-          if (S::kRed == 1) sync_team();
+      for (int mt = 0; mt < MT; ++mt) {
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int r = 0; r < 4; ++r)
-              buf[((warp * NT + nt) * 4 + r) * 32 + lane] = acc[0][mt][nt][r];
-        }
-        sync_team();
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          if ((sums + nt) % team != part) continue;
-          float (&v)[4] = acc[0][mt][nt];
+        for (int n0 = 0; n0 < NT; n0 += kAtOnce, ++sums) {
+          float* buf = red + sums % S::kRed * S::kRedFloats;
           if (team > 1) {
-            const float* at = buf + ((warp - part) * NT + nt) * 4 * 32 + lane;
+            if (S::kRed == 1) sync_team();
 #pragma unroll
-            for (int r = 0; r < 4; ++r) v[r] = at[r * 32] + at[(NT * 4 + r) * 32];
+            for (int i = 0; i < kAtOnce; ++i)
 #pragma unroll
-            for (int i = 2; i < 8; ++i)
-              if (i < team) {
-#pragma unroll
-                for (int r = 0; r < 4; ++r) v[r] += at[(i * NT * 4 + r) * 32];
-              }
+              for (int r = 0; r < 4; ++r)
+                buf[((warp * kAtOnce + i) * 4 + r) * 32 + lane] = acc[0][mt][n0 + i][r];
           }
-          if (kLowColumns) {  // columns n and n + 4
+          sync_team();
 #pragma unroll
-            for (int r = 0; r < 4; ++r) v[r] += __shfl_xor_sync(kFull, v[r], 2);
+          for (int i = 0; i < kAtOnce; ++i) {
+            const int nt = n0 + i;
+            if ((sums + i) % team != part) continue;
+            float (&v)[4] = acc[0][mt][nt];
+            if (team > 1) {
+              const float* at = buf + ((warp - part * WM) * kAtOnce + i) * 4 * 32 + lane;
+#pragma unroll
+              for (int r = 0; r < 4; ++r) v[r] = at[r * 32] + at[(WM * kAtOnce * 4 + r) * 32];
+#pragma unroll
+              for (int u = 2; u < S::kMaxTeam; ++u)
+                if (u < team) {
+#pragma unroll
+                  for (int r = 0; r < 4; ++r) v[r] += at[(u * WM * kAtOnce * 4 + r) * 32];
+                }
+            }
+            if (kLowColumns) {  // columns n and n + 4
+#pragma unroll
+              for (int r = 0; r < 4; ++r) v[r] += __shfl_xor_sync(kFull, v[r], 2);
+            }
+            const int n = nt * 8 + 2 * (lane & 3);
+            const int row = first_row(j, mt) + (lane >> 2);
+            if (n < cnt) store(g.order[begin + n], row, v[0], v[2], inverse(f[nt][0]));
+            if (n + 1 < cnt) store(g.order[begin + n + 1], row, v[1], v[3], inverse(f[nt][1]));
           }
-          const int n = nt * 8 + 2 * (lane & 3);
-          const int row = (j.tile * MT + mt) * kRows + (lane >> 2);
-          if (n < cnt) store(g.order[begin + n], row, v[0], v[2], inverse(f[nt][0]));
-          if (n + 1 < cnt) store(g.order[begin + n + 1], row, v[1], v[3], inverse(f[nt][1]));
         }
       }
       if (leader && ends) ticket = static_cast<int>(atomicAdd(given, 1u));
@@ -1056,12 +1078,12 @@ cudaError_t launch_layer(const moe_handle* h, const moe_layer_args& q, int T, vo
   // few: 6 tokens an expert and less in the mean; packed: 2 and less
   const int64_t entries = static_cast<int64_t>(T) * K;
   if (q.weight_dtype == MOE_E4M3)
-    return entries > 6 * a.E   ? launch_shape<Shape<256, 4, 4, 1, 192, true, false>>(h, a, s)
-           : entries > 2 * a.E ? launch_shape<Shape<512, 1, 1, 2, 192, true, false>>(h, a, s)
-                               : launch_shape<Shape<512, 1, 1, 2, 192, true, true>>(h, a, s);
-  return entries > 6 * a.E   ? launch_shape<Shape<256, 4, 6, 1, 168, false, false>>(h, a, s)
-         : entries > 2 * a.E ? launch_shape<Shape<512, 1, 1, 2, 192, false, false>>(h, a, s)
-                             : launch_shape<Shape<512, 1, 1, 2, 192, false, true>>(h, a, s);
+    return entries > 6 * a.E   ? launch_shape<Shape<256, 2, 2, 4, 2, 192, true, false>>(h, a, s)
+           : entries > 2 * a.E ? launch_shape<Shape<512, 1, 1, 1, 2, 192, true, false>>(h, a, s)
+                               : launch_shape<Shape<512, 1, 1, 1, 2, 192, true, true>>(h, a, s);
+  return entries > 6 * a.E   ? launch_shape<Shape<256, 2, 2, 6, 2, 168, false, false>>(h, a, s)
+         : entries > 2 * a.E ? launch_shape<Shape<512, 1, 1, 1, 2, 192, false, false>>(h, a, s)
+                             : launch_shape<Shape<512, 1, 1, 1, 2, 192, false, true>>(h, a, s);
 }
 
 }  // namespace moe
