@@ -49,6 +49,9 @@ struct ActArgs {
   uint32_t* flags;
 };
 
+// Byte of a row's 16-byte vector v.
+__device__ __forceinline__ int64_t byte_of(int v) { return static_cast<int64_t>(v) * 16; }
+
 __device__ __forceinline__ uint4 philox(uint4 c, uint32_t k0, uint32_t k1) {
 #pragma unroll
   for (int r = 0; r < 10; ++r) {
@@ -167,7 +170,7 @@ __global__ void __launch_bounds__(kActThreads) act_rows_kernel(ActArgs a) {
     const float ws = DROP ? w * a.keep_scale : w;
     if (ent < 0) {  // a pad row
       const float zero[N] = {};
-      for (int v = v0 + lane; v < end; v += 32) st_vec(out + v * 16, VT::from_f32(zero));
+      for (int v = v0 + lane; v < end; v += 32) st_vec(out + byte_of(v), VT::from_f32(zero));
       continue;
     }
     for (int v = v0 + lane; v < end; v += 32 * kAhead) {
@@ -175,8 +178,8 @@ __global__ void __launch_bounds__(kActThreads) act_rows_kernel(ActArgs a) {
 #pragma unroll
       for (int k = 0; k < kAhead; ++k)
         if (v + 32 * k < end) {
-          gv[k] = ld_stream(row + (v + 32 * k) * 16);
-          uv[k] = ld_stream(row + a.half_bytes + (v + 32 * k) * 16);
+          gv[k] = ld_stream(row + byte_of(v + 32 * k));
+          uv[k] = ld_stream(row + a.half_bytes + byte_of(v + 32 * k));
         }
 #pragma unroll
       for (int k = 0; k < kAhead; ++k) {
@@ -191,7 +194,7 @@ __global__ void __launch_bounds__(kActThreads) act_rows_kernel(ActArgs a) {
           const float o = gate_value<ACT, kFast>(g[j]) * u[j] * ws;
           g[j] = !DROP || kept[j] ? o : 0.0f;
         }
-        st_vec_cs(out + (v + 32 * k) * 16, VT::from_f32(g));
+        st_vec_cs(out + byte_of(v + 32 * k), VT::from_f32(g));
       }
     }
   }
@@ -226,14 +229,14 @@ __global__ void __launch_bounds__(kActThreads) act_rows_bwd_kernel(ActArgs a) {
     float dot = 0.0f;
     if (ent < 0) {  // a pad row
       const float zero[N] = {};
-      for (int v = lane; v < 2 * a.nvec; v += 32) st_vec(orow + v * 16, VT::from_f32(zero));
+      for (int v = lane; v < 2 * a.nvec; v += 32) st_vec(orow + byte_of(v), VT::from_f32(zero));
       continue;
     }
     for (int v = lane; v < a.nvec; v += 32) {
       float g[N], u[N], d[N];
-      VT::to_f32(ld_vec(grow + v * 16), g);
-      VT::to_f32(ld_vec(grow + a.half_bytes + v * 16), u);
-      VT::to_f32(ld_vec(drow + v * 16), d);
+      VT::to_f32(ld_vec(grow + byte_of(v)), g);
+      VT::to_f32(ld_vec(grow + a.half_bytes + byte_of(v)), u);
+      VT::to_f32(ld_vec(drow + byte_of(v)), d);
       bool kept[N];
       if (DROP) kept_elements<N>(kept, v, ent, a.drop, key, offset);
 #pragma unroll
@@ -249,8 +252,8 @@ __global__ void __launch_bounds__(kActThreads) act_rows_bwd_kernel(ActArgs a) {
         g[j] = live ? dw * u[j] * da : 0.0f;
         u[j] = live ? dw * act : 0.0f;
       }
-      st_vec(orow + v * 16, VT::from_f32(g));
-      st_vec(orow + a.half_bytes + v * 16, VT::from_f32(u));
+      st_vec(orow + byte_of(v), VT::from_f32(g));
+      st_vec(orow + a.half_bytes + byte_of(v), VT::from_f32(u));
     }
     if (a.gw) {
 #pragma unroll

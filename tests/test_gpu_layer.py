@@ -108,6 +108,20 @@ CASES = [
     dict(T=4, E=16, K=3, H=400, I=176, e4m3=True, shared=1),     # blocks cut at 2I, H and I
     dict(T=20, E=6, K=2, H=128, I=336, e4m3=True, act="gelu"),
     dict(T=70, E=4, K=2, H=272, I=128, e4m3=True, score="sigmoid", scale=0.5),
+    # between 2 and 6 tokens an expert in the mean, shared experts with more
+    dict(T=24, E=16, K=3, H=328, I=152, shared=1),
+    dict(T=24, E=16, K=3, H=336, I=160, shared=1, e4m3=True),
+    dict(T=31, E=32, K=5, H=128, I=104, act="gelu"),
+    # more than 6, rows cut inside the last tile of 4 x 16
+    dict(T=60, E=6, K=2, H=392, I=264, shared=1),
+    dict(T=100, E=12, K=5, H=464, I=304, e4m3=True, act="gelu"),
+    # 32 entries and one more (the grouping of one warp, of the block)
+    dict(T=8, E=9, K=4, H=64, I=64),
+    dict(T=11, E=9, K=2, H=64, I=64, shared=1),
+    # thousands of jobs on teams of 8 and 4: all but the first two or so of a
+    # team come from the counter
+    dict(T=8, E=16, K=4, H=4096, I=1152),
+    dict(T=8, E=16, K=4, H=4096, I=1152, e4m3=True),
 ]
 
 
@@ -200,7 +214,6 @@ def test_e4m3_codes_read_as_their_values():
     codes = torch.arange(256, dtype=torch.uint8)
     codes[0x7f] = codes[0xff] = 0
     w2 = codes.view(torch.float8_e4m3fn).reshape(1, H, 1).repeat(1, 1, I).contiguous().to(dev())
-    w13 = torch.zeros(1, 2 * I, 16 * 16, dtype=torch.float8_e4m3fn, device=dev())
     w13 = torch.zeros(1, 2 * I, H, dtype=torch.uint8, device=dev())
     one = torch.tensor([1.0]).to(torch.float8_e4m3fn).view(torch.uint8).item()
     w13[0, 3, 0] = one          # gate 3 = x0
@@ -274,6 +287,22 @@ def test_captured_graph_replays_with_new_inputs():
         graph.replay()
         _, _, got = p.check(n)
         assert (got[n:] == 7.0).all()
+
+
+def test_a_wait_that_gives_up_is_reported_and_the_next_call_works():
+    """With a wait limit of 1 ns the blocks that reach a grid barrier first give
+    up: the call returns, the status word says so, and with the usual limit
+    the same workspace works again."""
+    for e4m3 in (False, True):
+        p = Problem(T=6, E=8, K=2, H=512, I=256, e4m3=e4m3)
+        moe.moe_set_wait_limit(p.r.h, 1)
+        p.call()
+        torch.cuda.synchronize()
+        assert moe.moe_read_device_status(p.r.h) == moe.MOE_DEVERR_TIMEOUT
+        moe.moe_set_wait_limit(p.r.h, 0)
+        moe.moe_clear_device_status(p.r.h)
+        p.call()
+        p.check()
 
 
 def test_two_streams_with_a_workspace_each():
