@@ -39,6 +39,7 @@ EXPORTS = ("moe_status_string", "moe_workspace_bytes", "moe_handle_create", "moe
            "moe_act_rows", "moe_act_rows_bwd", "moe_layer_workspace_bytes", "moe_layer")
 MOE_LAYOUT_STATIC_COUNTERS = 65536
 MOE_LAYOUT_TILE_TOKENS = 512
+MOE_ACT_MAX_WIDTH = 1 << 26
 MOE_LAYER_MAX_TOKENS, MOE_LAYER_MAX_SHARED, MOE_LAYER_MAX_WIDTH = 128, 4, 65536
 
 

@@ -102,10 +102,9 @@ moe_status from_cuda(cudaError_t e) { return e == cudaSuccess ? MOE_OK : MOE_ERR
 
 cudaStream_t as_stream(void* s) { return static_cast<cudaStream_t>(s); }
 
-// Arguments the activation and its backward share.  Rows of 2I elements, so
-// I is held to half the range.
+// Arguments the activation and its backward share.
 bool act_args_ok(int32_t I, int32_t act, double p, const int64_t* rng) {
-  if (I > INT32_MAX / 2) return false;
+  if (I > MOE_ACT_MAX_WIDTH) return false;
   if (act != MOE_ACT_SILU && act != MOE_ACT_GELU) return false;
   if (!(p >= 0.0 && p < 1.0) || moe::dropped_of(p) >= 65536u) return false;
   return moe::dropped_of(p) == 0 || (rng && aligned(rng, 8));

@@ -433,8 +433,10 @@ moe_status moe_w2_absorbed(const moe_handle* h, const void* d_h, int32_t I, cons
  *            draws a new mask when d_rng is advanced before each replay (keep
  *            the pair of each step for its backward).  NULL if drop_p = 0.
  * A dropped element is 0 whatever its inputs hold, and so is a pad row; rows
- * behind the last segment are not written.  0 <= drop_p < 1 and D < 2^16.
+ * behind the last segment are not written.  0 <= drop_p < 1 and D < 2^16; I is
+ * at most MOE_ACT_MAX_WIDTH.
  */
+#define MOE_ACT_MAX_WIDTH (1 << 26)
 moe_status moe_act_rows(const moe_handle* h, const void* d_gu, int32_t I, int32_t dtype,
                         int32_t act, const float* d_recv_w, double drop_p, const int64_t* d_rng,
                         void* d_hs, void* stream);
