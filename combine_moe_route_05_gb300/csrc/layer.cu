@@ -469,14 +469,21 @@ struct Phase {
     tiles = (limit + kRows * kTiles - 1) / (kRows * kTiles);
     stages = (kd * kEb + kRowBytes - 1) / kRowBytes;
     nq = g.nslots * tiles;
-    // Many jobs: teams of up to 8 units (fewer where that leaves a unit less than
-    // four stages of a job), which makes jobs short enough to even out at the
-    // end what the SMs differ in speed.  Few: the team size with the fewest
-    // rounds over the grid, in units of a job of one.
+    // Many jobs: a larger team makes them shorter, so that they even out at the
+    // end what the SMs differ in speed, but has fewer stages between the
+    // barriers at their ends.  A team grows while each of its units keeps 8
+    // stages and it has less than 64 jobs, or 4 stages and 20 jobs (37 of 64
+    // tokens e4m3, DeepSeek-V3 shape: 1375 us with 4 stages and no count of
+    // jobs, 1279 so; 16 tokens, Qwen3-30B shape: 139 us with 8 stages alone, 133
+    // so).  Few: the team size with the fewest rounds over the grid, in units
+    // of a job of one.
     const int units = kUnits * gridDim.x;
     team = 1;
     if (nq >= units / S::kMaxTeam * 6) {
-      while (team < S::kMaxTeam && 8 * team <= stages) team *= 2;
+      const auto grows = [&](int per_unit, int64_t jobs) {
+        return 2 * per_unit * team <= stages && static_cast<int64_t>(nq) * team < jobs * units;
+      };
+      while (team < S::kMaxTeam && (grows(8, 64) || grows(4, 20))) team *= 2;
     } else {
       float best = 0.0f;
 #pragma unroll 1
