@@ -71,8 +71,8 @@ __device__ __forceinline__ uint4 philox(uint4 c, uint32_t k0, uint32_t k1) {
 // kept; drop16: the dropped values in the high half of a word, so that a high
 // half is compared in place and a low half after one shift.
 template <int N>
-__device__ __forceinline__ void kept_elements(bool (&kept)[N], int v, uint32_t ent, uint32_t drop16, uint2 key,
-                                              uint2 offset) {
+__device__ __forceinline__ void kept_elements(bool (&kept)[N], int v, uint32_t ent,
+                                              uint32_t drop16, uint2 key, uint2 offset) {
   const uint32_t oct = N == 8 ? v : v >> 1;
   const uint4 r = philox(make_uint4(oct, ent, offset.x, offset.y), key.x, key.y);
   const uint32_t w[4] = {r.x, r.y, r.z, r.w};
@@ -89,7 +89,8 @@ __device__ __forceinline__ float exp_neg(float c) {
   return FAST ? __expf(-c) : expf(-c);
 }
 
-// The gate's value a(g).  Below c = -88 e^-c is infinite and the sigmoid 0.
+// The gate's value a(g).  Below c = -87.3 the sigmoid, under 2^-126, is 0 (the
+// fast division's result for a denominator above 2^126, infinity among them).
 template <int ACT, bool FAST>
 __device__ __forceinline__ float gate_value(float g) {
   constexpr float kR = 1.5957691216057308f;  // 2 sqrt(2 / pi)
@@ -104,7 +105,9 @@ __device__ __forceinline__ void gate_terms(float g, float& s, float& q, float& d
   float c = g;
   dc = 1.0f;
   if (ACT == MOE_ACT_GELU) {
-    const float g2 = g * g;
+    // bounded, so that c' stays finite beside the 0 that it multiplies at
+    // saturation (from |g| = 1.9e19 on its square is infinite in fp32)
+    const float g2 = fminf(g * g, 1e30f);
     c = kR * g * (1.0f + 0.044715f * g2);
     dc = kR * (1.0f + 0.134145f * g2);
   }
@@ -135,7 +138,8 @@ __device__ __forceinline__ int rows_in_segments(const ActArgs& a) {
 }
 
 __device__ __forceinline__ uint2 split64(int64_t v) {
-  return make_uint2(static_cast<uint32_t>(v), static_cast<uint32_t>(static_cast<uint64_t>(v) >> 32));
+  return make_uint2(static_cast<uint32_t>(v),
+                    static_cast<uint32_t>(static_cast<uint64_t>(v) >> 32));
 }
 
 // Vectors of a row that a warp loads before it works on the first of them:
@@ -161,9 +165,11 @@ __global__ void __launch_bounds__(kActThreads) act_rows_kernel(ActArgs a) {
     offset = split64(a.rng[1]);
   }
   const int64_t W = static_cast<int64_t>(gridDim.x) * (kActThreads / 32);
-  for (int64_t i = static_cast<int64_t>(blockIdx.x) * (kActThreads / 32) + (threadIdx.x >> 5); i < total; i += W) {
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * (kActThreads / 32) + (threadIdx.x >> 5);
+       i < total; i += W) {
     const int r = pieces == 1 ? static_cast<int>(i) : static_cast<int>(i / pieces);
-    const int v0 = pieces == 1 ? 0 : static_cast<int>(i - static_cast<int64_t>(r) * pieces) * kPiece;
+    const int v0 =
+        pieces == 1 ? 0 : static_cast<int>(i - static_cast<int64_t>(r) * pieces) * kPiece;
     const int end = min(v0 + kPiece, a.nvec);
     const uint8_t* row = a.gu + static_cast<int64_t>(r) * 2 * a.half_bytes;
     uint8_t* out = a.out + static_cast<int64_t>(r) * a.half_bytes;
@@ -222,7 +228,8 @@ __global__ void __launch_bounds__(kActThreads) act_rows_bwd_kernel(ActArgs a) {
       if (__ldg(a.pos + i) < 0) a.gw[i] = 0.0f;
   }
   const int64_t W = static_cast<int64_t>(gridDim.x) * (kActThreads / 32);
-  for (int64_t i = static_cast<int64_t>(blockIdx.x) * (kActThreads / 32) + (threadIdx.x >> 5); i < nrows; i += W) {
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * (kActThreads / 32) + (threadIdx.x >> 5);
+       i < nrows; i += W) {
     const int r = static_cast<int>(i);
     const uint8_t* grow = a.gu + static_cast<int64_t>(r) * 2 * a.half_bytes;
     const uint8_t* drow = a.ghs + static_cast<int64_t>(r) * a.half_bytes;

@@ -165,6 +165,25 @@ def test_large_gates_and_values():
         assert torch.equal(ggu[:, I:][pos], (d * g)[pos]) and (ggu[:, I:][~pos].abs() < 1e-30).all()
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("act", ["silu", "gelu"])
+def test_gates_whose_square_is_infinite(dtype, act):
+    """Gates of +-2^70 and +-2^127: a is the identity or 0 and its derivative 1
+    or 0, as for any saturated gate."""
+    r, ent, end, gu, ghs, rw = problem(8, 4, 2, 64, dtype)
+    I = 64
+    gu[:, :I] = torch.tensor([2.0 ** 70, -2.0 ** 70, 2.0 ** 127, -2.0 ** 127], device=dev()).repeat(I // 4)
+    gu[:, I:].clamp_(-1, 1)
+    ghs.clamp_(-1, 1)
+    hs, ggu = torch.empty_like(ghs), torch.empty_like(gu)
+    moe.moe_act_rows(r.h, gu, None, hs, act=act)
+    moe.moe_act_rows_bwd(r.h, ghs, gu, None, ggu, act=act)
+    g, u, d = gu[:, :I], gu[:, I:], ghs
+    one = (g > 0).to(g.dtype)
+    assert torch.equal(hs, one * g * u)
+    assert torch.equal(ggu[:, :I], one * d * u) and torch.equal(ggu[:, I:], one * d * g)
+
+
 def test_masked_places_hide_nan_and_infinity():
     """NaN and infinity in dropped elements and pad rows reach no output."""
     p, seed, off = 0.5, 11, 12
