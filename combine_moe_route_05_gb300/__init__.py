@@ -673,17 +673,21 @@ class MoeRouter:
 
     def layer(self, x, logits, w13, w2, bias=None, s13=None, s2=None, live=None, act="silu",
               num_shared=0, stream=None):
-        """A whole MoE layer for a few tokens: (out, idx, w).  With `live`, rows
-        behind the live tokens are 0 (idx: -1)."""
+        """A whole MoE layer for a few tokens, routed by `logits`: (out, idx, w).
+        With `live`, rows behind the live tokens are 0 (idx: -1)."""
+        if logits is None:
+            raise ValueError("logits: given routes go through moe_layer, which reads idx and w")
         T, H = x.shape
-        make = torch.empty if live is None else torch.zeros
-        out = make(T, H, dtype=torch.bfloat16, device=x.device)
-        idx = torch.full((T, self.h.K), -1, dtype=torch.int32, device=x.device) if live is not None \
-            else torch.empty(T, self.h.K, dtype=torch.int32, device=x.device)
-        w = make(T, self.h.K, dtype=torch.float32, device=x.device)
-        ws = layer_workspace(self.h, H, w2.shape[2], num_shared)
-        moe_layer(self.h, x, logits, w13, w2, out, idx, w, ws, bias, s13, s2, live, act,
-                  num_shared, stream)
+        # the workspace and the cleared rows belong to the stream that uses them
+        with torch.cuda.stream(stream):
+            make = torch.empty if live is None else torch.zeros
+            out = make(T, H, dtype=torch.bfloat16, device=x.device)
+            idx = torch.full((T, self.h.K), -1, dtype=torch.int32, device=x.device) \
+                if live is not None else torch.empty(T, self.h.K, dtype=torch.int32, device=x.device)
+            w = make(T, self.h.K, dtype=torch.float32, device=x.device)
+            ws = layer_workspace(self.h, H, w2.shape[2], num_shared)
+            moe_layer(self.h, x, logits, w13, w2, out, idx, w, ws, bias, s13, s2, live, act,
+                      num_shared, stream)
         return out, idx, w
 
     def w2_absorbed(self, hrows, recv_w, w2, stream=None):

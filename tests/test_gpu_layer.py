@@ -205,6 +205,67 @@ def test_a_bad_token_stays_its_own():
     assert p.out[4].isnan().any() and not p.out[6].isfinite().all()
 
 
+@pytest.mark.parametrize("T,e4m3", [(10, True), (100, False), (100, True)])
+def test_a_bad_token_stays_its_own_in_every_kernel(T, e4m3):
+    p = Problem(T=T, E=8, K=2, H=144, I=48, e4m3=e4m3, shared=1)
+    p.call()
+    want = p.out.clone()
+    p.x[4, 7] = float("nan")
+    p.x[6, 0] = float("inf")
+    p.call()
+    torch.cuda.synchronize()
+    keep = [t for t in range(T) if t not in (4, 6)]
+    assert torch.equal(p.out[keep], want[keep])
+    assert p.out[4].isnan().any() and not p.out[6].isfinite().all()
+
+
+@pytest.mark.parametrize("T,live,e4m3", [(13, 5, True), (100, 7, False), (100, 61, True), (128, 0, True)])
+def test_live_tokens_in_every_kernel(T, live, e4m3):
+    p = Problem(T=T, E=6, K=2, H=160, I=48, shared=1, e4m3=e4m3)
+    p.logits[live:] = np.nan
+    p.x[live:] = float("nan")
+    p.call(live=torch.tensor([live], dtype=torch.int32, device=dev()))
+    idx, w, got = p.check(live)
+    assert (idx[live:] == -9).all() and (w[live:] == -9.0).all() and (got[live:] == 7.0).all()
+
+
+@pytest.mark.parametrize("T,H,I,e4m3", [(3, 264, 72, False), (100, 264, 72, False),
+                                        (3, 272, 80, True), (100, 272, 80, True)])
+def test_unreached_experts_are_not_read_into_the_sums(T, H, I, e4m3):
+    """Experts that no token takes hold NaN; the reached ones lie between them,
+    their last rows and columns cut inside a tile."""
+    p = Problem(T=T, E=7, K=2, H=H, I=I, e4m3=e4m3)
+    p.logits[:, [1, 4]] += 60.0
+    for e in (0, 2, 3, 5, 6):
+        for t in (p.w13, p.w2):
+            (t.view(torch.uint8) if e4m3 else t)[e] = 0x7f if e4m3 else float("nan")
+    p.call()
+    idx, _, _ = p.check()
+    assert set(idx.reshape(-1)) == {1, 4}
+
+
+def test_routes_without_an_expert_hide_their_scores():
+    p = Problem(T=5, E=6, K=3, H=88, I=48)
+    p.idx.copy_(torch.tensor([[0, -1, 2]] * 5, dtype=torch.int32))
+    p.w.copy_(torch.tensor([[0.5, float("nan"), 0.25]] * 5))
+    p.call(logits=None)
+    torch.cuda.synchronize()
+    got = p.out.clone()
+    assert got.isfinite().all()
+    p.w[:, 1] = 0.0
+    p.call(logits=None)
+    p.check()
+    assert torch.equal(p.out, got)
+
+
+def test_most_entries_and_experts():
+    """128 tokens of 16 + 4 experts, 512 + 4 experts: the largest tables."""
+    p = Problem(T=128, E=512, K=16, H=32, I=16, shared=4)
+    p.call()
+    p.check()
+    p.check_route()
+
+
 def test_e4m3_codes_read_as_their_values():
     """Every finite e4m3 code, subnormals among them, as a W2 weight: with one
     expert, I = 16 and a one-hot activation, out is scale * code * a, one
@@ -315,6 +376,58 @@ def test_two_streams_with_a_workspace_each():
             p.call(logits=l, stream=s)
     for p in ps:
         p.check()
+
+
+def test_calls_on_streams_of_three_priorities():
+    """Many calls in flight at once, one a part of the GPU and two all of it,
+    beside a plain product: none waits for blocks that cannot start."""
+    kws = (dict(T=1, E=8, K=2, H=512, I=256), dict(T=100, E=8, K=2, H=1024, I=512),
+           dict(T=24, E=8, K=2, H=1024, I=512, e4m3=True))
+    ps = [Problem(seed=s, **kw) for s, kw in enumerate(kws)]
+    low, high = torch.cuda.Stream.priority_range() if hasattr(torch.cuda.Stream, "priority_range") else (0, -1)
+    streams = [torch.cuda.Stream(priority=q) for q in (low, high, low)]
+    side = torch.cuda.Stream(priority=high)
+    logits = [to_dev(p.logits) for p in ps]
+    bias = [to_dev(p.bias) for p in ps]
+    a = torch.randn(4096, 4096, device=dev(), dtype=torch.bfloat16)
+    torch.cuda.synchronize()
+    for i in range(200):
+        for p, s, l in zip(ps, streams, logits):
+            p.call(logits=l, stream=s)
+        if i % 8 == 0:
+            with torch.cuda.stream(side):
+                a @ a
+    for p in ps:
+        p.check()
+
+
+def test_method_on_another_stream_keeps_its_workspace(monkeypatch):
+    """The workspace freed when the method returns is not given to the current
+    stream while the other one may still use it."""
+    p = Problem(T=9, E=8, K=2, H=64, I=32)
+    p.call()
+    torch.cuda.synchronize()
+    real, seen = moe.layer_workspace, []
+
+    def recorded(*a):
+        ws = real(*a)
+        seen.append((ws.data_ptr(), ws.numel()))
+        return ws
+    monkeypatch.setattr(moe, "layer_workspace", recorded)
+    s = torch.cuda.Stream()
+    logits = to_dev(p.logits)
+    torch.cuda.synchronize()
+    out, idx, w = p.r.layer(p.x, logits, p.w13, p.w2, stream=s)
+    mine = [torch.empty(seen[0][1], dtype=torch.uint8, device=dev()) for _ in range(3)]
+    assert seen[0][0] not in [t.data_ptr() for t in mine]
+    s.synchronize()
+    assert torch.equal(out, p.out) and torch.equal(idx, p.idx) and torch.equal(w, p.w)
+
+
+def test_method_without_logits_is_refused():
+    p = Problem(T=4, E=8, K=2, H=64, I=32)
+    with pytest.raises(ValueError):
+        p.r.layer(p.x, None, p.w13, p.w2)
 
 
 def test_binding_method_with_and_without_live():
