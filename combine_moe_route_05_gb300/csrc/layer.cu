@@ -35,254 +35,11 @@
 // would take four); x becomes fp16 times a power of two that brings its
 // token's largest value to [2^14, 2^15) (exact down to 2^-29 of that), and a
 // likewise per entry (11 bits).
-#include <cstdint>
-#include <type_traits>
-
-#include <cuda_fp16.h>
-
-#include "common.cuh"
-#include "internal.h"
+#include "layer.cuh"
 
 namespace moe {
 namespace {
 
-constexpr int kMaxEntries = MOE_LAYER_MAX_TOKENS * (MOE_MAX_TOPK + MOE_LAYER_MAX_SHARED);
-constexpr int kMaxExperts = MOE_MAX_EXPERTS + MOE_LAYER_MAX_SHARED;
-constexpr unsigned kFull = 0xffffffffu;
-constexpr uint16_t kNone = 0xffff;
-constexpr int kBarriers = 4;  // grid barriers of a call, at most
-constexpr int kTickets = 16;  // of a team's coming jobs
-
-struct LayerArgs {
-  const uint8_t* x;      // [T, H] bf16
-  const int32_t* idx;    // [T, K]
-  const float* w;        // [T, K]
-  const int32_t* live;   // live tokens or NULL
-  const uint8_t* w13;    // [E + S, 2I, H]
-  const uint8_t* w2;     // [E + S, H, I]
-  const float* s13;      // block scales of e4m3 weights
-  const float* s2;
-  __half* x16;           // [T, H] scaled x (e4m3)
-  float* xscale;         // [T] 1 / its factor (e4m3)
-  uint8_t* a;            // bf16 [2][T (K + S), I], high and low part; e4m3: fp16, scaled
-  float* a32;            // [T (K + S), I] (e4m3)
-  uint32_t* amax;        // [T (K + S)] bits of the largest |a| of an entry (e4m3)
-  float* y;              // [T (K + S), H]
-  uint32_t* arrived;     // blocks that reached each grid barrier (kBarriers), then the
-                         // jobs given out in each phase; zero at the start
-  __nv_bfloat16* out;    // [T, H]
-  int T, K, S, E, H, I;
-  int act;
-  unsigned long long wait_ns;
-  uint32_t* flags;
-};
-
-// ---------------------------------------------------------------------------
-// entries (t, k) grouped by expert
-
-// Shared-memory tables of a block.  Entry n = t (K + S) + k, the shared expert
-// j as k = K + j; experts are numbered shared first, so that their many
-// tokens do not come last.
-struct Groups {
-  uint16_t* order;        // entries, grouped
-  uint16_t* rank;         // an entry's place within its expert, kNone: dropped
-  uint16_t* slot_expert;  // experts with entries
-  int* cnt;               // per expert
-  int* start;
-  int* head;              // warp sums, number of slots
-  int tokens, nslots;
-};
-
-__host__ __device__ constexpr size_t up16(size_t b) { return (b + 15) / 16 * 16; }
-
-constexpr int kMaxWarps = 16;
-
-__host__ __device__ constexpr size_t groups_bytes(int T, int KS, int n_exp) {
-  return 2 * up16(2ull * T * KS) + up16(2ull * n_exp) + 2 * up16(4ull * n_exp) +
-         up16(4ull * (kMaxWarps + 1));
-}
-
-__device__ __forceinline__ int expert_of(const LayerArgs& a, int entry) {
-  const int t = entry / (a.K + a.S), k = entry - t * (a.K + a.S);
-  if (k >= a.K) return k - a.K;
-  const int e = __ldcg(a.idx + t * a.K + k);
-  return static_cast<unsigned>(e) < static_cast<unsigned>(a.E) ? e + a.S : e == -1 ? -1 : -2;
-}
-
-template <int kThreads>
-__device__ __forceinline__ void group_entries(const LayerArgs& a, Groups& g, uint8_t* smem) {
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int n_exp = a.E + a.S, KS = a.K + a.S;
-  g.order = reinterpret_cast<uint16_t*>(smem);
-  smem += up16(2ull * a.T * KS);
-  g.rank = reinterpret_cast<uint16_t*>(smem);
-  smem += up16(2ull * a.T * KS);
-  g.slot_expert = reinterpret_cast<uint16_t*>(smem);
-  smem += up16(2ull * n_exp);
-  g.cnt = reinterpret_cast<int*>(smem);
-  smem += up16(4ull * n_exp);
-  g.start = reinterpret_cast<int*>(smem);
-  smem += up16(4ull * n_exp);
-  g.head = reinterpret_cast<int*>(smem);
-
-  if (a.T * KS <= 32) {  // a warp's worth: without the tables of all experts
-    g.tokens = a.live ? min(max(__ldcg(a.live), 0), a.T) : a.T;
-    if (warp == 0) {
-      const bool mine = lane < g.tokens * KS;
-      int e = mine ? expert_of(a, lane) : -1;
-      if (e == -2 && blockIdx.x == 0) raise_flag(a.flags, MOE_DEVERR_BAD_EXPERT);
-      // the lanes of the same expert; a token's second one is dropped
-      uint32_t same = __match_any_sync(kFull, e);
-      const uint32_t token = ((1u << KS) - 1u) << (lane / KS * KS);
-      const bool twice = e >= a.S && (same & token & lanemask_lt()) != 0;
-      if (twice && blockIdx.x == 0) raise_flag(a.flags, MOE_DEVERR_DUP_EXPERT);
-      const bool ok = e >= 0 && !twice;
-      const uint32_t good = __ballot_sync(kFull, ok);
-      same &= good;
-      const int rank = __popc(same & lanemask_lt()), cnt = __popc(same);
-      const bool first = ok && rank == 0;
-      const uint32_t firsts = __ballot_sync(kFull, first);
-      int start = first ? cnt : 0;  // of the experts in order of their first entry
-#pragma unroll
-      for (int off = 1; off < 32; off <<= 1) {
-        const int v = __shfl_up_sync(kFull, start, off);
-        if (lane >= off) start += v;
-      }
-      start = __shfl_sync(kFull, start - cnt, ok ? __ffs(same) - 1 : 0);
-      if (mine) g.rank[lane] = ok ? static_cast<uint16_t>(rank) : kNone;
-      if (ok) g.order[start + rank] = static_cast<uint16_t>(lane);
-      if (first) {
-        g.slot_expert[__popc(firsts & lanemask_lt())] = static_cast<uint16_t>(e);
-        g.cnt[e] = cnt;
-        g.start[e] = start;
-      }
-      if (lane == 0) g.head[kMaxWarps] = __popc(firsts);
-    }
-    __syncthreads();
-    g.nslots = g.head[kMaxWarps];
-    return;
-  }
-  for (int e = tid; e < n_exp; e += kThreads) g.cnt[e] = 0;
-  g.tokens = a.live ? min(max(__ldcg(a.live), 0), a.T) : a.T;
-  const int n = g.tokens * KS;
-  // an entry's expert, checked, in `order` until the entries are placed
-  for (int i = tid; i < n; i += kThreads) {
-    const int e = expert_of(a, i);
-    if (e == -2 && blockIdx.x == 0) raise_flag(a.flags, MOE_DEVERR_BAD_EXPERT);
-    g.order[i] = e >= 0 ? static_cast<uint16_t>(e) : kNone;
-  }
-  __syncthreads();
-  for (int i = tid; i < n; i += kThreads) {
-    const uint16_t e = g.order[i];
-    bool ok = e != kNone;
-    if (ok && e >= a.S) {  // a repeated expert of the token counts once
-      bool seen = false;
-      for (int j = i / KS * KS; j < i; ++j) seen |= g.order[j] == e;
-      if (seen) {
-        ok = false;
-        if (blockIdx.x == 0) raise_flag(a.flags, MOE_DEVERR_DUP_EXPERT);
-      }
-    }
-    g.rank[i] = ok ? static_cast<uint16_t>(atomicAdd(&g.cnt[e], 1)) : kNone;
-  }
-  __syncthreads();
-  // exclusive scan of counts (low 16 bits) and of experts with entries (high)
-  constexpr int kPer = (kMaxExperts + kThreads - 1) / kThreads;
-  int own[kPer], sum = 0;
-#pragma unroll
-  for (int j = 0; j < kPer; ++j) {
-    const int e = tid * kPer + j;
-    const int c = e < n_exp ? g.cnt[e] : 0;
-    own[j] = sum;
-    sum += c + (c ? 0x10000 : 0);
-  }
-  int inc = sum;
-#pragma unroll
-  for (int off = 1; off < 32; off <<= 1) {
-    const int v = __shfl_up_sync(kFull, inc, off);
-    if (lane >= off) inc += v;
-  }
-  if (lane == 31) g.head[warp] = inc;
-  // the entries' experts, before `order` takes the entries
-  constexpr int kMine = kMaxEntries / kThreads;
-  uint16_t mine[kMine];
-#pragma unroll
-  for (int j = 0; j < kMine; ++j)
-    if (tid + j * kThreads < n) mine[j] = g.order[tid + j * kThreads];
-  __syncthreads();
-  int base = inc - sum;
-  for (int wv = 0; wv < warp; ++wv) base += g.head[wv];
-#pragma unroll
-  for (int j = 0; j < kPer; ++j) {
-    const int e = tid * kPer + j;
-    if (e < n_exp) {
-      const int at = base + own[j];
-      g.start[e] = at & 0xffff;
-      if (g.cnt[e]) g.slot_expert[at >> 16] = static_cast<uint16_t>(e);
-    }
-  }
-  if (tid == kThreads - 1) g.head[kMaxWarps] = (base + sum) >> 16;
-  __syncthreads();
-#pragma unroll
-  for (int j = 0; j < kMine; ++j) {
-    const int i = tid + j * kThreads;
-    if (i < n && g.rank[i] != kNone) g.order[g.start[mine[j]] + g.rank[i]] = static_cast<uint16_t>(i);
-  }
-  g.nslots = g.head[kMaxWarps];
-  __syncthreads();
-}
-
-// ---------------------------------------------------------------------------
-// grid-wide barriers
-
-__device__ __forceinline__ unsigned long long global_ns() {
-  unsigned long long t;
-  asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
-  return t;
-}
-
-// This block is done with what the others wait for.
-__device__ __forceinline__ void grid_arrive(uint32_t* arrived) {
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    __threadfence();
-    atomicAdd(arrived, 1u);
-  }
-}
-
-// Waits until every block of the grid has arrived; false, with the status bit
-// set, after the handle's limit.
-__device__ __forceinline__ bool grid_wait(const LayerArgs& a, uint32_t* arrived, int* ok) {
-  if (threadIdx.x == 0) {
-    const unsigned long long t0 = global_ns();
-    bool done = true;
-    for (;;) {
-      uint32_t n;
-      asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(n) : "l"(arrived) : "memory");
-      if (n >= gridDim.x) break;
-      if (global_ns() - t0 > a.wait_ns) {
-        raise_flag(a.flags, MOE_DEVERR_TIMEOUT);
-        done = false;
-        break;
-      }
-    }
-    __threadfence();
-    *ok = done;
-  }
-  __syncthreads();
-  return *ok != 0;
-}
-
-// ---------------------------------------------------------------------------
-// copies and products
-
-// Asynchronous copies of 16 bytes into shared memory; where !valid, zeros are
-// written and nothing is read.  Weights pass by L1, tokens are kept in it.
-__device__ __forceinline__ void copy16_stream(uint32_t dst, const void* src, bool valid) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
-               "r"(valid ? 16 : 0)
-               : "memory");
-}
 // Nothing at all where !any (predicated, since the lanes of a warp differ).
 __device__ __forceinline__ void copy16_keep(uint32_t dst, const void* src, bool valid, bool any) {
   asm volatile(
@@ -291,20 +48,6 @@ __device__ __forceinline__ void copy16_keep(uint32_t dst, const void* src, bool 
       "l"(src), "r"(valid ? 16 : 0), "r"(static_cast<int>(any))
       : "memory");
 }
-__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void copies_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-__device__ __forceinline__ Vec16 lds16(uint32_t p) {
-  Vec16 v;
-  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
-               : "=r"(v.u[0]), "=r"(v.u[1]), "=r"(v.u[2]), "=r"(v.u[3])
-               : "r"(p)
-               : "memory");
-  return v;
-}
-
 // 4 bytes of an asynchronous copy.
 __device__ __forceinline__ void copy4(uint32_t dst, const void* src) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
@@ -339,33 +82,6 @@ __device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uin
         "{%8,%9}, {%0,%1,%2,%3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-
-// Four e4m3 values as two pairs of fp16 (exact; NaN stays NaN).
-__device__ __forceinline__ void f16_of_e4m3(uint32_t four, uint32_t& lo, uint32_t& hi) {
-  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\t"
-      "cvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
-      : "=r"(lo), "=r"(hi)
-      : "r"(four));
-}
-
-__device__ __forceinline__ uint32_t f16x2(float lo, float hi) {
-  const __half2 h = __floats2half2_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&h);
-}
-
-// The power of two that brings a largest magnitude (its bits) to [2^14, 2^15);
-// 1 for zero and for what is not finite.
-__device__ __forceinline__ float f16_factor(uint32_t max_bits) {
-  const int e = static_cast<int>(max_bits >> 23);
-  if (max_bits == 0 || e >= 255) return 1.0f;
-  return __uint_as_float(static_cast<uint32_t>(min(max(127 + 14 + 127 - e, 1), 253)) << 23);
-}
-
-__device__ __forceinline__ float act_value(float g, int act) {
-  const float c = act == MOE_ACT_GELU
-                      ? 1.5957691216057308f * g * (1.0f + 0.044715f * g * g) : g;
-  return c < -80.0f ? g * 0.0f : g * __fdividef(1.0f, 1.0f + __expf(-c));
 }
 
 // A unit of WM warps shares a part of a job's k and its token rows; each warp
@@ -882,57 +598,6 @@ struct Phase {
   }
 };
 
-// fp16 copies of x and their factors: a block per token.
-template <int kThreads>
-__device__ __forceinline__ void scale_tokens(const LayerArgs& a, int tokens, uint32_t* red) {
-  for (int t = blockIdx.x; t < tokens; t += gridDim.x) {
-    const uint8_t* row = a.x + static_cast<int64_t>(t) * a.H * 2;
-    uint32_t m = 0;  // the largest |x|, as bits of a bf16 in the high half
-    for (int v = threadIdx.x; v < a.H / 8; v += kThreads) {
-      const Vec16 x = ld_vec(row + v * 16);
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        m = max(m, max(x.u[i] & 0x7fff0000u, (x.u[i] << 16) & 0x7fff0000u));
-    }
-    m = __reduce_max_sync(kFull, m);
-    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = m;
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < kThreads / 32; ++i) m = max(m, red[i]);
-    __syncthreads();
-    const float f = f16_factor(m);
-    uint8_t* dst = reinterpret_cast<uint8_t*>(a.x16) + static_cast<int64_t>(t) * a.H * 2;
-    for (int v = threadIdx.x; v < a.H / 8; v += kThreads) {
-      float e[8];
-      VecTraits<__nv_bfloat16>::to_f32(ld_vec(row + v * 16), e);
-      Vec16 o;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) o.u[i] = f16x2(e[2 * i] * f, e[2 * i + 1] * f);
-      st_vec(dst + v * 16, o);
-    }
-    if (threadIdx.x == 0) a.xscale[t] = 1.0f / f;
-    for (int k = threadIdx.x; k < a.K + a.S; k += kThreads) a.amax[t * (a.K + a.S) + k] = 0;
-  }
-}
-
-// fp16 copies of the activations, their factors from the entries' maxima.
-template <int kThreads>
-__device__ __forceinline__ void scale_activations(const LayerArgs& a, const Groups& g) {
-  const int per = a.I / 8;
-  const int64_t n = static_cast<int64_t>(g.tokens) * (a.K + a.S) * per;
-  for (int64_t i = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x; i < n;
-       i += static_cast<int64_t>(gridDim.x) * kThreads) {
-    const int entry = static_cast<int>(i / per);
-    if (g.rank[entry] == kNone) continue;
-    const float f = f16_factor(__ldcg(a.amax + entry));
-    const float4* src = reinterpret_cast<const float4*>(a.a32) + 2 * i;
-    const float4 lo = __ldcg(src), hi = __ldcg(src + 1);
-    const Vec16 o{f16x2(lo.x * f, lo.y * f), f16x2(lo.z * f, lo.w * f), f16x2(hi.x * f, hi.y * f),
-                  f16x2(hi.z * f, hi.w * f)};
-    st_vec(a.a + i * 16, o);
-  }
-}
-
 template <typename S>
 __global__ void __launch_bounds__(S::kThreads, 1) layer_kernel(LayerArgs a) {
   constexpr int kThreads = S::kThreads;
@@ -984,31 +649,7 @@ __global__ void __launch_bounds__(S::kThreads, 1) layer_kernel(LayerArgs a) {
   grid_arrive(arrived);
   if (!grid_wait(a, arrived, &ok)) return;
 
-  // the entries' rows summed per token, a thread per 4 columns
-  const int per = a.H / 4;
-  const int64_t n = static_cast<int64_t>(g.tokens) * per;
-  for (int64_t i = (static_cast<int64_t>(threadIdx.x >> 5) * gridDim.x + blockIdx.x) * 32 + (threadIdx.x & 31);
-       i < n; i += static_cast<int64_t>(gridDim.x) * kThreads) {
-    const int t = static_cast<int>(i / per), col = static_cast<int>(i - static_cast<int64_t>(t) * per) * 4;
-    float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    const float* y = a.y + static_cast<int64_t>(t) * KS * a.H + col;
-#pragma unroll 8
-    for (int kk = 0; kk < KS; ++kk) {
-      const bool kept = g.rank[t * KS + kk] != kNone;
-      const float w = kept && kk < a.K ? __ldg(a.w + t * a.K + kk) : 1.0f;
-      float4 f = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-      if (kept) f = __ldcg(reinterpret_cast<const float4*>(y + static_cast<int64_t>(kk) * a.H));
-      v.x = fmaf(w, f.x, v.x);
-      v.y = fmaf(w, f.y, v.y);
-      v.z = fmaf(w, f.z, v.z);
-      v.w = fmaf(w, f.w, v.w);
-    }
-    const __nv_bfloat162 lo = __floats2bfloat162_rn(v.x, v.y), hi = __floats2bfloat162_rn(v.z, v.w);
-    uint2 o;
-    o.x = *reinterpret_cast<const uint32_t*>(&lo);
-    o.y = *reinterpret_cast<const uint32_t*>(&hi);
-    *reinterpret_cast<uint2*>(a.out + static_cast<int64_t>(t) * a.H + col) = o;
-  }
+  sum_entries<kThreads>(a, g);
 }
 
 // Zeroes the barrier counters where no routing kernel does.
@@ -1084,13 +725,12 @@ cudaError_t launch_layer(const moe_handle* h, const moe_layer_args& q, int T, vo
   a.flags = h->flags;
   // few: 6 tokens an expert and less in the mean; packed: 2 and less
   const int64_t entries = static_cast<int64_t>(T) * K;
+  if (entries > 6 * a.E) return launch_layer_many(h, a, q.weight_dtype == MOE_E4M3, s);
   if (q.weight_dtype == MOE_E4M3)
-    return entries > 6 * a.E   ? launch_shape<Shape<256, 2, 2, 4, 2, 192, true, false>>(h, a, s)
-           : entries > 2 * a.E ? launch_shape<Shape<512, 1, 1, 1, 2, 192, true, false>>(h, a, s)
-                               : launch_shape<Shape<512, 1, 1, 1, 2, 192, true, true>>(h, a, s);
-  return entries > 6 * a.E   ? launch_shape<Shape<256, 2, 2, 6, 2, 168, false, false>>(h, a, s)
-         : entries > 2 * a.E ? launch_shape<Shape<512, 1, 1, 1, 2, 192, false, false>>(h, a, s)
-                             : launch_shape<Shape<512, 1, 1, 1, 2, 192, false, true>>(h, a, s);
+    return entries > 2 * a.E ? launch_shape<Shape<512, 1, 1, 1, 2, 192, true, false>>(h, a, s)
+                             : launch_shape<Shape<512, 1, 1, 1, 2, 192, true, true>>(h, a, s);
+  return entries > 2 * a.E ? launch_shape<Shape<512, 1, 1, 1, 2, 192, false, false>>(h, a, s)
+                           : launch_shape<Shape<512, 1, 1, 1, 2, 192, false, true>>(h, a, s);
 }
 
 }  // namespace moe

@@ -1,0 +1,96 @@
+// Building blocks of the kernels on the tensor cores (sm_103a): shared-memory
+// operand descriptors, bounded waits on mbarriers, tensor-memory loads.
+#ifndef MOE_TENSOR_CUH_
+#define MOE_TENSOR_CUH_
+
+#include "common.cuh"
+
+namespace moe {
+namespace {
+
+// Shared-memory matrix descriptor of a K-major operand tile in the 128-byte
+// swizzle layout (rows of 128 bytes, 8-row groups 1024 bytes apart): start
+// address >> 4 in bits 0-13, leading offset 16 B (unused by this layout) in
+// bits 16-29, stride offset 1024 B >> 4 in bits 32-45, descriptor version 1 in
+// bits 46-47, base offset 0 (tiles are 1024-byte aligned), swizzle mode 2
+// (128-byte) in bits 61-63.
+__device__ __forceinline__ uint64_t sw128_desc(uint32_t saddr) {
+  uint64_t d = static_cast<uint64_t>((saddr & 0x3ffffu) >> 4);
+  d |= static_cast<uint64_t>(16 >> 4) << 16;
+  d |= static_cast<uint64_t>(1024 >> 4) << 32;
+  d |= static_cast<uint64_t>(1) << 46;
+  d |= static_cast<uint64_t>(2) << 61;
+  return d;
+}
+
+__device__ __forceinline__ unsigned long long global_ns() {
+  unsigned long long t;
+  asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
+  return t;
+}
+
+// Wait for the phase of `bar` with the given parity; false after limit_ns.
+// Every wait and arrival here has the default semantics (acquire / release at
+// CTA scope), also across the pair: what crosses between the CTAs is tensor
+// memory (ordered by the tcgen05 fences around the barrier) and the bulk
+// copies (complete_tx makes them visible to the thread that observes the
+// phase).  Cluster-scope releases cost about 0.6 us each on this part, which
+// at one per slice and warp made the pair slower than a single CTA.
+// The test suspends the thread until the phase completes or about
+// kSuspendNs have passed, so that waiting warps (an epilogue waits a whole
+// tile) do not spend the issue slots the prologue needs.
+constexpr uint32_t kSuspendNs = 20000;
+
+__device__ __forceinline__ bool phase_done(uint64_t* bar, uint32_t parity) {
+  uint32_t done;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(done)
+      : "r"(smem_addr(bar)), "r"(parity), "r"(kSuspendNs)
+      : "memory");
+  return done != 0;
+}
+
+__device__ __forceinline__ bool wait_phase(uint64_t* bar, uint32_t parity,
+                                           unsigned long long limit_ns) {
+  if (phase_done(bar, parity)) return true;
+  const unsigned long long t0 = global_ns();
+  for (;;) {
+    if (phase_done(bar, parity)) return true;
+    if (global_ns() - t0 > limit_ns) return false;
+  }
+}
+
+__device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(bar)) : "memory");
+}
+
+__device__ __forceinline__ void tc_fence_before() {
+  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+}
+__device__ __forceinline__ void tc_fence_after() {
+  asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+}
+
+// 16 consecutive fp32 columns of this warp's 32 tensor-memory lanes.  The
+// load and its wait are one asm statement: the load is asynchronous, and the
+// registers are defined only once the wait has returned, so no use of them
+// may be scheduled in between.
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&v)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]),
+        "=r"(v[7]), "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]),
+        "=r"(v[14]), "=r"(v[15])
+      : "r"(taddr)
+      : "memory");
+}
+
+}  // namespace
+}  // namespace moe
+
+#endif  // MOE_TENSOR_CUH_
