@@ -10,8 +10,8 @@
 //
 //   warps 0..3   epilogue: a thread per weight row (tensor-memory lane)
 //   warp  4      issues the products
-//   warps 8..15  copy weights and tokens into the queue, 128-byte lines of a
-//                row at a time, swizzled as the products want them
+//   warps 8..15  fill the queue: weights by tensor copies (four threads, 32
+//                rows each), tokens row by row, since they are gathered
 //
 // Up tiles hold 64 outputs: in each warp's quarter of the 128 rows 16 gate rows
 // and the 16 up rows of the same outputs, so that the epilogue pairs gate and
@@ -36,6 +36,7 @@ constexpr int kEpilogueWarps = 4, kMmaWarp = 4, kFirstCopyWarp = 8, kCopyWarps =
 constexpr int kCopyThreads = 32 * kCopyWarps;
 static_assert((kFirstCopyWarp + kCopyWarps) * 32 == kThreads, "roles");
 constexpr int kTileRows = 128;
+constexpr int kParts = 4;        // tensor copies of a stage's weights
 constexpr uint32_t kWeightBytes = kTileRows * 128;  // of a stage: 128 bytes of each row
 constexpr int kJobRing = 32;     // jobs on their way from the copying warps to the others
 constexpr int kMaxRing = 10;     // stages of the queue
@@ -47,7 +48,9 @@ static_assert(kFixedBytes + groups_bytes(MOE_LAYER_MAX_TOKENS, MOE_MAX_TOPK + MO
                                          kMaxExperts) + 64 <= 227 * 1024, "shared memory budget");
 
 struct Barriers {
-  uint64_t full[kMaxRing];   // a stage is in place (an arrival per copying warp)
+  uint64_t landed[kMaxRing];  // a stage's weights are there
+  uint64_t full[kMaxRing];   // its tokens, too (an arrival per copying warp); e4m3: and
+                             // its fp16 weights
   uint64_t empty[kMaxRing];  // its products are done
   uint64_t a16_empty[2];     // e4m3: the products of an fp16 slice are done
   uint64_t acc_full[2];      // an accumulator is complete (the commit, and the issuing thread)
@@ -84,6 +87,15 @@ __device__ __forceinline__ void sts16(uint32_t p, const uint32_t (&v)[4]) {
   asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]),
                "r"(v[3])
                : "memory");
+}
+
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, int x, int y,
+                                            int z, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+      "[%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+      "l"(map), "r"(x), "r"(y), "r"(z), "r"(smem_addr(bar))
+      : "memory");
 }
 
 // All but the last `pending` groups of copies have landed.
@@ -128,6 +140,8 @@ struct Place {
 // Where each role stands in the queue and the accumulators: both run on from
 // the up to the down products.
 struct State {
+  Place sent{0, 0};   // copying: the next stage whose weights are asked for
+  int issued = 0;     // stages asked for
   Place fill{0, 0};   // copying: the next stage
   int landing = 0;    // copying: stages that are copied, not yet announced
   Place ready{0, 0};  // copying: the next to be announced; products: the next to be read
@@ -146,6 +160,7 @@ struct ManyPhase {
   const LayerArgs& a;
   const Groups& g;
   Barriers& b;
+  const CUtensorMap* map;
   uint32_t queue, a16;
   int ring, depth;        // stages, and how many of them are in flight
   uint32_t stage_bytes;
@@ -153,8 +168,8 @@ struct ManyPhase {
   uint32_t* given;
 
   __device__ __forceinline__ ManyPhase(const LayerArgs& args, const Groups& groups, Barriers& bars,
-                                       uint32_t smem)
-      : a(args), g(groups), b(bars), queue(smem) {
+                                       const CUtensorMap* weights, uint32_t smem)
+      : a(args), g(groups), b(bars), map(weights), queue(smem) {
     kd = UP ? a.H : a.I;
     limit = UP ? a.I : a.H;
     tiles = (limit + kTileOutputs - 1) / kTileOutputs;
@@ -191,36 +206,34 @@ struct ManyPhase {
 
   // -- copying warps
 
-  struct Rows {
-    const uint8_t* w[4];
-  };
-  __device__ __forceinline__ Rows weight_rows(int q, int tid) const {
-    const int slot = q / tiles, tile = q - slot * tiles;
-    const int64_t rows = static_cast<int64_t>(expert(slot)) * (UP ? 2 * a.I : a.H);
-    Rows r;
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      r.w[i] = (UP ? a.w13 : a.w2) + (rows + weight_row(tile, i * 32 + tid / 8)) * kd * kEb + tid % 8 * 16;
-    return r;
-  }
-  __device__ __forceinline__ void copy_weights(const Rows& r, int kb, uint32_t to, int tid) const {
-    const bool in = kb * 128 + tid % 8 * 16 < kd * kEb;
-    const int row = tid / 8;
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      copy16_stream(to + (FP8 ? i * 4096 + tid * 16
-                              : (i * 32 + row) * 128 + ((tid % 8 ^ (row & 7)) << 4)),
-                    r.w[i] + static_cast<int64_t>(kb) * 128, in);
+  // Asks for 128 bytes (column block kb) of the 128 weight rows of job q: up,
+  // for each quarter 16 gate rows and 16 up rows.  Behind the last output and
+  // the last column zeros arrive.
+  __device__ __forceinline__ void send_weights(State& s, int q, int kb, int tid) const {
+    const int part = tid / 32;
+    if (tid % 32 == 0 && part < kParts) {
+      const int slot = q / tiles, tile = q - slot * tiles;
+      uint64_t* bar = &b.landed[s.sent.slot];
+      mbar_arrive_expect_tx(bar, kWeightBytes / kParts);
+      tma_load_3d(stage(s.sent.slot) + part * (kWeightBytes / kParts), map, kb * (128 / kEb),
+                  (tile * kParts + part) * (UP ? 16 : 32), expert(slot) * (UP ? 2 : 1), bar);
+    }
+    s.sent.step(ring);
+    ++s.issued;
   }
   // Before the tokens are there: the weights of the first stages.
-  __device__ __forceinline__ int copy_ahead(const State& s, int tid) const {
+  __device__ __forceinline__ int send_ahead(State& s, int tid) const {
     const int q = blockIdx.x;
     if (q >= nq) return 0;
-    const Rows r = weight_rows(q, tid);
     const int n = min(depth, stages);
-    Place p = s.fill;
-    for (int kb = 0; kb < n; ++kb, p.step(ring)) copy_weights(r, kb, stage(p.slot), tid);
+    for (int kb = 0; kb < n; ++kb) send_weights(s, q, kb, tid);
     return n;
+  }
+  // After a wait that gave up: the weights on their way have landed.
+  __device__ __forceinline__ void drain(const State& s, int tid) const {
+    if (tid % 32 != 0 || tid / 32 >= kParts) return;
+    for (int i = max(s.issued - ring, 0); i < s.issued; ++i)
+      wait_phase(&b.landed[i % ring], (i / ring) & 1u, MOE_DEFAULT_WAIT_LIMIT_NS);
   }
 
   // The oldest stage that was copied is complete: e4m3 weights to fp16, and the
@@ -229,6 +242,7 @@ struct ManyPhase {
     bool ok = true;
     if (FP8) {
       ok = warp_wait(&b.a16_empty[s.a16.slot], s.a16.parity ^ 1u);
+      ok = warp_wait(&b.landed[s.ready.slot], s.ready.parity) && ok;
       const int row = tid / 8, c = tid % 8;
       const uint32_t from = stage(s.ready.slot) + tid * 16;
       const uint32_t to = a16 + s.a16.slot * kA16Bytes + (c >> 2) * (kTileRows * 128) + row * 128;
@@ -266,7 +280,6 @@ struct ManyPhase {
     while (q >= 0) {
       int ticket = 0;
       if (tid == 0) ticket = static_cast<int>(atomicAdd(given, 1u));
-      const Rows rows = weight_rows(q, tid);
       const int p = g.slot_expert[q / tiles];
       const uint8_t* src = UP ? (FP8 ? reinterpret_cast<const uint8_t*>(a.x16) : a.x) : a.a;
       for (int c0 = 0; c0 < g.cnt[p] && ok; c0 += kMaxN) {
@@ -290,7 +303,7 @@ struct ManyPhase {
           if (!ok) break;
           const uint32_t at = stage(s.fill.slot);
           if (ahead > 0) --ahead;
-          else copy_weights(rows, kb, at, tid);
+          else send_weights(s, q, kb, tid);
           const bool in = kb * (kAcross * 16) + unit * 16 < kd * 2;
           const uint8_t* tokens = src + kb * (kAcross * 16);
 #pragma unroll
@@ -325,8 +338,11 @@ struct ManyPhase {
     // a stage of nothing carries the end (jobs: -1)
     if (ok) ok = warp_wait(&b.empty[s.fill.slot], s.fill.parity ^ 1u);
     if ((tid & 31) == 0) mbar_arrive(&b.full[s.fill.slot]);
+    if (ok && tid % 32 == 0 && tid / 32 < kParts) mbar_arrive(&b.landed[s.fill.slot]);
     s.fill.step(ring);
     s.ready.step(ring);
+    s.sent.step(ring);
+    ++s.issued;
     ++s.job;
     return ok;
   }
@@ -346,6 +362,7 @@ struct ManyPhase {
         const uint32_t idesc = kFormat | (static_cast<uint32_t>(n >> 3) << 17);
         for (int kb = 0; kb < stages; ++kb) {
           if (!wait_phase(&b.full[s.ready.slot], s.ready.parity, a.wait_ns)) return false;
+          if (!FP8 && !wait_phase(&b.landed[s.ready.slot], s.ready.parity, a.wait_ns)) return false;
           if ((FP8 || kb == 0) && !wait_phase(&b.acc_empty[s.acc.slot], s.acc.parity ^ 1u, a.wait_ns))
             return false;
           tc_fence_after();
@@ -517,40 +534,44 @@ struct ManyPhase {
 
 template <bool FP8>
 __device__ __forceinline__ bool layer_body(const LayerArgs& a, const Groups& g, Barriers& b,
+                                           const CUtensorMap* w13, const CUtensorMap* w2,
                                            uint32_t queue, uint32_t tmem, int* ok) {
   const int tid = static_cast<int>(threadIdx.x) - kFirstCopyWarp * 32;
   uint32_t* arrived = a.arrived;  // of the next barrier
   State s;
-  {
-    const ManyPhase<FP8, true> up(a, g, b, queue);
-    int ahead = 0;
-    if (FP8) {
-      if (tid >= 0) ahead = up.copy_ahead(s, tid);
-      if (!grid_wait(a, arrived++, ok)) return false;
-    }
-    if (!up.run(s, ahead, tmem)) return false;
+  const ManyPhase<FP8, true> up(a, g, b, w13, queue);
+  const ManyPhase<FP8, false> down(a, g, b, w2, queue);
+  int ahead = 0;
+  bool done = true;
+  if (FP8) {
+    if (tid >= 0) ahead = up.send_ahead(s, tid);
+    done = grid_wait(a, arrived++, ok);
   }
-  grid_arrive(arrived);
-  {
-    const ManyPhase<FP8, false> down(a, g, b, queue);
-    int ahead = 0;
-    if (tid >= 0) ahead = down.copy_ahead(s, tid);
-    if (!grid_wait(a, arrived++, ok)) return false;
-    if (FP8) {
-      scale_activations<kThreads>(a, g);
-      grid_arrive(arrived);
-      if (!grid_wait(a, arrived++, ok)) return false;
-    }
-    if (!down.run(s, ahead, tmem)) return false;
+  done = done && up.run(s, ahead, tmem);
+  if (done) {
+    grid_arrive(arrived);
+    ahead = tid >= 0 ? down.send_ahead(s, tid) : 0;
+    done = grid_wait(a, arrived++, ok);
   }
-  grid_arrive(arrived);
-  if (!grid_wait(a, arrived, ok)) return false;
-  sum_entries<kThreads>(a, g);
-  return true;
+  if (FP8 && done) {
+    scale_activations<kThreads>(a, g);
+    grid_arrive(arrived);
+    done = grid_wait(a, arrived++, ok);
+  }
+  done = done && down.run(s, ahead, tmem);
+  if (done) {
+    grid_arrive(arrived);
+    if (grid_wait(a, arrived, ok)) sum_entries<kThreads>(a, g);
+    return true;
+  }
+  copies_wait<0>();
+  if (tid >= 0) down.drain(s, tid);
+  return false;
 }
 
 template <bool FP8>
-__global__ void __launch_bounds__(kThreads, 1) layer_many_kernel(LayerArgs a) {
+__global__ void __launch_bounds__(kThreads, 1) layer_many_kernel(
+    const __grid_constant__ CUtensorMap w13, const __grid_constant__ CUtensorMap w2, LayerArgs a) {
   constexpr uint32_t kColumns = 2 * ManyPhase<FP8, true>::kMaxN;
   extern __shared__ __align__(16) uint8_t raw[];
   __shared__ int ok;
@@ -563,6 +584,7 @@ __global__ void __launch_bounds__(kThreads, 1) layer_many_kernel(LayerArgs a) {
   group_entries<kThreads>(a, g, smem + kQueueBytes + kBarrierBytes);
   if (threadIdx.x == 0) {
     for (int i = 0; i < kMaxRing; ++i) {
+      mbar_init(&b.landed[i], kParts);
       mbar_init(&b.full[i], kCopyWarps);
       mbar_init(&b.empty[i], 1);
     }
@@ -590,8 +612,7 @@ __global__ void __launch_bounds__(kThreads, 1) layer_many_kernel(LayerArgs a) {
   }
   __syncthreads();
   const uint32_t tmem = b.tmem;
-  if (!layer_body<FP8>(a, g, b, smem_addr(smem), tmem, &ok)) {
-    copies_wait<0>();
+  if (!layer_body<FP8>(a, g, b, &w13, &w2, smem_addr(smem), tmem, &ok)) {
     if (threadIdx.x == kMmaWarp * 32) {
       mma_commit(&b.drained);
       wait_phase(&b.drained, 0, MOE_DEFAULT_WAIT_LIMIT_NS);
@@ -604,14 +625,36 @@ __global__ void __launch_bounds__(kThreads, 1) layer_many_kernel(LayerArgs a) {
                  : "memory");
 }
 
+// Weights as [matrices, rows, cols], boxes of 128 bytes of `box_rows` rows of
+// `box_mats` matrices; bf16 swizzled as the products read them.
+bool encode_weights(CUtensorMap* m, const void* base, bool e4m3, uint64_t cols, uint64_t rows,
+                    uint64_t mats, uint32_t box_rows, uint32_t box_mats) {
+  EncodeTiled fn = encode_fn();
+  if (!fn) return false;
+  const uint64_t eb = e4m3 ? 1 : 2;
+  const cuuint64_t dims[3] = {cols, rows, mats};
+  const cuuint64_t strides[2] = {cols * eb, rows * cols * eb};
+  const cuuint32_t box[3] = {static_cast<cuuint32_t>(128 / eb), box_rows, box_mats};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  return fn(m, e4m3 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
+            const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            e4m3 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 template <bool FP8>
 cudaError_t launch_one(const moe_handle* h, const LayerArgs& a, cudaStream_t s) {
+  CUtensorMap w13, w2;
+  const uint64_t n = a.E + a.S;
+  if (!encode_weights(&w13, a.w13, FP8, a.H, a.I, 2 * n, 16, 2) ||
+      !encode_weights(&w2, a.w2, FP8, a.I, a.H, n, 32, 1))
+    return cudaErrorInvalidValue;
   auto k = layer_many_kernel<FP8>;
   const size_t smem = kFixedBytes + groups_bytes(a.T, a.K + a.S, a.E + a.S);
   const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                              static_cast<int>(smem));
   if (e != cudaSuccess) return e;
-  return launch_chained(k, dim3(h->num_sms), dim3(kThreads), smem, s, true, a);
+  return launch_chained(k, dim3(h->num_sms), dim3(kThreads), smem, s, true, w13, w2, a);
 }
 
 }  // namespace
