@@ -598,6 +598,32 @@ struct Phase {
   }
 };
 
+// fp16 copies of x and their factors: a block per token.
+template <int kThreads>
+__device__ __forceinline__ void scale_tokens(const LayerArgs& a, int tokens, uint32_t* red) {
+  for (int t = blockIdx.x; t < tokens; t += gridDim.x) {
+    const uint8_t* row = a.x + static_cast<int64_t>(t) * a.H * 2;
+    const float f = f16_factor(block_max_bits<kThreads>(row, a.H, red));
+    uint8_t* dst = reinterpret_cast<uint8_t*>(a.x16) + static_cast<int64_t>(t) * a.H * 2;
+    for (int v = threadIdx.x; v < a.H / 8; v += kThreads)
+      st_vec(dst + v * 16, scaled_f16(ld_vec(row + v * 16), f));
+    if (threadIdx.x == 0) a.xscale[t] = 1.0f / f;
+    for (int k = threadIdx.x; k < a.K + a.S; k += kThreads) a.amax[t * (a.K + a.S) + k] = 0;
+  }
+}
+
+// fp16 copies of the activations, their factors from the entries' maxima.
+template <int kThreads>
+__device__ __forceinline__ void scale_activations(const LayerArgs& a, const Groups& g) {
+  const int per = a.I / 8;
+  const int64_t n = static_cast<int64_t>(g.tokens) * (a.K + a.S) * per;
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x; i < n;
+       i += static_cast<int64_t>(gridDim.x) * kThreads) {
+    const int entry = static_cast<int>(i / per);
+    if (g.rank[entry] != kNone) scale_activation(a, i, __ldcg(a.amax + entry));
+  }
+}
+
 template <typename S>
 __global__ void __launch_bounds__(S::kThreads, 1) layer_kernel(LayerArgs a) {
   constexpr int kThreads = S::kThreads;
@@ -606,7 +632,7 @@ __global__ void __launch_bounds__(S::kThreads, 1) layer_kernel(LayerArgs a) {
   grid_dependency_wait();
   float* red = reinterpret_cast<float*>(smem + S::kQueueBytes);
   Groups g;
-  group_entries<kThreads>(a, g, smem + S::kFixedBytes);
+  group_entries<kThreads, false>(a, g, smem + S::kFixedBytes, nullptr);
   const int KS = a.K + a.S;
   uint32_t* arrived = a.arrived;  // of the next barrier
   if (S::FP8) {

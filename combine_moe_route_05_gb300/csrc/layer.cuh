@@ -78,8 +78,12 @@ __device__ __forceinline__ int expert_of(const LayerArgs& a, int entry) {
   return static_cast<unsigned>(e) < static_cast<unsigned>(a.E) ? e + a.S : e == -1 ? -1 : -2;
 }
 
-template <int kThreads>
-__device__ __forceinline__ void group_entries(const LayerArgs& a, Groups& g, uint8_t* smem) {
+// The tables, in `smem`.  With `masks` (4 words of scratch an expert) the
+// entries of an expert come in the order of their tokens, so that all blocks
+// agree on it.
+template <int kThreads, bool kOrdered>
+__device__ __forceinline__ void group_entries(const LayerArgs& a, Groups& g, uint8_t* smem,
+                                              uint32_t* masks) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int n_exp = a.E + a.S, KS = a.K + a.S;
   g.order = reinterpret_cast<uint16_t*>(smem);
@@ -131,7 +135,11 @@ __device__ __forceinline__ void group_entries(const LayerArgs& a, Groups& g, uin
     g.nslots = g.head[kMaxWarps];
     return;
   }
-  for (int e = tid; e < n_exp; e += kThreads) g.cnt[e] = 0;
+  if (kOrdered) {
+    for (int i = tid; i < 4 * n_exp; i += kThreads) masks[i] = 0;
+  } else {
+    for (int e = tid; e < n_exp; e += kThreads) g.cnt[e] = 0;
+  }
   g.tokens = a.live ? min(max(__ldcg(a.live), 0), a.T) : a.T;
   const int n = g.tokens * KS;
   // an entry's expert, checked, in `order` until the entries are placed
@@ -152,7 +160,13 @@ __device__ __forceinline__ void group_entries(const LayerArgs& a, Groups& g, uin
         if (blockIdx.x == 0) raise_flag(a.flags, MOE_DEVERR_DUP_EXPERT);
       }
     }
-    g.rank[i] = ok ? static_cast<uint16_t>(atomicAdd(&g.cnt[e], 1)) : kNone;
+    if (kOrdered) {
+      const int t = i / KS;
+      if (ok) atomicOr(&masks[4 * e + t / 32], 1u << (t % 32));
+      g.rank[i] = ok ? 0 : kNone;
+    } else {
+      g.rank[i] = ok ? static_cast<uint16_t>(atomicAdd(&g.cnt[e], 1)) : kNone;
+    }
   }
   __syncthreads();
   // exclusive scan of counts (low 16 bits) and of experts with entries (high)
@@ -161,7 +175,15 @@ __device__ __forceinline__ void group_entries(const LayerArgs& a, Groups& g, uin
 #pragma unroll
   for (int j = 0; j < kPer; ++j) {
     const int e = tid * kPer + j;
-    const int c = e < n_exp ? g.cnt[e] : 0;
+    int c = 0;
+    if (e < n_exp) {
+      if (kOrdered) {
+        for (int i = 0; i < 4; ++i) c += __popc(masks[4 * e + i]);
+        g.cnt[e] = c;
+      } else {
+        c = g.cnt[e];
+      }
+    }
     own[j] = sum;
     sum += c + (c ? 0x10000 : 0);
   }
@@ -195,7 +217,16 @@ __device__ __forceinline__ void group_entries(const LayerArgs& a, Groups& g, uin
 #pragma unroll
   for (int j = 0; j < kMine; ++j) {
     const int i = tid + j * kThreads;
-    if (i < n && g.rank[i] != kNone) g.order[g.start[mine[j]] + g.rank[i]] = static_cast<uint16_t>(i);
+    if (i < n && g.rank[i] != kNone) {
+      if (kOrdered) {
+        const uint32_t* mask = masks + 4 * mine[j];
+        const int t = i / KS;
+        int rank = __popc(mask[t / 32] & ((1u << (t % 32)) - 1u));
+        for (int w = 0; w < t / 32; ++w) rank += __popc(mask[w]);
+        g.rank[i] = static_cast<uint16_t>(rank);
+      }
+      g.order[g.start[mine[j]] + g.rank[i]] = static_cast<uint16_t>(i);
+    }
   }
   g.nslots = g.head[kMaxWarps];
   __syncthreads();
@@ -287,55 +318,44 @@ __device__ __forceinline__ float act_value(float g, int act) {
   return c < -80.0f ? g * 0.0f : g * __fdividef(1.0f, 1.0f + __expf(-c));
 }
 
-// fp16 copies of x and their factors: a block per token.
+// The largest magnitude of a row of n bf16 values, as the bits of a float;
+// `red` holds a word a warp.  All threads of the block.
 template <int kThreads>
-__device__ __forceinline__ void scale_tokens(const LayerArgs& a, int tokens, uint32_t* red) {
-  for (int t = blockIdx.x; t < tokens; t += gridDim.x) {
-    const uint8_t* row = a.x + static_cast<int64_t>(t) * a.H * 2;
-    uint32_t m = 0;  // the largest |x|, as bits of a bf16 in the high half
-    for (int v = threadIdx.x; v < a.H / 8; v += kThreads) {
-      const Vec16 x = ld_vec(row + v * 16);
+__device__ __forceinline__ uint32_t block_max_bits(const uint8_t* row, int n, uint32_t* red) {
+  uint32_t m = 0;  // of a bf16 in the high half
+  for (int v = threadIdx.x; v < n / 8; v += kThreads) {
+    const Vec16 x = ld_vec(row + v * 16);
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        m = max(m, max(x.u[i] & 0x7fff0000u, (x.u[i] << 16) & 0x7fff0000u));
-    }
-    m = __reduce_max_sync(kFull, m);
-    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = m;
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < kThreads / 32; ++i) m = max(m, red[i]);
-    __syncthreads();
-    const float f = f16_factor(m);
-    uint8_t* dst = reinterpret_cast<uint8_t*>(a.x16) + static_cast<int64_t>(t) * a.H * 2;
-    for (int v = threadIdx.x; v < a.H / 8; v += kThreads) {
-      float e[8];
-      VecTraits<__nv_bfloat16>::to_f32(ld_vec(row + v * 16), e);
-      Vec16 o;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) o.u[i] = f16x2(e[2 * i] * f, e[2 * i + 1] * f);
-      st_vec(dst + v * 16, o);
-    }
-    if (threadIdx.x == 0) a.xscale[t] = 1.0f / f;
-    for (int k = threadIdx.x; k < a.K + a.S; k += kThreads) a.amax[t * (a.K + a.S) + k] = 0;
+    for (int i = 0; i < 4; ++i)
+      m = max(m, max(x.u[i] & 0x7fff0000u, (x.u[i] << 16) & 0x7fff0000u));
   }
+  m = __reduce_max_sync(kFull, m);
+  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = m;
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < kThreads / 32; ++i) m = max(m, red[i]);
+  __syncthreads();
+  return m;
 }
 
-// fp16 copies of the activations, their factors from the entries' maxima.
-template <int kThreads>
-__device__ __forceinline__ void scale_activations(const LayerArgs& a, const Groups& g) {
-  const int per = a.I / 8;
-  const int64_t n = static_cast<int64_t>(g.tokens) * (a.K + a.S) * per;
-  for (int64_t i = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x; i < n;
-       i += static_cast<int64_t>(gridDim.x) * kThreads) {
-    const int entry = static_cast<int>(i / per);
-    if (g.rank[entry] == kNone) continue;
-    const float f = f16_factor(__ldcg(a.amax + entry));
-    const float4* src = reinterpret_cast<const float4*>(a.a32) + 2 * i;
-    const float4 lo = __ldcg(src), hi = __ldcg(src + 1);
-    const Vec16 o{f16x2(lo.x * f, lo.y * f), f16x2(lo.z * f, lo.w * f), f16x2(hi.x * f, hi.y * f),
-                  f16x2(hi.z * f, hi.w * f)};
-    st_vec(a.a + i * 16, o);
-  }
+// 8 bf16 values times f, in fp16.
+__device__ __forceinline__ Vec16 scaled_f16(const Vec16& x, float f) {
+  float e[8];
+  VecTraits<__nv_bfloat16>::to_f32(x, e);
+  Vec16 o;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) o.u[i] = f16x2(e[2 * i] * f, e[2 * i + 1] * f);
+  return o;
+}
+
+// Vector i (8 values) of the fp16 activations, of an entry whose largest one
+// has the bits `max_bits`.
+__device__ __forceinline__ void scale_activation(const LayerArgs& a, int64_t i, uint32_t max_bits) {
+  const float f = f16_factor(max_bits);
+  const float4* src = reinterpret_cast<const float4*>(a.a32) + 2 * i;
+  const float4 lo = __ldcg(src), hi = __ldcg(src + 1);
+  st_vec(a.a + i * 16, Vec16{f16x2(lo.x * f, lo.y * f), f16x2(lo.z * f, lo.w * f),
+                             f16x2(hi.x * f, hi.y * f), f16x2(hi.z * f, hi.w * f)});
 }
 
 // The entries' rows summed per token, a thread per 4 columns.

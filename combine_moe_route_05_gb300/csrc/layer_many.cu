@@ -5,23 +5,25 @@
 // weights, but mma.sync no longer keeps up: each warp has to load every token's
 // operand for the few weight rows it holds.  Here 128 weight rows are the A
 // operand of tcgen05.mma and an expert's tokens (16 to 128 columns) the B
-// operand, both read from shared memory by the tensor core itself, so that a
-// stage of the queue costs its copies and nothing else.
+// operand, both read from shared memory by the tensor core itself.
 //
 //   warps 0..3   epilogue: a thread per weight row (tensor-memory lane)
 //   warp  4      issues the products
-//   warps 8..15  fill the queue: weights by tensor copies (four threads, 32
-//                rows each), tokens row by row, since they are gathered
+//   warp  5      fills the queue: tensor copies of weights and tokens
+//   warps 8..15  e4m3: turn the weights that have landed into fp16 (exact)
 //
-// Up tiles hold 64 outputs: in each warp's quarter of the 128 rows 16 gate rows
-// and the 16 up rows of the same outputs, so that the epilogue pairs gate and
-// up with one exchange between lanes n and n + 16.
+// For the tensor copies the tokens lie in the order of the experts: a first
+// pass copies x so, and the up products store a so.  That pass and its grid
+// barrier run while the first weights are on their way.
+//
+// Up tiles hold 64 outputs: 8 gate rows and the 8 up rows of the same outputs
+// in turn, so that the epilogue pairs gate and up with one exchange between
+// lanes n and n + 8.
 //
 // bf16: x as it is; a as the sum of two bf16 numbers, the low parts as further
-// products into the same accumulator.  e4m3: a copying thread turns the 16
-// weights it copied into fp16 (exact) on their way from the queue to the A
-// operand; the block scale of a row and 128 columns multiplies the products of
-// these columns, which the epilogue adds up in registers.
+// products into the same accumulator.  e4m3: x and a in fp16, scaled; the block
+// scale of a row and 128 columns multiplies the products of these columns,
+// which the epilogue adds up in registers.
 //
 // Jobs (an expert and a tile) are handed out by a counter; every wait is
 // bounded, and a wait that gives up ends the call with the status bit set.
@@ -32,35 +34,41 @@ namespace moe {
 namespace {
 
 constexpr int kThreads = 512;
-constexpr int kEpilogueWarps = 4, kMmaWarp = 4, kFirstCopyWarp = 8, kCopyWarps = 8;
-constexpr int kCopyThreads = 32 * kCopyWarps;
-static_assert((kFirstCopyWarp + kCopyWarps) * 32 == kThreads, "roles");
+constexpr int kEpilogueWarps = 4, kMmaWarp = 4, kLoadWarp = 5;
+constexpr int kFirstConvertWarp = 8, kConvertWarps = 8;
+static_assert((kFirstConvertWarp + kConvertWarps) * 32 == kThreads, "roles");
 constexpr int kTileRows = 128;
-constexpr int kParts = 4;        // tensor copies of a stage's weights
 constexpr uint32_t kWeightBytes = kTileRows * 128;  // of a stage: 128 bytes of each row
-constexpr int kJobRing = 32;     // jobs on their way from the copying warps to the others
+constexpr int kBoxTokens = 16;                      // of a tensor copy
+constexpr uint32_t kBoxBytes = kBoxTokens * 128;
+constexpr int kJobRing = 32;     // jobs on their way from the loading thread to the others
 constexpr int kMaxRing = 10;     // stages of the queue
 constexpr size_t kQueueBytes = 208 * 1024;
 constexpr uint32_t kA16Bytes = 2 * kTileRows * 128;  // 128 columns in fp16
 constexpr size_t kBarrierBytes = 512;
 constexpr size_t kFixedBytes = 1024 /* alignment */ + kQueueBytes + kBarrierBytes;
 static_assert(kFixedBytes + groups_bytes(MOE_LAYER_MAX_TOKENS, MOE_MAX_TOPK + MOE_LAYER_MAX_SHARED,
-                                         kMaxExperts) + 64 <= 227 * 1024, "shared memory budget");
+                                         kMaxExperts) + 256 <= 227 * 1024, "shared memory budget");
 
 struct Barriers {
-  uint64_t landed[kMaxRing];  // a stage's weights are there
-  uint64_t full[kMaxRing];   // its tokens, too (an arrival per copying warp); e4m3: and
-                             // its fp16 weights
-  uint64_t empty[kMaxRing];  // its products are done
-  uint64_t a16_empty[2];     // e4m3: the products of an fp16 slice are done
-  uint64_t acc_full[2];      // an accumulator is complete (the commit, and the issuing thread)
-  uint64_t acc_empty[2];     // and read (an arrival per epilogue warp)
-  uint64_t drained;          // after a wait that gave up: no product is under way
+  uint64_t landed[kMaxRing];  // a stage is there
+  uint64_t empty[kMaxRing];   // its products are done
+  uint64_t a16_full[2];       // e4m3: an fp16 slice is there (an arrival per converting warp)
+  uint64_t a16_empty[2];      // and its products are done
+  uint64_t acc_full[2];       // an accumulator is complete (the commit, and the issuing thread)
+  uint64_t acc_empty[2];      // and read (an arrival per epilogue warp)
+  uint64_t drained;           // after a wait that gave up: no product is under way
   int32_t jobs[kJobRing];
   uint32_t tmem;
-  int32_t max_tokens;        // of one expert
+  int32_t max_tokens;         // of one expert
+  int32_t rows;               // entries in all
 };
 static_assert(sizeof(Barriers) <= kBarrierBytes, "barriers");
+
+// The call's tensor maps.
+struct Maps {
+  CUtensorMap w13, w2, x, a;
+};
 
 __device__ __forceinline__ void mma_f16(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
                                         bool accumulate) {
@@ -97,33 +105,24 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map
       "l"(map), "r"(x), "r"(y), "r"(z), "r"(smem_addr(bar))
       : "memory");
 }
-
-// All but the last `pending` groups of copies have landed.
-__device__ __forceinline__ void copies_wait_for(int pending) {
-  switch (pending) {
-    case 1: copies_wait<1>(); break;
-    case 2: copies_wait<2>(); break;
-    case 3: copies_wait<3>(); break;
-    case 4: copies_wait<4>(); break;
-    case 5: copies_wait<5>(); break;
-    case 6: copies_wait<6>(); break;
-    case 7: copies_wait<7>(); break;
-    case 8: copies_wait<8>(); break;
-    default: copies_wait<0>(); break;
-  }
-}
-
-// The copying warps' barrier, with the AND of `p` over them.
-__device__ __forceinline__ bool copy_warps_and(bool p) {
-  uint32_t r;
+__device__ __forceinline__ void tma_load_5d(uint32_t dst, const CUtensorMap* map, int x, int y,
+                                            int z, int u, int v, uint64_t* bar) {
   asm volatile(
-      "{\n\t.reg .pred pi, po;\n\tsetp.ne.u32 pi, %1, 0;\n\t"
-      "bar.red.and.pred po, 1, %2, pi;\n\tselp.u32 %0, 1, 0, po;\n\t}"
-      : "=r"(r)
-      : "r"(static_cast<uint32_t>(p)), "n"(kCopyThreads)
+      "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+      "[%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(dst),
+      "l"(map), "r"(x), "r"(y), "r"(z), "r"(u), "r"(v), "r"(smem_addr(bar))
       : "memory");
-  return r != 0;
 }
+
+// Bytes that the barrier's phase waits for, without an arrival.
+__device__ __forceinline__ void mbar_expect_tx(uint64_t* bar, uint32_t bytes) {
+  asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(smem_addr(bar)),
+               "r"(bytes)
+               : "memory");
+}
+
+// What this thread wrote to or knows of in global memory, for tensor copies.
+__device__ __forceinline__ void fence_copies() { asm volatile("fence.proxy.async;" ::: "memory"); }
 
 // A place in a ring of n slots and the parity of its use.
 struct Place {
@@ -137,14 +136,13 @@ struct Place {
   }
 };
 
-// Where each role stands in the queue and the accumulators: both run on from
-// the up to the down products.
+// Where each role stands in the rings: all run on from the up to the down
+// products.
 struct State {
-  Place sent{0, 0};   // copying: the next stage whose weights are asked for
-  int issued = 0;     // stages asked for
-  Place fill{0, 0};   // copying: the next stage
-  int landing = 0;    // copying: stages that are copied, not yet announced
-  Place ready{0, 0};  // copying: the next to be announced; products: the next to be read
+  Place fill{0, 0};  // loading: the next stage
+  Place sent{0, 0};  // the next one whose weights are asked for
+  int issued = 0;    // stages asked for
+  Place read{0, 0};  // converting, products: the next stage to be read
   Place a16{0, 0};
   Place acc{0, 0};
   int job = 0;
@@ -156,20 +154,23 @@ struct ManyPhase {
   static constexpr int kTileOutputs = UP ? 64 : 128;
   static constexpr int kMaxN = FP8 ? 64 : 128;  // tokens of one pass over the weights
   static constexpr bool kLow = !UP && !FP8;     // a's low parts follow
+  static constexpr int kSlices = FP8 || kLow ? 2 : 1;  // of 128 bytes of a token's row in a stage
 
   const LayerArgs& a;
   const Groups& g;
   Barriers& b;
-  const CUtensorMap* map;
+  const CUtensorMap* weights;
+  const CUtensorMap* tokens;
   uint32_t queue, a16;
-  int ring, depth;        // stages, and how many of them are in flight
+  int ring;               // stages
   uint32_t stage_bytes;
   int kd, limit, tiles, stages, nq;
   uint32_t* given;
 
   __device__ __forceinline__ ManyPhase(const LayerArgs& args, const Groups& groups, Barriers& bars,
-                                       const CUtensorMap* weights, uint32_t smem)
-      : a(args), g(groups), b(bars), map(weights), queue(smem) {
+                                       const Maps& maps, uint32_t smem)
+      : a(args), g(groups), b(bars), weights(UP ? &maps.w13 : &maps.w2),
+        tokens(UP ? &maps.x : &maps.a), queue(smem) {
     kd = UP ? a.H : a.I;
     limit = UP ? a.I : a.H;
     tiles = (limit + kTileOutputs - 1) / kTileOutputs;
@@ -181,7 +182,6 @@ struct ManyPhase {
     stage_bytes = kWeightBytes + n * 256;
     const int room = static_cast<int>(kQueueBytes - (FP8 ? 2 * kA16Bytes : 0));
     ring = min(room / static_cast<int>(stage_bytes), kMaxRing);
-    depth = ring - 2;
     a16 = queue + static_cast<uint32_t>(kQueueBytes) - 2 * kA16Bytes;
   }
 
@@ -195,8 +195,7 @@ struct ManyPhase {
   // output the last one's again.
   __device__ __forceinline__ int weight_row(int tile, int r) const {
     if (!UP) return min(tile * 128 + r, limit - 1);
-    const int l = r & 31;
-    return min(tile * 64 + (r >> 5) * 16 + (l & 15), limit - 1) + (l < 16 ? 0 : a.I);
+    return min(tile * 64 + (r >> 4) * 8 + (r & 7), limit - 1) + (r & 8 ? a.I : 0);
   }
 
   // Every lane waits, and all leave together.
@@ -204,147 +203,118 @@ struct ManyPhase {
     return __all_sync(kFull, wait_phase(bar, parity, a.wait_ns));
   }
 
-  // -- copying warps
+  // -- the loading thread
 
-  // Asks for 128 bytes (column block kb) of the 128 weight rows of job q: up,
-  // for each quarter 16 gate rows and 16 up rows.  Behind the last output and
-  // the last column zeros arrive.
-  __device__ __forceinline__ void send_weights(State& s, int q, int kb, int tid) const {
-    const int part = tid / 32;
-    if (tid % 32 == 0 && part < kParts) {
-      const int slot = q / tiles, tile = q - slot * tiles;
-      uint64_t* bar = &b.landed[s.sent.slot];
-      mbar_arrive_expect_tx(bar, kWeightBytes / kParts);
-      tma_load_3d(stage(s.sent.slot) + part * (kWeightBytes / kParts), map, kb * (128 / kEb),
-                  (tile * kParts + part) * (UP ? 16 : 32), expert(slot) * (UP ? 2 : 1), bar);
-    }
+  // Asks for 128 bytes (column block kb) of the 128 weight rows of job q.
+  // Behind the last output and the last column zeros arrive.
+  __device__ __forceinline__ void send_weights(State& s, int q, int kb) const {
+    const int slot = q / tiles, tile = q - slot * tiles;
+    uint64_t* bar = &b.landed[s.sent.slot];
+    const uint32_t to = stage(s.sent.slot);
+    mbar_expect_tx(bar, kWeightBytes);
+    if (UP) tma_load_5d(to, weights, kb * (128 / kEb), 0, 0, tile * 8, expert(slot), bar);
+    else tma_load_3d(to, weights, kb * (128 / kEb), tile * 128, expert(slot), bar);
     s.sent.step(ring);
     ++s.issued;
   }
   // Before the tokens are there: the weights of the first stages.
-  __device__ __forceinline__ int send_ahead(State& s, int tid) const {
+  __device__ __forceinline__ int send_ahead(State& s) const {
     const int q = blockIdx.x;
     if (q >= nq) return 0;
-    const int n = min(depth, stages);
-    for (int kb = 0; kb < n; ++kb) send_weights(s, q, kb, tid);
+    const int n = min(ring, stages);
+    for (int kb = 0; kb < n; ++kb) send_weights(s, q, kb);
     return n;
   }
-  // After a wait that gave up: the weights on their way have landed.
-  __device__ __forceinline__ void drain(const State& s, int tid) const {
-    if (tid % 32 != 0 || tid / 32 >= kParts) return;
+  // After a wait that gave up: what is on its way has landed.
+  __device__ __forceinline__ void drain(State& s, int ahead) const {
+    for (; ahead > 0; --ahead, s.fill.step(ring)) mbar_arrive(&b.landed[s.fill.slot]);
     for (int i = max(s.issued - ring, 0); i < s.issued; ++i)
       wait_phase(&b.landed[i % ring], (i / ring) & 1u, MOE_DEFAULT_WAIT_LIMIT_NS);
   }
 
-  // The oldest stage that was copied is complete: e4m3 weights to fp16, and the
-  // news to the issuing warp.
-  __device__ __forceinline__ bool announce(State& s, int tid) const {
-    bool ok = true;
-    if (FP8) {
-      ok = warp_wait(&b.a16_empty[s.a16.slot], s.a16.parity ^ 1u);
-      ok = warp_wait(&b.landed[s.ready.slot], s.ready.parity) && ok;
-      const int row = tid / 8, c = tid % 8;
-      const uint32_t from = stage(s.ready.slot) + tid * 16;
-      const uint32_t to = a16 + s.a16.slot * kA16Bytes + (c >> 2) * (kTileRows * 128) + row * 128;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const Vec16 v = lds16(from + i * 4096);
-        uint32_t h[2][4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) f16_of_e4m3(v.u[j], h[j / 2][j % 2 * 2], h[j / 2][j % 2 * 2 + 1]);
-        // lanes of the second half write their units the other way round, so
-        // that the 8 lanes of a row meet 8 different banks
-        const int first = c >> 2;
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const int unit = (c & 3) * 2 + (j ^ first);
-          const uint32_t v4[4] = {first ^ j ? h[1][0] : h[0][0], first ^ j ? h[1][1] : h[0][1],
-                                  first ^ j ? h[1][2] : h[0][2], first ^ j ? h[1][3] : h[0][3]};
-          if (ok) sts16(to + i * 4096 + ((unit ^ (row & 7)) << 4), v4);
-        }
-      }
-      s.a16.step(2);
-    }
-    fence_operands();
-    __syncwarp();
-    if ((tid & 31) == 0) mbar_arrive(&b.full[s.ready.slot]);
-    s.ready.step(ring);
-    --s.landing;
-    return ok;
-  }
-
-  __device__ __forceinline__ bool copy(State& s, int ahead, int tid) const {
-    bool ok = true;
+  __device__ __forceinline__ bool load(State& s, int& ahead) const {
     int q = static_cast<int>(blockIdx.x) < nq ? static_cast<int>(blockIdx.x) : -1;
-    if (tid == 0) b.jobs[s.job % kJobRing] = q;
-    while (q >= 0) {
-      int ticket = 0;
-      if (tid == 0) ticket = static_cast<int>(atomicAdd(given, 1u));
+    for (;; ++s.job) {
+      b.jobs[s.job % kJobRing] = q;
+      if (q < 0) break;
+      const int ticket = static_cast<int>(atomicAdd(given, 1u));
       const int p = g.slot_expert[q / tiles];
-      const uint8_t* src = UP ? (FP8 ? reinterpret_cast<const uint8_t*>(a.x16) : a.x) : a.a;
-      for (int c0 = 0; c0 < g.cnt[p] && ok; c0 += kMaxN) {
-        const int cnt = min(g.cnt[p] - c0, kMaxN), begin = g.start[p] + c0;
-        const int n = columns(cnt);
-        // a row's units of 16 bytes: 8 in bf16, 16 (two slices) in fp16
-        constexpr int kAcross = FP8 ? 16 : 8, kDown = kCopyThreads / kAcross, kMost = kMaxN / kDown;
-        const int unit = tid % kAcross, row = tid / kAcross;
-        uint32_t from[kMost];
-#pragma unroll
-        for (int j = 0; j < kMost; ++j) {
-          const int r = row + j * kDown;
-          const int entry = g.order[begin + min(r, cnt - 1)];
-          from[j] = static_cast<uint32_t>(UP ? entry / (a.K + a.S) : entry) * (kd * 2u) + unit * 16;
-        }
-        const uint32_t to = kWeightBytes + (unit >> 3) * (n * 128) + row * 128 +
-                            (((unit & 7) ^ (row & 7)) << 4);
-        const int64_t low = static_cast<int64_t>(a.T) * (a.K + a.S) * kd * 2;
+      for (int c0 = 0; c0 < g.cnt[p]; c0 += kMaxN) {
+        const int n = columns(min(g.cnt[p] - c0, kMaxN)), row = g.start[p] + c0;
         for (int kb = 0; kb < stages; ++kb) {
-          ok = warp_wait(&b.empty[s.fill.slot], s.fill.parity ^ 1u);
-          if (!ok) break;
-          const uint32_t at = stage(s.fill.slot);
+          if (!wait_phase(&b.empty[s.fill.slot], s.fill.parity ^ 1u, a.wait_ns)) return false;
           if (ahead > 0) --ahead;
-          else send_weights(s, q, kb, tid);
-          const bool in = kb * (kAcross * 16) + unit * 16 < kd * 2;
-          const uint8_t* tokens = src + kb * (kAcross * 16);
+          else send_weights(s, q, kb);
+          uint64_t* bar = &b.landed[s.fill.slot];
+          uint32_t to = stage(s.fill.slot) + kWeightBytes;
+          mbar_arrive_expect_tx(bar, n * (128 * kSlices));
 #pragma unroll
-          for (int j = 0; j < kMost; ++j)
-            if (row + j * kDown < cnt) {
-              copy16_stream(at + to + j * (kDown * 128), tokens + from[j], in);
-              if (kLow) copy16_stream(at + to + n * 128 + j * (kDown * 128), tokens + low + from[j], in);
-            }
-          copies_commit();
-          ++s.landing;
+          for (int i = 0; i < kSlices; ++i)
+            for (int r = 0; r < n; r += kBoxTokens, to += kBoxBytes)
+              tma_load_3d(to, tokens, kb * (FP8 ? 128 : 64) + (FP8 ? i * 64 : 0), row + r,
+                          kLow ? i : 0, bar);
           s.fill.step(ring);
-          if (s.landing > depth) {
-            copies_wait_for(depth);
-            ok = announce(s, tid);
-            if (!ok) break;
-          }
         }
       }
-      ++s.job;
-      if (tid == 0) {
-        const int next = ticket + static_cast<int>(gridDim.x);
-        b.jobs[s.job % kJobRing] = next < nq ? next : -1;
-      }
-      if (!copy_warps_and(ok)) {
-        ok = false;
-        break;
-      }
-      q = b.jobs[s.job % kJobRing];
+      q = ticket + static_cast<int>(gridDim.x);
+      if (q >= nq) q = -1;
     }
-    copies_wait<0>();
-    while (s.landing > 0 && ok) ok = announce(s, tid);
-    // a stage of nothing carries the end (jobs: -1)
-    if (ok) ok = warp_wait(&b.empty[s.fill.slot], s.fill.parity ^ 1u);
-    if ((tid & 31) == 0) mbar_arrive(&b.full[s.fill.slot]);
-    if (ok && tid % 32 == 0 && tid / 32 < kParts) mbar_arrive(&b.landed[s.fill.slot]);
+    // a stage of nothing carries the end
+    if (!wait_phase(&b.empty[s.fill.slot], s.fill.parity ^ 1u, a.wait_ns)) return false;
+    mbar_arrive(&b.landed[s.fill.slot]);
     s.fill.step(ring);
-    s.ready.step(ring);
     s.sent.step(ring);
     ++s.issued;
     ++s.job;
-    return ok;
+    return true;
+  }
+
+  // -- converting warps (e4m3)
+
+  __device__ __forceinline__ bool convert(State& s, int tid) const {
+    const int row = tid / 8, c = tid % 8;
+    for (;; ++s.job) {
+      if (!warp_wait(&b.landed[s.read.slot], s.read.parity)) return false;
+      const int q = b.jobs[s.job % kJobRing];
+      if (q < 0) break;
+      const int p = g.slot_expert[q / tiles];
+      for (int n = (g.cnt[p] + kMaxN - 1) / kMaxN * stages; n > 0; --n) {
+        if (!warp_wait(&b.landed[s.read.slot], s.read.parity) ||
+            !warp_wait(&b.a16_empty[s.a16.slot], s.a16.parity ^ 1u))
+          return false;
+        const uint32_t from = stage(s.read.slot) + tid * 16;
+        const uint32_t to = a16 + s.a16.slot * kA16Bytes + (c >> 2) * (kTileRows * 128) + row * 128;
+        Vec16 v[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = lds16(from + i * 4096);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          uint32_t h[2][4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            f16_of_e4m3(v[i].u[j], h[j / 2][j % 2 * 2], h[j / 2][j % 2 * 2 + 1]);
+          // lanes of the second half write their units the other way round, so
+          // that the 8 lanes of a row meet 8 different banks
+          const bool turn = c >= 4;
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const int unit = (c & 3) * 2 + (turn ? 1 - j : j);
+            uint32_t w[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) w[k] = turn ? h[1 - j][k] : h[j][k];
+            sts16(to + i * 4096 + ((unit ^ (row & 7)) << 4), w);
+          }
+        }
+        fence_operands();
+        __syncwarp();
+        if ((tid & 31) == 0) mbar_arrive(&b.a16_full[s.a16.slot]);
+        s.a16.step(2);
+        s.read.step(ring);
+      }
+    }
+    s.read.step(ring);
+    ++s.job;
+    return true;
   }
 
   // -- the issuing thread
@@ -353,7 +323,7 @@ struct ManyPhase {
     constexpr uint32_t kFormat = (1u << 4) | (FP8 ? 0u : (1u << 7) | (1u << 10)) |
                                  (static_cast<uint32_t>(kTileRows >> 4) << 24);
     for (;; ++s.job) {
-      if (!wait_phase(&b.full[s.ready.slot], s.ready.parity, a.wait_ns)) return false;
+      if (!wait_phase(&b.landed[s.read.slot], s.read.parity, a.wait_ns)) return false;
       const int q = b.jobs[s.job % kJobRing];
       if (q < 0) break;
       const int p = g.slot_expert[q / tiles];
@@ -361,33 +331,30 @@ struct ManyPhase {
         const int n = columns(min(g.cnt[p] - c0, kMaxN));
         const uint32_t idesc = kFormat | (static_cast<uint32_t>(n >> 3) << 17);
         for (int kb = 0; kb < stages; ++kb) {
-          if (!wait_phase(&b.full[s.ready.slot], s.ready.parity, a.wait_ns)) return false;
-          if (!FP8 && !wait_phase(&b.landed[s.ready.slot], s.ready.parity, a.wait_ns)) return false;
+          if (!wait_phase(&b.landed[s.read.slot], s.read.parity, a.wait_ns)) return false;
+          if (FP8 && !wait_phase(&b.a16_full[s.a16.slot], s.a16.parity, a.wait_ns)) return false;
           if ((FP8 || kb == 0) && !wait_phase(&b.acc_empty[s.acc.slot], s.acc.parity ^ 1u, a.wait_ns))
             return false;
           tc_fence_after();
           const uint32_t d = tmem + s.acc.slot * kMaxN;
-          const uint32_t at = stage(s.ready.slot);
-          if (FP8) {
-            const uint32_t w = a16 + s.a16.slot * kA16Bytes;
+          const uint32_t at = stage(s.read.slot);
+          const uint64_t x = sw128_desc(at + kWeightBytes);
+          const uint64_t w = sw128_desc(FP8 ? a16 + s.a16.slot * kA16Bytes : at);
+          // the second slice: e4m3: the other 64 columns; a's low parts: the
+          // same weights again
+          const uint32_t w_next = FP8 ? kTileRows * 128 / 16 : 0;
 #pragma unroll
-            for (int k = 0; k < 8; ++k)
-              mma_f16(d, sw128_desc(w + k / 4 * (kTileRows * 128)) + k % 4 * 2,
-                      sw128_desc(at + kWeightBytes + k / 4 * (n * 128)) + k % 4 * 2, idesc, k > 0);
+          for (int i = 0; i < kSlices; ++i)
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              mma_f16(d, w + i * w_next + k * 2, x + i * (n * 8) + k * 2, idesc,
+                      (!FP8 && kb > 0) || i + k > 0);
+          if (FP8) {
             mma_commit(&b.a16_empty[s.a16.slot]);
             s.a16.step(2);
-          } else {
-            const uint64_t w = sw128_desc(at), x = sw128_desc(at + kWeightBytes);
-#pragma unroll
-            for (int k = 0; k < 4; ++k) mma_f16(d, w + k * 2, x + k * 2, idesc, kb > 0 || k > 0);
-            if (kLow) {
-              const uint64_t lo = sw128_desc(at + kWeightBytes + n * 128);
-#pragma unroll
-              for (int k = 0; k < 4; ++k) mma_f16(d, w + k * 2, lo + k * 2, idesc, true);
-            }
           }
-          mma_commit(&b.empty[s.ready.slot]);
-          s.ready.step(ring);
+          mma_commit(&b.empty[s.read.slot]);
+          s.read.step(ring);
           if (FP8 || kb == stages - 1) {
             mma_commit(&b.acc_full[s.acc.slot]);
             mbar_arrive(&b.acc_full[s.acc.slot]);
@@ -398,10 +365,10 @@ struct ManyPhase {
     }
     // the end: passed on as an accumulator of nothing
     if (!wait_phase(&b.acc_empty[s.acc.slot], s.acc.parity ^ 1u, a.wait_ns)) return false;
-    mma_commit(&b.empty[s.ready.slot]);
+    mma_commit(&b.empty[s.read.slot]);
     mma_commit(&b.acc_full[s.acc.slot]);
     mbar_arrive(&b.acc_full[s.acc.slot]);
-    s.ready.step(ring);
+    s.read.step(ring);
     s.acc.step(2);
     ++s.job;
     return true;
@@ -426,31 +393,32 @@ struct ManyPhase {
                                           int warp, int lane) const {
     const int KS = a.K + a.S;
     if (UP) {
-      const int o = tile * 64 + warp * 16 + (lane & 15);
-      const bool upper = lane >= 16;
+      const int o = tile * 64 + warp * 16 + (lane >> 4) * 8 + (lane & 7);
+      const bool upper = lane & 8;
 #pragma unroll
       for (int j = 0; j < 16; j += 2) {
         if (n0 + j >= cnt) break;  // uniform
-        // lane l takes column j, lane l + 16 column j + 1
-        const float other = __shfl_xor_sync(kFull, upper ? v[j] : v[j + 1], 16);
+        // lane l takes column j, lane l + 8 column j + 1
+        const float other = __shfl_xor_sync(kFull, upper ? v[j] : v[j + 1], 8);
         const float gate = upper ? other : v[j], up = upper ? v[j + 1] : other;
         const int n = n0 + j + (upper ? 1 : 0);
         const bool real = n < cnt && o < limit;
-        const int entry = g.order[begin + min(n, cnt - 1)];
+        const int64_t at = static_cast<int64_t>(begin + min(n, cnt - 1)) * a.I + o;
         if (FP8) {
+          const int entry = g.order[begin + min(n, cnt - 1)];
           const float f = __ldcg(a.xscale + entry / KS);
           const float h = act_value(gate * f, a.act) * (up * f);
-          if (real) a.a32[static_cast<int64_t>(entry) * a.I + o] = h;
+          if (real) a.a32[at] = h;
           const uint32_t m = real ? __float_as_uint(h) & 0x7fffffffu : 0u;
           const uint32_t m0 = __reduce_max_sync(kFull, upper ? 0u : m);
           const uint32_t m1 = __reduce_max_sync(kFull, upper ? m : 0u);
           // a maximum does not depend on the order
-          if ((lane & 15) == 0 && n < cnt) atomicMax(a.amax + entry, upper ? m1 : m0);
+          if ((lane & 23) == 0 && n < cnt) atomicMax(a.amax + entry, upper ? m1 : m0);
         } else if (real) {
           const float h = act_value(gate, a.act) * up;
           const __nv_bfloat16 hi = __float2bfloat16_rn(h);
           const float rest = h - __bfloat162float(hi);
-          __nv_bfloat16* dst = reinterpret_cast<__nv_bfloat16*>(a.a) + static_cast<int64_t>(entry) * a.I + o;
+          __nv_bfloat16* dst = reinterpret_cast<__nv_bfloat16*>(a.a) + at;
           dst[0] = hi;
           dst[static_cast<int64_t>(a.T) * KS * a.I] = __float2bfloat16_rn(isfinite(rest) ? rest : 0.0f);
         }
@@ -520,43 +488,87 @@ struct ManyPhase {
     return true;
   }
 
-  __device__ __forceinline__ bool run(State& s, int ahead, uint32_t tmem) const {
+  __device__ __forceinline__ bool run(State& s, int& ahead, uint32_t tmem) const {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     bool ok = true;
-    if (warp >= kFirstCopyWarp) ok = copy(s, ahead, threadIdx.x - kFirstCopyWarp * 32);
+    if (warp < kEpilogueWarps) ok = epilogue(s, tmem, warp, lane);
     else if (warp == kMmaWarp) ok = lane != 0 || products(s, tmem);
-    else if (warp < kEpilogueWarps) ok = epilogue(s, tmem, warp, lane);
+    else if (warp == kLoadWarp) ok = lane != 0 || load(s, ahead);
+    else if (FP8 && warp >= kFirstConvertWarp) ok = convert(s, threadIdx.x - kFirstConvertWarp * 32);
     if (!ok) raise_flag(a.flags, MOE_DEVERR_TIMEOUT);
     __syncwarp();
     return __syncthreads_and(ok) != 0;
   }
 };
 
+// The tokens in the order of the experts, a block per token: bf16 as they are;
+// e4m3: fp16 times the token's factor.
+template <bool FP8>
+__device__ __forceinline__ void sort_tokens(const LayerArgs& a, const Groups& g, uint32_t* red,
+                                            int* place) {
+  const int KS = a.K + a.S;
+  for (int t = blockIdx.x; t < g.tokens; t += gridDim.x) {
+    if (static_cast<int>(threadIdx.x) < KS) {
+      const int entry = t * KS + threadIdx.x;
+      place[threadIdx.x] = g.rank[entry] == kNone ? -1 : g.start[expert_of(a, entry)] + g.rank[entry];
+      if (FP8) a.amax[entry] = 0;
+    }
+    const uint8_t* row = a.x + static_cast<int64_t>(t) * a.H * 2;
+    float f = 1.0f;
+    if (FP8) {
+      f = f16_factor(block_max_bits<kThreads>(row, a.H, red));
+      if (threadIdx.x == 0) a.xscale[t] = 1.0f / f;
+    } else {
+      __syncthreads();
+    }
+    for (int v = threadIdx.x; v < a.H / 8; v += kThreads) {
+      Vec16 o = ld_vec(row + v * 16);
+      if (FP8) o = scaled_f16(o, f);
+      for (int k = 0; k < KS; ++k)
+        if (place[k] >= 0)
+          st_vec(reinterpret_cast<uint8_t*>(a.y) + static_cast<int64_t>(place[k]) * a.H * 2 + v * 16, o);
+    }
+    __syncthreads();
+  }
+}
+
+// fp16 copies of the activations, their factors from the entries' maxima.
+__device__ __forceinline__ void scale_sorted(const LayerArgs& a, const Groups& g, int rows) {
+  const int per = a.I / 8;
+  const int64_t n = static_cast<int64_t>(rows) * per;
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x; i < n;
+       i += static_cast<int64_t>(gridDim.x) * kThreads) {
+    const int r = static_cast<int>(i / per);
+    scale_activation(a, i, __ldcg(a.amax + g.order[r]));
+  }
+}
+
 template <bool FP8>
 __device__ __forceinline__ bool layer_body(const LayerArgs& a, const Groups& g, Barriers& b,
-                                           const CUtensorMap* w13, const CUtensorMap* w2,
-                                           uint32_t queue, uint32_t tmem, int* ok) {
-  const int tid = static_cast<int>(threadIdx.x) - kFirstCopyWarp * 32;
+                                           const Maps& maps, uint32_t queue, uint32_t tmem, int* ok) {
+  const bool loads = threadIdx.x == kLoadWarp * 32;
   uint32_t* arrived = a.arrived;  // of the next barrier
   State s;
-  const ManyPhase<FP8, true> up(a, g, b, w13, queue);
-  const ManyPhase<FP8, false> down(a, g, b, w2, queue);
+  const ManyPhase<FP8, true> up(a, g, b, maps, queue);
+  const ManyPhase<FP8, false> down(a, g, b, maps, queue);
   int ahead = 0;
-  bool done = true;
-  if (FP8) {
-    if (tid >= 0) ahead = up.send_ahead(s, tid);
-    done = grid_wait(a, arrived++, ok);
-  }
+  if (loads) ahead = up.send_ahead(s);
+  bool done = grid_wait(a, arrived++, ok);
+  fence_copies();
   done = done && up.run(s, ahead, tmem);
   if (done) {
+    fence_copies();
     grid_arrive(arrived);
-    ahead = tid >= 0 ? down.send_ahead(s, tid) : 0;
+    if (loads) ahead = down.send_ahead(s);
     done = grid_wait(a, arrived++, ok);
+    fence_copies();
   }
   if (FP8 && done) {
-    scale_activations<kThreads>(a, g);
+    scale_sorted(a, g, b.rows);
+    fence_copies();
     grid_arrive(arrived);
     done = grid_wait(a, arrived++, ok);
+    fence_copies();
   }
   done = done && down.run(s, ahead, tmem);
   if (done) {
@@ -564,31 +576,33 @@ __device__ __forceinline__ bool layer_body(const LayerArgs& a, const Groups& g, 
     if (grid_wait(a, arrived, ok)) sum_entries<kThreads>(a, g);
     return true;
   }
-  copies_wait<0>();
-  if (tid >= 0) down.drain(s, tid);
+  if (loads) down.drain(s, ahead);
   return false;
 }
 
 template <bool FP8>
 __global__ void __launch_bounds__(kThreads, 1) layer_many_kernel(
-    const __grid_constant__ CUtensorMap w13, const __grid_constant__ CUtensorMap w2, LayerArgs a) {
+    const __grid_constant__ Maps maps, LayerArgs a) {
   constexpr uint32_t kColumns = 2 * ManyPhase<FP8, true>::kMaxN;
   extern __shared__ __align__(16) uint8_t raw[];
   __shared__ int ok;
+  __shared__ int place[MOE_MAX_TOPK + MOE_LAYER_MAX_SHARED];
+  __shared__ uint32_t red[kThreads / 32];
   grid_dependency_wait();
   // operands begin on the 1024 bytes after which the swizzle repeats
   uint8_t* smem = raw + ((1024u - (smem_addr(raw) & 1023u)) & 1023u);
   Barriers& b = *reinterpret_cast<Barriers*>(smem + kQueueBytes);
   const int warp = threadIdx.x >> 5;
   Groups g;
-  group_entries<kThreads>(a, g, smem + kQueueBytes + kBarrierBytes);
+  group_entries<kThreads, true>(a, g, smem + kQueueBytes + kBarrierBytes,
+                                reinterpret_cast<uint32_t*>(smem));
   if (threadIdx.x == 0) {
     for (int i = 0; i < kMaxRing; ++i) {
-      mbar_init(&b.landed[i], kParts);
-      mbar_init(&b.full[i], kCopyWarps);
+      mbar_init(&b.landed[i], 1);
       mbar_init(&b.empty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
+      mbar_init(&b.a16_full[i], kConvertWarps);
       mbar_init(&b.a16_empty[i], 1);
       mbar_init(&b.acc_full[i], 2);
       mbar_init(&b.acc_empty[i], kEpilogueWarps);
@@ -596,6 +610,7 @@ __global__ void __launch_bounds__(kThreads, 1) layer_many_kernel(
     mbar_init(&b.drained, 1);
     fence_mbar_init();
     b.max_tokens = 0;
+    b.rows = 0;
   }
   if (warp == kMmaWarp)
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
@@ -605,14 +620,18 @@ __global__ void __launch_bounds__(kThreads, 1) layer_many_kernel(
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  for (int i = threadIdx.x; i < g.nslots; i += kThreads) atomicMax(&b.max_tokens, g.cnt[g.slot_expert[i]]);
-  if (FP8) {
-    scale_tokens<kThreads>(a, g.tokens, reinterpret_cast<uint32_t*>(smem));
-    grid_arrive(a.arrived);
+  for (int i = threadIdx.x; i < g.nslots; i += kThreads) {
+    const int p = g.slot_expert[i];
+    atomicMax(&b.max_tokens, g.cnt[p]);
+    atomicMax(&b.rows, g.start[p] + g.cnt[p]);
   }
+  sort_tokens<FP8>(a, g, red, place);
+  // the queue was scratch memory of the grouping
+  fence_copies();
+  grid_arrive(a.arrived);
   __syncthreads();
   const uint32_t tmem = b.tmem;
-  if (!layer_body<FP8>(a, g, b, &w13, &w2, smem_addr(smem), tmem, &ok)) {
+  if (!layer_body<FP8>(a, g, b, maps, smem_addr(smem), tmem, &ok)) {
     if (threadIdx.x == kMmaWarp * 32) {
       mma_commit(&b.drained);
       wait_phase(&b.drained, 0, MOE_DEFAULT_WAIT_LIMIT_NS);
@@ -625,36 +644,52 @@ __global__ void __launch_bounds__(kThreads, 1) layer_many_kernel(
                  : "memory");
 }
 
-// Weights as [matrices, rows, cols], boxes of 128 bytes of `box_rows` rows of
-// `box_mats` matrices; bf16 swizzled as the products read them.
-bool encode_weights(CUtensorMap* m, const void* base, bool e4m3, uint64_t cols, uint64_t rows,
-                    uint64_t mats, uint32_t box_rows, uint32_t box_mats) {
+// A tensor of 16-bit or 8-bit elements, innermost dimension first; boxes of 128
+// bytes by box[1], box[2], ...; `swizzled` as the products read them.
+bool encode(CUtensorMap* m, const void* base, bool bytes, bool swizzled, int rank,
+            const cuuint64_t* dims, const cuuint64_t* strides, const cuuint32_t* box) {
   EncodeTiled fn = encode_fn();
-  if (!fn) return false;
-  const uint64_t eb = e4m3 ? 1 : 2;
-  const cuuint64_t dims[3] = {cols, rows, mats};
-  const cuuint64_t strides[2] = {cols * eb, rows * cols * eb};
-  const cuuint32_t box[3] = {static_cast<cuuint32_t>(128 / eb), box_rows, box_mats};
-  const cuuint32_t estr[3] = {1, 1, 1};
-  return fn(m, e4m3 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
-            const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-            e4m3 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B,
-            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  const cuuint32_t estr[5] = {1, 1, 1, 1, 1};
+  return fn && fn(m, bytes ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank,
+                  const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  swizzled ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+bool encode_maps(Maps* m, const LayerArgs& a, bool e4m3) {
+  const cuuint64_t n = a.E + a.S, H = a.H, I = a.I, rows = static_cast<cuuint64_t>(a.T) * (a.K + a.S);
+  const cuuint64_t eb = e4m3 ? 1 : 2;
+  const cuuint32_t k = static_cast<cuuint32_t>(128 / eb);
+  // [expert][8 outputs][gate, up][output][column]: 8 gate rows and their 8 up
+  // rows in turn
+  const cuuint64_t d13[5] = {H, 8, 2, I / 8, n};
+  const cuuint64_t s13[4] = {H * eb, I * H * eb, 8 * H * eb, 2 * I * H * eb};
+  const cuuint32_t b13[5] = {k, 8, 2, 8, 1};
+  const cuuint64_t d2[3] = {I, H, n};
+  const cuuint64_t s2[2] = {I * eb, H * I * eb};
+  const cuuint32_t b2[3] = {k, kTileRows, 1};
+  // tokens: 16-bit either way
+  const cuuint64_t dx[3] = {H, rows, 1};
+  const cuuint64_t sx[2] = {H * 2, rows * H * 2};
+  const cuuint64_t da[3] = {I, rows, e4m3 ? 1ull : 2ull};
+  const cuuint64_t sa[2] = {I * 2, rows * I * 2};
+  const cuuint32_t bt[3] = {64, kBoxTokens, 1};
+  return encode(&m->w13, a.w13, e4m3, !e4m3, 5, d13, s13, b13) &&
+         encode(&m->w2, a.w2, e4m3, !e4m3, 3, d2, s2, b2) &&
+         encode(&m->x, a.y, false, true, 3, dx, sx, bt) &&
+         encode(&m->a, a.a, false, true, 3, da, sa, bt);
 }
 
 template <bool FP8>
 cudaError_t launch_one(const moe_handle* h, const LayerArgs& a, cudaStream_t s) {
-  CUtensorMap w13, w2;
-  const uint64_t n = a.E + a.S;
-  if (!encode_weights(&w13, a.w13, FP8, a.H, a.I, 2 * n, 16, 2) ||
-      !encode_weights(&w2, a.w2, FP8, a.I, a.H, n, 32, 1))
-    return cudaErrorInvalidValue;
+  Maps maps;
+  if (!encode_maps(&maps, a, FP8)) return cudaErrorInvalidValue;
   auto k = layer_many_kernel<FP8>;
   const size_t smem = kFixedBytes + groups_bytes(a.T, a.K + a.S, a.E + a.S);
   const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                              static_cast<int>(smem));
   if (e != cudaSuccess) return e;
-  return launch_chained(k, dim3(h->num_sms), dim3(kThreads), smem, s, true, w13, w2, a);
+  return launch_chained(k, dim3(h->num_sms), dim3(kThreads), smem, s, true, maps, a);
 }
 
 }  // namespace
