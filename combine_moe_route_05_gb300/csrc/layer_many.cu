@@ -9,7 +9,8 @@
 //
 //   warps 0..3   epilogue: a thread per weight row (tensor-memory lane)
 //   warp  4      issues the products
-//   warp  5      fills the queue: tensor copies of weights and tokens
+//   warps 5..7   fill the queue by tensor copies: 5 weights, 6 and 7 tokens
+//                (a thread takes 80 ns for each copy it asks for)
 //   warps 8..15  e4m3: turn the weights that have landed into fp16 (exact)
 //
 // For the tensor copies the tokens lie in the order of the experts: a first
@@ -34,31 +35,33 @@ namespace moe {
 namespace {
 
 constexpr int kThreads = 512;
-constexpr int kEpilogueWarps = 4, kMmaWarp = 4, kLoadWarp = 5;
+constexpr int kEpilogueWarps = 4, kMmaWarp = 4, kWeightWarp = 5, kTokenWarp = 6, kTokenWarps = 2;
 constexpr int kFirstConvertWarp = 8, kConvertWarps = 8;
 static_assert((kFirstConvertWarp + kConvertWarps) * 32 == kThreads, "roles");
 constexpr int kTileRows = 128;
 constexpr uint32_t kWeightBytes = kTileRows * 128;  // of a stage: 128 bytes of each row
-constexpr int kBoxTokens = 16;                      // of a tensor copy
+constexpr int kBoxTokens = 32;                      // of a tensor copy
 constexpr uint32_t kBoxBytes = kBoxTokens * 128;
 constexpr int kJobRing = 32;     // jobs on their way from the loading thread to the others
 constexpr int kMaxRing = 10;     // stages of the queue
-constexpr size_t kQueueBytes = 208 * 1024;
+constexpr int kMaxAcc = 4;       // accumulators
+constexpr size_t kQueueBytes = 208 * 1024 - 1024;
 constexpr uint32_t kA16Bytes = 2 * kTileRows * 128;  // 128 columns in fp16
-constexpr size_t kBarrierBytes = 512;
+constexpr size_t kBarrierBytes = 1024;
 constexpr size_t kFixedBytes = 1024 /* alignment */ + kQueueBytes + kBarrierBytes;
 static_assert(kFixedBytes + groups_bytes(MOE_LAYER_MAX_TOKENS, MOE_MAX_TOPK + MOE_LAYER_MAX_SHARED,
                                          kMaxExperts) + 256 <= 227 * 1024, "shared memory budget");
 
 struct Barriers {
-  uint64_t landed[kMaxRing];  // a stage is there
+  uint64_t weights[kMaxRing];  // a stage's weights are there
+  uint64_t tokens[kMaxRing];   // and its tokens (an arrival per loading thread)
   uint64_t empty[kMaxRing];   // its products are done
   uint64_t a16_full[2];       // e4m3: an fp16 slice is there (an arrival per converting warp)
   uint64_t a16_empty[2];      // and its products are done
-  uint64_t acc_full[2];       // an accumulator is complete (the commit, and the issuing thread)
-  uint64_t acc_empty[2];      // and read (an arrival per epilogue warp)
+  uint64_t acc_full[kMaxAcc];   // an accumulator is complete
+  uint64_t acc_empty[kMaxAcc];  // and read (an arrival per epilogue warp)
   uint64_t drained;           // after a wait that gave up: no product is under way
-  int32_t jobs[kJobRing];
+  unsigned long long jobs[kJobRing];  // number, counted from 1 << 32, plus q + 1 (0: the end)
   uint32_t tmem;
   int32_t max_tokens;         // of one expert
   int32_t rows;               // entries in all
@@ -114,13 +117,6 @@ __device__ __forceinline__ void tma_load_5d(uint32_t dst, const CUtensorMap* map
       : "memory");
 }
 
-// Bytes that the barrier's phase waits for, without an arrival.
-__device__ __forceinline__ void mbar_expect_tx(uint64_t* bar, uint32_t bytes) {
-  asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(smem_addr(bar)),
-               "r"(bytes)
-               : "memory");
-}
-
 // What this thread wrote to or knows of in global memory, for tensor copies.
 __device__ __forceinline__ void fence_copies() { asm volatile("fence.proxy.async;" ::: "memory"); }
 
@@ -139,10 +135,8 @@ struct Place {
 // Where each role stands in the rings: all run on from the up to the down
 // products.
 struct State {
-  Place fill{0, 0};  // loading: the next stage
-  Place sent{0, 0};  // the next one whose weights are asked for
-  int issued = 0;    // stages asked for
-  Place read{0, 0};  // converting, products: the next stage to be read
+  Place stage{0, 0};  // the next one to be filled or read
+  int issued = 0;     // loading: stages asked for
   Place a16{0, 0};
   Place acc{0, 0};
   int job = 0;
@@ -153,6 +147,7 @@ struct ManyPhase {
   static constexpr int kEb = FP8 ? 1 : 2;
   static constexpr int kTileOutputs = UP ? 64 : 128;
   static constexpr int kMaxN = FP8 ? 64 : 128;  // tokens of one pass over the weights
+  static constexpr int kAcc = FP8 ? 4 : 2;      // accumulators
   static constexpr bool kLow = !UP && !FP8;     // a's low parts follow
   static constexpr int kSlices = FP8 || kLow ? 2 : 1;  // of 128 bytes of a token's row in a stage
 
@@ -178,14 +173,30 @@ struct ManyPhase {
     nq = g.nslots * tiles;
     given = a.arrived + kBarriers + (UP ? 0 : 1);
     // the same stages in both phases
-    const int n = columns(min(b.max_tokens, kMaxN));
+    const int n = boxed(min(b.max_tokens, kMaxN));
     stage_bytes = kWeightBytes + n * 256;
     const int room = static_cast<int>(kQueueBytes - (FP8 ? 2 * kA16Bytes : 0));
     ring = min(room / static_cast<int>(stage_bytes), kMaxRing);
     a16 = queue + static_cast<uint32_t>(kQueueBytes) - 2 * kA16Bytes;
   }
 
+  // Columns of the products, and rows that the tensor copies fill.
   static __device__ __forceinline__ int columns(int tokens) { return (tokens + 15) / 16 * 16; }
+  static __device__ __forceinline__ int boxed(int tokens) {
+    return (tokens + kBoxTokens - 1) / kBoxTokens * kBoxTokens;
+  }
+  // Job number i, once the weights' thread has taken it: q, -1 at the end, -2
+  // after the handle's limit.
+  __device__ __forceinline__ int job(int i) const {
+    const volatile unsigned long long* from = &b.jobs[i % kJobRing];
+    unsigned long long v = *from;
+    if (static_cast<int>(v >> 32) != i + 1) {
+      const unsigned long long t0 = global_ns();
+      while (static_cast<int>((v = *from) >> 32) != i + 1)
+        if (global_ns() - t0 > a.wait_ns) return -2;
+    }
+    return static_cast<int>(v & 0xffffffffu) - 1;
+  }
   __device__ __forceinline__ uint32_t stage(int slot) const { return queue + slot * stage_bytes; }
   __device__ __forceinline__ int expert(int slot) const {
     const int p = g.slot_expert[slot];
@@ -203,18 +214,18 @@ struct ManyPhase {
     return __all_sync(kFull, wait_phase(bar, parity, a.wait_ns));
   }
 
-  // -- the loading thread
+  // -- the loading threads
 
   // Asks for 128 bytes (column block kb) of the 128 weight rows of job q.
   // Behind the last output and the last column zeros arrive.
   __device__ __forceinline__ void send_weights(State& s, int q, int kb) const {
     const int slot = q / tiles, tile = q - slot * tiles;
-    uint64_t* bar = &b.landed[s.sent.slot];
-    const uint32_t to = stage(s.sent.slot);
-    mbar_expect_tx(bar, kWeightBytes);
+    uint64_t* bar = &b.weights[s.stage.slot];
+    const uint32_t to = stage(s.stage.slot);
+    mbar_arrive_expect_tx(bar, kWeightBytes);
     if (UP) tma_load_5d(to, weights, kb * (128 / kEb), 0, 0, tile * 8, expert(slot), bar);
     else tma_load_3d(to, weights, kb * (128 / kEb), tile * 128, expert(slot), bar);
-    s.sent.step(ring);
+    s.stage.step(ring);
     ++s.issued;
   }
   // Before the tokens are there: the weights of the first stages.
@@ -225,48 +236,60 @@ struct ManyPhase {
     for (int kb = 0; kb < n; ++kb) send_weights(s, q, kb);
     return n;
   }
-  // After a wait that gave up: what is on its way has landed.
-  __device__ __forceinline__ void drain(State& s, int ahead) const {
-    for (; ahead > 0; --ahead, s.fill.step(ring)) mbar_arrive(&b.landed[s.fill.slot]);
-    for (int i = max(s.issued - ring, 0); i < s.issued; ++i)
-      wait_phase(&b.landed[i % ring], (i / ring) & 1u, MOE_DEFAULT_WAIT_LIMIT_NS);
-  }
-
-  __device__ __forceinline__ bool load(State& s, int& ahead) const {
+  __device__ __forceinline__ bool load_weights(State& s, int ahead) const {
     int q = static_cast<int>(blockIdx.x) < nq ? static_cast<int>(blockIdx.x) : -1;
     for (;; ++s.job) {
-      b.jobs[s.job % kJobRing] = q;
+      *const_cast<volatile unsigned long long*>(&b.jobs[s.job % kJobRing]) =
+          (static_cast<unsigned long long>(s.job + 1) << 32) + static_cast<uint32_t>(q + 1);
       if (q < 0) break;
       const int ticket = static_cast<int>(atomicAdd(given, 1u));
-      const int p = g.slot_expert[q / tiles];
-      for (int c0 = 0; c0 < g.cnt[p]; c0 += kMaxN) {
-        const int n = columns(min(g.cnt[p] - c0, kMaxN)), row = g.start[p] + c0;
-        for (int kb = 0; kb < stages; ++kb) {
-          if (!wait_phase(&b.empty[s.fill.slot], s.fill.parity ^ 1u, a.wait_ns)) return false;
-          if (ahead > 0) --ahead;
-          else send_weights(s, q, kb);
-          uint64_t* bar = &b.landed[s.fill.slot];
-          uint32_t to = stage(s.fill.slot) + kWeightBytes;
-          mbar_arrive_expect_tx(bar, n * (128 * kSlices));
-#pragma unroll
-          for (int i = 0; i < kSlices; ++i)
-            for (int r = 0; r < n; r += kBoxTokens, to += kBoxBytes)
-              tma_load_3d(to, tokens, kb * (FP8 ? 128 : 64) + (FP8 ? i * 64 : 0), row + r,
-                          kLow ? i : 0, bar);
-          s.fill.step(ring);
+      const int n = (g.cnt[g.slot_expert[q / tiles]] + kMaxN - 1) / kMaxN;
+      for (int pass = 0; pass < n; ++pass, ahead = 0)
+        for (int kb = ahead; kb < stages; ++kb) {
+          if (!wait_phase(&b.empty[s.stage.slot], s.stage.parity ^ 1u, a.wait_ns)) return false;
+          send_weights(s, q, kb);
         }
-      }
       q = ticket + static_cast<int>(gridDim.x);
       if (q >= nq) q = -1;
     }
-    // a stage of nothing carries the end
-    if (!wait_phase(&b.empty[s.fill.slot], s.fill.parity ^ 1u, a.wait_ns)) return false;
-    mbar_arrive(&b.landed[s.fill.slot]);
-    s.fill.step(ring);
-    s.sent.step(ring);
-    ++s.issued;
     ++s.job;
     return true;
+  }
+
+  // Thread `i` of the tokens' threads: one of two slices, or every other box.
+  __device__ __forceinline__ bool load_tokens(State& s, int i) const {
+    for (;; ++s.job) {
+      const int q = job(s.job);
+      if (q < 0) {
+        ++s.job;
+        return q == -1;
+      }
+      const int p = g.slot_expert[q / tiles];
+      for (int c0 = 0; c0 < g.cnt[p]; c0 += kMaxN) {
+        const int n = boxed(min(g.cnt[p] - c0, kMaxN)), row = g.start[p] + c0;
+        const int first = kSlices == 2 ? 0 : i * kBoxTokens;
+        constexpr int kStep = kSlices == 2 ? kBoxTokens : kTokenWarps * kBoxTokens;
+        const uint32_t bytes = n > first ? (n - first + kStep - 1) / kStep * kBoxBytes : 0;
+        for (int kb = 0; kb < stages; ++kb) {
+          if (!wait_phase(&b.empty[s.stage.slot], s.stage.parity ^ 1u, a.wait_ns)) return false;
+          uint64_t* bar = &b.tokens[s.stage.slot];
+          const uint32_t to = stage(s.stage.slot) + kWeightBytes + (kSlices == 2 ? i * n * 128 : 0);
+          mbar_arrive_expect_tx(bar, bytes);
+          for (int r = first; r < n; r += kStep)
+            tma_load_3d(to + r * 128, tokens, kb * (FP8 ? 128 : 64) + (FP8 ? i * 64 : 0), row + r,
+                        kLow ? i : 0, bar);
+          s.stage.step(ring);
+          ++s.issued;
+        }
+      }
+    }
+  }
+
+  // After a wait that gave up: what a loading thread asked for has landed (for
+  // certain after the default limit).
+  __device__ __forceinline__ void drain(const State& s, uint64_t* landed) const {
+    for (int i = max(s.issued - ring, 0); i < s.issued; ++i)
+      if (!wait_phase(&landed[i % ring], (i / ring) & 1u, MOE_DEFAULT_WAIT_LIMIT_NS)) return;
   }
 
   // -- converting warps (e4m3)
@@ -274,15 +297,17 @@ struct ManyPhase {
   __device__ __forceinline__ bool convert(State& s, int tid) const {
     const int row = tid / 8, c = tid % 8;
     for (;; ++s.job) {
-      if (!warp_wait(&b.landed[s.read.slot], s.read.parity)) return false;
-      const int q = b.jobs[s.job % kJobRing];
-      if (q < 0) break;
+      const int q = __shfl_sync(kFull, job(s.job), 0);
+      if (q < 0) {
+        ++s.job;
+        return q == -1;
+      }
       const int p = g.slot_expert[q / tiles];
       for (int n = (g.cnt[p] + kMaxN - 1) / kMaxN * stages; n > 0; --n) {
-        if (!warp_wait(&b.landed[s.read.slot], s.read.parity) ||
+        if (!warp_wait(&b.weights[s.stage.slot], s.stage.parity) ||
             !warp_wait(&b.a16_empty[s.a16.slot], s.a16.parity ^ 1u))
           return false;
-        const uint32_t from = stage(s.read.slot) + tid * 16;
+        const uint32_t from = stage(s.stage.slot) + tid * 16;
         const uint32_t to = a16 + s.a16.slot * kA16Bytes + (c >> 2) * (kTileRows * 128) + row * 128;
         Vec16 v[4];
 #pragma unroll
@@ -309,12 +334,9 @@ struct ManyPhase {
         __syncwarp();
         if ((tid & 31) == 0) mbar_arrive(&b.a16_full[s.a16.slot]);
         s.a16.step(2);
-        s.read.step(ring);
+        s.stage.step(ring);
       }
     }
-    s.read.step(ring);
-    ++s.job;
-    return true;
   }
 
   // -- the issuing thread
@@ -323,21 +345,25 @@ struct ManyPhase {
     constexpr uint32_t kFormat = (1u << 4) | (FP8 ? 0u : (1u << 7) | (1u << 10)) |
                                  (static_cast<uint32_t>(kTileRows >> 4) << 24);
     for (;; ++s.job) {
-      if (!wait_phase(&b.landed[s.read.slot], s.read.parity, a.wait_ns)) return false;
-      const int q = b.jobs[s.job % kJobRing];
-      if (q < 0) break;
+      const int q = job(s.job);
+      if (q < 0) {
+        ++s.job;
+        return q == -1;
+      }
       const int p = g.slot_expert[q / tiles];
       for (int c0 = 0; c0 < g.cnt[p]; c0 += kMaxN) {
-        const int n = columns(min(g.cnt[p] - c0, kMaxN));
-        const uint32_t idesc = kFormat | (static_cast<uint32_t>(n >> 3) << 17);
+        const int cnt = min(g.cnt[p] - c0, kMaxN);
+        const uint32_t idesc = kFormat | (static_cast<uint32_t>(columns(cnt) >> 3) << 17);
         for (int kb = 0; kb < stages; ++kb) {
-          if (!wait_phase(&b.landed[s.read.slot], s.read.parity, a.wait_ns)) return false;
-          if (FP8 && !wait_phase(&b.a16_full[s.a16.slot], s.a16.parity, a.wait_ns)) return false;
+          if (!wait_phase(&b.tokens[s.stage.slot], s.stage.parity, a.wait_ns)) return false;
+          if (!wait_phase(FP8 ? &b.a16_full[s.a16.slot] : &b.weights[s.stage.slot],
+                          FP8 ? s.a16.parity : s.stage.parity, a.wait_ns))
+            return false;
           if ((FP8 || kb == 0) && !wait_phase(&b.acc_empty[s.acc.slot], s.acc.parity ^ 1u, a.wait_ns))
             return false;
           tc_fence_after();
           const uint32_t d = tmem + s.acc.slot * kMaxN;
-          const uint32_t at = stage(s.read.slot);
+          const uint32_t at = stage(s.stage.slot);
           const uint64_t x = sw128_desc(at + kWeightBytes);
           const uint64_t w = sw128_desc(FP8 ? a16 + s.a16.slot * kA16Bytes : at);
           // the second slice: e4m3: the other 64 columns; a's low parts: the
@@ -347,31 +373,21 @@ struct ManyPhase {
           for (int i = 0; i < kSlices; ++i)
 #pragma unroll
             for (int k = 0; k < 4; ++k)
-              mma_f16(d, w + i * w_next + k * 2, x + i * (n * 8) + k * 2, idesc,
+              mma_f16(d, w + i * w_next + k * 2, x + i * (boxed(cnt) * 8) + k * 2, idesc,
                       (!FP8 && kb > 0) || i + k > 0);
           if (FP8) {
             mma_commit(&b.a16_empty[s.a16.slot]);
             s.a16.step(2);
           }
-          mma_commit(&b.empty[s.read.slot]);
-          s.read.step(ring);
+          mma_commit(&b.empty[s.stage.slot]);
+          s.stage.step(ring);
           if (FP8 || kb == stages - 1) {
             mma_commit(&b.acc_full[s.acc.slot]);
-            mbar_arrive(&b.acc_full[s.acc.slot]);
-            s.acc.step(2);
+            s.acc.step(kAcc);
           }
         }
       }
     }
-    // the end: passed on as an accumulator of nothing
-    if (!wait_phase(&b.acc_empty[s.acc.slot], s.acc.parity ^ 1u, a.wait_ns)) return false;
-    mma_commit(&b.empty[s.read.slot]);
-    mma_commit(&b.acc_full[s.acc.slot]);
-    mbar_arrive(&b.acc_full[s.acc.slot]);
-    s.read.step(ring);
-    s.acc.step(2);
-    ++s.job;
-    return true;
   }
 
   // -- epilogue warps
@@ -385,7 +401,7 @@ struct ManyPhase {
     tc_fence_before();
     __syncwarp();
     if (lane == 0) mbar_arrive(&b.acc_empty[s.acc.slot]);
-    s.acc.step(2);
+    s.acc.step(kAcc);
   }
 
   // 16 columns (tokens n0 ..) of the warp's rows of the tile.
@@ -439,9 +455,11 @@ struct ManyPhase {
   __device__ __forceinline__ bool epilogue(State& s, uint32_t tmem, int warp, int lane) const {
     const uint32_t mine = tmem + (static_cast<uint32_t>(warp * 32) << 16);
     for (;; ++s.job) {
-      if (!acc_ready(s)) return false;
-      const int q = b.jobs[s.job % kJobRing];
-      if (q < 0) break;
+      const int q = __shfl_sync(kFull, job(s.job), 0);
+      if (q < 0) {
+        ++s.job;
+        return q == -1;
+      }
       const int slot = q / tiles, tile = q - slot * tiles, p = g.slot_expert[slot];
       for (int c0 = 0; c0 < g.cnt[p]; c0 += kMaxN) {
         const int cnt = min(g.cnt[p] - c0, kMaxN), begin = g.start[p] + c0;
@@ -456,12 +474,13 @@ struct ManyPhase {
             if (kb + 1 < stages) next = __ldg(scale + kb + 1);
             if (!acc_ready(s)) return false;
 #pragma unroll
-            for (int c = 0; c < kMaxN / 16; ++c)
+            for (int c = 0; c < kMaxN / 16; c += 2)
               if (c * 16 < cnt) {
-                uint32_t v[16];
-                tmem_ld16(mine + s.acc.slot * kMaxN + c * 16, v);
+                uint32_t v[32];
+                tmem_ld32(mine + s.acc.slot * kMaxN + c * 16, v);
 #pragma unroll
-                for (int j = 0; j < 16; ++j) sum[c][j] = fmaf(f, __uint_as_float(v[j]), sum[c][j]);
+                for (int j = 0; j < 32; ++j)
+                  sum[c + j / 16][j % 16] = fmaf(f, __uint_as_float(v[j]), sum[c + j / 16][j % 16]);
               }
             acc_read(s, lane);
           }
@@ -483,18 +502,16 @@ struct ManyPhase {
         }
       }
     }
-    acc_read(s, lane);
-    ++s.job;
-    return true;
   }
 
-  __device__ __forceinline__ bool run(State& s, int& ahead, uint32_t tmem) const {
+  __device__ __forceinline__ bool run(State& s, int ahead, uint32_t tmem) const {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     bool ok = true;
     if (warp < kEpilogueWarps) ok = epilogue(s, tmem, warp, lane);
     else if (warp == kMmaWarp) ok = lane != 0 || products(s, tmem);
-    else if (warp == kLoadWarp) ok = lane != 0 || load(s, ahead);
-    else if (FP8 && warp >= kFirstConvertWarp) ok = convert(s, threadIdx.x - kFirstConvertWarp * 32);
+    else if (warp == kWeightWarp) ok = lane != 0 || load_weights(s, ahead);
+    else if (warp < kTokenWarp + kTokenWarps) ok = lane != 0 || load_tokens(s, warp - kTokenWarp);
+    else if (FP8) ok = convert(s, threadIdx.x - kFirstConvertWarp * 32);
     if (!ok) raise_flag(a.flags, MOE_DEVERR_TIMEOUT);
     __syncwarp();
     return __syncthreads_and(ok) != 0;
@@ -546,7 +563,7 @@ __device__ __forceinline__ void scale_sorted(const LayerArgs& a, const Groups& g
 template <bool FP8>
 __device__ __forceinline__ bool layer_body(const LayerArgs& a, const Groups& g, Barriers& b,
                                            const Maps& maps, uint32_t queue, uint32_t tmem, int* ok) {
-  const bool loads = threadIdx.x == kLoadWarp * 32;
+  const bool loads = threadIdx.x == kWeightWarp * 32;
   uint32_t* arrived = a.arrived;  // of the next barrier
   State s;
   const ManyPhase<FP8, true> up(a, g, b, maps, queue);
@@ -576,14 +593,17 @@ __device__ __forceinline__ bool layer_body(const LayerArgs& a, const Groups& g, 
     if (grid_wait(a, arrived, ok)) sum_entries<kThreads>(a, g);
     return true;
   }
-  if (loads) down.drain(s, ahead);
+  if (loads) down.drain(s, b.weights);
+  const int warp = threadIdx.x >> 5;
+  if (threadIdx.x % 32 == 0 && warp >= kTokenWarp && warp < kTokenWarp + kTokenWarps)
+    down.drain(s, b.tokens);
   return false;
 }
 
 template <bool FP8>
 __global__ void __launch_bounds__(kThreads, 1) layer_many_kernel(
     const __grid_constant__ Maps maps, LayerArgs a) {
-  constexpr uint32_t kColumns = 2 * ManyPhase<FP8, true>::kMaxN;
+  constexpr uint32_t kColumns = ManyPhase<FP8, true>::kAcc * ManyPhase<FP8, true>::kMaxN;
   extern __shared__ __align__(16) uint8_t raw[];
   __shared__ int ok;
   __shared__ int place[MOE_MAX_TOPK + MOE_LAYER_MAX_SHARED];
@@ -598,15 +618,19 @@ __global__ void __launch_bounds__(kThreads, 1) layer_many_kernel(
                                 reinterpret_cast<uint32_t*>(smem));
   if (threadIdx.x == 0) {
     for (int i = 0; i < kMaxRing; ++i) {
-      mbar_init(&b.landed[i], 1);
+      mbar_init(&b.weights[i], 1);
+      mbar_init(&b.tokens[i], kTokenWarps);
       mbar_init(&b.empty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&b.a16_full[i], kConvertWarps);
       mbar_init(&b.a16_empty[i], 1);
-      mbar_init(&b.acc_full[i], 2);
+    }
+    for (int i = 0; i < kMaxAcc; ++i) {
+      mbar_init(&b.acc_full[i], 1);
       mbar_init(&b.acc_empty[i], kEpilogueWarps);
     }
+    for (int i = 0; i < kJobRing; ++i) b.jobs[i] = 0;
     mbar_init(&b.drained, 1);
     fence_mbar_init();
     b.max_tokens = 0;
