@@ -82,6 +82,15 @@ __device__ __forceinline__ void mma_f16(uint32_t d, uint64_t a, uint64_t b, uint
       : "memory");
 }
 
+// One lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(r)::"memory");
+  return r != 0;
+}
+
 // One arrival on `bar` once every product this thread issued so far is done.
 __device__ __forceinline__ void mma_commit(uint64_t* bar) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
@@ -339,28 +348,32 @@ struct ManyPhase {
     }
   }
 
-  // -- the issuing thread
+  // -- the issuing warp
 
   __device__ __forceinline__ bool products(State& s, uint32_t tmem) const {
     constexpr uint32_t kFormat = (1u << 4) | (FP8 ? 0u : (1u << 7) | (1u << 10)) |
                                  (static_cast<uint32_t>(kTileRows >> 4) << 24);
+    // the whole warp goes along and one lane issues: the operands then stay in
+    // uniform registers
     for (;; ++s.job) {
-      const int q = job(s.job);
+      const int q = __shfl_sync(kFull, job(s.job), 0);
       if (q < 0) {
         ++s.job;
         return q == -1;
       }
       const int p = g.slot_expert[q / tiles];
-      for (int c0 = 0; c0 < g.cnt[p]; c0 += kMaxN) {
-        const int cnt = min(g.cnt[p] - c0, kMaxN);
+      const int all = __shfl_sync(kFull, g.cnt[p], 0);
+      for (int c0 = 0; c0 < all; c0 += kMaxN) {
+        const int cnt = min(all - c0, kMaxN);
         const uint32_t idesc = kFormat | (static_cast<uint32_t>(columns(cnt) >> 3) << 17);
+        const uint32_t x_next = boxed(cnt) * 8;
         for (int kb = 0; kb < stages; ++kb) {
-          if (!wait_phase(&b.tokens[s.stage.slot], s.stage.parity, a.wait_ns)) return false;
-          if (!wait_phase(FP8 ? &b.a16_full[s.a16.slot] : &b.weights[s.stage.slot],
-                          FP8 ? s.a16.parity : s.stage.parity, a.wait_ns))
-            return false;
-          if ((FP8 || kb == 0) && !wait_phase(&b.acc_empty[s.acc.slot], s.acc.parity ^ 1u, a.wait_ns))
-            return false;
+          bool ok = wait_phase(&b.tokens[s.stage.slot], s.stage.parity, a.wait_ns) &&
+                    wait_phase(FP8 ? &b.a16_full[s.a16.slot] : &b.weights[s.stage.slot],
+                               FP8 ? s.a16.parity : s.stage.parity, a.wait_ns);
+          if (FP8 || kb == 0)
+            ok = ok && wait_phase(&b.acc_empty[s.acc.slot], s.acc.parity ^ 1u, a.wait_ns);
+          if (!__all_sync(kFull, ok)) return false;
           tc_fence_after();
           const uint32_t d = tmem + s.acc.slot * kMaxN;
           const uint32_t at = stage(s.stage.slot);
@@ -369,22 +382,21 @@ struct ManyPhase {
           // the second slice: e4m3: the other 64 columns; a's low parts: the
           // same weights again
           const uint32_t w_next = FP8 ? kTileRows * 128 / 16 : 0;
+          if (elect_one()) {
 #pragma unroll
-          for (int i = 0; i < kSlices; ++i)
+            for (int i = 0; i < kSlices; ++i)
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-              mma_f16(d, w + i * w_next + k * 2, x + i * (boxed(cnt) * 8) + k * 2, idesc,
-                      (!FP8 && kb > 0) || i + k > 0);
-          if (FP8) {
-            mma_commit(&b.a16_empty[s.a16.slot]);
-            s.a16.step(2);
+              for (int k = 0; k < 4; ++k)
+                mma_f16(d, w + i * w_next + k * 2, x + i * x_next + k * 2, idesc,
+                        (!FP8 && kb > 0) || i + k > 0);
+            if (FP8) mma_commit(&b.a16_empty[s.a16.slot]);
+            mma_commit(&b.empty[s.stage.slot]);
+            if (FP8 || kb == stages - 1) mma_commit(&b.acc_full[s.acc.slot]);
           }
-          mma_commit(&b.empty[s.stage.slot]);
+          __syncwarp();
+          if (FP8) s.a16.step(2);
           s.stage.step(ring);
-          if (FP8 || kb == stages - 1) {
-            mma_commit(&b.acc_full[s.acc.slot]);
-            s.acc.step(kAcc);
-          }
+          if (FP8 || kb == stages - 1) s.acc.step(kAcc);
         }
       }
     }
@@ -508,7 +520,7 @@ struct ManyPhase {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     bool ok = true;
     if (warp < kEpilogueWarps) ok = epilogue(s, tmem, warp, lane);
-    else if (warp == kMmaWarp) ok = lane != 0 || products(s, tmem);
+    else if (warp == kMmaWarp) ok = products(s, tmem);
     else if (warp == kWeightWarp) ok = lane != 0 || load_weights(s, ahead);
     else if (warp < kTokenWarp + kTokenWarps) ok = lane != 0 || load_tokens(s, warp - kTokenWarp);
     else if (FP8) ok = convert(s, threadIdx.x - kFirstConvertWarp * 32);
