@@ -39,22 +39,21 @@ constexpr int kEpilogueWarps = 4, kMmaWarp = 4, kWeightWarp = 5, kTokenWarp = 6,
 constexpr int kFirstConvertWarp = 8, kConvertWarps = 8;
 static_assert((kFirstConvertWarp + kConvertWarps) * 32 == kThreads, "roles");
 constexpr int kTileRows = 128;
-constexpr uint32_t kWeightBytes = kTileRows * 128;  // of a stage: 128 bytes of each row
+constexpr uint32_t kTileBytes = kTileRows * 128;  // 128 bytes of each row
 constexpr int kBoxTokens = 32;                      // of a tensor copy
 constexpr uint32_t kBoxBytes = kBoxTokens * 128;
 constexpr int kJobRing = 32;     // jobs on their way from the loading thread to the others
 constexpr int kMaxRing = 10;     // stages of the queue
 constexpr int kMaxAcc = 4;       // accumulators
 constexpr size_t kQueueBytes = 208 * 1024 - 1024;
-constexpr uint32_t kA16Bytes = 2 * kTileRows * 128;  // 128 columns in fp16
+constexpr uint32_t kA16Bytes = 2 * kTileBytes;  // 128 columns in fp16
 constexpr size_t kBarrierBytes = 1024;
 constexpr size_t kFixedBytes = 1024 /* alignment */ + kQueueBytes + kBarrierBytes;
 static_assert(kFixedBytes + groups_bytes(MOE_LAYER_MAX_TOKENS, MOE_MAX_TOPK + MOE_LAYER_MAX_SHARED,
                                          kMaxExperts) + 256 <= 227 * 1024, "shared memory budget");
 
 struct Barriers {
-  uint64_t weights[kMaxRing];  // a stage's weights are there
-  uint64_t tokens[kMaxRing];   // and its tokens (an arrival per loading thread)
+  uint64_t landed[kMaxRing];  // a stage is there (an arrival per loading thread)
   uint64_t empty[kMaxRing];   // its products are done
   uint64_t a16_full[2];       // e4m3: an fp16 slice is there (an arrival per converting warp)
   uint64_t a16_empty[2];      // and its products are done
@@ -153,12 +152,14 @@ struct State {
 
 template <bool FP8, bool UP>
 struct ManyPhase {
-  static constexpr int kEb = FP8 ? 1 : 2;
   static constexpr int kTileOutputs = UP ? 64 : 128;
   static constexpr int kMaxN = FP8 ? 64 : 128;  // tokens of one pass over the weights
   static constexpr int kAcc = FP8 ? 4 : 2;      // accumulators
-  static constexpr bool kLow = !UP && !FP8;     // a's low parts follow
-  static constexpr int kSlices = FP8 || kLow ? 2 : 1;  // of 128 bytes of a token's row in a stage
+  static constexpr int kAccColumns = FP8 ? kMaxN : 2 * kMaxN;
+  static constexpr bool kLow = !UP && !FP8;     // a's low parts follow as further columns
+  // A stage: 128 columns of the weight rows, bf16 in two tiles, and of the
+  // tokens' rows, in two slices (of which each has its low parts behind it).
+  static constexpr uint32_t kWeightBytes = (FP8 ? 1 : 2) * kTileBytes;
 
   const LayerArgs& a;
   const Groups& g;
@@ -178,12 +179,12 @@ struct ManyPhase {
     kd = UP ? a.H : a.I;
     limit = UP ? a.I : a.H;
     tiles = (limit + kTileOutputs - 1) / kTileOutputs;
-    stages = (kd * kEb + 127) / 128;
+    stages = (kd + 127) / 128;
     nq = g.nslots * tiles;
     given = a.arrived + kBarriers + (UP ? 0 : 1);
     // the same stages in both phases
     const int n = boxed(min(b.max_tokens, kMaxN));
-    stage_bytes = kWeightBytes + n * 256;
+    stage_bytes = kWeightBytes + n * (FP8 ? 256 : 512);
     const int room = static_cast<int>(kQueueBytes - (FP8 ? 2 * kA16Bytes : 0));
     ring = min(room / static_cast<int>(stage_bytes), kMaxRing);
     a16 = queue + static_cast<uint32_t>(kQueueBytes) - 2 * kA16Bytes;
@@ -225,15 +226,18 @@ struct ManyPhase {
 
   // -- the loading threads
 
-  // Asks for 128 bytes (column block kb) of the 128 weight rows of job q.
-  // Behind the last output and the last column zeros arrive.
+  // Asks for column block kb of the 128 weight rows of job q.  Behind the last
+  // output and the last column zeros arrive.
   __device__ __forceinline__ void send_weights(State& s, int q, int kb) const {
     const int slot = q / tiles, tile = q - slot * tiles;
-    uint64_t* bar = &b.weights[s.stage.slot];
-    const uint32_t to = stage(s.stage.slot);
+    uint64_t* bar = &b.landed[s.stage.slot];
+    uint32_t to = stage(s.stage.slot);
     mbar_arrive_expect_tx(bar, kWeightBytes);
-    if (UP) tma_load_5d(to, weights, kb * (128 / kEb), 0, 0, tile * 8, expert(slot), bar);
-    else tma_load_3d(to, weights, kb * (128 / kEb), tile * 128, expert(slot), bar);
+#pragma unroll
+    for (int i = 0; i < (FP8 ? 1 : 2); ++i, to += kTileBytes) {
+      if (UP) tma_load_5d(to, weights, kb * 128 + i * 64, 0, 0, tile * 8, expert(slot), bar);
+      else tma_load_3d(to, weights, kb * 128 + i * 64, tile * 128, expert(slot), bar);
+    }
     s.stage.step(ring);
     ++s.issued;
   }
@@ -265,7 +269,7 @@ struct ManyPhase {
     return true;
   }
 
-  // Thread `i` of the tokens' threads: one of two slices, or every other box.
+  // Thread `i` of the tokens' threads: slice i.
   __device__ __forceinline__ bool load_tokens(State& s, int i) const {
     for (;; ++s.job) {
       const int q = job(s.job);
@@ -276,17 +280,15 @@ struct ManyPhase {
       const int p = g.slot_expert[q / tiles];
       for (int c0 = 0; c0 < g.cnt[p]; c0 += kMaxN) {
         const int n = boxed(min(g.cnt[p] - c0, kMaxN)), row = g.start[p] + c0;
-        const int first = kSlices == 2 ? 0 : i * kBoxTokens;
-        constexpr int kStep = kSlices == 2 ? kBoxTokens : kTokenWarps * kBoxTokens;
-        const uint32_t bytes = n > first ? (n - first + kStep - 1) / kStep * kBoxBytes : 0;
+        const uint32_t bytes = n * (kLow ? 256 : 128);
         for (int kb = 0; kb < stages; ++kb) {
           if (!wait_phase(&b.empty[s.stage.slot], s.stage.parity ^ 1u, a.wait_ns)) return false;
-          uint64_t* bar = &b.tokens[s.stage.slot];
-          const uint32_t to = stage(s.stage.slot) + kWeightBytes + (kSlices == 2 ? i * n * 128 : 0);
+          uint64_t* bar = &b.landed[s.stage.slot];
+          uint32_t to = stage(s.stage.slot) + kWeightBytes + i * bytes;
           mbar_arrive_expect_tx(bar, bytes);
-          for (int r = first; r < n; r += kStep)
-            tma_load_3d(to + r * 128, tokens, kb * (FP8 ? 128 : 64) + (FP8 ? i * 64 : 0), row + r,
-                        kLow ? i : 0, bar);
+          for (int low = 0; low < (kLow ? 2 : 1); ++low)
+            for (int r = 0; r < n; r += kBoxTokens, to += kBoxBytes)
+              tma_load_3d(to, tokens, kb * 128 + i * 64, row + r, low, bar);
           s.stage.step(ring);
           ++s.issued;
         }
@@ -296,9 +298,9 @@ struct ManyPhase {
 
   // After a wait that gave up: what a loading thread asked for has landed (for
   // certain after the default limit).
-  __device__ __forceinline__ void drain(const State& s, uint64_t* landed) const {
+  __device__ __forceinline__ void drain(const State& s) const {
     for (int i = max(s.issued - ring, 0); i < s.issued; ++i)
-      if (!wait_phase(&landed[i % ring], (i / ring) & 1u, MOE_DEFAULT_WAIT_LIMIT_NS)) return;
+      if (!wait_phase(&b.landed[i % ring], (i / ring) & 1u, MOE_DEFAULT_WAIT_LIMIT_NS)) return;
   }
 
   // -- converting warps (e4m3)
@@ -313,11 +315,11 @@ struct ManyPhase {
       }
       const int p = g.slot_expert[q / tiles];
       for (int n = (g.cnt[p] + kMaxN - 1) / kMaxN * stages; n > 0; --n) {
-        if (!warp_wait(&b.weights[s.stage.slot], s.stage.parity) ||
+        if (!warp_wait(&b.landed[s.stage.slot], s.stage.parity) ||
             !warp_wait(&b.a16_empty[s.a16.slot], s.a16.parity ^ 1u))
           return false;
         const uint32_t from = stage(s.stage.slot) + tid * 16;
-        const uint32_t to = a16 + s.a16.slot * kA16Bytes + (c >> 2) * (kTileRows * 128) + row * 128;
+        const uint32_t to = a16 + s.a16.slot * kA16Bytes + (c >> 2) * kTileBytes + row * 128;
         Vec16 v[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) v[i] = lds16(from + i * 4096);
@@ -365,29 +367,27 @@ struct ManyPhase {
       const int all = __shfl_sync(kFull, g.cnt[p], 0);
       for (int c0 = 0; c0 < all; c0 += kMaxN) {
         const int cnt = min(all - c0, kMaxN);
-        const uint32_t idesc = kFormat | (static_cast<uint32_t>(columns(cnt) >> 3) << 17);
-        const uint32_t x_next = boxed(cnt) * 8;
+        const int n = kLow ? 2 * boxed(cnt) : columns(cnt);
+        const uint32_t idesc = kFormat | (static_cast<uint32_t>(n >> 3) << 17);
+        const uint32_t x_next = boxed(cnt) * (kLow ? 16 : 8);
         for (int kb = 0; kb < stages; ++kb) {
-          bool ok = wait_phase(&b.tokens[s.stage.slot], s.stage.parity, a.wait_ns) &&
-                    wait_phase(FP8 ? &b.a16_full[s.a16.slot] : &b.weights[s.stage.slot],
-                               FP8 ? s.a16.parity : s.stage.parity, a.wait_ns);
+          // (e4m3: the converting warps have seen the stage land)
+          bool ok = FP8 ? wait_phase(&b.a16_full[s.a16.slot], s.a16.parity, a.wait_ns)
+                        : wait_phase(&b.landed[s.stage.slot], s.stage.parity, a.wait_ns);
           if (FP8 || kb == 0)
             ok = ok && wait_phase(&b.acc_empty[s.acc.slot], s.acc.parity ^ 1u, a.wait_ns);
           if (!__all_sync(kFull, ok)) return false;
           tc_fence_after();
-          const uint32_t d = tmem + s.acc.slot * kMaxN;
+          const uint32_t d = tmem + s.acc.slot * kAccColumns;
           const uint32_t at = stage(s.stage.slot);
           const uint64_t x = sw128_desc(at + kWeightBytes);
           const uint64_t w = sw128_desc(FP8 ? a16 + s.a16.slot * kA16Bytes : at);
-          // the second slice: e4m3: the other 64 columns; a's low parts: the
-          // same weights again
-          const uint32_t w_next = FP8 ? kTileRows * 128 / 16 : 0;
           if (elect_one()) {
 #pragma unroll
-            for (int i = 0; i < kSlices; ++i)
+            for (int i = 0; i < 2; ++i)
 #pragma unroll
               for (int k = 0; k < 4; ++k)
-                mma_f16(d, w + i * w_next + k * 2, x + i * x_next + k * 2, idesc,
+                mma_f16(d, w + i * (kTileBytes / 16) + k * 2, x + i * x_next + k * 2, idesc,
                         (!FP8 && kb > 0) || i + k > 0);
             if (FP8) mma_commit(&b.a16_empty[s.a16.slot]);
             mma_commit(&b.empty[s.stage.slot]);
@@ -489,7 +489,7 @@ struct ManyPhase {
             for (int c = 0; c < kMaxN / 16; c += 2)
               if (c * 16 < cnt) {
                 uint32_t v[32];
-                tmem_ld32(mine + s.acc.slot * kMaxN + c * 16, v);
+                tmem_ld32(mine + s.acc.slot * kAccColumns + c * 16, v);
 #pragma unroll
                 for (int j = 0; j < 32; ++j)
                   sum[c + j / 16][j % 16] = fmaf(f, __uint_as_float(v[j]), sum[c + j / 16][j % 16]);
@@ -503,11 +503,13 @@ struct ManyPhase {
           if (!acc_ready(s)) return false;
 #pragma unroll 1
           for (int n0 = 0; n0 < cnt; n0 += 16) {
-            uint32_t v[16];
-            tmem_ld16(mine + s.acc.slot * kMaxN + n0, v);
+            uint32_t v[16], low[16];
+            tmem_ld16(mine + s.acc.slot * kAccColumns + n0, v);
+            if (kLow) tmem_ld16(mine + s.acc.slot * kAccColumns + boxed(cnt) + n0, low);
             float f[16];
 #pragma unroll
-            for (int j = 0; j < 16; ++j) f[j] = __uint_as_float(v[j]);
+            for (int j = 0; j < 16; ++j)
+              f[j] = kLow ? __uint_as_float(v[j]) + __uint_as_float(low[j]) : __uint_as_float(v[j]);
             store16(f, n0, cnt, begin, tile, warp, lane);
           }
           acc_read(s, lane);
@@ -605,17 +607,15 @@ __device__ __forceinline__ bool layer_body(const LayerArgs& a, const Groups& g, 
     if (grid_wait(a, arrived, ok)) sum_entries<kThreads>(a, g);
     return true;
   }
-  if (loads) down.drain(s, b.weights);
   const int warp = threadIdx.x >> 5;
-  if (threadIdx.x % 32 == 0 && warp >= kTokenWarp && warp < kTokenWarp + kTokenWarps)
-    down.drain(s, b.tokens);
+  if (threadIdx.x % 32 == 0 && warp >= kWeightWarp && warp < kTokenWarp + kTokenWarps) down.drain(s);
   return false;
 }
 
 template <bool FP8>
 __global__ void __launch_bounds__(kThreads, 1) layer_many_kernel(
     const __grid_constant__ Maps maps, LayerArgs a) {
-  constexpr uint32_t kColumns = ManyPhase<FP8, true>::kAcc * ManyPhase<FP8, true>::kMaxN;
+  constexpr uint32_t kColumns = ManyPhase<FP8, true>::kAcc * ManyPhase<FP8, true>::kAccColumns;
   extern __shared__ __align__(16) uint8_t raw[];
   __shared__ int ok;
   __shared__ int place[MOE_MAX_TOPK + MOE_LAYER_MAX_SHARED];
@@ -630,8 +630,7 @@ __global__ void __launch_bounds__(kThreads, 1) layer_many_kernel(
                                 reinterpret_cast<uint32_t*>(smem));
   if (threadIdx.x == 0) {
     for (int i = 0; i < kMaxRing; ++i) {
-      mbar_init(&b.weights[i], 1);
-      mbar_init(&b.tokens[i], kTokenWarps);
+      mbar_init(&b.landed[i], 1 + kTokenWarps);
       mbar_init(&b.empty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
