@@ -417,8 +417,9 @@ struct ManyPhase {
   }
 
   // 16 columns (tokens n0 ..) of the warp's rows of the tile.
+  // factors (e4m3): lane l's entry l (n0 < 32) or 32 + l has this inverse factor.
   __device__ __forceinline__ void store16(const float (&v)[16], int n0, int cnt, int begin, int tile,
-                                          int warp, int lane) const {
+                                          int warp, int lane, float factors) const {
     const int KS = a.K + a.S;
     if (UP) {
       const int o = tile * 64 + warp * 16 + (lane >> 4) * 8 + (lane & 7);
@@ -434,7 +435,7 @@ struct ManyPhase {
         const int64_t at = static_cast<int64_t>(begin + min(n, cnt - 1)) * a.I + o;
         if (FP8) {
           const int entry = g.order[begin + min(n, cnt - 1)];
-          const float f = __ldcg(a.xscale + entry / KS);
+          const float f = __shfl_sync(kFull, factors, n & 31);
           const float h = act_value(gate * f, a.act) * (up * f);
           if (real) a.a32[at] = h;
           const uint32_t m = real ? __float_as_uint(h) & 0x7fffffffu : 0u;
@@ -454,14 +455,12 @@ struct ManyPhase {
       return;
     }
     const int row = tile * 128 + warp * 32 + lane;
-    if (row >= limit) return;
 #pragma unroll
-    for (int j = 0; j < 16; ++j)
-      if (n0 + j < cnt) {
-        const int entry = g.order[begin + n0 + j];
-        const float f = FP8 ? 1.0f / f16_factor(__ldcg(a.amax + entry)) : 1.0f;
-        a.y[static_cast<int64_t>(entry) * a.H + row] = FP8 ? v[j] * f : v[j];
-      }
+    for (int j = 0; j < 16; ++j) {
+      const float f = FP8 ? __shfl_sync(kFull, factors, (n0 + j) & 31) : 1.0f;
+      if (n0 + j < cnt && row < limit)
+        a.y[static_cast<int64_t>(g.order[begin + n0 + j]) * a.H + row] = FP8 ? v[j] * f : v[j];
+    }
   }
 
   __device__ __forceinline__ bool epilogue(State& s, uint32_t tmem, int warp, int lane) const {
@@ -479,6 +478,14 @@ struct ManyPhase {
           const int r = weight_row(tile, warp * 32 + lane);
           const int64_t row = static_cast<int64_t>(expert(slot)) * (((UP ? 2 * a.I : a.H) + 127) / 128) + r / 128;
           const float* scale = (UP ? a.s13 : a.s2) + row * stages;
+          // what undoes the factors of the columns, two a lane
+          uint32_t held[2];
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const int entry = g.order[begin + min(i * 32 + lane, cnt - 1)];
+            held[i] = UP ? __ldcg(reinterpret_cast<const uint32_t*>(a.xscale) + entry / (a.K + a.S))
+                         : __ldcg(a.amax + entry);
+          }
           float sum[kMaxN / 16][16] = {};
           float next = __ldg(scale);
           for (int kb = 0; kb < stages; ++kb) {
@@ -498,7 +505,11 @@ struct ManyPhase {
           }
 #pragma unroll
           for (int c = 0; c < kMaxN / 16; ++c)
-            if (c * 16 < cnt) store16(sum[c], c * 16, cnt, begin, tile, warp, lane);
+            if (c * 16 < cnt) {
+              const uint32_t bits = held[c / 2];
+              store16(sum[c], c * 16, cnt, begin, tile, warp, lane,
+                      UP ? __uint_as_float(bits) : 1.0f / f16_factor(bits));
+            }
         } else {
           if (!acc_ready(s)) return false;
 #pragma unroll 1
@@ -510,7 +521,7 @@ struct ManyPhase {
 #pragma unroll
             for (int j = 0; j < 16; ++j)
               f[j] = kLow ? __uint_as_float(v[j]) + __uint_as_float(low[j]) : __uint_as_float(v[j]);
-            store16(f, n0, cnt, begin, tile, warp, lane);
+            store16(f, n0, cnt, begin, tile, warp, lane, 1.0f);
           }
           acc_read(s, lane);
         }
@@ -539,12 +550,14 @@ __device__ __forceinline__ void sort_tokens(const LayerArgs& a, const Groups& g,
                                             int* place) {
   const int KS = a.K + a.S;
   for (int t = blockIdx.x; t < g.tokens; t += gridDim.x) {
+    const uint8_t* row = a.x + static_cast<int64_t>(t) * a.H * 2;
+    const bool has = static_cast<int>(threadIdx.x) < a.H / 8;
+    const Vec16 first = has ? ld_vec(row + threadIdx.x * 16) : Vec16{};
     if (static_cast<int>(threadIdx.x) < KS) {
       const int entry = t * KS + threadIdx.x;
       place[threadIdx.x] = g.rank[entry] == kNone ? -1 : g.start[expert_of(a, entry)] + g.rank[entry];
       if (FP8) a.amax[entry] = 0;
     }
-    const uint8_t* row = a.x + static_cast<int64_t>(t) * a.H * 2;
     float f = 1.0f;
     if (FP8) {
       f = f16_factor(block_max_bits<kThreads>(row, a.H, red));
@@ -553,7 +566,7 @@ __device__ __forceinline__ void sort_tokens(const LayerArgs& a, const Groups& g,
       __syncthreads();
     }
     for (int v = threadIdx.x; v < a.H / 8; v += kThreads) {
-      Vec16 o = ld_vec(row + v * 16);
+      Vec16 o = v < kThreads ? first : ld_vec(row + v * 16);
       if (FP8) o = scaled_f16(o, f);
       for (int k = 0; k < KS; ++k)
         if (place[k] >= 0)
@@ -576,13 +589,19 @@ __device__ __forceinline__ void scale_sorted(const LayerArgs& a, const Groups& g
 
 template <bool FP8>
 __device__ __forceinline__ bool layer_body(const LayerArgs& a, const Groups& g, Barriers& b,
-                                           const Maps& maps, uint32_t queue, uint32_t tmem, int* ok) {
+                                           const Maps& maps, uint32_t queue, uint32_t tmem, int* ok,
+                                           uint32_t* red, int* place) {
   const bool loads = threadIdx.x == kWeightWarp * 32;
   uint32_t* arrived = a.arrived;  // of the next barrier
   State s;
   const ManyPhase<FP8, true> up(a, g, b, maps, queue);
   const ManyPhase<FP8, false> down(a, g, b, maps, queue);
   int ahead = 0;
+  // the weights behind the tokens, whose way to memory they would fill (91 us
+  // so, 93 with the weights first: 128 tokens, 8 experts, 4096 x 2048)
+  sort_tokens<FP8>(a, g, red, place);
+  fence_copies();
+  grid_arrive(arrived);
   if (loads) ahead = up.send_ahead(s);
   bool done = grid_wait(a, arrived++, ok);
   fence_copies();
@@ -660,13 +679,11 @@ __global__ void __launch_bounds__(kThreads, 1) layer_many_kernel(
     atomicMax(&b.max_tokens, g.cnt[p]);
     atomicMax(&b.rows, g.start[p] + g.cnt[p]);
   }
-  sort_tokens<FP8>(a, g, red, place);
   // the queue was scratch memory of the grouping
   fence_copies();
-  grid_arrive(a.arrived);
   __syncthreads();
   const uint32_t tmem = b.tmem;
-  if (!layer_body<FP8>(a, g, b, maps, smem_addr(smem), tmem, &ok)) {
+  if (!layer_body<FP8>(a, g, b, maps, smem_addr(smem), tmem, &ok, red, place)) {
     if (threadIdx.x == kMmaWarp * 32) {
       mma_commit(&b.drained);
       wait_phase(&b.drained, 0, MOE_DEFAULT_WAIT_LIMIT_NS);
