@@ -46,7 +46,7 @@ constexpr int kJobRing = 32;     // jobs on their way from the loading thread to
 constexpr int kMaxRing = 10;     // stages of the queue
 constexpr int kMaxAcc = 4;       // accumulators
 constexpr size_t kQueueBytes = 208 * 1024 - 1024;
-constexpr uint32_t kA16Bytes = 2 * kTileBytes;  // 128 columns in fp16
+constexpr uint32_t kA16Columns = 64;  // of tensor memory: 128 fp16 columns of the weights
 constexpr size_t kBarrierBytes = 1024;
 constexpr size_t kFixedBytes = 1024 /* alignment */ + kQueueBytes + kBarrierBytes;
 static_assert(kFixedBytes + groups_bytes(MOE_LAYER_MAX_TOKENS, MOE_MAX_TOPK + MOE_LAYER_MAX_SHARED,
@@ -55,7 +55,7 @@ static_assert(kFixedBytes + groups_bytes(MOE_LAYER_MAX_TOKENS, MOE_MAX_TOPK + MO
 struct Barriers {
   uint64_t landed[kMaxRing];  // a stage is there (an arrival per loading thread)
   uint64_t empty[kMaxRing];   // its products are done
-  uint64_t a16_full[2];       // e4m3: an fp16 slice is there (an arrival per converting warp)
+  uint64_t a16_full[2];       // e4m3: the fp16 weights are there (an arrival per converting warp)
   uint64_t a16_empty[2];      // and its products are done
   uint64_t acc_full[kMaxAcc];   // an accumulator is complete
   uint64_t acc_empty[kMaxAcc];  // and read (an arrival per epilogue warp)
@@ -81,6 +81,16 @@ __device__ __forceinline__ void mma_f16(uint32_t d, uint64_t a, uint64_t b, uint
       : "memory");
 }
 
+// The same with A in tensor memory: lane = row, a 32-bit column two elements.
+__device__ __forceinline__ void mma_f16_tmem(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
+                                             bool accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(static_cast<uint32_t>(accumulate))
+      : "memory");
+}
+
 // One lane of a converged warp.
 __device__ __forceinline__ bool elect_one() {
   uint32_t r;
@@ -94,17 +104,6 @@ __device__ __forceinline__ bool elect_one() {
 __device__ __forceinline__ void mma_commit(uint64_t* bar) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
                    smem_addr(bar))
-               : "memory");
-}
-
-// What this thread wrote to shared memory, for the tensor core's reads.
-__device__ __forceinline__ void fence_operands() {
-  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-}
-
-__device__ __forceinline__ void sts16(uint32_t p, const uint32_t (&v)[4]) {
-  asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]),
-               "r"(v[3])
                : "memory");
 }
 
@@ -166,7 +165,7 @@ struct ManyPhase {
   Barriers& b;
   const CUtensorMap* weights;
   const CUtensorMap* tokens;
-  uint32_t queue, a16;
+  uint32_t queue;
   int ring;               // stages
   uint32_t stage_bytes;
   int kd, limit, tiles, stages, nq;
@@ -185,9 +184,7 @@ struct ManyPhase {
     // the same stages in both phases
     const int n = boxed(min(b.max_tokens, kMaxN));
     stage_bytes = kWeightBytes + n * (FP8 ? 256 : 512);
-    const int room = static_cast<int>(kQueueBytes - (FP8 ? 2 * kA16Bytes : 0));
-    ring = min(room / static_cast<int>(stage_bytes), kMaxRing);
-    a16 = queue + static_cast<uint32_t>(kQueueBytes) - 2 * kA16Bytes;
+    ring = min(static_cast<int>(kQueueBytes / stage_bytes), kMaxRing);
   }
 
   // Columns of the products, and rows that the tensor copies fill.
@@ -305,8 +302,12 @@ struct ManyPhase {
 
   // -- converting warps (e4m3)
 
-  __device__ __forceinline__ bool convert(State& s, int tid) const {
-    const int row = tid / 8, c = tid % 8;
+  // Two warps a quarter of the rows, half the columns each; a thread has the
+  // row of its tensor-memory lane.
+  __device__ __forceinline__ bool convert(State& s, uint32_t tmem, int warp, int lane) const {
+    const int row = warp % 4 * 32 + lane, half = warp / 4 % 2;
+    const uint32_t mine = tmem + kAcc * kAccColumns + half * (kA16Columns / 2) +
+                          (static_cast<uint32_t>(warp % 4 * 32) << 16);
     for (;; ++s.job) {
       const int q = __shfl_sync(kFull, job(s.job), 0);
       if (q < 0) {
@@ -318,32 +319,19 @@ struct ManyPhase {
         if (!warp_wait(&b.landed[s.stage.slot], s.stage.parity) ||
             !warp_wait(&b.a16_empty[s.a16.slot], s.a16.parity ^ 1u))
           return false;
-        const uint32_t from = stage(s.stage.slot) + tid * 16;
-        const uint32_t to = a16 + s.a16.slot * kA16Bytes + (c >> 2) * kTileBytes + row * 128;
-        Vec16 v[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] = lds16(from + i * 4096);
+        tc_fence_after();
+        const uint32_t from = stage(s.stage.slot) + row * 128;
+        uint32_t h[32];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          uint32_t h[2][4];
+          const Vec16 v = lds16(from + (((half * 4 + i) ^ (row & 7)) << 4));
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
-            f16_of_e4m3(v[i].u[j], h[j / 2][j % 2 * 2], h[j / 2][j % 2 * 2 + 1]);
-          // lanes of the second half write their units the other way round, so
-          // that the 8 lanes of a row meet 8 different banks
-          const bool turn = c >= 4;
-#pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            const int unit = (c & 3) * 2 + (turn ? 1 - j : j);
-            uint32_t w[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) w[k] = turn ? h[1 - j][k] : h[j][k];
-            sts16(to + i * 4096 + ((unit ^ (row & 7)) << 4), w);
-          }
+          for (int j = 0; j < 4; ++j) f16_of_e4m3(v.u[j], h[i * 8 + j * 2], h[i * 8 + j * 2 + 1]);
         }
-        fence_operands();
+        tmem_st32(mine + s.a16.slot * kA16Columns, h);
+        tc_fence_before();
         __syncwarp();
-        if ((tid & 31) == 0) mbar_arrive(&b.a16_full[s.a16.slot]);
+        if (lane == 0) mbar_arrive(&b.a16_full[s.a16.slot]);
         s.a16.step(2);
         s.stage.step(ring);
       }
@@ -381,14 +369,17 @@ struct ManyPhase {
           const uint32_t d = tmem + s.acc.slot * kAccColumns;
           const uint32_t at = stage(s.stage.slot);
           const uint64_t x = sw128_desc(at + kWeightBytes);
-          const uint64_t w = sw128_desc(FP8 ? a16 + s.a16.slot * kA16Bytes : at);
+          const uint64_t w = sw128_desc(at);
+          const uint32_t w16 = tmem + kAcc * kAccColumns + s.a16.slot * kA16Columns;
           if (elect_one()) {
 #pragma unroll
             for (int i = 0; i < 2; ++i)
 #pragma unroll
-              for (int k = 0; k < 4; ++k)
-                mma_f16(d, w + i * (kTileBytes / 16) + k * 2, x + i * x_next + k * 2, idesc,
-                        (!FP8 && kb > 0) || i + k > 0);
+              for (int k = 0; k < 4; ++k) {
+                const uint64_t tokens = x + i * x_next + k * 2;
+                if (FP8) mma_f16_tmem(d, w16 + (i * 4 + k) * 8, tokens, idesc, i + k > 0);
+                else mma_f16(d, w + i * (kTileBytes / 16) + k * 2, tokens, idesc, kb > 0 || i + k > 0);
+              }
             if (FP8) mma_commit(&b.a16_empty[s.a16.slot]);
             mma_commit(&b.empty[s.stage.slot]);
             if (FP8 || kb == stages - 1) mma_commit(&b.acc_full[s.acc.slot]);
@@ -536,7 +527,7 @@ struct ManyPhase {
     else if (warp == kMmaWarp) ok = products(s, tmem);
     else if (warp == kWeightWarp) ok = lane != 0 || load_weights(s, ahead);
     else if (warp < kTokenWarp + kTokenWarps) ok = lane != 0 || load_tokens(s, warp - kTokenWarp);
-    else if (FP8) ok = convert(s, threadIdx.x - kFirstConvertWarp * 32);
+    else if (FP8) ok = convert(s, tmem, warp, lane);
     if (!ok) raise_flag(a.flags, MOE_DEVERR_TIMEOUT);
     __syncwarp();
     return __syncthreads_and(ok) != 0;
@@ -634,7 +625,9 @@ __device__ __forceinline__ bool layer_body(const LayerArgs& a, const Groups& g, 
 template <bool FP8>
 __global__ void __launch_bounds__(kThreads, 1) layer_many_kernel(
     const __grid_constant__ Maps maps, LayerArgs a) {
-  constexpr uint32_t kColumns = ManyPhase<FP8, true>::kAcc * ManyPhase<FP8, true>::kAccColumns;
+  constexpr uint32_t kColumns = 512;
+  static_assert(ManyPhase<FP8, true>::kAcc * ManyPhase<FP8, true>::kAccColumns +
+                    (FP8 ? 2 * kA16Columns : 0) <= kColumns, "tensor memory budget");
   extern __shared__ __align__(16) uint8_t raw[];
   __shared__ int ok;
   __shared__ int place[MOE_MAX_TOPK + MOE_LAYER_MAX_SHARED];
@@ -697,15 +690,14 @@ __global__ void __launch_bounds__(kThreads, 1) layer_many_kernel(
 }
 
 // A tensor of 16-bit or 8-bit elements, innermost dimension first; boxes of 128
-// bytes by box[1], box[2], ...; `swizzled` as the products read them.
-bool encode(CUtensorMap* m, const void* base, bool bytes, bool swizzled, int rank,
+// bytes by box[1], box[2], ..., swizzled as the products read them.
+bool encode(CUtensorMap* m, const void* base, bool bytes, int rank,
             const cuuint64_t* dims, const cuuint64_t* strides, const cuuint32_t* box) {
   EncodeTiled fn = encode_fn();
   const cuuint32_t estr[5] = {1, 1, 1, 1, 1};
   return fn && fn(m, bytes ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank,
                   const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                  swizzled ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
-                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+                  CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 bool encode_maps(Maps* m, const LayerArgs& a, bool e4m3) {
@@ -726,10 +718,10 @@ bool encode_maps(Maps* m, const LayerArgs& a, bool e4m3) {
   const cuuint64_t da[3] = {I, rows, e4m3 ? 1ull : 2ull};
   const cuuint64_t sa[2] = {I * 2, rows * I * 2};
   const cuuint32_t bt[3] = {64, kBoxTokens, 1};
-  return encode(&m->w13, a.w13, e4m3, !e4m3, 5, d13, s13, b13) &&
-         encode(&m->w2, a.w2, e4m3, !e4m3, 3, d2, s2, b2) &&
-         encode(&m->x, a.y, false, true, 3, dx, sx, bt) &&
-         encode(&m->a, a.a, false, true, 3, da, sa, bt);
+  return encode(&m->w13, a.w13, e4m3, 5, d13, s13, b13) &&
+         encode(&m->w2, a.w2, e4m3, 3, d2, s2, b2) &&
+         encode(&m->x, a.y, false, 3, dx, sx, bt) &&
+         encode(&m->a, a.a, false, 3, da, sa, bt);
 }
 
 template <bool FP8>
