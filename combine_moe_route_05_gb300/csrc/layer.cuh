@@ -64,7 +64,7 @@ struct Groups {
 
 __host__ __device__ constexpr size_t up16(size_t b) { return (b + 15) / 16 * 16; }
 
-constexpr int kMaxWarps = 16;
+constexpr int kMaxWarps = 20;
 
 __host__ __device__ constexpr size_t groups_bytes(int T, int KS, int n_exp) {
   return 2 * up16(2ull * T * KS) + up16(2ull * n_exp) + 2 * up16(4ull * n_exp) +

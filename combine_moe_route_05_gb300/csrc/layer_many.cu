@@ -7,7 +7,8 @@
 // operand of tcgen05.mma and an expert's tokens (16 to 128 columns) the B
 // operand, both read from shared memory by the tensor core itself.
 //
-//   warps 0..3   epilogue: a thread per weight row (tensor-memory lane)
+//   warps 0..3, 16..19  epilogue: a thread per weight row (tensor-memory lane),
+//                half the columns each
 //   warp  4      issues the products
 //   warps 5..7   fill the queue by tensor copies: 5 weights, 6 and 7 tokens
 //                (a thread takes 80 ns for each copy it asks for)
@@ -34,10 +35,11 @@
 namespace moe {
 namespace {
 
-constexpr int kThreads = 512;
-constexpr int kEpilogueWarps = 4, kMmaWarp = 4, kWeightWarp = 5, kTokenWarp = 6, kTokenWarps = 2;
+constexpr int kThreads = 640;
+constexpr int kEpilogueWarps = 8, kSecondEpilogueWarp = 16, kMmaWarp = 4, kWeightWarp = 5, kTokenWarp = 6, kTokenWarps = 2;
 constexpr int kFirstConvertWarp = 8, kConvertWarps = 8;
-static_assert((kFirstConvertWarp + kConvertWarps) * 32 == kThreads, "roles");
+static_assert(kFirstConvertWarp + kConvertWarps == kSecondEpilogueWarp &&
+                  (kSecondEpilogueWarp + 4) * 32 == kThreads, "roles");
 constexpr int kTileRows = 128;
 constexpr uint32_t kTileBytes = kTileRows * 128;  // 128 bytes of each row
 constexpr int kBoxTokens = 32;                      // of a tensor copy
@@ -407,45 +409,41 @@ struct ManyPhase {
     s.acc.step(kAcc);
   }
 
-  // 16 columns (tokens n0 ..) of the warp's rows of the tile.
-  // factors (e4m3): lane l's entry l (n0 < 32) or 32 + l has this inverse factor.
+  // 16 columns (tokens n0 ..) of the warp's rows of the tile; lane n % 32 has
+  // the inverse factor of token n (e4m3).
   __device__ __forceinline__ void store16(const float (&v)[16], int n0, int cnt, int begin, int tile,
-                                          int warp, int lane, float factors) const {
-    const int KS = a.K + a.S;
+                                          int quarter, int lane, float factors) const {
     if (UP) {
-      const int o = tile * 64 + warp * 16 + (lane >> 4) * 8 + (lane & 7);
+      const int o = tile * 64 + quarter * 16 + (lane >> 4) * 8 + (lane & 7);
       const bool upper = lane & 8;
 #pragma unroll
       for (int j = 0; j < 16; j += 2) {
-        if (n0 + j >= cnt) break;  // uniform
         // lane l takes column j, lane l + 8 column j + 1
         const float other = __shfl_xor_sync(kFull, upper ? v[j] : v[j + 1], 8);
-        const float gate = upper ? other : v[j], up = upper ? v[j + 1] : other;
+        float gate = upper ? other : v[j], up = upper ? v[j + 1] : other;
         const int n = n0 + j + (upper ? 1 : 0);
-        const bool real = n < cnt && o < limit;
-        const int64_t at = static_cast<int64_t>(begin + min(n, cnt - 1)) * a.I + o;
         if (FP8) {
-          const int entry = g.order[begin + min(n, cnt - 1)];
           const float f = __shfl_sync(kFull, factors, n & 31);
-          const float h = act_value(gate * f, a.act) * (up * f);
-          if (real) a.a32[at] = h;
-          const uint32_t m = real ? __float_as_uint(h) & 0x7fffffffu : 0u;
-          const uint32_t m0 = __reduce_max_sync(kFull, upper ? 0u : m);
-          const uint32_t m1 = __reduce_max_sync(kFull, upper ? m : 0u);
-          // a maximum does not depend on the order
-          if ((lane & 23) == 0 && n < cnt) atomicMax(a.amax + entry, upper ? m1 : m0);
-        } else if (real) {
-          const float h = act_value(gate, a.act) * up;
+          gate *= f;
+          up *= f;
+        }
+        const float h = act_value(gate, a.act) * up;
+        if (n >= cnt || o >= limit) continue;
+        const int64_t at = static_cast<int64_t>(begin + n) * a.I + o;
+        if (FP8) {
+          a.a32[at] = h;
+        } else {
           const __nv_bfloat16 hi = __float2bfloat16_rn(h);
           const float rest = h - __bfloat162float(hi);
           __nv_bfloat16* dst = reinterpret_cast<__nv_bfloat16*>(a.a) + at;
           dst[0] = hi;
-          dst[static_cast<int64_t>(a.T) * KS * a.I] = __float2bfloat16_rn(isfinite(rest) ? rest : 0.0f);
+          dst[static_cast<int64_t>(a.T) * (a.K + a.S) * a.I] =
+              __float2bfloat16_rn(isfinite(rest) ? rest : 0.0f);
         }
       }
       return;
     }
-    const int row = tile * 128 + warp * 32 + lane;
+    const int row = tile * 128 + quarter * 32 + lane;
 #pragma unroll
     for (int j = 0; j < 16; ++j) {
       const float f = FP8 ? __shfl_sync(kFull, factors, (n0 + j) & 31) : 1.0f;
@@ -454,8 +452,11 @@ struct ManyPhase {
     }
   }
 
-  __device__ __forceinline__ bool epilogue(State& s, uint32_t tmem, int warp, int lane) const {
-    const uint32_t mine = tmem + (static_cast<uint32_t>(warp * 32) << 16);
+  // Warp `quarter` of set `set`: the first or second half of the columns, in
+  // steps of 16.
+  __device__ __forceinline__ bool epilogue(State& s, uint32_t tmem, int set, int quarter,
+                                           int lane) const {
+    const uint32_t mine = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
     for (;; ++s.job) {
       const int q = __shfl_sync(kFull, job(s.job), 0);
       if (q < 0) {
@@ -465,46 +466,44 @@ struct ManyPhase {
       const int slot = q / tiles, tile = q - slot * tiles, p = g.slot_expert[slot];
       for (int c0 = 0; c0 < g.cnt[p]; c0 += kMaxN) {
         const int cnt = min(g.cnt[p] - c0, kMaxN), begin = g.start[p] + c0;
+        const int half = (columns(cnt) / 16 + 1) / 2 * 16;
+        const int first = set * half, last = min(first + half, cnt);
         if (FP8) {
-          const int r = weight_row(tile, warp * 32 + lane);
+          static_assert(!FP8 || kMaxN <= 64, "32 columns a set");
+          const int r = weight_row(tile, quarter * 32 + lane);
           const int64_t row = static_cast<int64_t>(expert(slot)) * (((UP ? 2 * a.I : a.H) + 127) / 128) + r / 128;
           const float* scale = (UP ? a.s13 : a.s2) + row * stages;
-          // what undoes the factors of the columns, two a lane
-          uint32_t held[2];
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const int entry = g.order[begin + min(i * 32 + lane, cnt - 1)];
-            held[i] = UP ? __ldcg(reinterpret_cast<const uint32_t*>(a.xscale) + entry / (a.K + a.S))
-                         : __ldcg(a.amax + entry);
-          }
-          float sum[kMaxN / 16][16] = {};
+          // what undoes the factor of column first + lane
+          const int entry = g.order[begin + min(first + lane, cnt - 1)];
+          const float factor = __ldcg((UP ? a.xscale + entry / (a.K + a.S)
+                                          : reinterpret_cast<const float*>(a.amax) + entry));
+          float sum[2][16] = {};
           float next = __ldg(scale);
           for (int kb = 0; kb < stages; ++kb) {
             const float f = next;
             if (kb + 1 < stages) next = __ldg(scale + kb + 1);
             if (!acc_ready(s)) return false;
+            if (first < cnt) {
+              uint32_t v[32];
+              tmem_ld32(mine + s.acc.slot * kAccColumns + first, v);
+              acc_read(s, lane);
 #pragma unroll
-            for (int c = 0; c < kMaxN / 16; c += 2)
-              if (c * 16 < cnt) {
-                uint32_t v[32];
-                tmem_ld32(mine + s.acc.slot * kAccColumns + c * 16, v);
-#pragma unroll
-                for (int j = 0; j < 32; ++j)
-                  sum[c + j / 16][j % 16] = fmaf(f, __uint_as_float(v[j]), sum[c + j / 16][j % 16]);
-              }
-            acc_read(s, lane);
-          }
-#pragma unroll
-          for (int c = 0; c < kMaxN / 16; ++c)
-            if (c * 16 < cnt) {
-              const uint32_t bits = held[c / 2];
-              store16(sum[c], c * 16, cnt, begin, tile, warp, lane,
-                      UP ? __uint_as_float(bits) : 1.0f / f16_factor(bits));
+              for (int j = 0; j < 32; ++j)
+                sum[j / 16][j % 16] = fmaf(f, __uint_as_float(v[j]), sum[j / 16][j % 16]);
+            } else {
+              acc_read(s, lane);
             }
+          }
+          // (a lane of the factors is a column modulo 32 from `first` on)
+          const float turned = __shfl_sync(kFull, factor, (lane - first) & 31);
+#pragma unroll
+          for (int c = 0; c < 2; ++c)
+            if (first + c * 16 < last)
+              store16(sum[c], first + c * 16, cnt, begin, tile, quarter, lane, turned);
         } else {
           if (!acc_ready(s)) return false;
 #pragma unroll 1
-          for (int n0 = 0; n0 < cnt; n0 += 16) {
+          for (int n0 = first; n0 < last; n0 += 16) {
             uint32_t v[16], low[16];
             tmem_ld16(mine + s.acc.slot * kAccColumns + n0, v);
             if (kLow) tmem_ld16(mine + s.acc.slot * kAccColumns + boxed(cnt) + n0, low);
@@ -512,7 +511,7 @@ struct ManyPhase {
 #pragma unroll
             for (int j = 0; j < 16; ++j)
               f[j] = kLow ? __uint_as_float(v[j]) + __uint_as_float(low[j]) : __uint_as_float(v[j]);
-            store16(f, n0, cnt, begin, tile, warp, lane, 1.0f);
+            store16(f, n0, cnt, begin, tile, quarter, lane, 1.0f);
           }
           acc_read(s, lane);
         }
@@ -523,7 +522,7 @@ struct ManyPhase {
   __device__ __forceinline__ bool run(State& s, int ahead, uint32_t tmem) const {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     bool ok = true;
-    if (warp < kEpilogueWarps) ok = epilogue(s, tmem, warp, lane);
+    if (warp < 4 || warp >= kSecondEpilogueWarp) ok = epilogue(s, tmem, warp / 16, warp % 4, lane);
     else if (warp == kMmaWarp) ok = products(s, tmem);
     else if (warp == kWeightWarp) ok = lane != 0 || load_weights(s, ahead);
     else if (warp < kTokenWarp + kTokenWarps) ok = lane != 0 || load_tokens(s, warp - kTokenWarp);
@@ -547,7 +546,6 @@ __device__ __forceinline__ void sort_tokens(const LayerArgs& a, const Groups& g,
     if (static_cast<int>(threadIdx.x) < KS) {
       const int entry = t * KS + threadIdx.x;
       place[threadIdx.x] = g.rank[entry] == kNone ? -1 : g.start[expert_of(a, entry)] + g.rank[entry];
-      if (FP8) a.amax[entry] = 0;
     }
     float f = 1.0f;
     if (FP8) {
@@ -567,14 +565,24 @@ __device__ __forceinline__ void sort_tokens(const LayerArgs& a, const Groups& g,
   }
 }
 
-// fp16 copies of the activations, their factors from the entries' maxima.
+// fp16 copies of the activations, a warp per row: its factor from its largest
+// value, and what undoes it in place of the maximum.
 __device__ __forceinline__ void scale_sorted(const LayerArgs& a, const Groups& g, int rows) {
-  const int per = a.I / 8;
-  const int64_t n = static_cast<int64_t>(rows) * per;
-  for (int64_t i = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x; i < n;
-       i += static_cast<int64_t>(gridDim.x) * kThreads) {
-    const int r = static_cast<int>(i / per);
-    scale_activation(a, i, __ldcg(a.amax + g.order[r]));
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  for (int r = warp * gridDim.x + blockIdx.x; r < rows; r += gridDim.x * (kThreads / 32)) {
+    const int64_t at = static_cast<int64_t>(r) * (a.I / 8);
+    const uint4* src = reinterpret_cast<const uint4*>(a.a32 + static_cast<int64_t>(r) * a.I);
+    uint32_t m = 0;
+#pragma unroll 4
+    for (int v = lane; v < a.I / 4; v += 32) {
+      const uint4 x = __ldcg(src + v);
+      m = max(max(m, max(x.x & 0x7fffffffu, x.y & 0x7fffffffu)),
+              max(x.z & 0x7fffffffu, x.w & 0x7fffffffu));
+    }
+    m = __reduce_max_sync(kFull, m);
+#pragma unroll 2
+    for (int v = lane; v < a.I / 8; v += 32) scale_activation(a, at + v, m);
+    if (lane == 0) reinterpret_cast<float*>(a.amax)[g.order[r]] = 1.0f / f16_factor(m);
   }
 }
 
