@@ -483,7 +483,13 @@ struct ManyPhase {
             const float f = next;
             if (kb + 1 < stages) next = __ldg(scale + kb + 1);
             if (!acc_ready(s)) return false;
-            if (first < cnt) {
+            if (first < cnt && half == 16) {
+              uint32_t v[16];
+              tmem_ld16(mine + s.acc.slot * kAccColumns + first, v);
+              acc_read(s, lane);
+#pragma unroll
+              for (int j = 0; j < 16; ++j) sum[0][j] = fmaf(f, __uint_as_float(v[j]), sum[0][j]);
+            } else if (first < cnt) {
               uint32_t v[32];
               tmem_ld32(mine + s.acc.slot * kAccColumns + first, v);
               acc_read(s, lane);
