@@ -84,36 +84,23 @@ __device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uin
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// A unit of WM warps shares a part of a job's k and its token rows; each warp
-// has MT tiles of 16 weight rows by NT tiles of up to 8 tokens.  A stage of the
-// queue holds STEPS steps of 64 bytes of each row.
-template <int THREADS_, int WM_, int MT_, int NT_, int STEPS_, int QUEUE_KB_, bool FP8_, bool PACKED_>
-struct Shape {
-  static constexpr int kQueueBytes = QUEUE_KB_ * 1024;
-  static constexpr int kThreads = THREADS_, kWarps = THREADS_ / 32;
-  static constexpr int WM = WM_, MT = MT_, NT = NT_, kSteps = STEPS_;
-  static constexpr int kTiles = WM * MT, kUnits = kWarps / WM;
-  static constexpr int kMaxTeam = kUnits < 8 ? kUnits : 8;
-  static constexpr bool FP8 = FP8_, kPacked = PACKED_;
-  // a in two bf16 parts; with many tokens in one, whose copies and products
-  // would bound the down phase twice over
-  static constexpr bool kSplit = NT == 1;
-  static_assert(!kPacked || MT * NT == 1, "packed");
-  static constexpr int kRed = MT * NT == 1 ? 2 : 1;  // buffers of partial sums
-  static constexpr int kAtOnce = NT > 1 ? 2 : 1;     // token tiles in a buffer
-  static_assert(NT % kAtOnce == 0, "sums");
-  static constexpr int kRedFloats = kWarps * kAtOnce * 4 * 32;
-  static constexpr int kMaxStages = 8;
-  // behind the queue: partial sums, tickets, block scales of the stages
-  static constexpr int kRedBytes = kRed * kRedFloats * 4;
-  static constexpr int kTicketBytes = kWarps * kTickets * 4;
-  static constexpr int kScaleBytes = FP8 ? kWarps * kMaxStages * 2 * MT * 4 : 0;
-  static constexpr size_t kFixedBytes = kQueueBytes + kRedBytes + kTicketBytes + kScaleBytes;
-  static constexpr size_t smem(int T, int KS, int n_exp) { return kFixedBytes + groups_bytes(T, KS, n_exp); }
-  static_assert(kWarps <= kMaxWarps, "warps");
-  static_assert(smem(MOE_LAYER_MAX_TOKENS, MOE_MAX_TOPK + MOE_LAYER_MAX_SHARED, kMaxExperts) <=
-                    227 * 1024, "shared memory budget");
-};
+// The products of one phase (up or down) for one thread.  PACKED: 4 tokens to a
+// tile of 8, so that more of the queue holds weights.
+constexpr int kWarps = 16, kThreads = 32 * kWarps;
+static_assert(kWarps <= kMaxWarps, "warps");
+constexpr int kMaxTeam = 8;
+constexpr int kSteps = 2;  // of 64 bytes of a row, in a stage of the queue
+constexpr int kQueueBytes = 192 * 1024;
+constexpr int kMaxStages = 8;
+// behind the queue: two buffers of partial sums, tickets, block scales of the
+// stages (e4m3)
+constexpr int kSumFloats = kWarps * 4 * 32;
+constexpr int kSumBytes = 2 * kSumFloats * 4;
+constexpr int kTicketBytes = kWarps * kTickets * 4;
+constexpr int kScaleBytes = kWarps * kMaxStages * 2 * 4;
+constexpr size_t kFixedBytes = kQueueBytes + kSumBytes + kTicketBytes + kScaleBytes;
+static_assert(kFixedBytes + groups_bytes(MOE_LAYER_MAX_TOKENS, MOE_MAX_TOPK + MOE_LAYER_MAX_SHARED,
+                                         kMaxExperts) + 64 <= 227 * 1024, "shared memory budget");
 
 // Tokens [c0, c0 + kTokens) of the expert in slot `slot`, output tile `tile`;
 // q = slot * tiles + tile, i its place in the team's sequence.
@@ -121,104 +108,100 @@ struct Job {
   int i, q, slot, tile, c0;
 };
 
-// The products of one phase (up or down) for one thread.
-template <typename S, bool UP>
+template <bool FP8, bool PACKED, bool UP>
 struct Phase {
-  static constexpr int WM = S::WM, MT = S::MT, NT = S::NT, kTiles = S::kTiles, kUnits = S::kUnits;
-  static constexpr int kAtOnce = S::kAtOnce;
-  static constexpr bool FP8 = S::FP8;
+  static_assert(PACKED || !FP8, "e4m3 comes packed");
   static constexpr int kEb = FP8 ? 1 : 2;
-  static constexpr int kRowBytes = 64 * S::kSteps;  // of a weight row in a stage
-  static constexpr int kRows = UP ? 8 : 16;         // outputs that 16 weight rows give
-  // Packed: 4 tokens to a tile, so that more of the queue holds weights.
-  // bf16: rows (and columns) 4..7 of the tile are the low parts of rows 0..3,
-  // one product for both, added at the end.
-  static constexpr bool kPacked = S::kPacked && (FP8 || !UP);
+  static constexpr int kRowBytes = 64 * kSteps;  // of a weight row in a stage
+  static constexpr int kRows = UP ? 8 : 16;      // outputs that 16 weight rows give
+  // The low parts of a in bf16.  Packed: as rows (and columns) 4..7 of the tile,
+  // one product for both, added at the end; else behind the tile.
+  static constexpr bool kPacked = PACKED && (FP8 || !UP);
   static constexpr bool kLowColumns = kPacked && !FP8;
-  static constexpr int kTokens = kPacked ? 4 : 8 * NT;      // of a job
-  static constexpr bool kLowRows = !UP && !FP8 && S::kSplit && !kPacked;  // behind the tiles
-  static constexpr int kTokenRows = kPacked && FP8 ? 4 : NT * 8 * (kLowRows ? 2 : 1);
-  static constexpr int kTokenBytes = kRowBytes * 2 / kEb;   // of a token row in a stage
-  static constexpr int kLoads = FP8 || kLowRows ? 2 : 1;    // 16-byte vectors of a lane and step
+  static constexpr bool kLowRows = !UP && !PACKED;
+  static constexpr int kTokens = kPacked ? 4 : 8;  // of a job
+  static constexpr int kTokenRows = FP8 ? 4 : kLowRows ? 16 : 8;
+  static constexpr int kTokenBytes = kRowBytes * 2 / kEb;  // of a token row in a stage
+  static constexpr int kLoads = FP8 || kLowRows ? 2 : 1;   // 16-byte vectors of a lane and step
   // lanes along a row, and rows, of one copy instruction
   static constexpr int kAcross = kRowBytes / 16, kDown = 32 / kAcross;
   static constexpr int kTokenAcross = kTokenBytes / 16, kTokenDown = 32 / kTokenAcross;
-  static constexpr int kTokenCopies = kTokenRows / kTokenDown / WM;
-  static constexpr int kWeightBytes = kTiles * 16 * kRowBytes;  // of a unit's stage
-  static constexpr int kUnitBytes = kWeightBytes + kTokenRows * kTokenBytes;
-  static constexpr int kStageBytes = kUnits * kUnitBytes;
-  static constexpr int kStages = S::kQueueBytes / kStageBytes < S::kMaxStages ? S::kQueueBytes / kStageBytes
-                                                                              : S::kMaxStages;
+  static constexpr int kTokenCopies = kTokenRows / kTokenDown;
+  static constexpr int kWeightBytes = 16 * kRowBytes;  // of a warp's stage
+  static constexpr int kWarpBytes = kWeightBytes + kTokenRows * kTokenBytes;
+  static constexpr int kStageBytes = kWarps * kWarpBytes;
+  static constexpr int kStages = kQueueBytes / kStageBytes < kMaxStages ? kQueueBytes / kStageBytes
+                                                                        : kMaxStages;
   // an instruction's rows begin at an even one, and weights end on 128 bytes
-  static_assert(kTokenRows % (kTokenDown * WM) == 0 && 8 % kDown == 0 && kDown % 2 == 0 && kTokenDown % 2 == 0 &&
-                    kWeightBytes % 128 == 0, "copies");
+  static_assert(kTokenRows % kTokenDown == 0 && 8 % kDown == 0 && kDown % 2 == 0 &&
+                    kTokenDown % 2 == 0 && kWeightBytes % 128 == 0, "copies");
   static_assert(kStages >= 3, "queue");
 
   const LayerArgs& a;
   const Groups& g;
-  uint32_t queue;   // shared-memory address of this unit's queue
+  uint32_t queue;   // shared-memory address of this warp's queue
   uint32_t scales;  // of the warp's block scales
   // this lane's places in a stage: where it copies to and loads from
   uint32_t copy_weight, copy_token, load_weight, load_token;
   int kd, tiles, limit, stages, nq;
-  int lane, warp, unit, mine;  // mine: the warp's first row tile in its unit
-  int team, part, first_q, stride_q;  // units that split a job's k
+  int lane, warp;
+  int team, part, first_q, stride_q;  // warps that split a job's k
   int fixed;       // jobs of a team that are dealt out beforehand
   int* tickets;    // the team's others
   uint32_t* given;
 
   __device__ __forceinline__ Phase(const LayerArgs& args, const Groups& groups, uint8_t* smem)
       : a(args), g(groups), lane(threadIdx.x & 31), warp(threadIdx.x >> 5) {
-    unit = warp / WM;
-    mine = warp % WM * MT;
-    queue = smem_addr(smem) + unit * kUnitBytes;
-    scales = smem_addr(smem) + S::kQueueBytes + S::kRedBytes + S::kTicketBytes + warp * S::kMaxStages * 2 * MT * 4;
+    queue = smem_addr(smem) + warp * kWarpBytes;
+    scales = smem_addr(smem) + kQueueBytes + kSumBytes + kTicketBytes + warp * kMaxStages * 2 * 4;
     {
       const int row = lane / kAcross, token = lane / kTokenAcross, odd = (lane >> 2) & 1;
-      copy_weight = (mine * 16 + row) * kRowBytes + ((lane % kAcross * 16) ^ (row % 2 * kTurn));
-      copy_token = kWeightBytes + (warp % WM * kTokenCopies * kTokenDown + token) * kTokenBytes + ((lane % kTokenAcross * 16) ^ (token % 2 * kTokenTurn));
-      load_weight = (mine * 16 + (lane >> 2)) * kRowBytes + (((lane & 3) * 16) ^ (odd * kTurn));
-      load_token = kWeightBytes + (lane >> 2) * kTokenBytes + (((lane & 3) * (FP8 ? 32 : 16)) ^ (odd * kTokenTurn));
+      copy_weight = row * kRowBytes + ((lane % kAcross * 16) ^ (row % 2 * kTurn));
+      copy_token = kWeightBytes + token * kTokenBytes +
+                   ((lane % kTokenAcross * 16) ^ (token % 2 * kTokenTurn));
+      load_weight = (lane >> 2) * kRowBytes + (((lane & 3) * 16) ^ (odd * kTurn));
+      load_token = kWeightBytes + (lane >> 2) * kTokenBytes +
+                   (((lane & 3) * (FP8 ? 32 : 16)) ^ (odd * kTokenTurn));
     }
     kd = UP ? a.H : a.I;
     limit = UP ? a.I : a.H;
-    tiles = (limit + kRows * kTiles - 1) / (kRows * kTiles);
+    tiles = (limit + kRows - 1) / kRows;
     stages = (kd * kEb + kRowBytes - 1) / kRowBytes;
     nq = g.nslots * tiles;
     // Many jobs: a larger team makes them shorter, so that they even out at the
     // end what the SMs differ in speed, but has fewer stages between the
-    // barriers at their ends.  A team grows while each of its units keeps 8
+    // barriers at their ends.  A team grows while each of its warps keeps 8
     // stages and it has less than 64 jobs, or 4 stages and 20 jobs (37 of 64
     // tokens e4m3, DeepSeek-V3 shape: 1375 us with 4 stages and no count of
     // jobs, 1279 so; 16 tokens, Qwen3-30B shape: 139 us with 8 stages alone, 133
-    // so).  Few: the team size with the fewest rounds over the grid, in units
+    // so).  Few: the team size with the fewest rounds over the grid, in rounds
     // of a job of one.
-    const int units = kUnits * gridDim.x;
+    const int warps = kWarps * gridDim.x;
     team = 1;
-    if (nq >= units / S::kMaxTeam * 6) {
-      const auto grows = [&](int per_unit, int64_t jobs) {
-        return 2 * per_unit * team <= stages && static_cast<int64_t>(nq) * team < jobs * units;
+    if (nq >= warps / kMaxTeam * 6) {
+      const auto grows = [&](int per_warp, int64_t jobs) {
+        return 2 * per_warp * team <= stages && static_cast<int64_t>(nq) * team < jobs * warps;
       };
-      while (team < S::kMaxTeam && (grows(8, 64) || grows(4, 20))) team *= 2;
+      while (team < kMaxTeam && (grows(8, 64) || grows(4, 20))) team *= 2;
     } else {
       float best = 0.0f;
 #pragma unroll 1
-      for (int n = 1; n <= S::kMaxTeam && n <= stages; n *= 2) {
-        const float cost = static_cast<float>((nq * n + units - 1) / units) / n;
+      for (int n = 1; n <= kMaxTeam && n <= stages; n *= 2) {
+        const float cost = static_cast<float>((nq * n + warps - 1) / warps) / n;
         if (n == 1 || cost < best) {
           best = cost;
           team = n;
         }
       }
     }
-    first_q = blockIdx.x + gridDim.x * (unit / team);
-    stride_q = gridDim.x * (kUnits / team);
-    part = unit % team;
+    first_q = blockIdx.x + gridDim.x * (warp / team);
+    stride_q = gridDim.x * (kWarps / team);
+    part = warp % team;
     // the copies of a warp run at most (per - 1 + kStages) / per jobs ahead,
     // and a ticket is there from the second job behind its request on
     const int per = stages / team;
     fixed = (per - 1 + kStages) / per + 1;
-    tickets = reinterpret_cast<int*>(smem + S::kQueueBytes + S::kRedBytes) + unit / team * kTickets;
+    tickets = reinterpret_cast<int*>(smem + kQueueBytes + kSumBytes) + warp / team * kTickets;
     given = a.arrived + kBarriers + (UP ? 0 : 1);
   }
 
@@ -232,17 +215,11 @@ struct Phase {
     if (j.c0 + kTokens < g.cnt[g.slot_expert[j.slot]]) return Job{j.i, j.q, j.slot, j.tile, j.c0 + kTokens};
     return at(j.i + 1);
   }
-  // The first output of the warp's tile mt, and whether there is one.
-  __device__ __forceinline__ int first_row(const Job& j, int mt) const {
-    return (j.tile * kTiles + mine + mt) * kRows;
-  }
-  __device__ __forceinline__ bool has_rows(const Job& j, int mt) const {
-    return kTiles == 1 || first_row(j, mt) < limit;
-  }
+  __device__ __forceinline__ int first_row(const Job& j) const { return j.tile * kRows; }
   // Odd rows have two halves of their 16-byte units changed over (bit 2 of a
   // unit's number, e4m3 tokens: bit 0), so that the 8 lanes of a shared-memory
   // access, 4 each of two rows, meet no bank twice.
-  static constexpr int kTurn = S::kSteps == 2 ? 64 : 0, kTokenTurn = FP8 ? 16 : kTurn;
+  static constexpr int kTurn = 64, kTokenTurn = FP8 ? 16 : kTurn;
 
   // Where this warp's next copies come from.  A copy instruction takes kDown
   // rows of kRowBytes: whole 128-byte lines of few rows (16 rows by 64 bytes
@@ -254,22 +231,22 @@ struct Phase {
     int64_t half;           // from rows 0..7 of a tile to rows 8..15
     const uint8_t* col[kTokenCopies];  // this lane's places in rows of x or a
     uint32_t have;          // bit i: there is a row in col[i]
-    const float* scale;     // the block scales' row of lanes 0 .. 2 MT - 1
+    const float* scale;     // the block scales' row of lanes 0 and 1
   };
 
   __device__ __forceinline__ void open(Cursor& c) const {
     if (!valid(c.j)) return;
     const int p = g.slot_expert[c.j.slot];
     const int e = p < a.S ? a.E + p : p - a.S;
-    const int r0 = has_rows(c.j, 0) ? first_row(c.j, 0) : 0;  // of no outputs: any rows
+    const int r0 = first_row(c.j);
     const int64_t all_rows = UP ? 2 * a.I : a.H;
     c.o = part * kRowBytes;
     c.row = (UP ? a.w13 : a.w2) + (e * all_rows + r0 + lane / kAcross) * kd * kEb + c.o + lane % kAcross * 16;
     // the last tile of the down products may have no second half: it reads
     // the first again, and its results go nowhere
-    c.half = static_cast<int64_t>(UP ? a.I : kTiles == 1 && r0 + 8 >= limit ? 0 : 8) * kd * kEb;
-    if (FP8 && lane < 2 * MT) {
-      const int r = min(r0 + lane / 2 * kRows, limit - 8) + (UP && lane % 2 ? a.I : 0);
+    c.half = static_cast<int64_t>(UP ? a.I : r0 + 8 >= limit ? 0 : 8) * kd * kEb;
+    if (FP8 && lane < 2) {
+      const int r = r0 + (UP && lane ? a.I : 0);
       c.scale = (UP ? a.s13 : a.s2) + (e * ((all_rows + 127) / 128) + r / 128) * ((kd + 127) / 128);
     }
     const int cnt = min(g.cnt[p] - c.j.c0, kTokens), begin = g.start[p] + c.j.c0;
@@ -278,13 +255,14 @@ struct Phase {
     c.have = 0;
 #pragma unroll
     for (int i = 0; i < kTokenCopies; ++i) {
-      const int row = (warp % WM * kTokenCopies + i) * kTokenDown + lane / kTokenAcross;
-      const bool low = kLowColumns ? row >= 4 : kLowRows && row >= NT * 8;
-      const int n = kLowColumns ? row & 3 : low ? row - NT * 8 : row;
+      const int row = i * kTokenDown + lane / kTokenAcross;
+      const bool low = kLowColumns ? row >= 4 : kLowRows && row >= 8;
+      const int n = kLowColumns ? row & 3 : row & 7;
       c.col[i] = src;
       if (n < cnt) {
         const int entry = g.order[begin + n];
-        c.col[i] += static_cast<int64_t>((UP ? entry / (a.K + a.S) : entry) + (low ? a.T * (a.K + a.S) : 0)) * kd * 2;
+        c.col[i] += static_cast<int64_t>((UP ? entry / (a.K + a.S) : entry) +
+                                         (low ? a.T * (a.K + a.S) : 0)) * kd * 2;
         c.have |= 1u << i;
       }
     }
@@ -313,21 +291,12 @@ struct Phase {
     const int64_t down = static_cast<int64_t>(kDown) * kd * kEb;
     dst += copy_weight;
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt) {
-      // a tile (or its second half) without outputs reads the first again
-      const bool rows = has_rows(c.j, mt);
-      const bool second = UP || kTiles == 1 || first_row(c.j, mt) + 8 < limit;
-      const uint8_t* tile = c.row + (rows ? static_cast<int64_t>(mt * kRows) * kd * kEb : 0);
+    for (int h = 0; h < 2; ++h)
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const uint8_t* p = tile + (h && second ? c.half : 0);
-#pragma unroll
-        for (int i = 0; i < 8 / kDown; ++i)
-          copy16_stream(dst + (mt * 16 + h * 8 + i * kDown) * kRowBytes, p + i * down, in);
-      }
-    }
-    if (FP8 && lane < 2 * MT)
-      copy4(scales + ((dst - copy_weight - queue) / kStageBytes * 2 * MT + lane) * 4, c.scale + c.o / 128);
+      for (int i = 0; i < 8 / kDown; ++i)
+        copy16_stream(dst + (h * 8 + i * kDown) * kRowBytes, c.row + (h ? c.half : 0) + i * down, in);
+    if (FP8 && lane < 2)
+      copy4(scales + ((dst - copy_weight - queue) / kStageBytes * 2 + lane) * 4, c.scale + c.o / 128);
   }
   __device__ __forceinline__ void copy_tokens(const Cursor& c, uint32_t dst) const {
     const bool in = c.o * (2 / kEb) + lane % kTokenAcross * 16 < kd * 2;
@@ -337,106 +306,86 @@ struct Phase {
       copy16_keep(dst + i * kTokenDown * kTokenBytes, c.col[i], in, (c.have >> i) & 1u);
   }
 
-  // The token (of the job) that this lane's operand holds in tile nt.
-  __device__ __forceinline__ int lane_token(int nt) const {
-    return kLowColumns ? (lane >> 2) & 3 : nt * 8 + (lane >> 2);
+  // The token (of the job) that this lane's operand holds.
+  __device__ __forceinline__ int lane_token() const {
+    return kLowColumns ? (lane >> 2) & 3 : lane >> 2;
   }
 
   // One stage's operands.
   struct Operands {
-    Vec16 w[S::kSteps][MT][2];
-    Vec16 x[S::kSteps][NT][kLoads];
-    float sc[MT][2];  // block scales of the lane's accumulator rows
+    Vec16 w[kSteps][2];
+    Vec16 x[kSteps][kLoads];
+    float sc[2];  // block scales of the lane's accumulator rows
   };
 
-  // has: bit nt: the lane has a token in tile nt (without one its operand
-  // registers, and the columns of its sums, mean nothing).
-  __device__ __forceinline__ void load(Operands& v, uint32_t at, uint32_t has) const {
+  // has: the lane has a token (without one its operand registers, and the
+  // columns of its sums, mean nothing).
+  __device__ __forceinline__ void load(Operands& v, uint32_t at, bool has) const {
 #pragma unroll
-    for (int st = 0; st < S::kSteps; ++st) {
+    for (int st = 0; st < kSteps; ++st) {
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
+      for (int i = 0; i < kLoads; ++i) {
+        const uint32_t from =
+            FP8 ? (load_token ^ (i * kTokenTurn)) + st * 128 : load_token ^ (st * kTokenTurn);
+        lds16_if(v.x[st][i], at + from + (kLowRows ? i * 8 : 0) * kTokenBytes, has);
+      }
 #pragma unroll
-        for (int i = 0; i < kLoads; ++i) {
-          const uint32_t from = FP8 ? (load_token ^ (i * kTokenTurn)) + st * 128 : load_token ^ (st * kTokenTurn);
-          lds16_if(v.x[st][nt][i], at + from + (nt * 8 + (kLowRows ? i * NT * 8 : 0)) * kTokenBytes, (has >> nt) & 1u);
-        }
-#pragma unroll
-      for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-          v.w[st][mt][h] = lds16(at + (load_weight ^ (st * kTurn)) + (mt * 16 + h * 8) * kRowBytes);
+      for (int h = 0; h < 2; ++h)
+        v.w[st][h] = lds16(at + (load_weight ^ (st * kTurn)) + h * 8 * kRowBytes);
     }
     if (FP8) {
 #pragma unroll
-      for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-          v.sc[mt][h] = lds4(scales + ((at - queue) / kStageBytes * 2 * MT + mt * 2 + h) * 4);
+      for (int h = 0; h < 2; ++h) v.sc[h] = lds4(scales + ((at - queue) / kStageBytes * 2 + h) * 4);
     }
   }
 
   // Sums that run beside each other, so that a product need not wait for the
   // one before it; added at the end of a job (bf16) or a stage (e4m3).
-  static constexpr int kChains = MT * NT > 1 ? 1 : FP8 ? 2 : 4;
+  static constexpr int kChains = FP8 ? 2 : 4;
 
   // acc += the products of one stage.
-  __device__ __forceinline__ void multiply(float (&acc)[kChains][MT][NT][4], const Operands& v) const {
+  __device__ __forceinline__ void multiply(float (&acc)[kChains][4], const Operands& v) const {
+    float sum[kChains][4] = {};
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt) {
-      float sum[FP8 ? kChains : 1][NT][4] = {};
+    for (int st = 0; st < kSteps; ++st) {
+      const Vec16& w0 = v.w[st][0];
+      const Vec16& w1 = v.w[st][1];
+      if (!FP8) {
 #pragma unroll
-      for (int st = 0; st < S::kSteps; ++st) {
-        const Vec16& w0 = v.w[st][mt][0];
-        const Vec16& w1 = v.w[st][mt][1];
-        if (!FP8) {
+        for (int q = 0; q < 4; q += 2)
 #pragma unroll
-          for (int q = 0; q < 4; q += 2)
+          for (int i = 0; i < kLoads; ++i)
+            mma<false>(acc[(q / 2 + st * 2) % kChains], w0.u[q], w1.u[q], w0.u[q + 1], w1.u[q + 1],
+                       v.x[st][i].u[q], v.x[st][i].u[q + 1]);
+      } else {
 #pragma unroll
-            for (int i = 0; i < kLoads; ++i)
-#pragma unroll
-              for (int nt = 0; nt < NT; ++nt)
-                mma<false>(acc[(q / 2 + st * 2) % kChains][mt][nt], w0.u[q], w1.u[q], w0.u[q + 1],
-                           w1.u[q + 1], v.x[st][nt][i].u[q], v.x[st][nt][i].u[q + 1]);
-        } else {
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            uint32_t a0, a1, a2, a3;
-            f16_of_e4m3(w0.u[q], a0, a2);
-            f16_of_e4m3(w1.u[q], a1, a3);
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-              mma<true>(sum[FP8 ? q % kChains : 0][nt], a0, a1, a2, a3,
-                        v.x[st][nt][(q / 2) % kLoads].u[q % 2 * 2],
-                        v.x[st][nt][(q / 2) % kLoads].u[q % 2 * 2 + 1]);
-          }
+        for (int q = 0; q < 4; ++q) {
+          uint32_t a0, a1, a2, a3;
+          f16_of_e4m3(w0.u[q], a0, a2);
+          f16_of_e4m3(w1.u[q], a1, a3);
+          mma<true>(sum[q % kChains], a0, a1, a2, a3, v.x[st][(q / 2) % kLoads].u[q % 2 * 2],
+                    v.x[st][(q / 2) % kLoads].u[q % 2 * 2 + 1]);
         }
       }
-      if (FP8) {
+    }
+    if (FP8) {
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            float t = sum[0][nt][r];
-#pragma unroll
-            for (int c = 1; c < (FP8 ? kChains : 1); ++c) t += sum[c][nt][r];
-            acc[0][mt][nt][r] = fmaf(v.sc[mt][r / 2], t, acc[0][mt][nt][r]);
-          }
-      }
+      for (int r = 0; r < 4; ++r) acc[0][r] = fmaf(v.sc[r / 2], sum[0][r] + sum[1][r], acc[0][r]);
     }
   }
 
   // What undoes an entry's factor (e4m3): loaded at a job's start, worked out
   // at its end.
   __device__ __forceinline__ uint32_t held_factor(int entry) const {
-    return UP ? __ldcg(reinterpret_cast<const uint32_t*>(a.xscale) + entry / (a.K + a.S)) : __ldcg(a.amax + entry);
+    return UP ? __ldcg(reinterpret_cast<const uint32_t*>(a.xscale) + entry / (a.K + a.S))
+              : __ldcg(a.amax + entry);
   }
   static __device__ __forceinline__ float inverse(uint32_t held) {
     return UP ? __uint_as_float(held) : 1.0f / f16_factor(held);
   }
 
-  // One result pair of entry `entry`, f its inverse(): up: gate and up of output `row`; down:
-  // outputs row and row + 8.
+  // One result pair of entry `entry`, f its inverse(): up: gate and up of output
+  // `row`; down: outputs row and row + 8.
   __device__ __forceinline__ void store(int entry, int row, float v0, float v1, float f) const {
     if (row >= limit) return;
     const int KS = a.K + a.S;
@@ -461,20 +410,13 @@ struct Phase {
       const float rest = h - __bfloat162float(hi);
       __nv_bfloat16* dst = reinterpret_cast<__nv_bfloat16*>(a.a) + static_cast<int64_t>(entry) * a.I + row;
       dst[0] = hi;
-      if (S::kSplit)
-        dst[static_cast<int64_t>(a.T) * KS * a.I] = __float2bfloat16_rn(isfinite(rest) ? rest : 0.0f);
+      dst[static_cast<int64_t>(a.T) * KS * a.I] = __float2bfloat16_rn(isfinite(rest) ? rest : 0.0f);
     }
   }
 
   __device__ __forceinline__ void sync_team() const {
-    if (team == 1) sync_unit();
-    else asm volatile("bar.sync %0, %1;" ::"r"(unit / team + 1), "r"(team * WM * 32) : "memory");
-  }
-  // Barriers 1 .. 8 are the teams', 8 .. 15 the units' (of two warps: at most
-  // 8 units, whose teams of two and more take 1 .. 4).
-  __device__ __forceinline__ void sync_unit() const {
-    if (WM == 1) __syncwarp();
-    else asm volatile("bar.sync %0, %1;" ::"r"(unit + 8), "r"(WM * 32) : "memory");
+    if (team == 1) __syncwarp();
+    else asm volatile("bar.sync %0, %1;" ::"r"(warp / team + 1), "r"(team * 32) : "memory");
   }
 
   // The first stages: all of them, or the weights alone while the tokens are
@@ -496,7 +438,7 @@ struct Phase {
 
   // Everything else.
   __device__ __forceinline__ void run(Cursor& c, float* red) const {
-    const bool leader = part == 0 && warp % WM == 0 && lane == 0;
+    const bool leader = part == 0 && lane == 0;
     int ticket = 0, sums = 0;
     if (leader) ticket = static_cast<int>(atomicAdd(given, 1u));
     uint32_t from = queue, to = queue + (kStages - 1) * kStageBytes;
@@ -505,28 +447,23 @@ struct Phase {
     while (valid(j)) {
       const int p = g.slot_expert[j.slot];
       const int cnt = min(g.cnt[p] - j.c0, kTokens), begin = g.start[p] + j.c0;
-      uint32_t has = 0;
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) has |= (lane_token(nt) < cnt ? 1u : 0u) << nt;
-      uint32_t f[NT][2] = {};
+      uint32_t f[2] = {};
       if (FP8) {
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const int n = nt * 8 + 2 * (lane & 3) + i;
-            if (n < cnt) f[nt][i] = held_factor(g.order[begin + n]);
-          }
+        for (int i = 0; i < 2; ++i) {
+          const int n = 2 * (lane & 3) + i;
+          if (n < cnt) f[i] = held_factor(g.order[begin + n]);
+        }
       }
-      float acc[kChains][MT][NT][4] = {};
+      float acc[kChains][4] = {};
 #pragma unroll 1
       for (int st = part; st < stages; st += team) {
         copies_wait<kStages - 2>();
         // the lanes' copies are there for one another, and no lane still
         // reads the slot that is filled next
-        sync_unit();
+        __syncwarp();
         Operands v;
-        load(v, from, has);
+        load(v, from, lane_token() < cnt);
         // the stage before this one has been multiplied: its slot is free
         if (valid(c.j)) {
           copy_weights(c, to);
@@ -538,11 +475,12 @@ struct Phase {
         to = from;
         from = from + kStageBytes == queue + kStages * kStageBytes ? queue : from + kStageBytes;
       }
+      float (&v)[4] = acc[0];
       if (!FP8) {
 #pragma unroll
         for (int i = 1; i < kChains; ++i)
 #pragma unroll
-          for (int r = 0; r < 4; ++r) acc[0][0][0][r] += acc[i][0][0][r];
+          for (int r = 0; r < 4; ++r) v[r] += acc[i][r];
       }
       // the ticket that was asked for at the last job's end
       const bool ends = j.c0 + kTokens >= g.cnt[p];
@@ -550,46 +488,32 @@ struct Phase {
       // The team's partial sums, added in warp order by one of its warps.  With
       // two buffers, whoever writes one has passed the sync behind the reads
       // of its last contents.
+      float* buf = red + sums % 2 * kSumFloats;
+      if (team > 1) {
 #pragma unroll
-      for (int mt = 0; mt < MT; ++mt) {
+        for (int r = 0; r < 4; ++r) buf[(warp * 4 + r) * 32 + lane] = v[r];
+      }
+      sync_team();
+      if (sums++ % team == part) {
+        if (team > 1) {
+          const float* at = buf + (warp - part) * 4 * 32 + lane;
 #pragma unroll
-        for (int n0 = 0; n0 < NT; n0 += kAtOnce, ++sums) {
-          float* buf = red + sums % S::kRed * S::kRedFloats;
-          if (team > 1) {
-            if (S::kRed == 1) sync_team();
+          for (int r = 0; r < 4; ++r) v[r] = at[r * 32] + at[(4 + r) * 32];
 #pragma unroll
-            for (int i = 0; i < kAtOnce; ++i)
+          for (int u = 2; u < kMaxTeam; ++u)
+            if (u < team) {
 #pragma unroll
-              for (int r = 0; r < 4; ++r)
-                buf[((warp * kAtOnce + i) * 4 + r) * 32 + lane] = acc[0][mt][n0 + i][r];
-          }
-          sync_team();
-#pragma unroll
-          for (int i = 0; i < kAtOnce; ++i) {
-            const int nt = n0 + i;
-            if ((sums + i) % team != part) continue;
-            float (&v)[4] = acc[0][mt][nt];
-            if (team > 1) {
-              const float* at = buf + ((warp - part * WM) * kAtOnce + i) * 4 * 32 + lane;
-#pragma unroll
-              for (int r = 0; r < 4; ++r) v[r] = at[r * 32] + at[(WM * kAtOnce * 4 + r) * 32];
-#pragma unroll
-              for (int u = 2; u < S::kMaxTeam; ++u)
-                if (u < team) {
-#pragma unroll
-                  for (int r = 0; r < 4; ++r) v[r] += at[(u * WM * kAtOnce * 4 + r) * 32];
-                }
+              for (int r = 0; r < 4; ++r) v[r] += at[(u * 4 + r) * 32];
             }
-            if (kLowColumns) {  // columns n and n + 4
-#pragma unroll
-              for (int r = 0; r < 4; ++r) v[r] += __shfl_xor_sync(kFull, v[r], 2);
-            }
-            const int n = nt * 8 + 2 * (lane & 3);
-            const int row = first_row(j, mt) + (lane >> 2);
-            if (n < cnt) store(g.order[begin + n], row, v[0], v[2], inverse(f[nt][0]));
-            if (n + 1 < cnt) store(g.order[begin + n + 1], row, v[1], v[3], inverse(f[nt][1]));
-          }
         }
+        if (kLowColumns) {  // columns n and n + 4
+#pragma unroll
+          for (int r = 0; r < 4; ++r) v[r] += __shfl_xor_sync(kFull, v[r], 2);
+        }
+        const int n = 2 * (lane & 3);
+        const int row = first_row(j) + (lane >> 2);
+        if (n < cnt) store(g.order[begin + n], row, v[0], v[2], inverse(f[0]));
+        if (n + 1 < cnt) store(g.order[begin + n + 1], row, v[1], v[3], inverse(f[1]));
       }
       if (leader && ends) ticket = static_cast<int>(atomicAdd(given, 1u));
       j = next(j);
@@ -599,7 +523,6 @@ struct Phase {
 };
 
 // fp16 copies of x and their factors: a block per token.
-template <int kThreads>
 __device__ __forceinline__ void scale_tokens(const LayerArgs& a, int tokens, uint32_t* red) {
   for (int t = blockIdx.x; t < tokens; t += gridDim.x) {
     const uint8_t* row = a.x + static_cast<int64_t>(t) * a.H * 2;
@@ -613,7 +536,6 @@ __device__ __forceinline__ void scale_tokens(const LayerArgs& a, int tokens, uin
 }
 
 // fp16 copies of the activations, their factors from the entries' maxima.
-template <int kThreads>
 __device__ __forceinline__ void scale_activations(const LayerArgs& a, const Groups& g) {
   const int per = a.I / 8;
   const int64_t n = static_cast<int64_t>(g.tokens) * (a.K + a.S) * per;
@@ -624,25 +546,23 @@ __device__ __forceinline__ void scale_activations(const LayerArgs& a, const Grou
   }
 }
 
-template <typename S>
-__global__ void __launch_bounds__(S::kThreads, 1) layer_kernel(LayerArgs a) {
-  constexpr int kThreads = S::kThreads;
+template <bool FP8, bool PACKED>
+__global__ void __launch_bounds__(kThreads, 1) layer_kernel(LayerArgs a) {
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ int ok;
   grid_dependency_wait();
-  float* red = reinterpret_cast<float*>(smem + S::kQueueBytes);
+  float* red = reinterpret_cast<float*>(smem + kQueueBytes);
   Groups g;
-  group_entries<kThreads, false>(a, g, smem + S::kFixedBytes, nullptr);
-  const int KS = a.K + a.S;
+  group_entries<kThreads, false>(a, g, smem + kFixedBytes, nullptr);
   uint32_t* arrived = a.arrived;  // of the next barrier
-  if (S::FP8) {
-    scale_tokens<kThreads>(a, g.tokens, reinterpret_cast<uint32_t*>(red));
+  if (FP8) {
+    scale_tokens(a, g.tokens, reinterpret_cast<uint32_t*>(red));
     grid_arrive(arrived);
   }
   {
-    const Phase<S, true> up(a, g, smem);
-    typename Phase<S, true>::Cursor c = up.begin();
-    if (S::FP8) {
+    const Phase<FP8, PACKED, true> up(a, g, smem);
+    typename Phase<FP8, PACKED, true>::Cursor c = up.begin();
+    if (FP8) {
       up.template start<true, false>(c);
       if (!grid_wait(a, arrived++, &ok)) {
         copies_wait<0>();
@@ -656,12 +576,12 @@ __global__ void __launch_bounds__(S::kThreads, 1) layer_kernel(LayerArgs a) {
   }
   grid_arrive(arrived);
   {
-    const Phase<S, false> down(a, g, smem);
-    typename Phase<S, false>::Cursor c = down.begin();
+    const Phase<FP8, PACKED, false> down(a, g, smem);
+    typename Phase<FP8, PACKED, false>::Cursor c = down.begin();
     down.template start<true, false>(c);
     bool done = grid_wait(a, arrived++, &ok);
-    if (S::FP8 && done) {
-      scale_activations<kThreads>(a, g);
+    if (FP8 && done) {
+      scale_activations(a, g);
       grid_arrive(arrived);
       done = grid_wait(a, arrived++, &ok);
     }
@@ -684,15 +604,15 @@ __global__ void layer_start_kernel(uint32_t* arrived) {
   if (threadIdx.x < kLayerCounters) arrived[threadIdx.x] = 0;
 }
 
-template <typename S>
-cudaError_t launch_shape(const moe_handle* h, const LayerArgs& a, cudaStream_t s) {
-  auto k = layer_kernel<S>;
-  const size_t smem = S::smem(a.T, a.K + a.S, a.E + a.S);
+template <bool FP8, bool PACKED>
+cudaError_t launch_few(const moe_handle* h, const LayerArgs& a, cudaStream_t s) {
+  auto k = layer_kernel<FP8, PACKED>;
+  const size_t smem = kFixedBytes + groups_bytes(a.T, a.K + a.S, a.E + a.S);
   // per device and cheap: no state to keep
   const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                              static_cast<int>(smem));
   if (e != cudaSuccess) return e;
-  return launch_chained(k, dim3(h->num_sms), dim3(S::kThreads), smem, s, true, a);
+  return launch_chained(k, dim3(h->num_sms), dim3(kThreads), smem, s, true, a);
 }
 
 }  // namespace
@@ -749,14 +669,20 @@ cudaError_t launch_layer(const moe_handle* h, const moe_layer_args& q, int T, vo
   a.act = q.act;
   a.wait_ns = h->wait_ns;
   a.flags = h->flags;
-  // few: 6 tokens an expert and less in the mean; packed: 2 and less
+  // Tokens an expert in the mean from which on the kernel of layer_many.cu is the
+  // faster one.  bf16: 3 to 7, the more the fewer weights there are (64 experts,
+  // top 8, 2048 x 1408: 184 against 181 us at 4 tokens, 194 against 183 at 5;
+  // 1024 x 512: 54 against 59 at 5, 65 against 59 at 8).  e4m3, whose weights
+  // the kernel here converts again for every 4 tokens: 0.5 to 1.5 (2048 x 1408:
+  // 80 against 78 us at 0.5, 123 against 97 at 1; 16 experts, top 2, 4096 x
+  // 2048: 71 against 78 at 1, 93 against 89 at 1.5).  Packed up to 2 tokens (128
+  // experts, top 8, 2048 x 768: 92 us, unpacked 94, at 0.5; 211 and 206 at 4,
+  // where 4 tokens to a tile make second passes).
   const int64_t entries = static_cast<int64_t>(T) * K;
-  if (entries > 6 * a.E) return launch_layer_many(h, a, q.weight_dtype == MOE_E4M3, s);
-  if (q.weight_dtype == MOE_E4M3)
-    return entries > 2 * a.E ? launch_shape<Shape<512, 1, 1, 1, 2, 192, true, false>>(h, a, s)
-                             : launch_shape<Shape<512, 1, 1, 1, 2, 192, true, true>>(h, a, s);
-  return entries > 2 * a.E ? launch_shape<Shape<512, 1, 1, 1, 2, 192, false, false>>(h, a, s)
-                           : launch_shape<Shape<512, 1, 1, 1, 2, 192, false, true>>(h, a, s);
+  const bool e4m3 = q.weight_dtype == MOE_E4M3;
+  if (entries > (e4m3 ? 1 : 5) * a.E) return launch_layer_many(h, a, e4m3, s);
+  if (e4m3) return launch_few<true, true>(h, a, s);
+  return entries > 2 * a.E ? launch_few<false, false>(h, a, s) : launch_few<false, true>(h, a, s);
 }
 
 }  // namespace moe

@@ -244,6 +244,110 @@ def test_unreached_experts_are_not_read_into_the_sums(T, H, I, e4m3):
     assert set(idx.reshape(-1)) == {1, 4}
 
 
+@pytest.mark.parametrize("kw", [
+    dict(T=8, E=1, K=1, H=8, I=8),                  # 32 entries and less, smallest sizes
+    dict(T=40, E=2, K=2, H=8, I=16, shared=1),
+    dict(T=9, E=1, K=1, H=16, I=16, e4m3=True),
+    dict(T=128, E=2, K=1, H=16, I=32, e4m3=True),
+    dict(T=128, E=3, K=3, H=136, I=136, shared=4),  # 128 tokens an expert, a 128-column block and 8
+    dict(T=128, E=3, K=2, H=144, I=144, shared=2, e4m3=True, act="gelu"),
+    dict(T=64, E=4, K=2, H=1032, I=520, act="gelu"),
+    dict(T=37, E=2, K=1, H=4096, I=2048),           # jobs for some blocks only
+    dict(T=17, E=4, K=1, H=272, I=80, e4m3=True),   # 16 and 32 columns and one more
+    dict(T=33, E=1, K=1, H=128, I=64, e4m3=True),
+    dict(T=65, E=1, K=1, H=256, I=64, e4m3=True),
+], ids=lambda k: "-".join("%s" % v for v in k.values()))
+def test_layer_with_many_tokens_an_expert(kw):
+    p = Problem(**kw)
+    p.call()
+    p.check()
+    p.check_route()
+    first = p.out.clone()
+    p.call()
+    assert torch.equal(p.out, first)
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_many_tokens_given_routes_some_without_an_expert(e4m3):
+    p = Problem(T=90, E=5, K=3, H=176, I=96, e4m3=e4m3)
+    g = np.random.default_rng(3)
+    idx = np.argsort(g.random((90, 5)), axis=1)[:, :3].astype(np.int32)
+    idx[g.random((90, 3)) < 0.3] = -1
+    idx[7] = -1
+    idx[idx == 2] = -1                 # an expert that nobody takes
+    p.idx.copy_(to_dev(idx))
+    p.w.copy_(torch.rand(90, 3, device=dev()))
+    p.call(logits=None)
+    _, _, got = p.check()
+    assert (got[7] == 0).all()
+    idx[11] = [0, 0, 99]
+    p.idx.copy_(to_dev(idx))
+    p.call(logits=None)
+    p.check(flags=moe.MOE_DEVERR_BAD_EXPERT | moe.MOE_DEVERR_DUP_EXPERT)
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_many_tokens_in_a_captured_graph_in_place(e4m3):
+    p = Problem(T=80, E=6, K=2, H=160, I=96, shared=1, e4m3=e4m3)
+    logits = to_dev(p.logits)
+    live = torch.tensor([80], dtype=torch.int32, device=dev())
+    x = p.x.clone()
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        p.call(logits=logits, live=live, x=x, out=x)
+    s.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=s):
+        x.copy_(p.x)
+        p.call(logits=logits, live=live, x=x, out=x)
+        p.call(logits=logits, live=live)
+    for n in (80, 33, 1):
+        live.fill_(n)
+        graph.replay()
+        p.check(n)
+        assert torch.equal(x[:n], p.out[:n]) and torch.equal(x[n:], p.x[n:])
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_many_tokens_a_wait_that_gives_up(e4m3):
+    p = Problem(T=60, E=4, K=2, H=512, I=256, e4m3=e4m3)
+    moe.moe_set_wait_limit(p.r.h, 1)
+    p.call()
+    torch.cuda.synchronize()
+    assert moe.moe_read_device_status(p.r.h) == moe.MOE_DEVERR_TIMEOUT
+    moe.moe_set_wait_limit(p.r.h, 0)
+    moe.moe_clear_device_status(p.r.h)
+    p.call()
+    p.check()
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_many_tokens_weights_past_32_bit_offsets(e4m3):
+    """Experts 39 and 40 of 41 begin past 2^31 elements of w13."""
+    E, H, I, T = 41, 7168, 4096, 128
+    r = moe.MoeRouter(E, 2, 1, T)
+    dt = torch.float8_e4m3fn if e4m3 else torch.bfloat16
+    w13 = torch.zeros(E, 2 * I, H, dtype=torch.uint8 if e4m3 else dt, device=dev())
+    w2 = torch.zeros(E, H, I, dtype=torch.uint8 if e4m3 else dt, device=dev())
+    one = torch.tensor([1.0]).to(dt).view(torch.uint8).item() if e4m3 else 1.0
+    for e, col in ((39, 6), (40, 4000)):
+        w13[e, col, 11] = one
+        w13[e, I + col, 12] = one
+        w2[e, 7000 + e, col] = one
+    if e4m3:
+        w13, w2 = w13.view(dt), w2.view(dt)
+    x = torch.zeros(T, H, dtype=torch.bfloat16, device=dev())
+    x[:, 11], x[:, 12] = 64.0, 0.5
+    logits = torch.zeros(T, E, device=dev())
+    logits[:, 39:] = 8.0
+    scales = dict(s13=torch.ones(E, 64, 56, device=dev()), s2=torch.ones(E, 56, 32, device=dev())) if e4m3 else {}
+    out, idx, w = r.layer(x, logits, w13, w2, **scales)
+    assert (idx.sort(1).values == torch.tensor([39, 40], device=dev())).all()
+    assert (out[:, 7039] == 16.0).all() and (out[:, 7040] == 16.0).all()
+    assert (out != 0).sum().item() == 2 * T
+
+
 def test_routes_without_an_expert_hide_their_scores():
     p = Problem(T=5, E=6, K=3, H=88, I=48)
     p.idx.copy_(torch.tensor([[0, -1, 2]] * 5, dtype=torch.int32))
