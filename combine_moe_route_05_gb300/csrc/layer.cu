@@ -1,28 +1,28 @@
 // A whole MoE layer for a few tokens (sm_103a): after the routing, one kernel
-// that streams the reached experts' weights once.
+// that streams the reached experts' weights once.  This file: experts with a
+// handful of tokens, and the call itself; layer_many.cu: more tokens an expert.
 //
 //   up:      a[t,k,i] = act(<w13_e[i], x_t>) * <w13_e[I + i], x_t>
 //   down:    y[t,k,n] = <w2_e[n], a[t,k]>                            (fp32)
 //   combine: out[t]   = round(sum_k w[t,k] y[t,k] + sum_j y[t, K + j])
 //
-// With at most 128 tokens an expert sees a handful of them, so the layer is
-// bound by reading its weights.  The products run on mma.m16n8k16 with 16
-// weight rows as the one operand and 8 of the expert's tokens as the other.
-// The order of the k index is free as long as both operands agree, so a lane
-// takes 16 contiguous bytes of its two weight rows as the operand registers
-// of two (bf16) or four (e4m3) products, with its token's values at the same
-// k beside them.  In the up products rows 0..7 of the 16 are gate rows and
-// 8..15 the up rows of the same outputs: a lane's accumulators then hold gate
-// and up of one output and the activation needs no exchange.
+// Bound by reading the weights: 2 operations a byte and token.  The products
+// run on mma.m16n8k16 with 16 weight rows as the one operand and up to 8 of
+// the expert's tokens as the other.  The order of the k index is free as long
+// as both operands agree, so a lane takes 16 contiguous bytes of its two weight
+// rows as the operand registers of two (bf16) or four (e4m3) products, with its
+// token's values at the same k beside them.  In the up products rows 0..7 of
+// the 16 are gate rows and 8..15 the up rows of the same outputs: a lane's
+// accumulators then hold gate and up of one output and the activation needs no
+// exchange.
 //
 // Every warp copies what it will itself multiply into a queue of its own in
 // shared memory (cp.async), several stages ahead and across the ends of jobs,
 // so the stream of weights has no gaps and the queue needs no barrier.  A job
-// is one expert and one tile of outputs; a team of 1, 2, 4 or 8 warps, as many
-// as make the jobs fill the grid evenly, splits its k and adds its partial
-// sums in warp order.  Jobs go round over the blocks, expert by expert, so
-// that neighbouring blocks read neighbouring rows and the experts with many
-// tokens spread over all blocks.
+// is one expert and one tile of outputs; a team of 1, 2, 4 or 8 warps splits
+// its k and adds its partial sums in warp order.  A team's first jobs are dealt
+// out beforehand, the others by a counter: the SMs differ in speed by a fifth
+// (their way to memory), and jobs dealt out in turn all waited for the slowest.
 //
 // The three parts are one cooperative kernel, with grid-wide barriers between
 // them (bounded waits): the queue takes the first W2 rows before it waits for
@@ -35,6 +35,14 @@
 // would take four); x becomes fp16 times a power of two that brings its
 // token's largest value to [2^14, 2^15) (exact down to 2^-29 of that), and a
 // likewise per entry (11 bits).
+//
+// Measured, routing included (GPU time of a replayed graph; weights read once
+// at the copy rate of 6.78 TB/s): 16 tokens, 128 experts, top 8, 2048 x 768,
+// bf16: 135 us (115; DRAM reads 785 MB, the weights' 778 and the tokens); 4
+// tokens, 256 experts and a shared one, 7168 x 2048: 413 us (410); 1 token,
+// 2048 x 768: 29 us (11): there the parts in front of and between the products
+// bound it: routing 5, grouping 2, the first weights' latency 3, two grid
+// barriers 3, the sum 2 us.
 #include "layer.cuh"
 
 namespace moe {

@@ -24,10 +24,12 @@ struct LayerArgs {
   const float* s2;
   __half* x16;           // [T, H] scaled x (e4m3)
   float* xscale;         // [T] 1 / its factor (e4m3)
+  // the next two by entry t (K + S) + k, for many tokens in the experts' order
   uint8_t* a;            // bf16 [2][T (K + S), I], high and low part; e4m3: fp16, scaled
   float* a32;            // [T (K + S), I] (e4m3)
-  uint32_t* amax;        // [T (K + S)] bits of the largest |a| of an entry (e4m3)
-  float* y;              // [T (K + S), H]
+  uint32_t* amax;        // [T (K + S)] bits of the largest |a| of an entry (e4m3); for many
+                         // tokens a float, what undoes the entry's factor
+  float* y;              // [T (K + S), H]; for many tokens first x in the experts' order
   uint32_t* arrived;     // blocks that reached each grid barrier (kBarriers), then the
                          // jobs given out in each phase; zero at the start
   __nv_bfloat16* out;    // [T, H]
@@ -277,7 +279,9 @@ __device__ __forceinline__ void copy16_stream(uint32_t dst, const void* src, boo
                "r"(valid ? 16 : 0)
                : "memory");
 }
-__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+__device__ __forceinline__ void copies_commit() {
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
 template <int N>
 __device__ __forceinline__ void copies_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
@@ -364,9 +368,11 @@ __device__ __forceinline__ void sum_entries(const LayerArgs& a, const Groups& g)
   const int KS = a.K + a.S;
   const int per = a.H / 4;
   const int64_t n = static_cast<int64_t>(g.tokens) * per;
-  for (int64_t i = (static_cast<int64_t>(threadIdx.x >> 5) * gridDim.x + blockIdx.x) * 32 + (threadIdx.x & 31);
+  for (int64_t i = (static_cast<int64_t>(threadIdx.x >> 5) * gridDim.x + blockIdx.x) * 32 +
+                   (threadIdx.x & 31);
        i < n; i += static_cast<int64_t>(gridDim.x) * kThreads) {
-    const int t = static_cast<int>(i / per), col = static_cast<int>(i - static_cast<int64_t>(t) * per) * 4;
+    const int t = static_cast<int>(i / per);
+    const int col = static_cast<int>(i - static_cast<int64_t>(t) * per) * 4;
     float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     const float* y = a.y + static_cast<int64_t>(t) * KS * a.H + col;
 #pragma unroll 8

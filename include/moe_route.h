@@ -459,10 +459,13 @@ moe_status moe_act_rows_bwd(const moe_handle* h, const void* d_ghs, const void* 
  * layout: routing, the experts and the weighted sum, reading the weights of
  * each reached expert once.  The layer is that of the separate calls
  * (moe_route_topk, gate/up GEMM, moe_act_rows, W2, moe_combine):
- *   a[t,k,i] = round_bf16( act(<w13_e[i], x_t>) * <w13_e[I + i], x_t> )
+ *   a[t,k,i] = act(<w13_e[i], x_t>) * <w13_e[I + i], x_t>
  *   out[t]   = round_bf16( sum_k w[t,k] <w2_e, a[t,k]> + sum_j <w2_(E+j), a[t,K+j]> )
- * with e = idx[t,k]; fp32 sums; a is rounded to bf16 because it is the operand
- * of the second product.  Deterministic: the same inputs give the same bits.
+ * with e = idx[t,k]; fp32 sums.  a is the operand of the second product: with
+ * bf16 weights as the sum of two bf16 numbers (16 bits), with e4m3 weights in
+ * fp16 (11 bits) times a power of two per entry, and so is x there (its bf16
+ * values exactly, down to 2^-29 of the token's largest).  Deterministic: the
+ * same inputs give the same bits.
  *   d_x [T,H] bf16;  d_out [T,H] bf16 (may be d_x: in place)
  *   d_logits [T,E] fp32 and d_bias [E] or NULL as in moe_route_topk, which
  *     fills d_idx [T,K] int32 and d_w [T,K] fp32.  d_logits NULL: the caller's
@@ -484,7 +487,12 @@ moe_status moe_act_rows_bwd(const moe_handle* h, const void* d_ghs, const void* 
  * go through the dispatch.  The handle gives the routing configuration and
  * the status word; its layout is neither read nor changed.
  * d_workspace: moe_layer_workspace_bytes(c, H, I, S) bytes, 256-byte aligned,
- * free after the call's work; calls that may overlap on the GPU need one each.
+ * free after the call's work; calls that may overlap on the GPU need one each
+ * (so do graphs that may be replayed at the same time).
+ * The call takes every SM (a cooperative grid) and waits inside the kernel, at
+ * most the handle's wait limit each time: a wait that gives up sets
+ * MOE_DEVERR_TIMEOUT and ends the kernel, with d_out partly or not written; the
+ * next call needs nothing cleared but the status word.
  */
 #define MOE_LAYER_MAX_TOKENS 128
 #define MOE_LAYER_MAX_SHARED 4
@@ -532,12 +540,13 @@ moe_status moe_clear_device_status(moe_handle* h, void* stream);
 
 /*
  * Time limit, in nanoseconds, of every bounded wait inside this handle's
- * kernels: the single-launch layout's wait for all tiles' counts, and the
- * pipeline waits of moe_w2_absorbed ([AutoEP-DeepEP] review fix: a transport
- * that runs out of what it needs must fail, not fault).  A wait that gives up
- * sets MOE_DEVERR_TIMEOUT, and the kernel stops writing and returns (the W2
- * GEMM first waits, within the same limit, for the copies it has in flight
- * and releases its tensor memory).  limit_ns = 0 restores the default, one
+ * kernels: the single-launch layout's wait for all tiles' counts, the pipeline
+ * waits of moe_w2_absorbed, and the grid barriers and pipeline waits of
+ * moe_layer ([AutoEP-DeepEP] review fix: a transport that runs out of what it
+ * needs must fail, not fault).  A wait that gives up sets MOE_DEVERR_TIMEOUT,
+ * and the kernel stops writing and returns (the W2 GEMM and moe_layer first
+ * wait, again with a limit, for the copies they have in flight and release
+ * their tensor memory).  limit_ns = 0 restores the default, one
  * second; a short limit is for tests that make a wait run out.  Host-only:
  * applies to launches made after the call.
  */
