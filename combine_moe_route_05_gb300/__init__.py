@@ -157,26 +157,30 @@ def _call(h, fn, *args):
     """Library function `fn` called with the handle's device current (the
     library refuses a call made while another device is current)."""
     f = getattr(_lib or lib(), fn)
-    if _current_device() != h.device.index:
-        with torch.cuda.device(h.device):
-            _check(fn, f(*args))
+    if _current_device() == h.index:
+        s = f(*args)
     else:
-        _check(fn, f(*args))
+        with torch.cuda.device(h.device):
+            s = f(*args)
+    if s != MOE_OK:
+        raise MoeError(fn, s)
+
+
+_ROW_DTYPES = {torch.bfloat16: MOE_BF16, torch.float32: MOE_F32}
 
 
 def _row_dtype(t):
-    if t.dtype == torch.bfloat16:
-        return MOE_BF16
-    if t.dtype == torch.float32:
-        return MOE_F32
-    raise TypeError("row tensors must be bfloat16 or float32, got %s" % t.dtype)
+    d = _ROW_DTYPES.get(t.dtype)
+    if d is None:
+        raise TypeError("row tensors must be bfloat16 or float32, got %s" % t.dtype)
+    return d
 
 
 def _req(t, dtype=None, shape=None, name="tensor", device=None):
     if t is None:
         return
     # the usual case first: these checks are most of a small call's host time
-    if dtype is not None and t.dtype == dtype and t.device == device and t.shape == shape \
+    if (dtype is None or t.dtype is dtype) and t.shape == shape and t.device == device \
             and t.is_contiguous():
         return
     if shape is not None and any(d < 0 for d in shape):
@@ -210,6 +214,10 @@ class Handle:
 
     def __init__(self, cfg, device=None):
         self.cfg = cfg
+        # plain copies: the library keeps its own of the configuration, and a
+        # call reads these several times
+        self.E, self.K, self.R = cfg.num_experts, cfg.top_k, cfg.num_ranks
+        self.pad = max(1, cfg.pad_align)
         nbytes = moe_workspace_bytes(cfg)
         if nbytes == 0:
             raise MoeError("moe_workspace_bytes", MOE_ERR_INVALID)
@@ -224,6 +232,7 @@ class Handle:
                                            ctypes.byref(h)))
         self.ptr = h
         self.device = dev
+        self.index = dev.index
         self.T = -1
 
     def close(self):
@@ -236,22 +245,6 @@ class Handle:
             self.close()
         except Exception:
             pass
-
-    @property
-    def E(self):
-        return self.cfg.num_experts
-
-    @property
-    def K(self):
-        return self.cfg.top_k
-
-    @property
-    def R(self):
-        return self.cfg.num_ranks
-
-    @property
-    def pad(self):
-        return max(1, self.cfg.pad_align)
 
     @property
     def recv_rows(self):
@@ -423,18 +416,21 @@ def moe_w2_absorbed(h, hrows, recv_w, w2, y, stream=None):
           _stream(stream, d))
 
 
+_ACTS = {"silu": MOE_ACT_SILU, "gelu": MOE_ACT_GELU}
+
+
 def _act(act):
-    return {"silu": MOE_ACT_SILU, "gelu": MOE_ACT_GELU}[act] if isinstance(act, str) else int(act)
+    return _ACTS[act] if isinstance(act, str) else int(act)
 
 
 def moe_act_rows(h, gu, recv_w, hs, act="silu", p=0.0, rng=None, stream=None):
     """hs = recv_w * dropout(act(gate) * up) per receive row, gu = [gate, up];
     recv_w None: 1.  rng: int64 [2] CUDA tensor (seed, offset), needed if p > 0."""
     I = hs.shape[1]
-    d = h.device
-    _req(gu, hs.dtype, (h.recv_rows, 2 * I), "gu", d)
-    _req(recv_w, torch.float32, (h.recv_rows,), "recv_w", d)
-    _req(hs, None, (h.recv_rows, I), "hs", d)
+    d, rows = h.device, h.recv_rows
+    _req(gu, hs.dtype, (rows, 2 * I), "gu", d)
+    _req(recv_w, torch.float32, (rows,), "recv_w", d)
+    _req(hs, None, (rows, I), "hs", d)
     _req(rng, torch.int64, (2,), "rng", d)
     _call(h, "moe_act_rows", h.ptr, _ptr(gu), I, _row_dtype(hs), _act(act), _ptr(recv_w), float(p),
           _ptr(rng), _ptr(hs), _stream(stream, d))
@@ -444,11 +440,11 @@ def moe_act_rows_bwd(h, ghs, gu, recv_w, ggu, gw=None, act="silu", p=0.0, rng=No
     """Backward of moe_act_rows: ggu (may be gu) and, with recv_w, the score
     gradient gw [T, K] (None: not computed)."""
     I = ghs.shape[1]
-    d = h.device
-    _req(ghs, None, (h.recv_rows, I), "ghs", d)
-    _req(gu, ghs.dtype, (h.recv_rows, 2 * I), "gu", d)
-    _req(recv_w, torch.float32, (h.recv_rows,), "recv_w", d)
-    _req(ggu, ghs.dtype, (h.recv_rows, 2 * I), "ggu", d)
+    d, rows, dtype = h.device, h.recv_rows, ghs.dtype
+    _req(ghs, None, (rows, I), "ghs", d)
+    _req(gu, dtype, (rows, 2 * I), "gu", d)
+    _req(recv_w, torch.float32, (rows,), "recv_w", d)
+    _req(ggu, dtype, (rows, 2 * I), "ggu", d)
     _req(gw, torch.float32, (h.T, h.K), "gw", d)
     _req(rng, torch.int64, (2,), "rng", d)
     _call(h, "moe_act_rows_bwd", h.ptr, _ptr(ghs), _ptr(gu), I, _row_dtype(ghs), _act(act),
