@@ -56,7 +56,8 @@ constexpr int kTickets = 16;  // of a team's coming jobs
 // tokens do not come last.
 struct Groups {
   uint16_t* order;        // entries, grouped
-  uint16_t* rank;         // an entry's place within its expert, kNone: dropped
+  uint16_t* rank;         // an entry's place within its expert (ordered: in `order`), kNone:
+                          // dropped
   uint16_t* slot_expert;  // experts with entries
   int* cnt;               // per expert
   int* start;
@@ -124,7 +125,7 @@ __device__ __forceinline__ void group_entries(const LayerArgs& a, Groups& g, uin
         if (lane >= off) start += v;
       }
       start = __shfl_sync(kFull, start - cnt, ok ? __ffs(same) - 1 : 0);
-      if (mine) g.rank[lane] = ok ? static_cast<uint16_t>(rank) : kNone;
+      if (mine) g.rank[lane] = ok ? static_cast<uint16_t>(kOrdered ? start + rank : rank) : kNone;
       if (ok) g.order[start + rank] = static_cast<uint16_t>(lane);
       if (first) {
         g.slot_expert[__popc(firsts & lanemask_lt())] = static_cast<uint16_t>(e);
@@ -220,14 +221,15 @@ __device__ __forceinline__ void group_entries(const LayerArgs& a, Groups& g, uin
   for (int j = 0; j < kMine; ++j) {
     const int i = tid + j * kThreads;
     if (i < n && g.rank[i] != kNone) {
-      if (kOrdered) {
+      int at = g.start[mine[j]] + g.rank[i];
+      if (kOrdered) {  // rank: 0 so far
         const uint32_t* mask = masks + 4 * mine[j];
         const int t = i / KS;
-        int rank = __popc(mask[t / 32] & ((1u << (t % 32)) - 1u));
-        for (int w = 0; w < t / 32; ++w) rank += __popc(mask[w]);
-        g.rank[i] = static_cast<uint16_t>(rank);
+        at += __popc(mask[t / 32] & ((1u << (t % 32)) - 1u));
+        for (int w = 0; w < t / 32; ++w) at += __popc(mask[w]);
+        g.rank[i] = static_cast<uint16_t>(at);
       }
-      g.order[g.start[mine[j]] + g.rank[i]] = static_cast<uint16_t>(i);
+      g.order[at] = static_cast<uint16_t>(i);
     }
   }
   g.nslots = g.head[kMaxWarps];

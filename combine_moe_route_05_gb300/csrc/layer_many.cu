@@ -40,13 +40,13 @@
 //
 // Measured, routing included (GPU time of a replayed graph; in brackets: weights
 // read once at the copy rate of 6.78 TB/s).  128 tokens, 8 experts, top 2, 4096
-// x 2048: bf16 90 us (60), e4m3 83 (30); 128 tokens, 64 experts, top 8, 2048 x
-// 1408, bf16: 193 us (163); 37 live of 64 tokens, 256 experts, top 8, 7168 x
-// 2048, e4m3: 1248 us (1156).  bf16: the up products read at 6.1, the down ones
+// x 2048: bf16 90 us (60), e4m3 81 (30); 128 tokens, 64 experts, top 8, 2048 x
+// 1408, bf16: 192 us (163); 37 live of 64 tokens, 256 experts, top 8, 7168 x
+// 2048, e4m3: 1237 us (1156).  bf16: the up products read at 6.1, the down ones
 // at 5.8 TB/s (DRAM reads 407 MB, the weights' 403); the rest is routing 5,
 // grouping 3, sorting and its barrier 4, the other barriers and the first
 // weights' latency 7, the sum 2 us.  e4m3: half the bytes and the same fixed
-// parts; a stage takes some 950 cycles where the copy rate would allow 690,
+// parts; a stage takes some 900 cycles where the copy rate would allow 690,
 // most of it the epilogue, which reads and scales every column block's sums.
 #include "layer.cuh"
 
@@ -76,8 +76,9 @@ static_assert(kFixedBytes + groups_bytes(MOE_LAYER_MAX_TOKENS, MOE_MAX_TOPK + MO
 struct Barriers {
   uint64_t landed[kMaxRing];  // a stage is there (an arrival per loading thread)
   uint64_t empty[kMaxRing];   // its products are done
-  uint64_t a16_full[2];       // e4m3: the fp16 weights are there (an arrival per converting warp)
-  uint64_t a16_empty[2];      // and its products are done
+  // e4m3: an accumulator's fp16 weights are there (an arrival per converting
+  // warp), and it is free, which the converting warps have waited for
+  uint64_t a16_full[kMaxAcc];
   uint64_t acc_full[kMaxAcc];   // an accumulator is complete
   uint64_t acc_empty[kMaxAcc];  // and read (an arrival per epilogue warp)
   uint64_t drained;           // after a wait that gave up: no product is under way
@@ -165,7 +166,6 @@ struct Place {
 struct State {
   Place stage{0, 0};  // the next one to be filled or read
   int issued = 0;     // loading: stages asked for
-  Place a16{0, 0};
   Place acc{0, 0};
   int job = 0;
 };
@@ -337,8 +337,10 @@ struct ManyPhase {
       }
       const int p = g.slot_expert[q / tiles];
       for (int n = (g.cnt[p] + kMaxN - 1) / kMaxN * stages; n > 0; --n) {
+        // the accumulator has been read, so the products of its last weights
+        // are done, too
         if (!warp_wait(&b.landed[s.stage.slot], s.stage.parity) ||
-            !warp_wait(&b.a16_empty[s.a16.slot], s.a16.parity ^ 1u))
+            !warp_wait(&b.acc_empty[s.acc.slot], s.acc.parity ^ 1u))
           return false;
         tc_fence_after();
         const uint32_t from = stage(s.stage.slot) + row * 128;
@@ -349,11 +351,11 @@ struct ManyPhase {
 #pragma unroll
           for (int j = 0; j < 4; ++j) f16_of_e4m3(v.u[j], h[i * 8 + j * 2], h[i * 8 + j * 2 + 1]);
         }
-        tmem_st32(mine + s.a16.slot * kA16Columns, h);
+        tmem_st32(mine + s.acc.slot * kA16Columns, h);
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&b.a16_full[s.a16.slot]);
-        s.a16.step(2);
+        if (lane == 0) mbar_arrive(&b.a16_full[s.acc.slot]);
+        s.acc.step(kAcc);
         s.stage.step(ring);
       }
     }
@@ -380,10 +382,11 @@ struct ManyPhase {
         const uint32_t idesc = kFormat | (static_cast<uint32_t>(n >> 3) << 17);
         const uint32_t x_next = boxed(cnt) * (kLow ? 16 : 8);
         for (int kb = 0; kb < stages; ++kb) {
-          // (e4m3: the converting warps have seen the stage land)
-          bool ok = FP8 ? wait_phase(&b.a16_full[s.a16.slot], s.a16.parity, a.wait_ns)
+          // e4m3: the converting warps have seen the stage land and the
+          // accumulator free
+          bool ok = FP8 ? wait_phase(&b.a16_full[s.acc.slot], s.acc.parity, a.wait_ns)
                         : wait_phase(&b.landed[s.stage.slot], s.stage.parity, a.wait_ns);
-          if (FP8 || kb == 0)
+          if (!FP8 && kb == 0)
             ok = ok && wait_phase(&b.acc_empty[s.acc.slot], s.acc.parity ^ 1u, a.wait_ns);
           if (!__all_sync(kFull, ok)) return false;
           tc_fence_after();
@@ -391,7 +394,7 @@ struct ManyPhase {
           const uint32_t at = stage(s.stage.slot);
           const uint64_t x = sw128_desc(at + kWeightBytes);
           const uint64_t w = sw128_desc(at);
-          const uint32_t w16 = tmem + kAcc * kAccColumns + s.a16.slot * kA16Columns;
+          const uint32_t w16 = tmem + kAcc * kAccColumns + s.acc.slot * kA16Columns;
           if (elect_one()) {
 #pragma unroll
             for (int i = 0; i < 2; ++i)
@@ -401,12 +404,10 @@ struct ManyPhase {
                 if (FP8) mma_f16_tmem(d, w16 + (i * 4 + k) * 8, tokens, idesc, i + k > 0);
                 else mma_f16(d, w + i * (kTileBytes / 16) + k * 2, tokens, idesc, kb > 0 || i + k > 0);
               }
-            if (FP8) mma_commit(&b.a16_empty[s.a16.slot]);
             mma_commit(&b.empty[s.stage.slot]);
             if (FP8 || kb == stages - 1) mma_commit(&b.acc_full[s.acc.slot]);
           }
           __syncwarp();
-          if (FP8) s.a16.step(2);
           s.stage.step(ring);
           if (FP8 || kb == stages - 1) s.acc.step(kAcc);
         }
@@ -561,32 +562,26 @@ struct ManyPhase {
 // The tokens in the order of the experts, a block per token: bf16 as they are;
 // e4m3: fp16 times the token's factor.
 template <bool FP8>
-__device__ __forceinline__ void sort_tokens(const LayerArgs& a, const Groups& g, uint32_t* red,
-                                            int* place) {
+__device__ __forceinline__ void sort_tokens(const LayerArgs& a, const Groups& g, uint32_t* red) {
   const int KS = a.K + a.S;
   for (int t = blockIdx.x; t < g.tokens; t += gridDim.x) {
     const uint8_t* row = a.x + static_cast<int64_t>(t) * a.H * 2;
     const bool has = static_cast<int>(threadIdx.x) < a.H / 8;
     const Vec16 first = has ? ld_vec(row + threadIdx.x * 16) : Vec16{};
-    if (static_cast<int>(threadIdx.x) < KS) {
-      const int entry = t * KS + threadIdx.x;
-      place[threadIdx.x] = g.rank[entry] == kNone ? -1 : g.start[expert_of(a, entry)] + g.rank[entry];
-    }
     float f = 1.0f;
     if (FP8) {
       f = f16_factor(block_max_bits<kThreads>(row, a.H, red));
       if (threadIdx.x == 0) a.xscale[t] = 1.0f / f;
-    } else {
-      __syncthreads();
     }
     for (int v = threadIdx.x; v < a.H / 8; v += kThreads) {
       Vec16 o = v < kThreads ? first : ld_vec(row + v * 16);
       if (FP8) o = scaled_f16(o, f);
-      for (int k = 0; k < KS; ++k)
-        if (place[k] >= 0)
-          st_vec(reinterpret_cast<uint8_t*>(a.y) + static_cast<int64_t>(place[k]) * a.H * 2 + v * 16, o);
+      for (int k = 0; k < KS; ++k) {
+        const int at = g.rank[t * KS + k];
+        if (at != kNone)
+          st_vec(reinterpret_cast<uint8_t*>(a.y) + static_cast<int64_t>(at) * a.H * 2 + v * 16, o);
+      }
     }
-    __syncthreads();
   }
 }
 
@@ -614,7 +609,7 @@ __device__ __forceinline__ void scale_sorted(const LayerArgs& a, const Groups& g
 template <bool FP8>
 __device__ __forceinline__ bool layer_body(const LayerArgs& a, const Groups& g, Barriers& b,
                                            const Maps& maps, uint32_t queue, uint32_t tmem, int* ok,
-                                           uint32_t* red, int* place) {
+                                           uint32_t* red) {
   const bool loads = threadIdx.x == kWeightWarp * 32;
   uint32_t* arrived = a.arrived;  // of the next barrier
   State s;
@@ -623,7 +618,7 @@ __device__ __forceinline__ bool layer_body(const LayerArgs& a, const Groups& g, 
   int ahead = 0;
   // the weights behind the tokens, whose way to memory they would fill (91 us
   // so, 93 with the weights first: 128 tokens, 8 experts, 4096 x 2048)
-  sort_tokens<FP8>(a, g, red, place);
+  sort_tokens<FP8>(a, g, red);
   fence_copies();
   grid_arrive(arrived);
   if (loads) ahead = up.send_ahead(s);
@@ -660,10 +655,9 @@ __global__ void __launch_bounds__(kThreads, 1) layer_many_kernel(
     const __grid_constant__ Maps maps, LayerArgs a) {
   constexpr uint32_t kColumns = 512;
   static_assert(ManyPhase<FP8, true>::kAcc * ManyPhase<FP8, true>::kAccColumns +
-                    (FP8 ? 2 * kA16Columns : 0) <= kColumns, "tensor memory budget");
+                    (FP8 ? ManyPhase<FP8, true>::kAcc * kA16Columns : 0) <= kColumns, "tensor memory budget");
   extern __shared__ __align__(16) uint8_t raw[];
   __shared__ int ok;
-  __shared__ int place[MOE_MAX_TOPK + MOE_LAYER_MAX_SHARED];
   __shared__ uint32_t red[kThreads / 32];
   grid_dependency_wait();
   // operands begin on the 1024 bytes after which the swizzle repeats
@@ -678,11 +672,8 @@ __global__ void __launch_bounds__(kThreads, 1) layer_many_kernel(
       mbar_init(&b.landed[i], 1 + kTokenWarps);
       mbar_init(&b.empty[i], 1);
     }
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(&b.a16_full[i], kConvertWarps);
-      mbar_init(&b.a16_empty[i], 1);
-    }
     for (int i = 0; i < kMaxAcc; ++i) {
+      mbar_init(&b.a16_full[i], kConvertWarps);
       mbar_init(&b.acc_full[i], 1);
       mbar_init(&b.acc_empty[i], kEpilogueWarps);
     }
@@ -709,7 +700,7 @@ __global__ void __launch_bounds__(kThreads, 1) layer_many_kernel(
   fence_copies();
   __syncthreads();
   const uint32_t tmem = b.tmem;
-  if (!layer_body<FP8>(a, g, b, maps, smem_addr(smem), tmem, &ok, red, place)) {
+  if (!layer_body<FP8>(a, g, b, maps, smem_addr(smem), tmem, &ok, red)) {
     if (threadIdx.x == kMmaWarp * 32) {
       mma_commit(&b.drained);
       wait_phase(&b.drained, 0, MOE_DEFAULT_WAIT_LIMIT_NS);
