@@ -42,7 +42,7 @@
 // read once at the copy rate of 6.78 TB/s).  128 tokens, 8 experts, top 2, 4096
 // x 2048: bf16 90 us (60), e4m3 81 (30); 128 tokens, 64 experts, top 8, 2048 x
 // 1408, bf16: 192 us (163); 37 live of 64 tokens, 256 experts, top 8, 7168 x
-// 2048, e4m3: 1237 us (1156).  bf16: the up products read at 6.1, the down ones
+// 2048, e4m3: 1199-1215 us (1156).  bf16: the up products read at 6.1, the down ones
 // at 5.8 TB/s (DRAM reads 407 MB, the weights' 403); the rest is routing 5,
 // grouping 3, sorting and its barrier 4, the other barriers and the first
 // weights' latency 7, the sum 2 us.  e4m3: half the bytes and the same fixed
@@ -61,7 +61,10 @@ static_assert(kFirstConvertWarp + kConvertWarps == kSecondEpilogueWarp &&
                   (kSecondEpilogueWarp + 4) * 32 == kThreads, "roles");
 constexpr int kTileRows = 128;
 constexpr uint32_t kTileBytes = kTileRows * 128;  // 128 bytes of each row
-constexpr int kBoxTokens = 32;                    // of a tensor copy
+// Tokens of a tensor copy, and the step in which products take columns (a copy of
+// 32 fills more of the queue than most experts need: 1218 against 1199 us, 37 of
+// 64 tokens below).
+constexpr int kBoxTokens = 16;
 constexpr uint32_t kBoxBytes = kBoxTokens * 128;
 constexpr int kJobRing = 32;     // jobs on their way from the loading thread to the others
 constexpr int kMaxRing = 10;     // stages of the queue
@@ -203,14 +206,13 @@ struct ManyPhase {
     nq = g.nslots * tiles;
     given = a.arrived + kBarriers + (UP ? 0 : 1);
     // the same stages in both phases
-    const int n = boxed(min(b.max_tokens, kMaxN));
+    const int n = columns(min(b.max_tokens, kMaxN));
     stage_bytes = kWeightBytes + n * (FP8 ? 256 : 512);
     ring = min(static_cast<int>(kQueueBytes / stage_bytes), kMaxRing);
   }
 
   // Columns of the products, and rows that the tensor copies fill.
-  static __device__ __forceinline__ int columns(int tokens) { return (tokens + 15) / 16 * 16; }
-  static __device__ __forceinline__ int boxed(int tokens) {
+  static __device__ __forceinline__ int columns(int tokens) {
     return (tokens + kBoxTokens - 1) / kBoxTokens * kBoxTokens;
   }
   // Job number i, once the weights' thread has taken it: q, -1 at the end, -2
@@ -297,7 +299,7 @@ struct ManyPhase {
       }
       const int p = g.slot_expert[q / tiles];
       for (int c0 = 0; c0 < g.cnt[p]; c0 += kMaxN) {
-        const int n = boxed(min(g.cnt[p] - c0, kMaxN)), row = g.start[p] + c0;
+        const int n = columns(min(g.cnt[p] - c0, kMaxN)), row = g.start[p] + c0;
         const uint32_t bytes = n * (kLow ? 256 : 128);
         for (int kb = 0; kb < stages; ++kb) {
           if (!wait_phase(&b.empty[s.stage.slot], s.stage.parity ^ 1u, a.wait_ns)) return false;
@@ -378,9 +380,9 @@ struct ManyPhase {
       const int all = __shfl_sync(kFull, g.cnt[p], 0);
       for (int c0 = 0; c0 < all; c0 += kMaxN) {
         const int cnt = min(all - c0, kMaxN);
-        const int n = kLow ? 2 * boxed(cnt) : columns(cnt);
+        const int n = kLow ? 2 * columns(cnt) : columns(cnt);
         const uint32_t idesc = kFormat | (static_cast<uint32_t>(n >> 3) << 17);
-        const uint32_t x_next = boxed(cnt) * (kLow ? 16 : 8);
+        const uint32_t x_next = columns(cnt) * (kLow ? 16 : 8);
         for (int kb = 0; kb < stages; ++kb) {
           // e4m3: the converting warps have seen the stage land and the
           // accumulator free
@@ -532,7 +534,7 @@ struct ManyPhase {
           for (int n0 = first; n0 < last; n0 += 16) {
             uint32_t v[16], low[16];
             tmem_ld16(mine + s.acc.slot * kAccColumns + n0, v);
-            if (kLow) tmem_ld16(mine + s.acc.slot * kAccColumns + boxed(cnt) + n0, low);
+            if (kLow) tmem_ld16(mine + s.acc.slot * kAccColumns + columns(cnt) + n0, low);
             float f[16];
 #pragma unroll
             for (int j = 0; j < 16; ++j)
