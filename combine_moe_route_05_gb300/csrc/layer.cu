@@ -40,9 +40,9 @@
 // read once at the copy rate of 6.78 TB/s; ranges: different boxes): 16 tokens,
 // 128 experts, top 8, 2048 x 768, bf16: 130-134 us (115; DRAM reads 785 MB, the
 // weights' 778 and the tokens); 4 tokens, 256 experts and a shared one, 7168 x
-// 2048: 399-413 us (410); 1 token, 2048 x 768: 28 us (11): there the parts in
+// 2048: 399-413 us (410); 1 token, 2048 x 768: 27 us (11): there the parts in
 // front of and between the products bound it: routing 4.5, grouping 1, the
-// first weights' latency 2, two grid barriers 4, the sum 2 us.
+// first weights' latency 2, two grid barriers 3.5, the sum 2 us.
 #include "layer.cuh"
 
 namespace moe {

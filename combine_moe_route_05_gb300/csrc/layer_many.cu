@@ -404,7 +404,8 @@ struct ManyPhase {
               for (int k = 0; k < 4; ++k) {
                 const uint64_t tokens = x + i * x_next + k * 2;
                 if (FP8) mma_f16_tmem(d, w16 + (i * 4 + k) * 8, tokens, idesc, i + k > 0);
-                else mma_f16(d, w + i * (kTileBytes / 16) + k * 2, tokens, idesc, kb > 0 || i + k > 0);
+                else mma_f16(d, w + i * (kTileBytes / 16) + k * 2, tokens, idesc,
+                             kb > 0 || i + k > 0);
               }
             mma_commit(&b.empty[s.stage.slot]);
             if (FP8 || kb == stages - 1) mma_commit(&b.acc_full[s.acc.slot]);
@@ -493,7 +494,8 @@ struct ManyPhase {
         if (FP8) {
           static_assert(!FP8 || kMaxN <= 64, "32 columns a set");
           const int r = weight_row(tile, quarter * 32 + lane);
-          const int64_t row = static_cast<int64_t>(expert(slot)) * (((UP ? 2 * a.I : a.H) + 127) / 128) + r / 128;
+          const int64_t row =
+              static_cast<int64_t>(expert(slot)) * (((UP ? 2 * a.I : a.H) + 127) / 128) + r / 128;
           const float* scale = (UP ? a.s13 : a.s2) + row * stages;
           // what undoes the factor of column first + lane
           const int entry = g.order[begin + min(first + lane, cnt - 1)];
@@ -581,7 +583,8 @@ __device__ __forceinline__ void sort_tokens(const LayerArgs& a, const Groups& g,
       for (int k = 0; k < KS; ++k) {
         const int at = g.rank[t * KS + k];
         if (at != kNone)
-          st_vec(reinterpret_cast<uint8_t*>(a.y) + static_cast<int64_t>(at) * a.H * 2 + v * 16, o);
+          st_vec(reinterpret_cast<uint8_t*>(a.y) + static_cast<int64_t>(at) * a.H * 2 + v * 16,
+                 o);
       }
     }
   }
@@ -657,7 +660,8 @@ __global__ void __launch_bounds__(kThreads, 1) layer_many_kernel(
     const __grid_constant__ Maps maps, LayerArgs a) {
   constexpr uint32_t kColumns = 512;
   static_assert(ManyPhase<FP8, true>::kAcc * ManyPhase<FP8, true>::kAccColumns +
-                    (FP8 ? ManyPhase<FP8, true>::kAcc * kA16Columns : 0) <= kColumns, "tensor memory budget");
+                    (FP8 ? ManyPhase<FP8, true>::kAcc * kA16Columns : 0) <= kColumns,
+                "tensor memory budget");
   extern __shared__ __align__(16) uint8_t raw[];
   __shared__ int ok;
   __shared__ uint32_t red[kThreads / 32];
@@ -703,7 +707,7 @@ __global__ void __launch_bounds__(kThreads, 1) layer_many_kernel(
   __syncthreads();
   const uint32_t tmem = b.tmem;
   if (!layer_body<FP8>(a, g, b, maps, smem_addr(smem), tmem, &ok, red)) {
-    if (threadIdx.x == kMmaWarp * 32) {
+    if (warp == kMmaWarp && elect_one()) {  // the lane that issued them
       mma_commit(&b.drained);
       wait_phase(&b.drained, 0, MOE_DEFAULT_WAIT_LIMIT_NS);
     }
@@ -723,7 +727,8 @@ bool encode(CUtensorMap* m, const void* base, bool bytes, int rank,
   const cuuint32_t estr[5] = {1, 1, 1, 1, 1};
   return fn && fn(m, bytes ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank,
                   const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                  CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+                  CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 bool encode_maps(Maps* m, const LayerArgs& a, bool e4m3) {
