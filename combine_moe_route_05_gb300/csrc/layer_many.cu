@@ -46,8 +46,9 @@
 // at 5.8 TB/s (DRAM reads 407 MB, the weights' 403); the rest is routing 5,
 // grouping 3, sorting and its barrier 4, the other barriers and the first
 // weights' latency 7, the sum 2 us.  e4m3: half the bytes and the same fixed
-// parts; a stage takes some 900 cycles where the copy rate would allow 690,
-// most of it the epilogue, which reads and scales every column block's sums.
+// parts; a stage takes some 900 cycles, which are its copies': 28 KB, 12 of them
+// tokens, at 62 GB/s an SM (75 is the most that copies from L2 reached); without
+// the products, the conversion or the epilogue it takes as long, within 4%.
 #include "layer.cuh"
 
 namespace moe {
