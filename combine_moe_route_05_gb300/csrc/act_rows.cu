@@ -6,7 +6,8 @@
 // (1 + tanh z) / 2 = sigmoid(2 z)), so one exponential and one reciprocal
 // serve the value and the derivative a' = s + g c' s (1 - s).  1 - s is taken
 // as e^-c * s, which keeps its relative accuracy where s is near 1; below
-// c = -80 the sigmoid (under 2e-35) counts as 0, so that e^-c stays finite.
+// c = -87.3 the sigmoid, under 2^-126, is 0 (the fast division's result for a
+// denominator above 2^126), and a' with it.
 //
 // The dropout mask is never stored: Philox4x32-10 (Salmon, Moraes, Dror and
 // Shaw, "Parallel random numbers: as easy as 1, 2, 3", 2011) of the counter
@@ -89,8 +90,7 @@ __device__ __forceinline__ float exp_neg(float c) {
   return FAST ? __expf(-c) : expf(-c);
 }
 
-// The gate's value a(g).  Below c = -87.3 the sigmoid, under 2^-126, is 0 (the
-// fast division's result for a denominator above 2^126, infinity among them).
+// The gate's value a(g).
 template <int ACT, bool FAST>
 __device__ __forceinline__ float gate_value(float g) {
   constexpr float kR = 1.5957691216057308f;  // 2 sqrt(2 / pi)
@@ -113,11 +113,7 @@ __device__ __forceinline__ void gate_terms(float g, float& s, float& q, float& d
   }
   const float e = exp_neg<FAST>(c);
   s = __fdividef(1.0f, 1.0f + e);
-  q = e * s;
-  if (c < -80.0f) {
-    s = 0.0f;
-    q = 1.0f;
-  }
+  q = fminf(e * s, 1.0f);  // infinity times 0: 1
 }
 
 // The entry t*K + k of receive row r, -1 for a pad row.
@@ -208,9 +204,16 @@ __global__ void __launch_bounds__(kActThreads) act_rows_kernel(ActArgs a) {
   }
 }
 
-// Backward: one warp per receive row; the score gradient is the row's sum.
-template <typename Elt, int ACT, bool DROP>
-__global__ void __launch_bounds__(kActThreads) act_rows_bwd_kernel(ActArgs a) {
+// Backward: one warp per receive row; the score gradient is the row's sum, if
+// it is asked for (GW).  With dropout the issue slots bind nearly as much as
+// memory (some 40 instructions an element with GELU), and registers beside them:
+// 65536 rows of 2048, bf16, with score gradient: SiLU 197 us with 10 blocks an SM,
+// 200 with 12 and 204 where the compiler chose, GELU 227, 209 and 214 (either
+// without dropout: 197).  A warp per 64 vectors of a row (without GW) was
+// slower with dropout (SiLU 196 -> 211, GELU 212 -> 252).
+template <typename Elt, int ACT, bool DROP, bool GW>
+__global__ void __launch_bounds__(kActThreads, ACT == MOE_ACT_GELU ? 12 : 10)
+    act_rows_bwd_kernel(ActArgs a) {
   using VT = VecTraits<Elt>;
   constexpr int N = VT::N;
   constexpr bool kFast = N == 8;
@@ -221,7 +224,7 @@ __global__ void __launch_bounds__(kActThreads) act_rows_bwd_kernel(ActArgs a) {
     key = split64(a.rng[0]);
     offset = split64(a.rng[1]);
   }
-  if (a.gw) {  // entries without a receive row
+  if (GW) {  // entries without a receive row
     const int64_t n = static_cast<int64_t>(a.T) * a.K;
     for (int64_t i = static_cast<int64_t>(blockIdx.x) * kActThreads + threadIdx.x; i < n;
          i += static_cast<int64_t>(gridDim.x) * kActThreads)
@@ -236,6 +239,7 @@ __global__ void __launch_bounds__(kActThreads) act_rows_bwd_kernel(ActArgs a) {
     uint8_t* orow = a.out + static_cast<int64_t>(r) * 2 * a.half_bytes;
     const int ent = entry_of(a, r);
     const float w = a.rw ? __ldg(a.rw + r) : 1.0f;
+    const float ws = DROP ? w * a.keep_scale : w;
     float dot = 0.0f;
     if (ent < 0) {  // a pad row
       const float zero[N] = {};
@@ -253,22 +257,21 @@ __global__ void __launch_bounds__(kActThreads) act_rows_bwd_kernel(ActArgs a) {
       for (int j = 0; j < N; ++j) {
         float s, q, dc;
         gate_terms<ACT, kFast>(g[j], s, q, dc);
-        const bool live = !DROP || kept[j];
-        const float dk = DROP ? d[j] * a.keep_scale : d[j];
-        const float dw = dk * w;
+        const float dw = d[j] * ws;
         const float act = g[j] * s;
         const float da = s + act * q * dc;
-        dot = live ? fmaf(dk * act, u[j], dot) : dot;
+        const bool live = !DROP || kept[j];
+        if (GW) dot = live ? fmaf(d[j] * act, u[j], dot) : dot;
         g[j] = live ? dw * u[j] * da : 0.0f;
         u[j] = live ? dw * act : 0.0f;
       }
       st_vec(orow + v * 16, VT::from_f32(g));
       st_vec(orow + a.half_bytes + v * 16, VT::from_f32(u));
     }
-    if (a.gw) {
+    if (GW) {
 #pragma unroll
       for (int off = 16; off > 0; off >>= 1) dot += __shfl_xor_sync(kFull, dot, off);
-      if (lane == 0) a.gw[ent] = dot;
+      if (lane == 0) a.gw[ent] = DROP ? dot * a.keep_scale : dot;
     }
   }
 }
@@ -295,8 +298,11 @@ ActArgs act_args(const moe_handle* h, int I, int dtype, const float* rw, double 
 
 template <typename Elt, int ACT, bool DROP>
 cudaError_t launch_t(const moe_handle* h, const ActArgs& a, bool bwd, cudaStream_t s) {
-  auto k = bwd ? act_rows_bwd_kernel<Elt, ACT, DROP> : act_rows_kernel<Elt, ACT, DROP>;
-  const long long items = static_cast<long long>(a.rows) * (bwd ? 1 : (a.nvec + kPiece - 1) / kPiece);
+  auto k = !bwd   ? act_rows_kernel<Elt, ACT, DROP>
+           : a.gw ? act_rows_bwd_kernel<Elt, ACT, DROP, true>
+                  : act_rows_bwd_kernel<Elt, ACT, DROP, false>;
+  const long long items =
+      static_cast<long long>(a.rows) * (bwd ? 1 : (a.nvec + kPiece - 1) / kPiece);
   const long long blocks = (items + kActThreads / 32 - 1) / (kActThreads / 32);
   // a block per kActThreads / 32 items, not one wave of resident blocks: the
   // SMs take blocks at their own pace (DeepSeek-V3 shape with dropout: forward
