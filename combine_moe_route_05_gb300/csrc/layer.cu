@@ -38,9 +38,9 @@
 //
 // Measured, routing included (GPU time of a replayed graph; in brackets: weights
 // read once at the copy rate of 6.78 TB/s; ranges: different boxes): 16 tokens,
-// 128 experts, top 8, 2048 x 768, bf16: 130-134 us (115; DRAM reads 785 MB, the
+// 128 experts, top 8, 2048 x 768, bf16: 129-134 us (115; DRAM reads 785 MB, the
 // weights' 778 and the tokens); 4 tokens, 256 experts and a shared one, 7168 x
-// 2048: 399-413 us (410); 1 token, 2048 x 768: 27 us (11): there the parts in
+// 2048: 397-413 us (410); 1 token, 2048 x 768: 27 us (11): there the parts in
 // front of and between the products bound it: routing 4.5, grouping 1, the
 // first weights' latency 2, two grid barriers 3.5, the sum 2 us.
 #include "layer.cuh"
@@ -681,14 +681,15 @@ cudaError_t launch_layer(const moe_handle* h, const moe_layer_args& q, int T, vo
   // faster one.  bf16: 3 to 7, the more the fewer weights there are (64 experts,
   // top 8, 2048 x 1408: 184 against 181 us at 4 tokens, 194 against 183 at 5;
   // 1024 x 512: 54 against 59 at 5, 65 against 59 at 8).  e4m3, whose weights
-  // the kernel here converts again for every 4 tokens: 0.5 to 1.5 (2048 x 1408:
-  // 80 against 78 us at 0.5, 123 against 97 at 1; 16 experts, top 2, 4096 x
-  // 2048: 71 against 78 at 1, 93 against 89 at 1.5).  Packed up to 2 tokens (128
+  // the kernel here converts again for every 4 tokens: 1, or some 48 entries in
+  // all (16 experts, top 2, 4096 x 2048: 71 against 78 us at 16 entries, 93
+  // against 89 at 24; 256 experts, top 8, 7168 x 2048: 234 against 250 at 32
+  // entries, 426 against 408 at 64).  Packed up to 2 tokens (128
   // experts, top 8, 2048 x 768: 92 us, unpacked 94, at 0.5; 211 and 206 at 4,
   // where 4 tokens to a tile make second passes).
   const int64_t entries = static_cast<int64_t>(T) * K;
   const bool e4m3 = q.weight_dtype == MOE_E4M3;
-  if (entries > (e4m3 ? 1 : 5) * a.E) return launch_layer_many(h, a, e4m3, s);
+  if (entries > (e4m3 ? (a.E < 48 ? a.E : 48) : 5 * a.E)) return launch_layer_many(h, a, e4m3, s);
   if (e4m3) return launch_few<true, true>(h, a, s);
   return entries > 2 * a.E ? launch_few<false, false>(h, a, s) : launch_few<false, true>(h, a, s);
 }
