@@ -505,6 +505,31 @@ def test_calls_on_streams_of_three_priorities():
         p.check()
 
 
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_beside_the_w2_product_on_another_stream(e4m3):
+    """Both kernels want whole SMs and their tensor memory: they take turns."""
+    p = Problem(T=100, E=8, K=2, H=1024, I=512, e4m3=e4m3)
+    T, H, I = 2048, 1024, 512
+    r = moe.MoeRouter(8, 2, 1, T)
+    g = torch.Generator().manual_seed(5)
+    idx, w = r.route(torch.randn(T, 8, generator=g).to(dev()))
+    r.layout(idx)
+    h = torch.randn(r.h.recv_rows, I, generator=g).to(dev(), torch.bfloat16)
+    rw = torch.rand(r.h.recv_rows, generator=g).to(dev())
+    w2 = (torch.randn(8, H, I, generator=g) * I ** -0.5).to(dev(), torch.bfloat16)
+    want = r.w2_absorbed(h, rw, w2)
+    logits = to_dev(p.logits)
+    y = torch.empty_like(want)
+    torch.cuda.synchronize()
+    a, b = torch.cuda.Stream(), torch.cuda.Stream(priority=-1)
+    for _ in range(60):
+        moe.moe_w2_absorbed(r.h, h, rw, w2, y, stream=a)
+        p.call(logits=logits, stream=b)
+    torch.cuda.synchronize()
+    assert moe.moe_read_device_status(r.h) == 0 and torch.equal(y, want)
+    p.check()
+
+
 def test_method_on_another_stream_keeps_its_workspace(monkeypatch):
     """The workspace freed when the method returns is not given to the current
     stream while the other one may still use it."""
