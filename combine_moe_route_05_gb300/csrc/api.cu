@@ -171,6 +171,7 @@ moe_status moe_handle_create(const moe_config* c, void* d_workspace, size_t work
   // fails with "no kernel image" on a device the library was not built for
   if (moe::prepare_layout_kernels() != cudaSuccess) return MOE_ERR_CUDA;
   if (moe::prepare_w2_kernel() != cudaSuccess) return MOE_ERR_CUDA;
+  if (moe::prepare_layer_kernels() != cudaSuccess) return MOE_ERR_CUDA;
 
   uint8_t* ws = static_cast<uint8_t*>(d_workspace);
   if (cudaMemset(ws, 0, p.S + sizeof(int32_t)) != cudaSuccess) return MOE_ERR_CUDA;

@@ -114,6 +114,7 @@ struct LayerPlan {
   size_t a, a32, y, x16, xscale, amax, arrived, total;
 };
 LayerPlan layer_plan(int T, int K, int S, int H, int I);
+cudaError_t prepare_layer_kernels();
 cudaError_t launch_layer(const moe_handle* h, const moe_layer_args& q, int T, void* workspace,
                          cudaStream_t s);
 

@@ -107,8 +107,7 @@ constexpr int kSumBytes = 2 * kSumFloats * 4;
 constexpr int kTicketBytes = kWarps * kTickets * 4;
 constexpr int kScaleBytes = kWarps * kMaxStages * 2 * 4;
 constexpr size_t kFixedBytes = kQueueBytes + kSumBytes + kTicketBytes + kScaleBytes;
-static_assert(kFixedBytes + groups_bytes(MOE_LAYER_MAX_TOKENS, MOE_MAX_TOPK + MOE_LAYER_MAX_SHARED,
-                                         kMaxExperts) + 64 <= 227 * 1024, "shared memory budget");
+static_assert(kFixedBytes + kMaxGroupsBytes + 64 <= 227 * 1024, "shared memory budget");
 
 // Tokens [c0, c0 + kTokens) of the expert in slot `slot`, output tile `tile`;
 // q = slot * tiles + tile, i its place in the team's sequence.
@@ -614,16 +613,18 @@ __global__ void layer_start_kernel(uint32_t* arrived) {
 
 template <bool FP8, bool PACKED>
 cudaError_t launch_few(const moe_handle* h, const LayerArgs& a, cudaStream_t s) {
-  auto k = layer_kernel<FP8, PACKED>;
   const size_t smem = kFixedBytes + groups_bytes(a.T, a.K + a.S, a.E + a.S);
-  // per device and cheap: no state to keep
-  const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             static_cast<int>(smem));
-  if (e != cudaSuccess) return e;
-  return launch_chained(k, dim3(h->num_sms), dim3(kThreads), smem, s, true, a);
+  return launch_chained(layer_kernel<FP8, PACKED>, dim3(h->num_sms), dim3(kThreads), smem, s, true, a);
 }
 
 }  // namespace
+
+cudaError_t prepare_layer_kernels() {
+  cudaError_t e = allow_shared(layer_kernel<false, false>, kFixedBytes);
+  if (e == cudaSuccess) e = allow_shared(layer_kernel<false, true>, kFixedBytes);
+  if (e == cudaSuccess) e = allow_shared(layer_kernel<true, true>, kFixedBytes);
+  return e == cudaSuccess ? prepare_layer_many_kernels() : e;
+}
 
 LayerPlan layer_plan(int T, int K, int S, int H, int I) {
   auto up = [](size_t b) { return (b + 255) / 256 * 256; };

@@ -74,6 +74,19 @@ __host__ __device__ constexpr size_t groups_bytes(int T, int KS, int n_exp) {
          up16(4ull * (kMaxWarps + 1));
 }
 
+constexpr size_t kMaxGroupsBytes =
+    groups_bytes(MOE_LAYER_MAX_TOKENS, MOE_MAX_TOPK + MOE_LAYER_MAX_SHARED, kMaxExperts);
+
+// Lets a kernel have the shared memory of its largest call.  The limit belongs to
+// the kernel and the device, so it is set once, at the handle's creation, and to
+// a constant: set by each call to its own size it could go down between another
+// thread's setting and launch.
+template <typename Kernel>
+cudaError_t allow_shared(Kernel kernel, size_t fixed) {
+  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              static_cast<int>(fixed + kMaxGroupsBytes));
+}
+
 __device__ __forceinline__ int expert_of(const LayerArgs& a, int entry) {
   const int t = entry / (a.K + a.S), k = entry - t * (a.K + a.S);
   if (k >= a.K) return k - a.K;
@@ -409,6 +422,7 @@ __device__ __forceinline__ void sum_entries(const LayerArgs& a, const Groups& g)
 }  // namespace
 
 // The kernel on the tensor memory, for many tokens an expert.
+cudaError_t prepare_layer_many_kernels();
 cudaError_t launch_layer_many(const moe_handle* h, const LayerArgs& a, bool e4m3, cudaStream_t s);
 
 }  // namespace moe

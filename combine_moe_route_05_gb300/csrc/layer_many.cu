@@ -74,8 +74,7 @@ constexpr size_t kQueueBytes = 208 * 1024 - 1024;
 constexpr uint32_t kA16Columns = 64;  // of tensor memory: 128 fp16 columns of the weights
 constexpr size_t kBarrierBytes = 1024;
 constexpr size_t kFixedBytes = 1024 /* alignment */ + kQueueBytes + kBarrierBytes;
-static_assert(kFixedBytes + groups_bytes(MOE_LAYER_MAX_TOKENS, MOE_MAX_TOPK + MOE_LAYER_MAX_SHARED,
-                                         kMaxExperts) + 256 <= 227 * 1024, "shared memory budget");
+static_assert(kFixedBytes + kMaxGroupsBytes + 256 <= 227 * 1024, "shared memory budget");
 
 struct Barriers {
   uint64_t landed[kMaxRing];  // a stage is there (an arrival per loading thread)
@@ -760,15 +759,16 @@ template <bool FP8>
 cudaError_t launch_one(const moe_handle* h, const LayerArgs& a, cudaStream_t s) {
   Maps maps;
   if (!encode_maps(&maps, a, FP8)) return cudaErrorInvalidValue;
-  auto k = layer_many_kernel<FP8>;
   const size_t smem = kFixedBytes + groups_bytes(a.T, a.K + a.S, a.E + a.S);
-  const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             static_cast<int>(smem));
-  if (e != cudaSuccess) return e;
-  return launch_chained(k, dim3(h->num_sms), dim3(kThreads), smem, s, true, maps, a);
+  return launch_chained(layer_many_kernel<FP8>, dim3(h->num_sms), dim3(kThreads), smem, s, true, maps, a);
 }
 
 }  // namespace
+
+cudaError_t prepare_layer_many_kernels() {
+  const cudaError_t e = allow_shared(layer_many_kernel<false>, kFixedBytes);
+  return e == cudaSuccess ? allow_shared(layer_many_kernel<true>, kFixedBytes) : e;
+}
 
 cudaError_t launch_layer_many(const moe_handle* h, const LayerArgs& a, bool e4m3, cudaStream_t s) {
   return e4m3 ? launch_one<true>(h, a, s) : launch_one<false>(h, a, s);

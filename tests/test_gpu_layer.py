@@ -3,6 +3,7 @@ element-wise bound that tests/expert_ref.py derives; its routing against the
 oracle; and the calls around it (padded batches, given routes, graphs, streams,
 in place, the separate calls of the same layer)."""
 import ctypes
+import threading
 
 import numpy as np
 import pytest
@@ -629,3 +630,41 @@ def test_weights_past_32_bit_offsets():
     logits[0, 40] = 5.0
     out, idx, _ = r.layer(x, logits, w13, w2)
     assert idx.item() == 40 and out[0, 7000].item() == 32.0 and out.abs().sum().item() == 32.0
+
+
+@pytest.mark.parametrize("large,small", [
+    (dict(T=128, E=512, K=8, H=16, I=16), dict(T=1, E=4, K=1, H=16, I=16)),
+    (dict(T=128, E=160, K=5, H=16, I=16), dict(T=4, E=1, K=1, H=16, I=16)),
+    (dict(T=6, E=512, K=8, H=16, I=16, e4m3=True), dict(T=1, E=4, K=1, H=16, I=16, e4m3=True)),
+    (dict(T=128, E=40, K=16, H=16, I=16, shared=4), dict(T=8, E=1, K=1, H=16, I=16)),
+    (dict(T=128, E=40, K=16, H=16, I=16, shared=4, e4m3=True), dict(T=8, E=1, K=1, H=16, I=16, e4m3=True)),
+], ids=["packed", "unpacked", "e4m3", "many", "many-e4m3"])
+def test_two_host_threads_with_tables_of_other_sizes(large, small):
+    """The same kernel called from two threads, each with its own handle, stream
+    and workspace, once with the largest tables and once with the smallest."""
+    ps = [Problem(**kw) for kw in (large, small)]
+    streams = [torch.cuda.Stream() for _ in ps]
+    logits = [to_dev(p.logits) for p in ps]
+    torch.cuda.synchronize()
+    start, refused = threading.Barrier(2), [0, 0]
+
+    def work(i):
+        p, L = ps[i], moe.lib()
+        a = moe.MoeLayerArgs(p.x.data_ptr(), logits[i].data_ptr(), None, None, p.w13.data_ptr(), p.w2.data_ptr(),
+                             p.s13.data_ptr() if p.s13 is not None else None,
+                             p.s2.data_ptr() if p.s2 is not None else None, p.out.data_ptr(), p.idx.data_ptr(),
+                             p.w.data_ptr(), p.H, p.I, p.S, moe.MOE_BF16 if p.s13 is None else moe.MOE_E4M3, 0)
+        with torch.cuda.device(dev()):
+            start.wait()
+            for _ in range(1500):
+                refused[i] += L.moe_layer(p.r.h.ptr, ctypes.byref(a), p.T, p.ws.data_ptr(), p.ws.numel(),
+                                          streams[i].cuda_stream) != moe.MOE_OK
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert refused == [0, 0]
+    for p in ps:
+        p.check()
