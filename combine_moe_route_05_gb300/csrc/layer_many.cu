@@ -57,6 +57,7 @@ namespace {
 constexpr int kThreads = 640;
 constexpr int kEpilogueWarps = 8, kSecondEpilogueWarp = 16;
 constexpr int kMmaWarp = 4, kWeightWarp = 5, kTokenWarp = 6, kTokenWarps = 2;
+constexpr int kLoadWarps = 1 + kTokenWarps;
 constexpr int kFirstConvertWarp = 8, kConvertWarps = 8;
 static_assert(kFirstConvertWarp + kConvertWarps == kSecondEpilogueWarp &&
                   (kSecondEpilogueWarp + 4) * 32 == kThreads, "roles");
@@ -85,6 +86,7 @@ struct Barriers {
   uint64_t acc_full[kMaxAcc];   // an accumulator is complete
   uint64_t acc_empty[kMaxAcc];  // and read (an arrival per epilogue warp)
   uint64_t drained;           // after a wait that gave up: no product is under way
+  int32_t issued[kLoadWarps]; // and the stages that each loading thread began
   unsigned long long jobs[kJobRing];  // number, counted from 1 << 32, plus q + 1 (0: the end)
   uint32_t tmem;
   int32_t max_tokens;         // of one expert
@@ -316,11 +318,24 @@ struct ManyPhase {
     }
   }
 
-  // After a wait that gave up: what a loading thread asked for has landed (for
-  // certain after the default limit).
+  // After a wait that gave up, by all threads: waits until what was asked for has
+  // landed, a few microseconds (for certain after the default limit, whatever the
+  // handle's).  The loading threads stand at different stages: those behind
+  // arrive, without bytes, for the stages that another has begun, which would
+  // not complete otherwise.  Whoever began a stage had seen the last use of its
+  // place end, so these arrivals count for the stage and not for that use.
   __device__ __forceinline__ void drain(const State& s) const {
-    for (int i = max(s.issued - ring, 0); i < s.issued; ++i)
-      if (!wait_phase(&b.landed[i % ring], (i / ring) & 1u, MOE_DEFAULT_WAIT_LIMIT_NS)) return;
+    const int i = static_cast<int>(threadIdx.x >> 5) - kWeightWarp;
+    const bool loads = threadIdx.x % 32 == 0 && i >= 0 && i < kLoadWarps;
+    if (loads) b.issued[i] = s.issued;
+    __syncthreads();
+    if (!loads) return;
+    int last = 0;
+#pragma unroll
+    for (int j = 0; j < kLoadWarps; ++j) last = max(last, b.issued[j]);
+    for (int n = s.issued; n < last; ++n) mbar_arrive(&b.landed[n % ring]);
+    for (int n = max(last - ring, 0); n < last; ++n)
+      if (!wait_phase(&b.landed[n % ring], (n / ring) & 1u, MOE_DEFAULT_WAIT_LIMIT_NS)) return;
   }
 
   // -- converting warps (e4m3)
@@ -650,8 +665,7 @@ __device__ __forceinline__ bool layer_body(const LayerArgs& a, const Groups& g, 
     if (grid_wait(a, arrived, ok)) sum_entries<kThreads>(a, g);
     return true;
   }
-  const int warp = threadIdx.x >> 5;
-  if (threadIdx.x % 32 == 0 && warp >= kWeightWarp && warp < kTokenWarp + kTokenWarps) down.drain(s);
+  down.drain(s);
   return false;
 }
 
@@ -675,7 +689,7 @@ __global__ void __launch_bounds__(kThreads, 1) layer_many_kernel(
                                 reinterpret_cast<uint32_t*>(smem));
   if (threadIdx.x == 0) {
     for (int i = 0; i < kMaxRing; ++i) {
-      mbar_init(&b.landed[i], 1 + kTokenWarps);
+      mbar_init(&b.landed[i], kLoadWarps);
       mbar_init(&b.empty[i], 1);
     }
     for (int i = 0; i < kMaxAcc; ++i) {

@@ -4,6 +4,7 @@ oracle; and the calls around it (padded batches, given routes, graphs, streams,
 in place, the separate calls of the same layer)."""
 import ctypes
 import threading
+import time
 
 import numpy as np
 import pytest
@@ -668,3 +669,50 @@ def test_two_host_threads_with_tables_of_other_sizes(large, small):
     assert refused == [0, 0]
     for p in ps:
         p.check()
+
+
+@pytest.mark.parametrize("kw", [dict(T=60, E=4, K=2, H=512, I=256), dict(T=60, E=4, K=2, H=512, I=256, e4m3=True),
+                                dict(T=6, E=8, K=2, H=512, I=256), dict(T=4, E=8, K=2, H=512, I=256, e4m3=True)],
+                         ids=["many", "many-e4m3", "few", "few-e4m3"])
+def test_a_wait_that_gives_up_ends_the_call_soon(kw):
+    """The kernel ends within the handle's limit and the time of the copies under
+    way, not after the default limit of a second."""
+    p = Problem(**kw)
+    logits = to_dev(p.logits)
+    p.call(logits=logits)
+    moe.moe_set_wait_limit(p.r.h, 1)
+    torch.cuda.synchronize()
+    t0 = time.monotonic()
+    p.call(logits=logits)
+    torch.cuda.synchronize()
+    assert time.monotonic() - t0 < 0.5
+    assert moe.moe_read_device_status(p.r.h) == moe.MOE_DEVERR_TIMEOUT
+    moe.moe_set_wait_limit(p.r.h, 0)
+    moe.moe_clear_device_status(p.r.h)
+    p.call()
+    p.check()
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_waits_that_give_up_anywhere_in_the_kernel(e4m3):
+    """Limits from nothing to about the kernel's time: the waits of every part run
+    out in some block.  Each call ends soon, and the next one is right."""
+    p = Problem(T=128, E=8, K=2, H=2048, I=1024, shared=1, e4m3=e4m3)
+    logits = to_dev(p.logits)
+    p.call(logits=logits)
+    want = p.check()[2]
+    for limit in (1, 1000, 2000, 4000, 8000, 16000, 32000, 64000):
+        moe.moe_set_wait_limit(p.r.h, limit)
+        torch.cuda.synchronize()
+        t0 = time.monotonic()
+        for _ in range(3):
+            p.call(logits=logits)
+        torch.cuda.synchronize()
+        assert time.monotonic() - t0 < 0.5
+        assert moe.moe_read_device_status(p.r.h) in (0, moe.MOE_DEVERR_TIMEOUT)
+        moe.moe_set_wait_limit(p.r.h, 0)
+        moe.moe_clear_device_status(p.r.h)
+        p.call(logits=logits)
+        torch.cuda.synchronize()
+        assert moe.moe_read_device_status(p.r.h) == 0
+        assert np.array_equal(p.out.double().cpu().numpy(), want)
