@@ -573,8 +573,19 @@ def layout_tensors(h):
     return out
 
 
+def _kept_for_caller(stream, *tensors):
+    """Tensors that belong to `stream`, for use on the current one too: freed, their
+    memory is not taken again before the work queued there by then is done."""
+    if stream is not None and stream != torch.cuda.current_stream(stream.device):
+        for t in tensors:
+            if t is not None:
+                t.record_stream(torch.cuda.current_stream(stream.device))
+
+
 class MoeRouter:
-    """Owns a handle; methods allocate their outputs and call the moe_* bindings."""
+    """Owns a handle; methods allocate their outputs and call the moe_* bindings.
+    act_rows, act_rows_bwd and layer allocate on the stream that they run on (the
+    others on the current one)."""
 
     def __init__(self, num_experts, top_k, num_ranks, max_tokens, **kw):
         self.cfg = make_config(num_experts, top_k, num_ranks, max_tokens, **kw)
@@ -655,16 +666,20 @@ class MoeRouter:
     def act_rows(self, gu, recv_w=None, act="silu", p=0.0, rng=None, stream=None):
         """Gated activation of [rows, 2I] gate/up rows with the routed score
         and dropout."""
-        hs = torch.empty(gu.shape[0], gu.shape[1] // 2, dtype=gu.dtype, device=gu.device)
-        moe_act_rows(self.h, gu, recv_w, hs, act, p, rng, stream)
+        with torch.cuda.stream(stream):
+            hs = torch.empty(gu.shape[0], gu.shape[1] // 2, dtype=gu.dtype, device=gu.device)
+            moe_act_rows(self.h, gu, recv_w, hs, act, p, rng, stream)
+        _kept_for_caller(stream, hs)
         return hs
 
     def act_rows_bwd(self, ghs, gu, recv_w=None, act="silu", p=0.0, rng=None, stream=None):
         """(ggu, gw); gw is None without recv_w."""
-        ggu = torch.empty_like(gu)
-        gw = torch.empty(max(self.h.T, 0), self.h.K, dtype=torch.float32, device=gu.device) \
-            if recv_w is not None else None
-        moe_act_rows_bwd(self.h, ghs, gu, recv_w, ggu, gw, act, p, rng, stream)
+        with torch.cuda.stream(stream):
+            ggu = torch.empty_like(gu)
+            gw = torch.empty(max(self.h.T, 0), self.h.K, dtype=torch.float32, device=gu.device) \
+                if recv_w is not None else None
+            moe_act_rows_bwd(self.h, ghs, gu, recv_w, ggu, gw, act, p, rng, stream)
+        _kept_for_caller(stream, ggu, gw)
         return ggu, gw
 
     def layer(self, x, logits, w13, w2, bias=None, s13=None, s2=None, live=None, act="silu",
@@ -684,6 +699,7 @@ class MoeRouter:
             ws = layer_workspace(self.h, H, w2.shape[2], num_shared)
             moe_layer(self.h, x, logits, w13, w2, out, idx, w, ws, bias, s13, s2, live, act,
                       num_shared, stream)
+        _kept_for_caller(stream, out, idx, w)
         return out, idx, w
 
     def w2_absorbed(self, hrows, recv_w, w2, stream=None):

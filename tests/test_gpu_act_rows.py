@@ -308,3 +308,35 @@ def test_empty_batch_and_other_stream():
     got = r.act_rows(gu, rw, p=0.1, rng=rng_of(1, 2), stream=s)
     s.synchronize()
     assert torch.equal(got, want)
+
+
+def outputs_of(method, stream):
+    """Their (address, bytes), freed, after the current stream has been made to wait
+    for `stream` and given some 50 ms of work."""
+    out = method(stream)
+    torch.cuda.current_stream().wait_stream(stream)
+    torch.cuda._sleep(100000000)
+    return [(t.data_ptr(), t.numel() * t.element_size()) for t in out]
+
+
+@pytest.mark.parametrize("name", ["act_rows", "act_rows_bwd", "layer"])
+def test_methods_on_another_stream_keep_their_outputs(name):
+    """What a method returns, once freed, is given neither to the current stream
+    while the other one may still write it nor to the other one while the current
+    one may still read it."""
+    r, ent, end, gu, ghs, rw = problem(100, 4, 2, 64, "bf16")
+    x = torch.randn(8, 64, device=dev()).to(torch.bfloat16)
+    w13, w2 = torch.zeros(4, 64, 64, device=dev()).to(torch.bfloat16), torch.zeros(4, 64, 32, device=dev()).to(torch.bfloat16)
+    logits = torch.randn(8, 4, device=dev())
+    method = {"act_rows": lambda s: (r.act_rows(gu, rw, stream=s),),
+              "act_rows_bwd": lambda s: r.act_rows_bwd(ghs, gu, rw, stream=s),
+              "layer": lambda s: r.layer(x, logits, w13, w2, stream=s)}[name]
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    seen = outputs_of(method, s)
+    here = [torch.empty(n, dtype=torch.uint8, device=dev()) for _, n in seen for _ in range(2)]
+    with torch.cuda.stream(s):
+        there = [torch.empty(n, dtype=torch.uint8, device=dev()) for _, n in seen for _ in range(2)]
+    assert not torch.cuda.current_stream().query()  # the current stream is not done with them
+    assert not {p for p, _ in seen} & {t.data_ptr() for t in here + there}
+    torch.cuda.synchronize()
