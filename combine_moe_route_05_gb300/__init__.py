@@ -221,7 +221,9 @@ class Handle:
         nbytes = moe_workspace_bytes(cfg)
         if nbytes == 0:
             raise MoeError("moe_workspace_bytes", MOE_ERR_INVALID)
-        dev = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
+        dev = torch.device("cuda" if device is None else device)
+        if dev.type == "cuda" and dev.index is None:  # tensors' devices have an index
+            dev = torch.device("cuda", torch.cuda.current_device())
         with torch.cuda.device(dev):
             # 256-byte aligned: the caching allocator returns 512-byte aligned blocks
             self.workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)

@@ -273,3 +273,16 @@ def test_weights_over_the_exponent_range(score_fn, renorm):
         idx, w = oracle.route_sigmoid_grouped(logits, None, K, 1, 1, 1, renorm)
     assert np.array_equal(to_host(gi), idx)
     assert_ulp(to_host(gw_), w, 1, "w")
+
+
+def test_handle_on_a_device_without_an_index():
+    """device="cuda" is the current one: row calls and the status calls take it."""
+    h = moe.Handle(moe.make_config(8, 2, 1, 16), device="cuda")
+    assert h.device == dev()
+    moe.moe_clear_device_status(h)
+    logits = torch.randn(16, 8, device=dev())
+    idx = torch.empty(16, 2, dtype=torch.int32, device=dev())
+    w = torch.empty(16, 2, device=dev())
+    moe.moe_route_topk(h, logits, None, idx, w)
+    assert moe.moe_read_device_status(h) == 0
+    assert torch.equal(idx.long(), logits.topk(2).indices)
