@@ -100,6 +100,9 @@ constexpr int kMaxTeam = 8;
 constexpr int kSteps = 2;  // of 64 bytes of a row, in a stage of the queue
 constexpr int kQueueBytes = 192 * 1024;
 constexpr int kMaxStages = 8;
+// a team holds tickets for at most kMaxStages + 1 coming jobs (`fixed` below), and
+// one warp may still read the last one's
+static_assert(kMaxStages + 2 < kTickets, "tickets");
 // behind the queue: two buffers of partial sums, tickets, block scales of the
 // stages (e4m3)
 constexpr int kSumFloats = kWarps * 4 * 32;

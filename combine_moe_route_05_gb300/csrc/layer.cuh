@@ -45,6 +45,9 @@ constexpr int kMaxEntries = MOE_LAYER_MAX_TOKENS * (MOE_MAX_TOPK + MOE_LAYER_MAX
 constexpr int kMaxExperts = MOE_MAX_EXPERTS + MOE_LAYER_MAX_SHARED;
 constexpr unsigned kFull = 0xffffffffu;
 constexpr uint16_t kNone = 0xffff;
+static_assert(kMaxEntries < kNone && kMaxExperts < kNone, "16-bit tables");
+constexpr int kMaskWords = 4;  // of 32 tokens, for each expert
+static_assert(MOE_LAYER_MAX_TOKENS <= 32 * kMaskWords, "token masks");
 constexpr int kBarriers = 4;  // grid barriers of a call, at most
 constexpr int kTickets = 16;  // of a team's coming jobs
 
@@ -94,7 +97,7 @@ __device__ __forceinline__ int expert_of(const LayerArgs& a, int entry) {
   return static_cast<unsigned>(e) < static_cast<unsigned>(a.E) ? e + a.S : e == -1 ? -1 : -2;
 }
 
-// The tables, in `smem`.  With `masks` (4 words of scratch an expert) the
+// The tables, in `smem`.  With `masks` (kMaskWords of scratch an expert) the
 // entries of an expert come in the order of their tokens, so that all blocks
 // agree on it.
 template <int kThreads, bool kOrdered>
@@ -152,7 +155,7 @@ __device__ __forceinline__ void group_entries(const LayerArgs& a, Groups& g, uin
     return;
   }
   if (kOrdered) {
-    for (int i = tid; i < 4 * n_exp; i += kThreads) masks[i] = 0;
+    for (int i = tid; i < kMaskWords * n_exp; i += kThreads) masks[i] = 0;
   } else {
     for (int e = tid; e < n_exp; e += kThreads) g.cnt[e] = 0;
   }
@@ -178,7 +181,7 @@ __device__ __forceinline__ void group_entries(const LayerArgs& a, Groups& g, uin
     }
     if (kOrdered) {
       const int t = i / KS;
-      if (ok) atomicOr(&masks[4 * e + t / 32], 1u << (t % 32));
+      if (ok) atomicOr(&masks[kMaskWords * e + t / 32], 1u << (t % 32));
       g.rank[i] = ok ? 0 : kNone;
     } else {
       g.rank[i] = ok ? static_cast<uint16_t>(atomicAdd(&g.cnt[e], 1)) : kNone;
@@ -194,7 +197,7 @@ __device__ __forceinline__ void group_entries(const LayerArgs& a, Groups& g, uin
     int c = 0;
     if (e < n_exp) {
       if (kOrdered) {
-        for (int i = 0; i < 4; ++i) c += __popc(masks[4 * e + i]);
+        for (int i = 0; i < kMaskWords; ++i) c += __popc(masks[kMaskWords * e + i]);
         g.cnt[e] = c;
       } else {
         c = g.cnt[e];
@@ -211,7 +214,7 @@ __device__ __forceinline__ void group_entries(const LayerArgs& a, Groups& g, uin
   }
   if (lane == 31) g.head[warp] = inc;
   // the entries' experts, before `order` takes the entries
-  constexpr int kMine = kMaxEntries / kThreads;
+  constexpr int kMine = (kMaxEntries + kThreads - 1) / kThreads;
   uint16_t mine[kMine];
 #pragma unroll
   for (int j = 0; j < kMine; ++j)
@@ -236,7 +239,7 @@ __device__ __forceinline__ void group_entries(const LayerArgs& a, Groups& g, uin
     if (i < n && g.rank[i] != kNone) {
       int at = g.start[mine[j]] + g.rank[i];
       if (kOrdered) {  // rank: 0 so far
-        const uint32_t* mask = masks + 4 * mine[j];
+        const uint32_t* mask = masks + kMaskWords * mine[j];
         const int t = i / KS;
         at += __popc(mask[t / 32] & ((1u << (t % 32)) - 1u));
         for (int w = 0; w < t / 32; ++w) at += __popc(mask[w]);

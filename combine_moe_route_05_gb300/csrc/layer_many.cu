@@ -75,6 +75,7 @@ constexpr size_t kQueueBytes = 208 * 1024 - 1024;
 constexpr uint32_t kA16Columns = 64;  // of tensor memory: 128 fp16 columns of the weights
 constexpr size_t kBarrierBytes = 1024;
 constexpr size_t kFixedBytes = 1024 /* alignment */ + kQueueBytes + kBarrierBytes;
+static_assert(kMaskWords * kMaxExperts * 4 <= kQueueBytes, "masks in the queue's place");
 static_assert(kFixedBytes + kMaxGroupsBytes + 256 <= 227 * 1024, "shared memory budget");
 
 struct Barriers {
