@@ -691,9 +691,22 @@ cudaError_t launch_layer(const moe_handle* h, const moe_layer_args& q, int T, vo
   // entries, 426 against 408 at 64).  Packed up to 2 tokens (128
   // experts, top 8, 2048 x 768: 92 us, unpacked 94, at 0.5; 211 and 206 at 4,
   // where 4 tokens to a tile make second passes).
+  //
+  // A shared expert has all T tokens, whose passes over a tile (8 or 4 tokens
+  // each) one team makes in turn, and those of several run beside one another:
+  // from T (S + 1) = 24 (16 experts) to 56 (128) on the other kernel is the faster
+  // one with bf16 weights, from 16 on with e4m3 weights (64 experts, top 1, 2048 x
+  // 1408: bf16 with 1 shared expert 86.6 against 86.6 us at 28 tokens, 211 against
+  // 187 at 128, with 4 63 against 62 at 10, 341 against 197 at 128; e4m3 with 1
+  // 43.5 against 46 at 8, 55 against 52 at 10, 132 against 89 at 48).  Over 130
+  // random shapes with 1 to 4 shared experts the kernel taken is 0.6% above the
+  // faster one in the mean, 13% at most; without this part 5% and 138%.
   const int64_t entries = static_cast<int64_t>(T) * K;
   const bool e4m3 = q.weight_dtype == MOE_E4M3;
-  if (entries > (e4m3 ? (a.E < 48 ? a.E : 48) : 5 * a.E)) return launch_layer_many(h, a, e4m3, s);
+  const int most_shared = e4m3 ? 16 : 16 + a.E / 2 < 56 ? 16 + a.E / 2 : 56;
+  if (entries > (e4m3 ? (a.E < 48 ? a.E : 48) : 5 * a.E) ||
+      (a.S > 0 && T * (a.S + 1) > most_shared))
+    return launch_layer_many(h, a, e4m3, s);
   if (e4m3) return launch_few<true, true>(h, a, s);
   return entries > 2 * a.E ? launch_few<false, false>(h, a, s) : launch_few<false, true>(h, a, s);
 }

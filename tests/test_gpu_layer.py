@@ -716,3 +716,44 @@ def test_waits_that_give_up_anywhere_in_the_kernel(e4m3):
         torch.cuda.synchronize()
         assert moe.moe_read_device_status(p.r.h) == 0
         assert np.array_equal(p.out.double().cpu().numpy(), want)
+
+
+class KernelNodeParams(ctypes.Structure):
+    _fields_ = [("func", ctypes.c_void_p), ("grid", ctypes.c_uint * 3), ("block", ctypes.c_uint * 3),
+                ("shared", ctypes.c_uint), ("params", ctypes.c_void_p), ("extra", ctypes.c_void_p)]
+
+
+def kernels_of(call):
+    """Names of the kernels in a captured graph of `call`, in order."""
+    graph = torch.cuda.CUDAGraph(keep_graph=True)
+    with torch.cuda.graph(graph, stream=torch.cuda.Stream()):
+        call()
+    rt, raw, n = ctypes.CDLL("libcudart.so.13"), ctypes.c_void_p(graph.raw_cuda_graph()), ctypes.c_size_t(0)
+    assert rt.cudaGraphGetNodes(raw, None, ctypes.byref(n)) == 0
+    nodes = (ctypes.c_void_p * n.value)()
+    assert rt.cudaGraphGetNodes(raw, nodes, ctypes.byref(n)) == 0
+    names = []
+    for node in nodes:
+        p, name = KernelNodeParams(), ctypes.c_char_p()
+        assert rt.cudaGraphKernelNodeGetParams(ctypes.c_void_p(node), ctypes.byref(p)) == 0
+        assert rt.cudaFuncGetName(ctypes.byref(name), ctypes.c_void_p(p.func)) == 0
+        names.append(name.value.decode())
+    return names
+
+
+@pytest.mark.parametrize("kw,many", [
+    (dict(T=128, E=64, K=1, H=64, I=64, shared=2), True),    # 128 tokens' passes over the shared experts
+    (dict(T=128, E=64, K=1, H=64, I=64), False),             # 2 tokens an expert
+    (dict(T=16, E=64, K=1, H=64, I=64, shared=1), False),
+    (dict(T=48, E=64, K=1, H=64, I=64, shared=2, e4m3=True), True),
+    (dict(T=48, E=64, K=1, H=64, I=64, e4m3=True), False),
+    (dict(T=5, E=64, K=1, H=64, I=64, shared=2, e4m3=True), False),
+])
+def test_the_kernel_is_chosen_with_the_shared_experts_in_mind(kw, many):
+    p = Problem(**kw)
+    logits = to_dev(p.logits)
+    p.call(logits=logits)
+    p.check()
+    names = kernels_of(lambda: p.call(logits=logits))
+    assert len(names) == 2 and "route" in names[0]
+    assert ("layer_many_kernel" in names[1]) == many and "layer" in names[1]
