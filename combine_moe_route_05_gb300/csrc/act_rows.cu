@@ -209,7 +209,8 @@ __global__ void __launch_bounds__(kActThreads) act_rows_kernel(ActArgs a) {
 // memory (some 40 instructions an element with GELU), and registers beside them:
 // 65536 rows of 2048, bf16, with score gradient: SiLU 197 us with 10 blocks an SM,
 // 200 with 12 and 204 where the compiler chose, GELU 227, 209 and 214 (either
-// without dropout: 197).  A warp per 64 vectors of a row (without GW) was
+// without dropout: 197).  With 12 blocks GELU with dropout and score gradient
+// spills 16 bytes.  A warp per 64 vectors of a row (without GW) was
 // slower with dropout (SiLU 196 -> 211, GELU 212 -> 252).
 template <typename Elt, int ACT, bool DROP, bool GW>
 __global__ void __launch_bounds__(kActThreads, ACT == MOE_ACT_GELU ? 12 : 10)

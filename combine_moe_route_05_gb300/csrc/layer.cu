@@ -1,6 +1,7 @@
 // A whole MoE layer for a few tokens (sm_103a): after the routing, one kernel
-// that streams the reached experts' weights once.  This file: experts with a
-// handful of tokens, and the call itself; layer_many.cu: more tokens an expert.
+// that streams the reached experts' weights from memory once.  This file: experts
+// with a handful of tokens, and the call itself; layer_many.cu: more tokens an
+// expert.
 //
 //   up:      a[t,k,i] = act(<w13_e[i], x_t>) * <w13_e[I + i], x_t>
 //   down:    y[t,k,n] = <w2_e[n], a[t,k]>                            (fp32)
@@ -37,12 +38,16 @@
 // likewise per entry (11 bits).
 //
 // Measured, routing included (GPU time of a replayed graph; in brackets: weights
-// read once at the copy rate of 6.78 TB/s; ranges: different boxes): 16 tokens,
-// 128 experts, top 8, 2048 x 768, bf16: 129-134 us (115; DRAM reads 785 MB, the
+// read once at the copy rate of 6.78 TB/s; ranges: different boxes and routes, which
+// reach more or fewer experts than the mean in brackets): 16 tokens,
+// 128 experts, top 8, 2048 x 768, bf16: 127-136 us (115; DRAM reads 785 MB, the
 // weights' 778 and the tokens); 4 tokens, 256 experts and a shared one, 7168 x
-// 2048: 397-413 us (410); 1 token, 2048 x 768: 27 us (11): there the parts in
+// 2048: 397-443 us (410); 1 token, 2048 x 768: 27-29 us (11): there the parts in
 // front of and between the products bound it: routing 4.5, grouping 1, the
-// first weights' latency 2, two grid barriers 3.5, the sum 2 us.
+// first weights' latency 2, two grid barriers 3.5, the sum 2 us.  e4m3 weights: 4
+// tokens of the second shape 252-257 us (205), 16 of the first 106 (57), 1 of it 29
+// (6): the pass that scales the tokens, the one that scales the activations and a
+// grid barrier behind each come on top.
 #include "layer.cuh"
 
 namespace moe {
@@ -688,9 +693,16 @@ cudaError_t launch_layer(const moe_handle* h, const moe_layer_args& q, int T, vo
   // the kernel here converts again for every 4 tokens: 1, or some 48 entries in
   // all (16 experts, top 2, 4096 x 2048: 71 against 78 us at 16 entries, 93
   // against 89 at 24; 256 experts, top 8, 7168 x 2048: 234 against 250 at 32
-  // entries, 426 against 408 at 64).  Packed up to 2 tokens (128
-  // experts, top 8, 2048 x 768: 92 us, unpacked 94, at 0.5; 211 and 206 at 4,
-  // where 4 tokens to a tile make second passes).
+  // entries, 426 against 408 at 64).  T counts, not the live tokens, which the
+  // host does not know: 1 live of 128 tokens, 128 experts, top 8, 2048 x 768, takes
+  // 34 us by this rule, 30 with the other kernel (8 experts, top 2, 4096 x 2048: 39
+  // and 31).
+  //
+  // Packed up to 2 tokens: above it 4 tokens to a tile make second passes.  128
+  // experts, top 8, 2048 x 768: packed 89.0 us, unpacked 89.9 at 0.5, 130.4 and
+  // 131.1 at 1, 178.5 and 178.2 at 2, 196.1 and 193.0 at 3, 208.7 and 203.5 at 4;
+  // 32 experts, top 4, 4096 x 1024: 66.3 and 67.1, 96.3 and 97.0, 117.7 and 117.2,
+  // 132.1 and 128.2, 144.0 and 136.9.
   //
   // A shared expert has all T tokens, whose passes over a tile (8 or 4 tokens
   // each) one team makes in turn, and those of several run beside one another:

@@ -40,15 +40,16 @@
 //
 // Measured, routing included (GPU time of a replayed graph; in brackets: weights
 // read once at the copy rate of 6.78 TB/s).  128 tokens, 8 experts, top 2, 4096
-// x 2048: bf16 90 us (60), e4m3 81 (30); 128 tokens, 64 experts, top 8, 2048 x
+// x 2048: bf16 90-92 us (60), e4m3 80-81 (30); 128 tokens, 64 experts, top 8, 2048 x
 // 1408, bf16: 192 us (163); 37 live of 64 tokens, 256 experts, top 8, 7168 x
-// 2048, e4m3: 1199-1215 us (1156).  bf16: the up products read at 6.1, the down ones
+// 2048, e4m3: 1174-1215 us (1156).  bf16: the up products read at 6.1, the down ones
 // at 5.8 TB/s (DRAM reads 407 MB, the weights' 403); the rest is routing 5,
 // grouping 3, sorting and its barrier 4, the other barriers and the first
 // weights' latency 7, the sum 2 us.  e4m3: half the bytes and the same fixed
 // parts; a stage takes some 900 cycles, which are its copies': 28 KB, 12 of them
 // tokens, at 62 GB/s an SM (75 is the most that copies from L2 reached); without
 // the products, the conversion or the epilogue it takes as long, within 4%.
+// (It spills 36 bytes at its 96 registers, the most that 640 threads can have.)
 #include "layer.cuh"
 
 namespace moe {

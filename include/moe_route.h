@@ -457,7 +457,11 @@ moe_status moe_act_rows_bwd(const moe_handle* h, const void* d_ghs, const void* 
 /*
  * A whole MoE layer for a few tokens (a decode batch), without a dispatch
  * layout: routing, the experts and the weighted sum, reading the weights of
- * each reached expert once.  The layer is that of the separate calls
+ * each reached expert once from memory.  (An expert with more tokens than its
+ * kernel multiplies at a time reads them again for each further pass, right
+ * behind the last one and so from L2: more than 4 or 8 tokens where few tokens
+ * go to an expert, with e4m3 weights more than 64 where many do.)  The layer is
+ * that of the separate calls
  * (moe_route_topk, gate/up GEMM, moe_act_rows, W2, moe_combine):
  *   a[t,k,i] = act(<w13_e[i], x_t>) * <w13_e[I + i], x_t>
  *   out[t]   = round_bf16( sum_k w[t,k] <w2_e, a[t,k]> + sum_j <w2_(E+j), a[t,K+j]> )
