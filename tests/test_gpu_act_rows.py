@@ -340,3 +340,37 @@ def test_methods_on_another_stream_keep_their_outputs(name):
     assert not torch.cuda.current_stream().query()  # the current stream is not done with them
     assert not {p for p, _ in seen} & {t.data_ptr() for t in here + there}
     torch.cuda.synchronize()
+
+
+def test_methods_on_a_forked_stream_of_a_captured_graph():
+    """Both activations and the layer on a second stream inside a capture, an output
+    freed before the capture ends."""
+    r, ent, end, gu, ghs, rw = problem(60, 4, 2, 64, "bf16")
+    g = torch.Generator().manual_seed(3)
+    x = torch.randn(8, 64, generator=g).to(dev(), torch.bfloat16)
+    w13 = (torch.randn(4, 64, 64, generator=g) / 8).to(dev(), torch.bfloat16)
+    w2 = (torch.randn(4, 64, 32, generator=g) / 6).to(dev(), torch.bfloat16)
+    logits = torch.randn(8, 4, generator=g).to(dev())
+    side = torch.cuda.Stream()
+
+    def both(stream):
+        hs = r.act_rows(gu, rw, stream=stream)
+        ggu, gw = r.act_rows_bwd(ghs, gu, rw, stream=stream)
+        out = r.layer(x, logits, w13, w2, stream=stream)[0]
+        if stream is not None:
+            torch.cuda.current_stream().wait_stream(stream)
+        doubled = hs * 2
+        del hs
+        return doubled, ggu * 1, gw * 1, out * 1
+    want = both(None)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        side.wait_stream(torch.cuda.current_stream())
+        got = both(side)
+    for _ in range(3):
+        for t in got:
+            t.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
