@@ -41,7 +41,8 @@ DOMINANT = "combine_bwd"
 NOMINAL_HBM_GBS = 7900.0  # GB300 HBM3e data-sheet bandwidth, for context beside the measured peak
 KERNEL_SOURCES = ("combine_moe_route_05_gb300/csrc/rows.cu", "combine_moe_route_05_gb300/csrc/common.cuh",
                   "combine_moe_route_05_gb300/csrc/router_grad.cuh")
-W2_SOURCES = ("combine_moe_route_05_gb300/csrc/w2_gemm.cu", "combine_moe_route_05_gb300/csrc/common.cuh")
+W2_SOURCES = ("combine_moe_route_05_gb300/csrc/w2_gemm.cu", "combine_moe_route_05_gb300/csrc/common.cuh",
+              "combine_moe_route_05_gb300/csrc/tensor.cuh")
 # per-launch DRAM traffic of the roofline kernels, from one ncu pass each
 TRAFFIC_RECORDS = os.path.join(ROOT, "profiles", "traffic.json")
 L2_FLUSH_BYTES = 256 << 20  # twice the 129 MB L2

@@ -99,3 +99,20 @@ def test_traffic_records_are_consistent():
         cite = "(key `%s`): %.3fe9 bytes, workload %s, kernel source %s" % (
             key, traffic / 1e9, rec["workload"], rec["source"])
         assert cite in text, cite
+
+
+@pytest.mark.parametrize("sources", ["KERNEL_SOURCES", "W2_SOURCES"])
+def test_traffic_hashes_cover_the_kernels_headers(sources):
+    """A record counts for the kernel source that it was taken on: the hash is over
+    the translation unit and every device header (.cuh) that it includes."""
+    import re
+    files = getattr(bench, sources)
+    want, todo = set(), [files[0]]
+    while todo:
+        rel = todo.pop()
+        want.add(rel)
+        with open(os.path.join(ROOT, rel)) as f:
+            found = [os.path.join(os.path.dirname(rel), n)
+                     for n in re.findall(r'#include "(\w+\.cuh)"', f.read())]
+        todo += [n for n in found if n not in want]
+    assert set(files) == want
