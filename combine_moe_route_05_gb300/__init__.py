@@ -36,10 +36,13 @@ EXPORTS = ("moe_status_string", "moe_workspace_bytes", "moe_handle_create", "moe
            "moe_dispatch_layout_static", "moe_route_bwd", "moe_expand", "moe_combine_partial",
            "moe_combine_reduce", "moe_w2_absorbed", "moe_dispatch_layout_launches",
            "moe_dispatch_bwd_route", "moe_dispatch_bwd_route_launches", "moe_set_wait_limit",
-           "moe_act_rows", "moe_act_rows_bwd", "moe_layer_workspace_bytes", "moe_layer")
+           "moe_act_rows", "moe_act_rows_bwd", "moe_layer_workspace_bytes", "moe_layer",
+           "moe_balance_workspace_bytes", "moe_balance", "moe_balance_bwd", "moe_block_norm",
+           "moe_block_norm_workspace_bytes", "moe_block_norm_bwd")
 MOE_LAYOUT_STATIC_COUNTERS = 65536
 MOE_LAYOUT_TILE_TOKENS = 512
 MOE_ACT_MAX_WIDTH = 1 << 26
+MOE_NORM_MAX_WIDTH = 16384
 MOE_LAYER_MAX_TOKENS, MOE_LAYER_MAX_SHARED, MOE_LAYER_MAX_WIDTH = 128, 4, 65536
 
 
@@ -63,6 +66,22 @@ class MoeLayerArgs(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in (
         "d_x", "d_logits", "d_bias", "d_live", "d_w13", "d_w2", "d_s13", "d_s2", "d_out", "d_idx",
         "d_w")] + [(n, ctypes.c_int32) for n in ("H", "I", "num_shared", "weight_dtype", "act")]
+
+
+class MoeBlockNormArgs(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in (
+        "d_res", "d_y", "d_cw", "d_add", "d_gate", "d_w_post", "d_w_pre", "d_res_out", "d_x", "d_c",
+        "d_rstd_post", "d_rstd_pre")] + [(n, ctypes.c_double) for n in (
+            "res_scale", "eps", "weight_offset")] + [(n, ctypes.c_int32) for n in (
+                "H", "dtype", "weight_dtype", "gate_tokens", "gather")]
+
+
+class MoeBlockNormBwdArgs(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in (
+        "d_gres_out", "d_gx", "d_res_out", "d_c", "d_gate", "d_w_post", "d_w_pre", "d_rstd_post",
+        "d_rstd_pre", "d_gres", "d_gy", "d_ggate", "d_gw_post", "d_gw_pre")] + [
+            (n, ctypes.c_double) for n in ("res_scale", "weight_offset")] + [
+                (n, ctypes.c_int32) for n in ("H", "dtype", "weight_dtype", "gate_tokens")]
 
 
 class MoeError(RuntimeError):
@@ -119,6 +138,12 @@ def lib():
             "moe_act_rows_bwd": ([P, P, P, i32, i32, i32, P, ctypes.c_double, P, P, P, P], st),
             "moe_layer_workspace_bytes": ([P, i32, i32, i32], sz),
             "moe_layer": ([P, P, i32, P, sz, P], st),
+            "moe_balance_workspace_bytes": ([P, i32], sz),
+            "moe_balance": ([P, P, P, i32, P, i32, ctypes.c_double, P, P, P, P, sz, P], st),
+            "moe_balance_bwd": ([P, P, P, i32, P, i32, ctypes.c_double, P, P, P, P], st),
+            "moe_block_norm": ([P, P, i32, P], st),
+            "moe_block_norm_workspace_bytes": ([P, i32, i32, i32], sz),
+            "moe_block_norm_bwd": ([P, P, i32, P, sz, P], st),
         }
         for name, (args, res) in sigs.items():
             f = getattr(L, name)
@@ -500,6 +525,148 @@ def moe_layer(h, x, logits, w13, w2, out, idx, w, workspace, bias=None, s13=None
           _stream(stream, d))
 
 
+def moe_balance_workspace_bytes(cfg, num_seqs=1):
+    return lib().moe_balance_workspace_bytes(ctypes.byref(cfg), num_seqs)
+
+
+def balance_workspace(h, num_seqs=1):
+    """Workspace tensor for moe_balance on this handle (one per overlapping call)."""
+    n = moe_balance_workspace_bytes(h.cfg, num_seqs)
+    if n == 0:
+        raise MoeError("moe_balance_workspace_bytes", MOE_ERR_INVALID)
+    return torch.empty(n, dtype=torch.uint8, device=h.device)
+
+
+def _num_seqs(seq_off, device):
+    """Sequences of an offset table (int32 [S + 1]; None: one of all tokens)."""
+    if seq_off is None:
+        return 1
+    _req(seq_off, torch.int32, None, "seq_off", device)
+    if seq_off.dim() != 1 or seq_off.shape[0] < 2:
+        raise ValueError("seq_off must have shape (S + 1,), got %s" % (tuple(seq_off.shape),))
+    return seq_off.shape[0] - 1
+
+
+def moe_balance(h, logits, idx, loss, cnt, workspace, prob=None, seq_off=None, coef=1.0,
+                stream=None):
+    """Balance loss [1] with counts [S, E] (int32) and mean probabilities [S, E]
+    (None: not written) of the sequences of seq_off (None: one of all tokens)."""
+    T = logits.shape[0]
+    d = h.device
+    S = _num_seqs(seq_off, d)
+    _req(logits, torch.float32, (T, h.E), "logits", d)
+    _req(idx, torch.int32, (T, h.K), "idx", d)
+    _req(loss, torch.float32, (1,), "loss", d)
+    _req(cnt, torch.int32, (S, h.E), "cnt", d)
+    _req(prob, torch.float32, (S, h.E), "prob", d)
+    _req(workspace, torch.uint8, None, "workspace", d)
+    _call(h, "moe_balance", h.ptr, _ptr(logits), _ptr(idx), T, _ptr(seq_off), S, float(coef),
+          _ptr(loss), _ptr(cnt), _ptr(prob), _ptr(workspace), workspace.numel(),
+          _stream(stream, d))
+
+
+def moe_balance_bwd(h, logits, cnt, glogits, seq_off=None, coef=1.0, gloss=None, base=None,
+                    stream=None):
+    """glogits = base + gloss * dloss/dlogits with the forward's counts; gloss
+    fp32 [1] (None: 1), base [T, E] (None: 0; may be glogits)."""
+    T = logits.shape[0]
+    d = h.device
+    S = _num_seqs(seq_off, d)
+    _req(logits, torch.float32, (T, h.E), "logits", d)
+    _req(cnt, torch.int32, (S, h.E), "cnt", d)
+    _req(gloss, torch.float32, (1,), "gloss", d)
+    _req(base, torch.float32, (T, h.E), "base", d)
+    _req(glogits, torch.float32, (T, h.E), "glogits", d)
+    _call(h, "moe_balance_bwd", h.ptr, _ptr(logits), _ptr(cnt), T, _ptr(seq_off), S, float(coef),
+          _ptr(gloss), _ptr(base), _ptr(glogits), _stream(stream, d))
+
+
+def _norm_weights(w_post, w_pre, H, device):
+    """The norms' weights, [H] in one dtype: their C dtype."""
+    w = w_post if w_post is not None else w_pre
+    if w is None:
+        return MOE_F32
+    _req(w_post, w.dtype, (H,), "w_post", device)
+    _req(w_pre, w.dtype, (H,), "w_pre", device)
+    return _row_dtype(w)
+
+
+def _gate_rows(T, gate_tokens):
+    if gate_tokens < 1:
+        raise ValueError("gate_tokens must be at least 1, got %d" % gate_tokens)
+    return -(-T // gate_tokens)
+
+
+def moe_block_norm(h, res, res_out, x=None, y=None, gather=False, cw=None, add=None, gate=None,
+                   gate_tokens=1, w_post=None, w_pre=None, c=None, rstd_post=None, rstd_pre=None,
+                   res_scale=1.0, eps=1e-6, weight_offset=0.0, stream=None):
+    """res_out = res_scale * res + gate * norm(y + add), x = norm(res_out); y are
+    token rows, or with gather receive rows summed with the weights cw.  Without
+    y: x = norm(res), res_out None."""
+    T, H = res.shape
+    d, dt = h.device, res.dtype
+    rows = (h.recv_rows if gather else T, H)
+    _req(res, None, (T, H), "res", d)
+    _req(y, dt, rows, "y", d)
+    _req(cw, torch.float32, (T, h.K), "cw", d)
+    _req(add, dt, (T, H), "add", d)
+    _req(gate, dt, (_gate_rows(T, gate_tokens), H), "gate", d)
+    wd = _norm_weights(w_post, w_pre, H, d)
+    _req(res_out, dt, (T, H), "res_out", d)
+    _req(x, dt, (T, H), "x", d)
+    _req(c, dt, (T, H), "c", d)
+    _req(rstd_post, torch.float32, (T,), "rstd_post", d)
+    _req(rstd_pre, torch.float32, (T,), "rstd_pre", d)
+    a = MoeBlockNormArgs(_ptr(res), _ptr(y), _ptr(cw), _ptr(add), _ptr(gate), _ptr(w_post),
+                         _ptr(w_pre), _ptr(res_out), _ptr(x), _ptr(c), _ptr(rstd_post),
+                         _ptr(rstd_pre), res_scale, eps, weight_offset, H, _row_dtype(res), wd,
+                         gate_tokens, int(bool(gather)))
+    _call(h, "moe_block_norm", h.ptr, ctypes.byref(a), T, _stream(stream, d))
+
+
+def moe_block_norm_workspace_bytes(h, T, H, gate_tokens=1):
+    return lib().moe_block_norm_workspace_bytes(h.ptr, T, H, gate_tokens)
+
+
+def block_norm_workspace(h, T, H, gate_tokens=1):
+    """Workspace tensor for moe_block_norm_bwd (one per overlapping call)."""
+    n = moe_block_norm_workspace_bytes(h, T, H, gate_tokens)
+    if n == 0:
+        raise MoeError("moe_block_norm_workspace_bytes", MOE_ERR_INVALID)
+    return torch.empty(n, dtype=torch.uint8, device=h.device)
+
+
+def moe_block_norm_bwd(h, workspace, gres_out=None, gx=None, res_out=None, c=None, gate=None,
+                       gate_tokens=1, w_post=None, w_pre=None, rstd_post=None, rstd_pre=None,
+                       gres=None, gy=None, ggate=None, gw_post=None, gw_pre=None, res_scale=1.0,
+                       weight_offset=0.0, stream=None):
+    """Backward of moe_block_norm from the gradients gres_out and gx (either may
+    be None) into those of gres, gy, ggate, gw_post and gw_pre that are given."""
+    g = gres_out if gres_out is not None else gx
+    if g is None:
+        raise ValueError("gres_out or gx must be given")
+    T, H = g.shape
+    d, dt = h.device, g.dtype
+    groups = _gate_rows(T, gate_tokens)
+    for name, t in (("gres_out", gres_out), ("gx", gx), ("res_out", res_out), ("c", c),
+                    ("gres", gres), ("gy", gy)):
+        _req(t, dt, (T, H), name, d)
+    _req(gate, dt, (groups, H), "gate", d)
+    _req(ggate, dt, (groups, H), "ggate", d)
+    wd = _norm_weights(w_post, w_pre, H, d)
+    _req(rstd_post, torch.float32, (T,), "rstd_post", d)
+    _req(rstd_pre, torch.float32, (T,), "rstd_pre", d)
+    _req(gw_post, torch.float32, (H,), "gw_post", d)
+    _req(gw_pre, torch.float32, (H,), "gw_pre", d)
+    _req(workspace, torch.uint8, None, "workspace", d)
+    a = MoeBlockNormBwdArgs(_ptr(gres_out), _ptr(gx), _ptr(res_out), _ptr(c), _ptr(gate),
+                            _ptr(w_post), _ptr(w_pre), _ptr(rstd_post), _ptr(rstd_pre), _ptr(gres),
+                            _ptr(gy), _ptr(ggate), _ptr(gw_post), _ptr(gw_pre), res_scale,
+                            weight_offset, H, _row_dtype(g), wd, gate_tokens)
+    _call(h, "moe_block_norm_bwd", h.ptr, ctypes.byref(a), T, _ptr(workspace), workspace.numel(),
+          _stream(stream, d))
+
+
 def moe_dispatch_layout_launches(h, T):
     """Kernel launches moe_dispatch_layout makes for T tokens (1 or 2)."""
     n = ctypes.c_int32(0)
@@ -586,8 +753,9 @@ def _kept_for_caller(stream, *tensors):
 
 class MoeRouter:
     """Owns a handle; methods allocate their outputs and call the moe_* bindings.
-    act_rows, act_rows_bwd and layer allocate on the stream that they run on (the
-    others on the current one)."""
+    act_rows, act_rows_bwd, layer, balance, balance_bwd, block_norm and
+    block_norm_bwd allocate on the stream that they run on (the others on the
+    current one)."""
 
     def __init__(self, num_experts, top_k, num_ranks, max_tokens, **kw):
         self.cfg = make_config(num_experts, top_k, num_ranks, max_tokens, **kw)
@@ -703,6 +871,85 @@ class MoeRouter:
                       num_shared, stream)
         _kept_for_caller(stream, out, idx, w)
         return out, idx, w
+
+    def balance(self, logits, idx, seq_off=None, coef=1.0, stream=None):
+        """Balance loss of the routes idx: (loss [1], counts [S, E], mean
+        probabilities [S, E]); seq_off: int32 [S + 1] offsets of packed sequences."""
+        d = self.h.device
+        S = _num_seqs(seq_off, d)
+        with torch.cuda.stream(stream):
+            loss = torch.empty(1, dtype=torch.float32, device=d)
+            cnt = torch.empty(S, self.h.E, dtype=torch.int32, device=d)
+            prob = torch.empty(S, self.h.E, dtype=torch.float32, device=d)
+            ws = balance_workspace(self.h, S)
+            moe_balance(self.h, logits, idx, loss, cnt, ws, prob, seq_off, coef, stream)
+        _kept_for_caller(stream, loss, cnt, prob)
+        return loss, cnt, prob
+
+    def balance_bwd(self, logits, cnt, seq_off=None, coef=1.0, gloss=None, base=None, stream=None):
+        """glogits = base + gloss * dloss/dlogits; rows of tokens outside the
+        sequences are base's (0 without one)."""
+        with torch.cuda.stream(stream):
+            if seq_off is None:
+                glogits = torch.empty_like(logits)
+            else:
+                glogits = torch.zeros_like(logits) if base is None else base.clone()
+            moe_balance_bwd(self.h, logits, cnt, glogits, seq_off, coef, gloss, base, stream)
+        _kept_for_caller(stream, glogits)
+        return glogits
+
+    def block_norm(self, res, y=None, gather=False, cw=None, add=None, gate=None, gate_tokens=1,
+                   w_post=None, w_pre=None, res_scale=1.0, eps=1e-6, weight_offset=0.0, save=False,
+                   stream=None):
+        """The norms around a block (see moe_block_norm): (res_out, x, saved).
+        res_out is None without y, x without w_pre; saved (None without `save`):
+        what block_norm_bwd needs, a dict."""
+        T = res.shape[0]
+        with torch.cuda.stream(stream):
+            res_out = torch.empty_like(res) if y is not None else None
+            x = torch.empty_like(res) if w_pre is not None else None
+            saved = None
+            if save:
+                own = y is not None and (gather or add is not None)
+                saved = dict(res_out=res if y is None else res_out,
+                             c=torch.empty_like(res) if own else y,
+                             rstd_post=torch.empty(T, dtype=torch.float32, device=res.device)
+                             if w_post is not None else None,
+                             rstd_pre=torch.empty(T, dtype=torch.float32, device=res.device)
+                             if w_pre is not None else None)
+            moe_block_norm(self.h, res, res_out, x, y, gather, cw, add, gate, gate_tokens, w_post,
+                           w_pre, saved["c"] if save and own else None,
+                           saved["rstd_post"] if save else None,
+                           saved["rstd_pre"] if save else None, res_scale, eps, weight_offset,
+                           stream)
+        _kept_for_caller(stream, res_out, x, *(saved.values() if save else ()))
+        return res_out, x, saved
+
+    def block_norm_bwd(self, gres_out, gx, saved, gate=None, gate_tokens=1, w_post=None,
+                       w_pre=None, res_scale=1.0, weight_offset=0.0, stream=None):
+        """(gres, gy, ggate, gw_post, gw_pre) from the gradients of res_out and x
+        (either may be None) and what block_norm saved; None for what the forward
+        did not have."""
+        g = gres_out if gres_out is not None else gx
+        if g is None:
+            raise ValueError("gres_out or gx must be given")
+        T, H = g.shape
+        has = saved["c"] is not None
+        with torch.cuda.stream(stream):
+            gres = torch.empty_like(g)
+            gy = torch.empty_like(g) if has else None
+            ggate = torch.empty_like(gate) if gate is not None else None
+            gw_post, gw_pre = (torch.empty(H, dtype=torch.float32, device=g.device)
+                               if w is not None else None for w in (w_post, w_pre))
+            ws = block_norm_workspace(self.h, T, H, gate_tokens)
+            moe_block_norm_bwd(self.h, ws, gres_out, gx, saved["res_out"], saved["c"], gate,
+                               gate_tokens, w_post, w_pre if gx is not None else None,
+                               saved["rstd_post"], saved["rstd_pre"], gres, gy, ggate, gw_post,
+                               gw_pre if gx is not None else None, res_scale, weight_offset, stream)
+            if gx is None and gw_pre is not None:
+                gw_pre.zero_()
+        _kept_for_caller(stream, gres, gy, ggate, gw_post, gw_pre)
+        return gres, gy, ggate, gw_post, gw_pre
 
     def w2_absorbed(self, hrows, recv_w, w2, stream=None):
         y = torch.empty(hrows.shape[0], w2.shape[1], dtype=torch.bfloat16, device=hrows.device)

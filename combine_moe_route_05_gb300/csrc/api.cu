@@ -122,6 +122,20 @@ bool layer_sizes_ok(const moe_config* c, int32_t H, int32_t I, int32_t num_share
   return num_shared >= 0 && num_shared <= MOE_LAYER_MAX_SHARED && c->num_experts >= 1;
 }
 
+// Sequences of a balance loss: their table, and the factor.
+bool balance_args_ok(const int32_t* off, int32_t S, double coef) {
+  if (S < 1 || (!off && S != 1) || !aligned(off, 4)) return false;
+  return std::isfinite(static_cast<float>(coef));
+}
+
+// What the norms and their backward share.
+bool norm_sizes_ok(int32_t H, int32_t dtype, int32_t weight_dtype, int32_t gate_tokens,
+                   double res_scale, double offset) {
+  if (!empty_rows_ok(H, dtype) || H > MOE_NORM_MAX_WIDTH) return false;
+  if (!valid_dtype(weight_dtype) || gate_tokens < 1) return false;
+  return std::isfinite(static_cast<float>(res_scale)) && std::isfinite(static_cast<float>(offset));
+}
+
 // Every launch goes to the current device, and every pointer a call gets must
 // live on the handle's device: a call made while another device is current
 // is refused before anything is launched.
@@ -479,6 +493,120 @@ moe_status moe_layer(const moe_handle* h, const moe_layer_args* q, int32_t T, vo
       workspace_bytes < moe::layer_plan(T, h->cfg.top_k, q->num_shared, q->H, q->I).total)
     return MOE_ERR_INVALID;
   return from_cuda(moe::launch_layer(h, *q, T, d_workspace, as_stream(stream)));
+}
+
+size_t moe_balance_workspace_bytes(const moe_config* c, int32_t num_seqs) {
+  if (!config_valid(c) || num_seqs < 1) return 0;
+  return moe::balance_plan(c->num_experts, num_seqs).total;
+}
+
+moe_status moe_balance(const moe_handle* h, const float* d_logits, const int32_t* d_idx, int32_t T,
+                       const int32_t* d_seq_off, int32_t num_seqs, double coef, float* d_loss,
+                       int32_t* d_cnt, float* d_prob, void* d_workspace, size_t workspace_bytes,
+                       void* stream) {
+  if (!h || T < 0) return MOE_ERR_INVALID;
+  if (!on_handle_device(h)) return MOE_ERR_INVALID;
+  if (T > h->cfg.max_tokens) return MOE_ERR_CAPACITY;
+  if (!balance_args_ok(d_seq_off, num_seqs, coef)) return MOE_ERR_INVALID;
+  if (!d_loss || !d_cnt || (T > 0 && (!d_logits || !d_idx))) return MOE_ERR_INVALID;
+  if (!aligned(d_logits, 4) || !aligned(d_idx, 4) || !aligned(d_loss, 4) || !aligned(d_cnt, 4) ||
+      !aligned(d_prob, 4))
+    return MOE_ERR_INVALID;
+  if (!d_workspace || !aligned(d_workspace, kAlign) ||
+      workspace_bytes < moe::balance_plan(h->cfg.num_experts, num_seqs).total)
+    return MOE_ERR_INVALID;
+  return from_cuda(moe::launch_balance(h, d_logits, d_idx, T, d_seq_off, num_seqs, coef, d_loss,
+                                       d_cnt, d_prob, d_workspace, as_stream(stream)));
+}
+
+moe_status moe_balance_bwd(const moe_handle* h, const float* d_logits, const int32_t* d_cnt,
+                           int32_t T, const int32_t* d_seq_off, int32_t num_seqs, double coef,
+                           const float* d_gloss, const float* d_base, float* d_glogits,
+                           void* stream) {
+  if (!h || T < 0) return MOE_ERR_INVALID;
+  if (!on_handle_device(h)) return MOE_ERR_INVALID;
+  if (T > h->cfg.max_tokens) return MOE_ERR_CAPACITY;
+  if (!balance_args_ok(d_seq_off, num_seqs, coef)) return MOE_ERR_INVALID;
+  if (T > 0 && (!d_logits || !d_cnt || !d_glogits)) return MOE_ERR_INVALID;
+  if (!aligned(d_logits, 4) || !aligned(d_cnt, 4) || !aligned(d_gloss, 4) || !aligned(d_base, 4) ||
+      !aligned(d_glogits, 4))
+    return MOE_ERR_INVALID;
+  return from_cuda(moe::launch_balance_bwd(h, d_logits, d_cnt, T, d_seq_off, num_seqs, coef,
+                                           d_gloss, d_base, d_glogits, as_stream(stream)));
+}
+
+moe_status moe_block_norm(const moe_handle* h, const moe_block_norm_args* q, int32_t T,
+                          void* stream) {
+  if (!h || !q || T < 0) return MOE_ERR_INVALID;
+  if (!on_handle_device(h)) return MOE_ERR_INVALID;
+  if (!norm_sizes_ok(q->H, q->dtype, q->weight_dtype, q->gate_tokens, q->res_scale,
+                     q->weight_offset))
+    return MOE_ERR_INVALID;
+  const float eps = static_cast<float>(q->eps);
+  if (!(eps > 0.0f) || !std::isfinite(eps)) return MOE_ERR_INVALID;
+  if (q->gather != 0 && q->gather != 1) return MOE_ERR_INVALID;
+  if (T > h->cfg.max_tokens) return MOE_ERR_CAPACITY;
+  if (q->gather) {
+    if (h->T < 0) return MOE_ERR_STATE;
+    if (T != h->T) return MOE_ERR_INVALID;
+  }
+  if (T == 0) return MOE_OK;
+  if ((q->d_x != nullptr) != (q->d_w_pre != nullptr)) return MOE_ERR_INVALID;
+  if (q->d_rstd_pre && !q->d_x) return MOE_ERR_INVALID;
+  if (q->d_rstd_post && !q->d_w_post) return MOE_ERR_INVALID;
+  if (q->d_cw && !q->gather) return MOE_ERR_INVALID;
+  if (q->d_y) {
+    if (!q->d_res_out) return MOE_ERR_INVALID;
+  } else if (q->gather || q->d_add || q->d_gate || q->d_w_post || q->d_c || q->d_res_out ||
+             !q->d_x) {
+    return MOE_ERR_INVALID;
+  }
+  if (!q->d_res || !aligned(q->d_res, 16) || !aligned(q->d_y, 16) || !aligned(q->d_add, 16) ||
+      !aligned(q->d_gate, 16) || !aligned(q->d_w_post, 16) || !aligned(q->d_w_pre, 16) ||
+      !aligned(q->d_res_out, 16) || !aligned(q->d_x, 16) || !aligned(q->d_c, 16))
+    return MOE_ERR_INVALID;
+  if (!aligned(q->d_cw, 4) || !aligned(q->d_rstd_post, 4) || !aligned(q->d_rstd_pre, 4))
+    return MOE_ERR_INVALID;
+  return from_cuda(moe::launch_block_norm(h, *q, T, as_stream(stream)));
+}
+
+size_t moe_block_norm_workspace_bytes(const moe_handle* h, int32_t T, int32_t H,
+                                      int32_t gate_tokens) {
+  if (!h || T < 0 || T > h->cfg.max_tokens || H < 1 || H > MOE_NORM_MAX_WIDTH || gate_tokens < 1)
+    return 0;
+  return moe::block_norm_workspace(h, T, H, gate_tokens);
+}
+
+moe_status moe_block_norm_bwd(const moe_handle* h, const moe_block_norm_bwd_args* q, int32_t T,
+                              void* d_workspace, size_t workspace_bytes, void* stream) {
+  if (!h || !q || T < 0) return MOE_ERR_INVALID;
+  if (!on_handle_device(h)) return MOE_ERR_INVALID;
+  if (!norm_sizes_ok(q->H, q->dtype, q->weight_dtype, q->gate_tokens, q->res_scale,
+                     q->weight_offset))
+    return MOE_ERR_INVALID;
+  if (T > h->cfg.max_tokens) return MOE_ERR_CAPACITY;
+  if (q->d_ggate && !q->d_gate) return MOE_ERR_INVALID;
+  if (q->d_gw_post && !q->d_w_post) return MOE_ERR_INVALID;
+  if (q->d_gw_pre && !q->d_w_pre) return MOE_ERR_INVALID;
+  if (T > 0) {
+    if (!q->d_gres_out && !q->d_gx) return MOE_ERR_INVALID;
+    if ((q->d_gx != nullptr) != (q->d_w_pre != nullptr)) return MOE_ERR_INVALID;
+    if (q->d_gx && (!q->d_res_out || !q->d_rstd_pre)) return MOE_ERR_INVALID;
+    if ((q->d_gate || q->d_w_post) && !q->d_c) return MOE_ERR_INVALID;
+    if (q->d_w_post && !q->d_rstd_post) return MOE_ERR_INVALID;
+  }
+  if (!aligned(q->d_gres_out, 16) || !aligned(q->d_gx, 16) || !aligned(q->d_res_out, 16) ||
+      !aligned(q->d_c, 16) || !aligned(q->d_gate, 16) || !aligned(q->d_w_post, 16) ||
+      !aligned(q->d_w_pre, 16) || !aligned(q->d_gres, 16) || !aligned(q->d_gy, 16) ||
+      !aligned(q->d_ggate, 16))
+    return MOE_ERR_INVALID;
+  if (!aligned(q->d_rstd_post, 4) || !aligned(q->d_rstd_pre, 4) || !aligned(q->d_gw_post, 4) ||
+      !aligned(q->d_gw_pre, 4))
+    return MOE_ERR_INVALID;
+  if (!d_workspace || !aligned(d_workspace, kAlign) ||
+      workspace_bytes < moe::block_norm_workspace(h, T, q->H, q->gate_tokens))
+    return MOE_ERR_INVALID;
+  return from_cuda(moe::launch_block_norm_bwd(h, *q, T, d_workspace, as_stream(stream)));
 }
 
 moe_status moe_read_device_status(const moe_handle* h, uint32_t* host_flags) {

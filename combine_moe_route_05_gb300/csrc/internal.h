@@ -118,6 +118,25 @@ cudaError_t prepare_layer_kernels();
 cudaError_t launch_layer(const moe_handle* h, const moe_layer_args& q, int T, void* workspace,
                          cudaStream_t s);
 
+// Workspace of the balance loss: byte offsets of the last block's ticket, the
+// fragments' sums and counts and the sequences' parts of the loss.
+struct BalancePlan {
+  size_t ticket, slot_p, slot_c, part, total;
+};
+BalancePlan balance_plan(int E, int S);
+cudaError_t launch_balance(const moe_handle* h, const float* logits, const int32_t* idx, int T,
+                           const int32_t* off, int S, double coef, float* loss, int32_t* cnt,
+                           float* prob, void* workspace, cudaStream_t s);
+cudaError_t launch_balance_bwd(const moe_handle* h, const float* logits, const int32_t* cnt, int T,
+                               const int32_t* off, int S, double coef, const float* gloss,
+                               const float* base, float* glogits, cudaStream_t s);
+
+size_t block_norm_workspace(const moe_handle* h, int T, int H, int gate_tokens);
+cudaError_t launch_block_norm(const moe_handle* h, const moe_block_norm_args& q, int T,
+                              cudaStream_t s);
+cudaError_t launch_block_norm_bwd(const moe_handle* h, const moe_block_norm_bwd_args& q, int T,
+                                  void* workspace, cudaStream_t s);
+
 int layout_launches(const moe_config& c, int T);
 cudaError_t prepare_w2_kernel();
 bool w2_shape_ok(int I, int H);

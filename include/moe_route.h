@@ -529,6 +529,164 @@ moe_status moe_layer(const moe_handle* h, const moe_layer_args* args, int32_t T,
                      size_t workspace_bytes, void* stream);
 
 /*
+ * Balance loss of the router with per-expert counts (the pages balance with the
+ * score-correction bias alone; this is the loss that is added to a training
+ * step's).  For sequence s of n_s tokens, c[s,e] its entries of expert e in
+ * d_idx and p[t,e] = softmax(l_t)_e, or sigmoid(l_te) / sum_j sigmoid(l_tj):
+ *   *d_loss     = coef / S' * sum_s E / (K n_s^2) * sum_e c[s,e] sum_t p[t,e]
+ *   d_cnt[s,e]  = c[s,e]
+ *   d_prob[s,e] = 1 / n_s * sum_t p[t,e]          (not written if d_prob is NULL)
+ * over the tokens t of s; S' = sequences that are not empty (a loss of 0 if
+ * there is none).  p is over all E experts, whatever groups, renorm, scale and
+ * bias the routing has.  fp32, sums in a fixed order: the same inputs give the
+ * same bits.
+ *   d_logits [T,E] fp32, d_idx [T,K] int32 as in moe_route_topk.  An entry of
+ *     -1 is no expert; any other index outside [0,E) (MOE_DEVERR_BAD_EXPERT) and
+ *     a token's repeated expert (MOE_DEVERR_DUP_EXPERT) are flagged and not
+ *     counted.  A logit of -inf is a masked expert, p = 0; a token without any
+ *     other has p = 0 throughout, and so has one with a NaN or +inf logit, which
+ *     is flagged (MOE_DEVERR_NONFINITE).  Both count as tokens.
+ *   d_seq_off int32 [num_seqs + 1] on the device: sequence s is tokens
+ *     d_seq_off[s] <= t < d_seq_off[s + 1]; NULL: one sequence of all T tokens
+ *     (num_seqs = 1).  Tokens before the first or behind the last are not read.
+ *     Offsets that fall or lie outside [0,T] are flagged (MOE_DEVERR_BAD_LAYOUT)
+ *     and the results unspecified.
+ *   d_loss fp32 [1], d_cnt int32 [num_seqs, E], d_prob fp32 [num_seqs, E].
+ * d_workspace: moe_balance_workspace_bytes(c, num_seqs) bytes (for any T),
+ * 256-byte aligned, free after the call's work; calls that may overlap on the
+ * GPU need one each.  The handle's layout is neither read nor changed.
+ */
+size_t moe_balance_workspace_bytes(const moe_config* c, int32_t num_seqs);
+
+moe_status moe_balance(const moe_handle* h, const float* d_logits, const int32_t* d_idx, int32_t T,
+                       const int32_t* d_seq_off, int32_t num_seqs, double coef, float* d_loss,
+                       int32_t* d_cnt, float* d_prob, void* d_workspace, size_t workspace_bytes,
+                       void* stream);
+
+/*
+ * Gradient of moe_balance to the logits, the counts held fixed:
+ *   d_glogits[t,j] = d_base[t,j] + *d_gloss * coef / S' * E / (K n_s^2)
+ *                    * q[t,j] (c[s,j] - sum_e c[s,e] p[t,e]),
+ *   q = p (softmax), sigmoid (1 - sigmoid) / sum_j sigmoid (sigmoid scores).
+ * d_cnt is the forward's.  d_gloss fp32 [1] on the device (the gradient of the
+ * loss; NULL: 1), d_base [T,E] fp32 (a gradient to add to, for example that of
+ * moe_route_bwd; NULL: 0), which may be d_glogits.  Rows of tokens outside the
+ * sequences are not written.  Tokens without p (see above) get d_base alone.
+ */
+moe_status moe_balance_bwd(const moe_handle* h, const float* d_logits, const int32_t* d_cnt,
+                           int32_t T, const int32_t* d_seq_off, int32_t num_seqs, double coef,
+                           const float* d_gloss, const float* d_base, float* d_glogits,
+                           void* stream);
+
+/*
+ * The norms around a block, with its gate and the residual sum, in one pass.
+ * For token t:
+ *   c    = y + add            y = d_y[t], or with gather = 1 the sum of
+ *                             moe_combine, sum_k d_cw[t,k] d_y[pos[t,k]]
+ *   u    = c * r_post * (w_post + weight_offset)    (d_w_post NULL: u = c)
+ *   res' = res_scale * res + gate[t / gate_tokens] * u
+ *   x    = res' * r_pre * (w_pre + weight_offset)
+ * r = 1 / sqrt(mean(v^2) + eps) of the row v that it multiplies.  fp32 sums,
+ * each output rounded once; x is made from res' before that is rounded.
+ *   d_res  [T,H] the residual stream;  d_y [T,H] the block's output, with gather
+ *     the receive rows [RR,H] of the current layout (whose T the call's must be;
+ *     d_cw [T,K] fp32 or NULL: plain sum);  NULL: no block, res' = res, and only
+ *     x is made (d_add, d_gate, d_w_post, d_c, d_res_out, d_rstd_post NULL).
+ *   d_add  [T,H] or NULL: rows added to the block's (a shared expert's).
+ *   d_gate [ceil(T / gate_tokens), H] or NULL: 1.  gate_tokens = 1: a row per
+ *     token; T or more: one for all.
+ *   d_w_post, d_w_pre [H] in weight_dtype (MOE_BF16 or MOE_F32), d_w_pre given
+ *     exactly if d_x is.  weight_offset is added to each (1 for weights that
+ *     are stored as their distance from 1).
+ *   d_res_out [T,H] (may be d_res), d_x [T,H] or NULL, and for the backward,
+ *     each may be NULL: d_c [T,H] (may be d_add, or without gather d_y),
+ *     d_rstd_post, d_rstd_pre [T] fp32.
+ * All rows in `dtype`, H at most MOE_NORM_MAX_WIDTH; res_scale finite, eps > 0.
+ * The square of a row's values must not overflow fp32 (|v| < 1e17).  Without gather the handle's layout is neither read
+ * nor changed.
+ */
+#define MOE_NORM_MAX_WIDTH 16384
+
+typedef struct moe_block_norm_args {
+  const void* d_res;
+  const void* d_y;
+  const float* d_cw;
+  const void* d_add;
+  const void* d_gate;
+  const void* d_w_post;
+  const void* d_w_pre;
+  void* d_res_out;
+  void* d_x;
+  void* d_c;
+  float* d_rstd_post;
+  float* d_rstd_pre;
+  double res_scale;
+  double eps;
+  double weight_offset;
+  int32_t H;
+  int32_t dtype;
+  int32_t weight_dtype;
+  int32_t gate_tokens;
+  int32_t gather; /* 0: token rows, 1: receive rows */
+} moe_block_norm_args;
+
+moe_status moe_block_norm(const moe_handle* h, const moe_block_norm_args* args, int32_t T,
+                          void* stream);
+
+/*
+ * Backward of moe_block_norm: from the gradients of res' and x,
+ *   D       = gres' + r_pre (v - n mean(v n)),   v = gx (w_pre + weight_offset),
+ *                                                n = res' r_pre
+ *   gres    = res_scale * D
+ *   ggate   = sum over the group's tokens of D u
+ *   g       = gate * D
+ *   gy      = r_post (v - m mean(v m)), v = g (w_post + weight_offset),
+ *             m = c r_post                          (no d_w_post: gy = g)
+ *   gw_post = sum_t g m,   gw_pre = sum_t gx n
+ * gy is the gradient of c: of the token rows y, of d_add, and with gather the
+ * row gradient that moe_combine_bwd takes.
+ *   d_gres_out, d_gx [T,H]: gradients of res' and x, either may be NULL (0).
+ *   d_res_out (with d_gx), d_c (with d_gate or d_w_post; the block's output or
+ *     the forward's d_c), d_rstd_pre (with d_gx), d_rstd_post (with d_w_post):
+ *     the forward's.  d_w_pre given exactly if d_gx is.
+ *   Outputs, each may be NULL: d_gres [T,H] (may be d_gres_out), d_gy [T,H],
+ *     d_ggate (as d_gate, in dtype), d_gw_post and d_gw_pre [H] fp32.
+ * Sums over tokens are fp32 and in a fixed order: the same inputs give the same
+ * bits.  d_workspace: moe_block_norm_workspace_bytes(h, T, H, gate_tokens)
+ * bytes (which does not fall as T grows), 256-byte aligned, free after the
+ * call's work; calls that may overlap on the GPU need one each.
+ */
+typedef struct moe_block_norm_bwd_args {
+  const void* d_gres_out;
+  const void* d_gx;
+  const void* d_res_out;
+  const void* d_c;
+  const void* d_gate;
+  const void* d_w_post;
+  const void* d_w_pre;
+  const float* d_rstd_post;
+  const float* d_rstd_pre;
+  void* d_gres;
+  void* d_gy;
+  void* d_ggate;
+  float* d_gw_post;
+  float* d_gw_pre;
+  double res_scale;
+  double weight_offset;
+  int32_t H;
+  int32_t dtype;
+  int32_t weight_dtype;
+  int32_t gate_tokens;
+} moe_block_norm_bwd_args;
+
+/* 0 if a size is invalid. */
+size_t moe_block_norm_workspace_bytes(const moe_handle* h, int32_t T, int32_t H,
+                                      int32_t gate_tokens);
+
+moe_status moe_block_norm_bwd(const moe_handle* h, const moe_block_norm_bwd_args* args, int32_t T,
+                              void* d_workspace, size_t workspace_bytes, void* stream);
+
+/*
  * Copies the device status word to *host_flags (MOE_DEVERR_* bits).  This
  * SYNCHRONISES the handle's device; keep it off the hot path.
  */
