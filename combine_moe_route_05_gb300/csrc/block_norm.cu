@@ -6,10 +6,18 @@
 //   res' = res_scale * res + gate * (c r_c (w_post + offset))
 //   x    = res' r_p (w_pre + offset),    r_v = 1 / sqrt(mean(v^2) + eps)
 //
-// One pass over the rows: a team of threads holds a row in registers, 16
-// elements a thread, and the two sums of squares are its only exchange.  x is
-// made from the sum before that is rounded; sums are fp32, each output is
-// rounded once.
+// One pass over the rows: a team of threads (a warp, or a block) holds a row in
+// registers, 16 elements a thread, and the two sums of squares are its only
+// exchange.  x is made from the sum before that is rounded; sums are fp32, each
+// output is rounded once.
+//
+// Bound by HBM; what stands in its way are the two sums in a row's chain.  Each
+// thread therefore copies the vectors that it will need itself into shared memory
+// ahead of time (cp.async: no other thread waits for them), so loads go on while
+// the team waits for its sums, and its weights, in fp32 with their offset, stay
+// there too.  Arithmetic is on pairs of fp32 (one instruction for both), which
+// halves what the issue slots have to do: without it the backward took 52
+// instructions an element and ran at half of the copy rate.
 #include <type_traits>
 
 #include "common.cuh"
@@ -25,10 +33,184 @@ constexpr int kTeams = 4;          // one-warp teams of a block
 // Tokens whose column sums are added up in registers before they go to memory:
 // bounds the number of fp32 additions in a row for any T.
 constexpr int kFlush = 1024;
+constexpr size_t kShared = 226 * 1024;  // dynamic shared memory of a block, at most
+constexpr size_t kSmShared = 228 * 1024, kBlockShared = 1024 + 512;  // of an SM; a block's own share
+
+// ---------------------------------------------------------------------------
+// pairs of fp32
+
+using F2 = unsigned long long;
+
+__device__ __forceinline__ F2 pair(float a, float b) {
+  F2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float2 split(F2 a) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(a));
+  return r;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+  F2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+  F2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ F2 add2(F2 a, F2 b) {
+  F2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ F2 both(float a) { return pair(a, a); }
+__device__ __forceinline__ float sum_of(F2 a) {
+  const float2 v = split(a);
+  return v.x + v.y;
+}
+
+// A 16-byte vector of a row as pairs (bf16: 4, fp32: 2), and back, rounded.
+template <typename Elt>
+struct PairTraits;
+template <>
+struct PairTraits<__nv_bfloat16> {
+  static constexpr int P = 4;
+  __device__ __forceinline__ static void to(const Vec16& v, F2* f) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      f[i] = pair(__uint_as_float(v.u[i] << 16), __uint_as_float(v.u[i] & 0xffff0000u));
+  }
+  __device__ __forceinline__ static Vec16 from(const F2* f) {
+    Vec16 v;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 a = split(f[i]);
+      const __nv_bfloat162 b = __floats2bfloat162_rn(a.x, a.y);
+      v.u[i] = *reinterpret_cast<const uint32_t*>(&b);
+    }
+    return v;
+  }
+};
+template <>
+struct PairTraits<float> {
+  static constexpr int P = 2;
+  __device__ __forceinline__ static void to(const Vec16& v, F2* f) {
+    f[0] = pair(__uint_as_float(v.u[0]), __uint_as_float(v.u[1]));
+    f[1] = pair(__uint_as_float(v.u[2]), __uint_as_float(v.u[3]));
+  }
+  __device__ __forceinline__ static Vec16 from(const F2* f) {
+    const float2 a = split(f[0]), b = split(f[1]);
+    return Vec16{{__float_as_uint(a.x), __float_as_uint(a.y), __float_as_uint(b.x),
+                  __float_as_uint(b.y)}};
+  }
+};
+
+// ---------------------------------------------------------------------------
+// a thread's own shared memory: vectors on their way, weights
+
+__device__ __forceinline__ void commit_copies() {
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
+// Waits until at most N of the thread's groups of copies are under way.
+template <int N>
+__device__ __forceinline__ void wait_copies() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+// 16 bytes, or zeros where there is nothing to read (`from` is not read then).
+__device__ __forceinline__ void copy_async(uint32_t to, const void* from, bool real) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from),
+               "r"(real ? 16 : 0)
+               : "memory");
+}
+__device__ __forceinline__ Vec16 ld_shared(uint32_t a) {
+  Vec16 v;
+  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(v.u[0]), "=r"(v.u[1]), "=r"(v.u[2]), "=r"(v.u[3])
+               : "r"(a)
+               : "memory");
+  return v;
+}
+__device__ __forceinline__ void st_shared(uint32_t a, float4 v) {
+  asm volatile("st.shared.v4.f32 [%0], {%1,%2,%3,%4};" ::"r"(a), "f"(v.x), "f"(v.y), "f"(v.z),
+               "f"(v.w)
+               : "memory");
+}
+
+// The thread's 16 weights of w, four at a time (a quarter is `step` bytes from
+// the next), zero behind the row's end; vectors of N elements, the thread's are
+// tid, tid + threads, ...
+template <int N>
+__device__ __forceinline__ void keep_weights(const uint8_t* w, int f32, float offset, uint32_t to,
+                                             uint32_t step, int tid, int threads, int nvec) {
+#pragma unroll
+  for (int q = 0; q < kEpt / 4; ++q) {
+    const int v = tid + q / (N / 4) * threads;
+    float4 f{0.0f, 0.0f, 0.0f, 0.0f};
+    if (v < nvec) {
+      const int at = v * (N / 4) + q % (N / 4);
+      if (f32) {
+        f = __ldg(reinterpret_cast<const float4*>(w) + at);
+      } else {
+        const uint2 b = __ldg(reinterpret_cast<const uint2*>(w) + at);
+        f = make_float4(__uint_as_float(b.x << 16), __uint_as_float(b.x & 0xffff0000u),
+                        __uint_as_float(b.y << 16), __uint_as_float(b.y & 0xffff0000u));
+      }
+      f = make_float4(f.x + offset, f.y + offset, f.z + offset, f.w + offset);
+    }
+    st_shared(to + q * step, f);
+  }
+}
+// The weights of the thread's vector i.
+template <int N>
+__device__ __forceinline__ void kept_weights(uint32_t at, uint32_t step, int i, F2* f) {
+#pragma unroll
+  for (int q = 0; q < N / 4; ++q) {
+    const Vec16 v = ld_shared(at + (i * (N / 4) + q) * step);
+    f[2 * q] = pair(__uint_as_float(v.u[0]), __uint_as_float(v.u[1]));
+    f[2 * q + 1] = pair(__uint_as_float(v.u[2]), __uint_as_float(v.u[3]));
+  }
+}
+
+// Sum over the team: a warp, or the block, whose warps hand over through `red`
+// (two sets of 32 values, taken in turn, so that one barrier a sum is enough;
+// zero behind the last warp's, so that they can be read four at a time).
+template <bool WARP>
+__device__ __forceinline__ float team_sum(float v, float* red, int& turn) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
+  if constexpr (WARP) return v;
+  const int warps = blockDim.x >> 5;
+  float* set = red + turn;
+  turn ^= 32;
+  if ((threadIdx.x & 31) == 0) set[threadIdx.x >> 5] = v;
+  __syncthreads();
+  float4 a = *reinterpret_cast<const float4*>(set);
+  for (int w = 4; w < warps; w += 4) {
+    const float4 b = *reinterpret_cast<const float4*>(set + w);
+    a.x += b.x;
+    a.y += b.y;
+    a.z += b.z;
+    a.w += b.w;
+  }
+  return (a.x + a.y) + (a.z + a.w);
+}
+template <bool WARP>
+__device__ __forceinline__ void clear_sums(float* red) {
+  if constexpr (!WARP) {
+    for (int i = threadIdx.x; i < 64; i += blockDim.x) red[i] = 0.0f;
+    __syncthreads();
+  }
+}
+
+// ---------------------------------------------------------------------------
+// forward
 
 struct NormArgs {
   const uint8_t* y;      // [T, H], [rows, H] with pos, or NULL
-  const int32_t* pos;    // [T, K] or NULL
+  const int32_t* pos;    // [T, K] or NULL (then K = 1)
   const float* cw;       // [T, K] or NULL
   const uint8_t* add;    // [T, H] or NULL
   const uint8_t* res;    // [T, H]
@@ -42,172 +224,219 @@ struct NormArgs {
   float* rstd_pre;       // [T] or NULL
   int64_t row_bytes;
   int T, H, nvec, K, rows, gate_tokens;
+  int units;             // teams; a team takes every units-th token
+  int piece_rows;        // rows that a piece has
   int w_f32;             // weights in fp32 (else bf16)
   float res_scale, eps, offset, inv_h;
   uint32_t* flags;
 };
 
-// N weights from column c on, with the offset that the stored ones lack.
-template <int N>
-__device__ __forceinline__ void load_weights(const uint8_t* w, int f32, int c, float offset,
-                                             float (&f)[N]) {
-  if (f32) {
-#pragma unroll
-    for (int i = 0; i < N; i += 4) {
-      const float4 v = __ldg(reinterpret_cast<const float4*>(w) + (c + i) / 4);
-      f[i] = v.x;
-      f[i + 1] = v.y;
-      f[i + 2] = v.z;
-      f[i + 3] = v.w;
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < N; i += 4) {
-      const uint2 v = __ldg(reinterpret_cast<const uint2*>(w) + (c + i) / 4);
-      f[i] = __uint_as_float(v.x << 16);
-      f[i + 1] = __uint_as_float(v.x & 0xffff0000u);
-      f[i + 2] = __uint_as_float(v.y << 16);
-      f[i + 3] = __uint_as_float(v.y & 0xffff0000u);
-    }
-  }
-#pragma unroll
-  for (int i = 0; i < N; ++i) f[i] += offset;
-}
-
-// Sum over the team: a warp, or the block, whose warps hand over through `red`
-// (two sets of 32 values, taken in turn, so that one barrier a sum is enough).
-template <bool WARP>
-__device__ __forceinline__ float team_sum(float v, float (*red)[32], int& turn) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
-  if (WARP) return v;
-  const int lane = threadIdx.x & 31, warps = blockDim.x >> 5;
-  float* set = red[turn];
-  turn ^= 1;
-  if (lane == 0) set[threadIdx.x >> 5] = v;
-  __syncthreads();
-  v = lane < warps ? set[lane] : 0.0f;
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
-  return v;
-}
-
-template <typename Elt, int KMAX, bool WARP, int MAXT>
+// A team takes every units-th token.  A piece is a vector a thread of every row
+// that the sum needs; a token has V.  AHEAD: tokens whose pieces are in shared
+// memory or on their way there (0: vectors are loaded when they are needed).
+// KMAX: rows that are summed at most (1: token rows).
+template <typename Elt, int KMAX, bool WARP, int MAXT, int AHEAD>
 __global__ void __launch_bounds__(MAXT, 1) block_norm_kernel(NormArgs a) {
-  using VT = VecTraits<Elt>;
-  constexpr int N = VT::N, V = kEpt / N;
-  __shared__ float red[2][32];
+  using PT = PairTraits<Elt>;
+  constexpr int P = PT::P, N = 2 * P, V = kEpt / N;
+  constexpr bool GATHER = KMAX > 1;
+  __shared__ __align__(16) float red[64];
+  extern __shared__ __align__(16) uint8_t own[];
   const int tid = WARP ? threadIdx.x & 31 : threadIdx.x;
   const int step = WARP ? 32 : blockDim.x;
-  const int t = WARP ? blockIdx.x * kTeams + (threadIdx.x >> 5) : blockIdx.x;
-  if (t >= a.T) return;
-  int turn = 0;
-  const int64_t row = static_cast<int64_t>(t) * a.row_bytes;
-  float c[V][N];
-  Vec16 res[V];
+  const int unit = WARP ? blockIdx.x * kTeams + (threadIdx.x >> 5) : blockIdx.x;
+  if (unit >= a.units) return;  // a warp's; a block is always a unit
+  // the thread's weights, then its pieces
+  const uint32_t quarter = blockDim.x * 16;
+  const uint32_t wpost = smem_addr(own) + threadIdx.x * 16;
+  const uint32_t wpre = wpost + (a.w_post ? kEpt / 4 * quarter : 0);
+  const uint32_t pieces = wpre + (a.w_pre ? kEpt / 4 * quarter : 0);
+  const uint32_t piece_bytes = a.piece_rows * quarter;
+
+  int p[KMAX];                      // rows that the next pieces to be asked for sum
+  float wk[KMAX], wk_next[KMAX];    // weights of the token in work and the one behind it
+  auto entries = [&](int64_t t) {
 #pragma unroll
-  for (int i = 0; i < V; ++i) {
-    const int v = tid + i * step;
-    if (v < a.nvec) res[i] = ld_vec(a.res + row + v * 16);
-  }
-  float ss = 0.0f;
-  if (a.y) {
-    int p[KMAX > 0 ? KMAX : 1];
-    float wk[KMAX > 0 ? KMAX : 1];
-    if (KMAX > 0) {
+    for (int k = 0; k < KMAX; ++k) {
+      p[k] = GATHER ? -1 : static_cast<int>(t);
+      if (GATHER && k < a.K && t < a.T)
+        p[k] = checked_row(__ldg(a.pos + t * a.K + k), a.rows, a.flags);
+    }
+  };
+  auto weights = [&](int64_t t, float (&w)[KMAX]) {
 #pragma unroll
-      for (int k = 0; k < KMAX; ++k) {
-        p[k] = -1;
-        wk[k] = 1.0f;
-        if (k < a.K) {
-          p[k] = checked_row(__ldg(a.pos + static_cast<size_t>(t) * a.K + k), a.rows, a.flags);
-          if (a.cw) wk[k] = __ldg(a.cw + static_cast<size_t>(t) * a.K + k);
-        }
+    for (int k = 0; k < KMAX; ++k) {
+      w[k] = 0.0f;
+      if (GATHER && k < a.K && t < a.T) {
+        // a dropped entry's row is zeros: whatever its weight is, it adds nothing
+        const int r = __ldg(a.pos + t * a.K + k);
+        if (static_cast<unsigned>(r) < static_cast<unsigned>(a.rows))
+          w[k] = a.cw ? __ldg(a.cw + t * a.K + k) : 1.0f;
       }
     }
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
+  };
+  auto gate_row = [&](int64_t t) { return t / a.gate_tokens * a.row_bytes; };
+  auto fetch = [&](int64_t t, int i, uint32_t to) {
+    if (t < a.T) {
       const int v = tid + i * step;
-#pragma unroll
-      for (int j = 0; j < N; ++j) c[i][j] = 0.0f;
-      if (v >= a.nvec) continue;
-      if (KMAX > 0) {
-        Vec16 in[KMAX > 0 ? KMAX : 1];
-#pragma unroll
-        for (int k = 0; k < KMAX; ++k)
-          if (p[k] >= 0) in[k] = ld_stream(a.y + static_cast<int64_t>(p[k]) * a.row_bytes + v * 16);
+      const bool in = v < a.nvec;
+      const int64_t at = in ? t * a.row_bytes + v * 16 : 0;
+      copy_async(to, a.res + at, in);
+      to += quarter;
+      if (a.y) {
 #pragma unroll
         for (int k = 0; k < KMAX; ++k) {
-          if (p[k] < 0) continue;
-          float f[N];
-          VT::to_f32(in[k], f);
-#pragma unroll
-          for (int j = 0; j < N; ++j) c[i][j] = fmaf(wk[k], f[j], c[i][j]);
+          if (k >= a.K) break;
+          const bool real = in && p[k] >= 0;
+          copy_async(to, a.y + (real ? p[k] * a.row_bytes + v * 16 : 0), real);
+          to += quarter;
         }
-      } else {
-        VT::to_f32(ld_vec(a.y + row + v * 16), c[i]);
       }
       if (a.add) {
-        float f[N];
-        VT::to_f32(ld_vec(a.add + row + v * 16), f);
-#pragma unroll
-        for (int j = 0; j < N; ++j) c[i][j] += f[j];
+        copy_async(to, a.add + at, in);
+        to += quarter;
       }
-      if (a.c) st_vec(a.c + row + v * 16, VT::from_f32(c[i]));
+      if (a.gate) copy_async(to, a.gate + (in ? gate_row(t) + v * 16 : 0), in);
+    }
+    commit_copies();
+  };
+
+  if (AHEAD > 0) {
 #pragma unroll
-      for (int j = 0; j < N; ++j) ss = fmaf(c[i][j], c[i][j], ss);
+    for (int n = 0; n < AHEAD; ++n) {
+      const int64_t t = unit + static_cast<int64_t>(n) * a.units;
+      entries(t);
+#pragma unroll
+      for (int i = 0; i < V; ++i) fetch(t, i, pieces + (n * V + i) * piece_bytes);
     }
-    float r = 1.0f;
-    if (a.w_post) {
-      r = 1.0f / sqrtf(team_sum<WARP>(ss, red, turn) * a.inv_h + a.eps);
-      if (a.rstd_post && tid == 0) a.rstd_post[t] = r;
+    entries(unit + static_cast<int64_t>(AHEAD) * a.units);
+    if (GATHER) weights(unit, wk);
+  }
+  if (a.w_post)
+    keep_weights<N>(a.w_post, a.w_f32, a.offset, wpost, quarter, tid, step, a.nvec);
+  if (a.w_pre) keep_weights<N>(a.w_pre, a.w_f32, a.offset, wpre, quarter, tid, step, a.nvec);
+  clear_sums<WARP>(red);
+  int turn = 0;
+  uint32_t stage = pieces;
+  for (int64_t t = unit; t < a.T; t += a.units) {
+    const int64_t row = t * a.row_bytes;
+    if (GATHER) {
+      if (AHEAD > 0) {
+        weights(t + a.units, wk_next);
+      } else {
+        entries(t);
+        weights(t, wk);
+      }
+    } else if (AHEAD == 0) {
+      entries(t);
     }
-    ss = 0.0f;
+    F2 c[V][P];
+    Vec16 res[V], gate[V];
+    F2 ss = 0;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       const int v = tid + i * step;
-      if (v >= a.nvec) continue;
-      float f[N];
+      const bool in = v < a.nvec;
+      if (AHEAD > 0) wait_copies<V * AHEAD - 1>();
+      uint32_t from = stage + i * piece_bytes;
+      auto next = [&](const uint8_t* g, bool real) {
+        Vec16 x{};
+        if (AHEAD > 0) {
+          x = ld_shared(from);
+          from += quarter;
+        } else if (real) {
+          x = ld_vec(g);
+        }
+        return x;
+      };
+      res[i] = next(a.res + row + v * 16, in);
+      if (a.y) {
+        if (GATHER) {
+          Vec16 in_rows[KMAX];
+          if (AHEAD == 0) {
+#pragma unroll
+            for (int k = 0; k < KMAX; ++k)
+              in_rows[k] = next(a.y + p[k] * a.row_bytes + v * 16, in && p[k] >= 0);
+          }
+#pragma unroll
+          for (int j = 0; j < P; ++j) c[i][j] = 0;
+#pragma unroll
+          for (int k = 0; k < KMAX; ++k) {
+            if (k >= a.K) break;
+            if (AHEAD > 0) in_rows[k] = next(nullptr, in);
+            F2 f[P];
+            PT::to(in_rows[k], f);
+#pragma unroll
+            for (int j = 0; j < P; ++j) c[i][j] = fma2(both(wk[k]), f[j], c[i][j]);
+          }
+        } else {
+          PT::to(next(a.y + row + v * 16, in), c[i]);
+        }
+        if (a.add) {
+          F2 f[P];
+          PT::to(next(a.add + row + v * 16, in), f);
+#pragma unroll
+          for (int j = 0; j < P; ++j) c[i][j] = add2(c[i][j], f[j]);
+        }
+        if (a.gate) gate[i] = next(a.gate + gate_row(t) + v * 16, in);
+        if (a.c && in) st_vec(a.c + row + v * 16, PT::from(c[i]));
+      } else {
+        PT::to(res[i], c[i]);
+      }
+#pragma unroll
+      for (int j = 0; j < P; ++j) ss = fma2(c[i][j], c[i][j], ss);
+      if (AHEAD > 0) fetch(t + static_cast<int64_t>(AHEAD) * a.units, i, stage + i * piece_bytes);
+    }
+    if (AHEAD > 0) {
+      entries(t + static_cast<int64_t>(AHEAD + 1) * a.units);
+      stage += V * piece_bytes;
+      if (stage == pieces + AHEAD * V * piece_bytes) stage = pieces;
+    }
+    if (a.y) {
+      float r = 1.0f;
       if (a.w_post) {
-        load_weights<N>(a.w_post, a.w_f32, v * N, a.offset, f);
-#pragma unroll
-        for (int j = 0; j < N; ++j) c[i][j] *= r * f[j];
+        r = 1.0f / sqrtf(team_sum<WARP>(sum_of(ss), red, turn) * a.inv_h + a.eps);
+        if (a.rstd_post && tid == 0) a.rstd_post[t] = r;
       }
-      if (a.gate) {
-        VT::to_f32(ld_vec(a.gate + static_cast<int64_t>(t / a.gate_tokens) * a.row_bytes + v * 16),
-                   f);
+      ss = 0;
 #pragma unroll
-        for (int j = 0; j < N; ++j) c[i][j] *= f[j];
-      }
-      VT::to_f32(res[i], f);
+      for (int i = 0; i < V; ++i) {
+        F2 f[P];
+        if (a.w_post) {
+          kept_weights<N>(wpost, quarter, i, f);
 #pragma unroll
-      for (int j = 0; j < N; ++j) {
-        c[i][j] = fmaf(a.res_scale, f[j], c[i][j]);
-        ss = fmaf(c[i][j], c[i][j], ss);
+          for (int j = 0; j < P; ++j) c[i][j] = mul2(mul2(c[i][j], both(r)), f[j]);
+        }
+        if (a.gate) {
+          PT::to(gate[i], f);
+#pragma unroll
+          for (int j = 0; j < P; ++j) c[i][j] = mul2(c[i][j], f[j]);
+        }
+        PT::to(res[i], f);
+#pragma unroll
+        for (int j = 0; j < P; ++j) {
+          c[i][j] = fma2(both(a.res_scale), f[j], c[i][j]);
+          ss = fma2(c[i][j], c[i][j], ss);
+        }
+        const int v = tid + i * step;
+        if (v < a.nvec) st_vec(a.res_out + row + v * 16, PT::from(c[i]));
       }
-      st_vec(a.res_out + row + v * 16, VT::from_f32(c[i]));
     }
-  } else {
+    if (a.x) {
+      const float r = 1.0f / sqrtf(team_sum<WARP>(sum_of(ss), red, turn) * a.inv_h + a.eps);
+      if (a.rstd_pre && tid == 0) a.rstd_pre[t] = r;
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-      if (tid + i * step >= a.nvec) continue;
-      VT::to_f32(res[i], c[i]);
+      for (int i = 0; i < V; ++i) {
+        F2 f[P];
+        kept_weights<N>(wpre, quarter, i, f);
 #pragma unroll
-      for (int j = 0; j < N; ++j) ss = fmaf(c[i][j], c[i][j], ss);
+        for (int j = 0; j < P; ++j) f[j] = mul2(mul2(c[i][j], both(r)), f[j]);
+        const int v = tid + i * step;
+        if (v < a.nvec) st_vec(a.x + row + v * 16, PT::from(f));
+      }
     }
-  }
-  if (!a.x) return;
-  const float r = 1.0f / sqrtf(team_sum<WARP>(ss, red, turn) * a.inv_h + a.eps);
-  if (a.rstd_pre && tid == 0) a.rstd_pre[t] = r;
 #pragma unroll
-  for (int i = 0; i < V; ++i) {
-    const int v = tid + i * step;
-    if (v >= a.nvec) continue;
-    float f[N];
-    load_weights<N>(a.w_pre, a.w_f32, v * N, a.offset, f);
-#pragma unroll
-    for (int j = 0; j < N; ++j) c[i][j] *= r * f[j];
-    st_vec(a.x + row + v * 16, VT::from_f32(c[i]));
+    for (int k = 0; k < KMAX; ++k) wk[k] = wk_next[k];
   }
 }
 
@@ -232,7 +461,7 @@ struct NormBwdArgs {
   float* part;              // [2, blocks, H] column sums: post, pre
   float* slots;             // [2 * units, H] gate sums of groups that span units
   int64_t row_bytes;
-  int T, H, nvec, gate_tokens;
+  int T, H, nvec, gate_tokens, groups;
   int chunk, units, blocks; // tokens of a unit (a team), units, blocks
   int w_f32;
   float res_scale, offset, inv_h;
@@ -240,150 +469,183 @@ struct NormBwdArgs {
 
 // Adds a thread's column sums to a row of fp32 sums (or writes them if they are
 // the first) and clears them.
-template <int N, int V>
-__device__ __forceinline__ void flush_sums(float (&acc)[V][N], float* to, bool first, int tid,
+template <int V, int P>
+__device__ __forceinline__ void flush_sums(F2 (&acc)[V][P], float* to, bool first, int tid,
                                            int step, int nvec) {
 #pragma unroll
   for (int i = 0; i < V; ++i) {
     const int v = tid + i * step;
-    if (v < nvec) {
 #pragma unroll
-      for (int j = 0; j < N; j += 4) {
-        float4* p = reinterpret_cast<float4*>(to + v * N + j);
+    for (int j = 0; j < P; j += 2) {
+      if (v < nvec) {
+        float4* p = reinterpret_cast<float4*>(to + (v * P + j) * 2);
         float4 s{0.0f, 0.0f, 0.0f, 0.0f};
         if (!first) s = *p;
-        s.x += acc[i][j];
-        s.y += acc[i][j + 1];
-        s.z += acc[i][j + 2];
-        s.w += acc[i][j + 3];
-        *p = s;
+        const float2 x = split(acc[i][j]), y = split(acc[i][j + 1]);
+        *p = make_float4(s.x + x.x, s.y + x.y, s.z + y.x, s.w + y.y);
       }
+      acc[i][j] = acc[i][j + 1] = 0;
     }
-#pragma unroll
-    for (int j = 0; j < N; ++j) acc[i][j] = 0.0f;
   }
 }
 
 // A unit (a team) takes `chunk` tokens in a row and holds the column sums of the
 // weights' gradients, and of the gate's while the tokens of its group last.
 // D = gres' + r_p (v - h mean(v h)), v = gx w_pre, h = res' r_p: the gradient of
-// the residual sum; then the same form behind the gate for c.
-template <typename Elt, bool GATE, bool WARP, int MAXT>
+// the residual sum; then the same form behind the gate for c.  AHEAD as in the
+// forward.
+template <typename Elt, bool GATE, bool WARP, int MAXT, int AHEAD>
 __global__ void __launch_bounds__(MAXT, 1) block_norm_bwd_kernel(NormBwdArgs a) {
-  using VT = VecTraits<Elt>;
-  constexpr int N = VT::N, V = kEpt / N;
-  __shared__ float red[2][32];
+  using PT = PairTraits<Elt>;
+  constexpr int P = PT::P, N = 2 * P, V = kEpt / N, ROWS = GATE ? 5 : 4;
+  __shared__ __align__(16) float red[64];
+  extern __shared__ __align__(16) uint8_t own[];
   const int tid = WARP ? threadIdx.x & 31 : threadIdx.x;
   const int step = WARP ? 32 : blockDim.x;
   const int unit = WARP ? blockIdx.x * kTeams + (threadIdx.x >> 5) : blockIdx.x;
   if (unit >= a.units) return;  // a warp's; a block is always a unit
-  int turn = 0;
-  float gpost[V][N], gpre[V][N], ggate[V][N];
-#pragma unroll
-  for (int i = 0; i < V; ++i)
-#pragma unroll
-    for (int j = 0; j < N; ++j) gpost[i][j] = gpre[i][j] = ggate[i][j] = 0.0f;
+  const uint32_t quarter = blockDim.x * 16;
+  const uint32_t wpost = smem_addr(own) + threadIdx.x * 16;
+  const uint32_t wpre = wpost + kEpt / 4 * quarter;
+  const uint32_t mine = wpre + kEpt / 4 * quarter;
+  constexpr int kToken = ROWS * V;  // vectors a thread holds of a token
   const int64_t begin64 = static_cast<int64_t>(unit) * a.chunk;
   const int begin = static_cast<int>(begin64 < a.T ? begin64 : a.T);
   const int end = static_cast<int>(begin64 + a.chunk < a.T ? begin64 + a.chunk : a.T);
+  const uint8_t* rows[5] = {a.gres_out, a.gx, a.gx ? a.res_out : nullptr, a.c, a.gate};
+  auto row_of = [&](int k, int64_t t) { return (k == 4 ? t / a.gate_tokens : t) * a.row_bytes; };
+  auto fetch = [&](int64_t t, uint32_t stage) {
+    if (t < end) {
+#pragma unroll
+      for (int k = 0; k < ROWS; ++k) {
+        if (!rows[k]) continue;
+        const uint8_t* p = rows[k] + row_of(k, t);
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+          const int v = tid + i * step;
+          const bool in = v < a.nvec;
+          copy_async(stage + (k * V + i) * quarter, p + (in ? v * 16 : 0), in);
+        }
+      }
+    }
+    commit_copies();
+  };
+  if (AHEAD > 0)
+    for (int n = 0; n < AHEAD; ++n)
+      fetch(static_cast<int64_t>(begin) + n, mine + n * kToken * quarter);
+  if (a.w_post)
+    keep_weights<N>(a.w_post, a.w_f32, a.offset, wpost, quarter, tid, step, a.nvec);
+  if (a.gx) keep_weights<N>(a.w_pre, a.w_f32, a.offset, wpre, quarter, tid, step, a.nvec);
+  clear_sums<WARP>(red);
+  F2 gpost[V][P], gpre[V][P], ggate[V][P];
+#pragma unroll
+  for (int i = 0; i < V; ++i)
+#pragma unroll
+    for (int j = 0; j < P; ++j) gpost[i][j] = gpre[i][j] = ggate[i][j] = 0;
   float* post_row = a.part + static_cast<size_t>(unit) * a.H;
   float* pre_row = a.part + static_cast<size_t>(a.units + unit) * a.H;
   bool first = true, gate_first = true;
-  int held = 0, gate_held = 0;
+  int held = 0, gate_held = 0, turn = 0;
+  uint32_t stage = mine;
   for (int t = begin; t < end; ++t) {
     const int64_t row = static_cast<int64_t>(t) * a.row_bytes;
-    float D[V][N], h[V][N];
-    float s = 0.0f;
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
+    auto load = [&](int k, int i, F2* f) {
+      Vec16 x{};
       const int v = tid + i * step;
-#pragma unroll
-      for (int j = 0; j < N; ++j) D[i][j] = 0.0f;
-      if (v < a.nvec && a.gres_out) VT::to_f32(ld_vec(a.gres_out + row + v * 16), D[i]);
-    }
+      if (AHEAD > 0) x = ld_shared(stage + (k * V + i) * quarter);
+      else if (v < a.nvec) x = ld_vec(rows[k] + row_of(k, t) + v * 16);
+      PT::to(x, f);
+    };
+    const float r_pre = a.gx ? __ldg(a.rstd_pre + t) : 0.0f;
+    const float r = a.w_post ? __ldg(a.rstd_post + t) : 1.0f;
+    if (AHEAD > 0) wait_copies<AHEAD - 1>();
+    F2 D[V][P], h[V][P];
     if (a.gx) {
-      const float r = __ldg(a.rstd_pre + t);
-      float vv[V][N];
+      F2 s = 0;
 #pragma unroll
       for (int i = 0; i < V; ++i) {
-        const int v = tid + i * step;
-        if (v >= a.nvec) continue;
-        float w[N];
-        VT::to_f32(ld_vec(a.gx + row + v * 16), vv[i]);
-        VT::to_f32(ld_vec(a.res_out + row + v * 16), h[i]);
-        load_weights<N>(a.w_pre, a.w_f32, v * N, a.offset, w);
+        F2 w[P];
+        load(1, i, D[i]);
+        load(2, i, h[i]);
+        kept_weights<N>(wpre, quarter, i, w);
 #pragma unroll
-        for (int j = 0; j < N; ++j) {
-          h[i][j] *= r;
-          gpre[i][j] = fmaf(vv[i][j], h[i][j], gpre[i][j]);
-          vv[i][j] *= w[j];
-          s = fmaf(vv[i][j], h[i][j], s);
+        for (int j = 0; j < P; ++j) {
+          h[i][j] = mul2(h[i][j], both(r_pre));
+          gpre[i][j] = fma2(D[i][j], h[i][j], gpre[i][j]);
+          D[i][j] = mul2(D[i][j], w[j]);
+          s = fma2(D[i][j], h[i][j], s);
         }
       }
-      s = team_sum<WARP>(s, red, turn) * a.inv_h;
+      const float m = team_sum<WARP>(sum_of(s), red, turn) * a.inv_h;
 #pragma unroll
-      for (int i = 0; i < V; ++i)
-        if (tid + i * step < a.nvec)
+      for (int i = 0; i < V; ++i) {
+        F2 g[P];
 #pragma unroll
-          for (int j = 0; j < N; ++j) D[i][j] = fmaf(r, fmaf(-s, h[i][j], vv[i][j]), D[i][j]);
+        for (int j = 0; j < P; ++j) g[j] = 0;
+        if (a.gres_out) load(0, i, g);
+#pragma unroll
+        for (int j = 0; j < P; ++j)
+          D[i][j] = fma2(both(r_pre), fma2(both(-m), h[i][j], D[i][j]), g[j]);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < V; ++i) load(0, i, D[i]);
     }
     if (a.gres) {
 #pragma unroll
       for (int i = 0; i < V; ++i) {
         const int v = tid + i * step;
-        if (v >= a.nvec) continue;
-        float o[N];
+        F2 o[P];
 #pragma unroll
-        for (int j = 0; j < N; ++j) o[j] = a.res_scale * D[i][j];
-        st_vec(a.gres + row + v * 16, VT::from_f32(o));
+        for (int j = 0; j < P; ++j) o[j] = mul2(both(a.res_scale), D[i][j]);
+        if (v < a.nvec) st_vec(a.gres + row + v * 16, PT::from(o));
       }
     }
-    const float r = a.w_post ? __ldg(a.rstd_post + t) : 1.0f;
-    s = 0.0f;
     if (a.c) {
+      F2 s = 0;
 #pragma unroll
       for (int i = 0; i < V; ++i) {
-        const int v = tid + i * step;
-        if (v >= a.nvec) continue;
-        float w[N], g[N];
-        VT::to_f32(ld_vec(a.c + row + v * 16), h[i]);
+        F2 w[P];
+        load(3, i, h[i]);
 #pragma unroll
-        for (int j = 0; j < N; ++j) {
-          h[i][j] *= r;
-          w[j] = 1.0f;
-        }
-        if (a.w_post) load_weights<N>(a.w_post, a.w_f32, v * N, a.offset, w);
+        for (int j = 0; j < P; ++j) h[i][j] = mul2(h[i][j], both(r));
+        if (a.w_post) kept_weights<N>(wpost, quarter, i, w);
         if (GATE) {
-          VT::to_f32(ld_vec(a.gate + static_cast<int64_t>(t / a.gate_tokens) * a.row_bytes + v * 16),
-                     g);
+          F2 g[P];
+          load(4, i, g);
 #pragma unroll
-          for (int j = 0; j < N; ++j) {
-            ggate[i][j] = fmaf(D[i][j], h[i][j] * w[j], ggate[i][j]);
-            D[i][j] *= g[j];
+          for (int j = 0; j < P; ++j) {
+            ggate[i][j] = fma2(D[i][j], a.w_post ? mul2(h[i][j], w[j]) : h[i][j], ggate[i][j]);
+            D[i][j] = mul2(D[i][j], g[j]);
           }
         }
         if (a.w_post) {
 #pragma unroll
-          for (int j = 0; j < N; ++j) {
-            gpost[i][j] = fmaf(D[i][j], h[i][j], gpost[i][j]);
-            D[i][j] *= w[j];
-            s = fmaf(D[i][j], h[i][j], s);
+          for (int j = 0; j < P; ++j) {
+            gpost[i][j] = fma2(D[i][j], h[i][j], gpost[i][j]);
+            D[i][j] = mul2(D[i][j], w[j]);
+            s = fma2(D[i][j], h[i][j], s);
           }
         }
       }
       if (a.w_post) {
-        s = team_sum<WARP>(s, red, turn) * a.inv_h;
+        const float m = team_sum<WARP>(sum_of(s), red, turn) * a.inv_h;
 #pragma unroll
         for (int i = 0; i < V; ++i)
-          if (tid + i * step < a.nvec)
 #pragma unroll
-            for (int j = 0; j < N; ++j) D[i][j] = r * fmaf(-s, h[i][j], D[i][j]);
+          for (int j = 0; j < P; ++j)
+            D[i][j] = mul2(both(r), fma2(both(-m), h[i][j], D[i][j]));
       }
     }
     if (a.gy) {
 #pragma unroll
       for (int i = 0; i < V; ++i)
-        if (tid + i * step < a.nvec) st_vec(a.gy + row + (tid + i * step) * 16, VT::from_f32(D[i]));
+        if (tid + i * step < a.nvec) st_vec(a.gy + row + (tid + i * step) * 16, PT::from(D[i]));
+    }
+    if (AHEAD > 0) {
+      fetch(static_cast<int64_t>(t) + AHEAD, stage);
+      stage += kToken * quarter;
+      if (stage == mine + AHEAD * kToken * quarter) stage = mine;
     }
     if (GATE && a.ggate) {
       const int group = t / a.gate_tokens;
@@ -397,35 +659,39 @@ __global__ void __launch_bounds__(MAXT, 1) block_norm_bwd_kernel(NormBwdArgs a) 
           const int v = tid + i * step;
           if (v < a.nvec) {
 #pragma unroll
-            for (int j = 0; j < N; ++j)
-              if (!gate_first) ggate[i][j] += slot[v * N + j];
-            st_vec(a.ggate + group * a.row_bytes + v * 16, VT::from_f32(ggate[i]));
+            for (int j = 0; j < P; ++j)
+              if (!gate_first) {
+                const float2 x = *reinterpret_cast<const float2*>(slot + (v * P + j) * 2);
+                ggate[i][j] = add2(ggate[i][j], pair(x.x, x.y));
+              }
+            st_vec(a.ggate + group * a.row_bytes + v * 16, PT::from(ggate[i]));
           }
 #pragma unroll
-          for (int j = 0; j < N; ++j) ggate[i][j] = 0.0f;
+          for (int j = 0; j < P; ++j) ggate[i][j] = 0;
         }
         gate_first = true;
         gate_held = 0;
       } else if (ends || t + 1 == end || ++gate_held == kFlush) {
-        flush_sums<N, V>(ggate, slot, gate_first, tid, step, a.nvec);
+        flush_sums(ggate, slot, gate_first, tid, step, a.nvec);
         gate_first = ends;
         gate_held = 0;
       }
     }
     if (++held == kFlush) {
-      if (a.gw_post) flush_sums<N, V>(gpost, post_row, first, tid, step, a.nvec);
-      if (a.gw_pre) flush_sums<N, V>(gpre, pre_row, first, tid, step, a.nvec);
+      if (a.gw_post) flush_sums(gpost, post_row, first, tid, step, a.nvec);
+      if (a.gw_pre) flush_sums(gpre, pre_row, first, tid, step, a.nvec);
       first = false;
       held = 0;
     }
   }
-  if (a.gw_post) flush_sums<N, V>(gpost, post_row, first, tid, step, a.nvec);
-  if (a.gw_pre) flush_sums<N, V>(gpre, pre_row, first, tid, step, a.nvec);
+  if (a.gw_post) flush_sums(gpost, post_row, first, tid, step, a.nvec);
+  if (a.gw_pre) flush_sums(gpre, pre_row, first, tid, step, a.nvec);
 }
 
 // Joins the units' column sums: row y = 0, 1 of the grid the weights'
-// gradients; row 2 + u the gate's of a group that begins in unit u and goes on
-// behind it.
+// gradients; row 2 + i the gate's of group i, or where there are more groups than
+// units of the one that goes on from unit i into the next; a group inside one
+// unit is done.
 template <typename Elt>
 __global__ void __launch_bounds__(1024) block_norm_join_kernel(NormBwdArgs a) {
   grid_dependency_wait();
@@ -442,16 +708,15 @@ __global__ void __launch_bounds__(1024) block_norm_join_kernel(NormBwdArgs a) {
     from += static_cast<size_t>(y) * a.units * a.H;
     if (!out) return;
   } else {
-    const int u = y - 2;
-    const int64_t begin = static_cast<int64_t>(u) * a.chunk, next = begin + a.chunk;
-    if (next >= a.T) return;
-    group = static_cast<int>(next / a.gate_tokens);
+    const int64_t next = (static_cast<int64_t>(y - 2) + 1) * a.chunk;
+    if (a.groups > a.units && next >= a.T) return;
+    group = a.groups > a.units ? static_cast<int>(next / a.gate_tokens) : y - 2;
     const int64_t g0 = static_cast<int64_t>(group) * a.gate_tokens;
-    if (g0 < begin || g0 >= next) return;  // begins elsewhere
     const int64_t g1 = min(g0 + a.gate_tokens, static_cast<int64_t>(a.T));
-    from = a.slots;
-    u0 = u;
+    u0 = static_cast<int>(g0 / a.chunk);
     u1 = static_cast<int>((g1 - 1) / a.chunk) + 1;
+    if (u1 - u0 < 2 || (a.groups > a.units && u0 != y - 2)) return;
+    from = a.slots;
     stride = 2;
     head = 1;
   }
@@ -491,7 +756,66 @@ void bwd_units(int T, int H, int num_sms, int* chunk, int* units) {
   *units = n;
 }
 
+size_t weight_bytes(int threads) { return static_cast<size_t>(threads) * kEpt * sizeof(float); }
+
+// Largest dynamic shared memory for a kernel that takes more than the default.
+template <typename K>
+cudaError_t allow_shared(K k) {
+  return cudaFuncSetAttribute(reinterpret_cast<const void*>(k),
+                              cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              static_cast<int>(kShared));
+}
+
+template <typename Elt, int KMAX>
+auto forward_kernel(bool warp, int threads, int ahead) {
+  if (warp)
+    return ahead == 2   ? block_norm_kernel<Elt, KMAX, true, 32 * kTeams, 2>
+           : ahead == 1 ? block_norm_kernel<Elt, KMAX, true, 32 * kTeams, 1>
+                        : block_norm_kernel<Elt, KMAX, true, 32 * kTeams, 0>;
+  if (threads <= 512)
+    return ahead == 2   ? block_norm_kernel<Elt, KMAX, false, 512, 2>
+           : ahead == 1 ? block_norm_kernel<Elt, KMAX, false, 512, 1>
+                        : block_norm_kernel<Elt, KMAX, false, 512, 0>;
+  return ahead >= 1 ? block_norm_kernel<Elt, KMAX, false, 1024, 1>
+                    : block_norm_kernel<Elt, KMAX, false, 1024, 0>;
+}
+
+template <typename Elt, bool GATE>
+auto backward_kernel(bool warp, int threads, int ahead) {
+  if (warp)
+    return ahead == 3   ? block_norm_bwd_kernel<Elt, GATE, true, 32 * kTeams, 3>
+           : ahead == 2 ? block_norm_bwd_kernel<Elt, GATE, true, 32 * kTeams, 2>
+                        : block_norm_bwd_kernel<Elt, GATE, true, 32 * kTeams, 0>;
+  if (threads <= 512)
+    return ahead == 3   ? block_norm_bwd_kernel<Elt, GATE, false, 512, 3>
+           : ahead == 2 ? block_norm_bwd_kernel<Elt, GATE, false, 512, 2>
+                        : block_norm_bwd_kernel<Elt, GATE, false, 512, 0>;
+  return block_norm_bwd_kernel<Elt, GATE, false, 1024, 0>;
+}
+
+template <typename Elt>
+cudaError_t allow_all() {
+  cudaError_t e = cudaSuccess;
+  for (int ahead = 0; ahead <= 3; ++ahead)
+    for (int threads : {128, 512, 1024})
+      for (bool warp : {false, true}) {
+        for (auto k : {forward_kernel<Elt, 1>(warp, threads, ahead),
+                       forward_kernel<Elt, 8>(warp, threads, ahead),
+                       forward_kernel<Elt, 16>(warp, threads, ahead)})
+          if (e == cudaSuccess) e = allow_shared(k);
+        for (auto k : {backward_kernel<Elt, false>(warp, threads, ahead),
+                       backward_kernel<Elt, true>(warp, threads, ahead)})
+          if (e == cudaSuccess) e = allow_shared(k);
+      }
+  return e;
+}
+
 }  // namespace
+
+cudaError_t prepare_block_norm_kernels() {
+  const cudaError_t e = allow_all<__nv_bfloat16>();
+  return e == cudaSuccess ? allow_all<float>() : e;
+}
 
 size_t block_norm_workspace(const moe_handle* h, int T, int H, int gate_tokens) {
   const int most = bwd_units_per_sm(H) * h->num_sms;  // grows with T, unlike the units in use
@@ -532,20 +856,26 @@ cudaError_t launch_block_norm(const moe_handle* h, const moe_block_norm_args& q,
   if (T == 0) return cudaSuccess;
   const bool warp = one_warp(q.H);
   const int threads = warp ? 32 * kTeams : team_threads(q.H);
-  auto pick = [&](auto elt, auto kmax) {
-    using Elt = decltype(elt);
-    constexpr int K = decltype(kmax)::value;
-    return warp ? block_norm_kernel<Elt, K, true, 32 * kTeams>
-           : threads <= 512 ? block_norm_kernel<Elt, K, false, 512>
-                            : block_norm_kernel<Elt, K, false, 1024>;
-  };
+  if (!q.gather) a.K = 1;
+  a.piece_rows = 1 + (a.y ? a.K : 0) + (a.add != nullptr) + (a.gate != nullptr);
+  const size_t kept = weight_bytes(threads) * ((a.w_post != nullptr) + (a.w_pre != nullptr));
+  const size_t token = static_cast<size_t>(threads) * kEpt * (bf16 ? 2 : 4) * a.piece_rows;
+  int ahead = 2;
+  while (ahead > 0 && kept + ahead * token > kShared) --ahead;
+  if (threads > 512 && ahead > 1) ahead = 1;
+  const size_t smem = kept + ahead * token;
   auto with = [&](auto elt) {
-    return !q.gather ? pick(elt, std::integral_constant<int, 0>{})
-           : a.K <= 8 ? pick(elt, std::integral_constant<int, 8>{})
-                      : pick(elt, std::integral_constant<int, 16>{});
+    using Elt = decltype(elt);
+    return !q.gather ? forward_kernel<Elt, 1>(warp, threads, ahead)
+           : a.K <= 8 ? forward_kernel<Elt, 8>(warp, threads, ahead)
+                      : forward_kernel<Elt, 16>(warp, threads, ahead);
   };
   auto k = bf16 ? with(__nv_bfloat16{}) : with(float{});
-  k<<<warp ? (T + kTeams - 1) / kTeams : T, threads, 0, s>>>(a);
+  const long long teams = warp ? kTeams : 1;
+  const long long most =
+      teams * h->num_sms * resident_blocks(reinterpret_cast<const void*>(k), threads, smem);
+  a.units = static_cast<int>(T < most ? T : most);
+  k<<<static_cast<unsigned>((a.units + teams - 1) / teams), threads, smem, s>>>(a);
   return cudaGetLastError();
 }
 
@@ -572,6 +902,7 @@ cudaError_t launch_block_norm_bwd(const moe_handle* h, const moe_block_norm_bwd_
   a.H = q.H;
   a.nvec = static_cast<int>(a.row_bytes / 16);
   a.gate_tokens = q.gate_tokens;
+  a.groups = T > 0 ? (T - 1) / q.gate_tokens + 1 : 0;
   a.w_f32 = q.weight_dtype == MOE_F32;
   a.res_scale = static_cast<float>(q.res_scale);
   a.offset = static_cast<float>(q.weight_offset);
@@ -582,25 +913,28 @@ cudaError_t launch_block_norm_bwd(const moe_handle* h, const moe_block_norm_bwd_
   const bool warp = one_warp(q.H);
   a.blocks = warp ? (a.units + kTeams - 1) / kTeams : a.units;
   const int threads = warp ? 32 * kTeams : team_threads(q.H);
-  auto pick = [&](auto elt, auto gated) {
-    using Elt = decltype(elt);
-    constexpr bool G = decltype(gated)::value;
-    return warp ? block_norm_bwd_kernel<Elt, G, true, 32 * kTeams>
-           : threads <= 512 ? block_norm_bwd_kernel<Elt, G, false, 512>
-                            : block_norm_bwd_kernel<Elt, G, false, 1024>;
-  };
-  using B = __nv_bfloat16;
   const bool gated = q.d_gate != nullptr;
-  auto k = bf16 ? (gated ? pick(B{}, std::true_type{}) : pick(B{}, std::false_type{}))
-                : (gated ? pick(float{}, std::true_type{}) : pick(float{}, std::false_type{}));
+  const size_t kept = 2 * weight_bytes(threads);
+  const size_t token = static_cast<size_t>(threads) * kEpt * (bf16 ? 2 : 4) * (gated ? 5 : 4);
+  const int blocks_per_sm = warp ? 16 / kTeams : bwd_units_per_sm(q.H);
+  const size_t most = kSmShared / blocks_per_sm - kBlockShared;
+  int ahead = threads > 512 ? 0 : 3;
+  while (ahead > 0 && kept + ahead * token > most) --ahead;
+  if (ahead == 1) ahead = 0;
+  const size_t smem = kept + ahead * token;
+  using B = __nv_bfloat16;
+  auto k = bf16 ? (gated ? backward_kernel<B, true>(warp, threads, ahead)
+                         : backward_kernel<B, false>(warp, threads, ahead))
+                : (gated ? backward_kernel<float, true>(warp, threads, ahead)
+                         : backward_kernel<float, false>(warp, threads, ahead));
   if (T > 0) {
-    k<<<a.blocks, threads, 0, s>>>(a);
+    k<<<a.blocks, threads, smem, s>>>(a);
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
   }
   const bool spans = a.ggate && a.gate_tokens > 1;
   if (!a.gw_post && !a.gw_pre && !spans) return cudaSuccess;
-  const int join_rows = spans ? 2 + a.units : 2;
+  const int join_rows = 2 + (!spans ? 0 : a.groups < a.units ? a.groups : a.units);
   if (T == 0) a.units = 0;  // sums of nothing
   return launch_chained(bf16 ? block_norm_join_kernel<B> : block_norm_join_kernel<float>,
                         dim3((q.H + 31) / 32, join_rows), dim3(1024), 0, s, false, a);

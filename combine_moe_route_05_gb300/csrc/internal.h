@@ -131,6 +131,7 @@ cudaError_t launch_balance_bwd(const moe_handle* h, const float* logits, const i
                                const int32_t* off, int S, double coef, const float* gloss,
                                const float* base, float* glogits, cudaStream_t s);
 
+cudaError_t prepare_block_norm_kernels();
 size_t block_norm_workspace(const moe_handle* h, int T, int H, int gate_tokens);
 cudaError_t launch_block_norm(const moe_handle* h, const moe_block_norm_args& q, int T,
                               cudaStream_t s);
