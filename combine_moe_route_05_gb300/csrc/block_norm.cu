@@ -18,7 +18,7 @@
 // there too.  Arithmetic is on pairs of fp32 (one instruction for both), which
 // halves what the issue slots have to do: without it the backward took 52
 // instructions an element and ran at half of the copy rate.
-#include <type_traits>
+#include <mutex>
 
 #include "common.cuh"
 #include "internal.h"
@@ -139,14 +139,19 @@ __device__ __forceinline__ void st_shared(uint32_t a, float4 v) {
                : "memory");
 }
 
-// The thread's 16 weights of w, four at a time (a quarter is `step` bytes from
-// the next), zero behind the row's end; vectors of N elements, the thread's are
-// tid, tid + threads, ...
+// A thread's shared memory is its own slots of 16 bytes, `sb` = 16 times the
+// block's threads from one to the next: the copies of a warp land side by side.
+// (Slots of a thread one behind another, with addresses known when compiled, took
+// the backward from 302 to 372 us at the DeepSeek-V3 shape.)
+constexpr int kWeightSlots = kEpt / 4;  // 16 fp32
+
+// Keeps the thread's 16 weights of w from `to` on, zero behind the row's end;
+// its vectors of N elements are tid, tid + threads, ...
 template <int N>
 __device__ __forceinline__ void keep_weights(const uint8_t* w, int f32, float offset, uint32_t to,
-                                             uint32_t step, int tid, int threads, int nvec) {
+                                             uint32_t sb, int tid, int threads, int nvec) {
 #pragma unroll
-  for (int q = 0; q < kEpt / 4; ++q) {
+  for (int q = 0; q < kWeightSlots; ++q) {
     const int v = tid + q / (N / 4) * threads;
     float4 f{0.0f, 0.0f, 0.0f, 0.0f};
     if (v < nvec) {
@@ -160,15 +165,15 @@ __device__ __forceinline__ void keep_weights(const uint8_t* w, int f32, float of
       }
       f = make_float4(f.x + offset, f.y + offset, f.z + offset, f.w + offset);
     }
-    st_shared(to + q * step, f);
+    st_shared(to + q * sb, f);
   }
 }
 // The weights of the thread's vector i.
 template <int N>
-__device__ __forceinline__ void kept_weights(uint32_t at, uint32_t step, int i, F2* f) {
+__device__ __forceinline__ void kept_weights(uint32_t at, uint32_t sb, int i, F2* f) {
 #pragma unroll
   for (int q = 0; q < N / 4; ++q) {
-    const Vec16 v = ld_shared(at + (i * (N / 4) + q) * step);
+    const Vec16 v = ld_shared(at + (i * (N / 4) + q) * sb);
     f[2 * q] = pair(__uint_as_float(v.u[0]), __uint_as_float(v.u[1]));
     f[2 * q + 1] = pair(__uint_as_float(v.u[2]), __uint_as_float(v.u[3]));
   }
@@ -225,172 +230,186 @@ struct NormArgs {
   int64_t row_bytes;
   int T, H, nvec, K, rows, gate_tokens;
   int units;             // teams; a team takes every units-th token
-  int piece_rows;        // rows that a piece has
   int w_f32;             // weights in fp32 (else bf16)
   float res_scale, eps, offset, inv_h;
   uint32_t* flags;
 };
 
-// A team takes every units-th token.  A piece is a vector a thread of every row
-// that the sum needs; a token has V.  AHEAD: tokens whose pieces are in shared
-// memory or on their way there (0: vectors are loaded when they are needed).
-// KMAX: rows that are summed at most (1: token rows).
+// A team takes every units-th token, a vector a thread of all its rows at a time.
+// AHEAD: tokens whose vectors are in shared memory or on their way there (0: they
+// are loaded when they are needed).  KMAX: rows that are summed at most (1: token
+// rows).
+template <int KMAX>
+struct NormSlots {  // of one vector's rows
+  static constexpr int Res = KMAX, Add = KMAX + 1, Gate = KMAX + 2, Count = KMAX + 3;
+};
+
+template <typename Elt, int KMAX, int AHEAD>
+constexpr int forward_slots() {
+  constexpr int V = kEpt / (2 * PairTraits<Elt>::P);
+  return 2 * kWeightSlots + AHEAD * V * NormSlots<KMAX>::Count;
+}
+
 template <typename Elt, int KMAX, bool WARP, int MAXT, int AHEAD>
 __global__ void __launch_bounds__(MAXT, 1) block_norm_kernel(NormArgs a) {
   using PT = PairTraits<Elt>;
+  using Slot = NormSlots<KMAX>;
   constexpr int P = PT::P, N = 2 * P, V = kEpt / N;
   constexpr bool GATHER = KMAX > 1;
+  const uint32_t sb = blockDim.x * 16;
+  const uint32_t vector = Slot::Count * sb, token = V * vector;  // bytes
+  static_assert(!GATHER || AHEAD < 2, "a token's weights are asked for one token ahead");
   __shared__ __align__(16) float red[64];
   extern __shared__ __align__(16) uint8_t own[];
   const int tid = WARP ? threadIdx.x & 31 : threadIdx.x;
   const int step = WARP ? 32 : blockDim.x;
   const int unit = WARP ? blockIdx.x * kTeams + (threadIdx.x >> 5) : blockIdx.x;
   if (unit >= a.units) return;  // a warp's; a block is always a unit
-  // the thread's weights, then its pieces
-  const uint32_t quarter = blockDim.x * 16;
   const uint32_t wpost = smem_addr(own) + threadIdx.x * 16;
-  const uint32_t wpre = wpost + (a.w_post ? kEpt / 4 * quarter : 0);
-  const uint32_t pieces = wpre + (a.w_pre ? kEpt / 4 * quarter : 0);
-  const uint32_t piece_bytes = a.piece_rows * quarter;
+  const uint32_t wpre = wpost + kWeightSlots * sb;
+  const uint32_t ring = wpre + kWeightSlots * sb;
+  bool in[V];    // vectors inside the row, and where
+  int at[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    in[i] = tid + i * step < a.nvec;
+    at[i] = in[i] ? (tid + i * step) * 16 : 0;
+  }
 
-  int p[KMAX];                      // rows that the next pieces to be asked for sum
-  float wk[KMAX], wk_next[KMAX];    // weights of the token in work and the one behind it
-  auto entries = [&](int64_t t) {
+  // receive rows and weights of a token's entries, as read
+  auto read_entries = [&](int64_t t, const auto* from, auto (&to)[KMAX], auto none) {
 #pragma unroll
     for (int k = 0; k < KMAX; ++k) {
-      p[k] = GATHER ? -1 : static_cast<int>(t);
-      if (GATHER && k < a.K && t < a.T)
-        p[k] = checked_row(__ldg(a.pos + t * a.K + k), a.rows, a.flags);
+      to[k] = none;
+      if (k < a.K && t < a.T) to[k] = __ldg(from + t * a.K + k);
     }
   };
-  auto weights = [&](int64_t t, float (&w)[KMAX]) {
+  auto check_entries = [&](int (&p)[KMAX]) {
 #pragma unroll
-    for (int k = 0; k < KMAX; ++k) {
-      w[k] = 0.0f;
-      if (GATHER && k < a.K && t < a.T) {
-        // a dropped entry's row is zeros: whatever its weight is, it adds nothing
-        const int r = __ldg(a.pos + t * a.K + k);
-        if (static_cast<unsigned>(r) < static_cast<unsigned>(a.rows))
-          w[k] = a.cw ? __ldg(a.cw + t * a.K + k) : 1.0f;
-      }
-    }
+    for (int k = 0; k < KMAX; ++k)
+      if (p[k] != -1) p[k] = checked_row(p[k], a.rows, a.flags);
   };
-  auto gate_row = [&](int64_t t) { return t / a.gate_tokens * a.row_bytes; };
+  int p[KMAX], p_read[KMAX];     // rows of the token asked for next, and of the one behind it
+  float wk[KMAX], w_read[KMAX];  // weights of the token in work and the one behind it
   auto fetch = [&](int64_t t, int i, uint32_t to) {
     if (t < a.T) {
-      const int v = tid + i * step;
-      const bool in = v < a.nvec;
-      const int64_t at = in ? t * a.row_bytes + v * 16 : 0;
-      copy_async(to, a.res + at, in);
-      to += quarter;
-      if (a.y) {
+      const int64_t off = t * a.row_bytes + at[i];
+      copy_async(to + Slot::Res * sb, a.res + off, in[i]);
+      if (GATHER) {
 #pragma unroll
         for (int k = 0; k < KMAX; ++k) {
           if (k >= a.K) break;
-          const bool real = in && p[k] >= 0;
-          copy_async(to, a.y + (real ? p[k] * a.row_bytes + v * 16 : 0), real);
-          to += quarter;
+          const bool real = in[i] && p[k] >= 0;
+          copy_async(to + k * sb, a.y + (real ? p[k] * a.row_bytes + at[i] : 0), real);
         }
+      } else if (a.y) {
+        copy_async(to, a.y + off, in[i]);
       }
-      if (a.add) {
-        copy_async(to, a.add + at, in);
-        to += quarter;
-      }
-      if (a.gate) copy_async(to, a.gate + (in ? gate_row(t) + v * 16 : 0), in);
+      if (a.add) copy_async(to + Slot::Add * sb, a.add + off, in[i]);
+      if (a.gate)
+        copy_async(to + Slot::Gate * sb,
+                   a.gate + (static_cast<unsigned>(t) / static_cast<unsigned>(a.gate_tokens)) *
+                                a.row_bytes + at[i],
+                   in[i]);
     }
     commit_copies();
   };
+  // weights as they count: a dropped entry's row is zeros, and whatever its
+  // weight is, it adds nothing
+  auto count_weights = [&](const float (&read)[KMAX]) {
+#pragma unroll
+    for (int k = 0; k < KMAX; ++k) wk[k] = p[k] < 0 ? 0.0f : a.cw ? read[k] : 1.0f;
+  };
 
   if (AHEAD > 0) {
-#pragma unroll
-    for (int n = 0; n < AHEAD; ++n) {
-      const int64_t t = unit + static_cast<int64_t>(n) * a.units;
-      entries(t);
-#pragma unroll
-      for (int i = 0; i < V; ++i) fetch(t, i, pieces + (n * V + i) * piece_bytes);
+    if (GATHER) {
+      read_entries(unit, a.pos, p, -1);
+      if (a.cw) read_entries(unit, a.cw, w_read, 0.0f);
+      read_entries(unit + static_cast<int64_t>(a.units), a.pos, p_read, -1);
+      check_entries(p);
+      count_weights(w_read);
     }
-    entries(unit + static_cast<int64_t>(AHEAD) * a.units);
-    if (GATHER) weights(unit, wk);
+#pragma unroll
+    for (int n = 0; n < AHEAD; ++n)
+#pragma unroll
+      for (int i = 0; i < V; ++i)
+        fetch(unit + static_cast<int64_t>(n) * a.units, i, ring + n * token + i * vector);
+    if (GATHER) {
+      check_entries(p_read);
+#pragma unroll
+      for (int k = 0; k < KMAX; ++k) p[k] = p_read[k];
+    }
   }
-  if (a.w_post)
-    keep_weights<N>(a.w_post, a.w_f32, a.offset, wpost, quarter, tid, step, a.nvec);
-  if (a.w_pre) keep_weights<N>(a.w_pre, a.w_f32, a.offset, wpre, quarter, tid, step, a.nvec);
+  if (a.w_post) keep_weights<N>(a.w_post, a.w_f32, a.offset, wpost, sb, tid, step, a.nvec);
+  if (a.w_pre) keep_weights<N>(a.w_pre, a.w_f32, a.offset, wpre, sb, tid, step, a.nvec);
   clear_sums<WARP>(red);
   int turn = 0;
-  uint32_t stage = pieces;
+  uint32_t stage = ring;
   for (int64_t t = unit; t < a.T; t += a.units) {
     const int64_t row = t * a.row_bytes;
     if (GATHER) {
       if (AHEAD > 0) {
-        weights(t + a.units, wk_next);
+        read_entries(t + 2 * static_cast<int64_t>(a.units), a.pos, p_read, -1);
+        if (a.cw) read_entries(t + a.units, a.cw, w_read, 0.0f);
       } else {
-        entries(t);
-        weights(t, wk);
+        read_entries(t, a.pos, p, -1);
+        if (a.cw) read_entries(t, a.cw, w_read, 0.0f);
+        check_entries(p);
+        count_weights(w_read);
       }
-    } else if (AHEAD == 0) {
-      entries(t);
     }
     F2 c[V][P];
     Vec16 res[V], gate[V];
     F2 ss = 0;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      const int v = tid + i * step;
-      const bool in = v < a.nvec;
       if (AHEAD > 0) wait_copies<V * AHEAD - 1>();
-      uint32_t from = stage + i * piece_bytes;
-      auto next = [&](const uint8_t* g, bool real) {
+      const uint32_t from = stage + i * vector;
+      auto get = [&](int slot, const uint8_t* g, bool real) {
         Vec16 x{};
-        if (AHEAD > 0) {
-          x = ld_shared(from);
-          from += quarter;
-        } else if (real) {
-          x = ld_vec(g);
-        }
+        if (AHEAD > 0) x = ld_shared(from + slot * sb);
+        else if (real) x = ld_vec(g);
         return x;
       };
-      res[i] = next(a.res + row + v * 16, in);
-      if (a.y) {
-        if (GATHER) {
-          Vec16 in_rows[KMAX];
-          if (AHEAD == 0) {
+      res[i] = get(Slot::Res, a.res + row + at[i], in[i]);
+      if (GATHER) {
+        Vec16 rows[KMAX];
+        if (AHEAD == 0)
 #pragma unroll
-            for (int k = 0; k < KMAX; ++k)
-              in_rows[k] = next(a.y + p[k] * a.row_bytes + v * 16, in && p[k] >= 0);
-          }
+          for (int k = 0; k < KMAX; ++k)
+            rows[k] = get(k, a.y + p[k] * a.row_bytes + at[i], in[i] && p[k] >= 0);
 #pragma unroll
-          for (int j = 0; j < P; ++j) c[i][j] = 0;
+        for (int j = 0; j < P; ++j) c[i][j] = 0;
 #pragma unroll
-          for (int k = 0; k < KMAX; ++k) {
-            if (k >= a.K) break;
-            if (AHEAD > 0) in_rows[k] = next(nullptr, in);
-            F2 f[P];
-            PT::to(in_rows[k], f);
-#pragma unroll
-            for (int j = 0; j < P; ++j) c[i][j] = fma2(both(wk[k]), f[j], c[i][j]);
-          }
-        } else {
-          PT::to(next(a.y + row + v * 16, in), c[i]);
-        }
-        if (a.add) {
+        for (int k = 0; k < KMAX; ++k) {
+          if (k >= a.K) break;
+          if (AHEAD > 0) rows[k] = get(k, nullptr, true);
           F2 f[P];
-          PT::to(next(a.add + row + v * 16, in), f);
+          PT::to(rows[k], f);
 #pragma unroll
-          for (int j = 0; j < P; ++j) c[i][j] = add2(c[i][j], f[j]);
+          for (int j = 0; j < P; ++j) c[i][j] = fma2(both(wk[k]), f[j], c[i][j]);
         }
-        if (a.gate) gate[i] = next(a.gate + gate_row(t) + v * 16, in);
-        if (a.c && in) st_vec(a.c + row + v * 16, PT::from(c[i]));
+      } else if (a.y) {
+        PT::to(get(0, a.y + row + at[i], in[i]), c[i]);
       } else {
         PT::to(res[i], c[i]);
       }
+      if (a.add) {
+        F2 f[P];
+        PT::to(get(Slot::Add, a.add + row + at[i], in[i]), f);
+#pragma unroll
+        for (int j = 0; j < P; ++j) c[i][j] = add2(c[i][j], f[j]);
+      }
+      if (a.gate)
+        gate[i] = get(Slot::Gate, a.gate + t / a.gate_tokens * a.row_bytes + at[i], in[i]);
+      if (a.c && in[i]) st_vec(a.c + row + at[i], PT::from(c[i]));
 #pragma unroll
       for (int j = 0; j < P; ++j) ss = fma2(c[i][j], c[i][j], ss);
-      if (AHEAD > 0) fetch(t + static_cast<int64_t>(AHEAD) * a.units, i, stage + i * piece_bytes);
+      if (AHEAD > 0) fetch(t + static_cast<int64_t>(AHEAD) * a.units, i, stage + i * vector);
     }
     if (AHEAD > 0) {
-      entries(t + static_cast<int64_t>(AHEAD + 1) * a.units);
-      stage += V * piece_bytes;
-      if (stage == pieces + AHEAD * V * piece_bytes) stage = pieces;
+      stage += token;
+      if (stage == ring + AHEAD * token) stage = ring;
     }
     if (a.y) {
       float r = 1.0f;
@@ -403,7 +422,7 @@ __global__ void __launch_bounds__(MAXT, 1) block_norm_kernel(NormArgs a) {
       for (int i = 0; i < V; ++i) {
         F2 f[P];
         if (a.w_post) {
-          kept_weights<N>(wpost, quarter, i, f);
+          kept_weights<N>(wpost, sb, i, f);
 #pragma unroll
           for (int j = 0; j < P; ++j) c[i][j] = mul2(mul2(c[i][j], both(r)), f[j]);
         }
@@ -418,8 +437,7 @@ __global__ void __launch_bounds__(MAXT, 1) block_norm_kernel(NormArgs a) {
           c[i][j] = fma2(both(a.res_scale), f[j], c[i][j]);
           ss = fma2(c[i][j], c[i][j], ss);
         }
-        const int v = tid + i * step;
-        if (v < a.nvec) st_vec(a.res_out + row + v * 16, PT::from(c[i]));
+        if (in[i]) st_vec(a.res_out + row + at[i], PT::from(c[i]));
       }
     }
     if (a.x) {
@@ -428,15 +446,18 @@ __global__ void __launch_bounds__(MAXT, 1) block_norm_kernel(NormArgs a) {
 #pragma unroll
       for (int i = 0; i < V; ++i) {
         F2 f[P];
-        kept_weights<N>(wpre, quarter, i, f);
+        kept_weights<N>(wpre, sb, i, f);
 #pragma unroll
         for (int j = 0; j < P; ++j) f[j] = mul2(mul2(c[i][j], both(r)), f[j]);
-        const int v = tid + i * step;
-        if (v < a.nvec) st_vec(a.x + row + v * 16, PT::from(f));
+        if (in[i]) st_vec(a.x + row + at[i], PT::from(f));
       }
     }
+    if (GATHER && AHEAD > 0) {
+      count_weights(w_read);
+      check_entries(p_read);
 #pragma unroll
-    for (int k = 0; k < KMAX; ++k) wk[k] = wk_next[k];
+      for (int k = 0; k < KMAX; ++k) p[k] = p_read[k];
+    }
   }
 }
 
@@ -494,48 +515,79 @@ __device__ __forceinline__ void flush_sums(F2 (&acc)[V][P], float* to, bool firs
 // D = gres' + r_p (v - h mean(v h)), v = gx w_pre, h = res' r_p: the gradient of
 // the residual sum; then the same form behind the gate for c.  AHEAD as in the
 // forward.
+template <typename Elt, bool GATE, int AHEAD>
+constexpr int backward_slots() {
+  constexpr int V = kEpt / (2 * PairTraits<Elt>::P);
+  return 2 * kWeightSlots + AHEAD * V * (GATE ? 5 : 4);
+}
+
 template <typename Elt, bool GATE, bool WARP, int MAXT, int AHEAD>
 __global__ void __launch_bounds__(MAXT, 1) block_norm_bwd_kernel(NormBwdArgs a) {
   using PT = PairTraits<Elt>;
   constexpr int P = PT::P, N = 2 * P, V = kEpt / N, ROWS = GATE ? 5 : 4;
+  const uint32_t sb = blockDim.x * 16, token = ROWS * V * sb;  // bytes
+  enum { GRes, Gx, ResOut, C, Gate };
   __shared__ __align__(16) float red[64];
   extern __shared__ __align__(16) uint8_t own[];
   const int tid = WARP ? threadIdx.x & 31 : threadIdx.x;
   const int step = WARP ? 32 : blockDim.x;
   const int unit = WARP ? blockIdx.x * kTeams + (threadIdx.x >> 5) : blockIdx.x;
   if (unit >= a.units) return;  // a warp's; a block is always a unit
-  const uint32_t quarter = blockDim.x * 16;
   const uint32_t wpost = smem_addr(own) + threadIdx.x * 16;
-  const uint32_t wpre = wpost + kEpt / 4 * quarter;
-  const uint32_t mine = wpre + kEpt / 4 * quarter;
-  constexpr int kToken = ROWS * V;  // vectors a thread holds of a token
+  const uint32_t wpre = wpost + kWeightSlots * sb;
+  const uint32_t ring = wpre + kWeightSlots * sb;
+  bool in[V];    // vectors inside the row, and where
+  int at[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    in[i] = tid + i * step < a.nvec;
+    at[i] = in[i] ? (tid + i * step) * 16 : 0;
+  }
   const int64_t begin64 = static_cast<int64_t>(unit) * a.chunk;
   const int begin = static_cast<int>(begin64 < a.T ? begin64 : a.T);
   const int end = static_cast<int>(begin64 + a.chunk < a.T ? begin64 + a.chunk : a.T);
-  const uint8_t* rows[5] = {a.gres_out, a.gx, a.gx ? a.res_out : nullptr, a.c, a.gate};
-  auto row_of = [&](int k, int64_t t) { return (k == 4 ? t / a.gate_tokens : t) * a.row_bytes; };
-  auto fetch = [&](int64_t t, uint32_t stage) {
-    if (t < end) {
+  // the gate's row of a token, for tokens in order: its offset and last token + 1
+  struct Group {
+    int64_t row, end;
+  };
+  auto group_of = [&](int t) {
+    const int64_t g = t / a.gate_tokens;
+    return Group{g * a.row_bytes, (g + 1) * a.gate_tokens};
+  };
+  Group asked = GATE ? group_of(begin) : Group{0, 0}, group = asked;
+  int64_t off = begin * a.row_bytes;  // of the row asked for next
+  int next = begin;
+  auto fetch = [&](uint32_t to) {
+    if (next < end) {
 #pragma unroll
-      for (int k = 0; k < ROWS; ++k) {
-        if (!rows[k]) continue;
-        const uint8_t* p = rows[k] + row_of(k, t);
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-          const int v = tid + i * step;
-          const bool in = v < a.nvec;
-          copy_async(stage + (k * V + i) * quarter, p + (in ? v * 16 : 0), in);
+      for (int i = 0; i < V; ++i) {
+        auto copy = [&](int k, const uint8_t* p, int64_t o) {
+          copy_async(to + (k * V + i) * sb, p + o + at[i], in[i]);
+        };
+        if (a.gx) {
+          copy(Gx, a.gx, off);
+          copy(ResOut, a.res_out, off);
         }
+        if (a.gres_out) copy(GRes, a.gres_out, off);
+        if (a.c) copy(C, a.c, off);
+        if (GATE) copy(Gate, a.gate, asked.row);
+      }
+      off += a.row_bytes;
+      ++next;
+      if (GATE && next == asked.end) {
+        asked.row += a.row_bytes;
+        asked.end += a.gate_tokens;
       }
     }
     commit_copies();
   };
   if (AHEAD > 0)
-    for (int n = 0; n < AHEAD; ++n)
-      fetch(static_cast<int64_t>(begin) + n, mine + n * kToken * quarter);
-  if (a.w_post)
-    keep_weights<N>(a.w_post, a.w_f32, a.offset, wpost, quarter, tid, step, a.nvec);
-  if (a.gx) keep_weights<N>(a.w_pre, a.w_f32, a.offset, wpre, quarter, tid, step, a.nvec);
+#pragma unroll
+    for (int n = 0; n < AHEAD; ++n) fetch(ring + n * token);
+  float r_pre = a.gx && begin < end ? __ldg(a.rstd_pre + begin) : 0.0f;
+  float r_post = a.w_post && begin < end ? __ldg(a.rstd_post + begin) : 1.0f;
+  if (a.w_post) keep_weights<N>(a.w_post, a.w_f32, a.offset, wpost, sb, tid, step, a.nvec);
+  if (a.gx) keep_weights<N>(a.w_pre, a.w_f32, a.offset, wpre, sb, tid, step, a.nvec);
   clear_sums<WARP>(red);
   F2 gpost[V][P], gpre[V][P], ggate[V][P];
 #pragma unroll
@@ -546,18 +598,20 @@ __global__ void __launch_bounds__(MAXT, 1) block_norm_bwd_kernel(NormBwdArgs a) 
   float* pre_row = a.part + static_cast<size_t>(a.units + unit) * a.H;
   bool first = true, gate_first = true;
   int held = 0, gate_held = 0, turn = 0;
-  uint32_t stage = mine;
-  for (int t = begin; t < end; ++t) {
-    const int64_t row = static_cast<int64_t>(t) * a.row_bytes;
-    auto load = [&](int k, int i, F2* f) {
+  uint32_t stage = ring;
+  int64_t row = begin * a.row_bytes;
+  for (int t = begin; t < end; ++t, row += a.row_bytes) {
+    auto load = [&](int k, int i, const uint8_t* p, int64_t o, F2* f) {
       Vec16 x{};
-      const int v = tid + i * step;
-      if (AHEAD > 0) x = ld_shared(stage + (k * V + i) * quarter);
-      else if (v < a.nvec) x = ld_vec(rows[k] + row_of(k, t) + v * 16);
+      if (AHEAD > 0) x = ld_shared(stage + (k * V + i) * sb);
+      else if (in[i]) x = ld_vec(p + o + at[i]);
       PT::to(x, f);
     };
-    const float r_pre = a.gx ? __ldg(a.rstd_pre + t) : 0.0f;
-    const float r = a.w_post ? __ldg(a.rstd_post + t) : 1.0f;
+    const float rp = r_pre, r = r_post;
+    if (t + 1 < end) {  // the next token's, a row's time ahead
+      if (a.gx) r_pre = __ldg(a.rstd_pre + t + 1);
+      if (a.w_post) r_post = __ldg(a.rstd_post + t + 1);
+    }
     if (AHEAD > 0) wait_copies<AHEAD - 1>();
     F2 D[V][P], h[V][P];
     if (a.gx) {
@@ -565,12 +619,12 @@ __global__ void __launch_bounds__(MAXT, 1) block_norm_bwd_kernel(NormBwdArgs a) 
 #pragma unroll
       for (int i = 0; i < V; ++i) {
         F2 w[P];
-        load(1, i, D[i]);
-        load(2, i, h[i]);
-        kept_weights<N>(wpre, quarter, i, w);
+        load(Gx, i, a.gx, row, D[i]);
+        load(ResOut, i, a.res_out, row, h[i]);
+        kept_weights<N>(wpre, sb, i, w);
 #pragma unroll
         for (int j = 0; j < P; ++j) {
-          h[i][j] = mul2(h[i][j], both(r_pre));
+          h[i][j] = mul2(h[i][j], both(rp));
           gpre[i][j] = fma2(D[i][j], h[i][j], gpre[i][j]);
           D[i][j] = mul2(D[i][j], w[j]);
           s = fma2(D[i][j], h[i][j], s);
@@ -582,23 +636,22 @@ __global__ void __launch_bounds__(MAXT, 1) block_norm_bwd_kernel(NormBwdArgs a) 
         F2 g[P];
 #pragma unroll
         for (int j = 0; j < P; ++j) g[j] = 0;
-        if (a.gres_out) load(0, i, g);
+        if (a.gres_out) load(GRes, i, a.gres_out, row, g);
 #pragma unroll
         for (int j = 0; j < P; ++j)
-          D[i][j] = fma2(both(r_pre), fma2(both(-m), h[i][j], D[i][j]), g[j]);
+          D[i][j] = fma2(both(rp), fma2(both(-m), h[i][j], D[i][j]), g[j]);
       }
     } else {
 #pragma unroll
-      for (int i = 0; i < V; ++i) load(0, i, D[i]);
+      for (int i = 0; i < V; ++i) load(GRes, i, a.gres_out, row, D[i]);
     }
     if (a.gres) {
 #pragma unroll
       for (int i = 0; i < V; ++i) {
-        const int v = tid + i * step;
         F2 o[P];
 #pragma unroll
         for (int j = 0; j < P; ++j) o[j] = mul2(both(a.res_scale), D[i][j]);
-        if (v < a.nvec) st_vec(a.gres + row + v * 16, PT::from(o));
+        if (in[i]) st_vec(a.gres + row + at[i], PT::from(o));
       }
     }
     if (a.c) {
@@ -606,13 +659,13 @@ __global__ void __launch_bounds__(MAXT, 1) block_norm_bwd_kernel(NormBwdArgs a) 
 #pragma unroll
       for (int i = 0; i < V; ++i) {
         F2 w[P];
-        load(3, i, h[i]);
+        load(C, i, a.c, row, h[i]);
 #pragma unroll
         for (int j = 0; j < P; ++j) h[i][j] = mul2(h[i][j], both(r));
-        if (a.w_post) kept_weights<N>(wpost, quarter, i, w);
+        if (a.w_post) kept_weights<N>(wpost, sb, i, w);
         if (GATE) {
           F2 g[P];
-          load(4, i, g);
+          load(Gate, i, a.gate, group.row, g);
 #pragma unroll
           for (int j = 0; j < P; ++j) {
             ggate[i][j] = fma2(D[i][j], a.w_post ? mul2(h[i][j], w[j]) : h[i][j], ggate[i][j]);
@@ -640,41 +693,45 @@ __global__ void __launch_bounds__(MAXT, 1) block_norm_bwd_kernel(NormBwdArgs a) 
     if (a.gy) {
 #pragma unroll
       for (int i = 0; i < V; ++i)
-        if (tid + i * step < a.nvec) st_vec(a.gy + row + (tid + i * step) * 16, PT::from(D[i]));
+        if (in[i]) st_vec(a.gy + row + at[i], PT::from(D[i]));
     }
     if (AHEAD > 0) {
-      fetch(static_cast<int64_t>(t) + AHEAD, stage);
-      stage += kToken * quarter;
-      if (stage == mine + AHEAD * kToken * quarter) stage = mine;
+      fetch(stage);
+      stage += token;
+      if (stage == ring + AHEAD * token) stage = ring;
     }
-    if (GATE && a.ggate) {
-      const int group = t / a.gate_tokens;
-      const int64_t g0 = static_cast<int64_t>(group) * a.gate_tokens;
-      const int64_t g1 = min(g0 + a.gate_tokens, static_cast<int64_t>(a.T));
-      const bool ends = t + 1 == g1;
-      float* slot = a.slots + static_cast<size_t>(2 * unit + (g0 >= begin)) * a.H;
-      if (ends && g0 >= begin) {  // all of the group's tokens
+    if (GATE) {
+      const int64_t g0 = group.end - a.gate_tokens;
+      const bool ends = t + 1 == group.end || t + 1 == a.T;
+      if (a.ggate) {
+        float* slot = a.slots + static_cast<size_t>(2 * unit + (g0 >= begin)) * a.H;
+        if (ends && g0 >= begin) {  // all of the group's tokens
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-          const int v = tid + i * step;
-          if (v < a.nvec) {
+          for (int i = 0; i < V; ++i) {
+            if (in[i]) {
 #pragma unroll
-            for (int j = 0; j < P; ++j)
-              if (!gate_first) {
-                const float2 x = *reinterpret_cast<const float2*>(slot + (v * P + j) * 2);
-                ggate[i][j] = add2(ggate[i][j], pair(x.x, x.y));
-              }
-            st_vec(a.ggate + group * a.row_bytes + v * 16, PT::from(ggate[i]));
+              for (int j = 0; j < P; ++j)
+                if (!gate_first) {
+                  const float2 x =
+                      *reinterpret_cast<const float2*>(slot + ((tid + i * step) * P + j) * 2);
+                  ggate[i][j] = add2(ggate[i][j], pair(x.x, x.y));
+                }
+              st_vec(a.ggate + group.row + at[i], PT::from(ggate[i]));
+            }
+#pragma unroll
+            for (int j = 0; j < P; ++j) ggate[i][j] = 0;
           }
-#pragma unroll
-          for (int j = 0; j < P; ++j) ggate[i][j] = 0;
+          gate_first = true;
+          gate_held = 0;
+        } else if (ends || t + 1 == end || ++gate_held == kFlush) {
+          flush_sums(ggate, slot, gate_first, tid, step, a.nvec);
+          gate_first = ends;
+          gate_held = 0;
         }
-        gate_first = true;
-        gate_held = 0;
-      } else if (ends || t + 1 == end || ++gate_held == kFlush) {
-        flush_sums(ggate, slot, gate_first, tid, step, a.nvec);
-        gate_first = ends;
-        gate_held = 0;
+      }
+      if (ends) {
+        group.row += a.row_bytes;
+        group.end += a.gate_tokens;
       }
     }
     if (++held == kFlush) {
@@ -756,8 +813,6 @@ void bwd_units(int T, int H, int num_sms, int* chunk, int* units) {
   *units = n;
 }
 
-size_t weight_bytes(int threads) { return static_cast<size_t>(threads) * kEpt * sizeof(float); }
-
 // Largest dynamic shared memory for a kernel that takes more than the default.
 template <typename K>
 cudaError_t allow_shared(K k) {
@@ -766,55 +821,112 @@ cudaError_t allow_shared(K k) {
                               static_cast<int>(kShared));
 }
 
+// A kernel, the tokens that it has under way, and its shared memory.
+template <typename A>
+struct Chosen {
+  void (*kernel)(A);
+  int ahead;
+  size_t shared;
+};
+
+template <typename Elt, int KMAX, bool WARP, int MAXT, int AHEAD>
+Chosen<NormArgs> forward(int threads) {
+  return {block_norm_kernel<Elt, KMAX, WARP, MAXT, AHEAD>, AHEAD,
+          static_cast<size_t>(threads) * forward_slots<Elt, KMAX, AHEAD>() * 16};
+}
+
+// The kernel with the most tokens under way whose shared memory fits into `most`.
+template <typename Elt, int KMAX, bool WARP, int MAXT>
+Chosen<NormArgs> forward_within(int threads, size_t most) {
+  if constexpr (KMAX == 1 && MAXT < 1024) {
+    const auto two = forward<Elt, KMAX, WARP, MAXT, 2>(threads);
+    if (two.shared <= most) return two;
+  }
+  const auto one = forward<Elt, KMAX, WARP, MAXT, 1>(threads);
+  return one.shared <= most ? one : forward<Elt, KMAX, WARP, MAXT, 0>(threads);
+}
 template <typename Elt, int KMAX>
-auto forward_kernel(bool warp, int threads, int ahead) {
-  if (warp)
-    return ahead == 2   ? block_norm_kernel<Elt, KMAX, true, 32 * kTeams, 2>
-           : ahead == 1 ? block_norm_kernel<Elt, KMAX, true, 32 * kTeams, 1>
-                        : block_norm_kernel<Elt, KMAX, true, 32 * kTeams, 0>;
-  if (threads <= 512)
-    return ahead == 2   ? block_norm_kernel<Elt, KMAX, false, 512, 2>
-           : ahead == 1 ? block_norm_kernel<Elt, KMAX, false, 512, 1>
-                        : block_norm_kernel<Elt, KMAX, false, 512, 0>;
-  return ahead >= 1 ? block_norm_kernel<Elt, KMAX, false, 1024, 1>
-                    : block_norm_kernel<Elt, KMAX, false, 1024, 0>;
+Chosen<NormArgs> forward_kernel(int H, int threads, size_t most) {
+  return one_warp(H)      ? forward_within<Elt, KMAX, true, 32 * kTeams>(threads, most)
+         : threads <= 512 ? forward_within<Elt, KMAX, false, 512>(threads, most)
+                          : forward_within<Elt, KMAX, false, 1024>(threads, most);
+}
+template <typename Elt>
+Chosen<NormArgs> forward_kernel(int kmax, int H, int threads, size_t most) {
+  return kmax == 1   ? forward_kernel<Elt, 1>(H, threads, most)
+         : kmax == 8 ? forward_kernel<Elt, 8>(H, threads, most)
+                     : forward_kernel<Elt, 16>(H, threads, most);
 }
 
+template <typename Elt, bool GATE, bool WARP, int MAXT, int AHEAD>
+Chosen<NormBwdArgs> backward(int threads) {
+  return {block_norm_bwd_kernel<Elt, GATE, WARP, MAXT, AHEAD>, AHEAD,
+          static_cast<size_t>(threads) * backward_slots<Elt, GATE, AHEAD>() * 16};
+}
+template <typename Elt, bool GATE, bool WARP, int MAXT>
+Chosen<NormBwdArgs> backward_within(int threads, size_t most) {
+  if constexpr (MAXT < 1024) {
+    const auto three = backward<Elt, GATE, WARP, MAXT, 3>(threads);
+    if (three.shared <= most) return three;
+    const auto two = backward<Elt, GATE, WARP, MAXT, 2>(threads);
+    if (two.shared <= most) return two;
+  }
+  return backward<Elt, GATE, WARP, MAXT, 0>(threads);
+}
 template <typename Elt, bool GATE>
-auto backward_kernel(bool warp, int threads, int ahead) {
-  if (warp)
-    return ahead == 3   ? block_norm_bwd_kernel<Elt, GATE, true, 32 * kTeams, 3>
-           : ahead == 2 ? block_norm_bwd_kernel<Elt, GATE, true, 32 * kTeams, 2>
-                        : block_norm_bwd_kernel<Elt, GATE, true, 32 * kTeams, 0>;
-  if (threads <= 512)
-    return ahead == 3   ? block_norm_bwd_kernel<Elt, GATE, false, 512, 3>
-           : ahead == 2 ? block_norm_bwd_kernel<Elt, GATE, false, 512, 2>
-                        : block_norm_bwd_kernel<Elt, GATE, false, 512, 0>;
-  return block_norm_bwd_kernel<Elt, GATE, false, 1024, 0>;
+Chosen<NormBwdArgs> backward_kernel(int H, int threads, size_t most) {
+  return one_warp(H)      ? backward_within<Elt, GATE, true, 32 * kTeams>(threads, most)
+         : threads <= 512 ? backward_within<Elt, GATE, false, 512>(threads, most)
+                          : backward_within<Elt, GATE, false, 1024>(threads, most);
 }
 
+// Shared memory for every kernel that the choices above can make.
+template <typename Elt, bool WARP, int MAXT>
+cudaError_t allow_team() {
+  cudaError_t e = cudaSuccess;
+  auto allow = [&](const auto& c) {
+    if (e == cudaSuccess) e = allow_shared(c.kernel);
+  };
+  allow(forward<Elt, 1, WARP, MAXT, 0>(MAXT));
+  allow(forward<Elt, 1, WARP, MAXT, 1>(MAXT));
+  allow(forward<Elt, 8, WARP, MAXT, 0>(MAXT));
+  allow(forward<Elt, 8, WARP, MAXT, 1>(MAXT));
+  allow(forward<Elt, 16, WARP, MAXT, 0>(MAXT));
+  allow(forward<Elt, 16, WARP, MAXT, 1>(MAXT));
+  allow(backward<Elt, false, WARP, MAXT, 0>(MAXT));
+  allow(backward<Elt, true, WARP, MAXT, 0>(MAXT));
+  if constexpr (MAXT < 1024) {
+    allow(forward<Elt, 1, WARP, MAXT, 2>(MAXT));
+    allow(backward<Elt, false, WARP, MAXT, 2>(MAXT));
+    allow(backward<Elt, false, WARP, MAXT, 3>(MAXT));
+    allow(backward<Elt, true, WARP, MAXT, 2>(MAXT));
+    allow(backward<Elt, true, WARP, MAXT, 3>(MAXT));
+  }
+  return e;
+}
 template <typename Elt>
 cudaError_t allow_all() {
-  cudaError_t e = cudaSuccess;
-  for (int ahead = 0; ahead <= 3; ++ahead)
-    for (int threads : {128, 512, 1024})
-      for (bool warp : {false, true}) {
-        for (auto k : {forward_kernel<Elt, 1>(warp, threads, ahead),
-                       forward_kernel<Elt, 8>(warp, threads, ahead),
-                       forward_kernel<Elt, 16>(warp, threads, ahead)})
-          if (e == cudaSuccess) e = allow_shared(k);
-        for (auto k : {backward_kernel<Elt, false>(warp, threads, ahead),
-                       backward_kernel<Elt, true>(warp, threads, ahead)})
-          if (e == cudaSuccess) e = allow_shared(k);
-      }
-  return e;
+  cudaError_t e = allow_team<Elt, true, 32 * kTeams>();
+  if (e == cudaSuccess) e = allow_team<Elt, false, 512>();
+  return e == cudaSuccess ? allow_team<Elt, false, 1024>() : e;
 }
 
 }  // namespace
 
+// Once for a device: the first call of a process loads the kernels.
 cudaError_t prepare_block_norm_kernels() {
-  const cudaError_t e = allow_all<__nv_bfloat16>();
-  return e == cudaSuccess ? allow_all<float>() : e;
+  static std::mutex mu;
+  static uint64_t done[4];  // a bit a device
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  std::lock_guard<std::mutex> lock(mu);
+  uint64_t* word = dev < 256 ? done + dev / 64 : nullptr;
+  if (word && (*word >> (dev % 64) & 1)) return cudaSuccess;
+  e = allow_all<__nv_bfloat16>();
+  if (e == cudaSuccess) e = allow_all<float>();
+  if (e == cudaSuccess && word) *word |= uint64_t{1} << (dev % 64);
+  return e;
 }
 
 size_t block_norm_workspace(const moe_handle* h, int T, int H, int gate_tokens) {
@@ -856,26 +968,14 @@ cudaError_t launch_block_norm(const moe_handle* h, const moe_block_norm_args& q,
   if (T == 0) return cudaSuccess;
   const bool warp = one_warp(q.H);
   const int threads = warp ? 32 * kTeams : team_threads(q.H);
-  if (!q.gather) a.K = 1;
-  a.piece_rows = 1 + (a.y ? a.K : 0) + (a.add != nullptr) + (a.gate != nullptr);
-  const size_t kept = weight_bytes(threads) * ((a.w_post != nullptr) + (a.w_pre != nullptr));
-  const size_t token = static_cast<size_t>(threads) * kEpt * (bf16 ? 2 : 4) * a.piece_rows;
-  int ahead = 2;
-  while (ahead > 0 && kept + ahead * token > kShared) --ahead;
-  if (threads > 512 && ahead > 1) ahead = 1;
-  const size_t smem = kept + ahead * token;
-  auto with = [&](auto elt) {
-    using Elt = decltype(elt);
-    return !q.gather ? forward_kernel<Elt, 1>(warp, threads, ahead)
-           : a.K <= 8 ? forward_kernel<Elt, 8>(warp, threads, ahead)
-                      : forward_kernel<Elt, 16>(warp, threads, ahead);
-  };
-  auto k = bf16 ? with(__nv_bfloat16{}) : with(float{});
+  const int kmax = !q.gather ? 1 : a.K <= 8 ? 8 : 16;
+  const auto c = bf16 ? forward_kernel<__nv_bfloat16>(kmax, q.H, threads, kShared)
+                      : forward_kernel<float>(kmax, q.H, threads, kShared);
   const long long teams = warp ? kTeams : 1;
-  const long long most =
-      teams * h->num_sms * resident_blocks(reinterpret_cast<const void*>(k), threads, smem);
+  const long long most = teams * h->num_sms *
+                         resident_blocks(reinterpret_cast<const void*>(c.kernel), threads, c.shared);
   a.units = static_cast<int>(T < most ? T : most);
-  k<<<static_cast<unsigned>((a.units + teams - 1) / teams), threads, smem, s>>>(a);
+  c.kernel<<<static_cast<unsigned>((a.units + teams - 1) / teams), threads, c.shared, s>>>(a);
   return cudaGetLastError();
 }
 
@@ -914,21 +1014,15 @@ cudaError_t launch_block_norm_bwd(const moe_handle* h, const moe_block_norm_bwd_
   a.blocks = warp ? (a.units + kTeams - 1) / kTeams : a.units;
   const int threads = warp ? 32 * kTeams : team_threads(q.H);
   const bool gated = q.d_gate != nullptr;
-  const size_t kept = 2 * weight_bytes(threads);
-  const size_t token = static_cast<size_t>(threads) * kEpt * (bf16 ? 2 : 4) * (gated ? 5 : 4);
   const int blocks_per_sm = warp ? 16 / kTeams : bwd_units_per_sm(q.H);
   const size_t most = kSmShared / blocks_per_sm - kBlockShared;
-  int ahead = threads > 512 ? 0 : 3;
-  while (ahead > 0 && kept + ahead * token > most) --ahead;
-  if (ahead == 1) ahead = 0;
-  const size_t smem = kept + ahead * token;
   using B = __nv_bfloat16;
-  auto k = bf16 ? (gated ? backward_kernel<B, true>(warp, threads, ahead)
-                         : backward_kernel<B, false>(warp, threads, ahead))
-                : (gated ? backward_kernel<float, true>(warp, threads, ahead)
-                         : backward_kernel<float, false>(warp, threads, ahead));
+  const auto k = bf16 ? (gated ? backward_kernel<B, true>(q.H, threads, most)
+                               : backward_kernel<B, false>(q.H, threads, most))
+                      : (gated ? backward_kernel<float, true>(q.H, threads, most)
+                               : backward_kernel<float, false>(q.H, threads, most));
   if (T > 0) {
-    k<<<a.blocks, threads, smem, s>>>(a);
+    k.kernel<<<a.blocks, threads, k.shared, s>>>(a);
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
   }
