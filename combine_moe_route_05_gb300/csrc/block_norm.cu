@@ -29,12 +29,12 @@ namespace {
 constexpr unsigned kFull = 0xffffffffu;
 constexpr int kEpt = 16;           // elements of a row a thread holds
 constexpr int kWarpRow = 32 * kEpt;  // widest row of a one-warp team
-constexpr int kTeams = 4;          // one-warp teams of a block
+constexpr int kTeamThreads = 512;  // threads of a block of several teams, at most
 // Tokens whose column sums are added up in registers before they go to memory:
 // bounds the number of fp32 additions in a row for any T.
 constexpr int kFlush = 1024;
-constexpr size_t kShared = 226 * 1024;  // dynamic shared memory of a block, at most
-constexpr size_t kSmShared = 228 * 1024, kBlockShared = 1024 + 512;  // of an SM; a block's own share
+constexpr int kJoinWarps = 16, kJoinCols = 64;  // of the kernel that joins the column sums
+constexpr size_t kShared = 224 * 1024;  // dynamic shared memory of a block, at most
 
 // ---------------------------------------------------------------------------
 // pairs of fp32
@@ -114,6 +114,11 @@ struct PairTraits<float> {
 __device__ __forceinline__ void commit_copies() {
   asm volatile("cp.async.commit_group;" ::: "memory");
 }
+// Lets the kernel behind this one (launched chained) get ready: its blocks wait for
+// the end of this grid themselves.
+__device__ __forceinline__ void release_join() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
 // Waits until at most N of the thread's groups of copies are under way.
 template <int N>
 __device__ __forceinline__ void wait_copies() {
@@ -139,17 +144,19 @@ __device__ __forceinline__ void st_shared(uint32_t a, float4 v) {
                : "memory");
 }
 
-// A thread's shared memory is its own slots of 16 bytes, `sb` = 16 times the
-// block's threads from one to the next: the copies of a warp land side by side.
-// (Slots of a thread one behind another, with addresses known when compiled, took
-// the backward from 302 to 372 us at the DeepSeek-V3 shape.)
+// Shared memory of a block: the weights, 16 bytes a thread of a team in each of
+// kWeightSlots rows (teams share them), then the vectors under way in slots of 16
+// bytes, `sb` = 16 times the block's threads from one to the next, so that a
+// warp's copies land side by side.  (Slots of a thread one behind another, with
+// addresses known when compiled, took the backward from 302 to 372 us at the
+// DeepSeek-V3 shape.)
 constexpr int kWeightSlots = kEpt / 4;  // 16 fp32
 
-// Keeps the thread's 16 weights of w from `to` on, zero behind the row's end;
-// its vectors of N elements are tid, tid + threads, ...
+// Keeps the 16 weights of a team's thread from `to` on (rows wb bytes apart), zero
+// behind the row's end; its vectors of N elements are tid, tid + threads, ...
 template <int N>
 __device__ __forceinline__ void keep_weights(const uint8_t* w, int f32, float offset, uint32_t to,
-                                             uint32_t sb, int tid, int threads, int nvec) {
+                                             uint32_t wb, int tid, int threads, int nvec) {
 #pragma unroll
   for (int q = 0; q < kWeightSlots; ++q) {
     const int v = tid + q / (N / 4) * threads;
@@ -165,50 +172,60 @@ __device__ __forceinline__ void keep_weights(const uint8_t* w, int f32, float of
       }
       f = make_float4(f.x + offset, f.y + offset, f.z + offset, f.w + offset);
     }
-    st_shared(to + q * sb, f);
+    st_shared(to + q * wb, f);
   }
 }
 // The weights of the thread's vector i.
 template <int N>
-__device__ __forceinline__ void kept_weights(uint32_t at, uint32_t sb, int i, F2* f) {
+__device__ __forceinline__ void kept_weights(uint32_t at, uint32_t wb, int i, F2* f) {
 #pragma unroll
   for (int q = 0; q < N / 4; ++q) {
-    const Vec16 v = ld_shared(at + (i * (N / 4) + q) * sb);
+    const Vec16 v = ld_shared(at + (i * (N / 4) + q) * wb);
     f[2 * q] = pair(__uint_as_float(v.u[0]), __uint_as_float(v.u[1]));
     f[2 * q + 1] = pair(__uint_as_float(v.u[2]), __uint_as_float(v.u[3]));
   }
 }
 
-// Sum over the team: a warp, or the block, whose warps hand over through `red`
-// (two sets of 32 values, taken in turn, so that one barrier a sum is enough;
-// zero behind the last warp's, so that they can be read four at a time).
-template <bool WARP>
-__device__ __forceinline__ float team_sum(float v, float* red, int& turn) {
+// Which team a thread is in, and where in it: blocks hold whole teams.
+template <bool WARP, int MAXT>
+struct Team {
+  int threads, index, tid;
+  float* red;  // two sets of 32 values, taken in turn (teams of several warps)
+  int turn = 0;
+  __device__ __forceinline__ Team(int team_threads, float* sums)
+      : threads(WARP ? 32 : team_threads),
+        index(WARP ? threadIdx.x >> 5 : threadIdx.x / team_threads),
+        tid(WARP ? threadIdx.x & 31 : threadIdx.x - index * team_threads),
+        red(sums + 64 * index) {
+    if (!WARP)
+      for (int i = tid; i < 64; i += threads) red[i] = 0.0f;
+  }
+  __device__ __forceinline__ void sync() {
+    asm volatile("bar.sync %0, %1;" ::"r"(index + 1), "r"(threads) : "memory");
+  }
+  // Sum over the team.  A barrier a sum is enough, and the values behind the last
+  // warp's stay zero, so that they are read four at a time.
+  __device__ __forceinline__ float sum(float v) {
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
-  if constexpr (WARP) return v;
-  const int warps = blockDim.x >> 5;
-  float* set = red + turn;
-  turn ^= 32;
-  if ((threadIdx.x & 31) == 0) set[threadIdx.x >> 5] = v;
-  __syncthreads();
-  float4 a = *reinterpret_cast<const float4*>(set);
-  for (int w = 4; w < warps; w += 4) {
-    const float4 b = *reinterpret_cast<const float4*>(set + w);
-    a.x += b.x;
-    a.y += b.y;
-    a.z += b.z;
-    a.w += b.w;
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
+    if constexpr (WARP) return v;
+    float* set = red + turn;
+    turn ^= 32;
+    if ((tid & 31) == 0) set[tid >> 5] = v;
+    sync();
+    float4 a = *reinterpret_cast<const float4*>(set);
+#pragma unroll
+    for (int w = 4; w < MAXT / 32; w += 4) {
+      const float4 b = *reinterpret_cast<const float4*>(set + w);
+      a.x += b.x;
+      a.y += b.y;
+      a.z += b.z;
+      a.w += b.w;
+    }
+    return (a.x + a.y) + (a.z + a.w);
   }
-  return (a.x + a.y) + (a.z + a.w);
-}
-template <bool WARP>
-__device__ __forceinline__ void clear_sums(float* red) {
-  if constexpr (!WARP) {
-    for (int i = threadIdx.x; i < 64; i += blockDim.x) red[i] = 0.0f;
-    __syncthreads();
-  }
-}
+};
+constexpr int kRed = 64 * 8;  // eight teams of two warps at most
 
 // ---------------------------------------------------------------------------
 // forward
@@ -230,6 +247,7 @@ struct NormArgs {
   int64_t row_bytes;
   int T, H, nvec, K, rows, gate_tokens;
   int units;             // teams; a team takes every units-th token
+  int teams, team_threads;  // of a block; of a team
   int w_f32;             // weights in fp32 (else bf16)
   float res_scale, eps, offset, inv_h;
   uint32_t* flags;
@@ -239,35 +257,26 @@ struct NormArgs {
 // AHEAD: tokens whose vectors are in shared memory or on their way there (0: they
 // are loaded when they are needed).  KMAX: rows that are summed at most (1: token
 // rows).
-template <int KMAX>
-struct NormSlots {  // of one vector's rows
-  static constexpr int Res = KMAX, Add = KMAX + 1, Gate = KMAX + 2, Count = KMAX + 3;
-};
-
-template <typename Elt, int KMAX, int AHEAD>
-constexpr int forward_slots() {
-  constexpr int V = kEpt / (2 * PairTraits<Elt>::P);
-  return 2 * kWeightSlots + AHEAD * V * NormSlots<KMAX>::Count;
-}
-
 template <typename Elt, int KMAX, bool WARP, int MAXT, int AHEAD>
-__global__ void __launch_bounds__(MAXT, 1) block_norm_kernel(NormArgs a) {
+__global__ void __launch_bounds__(MAXT, KMAX == 1 && MAXT <= 512 && sizeof(Elt) == 2 ? 2 : 1)
+    block_norm_kernel(NormArgs a) {
   using PT = PairTraits<Elt>;
-  using Slot = NormSlots<KMAX>;
   constexpr int P = PT::P, N = 2 * P, V = kEpt / N;
   constexpr bool GATHER = KMAX > 1;
-  const uint32_t sb = blockDim.x * 16;
-  const uint32_t vector = Slot::Count * sb, token = V * vector;  // bytes
   static_assert(!GATHER || AHEAD < 2, "a token's weights are asked for one token ahead");
-  __shared__ __align__(16) float red[64];
-  extern __shared__ __align__(16) uint8_t own[];
-  const int tid = WARP ? threadIdx.x & 31 : threadIdx.x;
-  const int step = WARP ? 32 : blockDim.x;
-  const int unit = WARP ? blockIdx.x * kTeams + (threadIdx.x >> 5) : blockIdx.x;
-  if (unit >= a.units) return;  // a warp's; a block is always a unit
-  const uint32_t wpost = smem_addr(own) + threadIdx.x * 16;
-  const uint32_t wpre = wpost + kWeightSlots * sb;
-  const uint32_t ring = wpre + kWeightSlots * sb;
+  __shared__ __align__(16) float red[kRed];
+  extern __shared__ __align__(16) uint8_t shared[];
+  Team<WARP, MAXT> team(a.team_threads, red);
+  const int tid = team.tid, step = team.threads;
+  const int unit = blockIdx.x * a.teams + team.index;
+  const uint32_t sb = blockDim.x * 16, wb = step * 16;
+  const uint32_t wpost = smem_addr(shared) + tid * 16;
+  const uint32_t wpre = wpost + (a.w_post ? kWeightSlots * wb : 0);
+  const uint32_t ring = smem_addr(shared) + threadIdx.x * 16 +
+                        ((a.w_post != nullptr) + (a.w_pre != nullptr)) * kWeightSlots * wb;
+  // slots of a vector's rows: the residual stream's, the block's, ...
+  const uint32_t add_at = sb * (1 + (a.y ? a.K : 0)), gate_at = add_at + (a.add ? sb : 0);
+  const uint32_t vector = gate_at + (a.gate ? sb : 0), token = V * vector;  // bytes
   bool in[V];    // vectors inside the row, and where
   int at[V];
 #pragma unroll
@@ -294,20 +303,20 @@ __global__ void __launch_bounds__(MAXT, 1) block_norm_kernel(NormArgs a) {
   auto fetch = [&](int64_t t, int i, uint32_t to) {
     if (t < a.T) {
       const int64_t off = t * a.row_bytes + at[i];
-      copy_async(to + Slot::Res * sb, a.res + off, in[i]);
+      copy_async(to, a.res + off, in[i]);
       if (GATHER) {
 #pragma unroll
         for (int k = 0; k < KMAX; ++k) {
           if (k >= a.K) break;
           const bool real = in[i] && p[k] >= 0;
-          copy_async(to + k * sb, a.y + (real ? p[k] * a.row_bytes + at[i] : 0), real);
+          copy_async(to + (k + 1) * sb, a.y + (real ? p[k] * a.row_bytes + at[i] : 0), real);
         }
       } else if (a.y) {
-        copy_async(to, a.y + off, in[i]);
+        copy_async(to + sb, a.y + off, in[i]);
       }
-      if (a.add) copy_async(to + Slot::Add * sb, a.add + off, in[i]);
+      if (a.add) copy_async(to + add_at, a.add + off, in[i]);
       if (a.gate)
-        copy_async(to + Slot::Gate * sb,
+        copy_async(to + gate_at,
                    a.gate + (static_cast<unsigned>(t) / static_cast<unsigned>(a.gate_tokens)) *
                                 a.row_bytes + at[i],
                    in[i]);
@@ -340,10 +349,12 @@ __global__ void __launch_bounds__(MAXT, 1) block_norm_kernel(NormArgs a) {
       for (int k = 0; k < KMAX; ++k) p[k] = p_read[k];
     }
   }
-  if (a.w_post) keep_weights<N>(a.w_post, a.w_f32, a.offset, wpost, sb, tid, step, a.nvec);
-  if (a.w_pre) keep_weights<N>(a.w_pre, a.w_f32, a.offset, wpre, sb, tid, step, a.nvec);
-  clear_sums<WARP>(red);
-  int turn = 0;
+  // each thread of the first team for its places in all teams
+  if (team.index == 0) {
+    if (a.w_post) keep_weights<N>(a.w_post, a.w_f32, a.offset, wpost, wb, tid, step, a.nvec);
+    if (a.w_pre) keep_weights<N>(a.w_pre, a.w_f32, a.offset, wpre, wb, tid, step, a.nvec);
+  }
+  __syncthreads();
   uint32_t stage = ring;
   for (int64_t t = unit; t < a.T; t += a.units) {
     const int64_t row = t * a.row_bytes;
@@ -365,43 +376,43 @@ __global__ void __launch_bounds__(MAXT, 1) block_norm_kernel(NormArgs a) {
     for (int i = 0; i < V; ++i) {
       if (AHEAD > 0) wait_copies<V * AHEAD - 1>();
       const uint32_t from = stage + i * vector;
-      auto get = [&](int slot, const uint8_t* g, bool real) {
+      auto get = [&](uint32_t slot, const uint8_t* g, bool real) {
         Vec16 x{};
-        if (AHEAD > 0) x = ld_shared(from + slot * sb);
+        if (AHEAD > 0) x = ld_shared(from + slot);
         else if (real) x = ld_vec(g);
         return x;
       };
-      res[i] = get(Slot::Res, a.res + row + at[i], in[i]);
+      res[i] = get(0, a.res + row + at[i], in[i]);
       if (GATHER) {
         Vec16 rows[KMAX];
         if (AHEAD == 0)
 #pragma unroll
           for (int k = 0; k < KMAX; ++k)
-            rows[k] = get(k, a.y + p[k] * a.row_bytes + at[i], in[i] && p[k] >= 0);
+            rows[k] = get((k + 1) * sb, a.y + p[k] * a.row_bytes + at[i], in[i] && p[k] >= 0);
 #pragma unroll
         for (int j = 0; j < P; ++j) c[i][j] = 0;
 #pragma unroll
         for (int k = 0; k < KMAX; ++k) {
           if (k >= a.K) break;
-          if (AHEAD > 0) rows[k] = get(k, nullptr, true);
+          if (AHEAD > 0) rows[k] = get((k + 1) * sb, nullptr, true);
           F2 f[P];
           PT::to(rows[k], f);
 #pragma unroll
           for (int j = 0; j < P; ++j) c[i][j] = fma2(both(wk[k]), f[j], c[i][j]);
         }
       } else if (a.y) {
-        PT::to(get(0, a.y + row + at[i], in[i]), c[i]);
+        PT::to(get(sb, a.y + row + at[i], in[i]), c[i]);
       } else {
         PT::to(res[i], c[i]);
       }
       if (a.add) {
         F2 f[P];
-        PT::to(get(Slot::Add, a.add + row + at[i], in[i]), f);
+        PT::to(get(add_at, a.add + row + at[i], in[i]), f);
 #pragma unroll
         for (int j = 0; j < P; ++j) c[i][j] = add2(c[i][j], f[j]);
       }
       if (a.gate)
-        gate[i] = get(Slot::Gate, a.gate + t / a.gate_tokens * a.row_bytes + at[i], in[i]);
+        gate[i] = get(gate_at, a.gate + t / a.gate_tokens * a.row_bytes + at[i], in[i]);
       if (a.c && in[i]) st_vec(a.c + row + at[i], PT::from(c[i]));
 #pragma unroll
       for (int j = 0; j < P; ++j) ss = fma2(c[i][j], c[i][j], ss);
@@ -414,7 +425,7 @@ __global__ void __launch_bounds__(MAXT, 1) block_norm_kernel(NormArgs a) {
     if (a.y) {
       float r = 1.0f;
       if (a.w_post) {
-        r = 1.0f / sqrtf(team_sum<WARP>(sum_of(ss), red, turn) * a.inv_h + a.eps);
+        r = 1.0f / sqrtf(team.sum(sum_of(ss)) * a.inv_h + a.eps);
         if (a.rstd_post && tid == 0) a.rstd_post[t] = r;
       }
       ss = 0;
@@ -422,7 +433,7 @@ __global__ void __launch_bounds__(MAXT, 1) block_norm_kernel(NormArgs a) {
       for (int i = 0; i < V; ++i) {
         F2 f[P];
         if (a.w_post) {
-          kept_weights<N>(wpost, sb, i, f);
+          kept_weights<N>(wpost, wb, i, f);
 #pragma unroll
           for (int j = 0; j < P; ++j) c[i][j] = mul2(mul2(c[i][j], both(r)), f[j]);
         }
@@ -441,12 +452,12 @@ __global__ void __launch_bounds__(MAXT, 1) block_norm_kernel(NormArgs a) {
       }
     }
     if (a.x) {
-      const float r = 1.0f / sqrtf(team_sum<WARP>(sum_of(ss), red, turn) * a.inv_h + a.eps);
+      const float r = 1.0f / sqrtf(team.sum(sum_of(ss)) * a.inv_h + a.eps);
       if (a.rstd_pre && tid == 0) a.rstd_pre[t] = r;
 #pragma unroll
       for (int i = 0; i < V; ++i) {
         F2 f[P];
-        kept_weights<N>(wpre, sb, i, f);
+        kept_weights<N>(wpre, wb, i, f);
 #pragma unroll
         for (int j = 0; j < P; ++j) f[j] = mul2(mul2(c[i][j], both(r)), f[j]);
         if (in[i]) st_vec(a.x + row + at[i], PT::from(f));
@@ -484,6 +495,7 @@ struct NormBwdArgs {
   int64_t row_bytes;
   int T, H, nvec, gate_tokens, groups;
   int chunk, units, blocks; // tokens of a unit (a team), units, blocks
+  int teams, team_threads;  // of a block; of a team
   int w_f32;
   float res_scale, offset, inv_h;
 };
@@ -515,27 +527,20 @@ __device__ __forceinline__ void flush_sums(F2 (&acc)[V][P], float* to, bool firs
 // D = gres' + r_p (v - h mean(v h)), v = gx w_pre, h = res' r_p: the gradient of
 // the residual sum; then the same form behind the gate for c.  AHEAD as in the
 // forward.
-template <typename Elt, bool GATE, int AHEAD>
-constexpr int backward_slots() {
-  constexpr int V = kEpt / (2 * PairTraits<Elt>::P);
-  return 2 * kWeightSlots + AHEAD * V * (GATE ? 5 : 4);
-}
-
 template <typename Elt, bool GATE, bool WARP, int MAXT, int AHEAD>
 __global__ void __launch_bounds__(MAXT, 1) block_norm_bwd_kernel(NormBwdArgs a) {
   using PT = PairTraits<Elt>;
   constexpr int P = PT::P, N = 2 * P, V = kEpt / N, ROWS = GATE ? 5 : 4;
-  const uint32_t sb = blockDim.x * 16, token = ROWS * V * sb;  // bytes
   enum { GRes, Gx, ResOut, C, Gate };
-  __shared__ __align__(16) float red[64];
-  extern __shared__ __align__(16) uint8_t own[];
-  const int tid = WARP ? threadIdx.x & 31 : threadIdx.x;
-  const int step = WARP ? 32 : blockDim.x;
-  const int unit = WARP ? blockIdx.x * kTeams + (threadIdx.x >> 5) : blockIdx.x;
-  if (unit >= a.units) return;  // a warp's; a block is always a unit
-  const uint32_t wpost = smem_addr(own) + threadIdx.x * 16;
-  const uint32_t wpre = wpost + kWeightSlots * sb;
-  const uint32_t ring = wpre + kWeightSlots * sb;
+  __shared__ __align__(16) float red[kRed];
+  extern __shared__ __align__(16) uint8_t shared[];
+  Team<WARP, MAXT> team(a.team_threads, red);
+  const int tid = team.tid, step = team.threads;
+  const int unit = blockIdx.x * a.teams + team.index;
+  const uint32_t sb = blockDim.x * 16, token = ROWS * V * sb, wb = step * 16;  // bytes
+  const uint32_t wpost = smem_addr(shared) + tid * 16;
+  const uint32_t wpre = wpost + kWeightSlots * wb;
+  const uint32_t ring = smem_addr(shared) + threadIdx.x * 16 + 2 * kWeightSlots * wb;
   bool in[V];    // vectors inside the row, and where
   int at[V];
 #pragma unroll
@@ -586,163 +591,206 @@ __global__ void __launch_bounds__(MAXT, 1) block_norm_bwd_kernel(NormBwdArgs a) 
     for (int n = 0; n < AHEAD; ++n) fetch(ring + n * token);
   float r_pre = a.gx && begin < end ? __ldg(a.rstd_pre + begin) : 0.0f;
   float r_post = a.w_post && begin < end ? __ldg(a.rstd_post + begin) : 1.0f;
-  if (a.w_post) keep_weights<N>(a.w_post, a.w_f32, a.offset, wpost, sb, tid, step, a.nvec);
-  if (a.gx) keep_weights<N>(a.w_pre, a.w_f32, a.offset, wpre, sb, tid, step, a.nvec);
-  clear_sums<WARP>(red);
+  if (team.index == 0) {
+    if (a.w_post) keep_weights<N>(a.w_post, a.w_f32, a.offset, wpost, wb, tid, step, a.nvec);
+    if (a.gx) keep_weights<N>(a.w_pre, a.w_f32, a.offset, wpre, wb, tid, step, a.nvec);
+  }
+  __syncthreads();
   F2 gpost[V][P], gpre[V][P], ggate[V][P];
 #pragma unroll
   for (int i = 0; i < V; ++i)
 #pragma unroll
     for (int j = 0; j < P; ++j) gpost[i][j] = gpre[i][j] = ggate[i][j] = 0;
-  float* post_row = a.part + static_cast<size_t>(unit) * a.H;
-  float* pre_row = a.part + static_cast<size_t>(a.units + unit) * a.H;
-  bool first = true, gate_first = true;
-  int held = 0, gate_held = 0, turn = 0;
+  // the block's rows of sums; a team adds to them when it has held kFlush tokens
+  // and at the end, the teams in turn
+  float* post_row = a.part + static_cast<size_t>(blockIdx.x) * a.H;
+  float* pre_row = a.part + static_cast<size_t>(a.blocks + blockIdx.x) * a.H;
+  bool gate_first = true;
+  int gate_held = 0;
   uint32_t stage = ring;
   int64_t row = begin * a.row_bytes;
-  for (int t = begin; t < end; ++t, row += a.row_bytes) {
-    auto load = [&](int k, int i, const uint8_t* p, int64_t o, F2* f) {
-      Vec16 x{};
-      if (AHEAD > 0) x = ld_shared(stage + (k * V + i) * sb);
-      else if (in[i]) x = ld_vec(p + o + at[i]);
-      PT::to(x, f);
-    };
-    const float rp = r_pre, r = r_post;
-    if (t + 1 < end) {  // the next token's, a row's time ahead
-      if (a.gx) r_pre = __ldg(a.rstd_pre + t + 1);
-      if (a.w_post) r_post = __ldg(a.rstd_post + t + 1);
-    }
-    if (AHEAD > 0) wait_copies<AHEAD - 1>();
-    F2 D[V][P], h[V][P];
-    if (a.gx) {
-      F2 s = 0;
-#pragma unroll
-      for (int i = 0; i < V; ++i) {
-        F2 w[P];
-        load(Gx, i, a.gx, row, D[i]);
-        load(ResOut, i, a.res_out, row, h[i]);
-        kept_weights<N>(wpre, sb, i, w);
-#pragma unroll
-        for (int j = 0; j < P; ++j) {
-          h[i][j] = mul2(h[i][j], both(rp));
-          gpre[i][j] = fma2(D[i][j], h[i][j], gpre[i][j]);
-          D[i][j] = mul2(D[i][j], w[j]);
-          s = fma2(D[i][j], h[i][j], s);
-        }
+  // All teams of a block make the same number of rounds of kFlush tokens; behind
+  // each they add their sums to the block's, one after the other.
+  const int rounds = (a.chunk - 1) / kFlush + 1;
+  for (int round = 0; round < rounds; ++round) {
+    const int stop = min(static_cast<int64_t>(end), begin64 + (round + 1) * static_cast<int64_t>(kFlush));
+    for (int t = begin64 + round * static_cast<int64_t>(kFlush); t < stop; ++t, row += a.row_bytes) {
+      auto load = [&](int k, int i, const uint8_t* p, int64_t o, F2* f) {
+        Vec16 x{};
+        if (AHEAD > 0) x = ld_shared(stage + (k * V + i) * sb);
+        else if (in[i]) x = ld_vec(p + o + at[i]);
+        PT::to(x, f);
+      };
+      const float rp = r_pre, r = r_post;
+      if (t + 1 < end) {  // the next token's, a row's time ahead
+        if (a.gx) r_pre = __ldg(a.rstd_pre + t + 1);
+        if (a.w_post) r_post = __ldg(a.rstd_post + t + 1);
       }
-      const float m = team_sum<WARP>(sum_of(s), red, turn) * a.inv_h;
+      if (AHEAD > 0) wait_copies<AHEAD - 1>();
+      F2 D[V][P], h[V][P];
+      if (a.gx) {
+        F2 s = 0;
 #pragma unroll
-      for (int i = 0; i < V; ++i) {
-        F2 g[P];
-#pragma unroll
-        for (int j = 0; j < P; ++j) g[j] = 0;
-        if (a.gres_out) load(GRes, i, a.gres_out, row, g);
-#pragma unroll
-        for (int j = 0; j < P; ++j)
-          D[i][j] = fma2(both(rp), fma2(both(-m), h[i][j], D[i][j]), g[j]);
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < V; ++i) load(GRes, i, a.gres_out, row, D[i]);
-    }
-    if (a.gres) {
-#pragma unroll
-      for (int i = 0; i < V; ++i) {
-        F2 o[P];
-#pragma unroll
-        for (int j = 0; j < P; ++j) o[j] = mul2(both(a.res_scale), D[i][j]);
-        if (in[i]) st_vec(a.gres + row + at[i], PT::from(o));
-      }
-    }
-    if (a.c) {
-      F2 s = 0;
-#pragma unroll
-      for (int i = 0; i < V; ++i) {
-        F2 w[P];
-        load(C, i, a.c, row, h[i]);
-#pragma unroll
-        for (int j = 0; j < P; ++j) h[i][j] = mul2(h[i][j], both(r));
-        if (a.w_post) kept_weights<N>(wpost, sb, i, w);
-        if (GATE) {
-          F2 g[P];
-          load(Gate, i, a.gate, group.row, g);
+        for (int i = 0; i < V; ++i) {
+          F2 w[P];
+          load(Gx, i, a.gx, row, D[i]);
+          load(ResOut, i, a.res_out, row, h[i]);
+          kept_weights<N>(wpre, wb, i, w);
 #pragma unroll
           for (int j = 0; j < P; ++j) {
-            ggate[i][j] = fma2(D[i][j], a.w_post ? mul2(h[i][j], w[j]) : h[i][j], ggate[i][j]);
-            D[i][j] = mul2(D[i][j], g[j]);
-          }
-        }
-        if (a.w_post) {
-#pragma unroll
-          for (int j = 0; j < P; ++j) {
-            gpost[i][j] = fma2(D[i][j], h[i][j], gpost[i][j]);
+            h[i][j] = mul2(h[i][j], both(rp));
+            gpre[i][j] = fma2(D[i][j], h[i][j], gpre[i][j]);
             D[i][j] = mul2(D[i][j], w[j]);
             s = fma2(D[i][j], h[i][j], s);
           }
         }
-      }
-      if (a.w_post) {
-        const float m = team_sum<WARP>(sum_of(s), red, turn) * a.inv_h;
+        const float m = team.sum(sum_of(s)) * a.inv_h;
 #pragma unroll
-        for (int i = 0; i < V; ++i)
+        for (int i = 0; i < V; ++i) {
+          F2 g[P];
+#pragma unroll
+          for (int j = 0; j < P; ++j) g[j] = 0;
+          if (a.gres_out) load(GRes, i, a.gres_out, row, g);
 #pragma unroll
           for (int j = 0; j < P; ++j)
-            D[i][j] = mul2(both(r), fma2(both(-m), h[i][j], D[i][j]));
+            D[i][j] = fma2(both(rp), fma2(both(-m), h[i][j], D[i][j]), g[j]);
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i) load(GRes, i, a.gres_out, row, D[i]);
       }
-    }
-    if (a.gy) {
+      if (a.gres) {
 #pragma unroll
-      for (int i = 0; i < V; ++i)
-        if (in[i]) st_vec(a.gy + row + at[i], PT::from(D[i]));
-    }
-    if (AHEAD > 0) {
-      fetch(stage);
-      stage += token;
-      if (stage == ring + AHEAD * token) stage = ring;
-    }
-    if (GATE) {
-      const int64_t g0 = group.end - a.gate_tokens;
-      const bool ends = t + 1 == group.end || t + 1 == a.T;
-      if (a.ggate) {
-        float* slot = a.slots + static_cast<size_t>(2 * unit + (g0 >= begin)) * a.H;
-        if (ends && g0 >= begin) {  // all of the group's tokens
+        for (int i = 0; i < V; ++i) {
+          F2 o[P];
 #pragma unroll
-          for (int i = 0; i < V; ++i) {
-            if (in[i]) {
-#pragma unroll
-              for (int j = 0; j < P; ++j)
-                if (!gate_first) {
-                  const float2 x =
-                      *reinterpret_cast<const float2*>(slot + ((tid + i * step) * P + j) * 2);
-                  ggate[i][j] = add2(ggate[i][j], pair(x.x, x.y));
-                }
-              st_vec(a.ggate + group.row + at[i], PT::from(ggate[i]));
-            }
-#pragma unroll
-            for (int j = 0; j < P; ++j) ggate[i][j] = 0;
-          }
-          gate_first = true;
-          gate_held = 0;
-        } else if (ends || t + 1 == end || ++gate_held == kFlush) {
-          flush_sums(ggate, slot, gate_first, tid, step, a.nvec);
-          gate_first = ends;
-          gate_held = 0;
+          for (int j = 0; j < P; ++j) o[j] = mul2(both(a.res_scale), D[i][j]);
+          if (in[i]) st_vec(a.gres + row + at[i], PT::from(o));
         }
       }
-      if (ends) {
-        group.row += a.row_bytes;
-        group.end += a.gate_tokens;
+      if (a.c) {
+        F2 s = 0;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+          F2 w[P];
+          load(C, i, a.c, row, h[i]);
+#pragma unroll
+          for (int j = 0; j < P; ++j) h[i][j] = mul2(h[i][j], both(r));
+          if (a.w_post) kept_weights<N>(wpost, wb, i, w);
+          if (GATE) {
+            F2 g[P];
+            load(Gate, i, a.gate, group.row, g);
+#pragma unroll
+            for (int j = 0; j < P; ++j) {
+              ggate[i][j] = fma2(D[i][j], a.w_post ? mul2(h[i][j], w[j]) : h[i][j], ggate[i][j]);
+              D[i][j] = mul2(D[i][j], g[j]);
+            }
+          }
+          if (a.w_post) {
+#pragma unroll
+            for (int j = 0; j < P; ++j) {
+              gpost[i][j] = fma2(D[i][j], h[i][j], gpost[i][j]);
+              D[i][j] = mul2(D[i][j], w[j]);
+              s = fma2(D[i][j], h[i][j], s);
+            }
+          }
+        }
+        if (a.w_post) {
+          const float m = team.sum(sum_of(s)) * a.inv_h;
+#pragma unroll
+          for (int i = 0; i < V; ++i)
+#pragma unroll
+            for (int j = 0; j < P; ++j)
+              D[i][j] = mul2(both(r), fma2(both(-m), h[i][j], D[i][j]));
+        }
+      }
+      if (a.gy) {
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+          if (in[i]) st_vec(a.gy + row + at[i], PT::from(D[i]));
+      }
+      if (AHEAD > 0) {
+        fetch(stage);
+        stage += token;
+        if (stage == ring + AHEAD * token) stage = ring;
+      }
+      if (GATE) {
+        const int64_t g0 = group.end - a.gate_tokens;
+        const bool ends = t + 1 == group.end || t + 1 == a.T;
+        if (a.ggate) {
+          float* slot = a.slots + static_cast<size_t>(2 * unit + (g0 >= begin)) * a.H;
+          if (ends && g0 >= begin) {  // all of the group's tokens
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+              if (in[i]) {
+#pragma unroll
+                for (int j = 0; j < P; ++j)
+                  if (!gate_first) {
+                    const float2 x =
+                        *reinterpret_cast<const float2*>(slot + ((tid + i * step) * P + j) * 2);
+                    ggate[i][j] = add2(ggate[i][j], pair(x.x, x.y));
+                  }
+                st_vec(a.ggate + group.row + at[i], PT::from(ggate[i]));
+              }
+#pragma unroll
+              for (int j = 0; j < P; ++j) ggate[i][j] = 0;
+            }
+            gate_first = true;
+            gate_held = 0;
+          } else if (ends || t + 1 == end || ++gate_held == kFlush) {
+            flush_sums(ggate, slot, gate_first, tid, step, a.nvec);
+            gate_first = ends;
+            gate_held = 0;
+          }
+        }
+        if (ends) {
+          group.row += a.row_bytes;
+          group.end += a.gate_tokens;
+        }
       }
     }
-    if (++held == kFlush) {
-      if (a.gw_post) flush_sums(gpost, post_row, first, tid, step, a.nvec);
-      if (a.gw_pre) flush_sums(gpre, pre_row, first, tid, step, a.nvec);
-      first = false;
-      held = 0;
+    if (a.teams > 1 && round + 1 == rounds) break;
+    for (int k = 0; k < a.teams; ++k) {
+      if (k > 0) __syncthreads();
+      if (k != team.index) continue;
+      if (a.gw_post) flush_sums(gpost, post_row, round + k == 0, tid, step, a.nvec);
+      if (a.gw_pre) flush_sums(gpre, pre_row, round + k == 0, tid, step, a.nvec);
     }
+    if (a.teams > 1) __syncthreads();
   }
-  if (a.gw_post) flush_sums(gpost, post_row, first, tid, step, a.nvec);
-  if (a.gw_pre) flush_sums(gpre, pre_row, first, tid, step, a.nvec);
+  release_join();
+  if (a.teams == 1) return;
+  // behind the last round the teams' sums meet in shared memory
+  wait_copies<0>();
+  auto meet = [&](const F2 (&acc)[V][P], float* to) {
+    __syncthreads();
+#pragma unroll
+    for (int q = 0; q < kWeightSlots; ++q) {
+      const float2 x = split(acc[q / (P / 2)][q % (P / 2) * 2]);
+      const float2 y = split(acc[q / (P / 2)][q % (P / 2) * 2 + 1]);
+      st_shared(ring + q * sb, make_float4(x.x, x.y, y.x, y.y));
+    }
+    __syncthreads();
+    const uint32_t first = smem_addr(shared) + 2 * kWeightSlots * wb;
+    for (int n = threadIdx.x; n < kWeightSlots * step; n += blockDim.x) {
+      const int q = n / step, thread = n - q * step;
+      const int v = thread + q / (P / 2) * step;
+      if (v >= a.nvec) continue;
+      float4* p = reinterpret_cast<float4*>(to + v * N + q % (P / 2) * 4);
+      float4 s{0.0f, 0.0f, 0.0f, 0.0f};
+      if (rounds > 1) s = *p;
+      for (int k = 0; k < a.teams; ++k) {
+        const Vec16 x = ld_shared(first + q * sb + k * wb + thread * 16);
+        s.x += __uint_as_float(x.u[0]);
+        s.y += __uint_as_float(x.u[1]);
+        s.z += __uint_as_float(x.u[2]);
+        s.w += __uint_as_float(x.u[3]);
+      }
+      *p = s;
+    }
+  };
+  if (a.gw_post) meet(gpost, post_row);
+  if (a.gw_pre) meet(gpre, pre_row);
 }
 
 // Joins the units' column sums: row y = 0, 1 of the grid the weights'
@@ -750,19 +798,19 @@ __global__ void __launch_bounds__(MAXT, 1) block_norm_bwd_kernel(NormBwdArgs a) 
 // units of the one that goes on from unit i into the next; a group inside one
 // unit is done.
 template <typename Elt>
-__global__ void __launch_bounds__(1024) block_norm_join_kernel(NormBwdArgs a) {
+__global__ void __launch_bounds__(32 * kJoinWarps) block_norm_join_kernel(NormBwdArgs a) {
   grid_dependency_wait();
-  __shared__ float ps[32][33];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
-  const int col = blockIdx.x * 32 + lane;
+  __shared__ float2 ps[kJoinWarps][32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int col = blockIdx.x * kJoinCols + 2 * lane;
   const int y = blockIdx.y;
   float* out = nullptr;
   const float* from = a.part;
-  int u0 = 0, u1 = a.units, stride = 1, head = 0;
+  int u0 = 0, u1 = a.blocks, stride = 1, head = 0;
   int group = 0;
   if (y < 2) {
     out = y == 0 ? a.gw_post : a.gw_pre;
-    from += static_cast<size_t>(y) * a.units * a.H;
+    from += static_cast<size_t>(y) * a.blocks * a.H;
     if (!out) return;
   } else {
     const int64_t next = (static_cast<int64_t>(y - 2) + 1) * a.chunk;
@@ -777,40 +825,41 @@ __global__ void __launch_bounds__(1024) block_norm_join_kernel(NormBwdArgs a) {
     stride = 2;
     head = 1;
   }
-  float p = 0.0f;
+  float2 p{0.0f, 0.0f};
   if (col < a.H)
-#pragma unroll 4
-    for (int u = u0 + warp; u < u1; u += warps)
-      p += __ldcg(from + static_cast<size_t>(stride * u + (u == u0 ? head : 0)) * a.H + col);
+#pragma unroll 8
+    for (int u = u0 + warp; u < u1; u += kJoinWarps) {
+      const float2 x = __ldcg(reinterpret_cast<const float2*>(
+          from + static_cast<size_t>(stride * u + (u == u0 ? head : 0)) * a.H + col));
+      p.x += x.x;
+      p.y += x.y;
+    }
   ps[warp][lane] = p;
   __syncthreads();
   if (warp != 0 || col >= a.H) return;
-  for (int w = 1; w < warps; ++w) p += ps[w][lane];
-  if (y < 2)
-    out[col] = p;
-  else
-    reinterpret_cast<Elt*>(a.ggate + group * a.row_bytes)[col] = static_cast<Elt>(p);
+#pragma unroll
+  for (int w = 1; w < kJoinWarps; ++w) {
+    p.x += ps[w][lane].x;
+    p.y += ps[w][lane].y;
+  }
+  if (y < 2) {
+    out[col] = p.x;
+    out[col + 1] = p.y;
+  } else {
+    Elt* g = reinterpret_cast<Elt*>(a.ggate + group * a.row_bytes) + col;
+    g[0] = static_cast<Elt>(p.x);
+    g[1] = static_cast<Elt>(p.y);
+  }
 }
 
 bool one_warp(int H) { return H <= kWarpRow; }
 
 int team_threads(int H) { return (H + kWarpRow - 1) / kWarpRow * 32; }
 
-// Tokens of a unit and units of the backward: as many threads an SM as its
-// registers hold.
-int bwd_units_per_sm(int H) {
-  return one_warp(H) ? 16 : 512 / team_threads(H) < 1 ? 1 : 512 / team_threads(H);
-}
-
-void bwd_units(int T, int H, int num_sms, int* chunk, int* units) {
-  const int most = bwd_units_per_sm(H) * num_sms;
-  int n = T < most ? T : most;
-  if (n < 1) n = 1;
-  *chunk = (T + n - 1) / n;
-  if (*chunk < 1) *chunk = 1;
-  n = (T + *chunk - 1) / *chunk;
-  if (n < 1) n = 1;
-  *units = n;
+// Teams of a block for T tokens: as many as it holds, once there is one for every SM.
+int teams_of(int T, int H, int num_sms) {
+  const int most = kTeamThreads / team_threads(H), wanted = (T + num_sms - 1) / num_sms;
+  return most < 1 || wanted < 1 ? 1 : wanted < most ? wanted : most;
 }
 
 // Largest dynamic shared memory for a kernel that takes more than the default.
@@ -829,86 +878,82 @@ struct Chosen {
   size_t shared;
 };
 
-template <typename Elt, int KMAX, bool WARP, int MAXT, int AHEAD>
-Chosen<NormArgs> forward(int threads) {
-  return {block_norm_kernel<Elt, KMAX, WARP, MAXT, AHEAD>, AHEAD,
-          static_cast<size_t>(threads) * forward_slots<Elt, KMAX, AHEAD>() * 16};
+size_t kept_bytes(int H, int weights) {
+  return static_cast<size_t>(team_threads(H)) * 16 * kWeightSlots * weights;
+}
+// Shared memory of `rows` rows' vectors in a block of `threads`.
+template <typename Elt>
+size_t token_bytes(int threads, int rows) {
+  return static_cast<size_t>(threads) * kEpt * sizeof(Elt) * rows;
 }
 
 // The kernel with the most tokens under way whose shared memory fits into `most`.
 template <typename Elt, int KMAX, bool WARP, int MAXT>
-Chosen<NormArgs> forward_within(int threads, size_t most) {
-  if constexpr (KMAX == 1 && MAXT < 1024) {
-    const auto two = forward<Elt, KMAX, WARP, MAXT, 2>(threads);
-    if (two.shared <= most) return two;
-  }
-  const auto one = forward<Elt, KMAX, WARP, MAXT, 1>(threads);
-  return one.shared <= most ? one : forward<Elt, KMAX, WARP, MAXT, 0>(threads);
+Chosen<NormArgs> forward_within(size_t kept, size_t token, size_t most) {
+  if constexpr (KMAX == 1 && MAXT < 1024)
+    if (kept + 2 * token <= most)
+      return {block_norm_kernel<Elt, KMAX, WARP, MAXT, 2>, 2, kept + 2 * token};
+  if (kept + token <= most) return {block_norm_kernel<Elt, KMAX, WARP, MAXT, 1>, 1, kept + token};
+  return {block_norm_kernel<Elt, KMAX, WARP, MAXT, 0>, 0, kept};
 }
 template <typename Elt, int KMAX>
-Chosen<NormArgs> forward_kernel(int H, int threads, size_t most) {
-  return one_warp(H)      ? forward_within<Elt, KMAX, true, 32 * kTeams>(threads, most)
-         : threads <= 512 ? forward_within<Elt, KMAX, false, 512>(threads, most)
-                          : forward_within<Elt, KMAX, false, 1024>(threads, most);
+Chosen<NormArgs> forward_kernel(int H, size_t kept, size_t token, size_t most) {
+  return one_warp(H) ? forward_within<Elt, KMAX, true, kTeamThreads>(kept, token, most)
+         : team_threads(H) <= kTeamThreads
+             ? forward_within<Elt, KMAX, false, kTeamThreads>(kept, token, most)
+             : forward_within<Elt, KMAX, false, 1024>(kept, token, most);
 }
 template <typename Elt>
-Chosen<NormArgs> forward_kernel(int kmax, int H, int threads, size_t most) {
-  return kmax == 1   ? forward_kernel<Elt, 1>(H, threads, most)
-         : kmax == 8 ? forward_kernel<Elt, 8>(H, threads, most)
-                     : forward_kernel<Elt, 16>(H, threads, most);
+Chosen<NormArgs> forward_kernel(int H, int kmax, int threads, int rows, int weights) {
+  const size_t kept = kept_bytes(H, weights), token = token_bytes<Elt>(threads, rows);
+  return kmax == 1   ? forward_kernel<Elt, 1>(H, kept, token, kShared)
+         : kmax == 8 ? forward_kernel<Elt, 8>(H, kept, token, kShared)
+                     : forward_kernel<Elt, 16>(H, kept, token, kShared);
 }
 
-template <typename Elt, bool GATE, bool WARP, int MAXT, int AHEAD>
-Chosen<NormBwdArgs> backward(int threads) {
-  return {block_norm_bwd_kernel<Elt, GATE, WARP, MAXT, AHEAD>, AHEAD,
-          static_cast<size_t>(threads) * backward_slots<Elt, GATE, AHEAD>() * 16};
-}
 template <typename Elt, bool GATE, bool WARP, int MAXT>
-Chosen<NormBwdArgs> backward_within(int threads, size_t most) {
+Chosen<NormBwdArgs> backward_within(size_t kept, size_t token, size_t most) {
   if constexpr (MAXT < 1024) {
-    const auto three = backward<Elt, GATE, WARP, MAXT, 3>(threads);
-    if (three.shared <= most) return three;
-    const auto two = backward<Elt, GATE, WARP, MAXT, 2>(threads);
-    if (two.shared <= most) return two;
+    if (kept + 3 * token <= most)
+      return {block_norm_bwd_kernel<Elt, GATE, WARP, MAXT, 3>, 3, kept + 3 * token};
+    if (kept + 2 * token <= most)
+      return {block_norm_bwd_kernel<Elt, GATE, WARP, MAXT, 2>, 2, kept + 2 * token};
   }
-  return backward<Elt, GATE, WARP, MAXT, 0>(threads);
+  return {block_norm_bwd_kernel<Elt, GATE, WARP, MAXT, 0>, 0, kept};
 }
 template <typename Elt, bool GATE>
-Chosen<NormBwdArgs> backward_kernel(int H, int threads, size_t most) {
-  return one_warp(H)      ? backward_within<Elt, GATE, true, 32 * kTeams>(threads, most)
-         : threads <= 512 ? backward_within<Elt, GATE, false, 512>(threads, most)
-                          : backward_within<Elt, GATE, false, 1024>(threads, most);
+Chosen<NormBwdArgs> backward_fitting(int H, size_t kept, size_t token, size_t most) {
+  return one_warp(H) ? backward_within<Elt, GATE, true, kTeamThreads>(kept, token, most)
+         : team_threads(H) <= kTeamThreads
+             ? backward_within<Elt, GATE, false, kTeamThreads>(kept, token, most)
+             : backward_within<Elt, GATE, false, 1024>(kept, token, most);
+}
+template <typename Elt, bool GATE>
+Chosen<NormBwdArgs> backward_kernel(int H, int threads) {
+  const size_t kept = kept_bytes(H, 2);
+  auto c = backward_fitting<Elt, GATE>(H, kept, token_bytes<Elt>(threads, GATE ? 5 : 4), kShared);
+  // the teams' sums meet there as well
+  const size_t meet = kept + static_cast<size_t>(threads) * kEpt * sizeof(float);
+  if (threads > team_threads(H) && c.shared < meet) c.shared = meet;
+  return c;
 }
 
 // Shared memory for every kernel that the choices above can make.
-template <typename Elt, bool WARP, int MAXT>
-cudaError_t allow_team() {
+template <typename Elt>
+cudaError_t allow_all() {
   cudaError_t e = cudaSuccess;
   auto allow = [&](const auto& c) {
     if (e == cudaSuccess) e = allow_shared(c.kernel);
   };
-  allow(forward<Elt, 1, WARP, MAXT, 0>(MAXT));
-  allow(forward<Elt, 1, WARP, MAXT, 1>(MAXT));
-  allow(forward<Elt, 8, WARP, MAXT, 0>(MAXT));
-  allow(forward<Elt, 8, WARP, MAXT, 1>(MAXT));
-  allow(forward<Elt, 16, WARP, MAXT, 0>(MAXT));
-  allow(forward<Elt, 16, WARP, MAXT, 1>(MAXT));
-  allow(backward<Elt, false, WARP, MAXT, 0>(MAXT));
-  allow(backward<Elt, true, WARP, MAXT, 0>(MAXT));
-  if constexpr (MAXT < 1024) {
-    allow(forward<Elt, 1, WARP, MAXT, 2>(MAXT));
-    allow(backward<Elt, false, WARP, MAXT, 2>(MAXT));
-    allow(backward<Elt, false, WARP, MAXT, 3>(MAXT));
-    allow(backward<Elt, true, WARP, MAXT, 2>(MAXT));
-    allow(backward<Elt, true, WARP, MAXT, 3>(MAXT));
-  }
+  for (int H : {kWarpRow, kTeamThreads * kEpt, 1024 * kEpt})
+    for (size_t fit = 0; fit <= 3; ++fit) {  // tokens that there is room for
+      allow(forward_kernel<Elt, 1>(H, 0, 1, fit));
+      allow(forward_kernel<Elt, 8>(H, 0, 1, fit));
+      allow(forward_kernel<Elt, 16>(H, 0, 1, fit));
+      allow(backward_fitting<Elt, false>(H, 0, 1, fit));
+      allow(backward_fitting<Elt, true>(H, 0, 1, fit));
+    }
   return e;
-}
-template <typename Elt>
-cudaError_t allow_all() {
-  cudaError_t e = allow_team<Elt, true, 32 * kTeams>();
-  if (e == cudaSuccess) e = allow_team<Elt, false, 512>();
-  return e == cudaSuccess ? allow_team<Elt, false, 1024>() : e;
 }
 
 }  // namespace
@@ -929,10 +974,20 @@ cudaError_t prepare_block_norm_kernels() {
   return e;
 }
 
+namespace {
+// Units of the backward for T tokens, at least: the workspace of T serves fewer.
+int units_of(int T, int H, int num_sms, int* teams) {
+  *teams = teams_of(T, H, num_sms);
+  const int blocks = (T + *teams - 1) / *teams;
+  return *teams * (blocks < 1 ? 1 : blocks < num_sms ? blocks : num_sms);
+}
+}  // namespace
+
 size_t block_norm_workspace(const moe_handle* h, int T, int H, int gate_tokens) {
-  const int most = bwd_units_per_sm(H) * h->num_sms;  // grows with T, unlike the units in use
-  const size_t units = T < 1 ? 1 : T < most ? T : most;
-  return 2 * units * (gate_tokens > 1 ? 2 : 1) * H * sizeof(float);
+  int teams;
+  const size_t units = units_of(T, H, h->num_sms, &teams);
+  const size_t blocks = T < 1 ? 1 : T < h->num_sms ? T : h->num_sms;
+  return (2 * blocks + (gate_tokens > 1 ? 2 * units : 0)) * H * sizeof(float);
 }
 
 cudaError_t launch_block_norm(const moe_handle* h, const moe_block_norm_args& q, int T,
@@ -966,16 +1021,22 @@ cudaError_t launch_block_norm(const moe_handle* h, const moe_block_norm_args& q,
   a.inv_h = 1.0f / q.H;
   a.flags = h->flags;
   if (T == 0) return cudaSuccess;
-  const bool warp = one_warp(q.H);
-  const int threads = warp ? 32 * kTeams : team_threads(q.H);
+  if (!q.gather) a.K = 1;
+  a.teams = teams_of(T, q.H, h->num_sms);
+  a.team_threads = team_threads(q.H);
+  const int threads = a.teams * a.team_threads;
   const int kmax = !q.gather ? 1 : a.K <= 8 ? 8 : 16;
-  const auto c = bf16 ? forward_kernel<__nv_bfloat16>(kmax, q.H, threads, kShared)
-                      : forward_kernel<float>(kmax, q.H, threads, kShared);
-  const long long teams = warp ? kTeams : 1;
-  const long long most = teams * h->num_sms *
-                         resident_blocks(reinterpret_cast<const void*>(c.kernel), threads, c.shared);
-  a.units = static_cast<int>(T < most ? T : most);
-  c.kernel<<<static_cast<unsigned>((a.units + teams - 1) / teams), threads, c.shared, s>>>(a);
+  const int rows = 1 + (a.y ? a.K : 0) + (a.add != nullptr) + (a.gate != nullptr);
+  const int weights = (a.w_post != nullptr) + (a.w_pre != nullptr);
+  const auto c = bf16 ? forward_kernel<__nv_bfloat16>(q.H, kmax, threads, rows, weights)
+                      : forward_kernel<float>(q.H, kmax, threads, rows, weights);
+  const long long most =
+      static_cast<long long>(h->num_sms) *
+      resident_blocks(reinterpret_cast<const void*>(c.kernel), threads, c.shared);
+  const int blocks = (T - 1) / a.teams + 1;
+  const int grid = static_cast<int>(blocks < most ? blocks : most);
+  a.units = grid * a.teams;
+  c.kernel<<<grid, threads, c.shared, s>>>(a);
   return cudaGetLastError();
 }
 
@@ -1007,20 +1068,19 @@ cudaError_t launch_block_norm_bwd(const moe_handle* h, const moe_block_norm_bwd_
   a.res_scale = static_cast<float>(q.res_scale);
   a.offset = static_cast<float>(q.weight_offset);
   a.inv_h = 1.0f / q.H;
-  bwd_units(T, q.H, h->num_sms, &a.chunk, &a.units);
+  a.units = units_of(T, q.H, h->num_sms, &a.teams);
+  a.chunk = T > 0 ? (T - 1) / a.units + 1 : 1;
+  a.blocks = a.units / a.teams;
+  a.team_threads = team_threads(q.H);
   a.part = static_cast<float*>(workspace);
-  a.slots = a.part + 2 * static_cast<size_t>(a.units) * q.H;
-  const bool warp = one_warp(q.H);
-  a.blocks = warp ? (a.units + kTeams - 1) / kTeams : a.units;
-  const int threads = warp ? 32 * kTeams : team_threads(q.H);
+  a.slots = a.part + 2 * static_cast<size_t>(a.blocks) * q.H;
+  const int threads = a.teams * a.team_threads;
   const bool gated = q.d_gate != nullptr;
-  const int blocks_per_sm = warp ? 16 / kTeams : bwd_units_per_sm(q.H);
-  const size_t most = kSmShared / blocks_per_sm - kBlockShared;
   using B = __nv_bfloat16;
-  const auto k = bf16 ? (gated ? backward_kernel<B, true>(q.H, threads, most)
-                               : backward_kernel<B, false>(q.H, threads, most))
-                      : (gated ? backward_kernel<float, true>(q.H, threads, most)
-                               : backward_kernel<float, false>(q.H, threads, most));
+  const auto k = bf16 ? (gated ? backward_kernel<B, true>(q.H, threads)
+                               : backward_kernel<B, false>(q.H, threads))
+                      : (gated ? backward_kernel<float, true>(q.H, threads)
+                               : backward_kernel<float, false>(q.H, threads));
   if (T > 0) {
     k.kernel<<<a.blocks, threads, k.shared, s>>>(a);
     const cudaError_t e = cudaGetLastError();
@@ -1029,9 +1089,10 @@ cudaError_t launch_block_norm_bwd(const moe_handle* h, const moe_block_norm_bwd_
   const bool spans = a.ggate && a.gate_tokens > 1;
   if (!a.gw_post && !a.gw_pre && !spans) return cudaSuccess;
   const int join_rows = 2 + (!spans ? 0 : a.groups < a.units ? a.groups : a.units);
-  if (T == 0) a.units = 0;  // sums of nothing
+  if (T == 0) a.blocks = 0;  // sums of nothing
   return launch_chained(bf16 ? block_norm_join_kernel<B> : block_norm_join_kernel<float>,
-                        dim3((q.H + 31) / 32, join_rows), dim3(1024), 0, s, false, a);
+                        dim3((q.H + kJoinCols - 1) / kJoinCols, join_rows), dim3(32 * kJoinWarps), 0, s, false,
+                        a);
 }
 
 }  // namespace moe
