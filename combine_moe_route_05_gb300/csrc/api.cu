@@ -186,6 +186,7 @@ moe_status moe_handle_create(const moe_config* c, void* d_workspace, size_t work
   if (moe::prepare_layout_kernels() != cudaSuccess) return MOE_ERR_CUDA;
   if (moe::prepare_w2_kernel() != cudaSuccess) return MOE_ERR_CUDA;
   if (moe::prepare_layer_kernels() != cudaSuccess) return MOE_ERR_CUDA;
+  if (moe::prepare_balance_kernels() != cudaSuccess) return MOE_ERR_CUDA;
   if (moe::prepare_block_norm_kernels() != cudaSuccess) return MOE_ERR_CUDA;
 
   uint8_t* ws = static_cast<uint8_t*>(d_workspace);
@@ -498,7 +499,7 @@ moe_status moe_layer(const moe_handle* h, const moe_layer_args* q, int32_t T, vo
 
 size_t moe_balance_workspace_bytes(const moe_config* c, int32_t num_seqs) {
   if (!config_valid(c) || num_seqs < 1) return 0;
-  return moe::balance_plan(c->num_experts, num_seqs).total;
+  return moe::balance_plan(c->num_experts).total;
 }
 
 moe_status moe_balance(const moe_handle* h, const float* d_logits, const int32_t* d_idx, int32_t T,
@@ -514,7 +515,7 @@ moe_status moe_balance(const moe_handle* h, const float* d_logits, const int32_t
       !aligned(d_prob, 4))
     return MOE_ERR_INVALID;
   if (!d_workspace || !aligned(d_workspace, kAlign) ||
-      workspace_bytes < moe::balance_plan(h->cfg.num_experts, num_seqs).total)
+      workspace_bytes < moe::balance_plan(h->cfg.num_experts).total)
     return MOE_ERR_INVALID;
   return from_cuda(moe::launch_balance(h, d_logits, d_idx, T, d_seq_off, num_seqs, coef, d_loss,
                                        d_cnt, d_prob, d_workspace, as_stream(stream)));

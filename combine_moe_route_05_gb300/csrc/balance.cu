@@ -14,8 +14,14 @@
 // sequence is a fragment.  A sequence inside one tile is finished there; the
 // fragments of one that spans tiles go to slots (two a tile suffice: one for
 // the fragment that began in an earlier tile, one for that which goes on into
-// the next) and a second kernel adds them up.  Every sum has a fixed order
-// (counts are integers), so repeated calls give the same bits.
+// the next), and a second kernel, one cluster, adds them up and the loss with
+// them.  Every sum has a fixed order (counts are integers), so repeated calls
+// give the same bits.
+//
+// Both passes read the logits once and are bound by HBM at the largest sizes,
+// below some 20 MB by the chain of dependent loads around that: offsets, logits,
+// slots.  So offsets are read by all threads at once and searched in shared
+// memory, and a warp loads several tokens' logits before it works on the first.
 #include <type_traits>
 
 #include "common.cuh"
@@ -25,11 +31,14 @@ namespace moe {
 namespace {
 
 constexpr unsigned kFull = 0xffffffffu;
-constexpr int kWarps = 8;
+constexpr int kWarps = 32;       // of a tile's block: one an SM
 constexpr int kThreads = kWarps * 32;
-constexpr int kMaxTiles = 1024;
-constexpr int kOffBatch = 256;   // sequence offsets staged at a time
-constexpr int kJoinCols = 32;    // experts of a block of the second kernel
+constexpr int kMaxTiles = 256;
+constexpr int kBwdWarps = 8;     // of a block of the backward
+constexpr int kOffBatch = 1024;  // sequence offsets staged at a time
+constexpr int kJoinWarps = 32;   // of a block of the second kernel
+constexpr int kCluster = 8;      // blocks of the second kernel
+constexpr int kSlots = 6;        // slots that one of its warps loads at a time
 // Tokens a team sums in registers before it adds them to shared memory: bounds
 // the number of fp32 additions in a row however long a tile is.
 constexpr int kFlush = 64;
@@ -41,7 +50,7 @@ struct BalArgs {
   const int32_t* off;    // [S + 1] or NULL: one sequence, all T tokens
   int T, E, K, S;
   int tile, tiles;       // tokens of a tile, tiles
-  int chunks;            // blocks of kJoinCols experts
+  int chunks;            // groups of 32 experts
   int vec;               // rows can be read 16 bytes at a time
   float coef;
   uint32_t* flags;
@@ -51,8 +60,8 @@ struct BalArgs {
   float* loss;           // [1]
   float* slot_p;         // [2 * tiles, E]
   int32_t* slot_c;       // [2 * tiles, E]
-  float* part;           // [S, chunks]
-  unsigned* ticket;
+  float* tile_loss;      // [tiles] of the sequences inside a tile
+  int32_t* tail;         // [tiles] the sequence that begins there and goes on, or -1
   // backward
   const int32_t* bcnt;   // [S, E]
   const float* gloss;    // [1] or NULL: 1
@@ -120,67 +129,117 @@ __device__ __forceinline__ void load_row(const T1* row, int E, bool vec, bool li
   }
 }
 
-// Turns a team's logits v into p and, for the backward, q (see the top).  A
-// logit of -inf is an expert that is masked out: p = q = 0.  A row without any
-// other is 0, and so is one with a NaN or +inf, for which `bad` is returned.
-// exp is the fast one: its error, 2 + |x| ulp at x <= 0, falls on values that
-// are e^x of the row's largest.
-template <int LPT, int NV, bool SIGMOID, bool GRAD>
-__device__ __forceinline__ bool probabilities(float (&v)[4 * NV], float (&q)[4 * NV]) {
-  constexpr int N = 4 * NV;
+// As load_row, of a gradient that may be written over in place.
+template <int LPT, int NV>
+__device__ __forceinline__ void load_base(const float* row, int E, bool vec, bool live, int tl,
+                                          float (&v)[4 * NV]) {
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    const int c = col_of<LPT>(tl, 4 * j);
+    if (vec) {
+      float4 x{0.0f, 0.0f, 0.0f, 0.0f};
+      if (live && c < E) x = *reinterpret_cast<const float4*>(row + c);
+      v[4 * j] = x.x;
+      v[4 * j + 1] = x.y;
+      v[4 * j + 2] = x.z;
+      v[4 * j + 3] = x.w;
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[4 * j + i] = live && c + i < E ? row[c + i] : 0.0f;
+    }
+  }
+}
+
+// 1 / x to 1 ulp, 0 above 2^126.
+__device__ __forceinline__ float reciprocal(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
+// e^(v - the team's largest) in place of v, and their sum.
+template <int LPT, int N>
+__device__ __forceinline__ float exponentials(float (&v)[N], bool& infinite) {
   float m = -kInf;
-  bool bad = false;
+#pragma unroll
+  for (int i = 0; i < N; ++i) m = fmaxf(m, v[i]);  // a NaN is not taken, but comes up in the sum
+  m = team_max<LPT>(m);
+  infinite = m == kInf;
+  const float sub = m > -kInf ? m : 0.0f;
+  float z = 0.0f;
 #pragma unroll
   for (int i = 0; i < N; ++i) {
-    m = fmaxf(m, v[i]);  // a NaN is not taken: `bad` finds it
-    bad |= !(v[i] < kInf);
+    v[i] = __expf(v[i] - sub);
+    z += v[i];
   }
-  m = team_max<LPT>(m);
+  return team_sum<LPT>(z);
+}
+
+// Turns a team's logits v into v = p * z and, for the backward of sigmoids, q =
+// (see the top) * z, and returns 1 / z.  A logit of -inf is an expert that is
+// masked out: p = q = 0.  A row without any other is 0, and so is one with a NaN
+// or +inf, which returns `bad`.  exp is the fast one: its error, 2 + |x| ulp, falls
+// for the softmax on values that are e^x of the row's largest.  `again` loads v
+// once more, for a row (`live`) whose sigmoids are all far below 1: those are e^l
+// to 1e-9, and normalised from the row's largest they cannot vanish together.
+template <int LPT, int NV, bool SIGMOID, bool GRAD, typename F>
+__device__ __forceinline__ float probabilities(float (&v)[4 * NV], float (&q)[4 * NV], bool live,
+                                               bool& bad, F&& again) {
+  constexpr int N = 4 * NV;
   float z = 0.0f;
-  // sigmoids all far below 1 are e^l to 1e-13, and normalised from the row's
-  // largest they cannot vanish together
-  const bool scaled = !SIGMOID || m < -30.0f;
-  if (scaled) {
-    const float sub = m > -kInf ? m : 0.0f;
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-      v[i] = __expf(v[i] - sub);
-      if (GRAD) q[i] = v[i];
-      z += v[i];
-    }
+  if (!SIGMOID) {
+    z = exponentials<LPT>(v, bad);
   } else {
+    float m = -kInf;
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      const float e = __expf(-fabsf(v[i]));
-      const float r = __fdividef(1.0f, 1.0f + e);
-      const float s = v[i] >= 0.0f ? r : e * r;
-      if (GRAD) q[i] = s * (v[i] >= 0.0f ? e * r : r);
+      m = fmaxf(m, v[i]);
+      const float e = __expf(-v[i]), s = reciprocal(1.0f + e);
+      if (GRAD) q[i] = s * (fminf(e, 1e30f) * s);  // 1 - s = e s
       v[i] = s;
       z += s;
     }
-  }
-  z = team_sum<LPT>(z);
-  // the team's lanes agree: the sum is the same in each, and so is this vote
-  const unsigned votes = __ballot_sync(kFull, bad);
-  const int first = (threadIdx.x & 31) / LPT * LPT;
-  bad = (votes >> first) & (LPT == 32 ? kFull : (1u << (LPT & 31)) - 1u);
-  const float inv = z > 0.0f && !bad ? 1.0f / z : 0.0f;
+    z = team_sum<LPT>(z);
+    const unsigned votes = __ballot_sync(kFull, m == kInf);
+    const int first = (threadIdx.x & 31) / LPT * LPT;
+    bad = (votes >> first) & (LPT == 32 ? kFull : (1u << (LPT & 31)) - 1u);
+    const bool small = live && z < 1e-9f;
+    if (__any_sync(kFull, small)) {
+      float w[N];
+      bool none;
+      again(w);
+      const float zw = exponentials<LPT>(w, none);
+      if (small) {
+        z = zw;
 #pragma unroll
-  for (int i = 0; i < N; ++i) {
-    v[i] = bad ? 0.0f : v[i] * inv;
-    if (GRAD) q[i] = bad ? 0.0f : q[i] * inv;
+        for (int i = 0; i < N; ++i) {
+          v[i] = w[i];
+          if (GRAD) q[i] = w[i];
+        }
+      }
+    }
   }
-  return bad;
+  bad |= !(z < kInf);
+  if (bad) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      v[i] = 0.0f;
+      if (GRAD && SIGMOID) q[i] = 0.0f;
+    }
+  }
+  return z > 0.0f && !bad ? 1.0f / z : 0.0f;
 }
 
-// Sum over the block's threads, the same in each; `red` holds kWarps values.
+// Sum over the block's threads, the same in each; `red` holds 32 values.
 __device__ __forceinline__ float block_sum(float v, float* red) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
-  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
+  const int lane = threadIdx.x & 31;
+  if (lane == 0) red[threadIdx.x >> 5] = v;
   __syncthreads();
-  v = 0.0f;
-  for (int w = 0; w < static_cast<int>(blockDim.x >> 5); ++w) v += red[w];
+  v = lane < static_cast<int>(blockDim.x >> 5) ? red[lane] : 0.0f;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
   __syncthreads();
   return v;
 }
@@ -190,112 +249,132 @@ __device__ __forceinline__ float seq_factor(const BalArgs& a, int n) {
   return static_cast<float>(a.E) / (static_cast<float>(a.K) * n) / n;
 }
 
-// The loss from the sequences' parts, by one block.
-__device__ void finish(const BalArgs& a) {
-  __shared__ double sums[32];
-  __shared__ int full[32];
-  double sum = 0.0;
-  int n = 0;
-  for (int64_t i = threadIdx.x; i < static_cast<int64_t>(a.S) * a.chunks; i += blockDim.x)
-    sum += static_cast<double>(__ldcg(a.part + i));
+// Sequences of the table that are not empty, and before whose end token t lies (the
+// index of the first that ends behind it), by the whole block.  Each offset is
+// read once; those of a table of at most kOffBatch sequences stay in `soff`.
+struct Table {
+  int full, first;
+  bool wrong;
+};
+__device__ __forceinline__ Table read_table(const BalArgs& a, int t, int* soff, int* red) {
+  if (!a.off) {
+    if (threadIdx.x < 2) soff[threadIdx.x] = threadIdx.x ? a.T : 0;
+    __syncthreads();
+    return Table{a.T > 0, t < a.T ? 0 : 1, false};
+  }
+  int full = 0, first = 0, wrong = 0;
   for (int s = threadIdx.x; s < a.S; s += blockDim.x) {
-    const int2 r = seq_range(a, s);
-    n += r.y > r.x;
+    const int lo = __ldg(a.off + s), hi = __ldg(a.off + s + 1);
+    const int2 r = range_of(lo, hi, a.T);
+    full += r.y > r.x;
+    first += hi <= t;
+    wrong |= lo < 0 || hi < lo || hi > a.T;
+    if (a.S <= kOffBatch) {
+      soff[s] = lo;
+      if (s == a.S - 1) soff[a.S] = hi;
+    }
   }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    sum += __shfl_xor_sync(kFull, sum, o);
-    n += __shfl_xor_sync(kFull, n, o);
-  }
+  full = __reduce_add_sync(kFull, full);
+  first = __reduce_add_sync(kFull, first);
+  wrong = __reduce_or_sync(kFull, wrong);
+  const int warp = threadIdx.x >> 5;
   if ((threadIdx.x & 31) == 0) {
-    sums[threadIdx.x >> 5] = sum;
-    full[threadIdx.x >> 5] = n;
+    red[warp] = full;
+    red[32 + warp] = first;
+    red[64 + warp] = wrong;
   }
   __syncthreads();
-  if (threadIdx.x == 0) {
-    for (int w = 1; w < static_cast<int>(blockDim.x >> 5); ++w) {
-      sum += sums[w];
-      n += full[w];
+  const int lane = threadIdx.x & 31;
+  const bool mine = lane < static_cast<int>(blockDim.x >> 5);
+  full = __reduce_add_sync(kFull, mine ? red[lane] : 0);
+  first = __reduce_add_sync(kFull, mine ? red[32 + lane] : 0);
+  wrong = __reduce_or_sync(kFull, mine ? red[64 + lane] : 0);
+  __syncthreads();
+  return Table{full, first, wrong != 0};
+}
+
+// Tokens of a team whose logits it loads before it works on the first of them.
+template <int NV>
+constexpr int kBatch = NV < 3 ? 4 / NV : 1;
+
+// Counts a token's entries; the later repeats of an expert are dropped.
+__device__ __forceinline__ void count_token(const BalArgs& a, unsigned t, int* hist) {
+  const int32_t* from = a.idx + static_cast<size_t>(t) * a.K;
+  int seen[MOE_MAX_TOPK];
+#pragma unroll
+  for (int k = 0; k < MOE_MAX_TOPK; ++k) seen[k] = k < a.K ? __ldg(from + k) : -1;
+#pragma unroll
+  for (int k = 0; k < MOE_MAX_TOPK; ++k) {
+    if (k >= a.K) break;
+    const int e = seen[k];
+    if (e == -1) continue;
+    if (static_cast<unsigned>(e) >= static_cast<unsigned>(a.E)) {
+      raise_flag(a.flags, MOE_DEVERR_BAD_EXPERT);
+      continue;
     }
-    *a.loss = n > 0 ? static_cast<float>(a.coef * sum / n) : 0.0f;
+    bool again = false;
+#pragma unroll
+    for (int b = 0; b < k; ++b) again |= seen[b] == e;
+    if (again) raise_flag(a.flags, MOE_DEVERR_DUP_EXPERT);
+    else atomicAdd(hist + e, 1);
   }
 }
 
 // Fragments of a tile: sums of p and counts of its tokens [t0, t1) of each
 // sequence.
 template <int LPT, int NV, bool SIGMOID>
-__global__ void __launch_bounds__(kThreads) balance_tile_kernel(BalArgs a) {
+__global__ void __launch_bounds__(kThreads, 1) balance_tile_kernel(BalArgs a) {
   grid_dependency_wait();
-  constexpr int N = 4 * NV, TPW = 32 / LPT;
+  constexpr int N = 4 * NV, TPW = 32 / LPT, U = kBatch<NV>;
   extern __shared__ float dyn[];
   float* stage = dyn;                                        // [kWarps][E]
   int* hist = reinterpret_cast<int*>(dyn + kWarps * a.E);    // [E]
   __shared__ int soff[kOffBatch + 1];
-  __shared__ float red[kWarps];
+  __shared__ int ired[96];
+  __shared__ float red[32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int team = lane / LPT, tl = lane % LPT;
-  if (blockIdx.x == 0 && threadIdx.x == 0) *a.ticket = 0;
-  if (a.off || a.T == 0) {  // empty sequences, and the offsets themselves
-    bool wrong = false;
-    const int W = gridDim.x * kWarps;
-    for (int s = blockIdx.x * kWarps + warp; s < a.S; s += W) {
-      const int lo = a.off ? __ldg(a.off + s) : 0, hi = a.off ? __ldg(a.off + s + 1) : 0;
-      wrong |= lo < 0 || hi < lo || hi > a.T;
-      const int2 r = range_of(lo, hi, a.T);
+  const int t0 = static_cast<int>(min(static_cast<int64_t>(blockIdx.x) * a.tile,
+                                      static_cast<int64_t>(a.T)));
+  const int t1 = static_cast<int>(min(static_cast<int64_t>(t0) + a.tile, static_cast<int64_t>(a.T)));
+  for (int e = threadIdx.x; e < a.E; e += kThreads) hist[e] = 0;
+  const Table table = read_table(a, t0, soff, ired);
+  const bool whole_table = a.S <= kOffBatch;
+  if (table.full < a.S) {  // empty sequences
+    for (int s = blockIdx.x * kWarps + warp; s < a.S; s += gridDim.x * kWarps) {
+      const int2 r = seq_range(a, s);
       if (r.y > r.x) continue;
       const size_t row = static_cast<size_t>(s) * a.E;
       for (int e = lane; e < a.E; e += 32) {
         a.cnt[row + e] = 0;
         if (a.prob) a.prob[row + e] = 0.0f;
       }
-      if (lane < a.chunks) a.part[static_cast<size_t>(s) * a.chunks + lane] = 0.0f;
     }
-    if (wrong) raise_flag(a.flags, MOE_DEVERR_BAD_LAYOUT);
   }
-  const int t0 = static_cast<int>(min(static_cast<int64_t>(blockIdx.x) * a.tile,
-                                      static_cast<int64_t>(a.T)));
-  const int t1 = static_cast<int>(min(static_cast<int64_t>(t0) + a.tile, static_cast<int64_t>(a.T)));
-  for (int e = threadIdx.x; e < a.E; e += kThreads) hist[e] = 0;
-  const int s0 = seq_of(a, t0);
+  if (blockIdx.x == 0 && threadIdx.x == 0 && table.wrong) raise_flag(a.flags, MOE_DEVERR_BAD_LAYOUT);
+  float loss = 0.0f;
+  int tail = -1;
   bool more = true;
-  for (int sb = s0; more && sb < a.S; sb += kOffBatch) {
+  for (int sb = table.first; more && sb < a.S; sb += kOffBatch) {
     const int ns = min(kOffBatch, a.S - sb);
-    __syncthreads();
-    for (int i = threadIdx.x; i <= ns; i += kThreads)
-      soff[i] = a.off ? __ldg(a.off + sb + i) : (i == 0 ? 0 : a.T);
-    __syncthreads();
+    const int* offs = soff + sb;
+    if (!whole_table) {
+      __syncthreads();
+      for (int i = threadIdx.x; i <= ns; i += kThreads) soff[i] = __ldg(a.off + sb + i);
+      __syncthreads();
+      offs = soff;
+    }
     for (int i = 0; i < ns; ++i) {
       const int s = sb + i;
-      const int2 r = range_of(soff[i], soff[i + 1], a.T);
-      if (soff[i] >= t1) {
+      const int2 r = range_of(offs[i], offs[i + 1], a.T);
+      if (offs[i] >= t1) {
         more = false;
         break;
       }
       const int f0 = max(r.x, t0), f1 = min(r.y, t1);
       if (f0 >= f1) continue;
-      // counts: a thread a token, whose later repeats of an expert are dropped
-      for (unsigned t = f0 + threadIdx.x; t < static_cast<unsigned>(f1); t += kThreads) {
-        const int32_t* entries = a.idx + static_cast<size_t>(t) * a.K;
-        int seen[MOE_MAX_TOPK];
-#pragma unroll
-        for (int k = 0; k < MOE_MAX_TOPK; ++k) {
-          if (k >= a.K) break;
-          const int e = __ldg(entries + k);
-          seen[k] = e;
-          if (e == -1) continue;
-          if (static_cast<unsigned>(e) >= static_cast<unsigned>(a.E)) {
-            raise_flag(a.flags, MOE_DEVERR_BAD_EXPERT);
-            continue;
-          }
-          bool again = false;
-#pragma unroll
-          for (int b = 0; b < k; ++b) again |= seen[b] == e;
-          if (again) raise_flag(a.flags, MOE_DEVERR_DUP_EXPERT);
-          else atomicAdd(hist + e, 1);
-        }
-      }
       // sums of p
-      float acc[N], v[N], unused[N];
+      float acc[N], unused[N];
 #pragma unroll
       for (int k = 0; k < N; ++k) acc[k] = 0.0f;
       bool begun = false;
@@ -315,20 +394,40 @@ __global__ void __launch_bounds__(kThreads) balance_tile_kernel(BalArgs a) {
         begun = true;
         held = 0;
       };
-      for (unsigned t = f0 + warp * TPW; t < static_cast<unsigned>(f1); t += kWarps * TPW) {
-        const bool live = t + team < static_cast<unsigned>(f1);
-        load_row<LPT, NV, float4>(a.logits + static_cast<size_t>(live ? t + team : t) * a.E, a.E,
-                                  a.vec, live, tl, -kInf, v);
-        if (probabilities<LPT, NV, SIGMOID, false>(v, unused) && tl == 0)
-          raise_flag(a.flags, MOE_DEVERR_NONFINITE);
+      const unsigned last = f1;
+      // a thread a token, from the last warp on: the first ones have more logits
+      for (unsigned t = f0 + (kThreads - 1 - threadIdx.x); t < last; t += kThreads)
+        count_token(a, t, hist);
+      constexpr unsigned kStep = kWarps * TPW;
+      for (unsigned base = f0 + warp * TPW; base < last; base += U * kStep) {
+        const unsigned t = base + team;
+        float v[U][N];
+        auto load = [&](int u, float (&to)[N]) {
+          const bool live = t + u * kStep < last;
+          load_row<LPT, NV, float4>(a.logits + static_cast<size_t>(live ? t + u * kStep : f0) * a.E,
+                                    a.E, a.vec, live, tl, -kInf, to);
+          return live;
+        };
+        bool live[U];
 #pragma unroll
-        for (int k = 0; k < N; ++k) acc[k] += v[k];
-        if (++held == kFlush) flush();
+        for (int u = 0; u < U; ++u) live[u] = load(u, v[u]);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          bool bad;
+          const float inv = probabilities<LPT, NV, SIGMOID, false>(
+              v[u], unused, live[u], bad, [&](float (&to)[N]) { load(u, to); });
+          if (bad && tl == 0) raise_flag(a.flags, MOE_DEVERR_NONFINITE);
+#pragma unroll
+          for (int k = 0; k < N; ++k) acc[k] = fmaf(v[u][k], inv, acc[k]);
+        }
+        held += U;
+        if (held >= kFlush) flush();
       }
       flush();
       __syncthreads();
       const bool whole = r.x >= t0 && r.y <= t1;
       const int slot = 2 * blockIdx.x + (r.x >= t0);
+      if (!whole && r.x >= t0) tail = s;
       float val = 0.0f;
       for (int e = threadIdx.x; e < a.E; e += kThreads) {
         float p = 0.0f;
@@ -347,164 +446,226 @@ __global__ void __launch_bounds__(kThreads) balance_tile_kernel(BalArgs a) {
           a.slot_c[at] = c;
         }
       }
-      if (whole) {
-        val = block_sum(val, red) * seq_factor(a, r.y - r.x);
-        if (threadIdx.x < a.chunks)
-          a.part[static_cast<size_t>(s) * a.chunks + threadIdx.x] = threadIdx.x == 0 ? val : 0.0f;
-      } else {
-        __syncthreads();  // stage and hist are taken up again
-      }
+      // (a barrier, too: stage and hist are taken up again)
+      val = block_sum(val, red);
+      if (whole) loss = fmaf(val, seq_factor(a, r.y - r.x), loss);
     }
   }
-  if (gridDim.x == 1) {  // every sequence is whole: the loss in the same launch
-    __syncthreads();
-    finish(a);
+  if (threadIdx.x == 0) {
+    if (gridDim.x == 1) {  // every sequence is whole: the loss in the same launch
+      *a.loss = table.full > 0 ? a.coef * loss / table.full : 0.0f;
+    } else {
+      a.tile_loss[blockIdx.x] = loss;
+      a.tail[blockIdx.x] = tail;
+    }
   }
 }
 
-// Sequences that span tiles: block (x, y) adds up the slots of one of them for
-// kJoinCols experts, a warp for every blockDim / 32-th slot; the last block to
-// end adds up the loss.
-__global__ void __launch_bounds__(1024) balance_join_kernel(BalArgs a) {
+// Sequences that span tiles.  A unit is 32 experts of one of them: `share` warps
+// of a block add up its slots.  Units go round the cluster's blocks; block 0 adds
+// up the loss.
+__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kJoinWarps * 32)
+    balance_join_kernel(BalArgs a, int items, int share) {
   grid_dependency_wait();
-  __shared__ float ps[32][kJoinCols];
-  __shared__ int cs[32][kJoinCols];
-  __shared__ bool last;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
-  // item x is sequence x, or where there are more sequences than tiles the one
-  // that goes on from tile x into the next
-  int s = blockIdx.x;
-  if (a.S > a.tiles) {
-    const int64_t next = (static_cast<int64_t>(blockIdx.x) + 1) * a.tile;
-    s = next < a.T ? seq_of(a, static_cast<int>(next)) : a.S;
-  }
-  if (s < a.S) {
-    const int2 r = seq_range(a, s);
-    const int b0 = r.x / a.tile, b1 = (r.y - 1) / a.tile;
-    if (r.y > r.x && b1 > b0 && (a.S <= a.tiles || b0 == static_cast<int>(blockIdx.x))) {
-      const int e = blockIdx.y * kJoinCols + lane;
-      float p = 0.0f;
-      int c = 0;
-      if (e < a.E)
-#pragma unroll 4
-        for (int b = b0 + warp; b <= b1; b += warps) {
-          const size_t at = static_cast<size_t>(2 * b + (b == b0)) * a.E + e;
-          p += __ldcg(a.slot_p + at);
-          c += __ldcg(a.slot_c + at);
-        }
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  __shared__ float ps[kJoinWarps][32];
+  __shared__ int cs[kJoinWarps][32];
+  __shared__ int soff[kOffBatch + 1];
+  __shared__ int ired[96];
+  __shared__ float losses[kJoinWarps], block_loss[kCluster];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int rank = blockIdx.x;  // in the one cluster
+  // the tiles' own losses are on their way meanwhile
+  float loss = 0.0f;
+  if (rank == 0)
+    for (int b = threadIdx.x; b < a.tiles; b += kJoinWarps * 32) loss += __ldcg(a.tile_loss + b);
+  const Table table = read_table(a, 0, soff, ired);
+  const int groups = kJoinWarps / share;  // units of a block at a time
+  const int units = items * a.chunks;
+  for (int n0 = rank * groups; n0 < units; n0 += kCluster * groups) {
+    const int n = n0 + warp / share;
+    int s = a.S, chunk = 0;
+    if (n < units) {
+      chunk = n % a.chunks;
+      s = n / a.chunks;
+      // where there are more sequences than tiles: that which goes on from a tile
+      if (a.S > a.tiles) s = __ldcg(a.tail + s);
+      if (s < 0) s = a.S;
+    }
+    int2 r = make_int2(0, 0);
+    if (s < a.S)
+      r = a.S <= kOffBatch ? range_of(soff[s], soff[s + 1], a.T) : seq_range(a, s);
+    const int b0 = r.x / a.tile, b1 = r.y > r.x ? (r.y - 1) / a.tile : b0;
+    const int e = chunk * 32 + lane;
+    const bool real = b1 > b0 && e < a.E;
+    float p = 0.0f;
+    int c = 0;
+    for (int b = b0 + warp % share; b <= b1 && real; b += kSlots * share) {
+      float x[kSlots];
+      int y[kSlots];
+#pragma unroll
+      for (int i = 0; i < kSlots; ++i) {  // all on their way together
+        const int bi = b + i * share;
+        const size_t at = static_cast<size_t>(2 * bi + (bi == b0)) * a.E + e;
+        x[i] = bi <= b1 ? __ldcg(a.slot_p + at) : 0.0f;
+        y[i] = bi <= b1 ? __ldcg(a.slot_c + at) : 0;
+      }
+#pragma unroll
+      for (int i = 0; i < kSlots; ++i) {
+        p += x[i];
+        c += y[i];
+      }
+    }
+    if (share > 1) {
+      __syncthreads();
       ps[warp][lane] = p;
       cs[warp][lane] = c;
       __syncthreads();
-      if (warp == 0) {
-        for (int w = 1; w < warps; ++w) {
-          p += ps[w][lane];
-          c += cs[w][lane];
+      if (warp % share == 0) {
+#pragma unroll 4
+        for (int w = 1; w < share; ++w) {
+          p += ps[warp + w][lane];
+          c += cs[warp + w][lane];
         }
-        float val = 0.0f;
-        if (e < a.E) {
-          const size_t at = static_cast<size_t>(s) * a.E + e;
-          a.cnt[at] = c;
-          if (a.prob) a.prob[at] = p / (r.y - r.x);
-          val = static_cast<float>(c) * p;
-        }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) val += __shfl_xor_sync(kFull, val, o);
-        if (lane == 0)
-          a.part[static_cast<size_t>(s) * a.chunks + blockIdx.y] = val * seq_factor(a, r.y - r.x);
       }
     }
+    if (real && warp % share == 0) {
+      const int n_tokens = r.y - r.x;
+      const size_t at = static_cast<size_t>(s) * a.E + e;
+      a.cnt[at] = c;
+      if (a.prob) a.prob[at] = p / n_tokens;
+      loss = fmaf(static_cast<float>(c) * p, seq_factor(a, n_tokens), loss);
+    }
   }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) loss += __shfl_xor_sync(kFull, loss, o);
+  if (lane == 0) losses[warp] = loss;
   __syncthreads();
+  if (warp == 0) {
+    loss = losses[lane];
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) loss += __shfl_xor_sync(kFull, loss, o);
+  }
+  // block 0 runs by now
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
   if (threadIdx.x == 0) {
-    __threadfence();
-    last = atomicAdd(a.ticket, 1u) == gridDim.x * gridDim.y - 1;
-    __threadfence();
+    uint32_t to;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(to) : "r"(smem_addr(block_loss + rank)));
+    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(to), "f"(loss) : "memory");
   }
-  __syncthreads();
-  if (last) finish(a);
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
+                   : "memory");
+  if (rank == 0 && threadIdx.x == 0) {
+    loss = 0.0f;
+#pragma unroll
+    for (int b = 0; b < kCluster; ++b) loss += block_loss[b];
+    *a.loss = table.full > 0 ? a.coef * loss / table.full : 0.0f;
+  }
 }
 
 // Backward: a team of lanes a token, a warp's tokens in a row.
 template <int LPT, int NV, bool SIGMOID>
-__global__ void __launch_bounds__(kThreads) balance_bwd_kernel(BalArgs a) {
-  constexpr int N = 4 * NV, TPW = 32 / LPT;
-  __shared__ int counts[kWarps];
+__global__ void __launch_bounds__(kBwdWarps * 32, 3) balance_bwd_kernel(BalArgs a) {
+  constexpr int N = 4 * NV, TPW = 32 / LPT, U = NV < 3 ? 2 : 1;
+  __shared__ int soff[kOffBatch + 1];
+  __shared__ int ired[96];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int team = lane / LPT, tl = lane % LPT;
-  int full = a.T > 0;
-  if (a.off) {  // sequences that are not empty
-    full = 0;
-    for (int s = threadIdx.x; s < a.S; s += kThreads) {
-      const int2 r = seq_range(a, s);
-      full += r.y > r.x;
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) full += __shfl_xor_sync(kFull, full, o);
-    if (lane == 0) counts[warp] = full;
-    __syncthreads();
-    full = 0;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) full += counts[w];
-  }
-  const float g = a.coef * (a.gloss ? __ldg(a.gloss) : 1.0f) / max(full, 1);
   int lo = 0, hi = a.T;  // tokens of any sequence
   if (a.off) {
     const int2 r = range_of(__ldg(a.off), __ldg(a.off + a.S), a.T);
     lo = r.x;
     hi = r.y;
   }
+  float g = a.gloss ? __ldg(a.gloss) : 1.0f;
+  const Table table = read_table(a, 0, soff, ired);
+  g *= a.coef / max(table.full, 1);
   const int64_t passes = (static_cast<int64_t>(hi) - lo + TPW - 1) / TPW;
-  const int64_t W = static_cast<int64_t>(gridDim.x) * kWarps;
+  const int64_t W = static_cast<int64_t>(gridDim.x) * kBwdWarps;
   const int64_t per = (passes + W - 1) / W;
-  const int64_t w0 = (static_cast<int64_t>(blockIdx.x) * kWarps + warp) * per;
+  const int64_t w0 = (static_cast<int64_t>(blockIdx.x) * kBwdWarps + warp) * per;
   const int64_t begin = lo + w0 * TPW, end = min(static_cast<int64_t>(hi), begin + per * TPW);
   if (begin >= end) return;
-  int s = -1;
   int2 r = make_int2(0, 0);
   float d[N], factor = 0.0f;  // counts less their mean; the sequence's factor
-  for (int64_t tt = begin; tt < end; tt += TPW) {
-    const int t = static_cast<int>(min(tt + team, end - 1));
-    const bool live = tt + team < end;
-    float v[N], q[N];
-    const size_t at = static_cast<size_t>(t) * a.E;
-    load_row<LPT, NV, float4>(a.logits + at, a.E, a.vec, live, tl, -kInf, v);
-    if (s < 0 || t >= r.y) {
+  // the sequence of token t, for tokens in order
+  auto enter = [&](int t) {
+    int s;
+    if (a.off && a.S <= kOffBatch) {
+      int x = 0, y = a.S;
+      while (x < y) {
+        const int mid = (x + y) >> 1;
+        if (soff[mid + 1] > t) y = mid;
+        else x = mid + 1;
+      }
+      s = min(x, a.S - 1);
+      r = range_of(soff[s], soff[s + 1], a.T);
+    } else {
       s = min(seq_of(a, t), a.S - 1);
       r = seq_range(a, s);
-      int c[N];
-      load_row<LPT, NV, int4>(a.bcnt + static_cast<size_t>(s) * a.E, a.E, a.vec, true, tl, 0, c);
-      const int n = r.y - r.x;
-      const int mean = static_cast<int>(static_cast<int64_t>(a.K) * n / a.E);
-#pragma unroll
-      for (int i = 0; i < N; ++i) d[i] = static_cast<float>(c[i] - mean);
-      factor = n > 0 ? g * seq_factor(a, n) : 0.0f;
     }
-    __syncwarp();
-    if (probabilities<LPT, NV, SIGMOID, true>(v, q) && tl == 0)
-      raise_flag(a.flags, MOE_DEVERR_NONFINITE);
-    float dot = 0.0f;
+    int c[N];
+    load_row<LPT, NV, int4>(a.bcnt + static_cast<size_t>(s) * a.E, a.E, a.vec, true, tl, 0, c);
+    const int n = r.y - r.x;
+    const int mean = static_cast<int>(static_cast<int64_t>(a.K) * n / a.E);
 #pragma unroll
-    for (int i = 0; i < N; ++i) dot = fmaf(v[i], d[i], dot);
-    dot = team_sum<LPT>(dot);
-    if (!live) continue;
+    for (int i = 0; i < N; ++i) d[i] = static_cast<float>(c[i] - mean);
+    factor = n > 0 ? g * seq_factor(a, n) : 0.0f;
+  };
+  bool entered = false;
+  for (int64_t tt = begin; tt < end; tt += U * TPW) {
+    float v[U][N], base[U][N], q[N];
 #pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      const int c = col_of<LPT>(tl, 4 * j);
-      if (a.vec) {
-        if (c >= a.E) continue;
-        float4 o{0.0f, 0.0f, 0.0f, 0.0f};
-        if (a.base) o = *reinterpret_cast<const float4*>(a.base + at + c);
-        o.x = fmaf(factor * q[4 * j], d[4 * j] - dot, o.x);
-        o.y = fmaf(factor * q[4 * j + 1], d[4 * j + 1] - dot, o.y);
-        o.z = fmaf(factor * q[4 * j + 2], d[4 * j + 2] - dot, o.z);
-        o.w = fmaf(factor * q[4 * j + 3], d[4 * j + 3] - dot, o.w);
-        *reinterpret_cast<float4*>(a.glogits + at + c) = o;
+    for (int u = 0; u < U; ++u) {
+      const int64_t t = tt + u * TPW + team;
+      const int64_t at = (t < end ? t : begin) * a.E;
+      load_row<LPT, NV, float4>(a.logits + at, a.E, a.vec, t < end, tl, -kInf, v[u]);
+      if (a.base) {
+        load_base<LPT, NV>(a.base + at, a.E, a.vec, t < end, tl, base[u]);
       } else {
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if (c + i < a.E)
-            a.glogits[at + c + i] = fmaf(factor * q[4 * j + i], d[4 * j + i] - dot,
-                                         a.base ? a.base[at + c + i] : 0.0f);
+        for (int i = 0; i < N; ++i) base[u][i] = 0.0f;
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int64_t t64 = tt + u * TPW + team;
+      const bool live = t64 < end;
+      const int t = static_cast<int>(t64);
+      if (live && (!entered || t >= r.y)) {
+        enter(t);
+        entered = true;
+      }
+      __syncwarp();
+      bool bad;
+      const float inv = probabilities<LPT, NV, SIGMOID, true>(
+          v[u], q, live, bad, [&](float (&to)[N]) {
+            load_row<LPT, NV, float4>(a.logits + (live ? t64 : begin) * a.E, a.E, a.vec, live, tl,
+                                      -kInf, to);
+          });
+      if (bad && tl == 0) raise_flag(a.flags, MOE_DEVERR_NONFINITE);
+      float dot = 0.0f;
+#pragma unroll
+      for (int i = 0; i < N; ++i) dot = fmaf(v[u][i], live ? d[i] : 0.0f, dot);
+      dot = team_sum<LPT>(dot) * inv;
+      const float scale = factor * inv;
+      if (!live) continue;
+      const size_t at = static_cast<size_t>(t) * a.E;
+#pragma unroll
+      for (int i = 0; i < N; ++i)
+        base[u][i] = fmaf(scale * (SIGMOID ? q[i] : v[u][i]), d[i] - dot, base[u][i]);
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        const int c = col_of<LPT>(tl, 4 * j);
+        const float* o = base[u] + 4 * j;
+        if (a.vec) {
+          if (c < a.E)
+            *reinterpret_cast<float4*>(a.glogits + at + c) = make_float4(o[0], o[1], o[2], o[3]);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (c + i < a.E) a.glogits[at + c + i] = o[i];
+        }
       }
     }
   }
@@ -538,7 +699,7 @@ BalArgs bal_args(const moe_handle* h, const float* logits, int T, const int32_t*
   a.E = h->cfg.num_experts;
   a.K = h->cfg.top_k;
   a.S = S;
-  a.chunks = (a.E + kJoinCols - 1) / kJoinCols;
+  a.chunks = (a.E + 31) / 32;
   a.coef = static_cast<float>(coef);
   a.flags = h->flags;
   return a;
@@ -546,7 +707,25 @@ BalArgs bal_args(const moe_handle* h, const float* logits, int T, const int32_t*
 
 }  // namespace
 
-BalancePlan balance_plan(int E, int S) {
+// The tile kernels take more shared memory than the default: once for a device.
+cudaError_t prepare_balance_kernels() {
+  cudaError_t e = cudaSuccess;
+  for (int E : {8, 16, 32, 64, 128, 256, 384, 512}) {
+    if (e != cudaSuccess) return e;
+    const int bytes = (kWarps + 1) * E * static_cast<int>(sizeof(float));
+    e = with_team(E, [&](auto lanes, auto vecs) {
+      cudaError_t r = cudaFuncSetAttribute(balance_tile_kernel<lanes(), vecs(), false>,
+                                           cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+      if (r == cudaSuccess)
+        r = cudaFuncSetAttribute(balance_tile_kernel<lanes(), vecs(), true>,
+                                 cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+      return r;
+    });
+  }
+  return e;
+}
+
+BalancePlan balance_plan(int E) {
   BalancePlan p{};
   size_t o = 0;
   auto take = [&](size_t bytes) {
@@ -554,10 +733,10 @@ BalancePlan balance_plan(int E, int S) {
     o = (o + bytes + 255) / 256 * 256;
     return at;
   };
-  p.ticket = take(sizeof(unsigned));
   p.slot_p = take(static_cast<size_t>(2 * kMaxTiles) * E * sizeof(float));
   p.slot_c = take(static_cast<size_t>(2 * kMaxTiles) * E * sizeof(int32_t));
-  p.part = take(static_cast<size_t>(S) * ((E + kJoinCols - 1) / kJoinCols) * sizeof(float));
+  p.tile_loss = take(kMaxTiles * sizeof(float));
+  p.tail = take(kMaxTiles * sizeof(int32_t));
   p.total = o;
   return p;
 }
@@ -566,21 +745,21 @@ cudaError_t launch_balance(const moe_handle* h, const float* logits, const int32
                            const int32_t* off, int S, double coef, float* loss, int32_t* cnt,
                            float* prob, void* workspace, cudaStream_t s) {
   BalArgs a = bal_args(h, logits, T, off, S, coef);
-  const BalancePlan p = balance_plan(a.E, S);
+  const BalancePlan p = balance_plan(a.E);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   a.idx = idx;
   a.loss = loss;
   a.cnt = cnt;
   a.prob = prob;
-  a.ticket = reinterpret_cast<unsigned*>(ws + p.ticket);
   a.slot_p = reinterpret_cast<float*>(ws + p.slot_p);
   a.slot_c = reinterpret_cast<int32_t*>(ws + p.slot_c);
-  a.part = reinterpret_cast<float*>(ws + p.part);
+  a.tile_loss = reinterpret_cast<float*>(ws + p.tile_loss);
+  a.tail = reinterpret_cast<int32_t*>(ws + p.tail);
   a.vec = rows_vec(a.E, logits);
-  // tiles of at least 8 tokens, four to an SM at most; one, and with it one
+  // tiles of at least 32 tokens, one to an SM at most; one, and with it one
   // launch, where a block reads all of the logits in about a launch's time
-  int tiles = 4 * h->num_sms < kMaxTiles ? 4 * h->num_sms : kMaxTiles;
-  if ((T + 7) / 8 < tiles) tiles = (T + 7) / 8;
+  int tiles = h->num_sms < kMaxTiles ? h->num_sms : kMaxTiles;
+  if ((T + 31) / 32 < tiles) tiles = (T + 31) / 32;
   if (static_cast<int64_t>(T) * a.E <= 16384) tiles = 1;
   if (tiles < 1) tiles = 1;
   a.tile = T > 0 ? (T + tiles - 1) / tiles : 1;
@@ -594,10 +773,10 @@ cudaError_t launch_balance(const moe_handle* h, const float* logits, const int32
   });
   if (e != cudaSuccess || a.tiles == 1) return e;
   const int items = S < a.tiles ? S : a.tiles;
-  int warps = 1;
-  while (warps < 32 && warps * items < a.tiles) warps *= 2;
-  return launch_chained(balance_join_kernel, dim3(items, a.chunks), dim3(32 * warps), 0, s, false,
-                        a);
+  int share = 1;  // warps of a unit: each loads its slots at once, as most sequences have them
+  while (share < kJoinWarps && share * kSlots * items < a.tiles) share *= 2;
+  return launch_chained(balance_join_kernel, dim3(kCluster), dim3(32 * kJoinWarps), 0, s, false, a,
+                        items, share);
 }
 
 cudaError_t launch_balance_bwd(const moe_handle* h, const float* logits, const int32_t* cnt, int T,
@@ -616,9 +795,9 @@ cudaError_t launch_balance_bwd(const moe_handle* h, const float* logits, const i
     constexpr int TPW = 32 / lanes();
     auto k = sigmoid ? balance_bwd_kernel<lanes(), vecs(), true>
                      : balance_bwd_kernel<lanes(), vecs(), false>;
-    const int64_t blocks = (static_cast<int64_t>(T) + kWarps * TPW - 1) / (kWarps * TPW);
-    const int64_t most = 8LL * h->num_sms;
-    k<<<static_cast<unsigned>(blocks < most ? blocks : most), kThreads, 0, s>>>(a);
+    const int64_t blocks = (static_cast<int64_t>(T) + kBwdWarps * TPW - 1) / (kBwdWarps * TPW);
+    const int64_t most = 3LL * h->num_sms;
+    k<<<static_cast<unsigned>(blocks < most ? blocks : most), kBwdWarps * 32, 0, s>>>(a);
     return cudaGetLastError();
   });
 }

@@ -118,12 +118,13 @@ cudaError_t prepare_layer_kernels();
 cudaError_t launch_layer(const moe_handle* h, const moe_layer_args& q, int T, void* workspace,
                          cudaStream_t s);
 
-// Workspace of the balance loss: byte offsets of the last block's ticket, the
-// fragments' sums and counts and the sequences' parts of the loss.
+// Workspace of the balance loss: byte offsets of the fragments' sums and counts,
+// the tiles' losses and the sequences that go on from them.
 struct BalancePlan {
-  size_t ticket, slot_p, slot_c, part, total;
+  size_t slot_p, slot_c, tile_loss, tail, total;
 };
-BalancePlan balance_plan(int E, int S);
+BalancePlan balance_plan(int E);
+cudaError_t prepare_balance_kernels();
 cudaError_t launch_balance(const moe_handle* h, const float* logits, const int32_t* idx, int T,
                            const int32_t* off, int S, double coef, float* loss, int32_t* cnt,
                            float* prob, void* workspace, cudaStream_t s);

@@ -145,7 +145,7 @@ def test_sizes_and_null_handles_are_refused_without_a_gpu():
     L = moe.lib()
     cfg = moe.make_config(64, 4, 1, 128)
     small, large = (moe.moe_balance_workspace_bytes(cfg, S) for S in (1, 1000))
-    assert 0 < small < large
+    assert 0 < small <= large
     assert moe.moe_balance_workspace_bytes(cfg, 0) == 0
     assert moe.moe_balance_workspace_bytes(moe.make_config(600, 4, 1, 128), 1) == 0
     assert L.moe_block_norm_workspace_bytes(None, 4, 64, 1) == 0
