@@ -38,7 +38,7 @@ constexpr int kBwdWarps = 8;     // of a block of the backward
 constexpr int kOffBatch = 1024;  // sequence offsets staged at a time
 constexpr int kJoinWarps = 32;   // of a block of the second kernel
 constexpr int kCluster = 8;      // blocks of the second kernel
-constexpr int kSlots = 6;        // slots that one of its warps loads at a time
+constexpr int kSlots = 12;       // slots that one of its warps loads at a time
 // Tokens a team sums in registers before it adds them to shared memory: bounds
 // the number of fp32 additions in a row however long a tile is.
 constexpr int kFlush = 64;
@@ -293,6 +293,18 @@ __device__ __forceinline__ Table read_table(const BalArgs& a, int t, int* soff, 
   return Table{full, first, wrong != 0};
 }
 
+constexpr int64_t kAhead = 128 * 1024;
+// Pulls the n bytes from p on into L2, but for what the ends share a 16-byte line
+// with: a hint that nothing waits for.
+__device__ __forceinline__ void prefetch_l2(const void* p, int64_t n) {
+  const uint64_t from = (reinterpret_cast<uint64_t>(p) + 15) & ~uint64_t{15};
+  const uint64_t to = (reinterpret_cast<uint64_t>(p) + n) & ~uint64_t{15};
+  if (to > from)
+    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(from),
+                 "r"(static_cast<uint32_t>(to - from))
+                 : "memory");
+}
+
 // Tokens of a team whose logits it loads before it works on the first of them.
 template <int NV>
 constexpr int kBatch = NV < 3 ? 4 / NV : 1;
@@ -324,6 +336,16 @@ __device__ __forceinline__ void count_token(const BalArgs& a, unsigned t, int* h
 // sequence.
 template <int LPT, int NV, bool SIGMOID>
 __global__ void __launch_bounds__(kThreads, 1) balance_tile_kernel(BalArgs a) {
+  // the tile's first logits and routes come into L2 while the kernel in front
+  // ends and the offsets are read
+  if (threadIdx.x == 0) {
+    const int64_t t = static_cast<int64_t>(blockIdx.x) * a.tile;
+    const int64_t n = min(static_cast<int64_t>(a.tile), static_cast<int64_t>(a.T) - t);
+    if (n > 0) {
+      prefetch_l2(a.logits + t * a.E, min(n * a.E * 4, kAhead));
+      prefetch_l2(a.idx + t * a.K, min(n * a.K * 4, kAhead));
+    }
+  }
   grid_dependency_wait();
   constexpr int N = 4 * NV, TPW = 32 / LPT, U = kBatch<NV>;
   extern __shared__ float dyn[];
@@ -773,8 +795,10 @@ cudaError_t launch_balance(const moe_handle* h, const float* logits, const int32
   });
   if (e != cudaSuccess || a.tiles == 1) return e;
   const int items = S < a.tiles ? S : a.tiles;
-  int share = 1;  // warps of a unit: each loads its slots at once, as most sequences have them
-  while (share < kJoinWarps && share * kSlots * items < a.tiles) share *= 2;
+  int share = 1;  // warps of a unit: all units in one round where they fit
+  while (share < kJoinWarps && 2 * share * items * a.chunks <= kCluster * kJoinWarps &&
+         share * kSlots * items < a.tiles)
+    share *= 2;
   return launch_chained(balance_join_kernel, dim3(kCluster), dim3(32 * kJoinWarps), 0, s, false, a,
                         items, share);
 }
