@@ -34,6 +34,8 @@ constexpr unsigned kFull = 0xffffffffu;
 constexpr int kWarps = 32;       // of a tile's block: one an SM
 constexpr int kThreads = kWarps * 32;
 constexpr int kMaxTiles = 256;
+constexpr int kFrags = 16;       // fragments that a tile works on at a time
+constexpr int kRows = kWarps + kFrags - 1;  // rows of sums: warp w's of fragment f is w + f
 constexpr int kBwdWarps = 8;     // of a block of the backward
 constexpr int kOffBatch = 1024;  // sequence offsets staged at a time
 constexpr int kJoinWarps = 32;   // of a block of the second kernel
@@ -150,6 +152,12 @@ __device__ __forceinline__ void load_base(const float* row, int E, bool vec, boo
   }
 }
 
+// e^x, 0 below 2^-126: the fast exponential without its subnormal results.
+__device__ __forceinline__ float exp_fast(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x * 1.4426950408889634f));
+  return r;
+}
 // 1 / x to 1 ulp, 0 above 2^126.
 __device__ __forceinline__ float reciprocal(float x) {
   float r;
@@ -169,7 +177,7 @@ __device__ __forceinline__ float exponentials(float (&v)[N], bool& infinite) {
   float z = 0.0f;
 #pragma unroll
   for (int i = 0; i < N; ++i) {
-    v[i] = __expf(v[i] - sub);
+    v[i] = exp_fast(v[i] - sub);
     z += v[i];
   }
   return team_sum<LPT>(z);
@@ -194,7 +202,7 @@ __device__ __forceinline__ float probabilities(float (&v)[4 * NV], float (&q)[4 
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       m = fmaxf(m, v[i]);
-      const float e = __expf(-v[i]), s = reciprocal(1.0f + e);
+      const float e = exp_fast(-v[i]), s = reciprocal(1.0f + e);
       if (GRAD) q[i] = s * (fminf(e, 1e30f) * s);  // 1 - s = e s
       v[i] = s;
       z += s;
@@ -332,8 +340,58 @@ __device__ __forceinline__ void count_token(const BalArgs& a, unsigned t, int* h
   }
 }
 
-// Fragments of a tile: sums of p and counts of its tokens [t0, t1) of each
-// sequence.
+// Fragments of a tile that are worked on together, in the order of their tokens.
+struct Fragments {
+  int n;                 // how many
+  int seq[kFrags], begin[kFrags], end[kFrags];
+  int length[kFrags];    // of the sequence
+  int kind[kFrags];      // 0: the whole sequence; 1: it began in an earlier tile; 2: it goes on
+  int next_seq, next_token;
+};
+
+// Finds the next fragments of tokens [cursor, t1), from sequence s on, by one warp.
+// Sequences that overlap (no table) are cut, so that tokens always rise.
+__device__ __forceinline__ void find_fragments(const BalArgs& a, const int* soff, int s, int cursor,
+                                               int t0, int t1, Fragments* f) {
+  const int lane = threadIdx.x & 31;
+  int n = 0;
+  bool more = true;
+  while (more && n < kFrags && s < a.S) {
+    const int mine = s + lane;
+    int2 r = make_int2(t1, t1);
+    if (mine < a.S)
+      r = a.S <= kOffBatch ? range_of(soff[mine], soff[mine + 1], a.T) : seq_range(a, mine);
+    unsigned some = __ballot_sync(kFull, r.y > r.x && r.x < t1 && r.y > cursor);
+    more = __all_sync(kFull, r.x < t1);
+    int done = 32;
+    while (some != 0 && n < kFrags) {
+      const int k = __ffs(some) - 1;
+      some &= some - 1;
+      const int lo = __shfl_sync(kFull, r.x, k), hi = __shfl_sync(kFull, r.y, k);
+      const int begin = max(lo, cursor), end = min(hi, t1);
+      if (begin >= end) continue;
+      if (lane == 0) {
+        f->seq[n] = s + k;
+        f->begin[n] = begin;
+        f->end[n] = end;
+        f->length[n] = hi - lo;
+        f->kind[n] = lo < t0 ? 1 : hi > t1 ? 2 : 0;
+      }
+      cursor = end;
+      if (++n == kFrags) done = k + 1;
+    }
+    s += done;
+  }
+  if (lane == 0) {
+    f->n = n;
+    f->next_seq = n == kFrags ? s : a.S;
+    f->next_token = cursor;
+  }
+}
+
+// A tile: sums of p and counts of its tokens [t0, t1) of each sequence.  Each warp
+// takes tokens in a row, so that it meets few sequences, and a block's fragments
+// are worked on together: one after the other they would cost some 3 us each.
 template <int LPT, int NV, bool SIGMOID>
 __global__ void __launch_bounds__(kThreads, 1) balance_tile_kernel(BalArgs a) {
   // the tile's first logits and routes come into L2 while the kernel in front
@@ -349,19 +407,19 @@ __global__ void __launch_bounds__(kThreads, 1) balance_tile_kernel(BalArgs a) {
   grid_dependency_wait();
   constexpr int N = 4 * NV, TPW = 32 / LPT, U = kBatch<NV>;
   extern __shared__ float dyn[];
-  float* stage = dyn;                                        // [kWarps][E]
-  int* hist = reinterpret_cast<int*>(dyn + kWarps * a.E);    // [E]
+  float* stage = dyn;                                     // [kRows][E]
+  int* hist = reinterpret_cast<int*>(dyn + kRows * a.E);  // [kFrags][E]
   __shared__ int soff[kOffBatch + 1];
   __shared__ int ired[96];
   __shared__ float red[32];
+  __shared__ Fragments frag;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int team = lane / LPT, tl = lane % LPT;
   const int t0 = static_cast<int>(min(static_cast<int64_t>(blockIdx.x) * a.tile,
                                       static_cast<int64_t>(a.T)));
   const int t1 = static_cast<int>(min(static_cast<int64_t>(t0) + a.tile, static_cast<int64_t>(a.T)));
-  for (int e = threadIdx.x; e < a.E; e += kThreads) hist[e] = 0;
+  for (int i = threadIdx.x; i < kFrags * a.E; i += kThreads) hist[i] = 0;
   const Table table = read_table(a, t0, soff, ired);
-  const bool whole_table = a.S <= kOffBatch;
   if (table.full < a.S) {  // empty sequences
     for (int s = blockIdx.x * kWarps + warp; s < a.S; s += gridDim.x * kWarps) {
       const int2 r = seq_range(a, s);
@@ -374,28 +432,27 @@ __global__ void __launch_bounds__(kThreads, 1) balance_tile_kernel(BalArgs a) {
     }
   }
   if (blockIdx.x == 0 && threadIdx.x == 0 && table.wrong) raise_flag(a.flags, MOE_DEVERR_BAD_LAYOUT);
-  float loss = 0.0f;
-  int tail = -1;
-  bool more = true;
-  for (int sb = table.first; more && sb < a.S; sb += kOffBatch) {
-    const int ns = min(kOffBatch, a.S - sb);
-    const int* offs = soff + sb;
-    if (!whole_table) {
-      __syncthreads();
-      for (int i = threadIdx.x; i <= ns; i += kThreads) soff[i] = __ldg(a.off + sb + i);
-      __syncthreads();
-      offs = soff;
+  float loss = 0.0f;  // the thread's part
+  int tail = -1, next_seq = table.first, next_token = t0;
+  while (next_seq < a.S && next_token < t1) {
+    if (warp == 0) find_fragments(a, soff, next_seq, next_token, t0, t1, &frag);
+    __syncthreads();
+    const int nf = frag.n;
+    if (nf == 0) break;
+    const int f0 = frag.begin[0], f1 = frag.end[nf - 1];
+    const int share = ((f1 - f0 - 1) / (kWarps * TPW) + 1) * TPW;  // tokens of a warp
+    const int w0 = min(static_cast<int64_t>(f0) + static_cast<int64_t>(warp) * share,
+                       static_cast<int64_t>(f1));
+    const int w1 = min(static_cast<int64_t>(w0) + share, static_cast<int64_t>(f1));
+    // counts: a thread a token
+    for (unsigned t = f0 + threadIdx.x; t < static_cast<unsigned>(f1); t += kThreads) {
+      int f = 0;
+      while (f + 1 < nf && static_cast<int>(t) >= frag.begin[f + 1]) ++f;
+      if (static_cast<int>(t) < frag.end[f]) count_token(a, t, hist + f * a.E);
     }
-    for (int i = 0; i < ns; ++i) {
-      const int s = sb + i;
-      const int2 r = range_of(offs[i], offs[i + 1], a.T);
-      if (offs[i] >= t1) {
-        more = false;
-        break;
-      }
-      const int f0 = max(r.x, t0), f1 = min(r.y, t1);
-      if (f0 >= f1) continue;
-      // sums of p
+    for (int f = 0; f < nf; ++f) {
+      const int x0 = max(w0, frag.begin[f]), x1 = min(w1, frag.end[f]);
+      if (x0 >= x1) continue;
       float acc[N], unused[N];
 #pragma unroll
       for (int k = 0; k < N; ++k) acc[k] = 0.0f;
@@ -408,7 +465,7 @@ __global__ void __launch_bounds__(kThreads, 1) balance_tile_kernel(BalArgs a) {
           for (int o = LPT; o < 32; o <<= 1) acc[k] += __shfl_xor_sync(kFull, acc[k], o);
           const int c = col_of<LPT>(tl, k);
           if (team == 0 && c < a.E) {
-            float* to = stage + warp * a.E + c;
+            float* to = stage + (warp + f) * a.E + c;
             *to = begun ? *to + acc[k] : acc[k];
           }
           acc[k] = 0.0f;
@@ -416,18 +473,14 @@ __global__ void __launch_bounds__(kThreads, 1) balance_tile_kernel(BalArgs a) {
         begun = true;
         held = 0;
       };
-      const unsigned last = f1;
-      // a thread a token, from the last warp on: the first ones have more logits
-      for (unsigned t = f0 + (kThreads - 1 - threadIdx.x); t < last; t += kThreads)
-        count_token(a, t, hist);
-      constexpr unsigned kStep = kWarps * TPW;
-      for (unsigned base = f0 + warp * TPW; base < last; base += U * kStep) {
-        const unsigned t = base + team;
+      const unsigned last = x1;
+      for (unsigned base = x0; base < last; base += U * TPW) {
         float v[U][N];
         auto load = [&](int u, float (&to)[N]) {
-          const bool live = t + u * kStep < last;
-          load_row<LPT, NV, float4>(a.logits + static_cast<size_t>(live ? t + u * kStep : f0) * a.E,
-                                    a.E, a.vec, live, tl, -kInf, to);
+          const unsigned t = base + u * TPW + team;
+          const bool live = t < last;
+          load_row<LPT, NV, float4>(a.logits + static_cast<size_t>(live ? t : x0) * a.E, a.E, a.vec,
+                                    live, tl, -kInf, to);
           return live;
         };
         bool live[U];
@@ -446,33 +499,34 @@ __global__ void __launch_bounds__(kThreads, 1) balance_tile_kernel(BalArgs a) {
         if (held >= kFlush) flush();
       }
       flush();
-      __syncthreads();
-      const bool whole = r.x >= t0 && r.y <= t1;
-      const int slot = 2 * blockIdx.x + (r.x >= t0);
-      if (!whole && r.x >= t0) tail = s;
-      float val = 0.0f;
-      for (int e = threadIdx.x; e < a.E; e += kThreads) {
-        float p = 0.0f;
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) p += stage[w * a.E + e];
-        const int c = hist[e];
-        hist[e] = 0;
-        if (whole) {
-          const size_t at = static_cast<size_t>(s) * a.E + e;
-          a.cnt[at] = c;
-          if (a.prob) a.prob[at] = p / (r.y - r.x);
-          val += static_cast<float>(c) * p;
-        } else {
-          const size_t at = static_cast<size_t>(slot) * a.E + e;
-          a.slot_p[at] = p;
-          a.slot_c[at] = c;
-        }
-      }
-      // (a barrier, too: stage and hist are taken up again)
-      val = block_sum(val, red);
-      if (whole) loss = fmaf(val, seq_factor(a, r.y - r.x), loss);
     }
+    __syncthreads();
+    for (int i = threadIdx.x; i < nf * a.E; i += kThreads) {
+      const int f = nf == 1 ? 0 : i / a.E, e = i - f * a.E;
+      const int first = (frag.begin[f] - f0) / share, end = (frag.end[f] - 1 - f0) / share;
+      float p = 0.0f;
+#pragma unroll 8
+      for (int w = first; w <= end; ++w) p += stage[(w + f) * a.E + e];
+      const int c = hist[i];
+      hist[i] = 0;
+      const int kind = frag.kind[f];
+      if (kind == 0) {
+        const size_t at = static_cast<size_t>(frag.seq[f]) * a.E + e;
+        a.cnt[at] = c;
+        if (a.prob) a.prob[at] = p / frag.length[f];
+        loss = fmaf(static_cast<float>(c) * p, seq_factor(a, frag.length[f]), loss);
+      } else {
+        const size_t at = static_cast<size_t>(2 * blockIdx.x + kind - 1) * a.E + e;
+        a.slot_p[at] = p;
+        a.slot_c[at] = c;
+      }
+    }
+    if (frag.kind[nf - 1] == 2) tail = frag.seq[nf - 1];
+    next_seq = frag.next_seq;
+    next_token = frag.next_token;
+    __syncthreads();  // stage, hist and frag are taken up again
   }
+  loss = block_sum(loss, red);
   if (threadIdx.x == 0) {
     if (gridDim.x == 1) {  // every sequence is whole: the loss in the same launch
       *a.loss = table.full > 0 ? a.coef * loss / table.full : 0.0f;
@@ -729,12 +783,16 @@ BalArgs bal_args(const moe_handle* h, const float* logits, int T, const int32_t*
 
 }  // namespace
 
+namespace {
+size_t tile_shared(int E) { return static_cast<size_t>(kRows + kFrags) * E * sizeof(float); }
+}  // namespace
+
 // The tile kernels take more shared memory than the default: once for a device.
 cudaError_t prepare_balance_kernels() {
   cudaError_t e = cudaSuccess;
   for (int E : {8, 16, 32, 64, 128, 256, 384, 512}) {
     if (e != cudaSuccess) return e;
-    const int bytes = (kWarps + 1) * E * static_cast<int>(sizeof(float));
+    const int bytes = static_cast<int>(tile_shared(E));
     e = with_team(E, [&](auto lanes, auto vecs) {
       cudaError_t r = cudaFuncSetAttribute(balance_tile_kernel<lanes(), vecs(), false>,
                                            cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
@@ -786,7 +844,7 @@ cudaError_t launch_balance(const moe_handle* h, const float* logits, const int32
   if (tiles < 1) tiles = 1;
   a.tile = T > 0 ? (T + tiles - 1) / tiles : 1;
   a.tiles = T > 0 ? (T + a.tile - 1) / a.tile : 1;
-  const size_t smem = static_cast<size_t>(kWarps + 1) * a.E * sizeof(float);
+  const size_t smem = tile_shared(a.E);
   const bool sigmoid = h->cfg.score_fn == MOE_SCORE_SIGMOID;
   cudaError_t e = with_team(a.E, [&](auto lanes, auto vecs) {
     auto k = sigmoid ? balance_tile_kernel<lanes(), vecs(), true>
