@@ -114,11 +114,6 @@ struct PairTraits<float> {
 __device__ __forceinline__ void commit_copies() {
   asm volatile("cp.async.commit_group;" ::: "memory");
 }
-// Lets the kernel behind this one (launched chained) get ready: its blocks wait for
-// the end of this grid themselves.
-__device__ __forceinline__ void release_join() {
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-}
 // Waits until at most N of the thread's groups of copies are under way.
 template <int N>
 __device__ __forceinline__ void wait_copies() {
@@ -266,6 +261,7 @@ __global__ void __launch_bounds__(MAXT, KMAX == 1 && MAXT <= 512 && sizeof(Elt) 
   static_assert(!GATHER || AHEAD < 2, "a token's weights are asked for one token ahead");
   __shared__ __align__(16) float red[kRed];
   extern __shared__ __align__(16) uint8_t shared[];
+  grid_dependency_wait();
   Team<WARP, MAXT> team(a.team_threads, red);
   const int tid = team.tid, step = team.threads;
   const int unit = blockIdx.x * a.teams + team.index;
@@ -534,6 +530,7 @@ __global__ void __launch_bounds__(MAXT, 1) block_norm_bwd_kernel(NormBwdArgs a) 
   enum { GRes, Gx, ResOut, C, Gate };
   __shared__ __align__(16) float red[kRed];
   extern __shared__ __align__(16) uint8_t shared[];
+  grid_dependency_wait();
   Team<WARP, MAXT> team(a.team_threads, red);
   const int tid = team.tid, step = team.threads;
   const int unit = blockIdx.x * a.teams + team.index;
@@ -758,7 +755,6 @@ __global__ void __launch_bounds__(MAXT, 1) block_norm_bwd_kernel(NormBwdArgs a) 
     }
     if (a.teams > 1) __syncthreads();
   }
-  release_join();
   if (a.teams == 1) return;
   // behind the last round the teams' sums meet in shared memory
   wait_copies<0>();
@@ -1036,8 +1032,7 @@ cudaError_t launch_block_norm(const moe_handle* h, const moe_block_norm_args& q,
   const int blocks = (T - 1) / a.teams + 1;
   const int grid = static_cast<int>(blocks < most ? blocks : most);
   a.units = grid * a.teams;
-  c.kernel<<<grid, threads, c.shared, s>>>(a);
-  return cudaGetLastError();
+  return launch_chained(c.kernel, dim3(grid), dim3(threads), c.shared, s, false, a);
 }
 
 cudaError_t launch_block_norm_bwd(const moe_handle* h, const moe_block_norm_bwd_args& q, int T,
@@ -1082,8 +1077,8 @@ cudaError_t launch_block_norm_bwd(const moe_handle* h, const moe_block_norm_bwd_
                       : (gated ? backward_kernel<float, true>(q.H, threads)
                                : backward_kernel<float, false>(q.H, threads));
   if (T > 0) {
-    k.kernel<<<a.blocks, threads, k.shared, s>>>(a);
-    const cudaError_t e = cudaGetLastError();
+    const cudaError_t e =
+        launch_chained(k.kernel, dim3(a.blocks), dim3(threads), k.shared, s, false, a);
     if (e != cudaSuccess) return e;
   }
   const bool spans = a.ggate && a.gate_tokens > 1;

@@ -171,3 +171,9 @@ def test_structs_match_the_header():
         want = [(m[2], ctypes.c_void_p if m[1] else kinds[m[0]])
                 for m in re.findall(r"(?:const )?(\w+)(\*?) (\w+);", body)]
         assert list(cls._fields_) == want
+    import struct
+    for form, cls in (("12P3d5i4x", moe.MoeBlockNormArgs), ("14P2d4i", moe.MoeBlockNormBwdArgs)):
+        assert struct.calcsize(form) == ctypes.sizeof(cls)
+        kinds = {ctypes.c_void_p: "P", ctypes.c_double: "d", ctypes.c_int32: "i"}
+        each = "".join(n * c for n, c in ((int(n or 1), c) for n, c in re.findall(r"(\d*)([Pdi])", form)))
+        assert each == "".join(kinds[t] for _, t in cls._fields_)
