@@ -133,6 +133,11 @@ __device__ __forceinline__ Vec16 ld_shared(uint32_t a) {
                : "memory");
   return v;
 }
+__device__ __forceinline__ void st_shared(uint32_t a, const Vec16& v) {
+  asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(a), "r"(v.u[0]), "r"(v.u[1]),
+               "r"(v.u[2]), "r"(v.u[3])
+               : "memory");
+}
 __device__ __forceinline__ void st_shared(uint32_t a, float4 v) {
   asm volatile("st.shared.v4.f32 [%0], {%1,%2,%3,%4};" ::"r"(a), "f"(v.x), "f"(v.y), "f"(v.z),
                "f"(v.w)
@@ -518,15 +523,26 @@ __device__ __forceinline__ void flush_sums(F2 (&acc)[V][P], float* to, bool firs
   }
 }
 
+// What a backward kernel does about the gate: there is none; a row per token; a row
+// per group of tokens.
+enum GateKind { kNoGate, kGateRows, kGateGroups };
+
 // A unit (a team) takes `chunk` tokens in a row and holds the column sums of the
-// weights' gradients, and of the gate's while the tokens of its group last.
-// D = gres' + r_p (v - h mean(v h)), v = gx w_pre, h = res' r_p: the gradient of
-// the residual sum; then the same form behind the gate for c.  AHEAD as in the
-// forward.
-template <typename Elt, bool GATE, bool WARP, int MAXT, int AHEAD>
+// weights' gradients.  D = gres' + r_p (v - h mean(v h)), v = gx w_pre, h = res'
+// r_p: the gradient of the residual sum; then the same form behind the gate for c.
+// Where a gate row serves a group of tokens, one sum over the group, A = sum D c r_c,
+// gives both gradients behind it, the gate's w_post A and w_post's gate A, and the
+// row's product with w_post is kept for the group.
+//
+// AHEAD as in the forward.  With room for one token alone, its vectors are asked for
+// in two parts, each as soon as that of the token before is used up (fp32 rows of
+// 7168: 98.6 -> 65.6 us for 2048 tokens); with more, at the token's end (sooner,
+// between its two sums, took 232 instead of 222 us at the DeepSeek-V3 shape).
+template <typename Elt, GateKind GATE, bool WARP, int MAXT, int AHEAD>
 __global__ void __launch_bounds__(MAXT, 1) block_norm_bwd_kernel(NormBwdArgs a) {
   using PT = PairTraits<Elt>;
-  constexpr int P = PT::P, N = 2 * P, V = kEpt / N, ROWS = GATE ? 5 : 4;
+  constexpr int P = PT::P, N = 2 * P, V = kEpt / N, ROWS = GATE == kGateRows ? 5 : 4;
+  constexpr bool PARTS = AHEAD == 1;
   enum { GRes, Gx, ResOut, C, Gate };
   __shared__ __align__(16) float red[kRed];
   extern __shared__ __align__(16) uint8_t shared[];
@@ -537,7 +553,10 @@ __global__ void __launch_bounds__(MAXT, 1) block_norm_bwd_kernel(NormBwdArgs a) 
   const uint32_t sb = blockDim.x * 16, token = ROWS * V * sb, wb = step * 16;  // bytes
   const uint32_t wpost = smem_addr(shared) + tid * 16;
   const uint32_t wpre = wpost + kWeightSlots * wb;
-  const uint32_t ring = smem_addr(shared) + threadIdx.x * 16 + 2 * kWeightSlots * wb;
+  // of a group: the gate's row, and its product with w_post
+  const uint32_t gate_row = smem_addr(shared) + threadIdx.x * 16 + 2 * kWeightSlots * wb;
+  const uint32_t gate_w = gate_row + V * sb;
+  const uint32_t ring = GATE == kGateGroups ? gate_w + kWeightSlots * sb : gate_row;
   bool in[V];    // vectors inside the row, and where
   int at[V];
 #pragma unroll
@@ -548,44 +567,34 @@ __global__ void __launch_bounds__(MAXT, 1) block_norm_bwd_kernel(NormBwdArgs a) 
   const int64_t begin64 = static_cast<int64_t>(unit) * a.chunk;
   const int begin = static_cast<int>(begin64 < a.T ? begin64 : a.T);
   const int end = static_cast<int>(begin64 + a.chunk < a.T ? begin64 + a.chunk : a.T);
-  // the gate's row of a token, for tokens in order: its offset and last token + 1
-  struct Group {
-    int64_t row, end;
+  auto copy = [&](uint32_t to, int k, int i, const uint8_t* p, int64_t off) {
+    copy_async(to + (k * V + i) * sb, p + off + at[i], in[i]);
   };
-  auto group_of = [&](int t) {
-    const int64_t g = t / a.gate_tokens;
-    return Group{g * a.row_bytes, (g + 1) * a.gate_tokens};
-  };
-  Group asked = GATE ? group_of(begin) : Group{0, 0}, group = asked;
-  int64_t off = begin * a.row_bytes;  // of the row asked for next
-  int next = begin;
-  auto fetch = [&](uint32_t to) {
-    if (next < end) {
+  // a token's rows of the residual stream and the norm, and those behind them
+  auto fetch = [&](bool first, bool second, int64_t off, uint32_t to) {
 #pragma unroll
-      for (int i = 0; i < V; ++i) {
-        auto copy = [&](int k, const uint8_t* p, int64_t o) {
-          copy_async(to + (k * V + i) * sb, p + o + at[i], in[i]);
-        };
-        if (a.gx) {
-          copy(Gx, a.gx, off);
-          copy(ResOut, a.res_out, off);
-        }
-        if (a.gres_out) copy(GRes, a.gres_out, off);
-        if (a.c) copy(C, a.c, off);
-        if (GATE) copy(Gate, a.gate, asked.row);
+    for (int i = 0; i < V; ++i) {
+      if (first && a.gx) {
+        copy(to, Gx, i, a.gx, off);
+        copy(to, ResOut, i, a.res_out, off);
       }
-      off += a.row_bytes;
-      ++next;
-      if (GATE && next == asked.end) {
-        asked.row += a.row_bytes;
-        asked.end += a.gate_tokens;
-      }
+      if (first && a.gres_out) copy(to, GRes, i, a.gres_out, off);
+      if (second && a.c) copy(to, C, i, a.c, off);
+      if (second && GATE == kGateRows) copy(to, Gate, i, a.gate, off);
     }
-    commit_copies();
   };
+  int64_t row = begin * a.row_bytes;
   if (AHEAD > 0)
 #pragma unroll
-    for (int n = 0; n < AHEAD; ++n) fetch(ring + n * token);
+    for (int n = 0; n < AHEAD; ++n) {
+      const bool real = n < end - begin;
+      if (PARTS) {
+        if (real) fetch(true, false, row, ring);
+        commit_copies();
+      }
+      if (real) fetch(!PARTS, true, row + n * a.row_bytes, ring + n * token);
+      commit_copies();
+    }
   float r_pre = a.gx && begin < end ? __ldg(a.rstd_pre + begin) : 0.0f;
   float r_post = a.w_post && begin < end ? __ldg(a.rstd_post + begin) : 1.0f;
   if (team.index == 0) {
@@ -593,29 +602,34 @@ __global__ void __launch_bounds__(MAXT, 1) block_norm_bwd_kernel(NormBwdArgs a) 
     if (a.gx) keep_weights<N>(a.w_pre, a.w_f32, a.offset, wpre, wb, tid, step, a.nvec);
   }
   __syncthreads();
-  F2 gpost[V][P], gpre[V][P], ggate[V][P];
+  F2 gpost[V][P], gpre[V][P], A[V][P];
 #pragma unroll
   for (int i = 0; i < V; ++i)
 #pragma unroll
-    for (int j = 0; j < P; ++j) gpost[i][j] = gpre[i][j] = ggate[i][j] = 0;
+    for (int j = 0; j < P; ++j) gpost[i][j] = gpre[i][j] = A[i][j] = 0;
   // the block's rows of sums; a team adds to them when it has held kFlush tokens
   // and at the end, the teams in turn
   float* post_row = a.part + static_cast<size_t>(blockIdx.x) * a.H;
   float* pre_row = a.part + static_cast<size_t>(a.blocks + blockIdx.x) * a.H;
-  bool gate_first = true;
+  // the token's group: its number and last token + 1
+  int group = GATE == kGateGroups ? begin / a.gate_tokens : 0;
+  int64_t group_end = (static_cast<int64_t>(group) + 1) * a.gate_tokens;
+  bool enters = true, gate_first = true;
   int gate_held = 0;
   uint32_t stage = ring;
-  int64_t row = begin * a.row_bytes;
   // All teams of a block make the same number of rounds of kFlush tokens; behind
   // each they add their sums to the block's, one after the other.
   const int rounds = (a.chunk - 1) / kFlush + 1;
   for (int round = 0; round < rounds; ++round) {
-    const int stop = min(static_cast<int64_t>(end), begin64 + (round + 1) * static_cast<int64_t>(kFlush));
-    for (int t = begin64 + round * static_cast<int64_t>(kFlush); t < stop; ++t, row += a.row_bytes) {
-      auto load = [&](int k, int i, const uint8_t* p, int64_t o, F2* f) {
+    const int stop = static_cast<int>(
+        min(static_cast<int64_t>(end), begin64 + (round + 1) * static_cast<int64_t>(kFlush)));
+    for (int t = static_cast<int>(min(static_cast<int64_t>(end),
+                                      begin64 + round * static_cast<int64_t>(kFlush)));
+         t < stop; ++t, row += a.row_bytes) {
+      auto load = [&](int k, int i, const uint8_t* p, F2* f) {
         Vec16 x{};
         if (AHEAD > 0) x = ld_shared(stage + (k * V + i) * sb);
-        else if (in[i]) x = ld_vec(p + o + at[i]);
+        else if (in[i]) x = ld_vec(p + row + at[i]);
         PT::to(x, f);
       };
       const float rp = r_pre, r = r_post;
@@ -623,15 +637,15 @@ __global__ void __launch_bounds__(MAXT, 1) block_norm_bwd_kernel(NormBwdArgs a) 
         if (a.gx) r_pre = __ldg(a.rstd_pre + t + 1);
         if (a.w_post) r_post = __ldg(a.rstd_post + t + 1);
       }
-      if (AHEAD > 0) wait_copies<AHEAD - 1>();
+      if (AHEAD > 0) wait_copies<PARTS ? 1 : AHEAD - 1>();
       F2 D[V][P], h[V][P];
       if (a.gx) {
         F2 s = 0;
 #pragma unroll
         for (int i = 0; i < V; ++i) {
           F2 w[P];
-          load(Gx, i, a.gx, row, D[i]);
-          load(ResOut, i, a.res_out, row, h[i]);
+          load(Gx, i, a.gx, D[i]);
+          load(ResOut, i, a.res_out, h[i]);
           kept_weights<N>(wpre, wb, i, w);
 #pragma unroll
           for (int j = 0; j < P; ++j) {
@@ -647,14 +661,14 @@ __global__ void __launch_bounds__(MAXT, 1) block_norm_bwd_kernel(NormBwdArgs a) 
           F2 g[P];
 #pragma unroll
           for (int j = 0; j < P; ++j) g[j] = 0;
-          if (a.gres_out) load(GRes, i, a.gres_out, row, g);
+          if (a.gres_out) load(GRes, i, a.gres_out, g);
 #pragma unroll
           for (int j = 0; j < P; ++j)
             D[i][j] = fma2(both(rp), fma2(both(-m), h[i][j], D[i][j]), g[j]);
         }
       } else {
 #pragma unroll
-        for (int i = 0; i < V; ++i) load(GRes, i, a.gres_out, row, D[i]);
+        for (int i = 0; i < V; ++i) load(GRes, i, a.gres_out, D[i]);
       }
       if (a.gres) {
 #pragma unroll
@@ -665,28 +679,72 @@ __global__ void __launch_bounds__(MAXT, 1) block_norm_bwd_kernel(NormBwdArgs a) 
           if (in[i]) st_vec(a.gres + row + at[i], PT::from(o));
         }
       }
+      if (PARTS) {
+        if (end - t > 1) fetch(true, false, row + a.row_bytes, stage);
+        commit_copies();
+        wait_copies<1>();
+      }
+      if (GATE == kGateGroups && enters) {
+        const uint8_t* p = a.gate + group * a.row_bytes;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+          Vec16 x{};
+          if (in[i]) {
+            x = ld_vec(p + at[i]);
+            if (group_end < end)  // the next group's, into L2
+              asm volatile("prefetch.global.L2 [%0];" ::"l"(p + a.row_bytes + at[i]));
+          }
+          F2 g[P], w[P];
+          PT::to(x, g);
+          st_shared(gate_row + i * sb, x);
+          if (a.w_post) {
+            kept_weights<N>(wpost, wb, i, w);
+#pragma unroll
+            for (int j = 0; j < P; ++j) g[j] = mul2(g[j], w[j]);
+          }
+#pragma unroll
+          for (int q = 0; q < P / 2; ++q) {
+            const float2 lo = split(g[2 * q]), hi = split(g[2 * q + 1]);
+            st_shared(gate_w + (i * (P / 2) + q) * sb, make_float4(lo.x, lo.y, hi.x, hi.y));
+          }
+        }
+        enters = false;
+      }
       if (a.c) {
         F2 s = 0;
 #pragma unroll
         for (int i = 0; i < V; ++i) {
           F2 w[P];
-          load(C, i, a.c, row, h[i]);
+          load(C, i, a.c, h[i]);
 #pragma unroll
-          for (int j = 0; j < P; ++j) h[i][j] = mul2(h[i][j], both(r));
-          if (a.w_post) kept_weights<N>(wpost, wb, i, w);
-          if (GATE) {
-            F2 g[P];
-            load(Gate, i, a.gate, group.row, g);
+          for (int j = 0; j < P; ++j) {
+            h[i][j] = mul2(h[i][j], both(r));
+            w[j] = both(1.0f);
+          }
+          if (GATE == kGateGroups) {
+            kept_weights<N>(gate_w, sb, i, w);
 #pragma unroll
-            for (int j = 0; j < P; ++j) {
-              ggate[i][j] = fma2(D[i][j], a.w_post ? mul2(h[i][j], w[j]) : h[i][j], ggate[i][j]);
-              D[i][j] = mul2(D[i][j], g[j]);
+            for (int j = 0; j < P; ++j) A[i][j] = fma2(D[i][j], h[i][j], A[i][j]);
+          } else {
+            if (a.w_post) kept_weights<N>(wpost, wb, i, w);
+            if (GATE == kGateRows) {
+              F2 g[P], o[P];
+              load(Gate, i, a.gate, g);
+#pragma unroll
+              for (int j = 0; j < P; ++j) {
+                o[j] = mul2(D[i][j], mul2(h[i][j], w[j]));
+                D[i][j] = mul2(D[i][j], g[j]);
+              }
+              if (a.ggate && in[i]) st_vec(a.ggate + row + at[i], PT::from(o));
+            }
+            if (a.w_post) {
+#pragma unroll
+              for (int j = 0; j < P; ++j) gpost[i][j] = fma2(D[i][j], h[i][j], gpost[i][j]);
             }
           }
-          if (a.w_post) {
+          if (a.w_post || GATE == kGateGroups) {
 #pragma unroll
             for (int j = 0; j < P; ++j) {
-              gpost[i][j] = fma2(D[i][j], h[i][j], gpost[i][j]);
               D[i][j] = mul2(D[i][j], w[j]);
               s = fma2(D[i][j], h[i][j], s);
             }
@@ -707,42 +765,55 @@ __global__ void __launch_bounds__(MAXT, 1) block_norm_bwd_kernel(NormBwdArgs a) 
           if (in[i]) st_vec(a.gy + row + at[i], PT::from(D[i]));
       }
       if (AHEAD > 0) {
-        fetch(stage);
+        if (end - t > AHEAD) fetch(!PARTS, true, row + AHEAD * a.row_bytes, stage);
+        commit_copies();
         stage += token;
         if (stage == ring + AHEAD * token) stage = ring;
       }
-      if (GATE) {
-        const int64_t g0 = group.end - a.gate_tokens;
-        const bool ends = t + 1 == group.end || t + 1 == a.T;
-        if (a.ggate) {
-          float* slot = a.slots + static_cast<size_t>(2 * unit + (g0 >= begin)) * a.H;
-          if (ends && g0 >= begin) {  // all of the group's tokens
+      if (GATE == kGateGroups) {
+        const bool ends = t + 1 == group_end || t + 1 == a.T;
+        if (ends || t + 1 == end || ++gate_held == kFlush) {
+          const bool all = ends && group_end - a.gate_tokens >= begin;  // of the group's tokens
+          float* slot = a.slots +
+                        static_cast<size_t>(2 * unit + (group_end - a.gate_tokens >= begin)) * a.H;
 #pragma unroll
-            for (int i = 0; i < V; ++i) {
-              if (in[i]) {
+          for (int i = 0; i < V; ++i) {
+            if (a.w_post) {
+              F2 g[P], w[P];
+              PT::to(ld_shared(gate_row + i * sb), g);
+              kept_weights<N>(wpost, wb, i, w);
 #pragma unroll
-                for (int j = 0; j < P; ++j)
-                  if (!gate_first) {
-                    const float2 x =
-                        *reinterpret_cast<const float2*>(slot + ((tid + i * step) * P + j) * 2);
-                    ggate[i][j] = add2(ggate[i][j], pair(x.x, x.y));
-                  }
-                st_vec(a.ggate + group.row + at[i], PT::from(ggate[i]));
+              for (int j = 0; j < P; ++j) {
+                gpost[i][j] = fma2(g[j], A[i][j], gpost[i][j]);
+                A[i][j] = mul2(w[j], A[i][j]);
               }
-#pragma unroll
-              for (int j = 0; j < P; ++j) ggate[i][j] = 0;
             }
-            gate_first = true;
-            gate_held = 0;
-          } else if (ends || t + 1 == end || ++gate_held == kFlush) {
-            flush_sums(ggate, slot, gate_first, tid, step, a.nvec);
-            gate_first = ends;
-            gate_held = 0;
+            if (all && a.ggate && in[i]) {
+#pragma unroll
+              for (int j = 0; j < P; ++j)
+                if (!gate_first) {
+                  const float2 x =
+                      *reinterpret_cast<const float2*>(slot + ((tid + i * step) * P + j) * 2);
+                  A[i][j] = add2(A[i][j], pair(x.x, x.y));
+                }
+              st_vec(a.ggate + group * a.row_bytes + at[i], PT::from(A[i]));
+            }
           }
-        }
-        if (ends) {
-          group.row += a.row_bytes;
-          group.end += a.gate_tokens;
+          if (!all && a.ggate) {
+            flush_sums(A, slot, gate_first, tid, step, a.nvec);
+          } else {
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+#pragma unroll
+              for (int j = 0; j < P; ++j) A[i][j] = 0;
+          }
+          gate_first = ends;
+          gate_held = 0;
+          if (ends) {
+            ++group;
+            group_end += a.gate_tokens;
+            enters = true;
+          }
         }
       }
     }
@@ -767,7 +838,7 @@ __global__ void __launch_bounds__(MAXT, 1) block_norm_bwd_kernel(NormBwdArgs a) 
       st_shared(ring + q * sb, make_float4(x.x, x.y, y.x, y.y));
     }
     __syncthreads();
-    const uint32_t first = smem_addr(shared) + 2 * kWeightSlots * wb;
+    const uint32_t first = smem_addr(shared) + 2 * kWeightSlots * wb + (ring - gate_row);
     for (int n = threadIdx.x; n < kWeightSlots * step; n += blockDim.x) {
       const int q = n / step, thread = n - q * step;
       const int v = thread + q / (P / 2) * step;
@@ -789,42 +860,44 @@ __global__ void __launch_bounds__(MAXT, 1) block_norm_bwd_kernel(NormBwdArgs a) 
   if (a.gw_pre) meet(gpre, pre_row);
 }
 
-// Joins the units' column sums: row y = 0, 1 of the grid the weights'
-// gradients; row 2 + i the gate's of group i, or where there are more groups than
-// units of the one that goes on from unit i into the next; a group inside one
-// unit is done.
+// Joins the units' column sums: row y = 0, 1 of the grid the weights' gradients,
+// the rows behind them the gate's, an item for every `share` warps: item i is
+// group i, or where there are more groups than units that which goes on from unit
+// i into the next.  A group inside one unit is done.
 template <typename Elt>
-__global__ void __launch_bounds__(32 * kJoinWarps) block_norm_join_kernel(NormBwdArgs a) {
+__global__ void __launch_bounds__(32 * kJoinWarps)
+    block_norm_join_kernel(NormBwdArgs a, int items, int share) {
   grid_dependency_wait();
   __shared__ float2 ps[kJoinWarps][32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int col = blockIdx.x * kJoinCols + 2 * lane;
   const int y = blockIdx.y;
+  const float* from = nullptr;
   float* out = nullptr;
-  const float* from = a.part;
-  int u0 = 0, u1 = a.blocks, stride = 1, head = 0;
-  int group = 0;
+  int u0 = 0, u1 = a.blocks, stride = 1, head = 0, group = -1;
   if (y < 2) {
+    share = kJoinWarps;
     out = y == 0 ? a.gw_post : a.gw_pre;
-    from += static_cast<size_t>(y) * a.blocks * a.H;
-    if (!out) return;
+    if (out) from = a.part + static_cast<size_t>(y) * a.blocks * a.H;
   } else {
-    const int64_t next = (static_cast<int64_t>(y - 2) + 1) * a.chunk;
-    if (a.groups > a.units && next >= a.T) return;
-    group = a.groups > a.units ? static_cast<int>(next / a.gate_tokens) : y - 2;
-    const int64_t g0 = static_cast<int64_t>(group) * a.gate_tokens;
-    const int64_t g1 = min(g0 + a.gate_tokens, static_cast<int64_t>(a.T));
-    u0 = static_cast<int>(g0 / a.chunk);
-    u1 = static_cast<int>((g1 - 1) / a.chunk) + 1;
-    if (u1 - u0 < 2 || (a.groups > a.units && u0 != y - 2)) return;
-    from = a.slots;
+    const int item = (y - 2) * (kJoinWarps / share) + warp / share;
+    const int64_t next = (static_cast<int64_t>(item) + 1) * a.chunk;
+    const bool by_unit = a.groups > a.units;
+    if (item < items && !(by_unit && next >= a.T)) {
+      group = by_unit ? static_cast<int>(next / a.gate_tokens) : item;
+      const int64_t g0 = static_cast<int64_t>(group) * a.gate_tokens;
+      const int64_t g1 = min(g0 + a.gate_tokens, static_cast<int64_t>(a.T));
+      u0 = static_cast<int>(g0 / a.chunk);
+      u1 = static_cast<int>((g1 - 1) / a.chunk) + 1;
+      if (u1 - u0 > 1 && !(by_unit && u0 != item)) from = a.slots;
+    }
     stride = 2;
     head = 1;
   }
   float2 p{0.0f, 0.0f};
-  if (col < a.H)
+  if (from && col < a.H)
 #pragma unroll 8
-    for (int u = u0 + warp; u < u1; u += kJoinWarps) {
+    for (int u = u0 + warp % share; u < u1; u += share) {
       const float2 x = __ldcg(reinterpret_cast<const float2*>(
           from + static_cast<size_t>(stride * u + (u == u0 ? head : 0)) * a.H + col));
       p.x += x.x;
@@ -832,11 +905,11 @@ __global__ void __launch_bounds__(32 * kJoinWarps) block_norm_join_kernel(NormBw
     }
   ps[warp][lane] = p;
   __syncthreads();
-  if (warp != 0 || col >= a.H) return;
-#pragma unroll
-  for (int w = 1; w < kJoinWarps; ++w) {
-    p.x += ps[w][lane].x;
-    p.y += ps[w][lane].y;
+  if (!from || warp % share != 0 || col >= a.H) return;
+#pragma unroll 4
+  for (int w = 1; w < share; ++w) {
+    p.x += ps[warp + w][lane].x;
+    p.y += ps[warp + w][lane].y;
   }
   if (y < 2) {
     out[col] = p.x;
@@ -907,7 +980,7 @@ Chosen<NormArgs> forward_kernel(int H, int kmax, int threads, int rows, int weig
                      : forward_kernel<Elt, 16>(H, kept, token, kShared);
 }
 
-template <typename Elt, bool GATE, bool WARP, int MAXT>
+template <typename Elt, GateKind GATE, bool WARP, int MAXT>
 Chosen<NormBwdArgs> backward_within(size_t kept, size_t token, size_t most) {
   if constexpr (MAXT < 1024) {
     if (kept + 3 * token <= most)
@@ -915,23 +988,34 @@ Chosen<NormBwdArgs> backward_within(size_t kept, size_t token, size_t most) {
     if (kept + 2 * token <= most)
       return {block_norm_bwd_kernel<Elt, GATE, WARP, MAXT, 2>, 2, kept + 2 * token};
   }
+  if (kept + token <= most)
+    return {block_norm_bwd_kernel<Elt, GATE, WARP, MAXT, 1>, 1, kept + token};
   return {block_norm_bwd_kernel<Elt, GATE, WARP, MAXT, 0>, 0, kept};
 }
-template <typename Elt, bool GATE>
+template <typename Elt, GateKind GATE>
 Chosen<NormBwdArgs> backward_fitting(int H, size_t kept, size_t token, size_t most) {
   return one_warp(H) ? backward_within<Elt, GATE, true, kTeamThreads>(kept, token, most)
          : team_threads(H) <= kTeamThreads
              ? backward_within<Elt, GATE, false, kTeamThreads>(kept, token, most)
              : backward_within<Elt, GATE, false, 1024>(kept, token, most);
 }
-template <typename Elt, bool GATE>
+template <typename Elt, GateKind GATE>
 Chosen<NormBwdArgs> backward_kernel(int H, int threads) {
-  const size_t kept = kept_bytes(H, 2);
-  auto c = backward_fitting<Elt, GATE>(H, kept, token_bytes<Elt>(threads, GATE ? 5 : 4), kShared);
+  size_t kept = kept_bytes(H, 2);
+  if (GATE == kGateGroups)  // a gate row and 16 fp32 a thread
+    kept += token_bytes<Elt>(threads, 1) + static_cast<size_t>(threads) * kEpt * sizeof(float);
+  auto c = backward_fitting<Elt, GATE>(
+      H, kept, token_bytes<Elt>(threads, GATE == kGateRows ? 5 : 4), kShared);
   // the teams' sums meet there as well
   const size_t meet = kept + static_cast<size_t>(threads) * kEpt * sizeof(float);
   if (threads > team_threads(H) && c.shared < meet) c.shared = meet;
   return c;
+}
+template <typename Elt>
+Chosen<NormBwdArgs> backward_kernel(GateKind gate, int H, int threads) {
+  return gate == kNoGate     ? backward_kernel<Elt, kNoGate>(H, threads)
+         : gate == kGateRows ? backward_kernel<Elt, kGateRows>(H, threads)
+                             : backward_kernel<Elt, kGateGroups>(H, threads);
 }
 
 // Shared memory for every kernel that the choices above can make.
@@ -946,8 +1030,9 @@ cudaError_t allow_all() {
       allow(forward_kernel<Elt, 1>(H, 0, 1, fit));
       allow(forward_kernel<Elt, 8>(H, 0, 1, fit));
       allow(forward_kernel<Elt, 16>(H, 0, 1, fit));
-      allow(backward_fitting<Elt, false>(H, 0, 1, fit));
-      allow(backward_fitting<Elt, true>(H, 0, 1, fit));
+      allow(backward_fitting<Elt, kNoGate>(H, 0, 1, fit));
+      allow(backward_fitting<Elt, kGateRows>(H, 0, 1, fit));
+      allow(backward_fitting<Elt, kGateGroups>(H, 0, 1, fit));
     }
   return e;
 }
@@ -1065,29 +1150,33 @@ cudaError_t launch_block_norm_bwd(const moe_handle* h, const moe_block_norm_bwd_
   a.inv_h = 1.0f / q.H;
   a.units = units_of(T, q.H, h->num_sms, &a.teams);
   a.chunk = T > 0 ? (T - 1) / a.units + 1 : 1;
+  // whole groups, where that leaves at most a fifth of the teams without work: none
+  // of them has to be joined then
+  const int64_t whole = (static_cast<int64_t>(a.chunk - 1) / q.gate_tokens + 1) * q.gate_tokens;
+  if (whole * 4 <= static_cast<int64_t>(a.chunk) * 5) a.chunk = static_cast<int>(whole);
   a.blocks = a.units / a.teams;
   a.team_threads = team_threads(q.H);
   a.part = static_cast<float*>(workspace);
   a.slots = a.part + 2 * static_cast<size_t>(a.blocks) * q.H;
   const int threads = a.teams * a.team_threads;
-  const bool gated = q.d_gate != nullptr;
-  using B = __nv_bfloat16;
-  const auto k = bf16 ? (gated ? backward_kernel<B, true>(q.H, threads)
-                               : backward_kernel<B, false>(q.H, threads))
-                      : (gated ? backward_kernel<float, true>(q.H, threads)
-                               : backward_kernel<float, false>(q.H, threads));
+  const GateKind gate = !q.d_gate ? kNoGate : q.gate_tokens == 1 ? kGateRows : kGateGroups;
+  const auto k = bf16 ? backward_kernel<__nv_bfloat16>(gate, q.H, threads)
+                      : backward_kernel<float>(gate, q.H, threads);
   if (T > 0) {
     const cudaError_t e =
         launch_chained(k.kernel, dim3(a.blocks), dim3(threads), k.shared, s, false, a);
     if (e != cudaSuccess) return e;
   }
-  const bool spans = a.ggate && a.gate_tokens > 1;
+  const bool spans = a.ggate && a.gate_tokens > 1 && a.chunk % a.gate_tokens != 0;
   if (!a.gw_post && !a.gw_pre && !spans) return cudaSuccess;
-  const int join_rows = 2 + (!spans ? 0 : a.groups < a.units ? a.groups : a.units);
+  const int items = !spans ? 0 : a.groups < a.units ? a.groups : a.units;
+  int share = 1;  // warps of an item: eight slots each
+  while (share < kJoinWarps && 8 * share * static_cast<int64_t>(a.chunk) < a.gate_tokens) share *= 2;
+  const int rows = 2 + (items * share + kJoinWarps - 1) / kJoinWarps;
   if (T == 0) a.blocks = 0;  // sums of nothing
-  return launch_chained(bf16 ? block_norm_join_kernel<B> : block_norm_join_kernel<float>,
-                        dim3((q.H + kJoinCols - 1) / kJoinCols, join_rows), dim3(32 * kJoinWarps), 0, s, false,
-                        a);
+  return launch_chained(bf16 ? block_norm_join_kernel<__nv_bfloat16> : block_norm_join_kernel<float>,
+                        dim3((q.H + kJoinCols - 1) / kJoinCols, rows), dim3(32 * kJoinWarps), 0, s,
+                        false, a, items, share);
 }
 
 }  // namespace moe
