@@ -37,10 +37,11 @@ constexpr int kMaxTiles = 256;
 constexpr int kFrags = 16;       // fragments that a tile works on at a time
 constexpr int kRows = kWarps + kFrags - 1;  // rows of sums: warp w's of fragment f is w + f
 constexpr int kBwdWarps = 8;     // of a block of the backward
-constexpr int kOffBatch = 1024;  // sequence offsets staged at a time
+constexpr int kOffBatch = 2048;  // sequences whose offsets are kept in shared memory
 constexpr int kJoinWarps = 32;   // of a block of the second kernel
 constexpr int kCluster = 8;      // blocks of the second kernel
-constexpr int kSlots = 12;       // slots that one of its warps loads at a time
+constexpr int kFew = 16;         // sequences that it looks at one by one
+constexpr int kSlots = 5;        // slots that one of its warps loads at a time
 // Tokens a team sums in registers before it adds them to shared memory: bounds
 // the number of fp32 additions in a row however long a tile is.
 constexpr int kFlush = 64;
@@ -52,7 +53,8 @@ struct BalArgs {
   const int32_t* off;    // [S + 1] or NULL: one sequence, all T tokens
   int T, E, K, S;
   int tile, tiles;       // tokens of a tile, tiles
-  int chunks;            // groups of 32 experts
+  int chunks;            // groups of 128 experts
+  int stride;            // of a slot: E rounded up to 4
   int vec;               // rows can be read 16 bytes at a time
   float coef;
   uint32_t* flags;
@@ -60,8 +62,8 @@ struct BalArgs {
   int32_t* cnt;          // [S, E]
   float* prob;           // [S, E] or NULL
   float* loss;           // [1]
-  float* slot_p;         // [2 * tiles, E]
-  int32_t* slot_c;       // [2 * tiles, E]
+  float* slot_p;         // [2 * tiles, stride]
+  int32_t* slot_c;       // [2 * tiles, stride]
   float* tile_loss;      // [tiles] of the sequences inside a tile
   int32_t* tail;         // [tiles] the sequence that begins there and goes on, or -1
   // backward
@@ -78,18 +80,6 @@ __device__ __forceinline__ int2 range_of(int lo, int hi, int T) {
 }
 __device__ __forceinline__ int2 seq_range(const BalArgs& a, int s) {
   return a.off ? range_of(__ldg(a.off + s), __ldg(a.off + s + 1), a.T) : make_int2(0, a.T);
-}
-
-// First sequence that ends behind token t (S if there is none).
-__device__ __forceinline__ int seq_of(const BalArgs& a, int t) {
-  if (!a.off) return t < a.T ? 0 : 1;
-  int lo = 0, hi = a.S;
-  while (lo < hi) {
-    const int mid = (lo + hi) >> 1;
-    if (__ldg(a.off + mid + 1) > t) hi = mid;
-    else lo = mid + 1;
-  }
-  return lo;
 }
 
 template <int LPT>
@@ -516,7 +506,7 @@ __global__ void __launch_bounds__(kThreads, 1) balance_tile_kernel(BalArgs a) {
         if (a.prob) a.prob[at] = p / frag.length[f];
         loss = fmaf(static_cast<float>(c) * p, seq_factor(a, frag.length[f]), loss);
       } else {
-        const size_t at = static_cast<size_t>(2 * blockIdx.x + kind - 1) * a.E + e;
+        const size_t at = static_cast<size_t>(2 * blockIdx.x + kind - 1) * a.stride + e;
         a.slot_p[at] = p;
         a.slot_c[at] = c;
       }
@@ -537,59 +527,72 @@ __global__ void __launch_bounds__(kThreads, 1) balance_tile_kernel(BalArgs a) {
   }
 }
 
-// Sequences that span tiles.  A unit is 32 experts of one of them: `share` warps
-// of a block add up its slots.  Units go round the cluster's blocks; block 0 adds
-// up the loss.
+// Sequences that span tiles.  A unit is 128 experts of one of them, four a lane:
+// `share` warps of a block add up its slots.  Units go round the cluster's blocks;
+// block 0 adds up the loss.
 __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kJoinWarps * 32)
-    balance_join_kernel(BalArgs a, int items, int share) {
-  grid_dependency_wait();
+    balance_join_kernel(BalArgs a, int share) {
   asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-  __shared__ float ps[kJoinWarps][32];
-  __shared__ int cs[kJoinWarps][32];
+  grid_dependency_wait();
+  __shared__ float4 ps[kJoinWarps][32];
+  __shared__ int4 cs[kJoinWarps][32];
   __shared__ int soff[kOffBatch + 1];
   __shared__ int ired[96];
   __shared__ float losses[kJoinWarps], block_loss[kCluster];
+  __shared__ int spans[kMaxTiles];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int rank = blockIdx.x;  // in the one cluster
-  // the tiles' own losses are on their way meanwhile
+  // the tiles' own losses, and the sequences that go on from one
   float loss = 0.0f;
-  if (rank == 0)
-    for (int b = threadIdx.x; b < a.tiles; b += kJoinWarps * 32) loss += __ldcg(a.tile_loss + b);
+  if (rank == 0 && threadIdx.x < a.tiles) loss = __ldcg(a.tile_loss + threadIdx.x);
+  // of a few sequences each is looked at, of many those that go on from a tile
+  const bool few = a.S <= kFew;
+  const int tail = !few && threadIdx.x < a.tiles ? __ldcg(a.tail + threadIdx.x) : -1;
   const Table table = read_table(a, 0, soff, ired);
+  int items = a.S;
+  if (!few) {  // one behind the other
+    const unsigned some = __ballot_sync(kFull, tail >= 0);
+    if (lane == 0) ired[warp] = __popc(some);
+    __syncthreads();
+    const int each = ired[lane];
+    const int before = __reduce_add_sync(kFull, lane < warp ? each : 0);
+    items = __reduce_add_sync(kFull, each);
+    if (tail >= 0) spans[before + __popc(some & lanemask_lt())] = tail;
+    __syncthreads();
+  }
   const int groups = kJoinWarps / share;  // units of a block at a time
   const int units = items * a.chunks;
   for (int n0 = rank * groups; n0 < units; n0 += kCluster * groups) {
     const int n = n0 + warp / share;
-    int s = a.S, chunk = 0;
+    int s = a.S, e = a.E;
     if (n < units) {
-      chunk = n % a.chunks;
-      s = n / a.chunks;
-      // where there are more sequences than tiles: that which goes on from a tile
-      if (a.S > a.tiles) s = __ldcg(a.tail + s);
-      if (s < 0) s = a.S;
+      s = few ? n / a.chunks : min(spans[n / a.chunks], a.S);
+      e = n % a.chunks * 128 + lane * 4;
     }
     int2 r = make_int2(0, 0);
-    if (s < a.S)
-      r = a.S <= kOffBatch ? range_of(soff[s], soff[s + 1], a.T) : seq_range(a, s);
+    if (s < a.S) r = a.S <= kOffBatch ? range_of(soff[s], soff[s + 1], a.T) : seq_range(a, s);
     const int b0 = r.x / a.tile, b1 = r.y > r.x ? (r.y - 1) / a.tile : b0;
-    const int e = chunk * 32 + lane;
     const bool real = b1 > b0 && e < a.E;
-    float p = 0.0f;
-    int c = 0;
+    float4 p{0.0f, 0.0f, 0.0f, 0.0f};
+    int4 c{0, 0, 0, 0};
     for (int b = b0 + warp % share; b <= b1 && real; b += kSlots * share) {
-      float x[kSlots];
-      int y[kSlots];
+      float4 x[kSlots];
+      int4 y[kSlots];
 #pragma unroll
       for (int i = 0; i < kSlots; ++i) {  // all on their way together
         const int bi = b + i * share;
-        const size_t at = static_cast<size_t>(2 * bi + (bi == b0)) * a.E + e;
-        x[i] = bi <= b1 ? __ldcg(a.slot_p + at) : 0.0f;
-        y[i] = bi <= b1 ? __ldcg(a.slot_c + at) : 0;
+        const size_t at = static_cast<size_t>(2 * bi + (bi == b0)) * a.stride + e;
+        x[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        y[i] = make_int4(0, 0, 0, 0);
+        if (bi <= b1) {
+          x[i] = __ldcg(reinterpret_cast<const float4*>(a.slot_p + at));
+          y[i] = __ldcg(reinterpret_cast<const int4*>(a.slot_c + at));
+        }
       }
 #pragma unroll
       for (int i = 0; i < kSlots; ++i) {
-        p += x[i];
-        c += y[i];
+        p = make_float4(p.x + x[i].x, p.y + x[i].y, p.z + x[i].z, p.w + x[i].w);
+        c = make_int4(c.x + y[i].x, c.y + y[i].y, c.z + y[i].z, c.w + y[i].w);
       }
     }
     if (share > 1) {
@@ -600,17 +603,27 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kJoinWarps * 
       if (warp % share == 0) {
 #pragma unroll 4
         for (int w = 1; w < share; ++w) {
-          p += ps[warp + w][lane];
-          c += cs[warp + w][lane];
+          const float4 x = ps[warp + w][lane];
+          const int4 y = cs[warp + w][lane];
+          p = make_float4(p.x + x.x, p.y + x.y, p.z + x.z, p.w + x.w);
+          c = make_int4(c.x + y.x, c.y + y.y, c.z + y.z, c.w + y.w);
         }
       }
     }
     if (real && warp % share == 0) {
       const int n_tokens = r.y - r.x;
-      const size_t at = static_cast<size_t>(s) * a.E + e;
-      a.cnt[at] = c;
-      if (a.prob) a.prob[at] = p / n_tokens;
-      loss = fmaf(static_cast<float>(c) * p, seq_factor(a, n_tokens), loss);
+      const float pe[4] = {p.x, p.y, p.z, p.w}, per_token = 1.0f / n_tokens;
+      const int ce[4] = {c.x, c.y, c.z, c.w};
+      float val = 0.0f;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (e + i >= a.E) break;
+        const size_t at = static_cast<size_t>(s) * a.E + e + i;
+        a.cnt[at] = ce[i];
+        if (a.prob) a.prob[at] = pe[i] * per_token;
+        val = fmaf(static_cast<float>(ce[i]), pe[i], val);
+      }
+      loss = fmaf(val, seq_factor(a, n_tokens), loss);
     }
   }
 #pragma unroll
@@ -664,22 +677,24 @@ __global__ void __launch_bounds__(kBwdWarps * 32, 3) balance_bwd_kernel(BalArgs 
   if (begin >= end) return;
   int2 r = make_int2(0, 0);
   float d[N], factor = 0.0f;  // counts less their mean; the sequence's factor
-  // the sequence of token t, for tokens in order
+  // the sequence of token t, for tokens in order: most often the next one
+  int s = -1;
   auto enter = [&](int t) {
-    int s;
-    if (a.off && a.S <= kOffBatch) {
-      int x = 0, y = a.S;
+    const bool kept = a.off && a.S <= kOffBatch;
+    auto end_of = [&](int n) { return kept ? soff[n + 1] : __ldg(a.off + n + 1); };
+    if (!a.off) {
+      s = 0;
+    } else {
+      int x = s + 1, y = a.S;
+      if (s >= 0 && x < y && end_of(x) > t) y = x;
       while (x < y) {
         const int mid = (x + y) >> 1;
-        if (soff[mid + 1] > t) y = mid;
+        if (end_of(mid) > t) y = mid;
         else x = mid + 1;
       }
       s = min(x, a.S - 1);
-      r = range_of(soff[s], soff[s + 1], a.T);
-    } else {
-      s = min(seq_of(a, t), a.S - 1);
-      r = seq_range(a, s);
     }
+    r = kept ? range_of(soff[s], soff[s + 1], a.T) : seq_range(a, s);
     int c[N];
     load_row<LPT, NV, int4>(a.bcnt + static_cast<size_t>(s) * a.E, a.E, a.vec, true, tl, 0, c);
     const int n = r.y - r.x;
@@ -753,10 +768,10 @@ template <typename F>
 cudaError_t with_team(int E, F&& f) {
   auto c = [&](auto lanes, auto vecs) { return f(lanes, vecs); };
   if (E <= 8) return c(std::integral_constant<int, 2>{}, std::integral_constant<int, 1>{});
-  if (E <= 16) return c(std::integral_constant<int, 4>{}, std::integral_constant<int, 1>{});
-  if (E <= 32) return c(std::integral_constant<int, 8>{}, std::integral_constant<int, 1>{});
-  if (E <= 64) return c(std::integral_constant<int, 16>{}, std::integral_constant<int, 1>{});
-  if (E <= 128) return c(std::integral_constant<int, 32>{}, std::integral_constant<int, 1>{});
+  if (E <= 16) return c(std::integral_constant<int, 2>{}, std::integral_constant<int, 2>{});
+  if (E <= 32) return c(std::integral_constant<int, 4>{}, std::integral_constant<int, 2>{});
+  if (E <= 64) return c(std::integral_constant<int, 8>{}, std::integral_constant<int, 2>{});
+  if (E <= 128) return c(std::integral_constant<int, 16>{}, std::integral_constant<int, 2>{});
   if (E <= 256) return c(std::integral_constant<int, 32>{}, std::integral_constant<int, 2>{});
   if (E <= 384) return c(std::integral_constant<int, 32>{}, std::integral_constant<int, 3>{});
   return c(std::integral_constant<int, 32>{}, std::integral_constant<int, 4>{});
@@ -775,7 +790,8 @@ BalArgs bal_args(const moe_handle* h, const float* logits, int T, const int32_t*
   a.E = h->cfg.num_experts;
   a.K = h->cfg.top_k;
   a.S = S;
-  a.chunks = (a.E + 31) / 32;
+  a.chunks = (a.E + 127) / 128;
+  a.stride = (a.E + 3) / 4 * 4;
   a.coef = static_cast<float>(coef);
   a.flags = h->flags;
   return a;
@@ -813,8 +829,9 @@ BalancePlan balance_plan(int E) {
     o = (o + bytes + 255) / 256 * 256;
     return at;
   };
-  p.slot_p = take(static_cast<size_t>(2 * kMaxTiles) * E * sizeof(float));
-  p.slot_c = take(static_cast<size_t>(2 * kMaxTiles) * E * sizeof(int32_t));
+  const size_t slots = static_cast<size_t>(2 * kMaxTiles) * ((E + 3) / 4 * 4);
+  p.slot_p = take(slots * sizeof(float));
+  p.slot_c = take(slots * sizeof(int32_t));
   p.tile_loss = take(kMaxTiles * sizeof(float));
   p.tail = take(kMaxTiles * sizeof(int32_t));
   p.total = o;
@@ -852,13 +869,12 @@ cudaError_t launch_balance(const moe_handle* h, const float* logits, const int32
     return launch_chained(k, dim3(a.tiles), dim3(kThreads), smem, s, false, a);
   });
   if (e != cudaSuccess || a.tiles == 1) return e;
-  const int items = S < a.tiles ? S : a.tiles;
-  int share = 1;  // warps of a unit: all units in one round where they fit
-  while (share < kJoinWarps && 2 * share * items * a.chunks <= kCluster * kJoinWarps &&
-         share * kSlots * items < a.tiles)
-    share *= 2;
+  // warps of a unit: as many as leave all units in one round
+  const int units = (S < a.tiles ? S : a.tiles) * a.chunks;
+  int share = 1;
+  while (share < kJoinWarps && 2 * share * units <= kCluster * kJoinWarps) share *= 2;
   return launch_chained(balance_join_kernel, dim3(kCluster), dim3(32 * kJoinWarps), 0, s, false, a,
-                        items, share);
+                        share);
 }
 
 cudaError_t launch_balance_bwd(const moe_handle* h, const float* logits, const int32_t* cnt, int T,

@@ -975,7 +975,9 @@ Chosen<NormArgs> forward_kernel(int H, size_t kept, size_t token, size_t most) {
 template <typename Elt>
 Chosen<NormArgs> forward_kernel(int H, int kmax, int threads, int rows, int weights) {
   const size_t kept = kept_bytes(H, weights), token = token_bytes<Elt>(threads, rows);
-  return kmax == 1   ? forward_kernel<Elt, 1>(H, kept, token, kShared)
+  // two blocks an SM where their registers and one token ahead allow it
+  const bool two = kmax == 1 && sizeof(Elt) == 2 && kept + token <= kShared / 2;
+  return kmax == 1   ? forward_kernel<Elt, 1>(H, kept, token, two ? kShared / 2 : kShared)
          : kmax == 8 ? forward_kernel<Elt, 8>(H, kept, token, kShared)
                      : forward_kernel<Elt, 16>(H, kept, token, kShared);
 }
