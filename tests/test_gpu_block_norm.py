@@ -421,3 +421,86 @@ def test_refusals():
         moe.moe_block_norm(h, p.res, o["res_out"], o["x"], y=p.res, w_post=p.w_post, w_pre=p.w_pre.float())
     torch.cuda.synchronize()
     assert moe.moe_read_device_status(h) == 0
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("pad", [1, 16])
+def test_a_training_step_of_a_block(score, pad):
+    """Pre-norm, routing, balance loss, dispatch, experts (here y = v * row), combine
+    with post-norm, gate and residual sum, the next pre-norm; and all of it backward,
+    against fp64 autograd with the routing's choice held fixed.  fp32 rows.  A chain
+    of some twenty fp32 operations whose sums have at most H = 512 terms or K = 4:
+    relative to each gradient's norm 1e-5 covers them (512 * 2^-24 = 3e-5 at worst for
+    one sum, typically its root); what the chain could lose, a term, is of order 1."""
+    T, H, E, K, coef, groups = 200, 512, 16, 4, 0.1, 3
+    g = np.random.default_rng(11)
+    f = lambda *s: g.standard_normal(s)  # noqa: E731
+    res0, wr, v = f(T, H), f(E, H) / np.sqrt(H), 1 + 0.3 * f(E, H)
+    w0, wpost, w1, gate = 1 + 0.1 * f(H), 1 + 0.1 * f(H), 1 + 0.1 * f(H), f(groups, H)
+    gres, gx = f(T, H), f(T, H)
+    off = np.array([0, 70, 70, 200], np.int32)
+    gate_tokens = -(-T // groups)
+    d32 = lambda a: torch.from_numpy(np.ascontiguousarray(a, np.float32)).to(dev())  # noqa: E731
+    r = moe.MoeRouter(E, K, 4, T, score_fn=score, pad_align=pad)
+    # forward
+    _, x0, s0 = r.block_norm(d32(res0), w_pre=d32(w0), eps=EPS, save=True)
+    logits = x0 @ d32(wr).T
+    idx, w = r.route(logits)
+    lay = r.layout(idx)
+    loss, cnt, _ = r.balance(logits, idx, seq_off=torch.from_numpy(off).to(dev()), coef=coef)
+    recv, _, _ = r.dispatch(x0, w)
+    expert = torch.zeros(r.h.recv_rows, dtype=torch.long, device=dev())
+    ends = lay["off_e"].long()
+    expert = torch.searchsorted(ends[1:].contiguous(), torch.arange(r.h.recv_rows, device=dev()), right=True).clamp(max=E - 1)
+    vd = d32(v)
+    y = recv * vd[expert]
+    kw = dict(gate=d32(gate), gate_tokens=gate_tokens, w_post=d32(wpost), res_scale=0.8)
+    res1, x1, s1 = r.block_norm(d32(res0), y, gather=True, cw=w, w_pre=d32(w1), eps=EPS, save=True, **kw)
+    # backward
+    gres1, gc, ggate, gwpost, gw1 = r.block_norm_bwd(d32(gres), d32(gx), s1, w_pre=d32(w1), **kw)
+    gy, gw = r.combine_bwd(gc, y, w)
+    gxd, glogits = r.dispatch_bwd_route(gy * vd[expert], logits, idx, gw)
+    glogits = r.balance_bwd(logits, cnt, seq_off=torch.from_numpy(off).to(dev()), coef=coef, base=glogits)
+    gx0 = gxd + glogits @ d32(wr)
+    gres0, _, _, _, gw0 = r.block_norm_bwd(gres1, gx0, s0, w_pre=d32(w0))
+    gwr = glogits.T @ x0
+    assert moe.moe_read_device_status(r.h) == 0
+    # the same in fp64
+    t = lambda a: torch.tensor(np.float32(a).astype(np.float64), requires_grad=True)  # noqa: E731
+    P = dict(res=t(res0), wr=t(wr), w0=t(w0), wpost=t(wpost), w1=t(w1), gate=t(gate))
+    norm = lambda a, b: a / torch.sqrt((a * a).mean(1, keepdim=True) + EPS) * b  # noqa: E731
+    a0 = norm(P["res"], P["w0"])
+    l = a0 @ P["wr"].T
+    ix = idx.long().cpu()
+    if score == "softmax":
+        p, sel = torch.softmax(l, 1), torch.softmax(torch.gather(l, 1, ix), 1)
+    else:
+        sg = torch.sigmoid(l)
+        p, sel = sg / sg.sum(1, keepdim=True), torch.gather(sg, 1, ix)
+        sel = sel / sel.sum(1, keepdim=True)
+    c = torch.zeros(T, H, dtype=torch.float64)
+    v64 = torch.from_numpy(np.float32(v).astype(np.float64))
+    for k in range(K):
+        c = c + sel[:, k, None] * a0 * v64[ix[:, k]]
+    r1 = 0.8 * P["res"] + P["gate"][torch.arange(T) // gate_tokens] * norm(c, P["wpost"])
+    b1 = norm(r1, P["w1"])
+    L = torch.zeros((), dtype=torch.float64)
+    for q in range(3):
+        a, b = int(off[q]), int(off[q + 1])
+        if b > a:
+            n = torch.bincount(ix[a:b].reshape(-1), minlength=E).double()
+            L = L + coef / 2 * E / (K * (b - a) ** 2) * (n * p[a:b].sum(0)).sum()
+    (L + (r1 * torch.from_numpy(np.float32(gres).astype(float))).sum()
+     + (b1 * torch.from_numpy(np.float32(gx).astype(float))).sum()).backward()
+
+    def close(got, want, what):
+        want = want.detach().numpy()
+        err = np.linalg.norm(f64(got) - want) / np.linalg.norm(want)
+        assert err <= 1e-5, "%s: %.3g" % (what, err)
+
+    close(loss, L.reshape(1), "loss")
+    close(res1, r1, "res1")
+    close(x1, b1, "x1")
+    for got, name in ((gres0, "res"), (gwr, "wr"), (gw0, "w0"), (gwpost, "wpost"), (gw1, "w1"),
+                      (ggate, "gate")):
+        close(got, P[name].grad, name)
