@@ -35,6 +35,7 @@ constexpr int kTeamThreads = 512;  // threads of a block of several teams, at mo
 constexpr int kFlush = 1024;
 constexpr int kJoinWarps = 16, kJoinCols = 64;  // of the kernel that joins the column sums
 constexpr size_t kShared = 224 * 1024;  // dynamic shared memory of a block, at most
+constexpr size_t kSmShared = 228 * 1024;  // of an SM, of which a block takes 1 KB for itself
 
 // ---------------------------------------------------------------------------
 // pairs of fp32
@@ -186,19 +187,25 @@ __device__ __forceinline__ void kept_weights(uint32_t at, uint32_t wb, int i, F2
   }
 }
 
-// Which team a thread is in, and where in it: blocks hold whole teams.
+// Which team a thread is in, and where in it: blocks hold whole teams.  WARP: teams
+// of a warp, or of half or a quarter of one for the narrowest rows.
 template <bool WARP, int MAXT>
 struct Team {
   int threads, index, tid;
   float* red;  // two sets of 32 values, taken in turn (teams of several warps)
   int turn = 0;
+  unsigned lanes;  // the team's, of its warp
   __device__ __forceinline__ Team(int team_threads, float* sums)
-      : threads(WARP ? 32 : team_threads),
-        index(WARP ? threadIdx.x >> 5 : threadIdx.x / team_threads),
-        tid(WARP ? threadIdx.x & 31 : threadIdx.x - index * team_threads),
-        red(sums + 64 * index) {
-    if (!WARP)
+      : threads(team_threads),
+        index(threadIdx.x / team_threads),
+        tid(threadIdx.x - index * team_threads),
+        red(sums + (WARP ? 0 : 64 * index)),
+        lanes(kFull) {
+    if (!WARP) {
       for (int i = tid; i < 64; i += threads) red[i] = 0.0f;
+    } else if (threads < 32) {
+      lanes = ((1u << threads) - 1u) << ((threadIdx.x & 31) - tid);
+    }
   }
   __device__ __forceinline__ void sync() {
     asm volatile("bar.sync %0, %1;" ::"r"(index + 1), "r"(threads) : "memory");
@@ -206,9 +213,12 @@ struct Team {
   // Sum over the team.  A barrier a sum is enough, and the values behind the last
   // warp's stay zero, so that they are read four at a time.
   __device__ __forceinline__ float sum(float v) {
+    if constexpr (WARP) {
+      for (int o = threads >> 1; o > 0; o >>= 1) v += __shfl_xor_sync(lanes, v, o);
+      return v;
+    }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
-    if constexpr (WARP) return v;
     float* set = red + turn;
     turn ^= 32;
     if ((tid & 31) == 0) set[tid >> 5] = v;
@@ -449,7 +459,7 @@ __global__ void __launch_bounds__(MAXT, KMAX == 1 && MAXT <= 512 && sizeof(Elt) 
           c[i][j] = fma2(both(a.res_scale), f[j], c[i][j]);
           ss = fma2(c[i][j], c[i][j], ss);
         }
-        if (in[i]) st_vec(a.res_out + row + at[i], PT::from(c[i]));
+        if (in[i]) st_vec_cs(a.res_out + row + at[i], PT::from(c[i]));
       }
     }
     if (a.x) {
@@ -461,7 +471,7 @@ __global__ void __launch_bounds__(MAXT, KMAX == 1 && MAXT <= 512 && sizeof(Elt) 
         kept_weights<N>(wpre, wb, i, f);
 #pragma unroll
         for (int j = 0; j < P; ++j) f[j] = mul2(mul2(c[i][j], both(r)), f[j]);
-        if (in[i]) st_vec(a.x + row + at[i], PT::from(f));
+        if (in[i]) st_vec_cs(a.x + row + at[i], PT::from(f));
       }
     }
     if (GATHER && AHEAD > 0) {
@@ -923,12 +933,15 @@ __global__ void __launch_bounds__(32 * kJoinWarps)
 
 bool one_warp(int H) { return H <= kWarpRow; }
 
-int team_threads(int H) { return (H + kWarpRow - 1) / kWarpRow * 32; }
+int team_threads(int H) { return H <= 128 ? 8 : H <= 256 ? 16 : (H + kWarpRow - 1) / kWarpRow * 32; }
 
 // Teams of a block for T tokens: as many as it holds, once there is one for every SM.
 int teams_of(int T, int H, int num_sms) {
-  const int most = kTeamThreads / team_threads(H), wanted = (T + num_sms - 1) / num_sms;
-  return most < 1 || wanted < 1 ? 1 : wanted < most ? wanted : most;
+  const int most = kTeamThreads / team_threads(H);
+  int n = (T + num_sms - 1) / num_sms;
+  n = most < 1 || n < 1 ? 1 : n < most ? n : most;
+  const int per_warp = 32 / team_threads(H);  // whole warps
+  return per_warp > 1 ? (n + per_warp - 1) / per_warp * per_warp : n;
 }
 
 // Largest dynamic shared memory for a kernel that takes more than the default.
@@ -976,8 +989,9 @@ template <typename Elt>
 Chosen<NormArgs> forward_kernel(int H, int kmax, int threads, int rows, int weights) {
   const size_t kept = kept_bytes(H, weights), token = token_bytes<Elt>(threads, rows);
   // two blocks an SM where their registers and one token ahead allow it
-  const bool two = kmax == 1 && sizeof(Elt) == 2 && kept + token <= kShared / 2;
-  return kmax == 1   ? forward_kernel<Elt, 1>(H, kept, token, two ? kShared / 2 : kShared)
+  const size_t half = kSmShared / 2 - 1024 - kRed * sizeof(float);
+  const bool two = kmax == 1 && sizeof(Elt) == 2 && kept + token <= half;
+  return kmax == 1   ? forward_kernel<Elt, 1>(H, kept, token, two ? half : kShared)
          : kmax == 8 ? forward_kernel<Elt, 8>(H, kept, token, kShared)
                      : forward_kernel<Elt, 16>(H, kept, token, kShared);
 }
