@@ -34,6 +34,7 @@ constexpr int kTeamThreads = 512;  // threads of a block of several teams, at mo
 // bounds the number of fp32 additions in a row for any T.
 constexpr int kFlush = 1024;
 constexpr int kJoinWarps = 16, kJoinCols = 64;  // of the kernel that joins the column sums
+constexpr int kJoinLoads = 10;  // of a warp at a time: all of an SM's sums in one
 constexpr size_t kShared = 224 * 1024;  // dynamic shared memory of a block, at most
 constexpr size_t kSmShared = 228 * 1024;  // of an SM, of which a block takes 1 KB for itself
 
@@ -153,29 +154,45 @@ __device__ __forceinline__ void st_shared(uint32_t a, float4 v) {
 // DeepSeek-V3 shape.)
 constexpr int kWeightSlots = kEpt / 4;  // 16 fp32
 
-// Keeps the 16 weights of a team's thread from `to` on (rows wb bytes apart), zero
-// behind the row's end; its vectors of N elements are tid, tid + threads, ...
+// The 16 weights of a team's thread on their way from memory to shared memory: asked
+// for ahead of the rows, which the weights would otherwise arrive behind.  Zero
+// behind the row's end; the thread's vectors of N elements are tid, tid + threads, ...
 template <int N>
-__device__ __forceinline__ void keep_weights(const uint8_t* w, int f32, float offset, uint32_t to,
-                                             uint32_t wb, int tid, int threads, int nvec) {
+struct Weights {
+  float4 f[kWeightSlots];
+  __device__ __forceinline__ void load(const uint8_t* w, int f32, int tid, int threads, int nvec) {
 #pragma unroll
-  for (int q = 0; q < kWeightSlots; ++q) {
-    const int v = tid + q / (N / 4) * threads;
-    float4 f{0.0f, 0.0f, 0.0f, 0.0f};
-    if (v < nvec) {
-      const int at = v * (N / 4) + q % (N / 4);
-      if (f32) {
-        f = __ldg(reinterpret_cast<const float4*>(w) + at);
-      } else {
-        const uint2 b = __ldg(reinterpret_cast<const uint2*>(w) + at);
-        f = make_float4(__uint_as_float(b.x << 16), __uint_as_float(b.x & 0xffff0000u),
-                        __uint_as_float(b.y << 16), __uint_as_float(b.y & 0xffff0000u));
+    for (int q = 0; q < kWeightSlots; ++q) {
+      const int v = tid + q / (N / 4) * threads;
+      f[q] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      if (w && v < nvec) {
+        const int at = v * (N / 4) + q % (N / 4);
+        if (f32) {
+          f[q] = __ldg(reinterpret_cast<const float4*>(w) + at);
+        } else {
+          const uint2 b = __ldg(reinterpret_cast<const uint2*>(w) + at);
+          f[q].x = __uint_as_float(b.x);  // spread out when they are kept
+          f[q].y = __uint_as_float(b.y);
+        }
       }
-      f = make_float4(f.x + offset, f.y + offset, f.z + offset, f.w + offset);
     }
-    st_shared(to + q * wb, f);
   }
-}
+  // from `to` on, in rows wb bytes apart
+  __device__ __forceinline__ void keep(int f32, float offset, uint32_t to, uint32_t wb, int tid,
+                                       int threads, int nvec) const {
+#pragma unroll
+    for (int q = 0; q < kWeightSlots; ++q) {
+      float4 x = f[q];
+      if (!f32) {
+        const uint32_t lo = __float_as_uint(x.x), hi = __float_as_uint(x.y);
+        x = make_float4(__uint_as_float(lo << 16), __uint_as_float(lo & 0xffff0000u),
+                        __uint_as_float(hi << 16), __uint_as_float(hi & 0xffff0000u));
+      }
+      const float o = tid + q / (N / 4) * threads < nvec ? offset : 0.0f;
+      st_shared(to + q * wb, make_float4(x.x + o, x.y + o, x.z + o, x.w + o));
+    }
+  }
+};
 // The weights of the thread's vector i.
 template <int N>
 __device__ __forceinline__ void kept_weights(uint32_t at, uint32_t wb, int i, F2* f) {
@@ -341,6 +358,11 @@ __global__ void __launch_bounds__(MAXT, KMAX == 1 && MAXT <= 512 && sizeof(Elt) 
     for (int k = 0; k < KMAX; ++k) wk[k] = p[k] < 0 ? 0.0f : a.cw ? read[k] : 1.0f;
   };
 
+  Weights<N> post, pre;
+  if (team.index == 0) {
+    post.load(a.w_post, a.w_f32, tid, step, a.nvec);
+    pre.load(a.w_pre, a.w_f32, tid, step, a.nvec);
+  }
   if (AHEAD > 0) {
     if (GATHER) {
       read_entries(unit, a.pos, p, -1);
@@ -362,8 +384,8 @@ __global__ void __launch_bounds__(MAXT, KMAX == 1 && MAXT <= 512 && sizeof(Elt) 
   }
   // each thread of the first team for its places in all teams
   if (team.index == 0) {
-    if (a.w_post) keep_weights<N>(a.w_post, a.w_f32, a.offset, wpost, wb, tid, step, a.nvec);
-    if (a.w_pre) keep_weights<N>(a.w_pre, a.w_f32, a.offset, wpre, wb, tid, step, a.nvec);
+    if (a.w_post) post.keep(a.w_f32, a.offset, wpost, wb, tid, step, a.nvec);
+    if (a.w_pre) pre.keep(a.w_f32, a.offset, wpre, wb, tid, step, a.nvec);
   }
   __syncthreads();
   uint32_t stage = ring;
@@ -594,6 +616,13 @@ __global__ void __launch_bounds__(MAXT, 1) block_norm_bwd_kernel(NormBwdArgs a) 
     }
   };
   int64_t row = begin * a.row_bytes;
+  float r_pre = a.gx && begin < end ? __ldg(a.rstd_pre + begin) : 0.0f;
+  float r_post = a.w_post && begin < end ? __ldg(a.rstd_post + begin) : 1.0f;
+  Weights<N> post, pre;
+  if (team.index == 0) {
+    post.load(a.w_post, a.w_f32, tid, step, a.nvec);
+    pre.load(a.gx ? a.w_pre : nullptr, a.w_f32, tid, step, a.nvec);
+  }
   if (AHEAD > 0)
 #pragma unroll
     for (int n = 0; n < AHEAD; ++n) {
@@ -605,11 +634,9 @@ __global__ void __launch_bounds__(MAXT, 1) block_norm_bwd_kernel(NormBwdArgs a) 
       if (real) fetch(!PARTS, true, row + n * a.row_bytes, ring + n * token);
       commit_copies();
     }
-  float r_pre = a.gx && begin < end ? __ldg(a.rstd_pre + begin) : 0.0f;
-  float r_post = a.w_post && begin < end ? __ldg(a.rstd_post + begin) : 1.0f;
   if (team.index == 0) {
-    if (a.w_post) keep_weights<N>(a.w_post, a.w_f32, a.offset, wpost, wb, tid, step, a.nvec);
-    if (a.gx) keep_weights<N>(a.w_pre, a.w_f32, a.offset, wpre, wb, tid, step, a.nvec);
+    if (a.w_post) post.keep(a.w_f32, a.offset, wpost, wb, tid, step, a.nvec);
+    if (a.gx) pre.keep(a.w_f32, a.offset, wpre, wb, tid, step, a.nvec);
   }
   __syncthreads();
   F2 gpost[V][P], gpre[V][P], A[V][P];
@@ -905,14 +932,22 @@ __global__ void __launch_bounds__(32 * kJoinWarps)
     head = 1;
   }
   float2 p{0.0f, 0.0f};
-  if (from && col < a.H)
-#pragma unroll 8
-    for (int u = u0 + warp % share; u < u1; u += share) {
-      const float2 x = __ldcg(reinterpret_cast<const float2*>(
-          from + static_cast<size_t>(stride * u + (u == u0 ? head : 0)) * a.H + col));
-      p.x += x.x;
-      p.y += x.y;
+  for (int ub = u0 + warp % share; ub < u1 && from && col < a.H; ub += kJoinLoads * share) {
+    float2 x[kJoinLoads];
+#pragma unroll
+    for (int i = 0; i < kJoinLoads; ++i) {  // all on their way together
+      const int u = ub + i * share;
+      x[i] = make_float2(0.0f, 0.0f);
+      if (u < u1)
+        x[i] = __ldcg(reinterpret_cast<const float2*>(
+            from + static_cast<size_t>(stride * u + (u == u0 ? head : 0)) * a.H + col));
     }
+#pragma unroll
+    for (int i = 0; i < kJoinLoads; ++i) {
+      p.x += x[i].x;
+      p.y += x[i].y;
+    }
+  }
   ps[warp][lane] = p;
   __syncthreads();
   if (!from || warp % share != 0 || col >= a.H) return;
