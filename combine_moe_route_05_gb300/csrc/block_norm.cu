@@ -233,23 +233,24 @@ struct Team {
     if constexpr (WARP) {
       for (int o = threads >> 1; o > 0; o >>= 1) v += __shfl_xor_sync(lanes, v, o);
       return v;
-    }
+    } else {
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
-    float* set = red + turn;
-    turn ^= 32;
-    if ((tid & 31) == 0) set[tid >> 5] = v;
-    sync();
-    float4 a = *reinterpret_cast<const float4*>(set);
+      for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
+      float* set = red + turn;
+      turn ^= 32;
+      if ((tid & 31) == 0) set[tid >> 5] = v;
+      sync();
+      float4 a = *reinterpret_cast<const float4*>(set);
 #pragma unroll
-    for (int w = 4; w < MAXT / 32; w += 4) {
-      const float4 b = *reinterpret_cast<const float4*>(set + w);
-      a.x += b.x;
-      a.y += b.y;
-      a.z += b.z;
-      a.w += b.w;
+      for (int w = 4; w < MAXT / 32; w += 4) {
+        const float4 b = *reinterpret_cast<const float4*>(set + w);
+        a.x += b.x;
+        a.y += b.y;
+        a.z += b.z;
+        a.w += b.w;
+      }
+      return (a.x + a.y) + (a.z + a.w);
     }
-    return (a.x + a.y) + (a.z + a.w);
   }
 };
 constexpr int kRed = 64 * 8;  // eight teams of two warps at most

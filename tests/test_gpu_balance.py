@@ -173,6 +173,24 @@ def test_masked_experts_and_rows(E, score):
 
 
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_masks_of_the_lowest_value(score):
+    p = Problem(300, 40, 2, score, seed=3)
+    low = np.finfo(np.float32).min
+    p.logits[:, 7] = low
+    p.logits[5:9, : 39] = low
+    loss, cnt, prob = p.forward()
+    wl, wc, wp = ref.balance(p.logits, p.idx, p.off, 40, score, 0.02)
+    assert np.array_equal(to_host(cnt), wc)
+    # 2 (2 + 1.16 x) ulp for unmasked logits, which are within x = 10 of each other
+    rel = 2 * (2 + 1.16 * 10) * 2.0 ** -23 + ref.CHAIN * ref.U32
+    assert (np.abs(to_host(prob) - wp) <= rel * wp + ref.TINY).all() and (to_host(prob)[0, 7] == 0)
+    assert abs(float(loss) - wl) <= (rel + 40 * ref.U32) * wl
+    g = to_host(p.backward(cnt))
+    assert np.isfinite(g).all() and (g[:, 7] == 0).all()
+    assert moe.moe_read_device_status(p.r.h) == 0
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
 def test_nan_and_inf_logits_are_flagged_and_count_for_nothing(score):
     for value in (np.nan, np.inf):
         p = Problem(300, 24, 2, score, seed=4)
@@ -296,6 +314,31 @@ def test_two_calls_at_once():
     torch.cuda.synchronize()
     for n, out in enumerate(outs):
         assert torch.equal(out[0], want[n % 2][0]) and torch.equal(out[1], want[n % 2][1])
+
+
+def test_two_graphs_replayed_at_once():
+    """Each with its own workspace, on one handle."""
+    ps = [Problem(5000, 64, 4, "softmax", offsets([1500 + i, 3000]), seed=i) for i in range(2)]
+    h = ps[0].r.h
+    graphs, outs = [], []
+    want = [p.forward() for p in ps]
+    for p in ps:
+        l, i, o, ws = to_dev(p.logits), to_dev(p.idx), to_dev(p.off), moe.balance_workspace(h, 2)
+        out = (torch.empty(1, device=dev()), torch.empty(2, 64, dtype=torch.int32, device=dev()))
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            moe.moe_balance(h, l, i, out[0], out[1], ws, seq_off=o, coef=0.02)
+        graphs.append((g, l, i, o, ws))
+        outs.append(out)
+    streams = [torch.cuda.Stream() for _ in ps]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for (g, *_), st in zip(graphs, streams):
+            with torch.cuda.stream(st):
+                g.replay()
+    torch.cuda.synchronize()
+    for o, w in zip(outs, want):
+        assert torch.equal(o[0], w[0]) and torch.equal(o[1], w[1])
 
 
 def test_methods_allocate_what_they_return():

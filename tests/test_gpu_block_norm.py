@@ -201,6 +201,24 @@ def test_column_sums_over_units_and_groups(T, H, dtype, gate):
     Problem(T, H, dtype, gate=gate, seed=gate).check_backward()
 
 
+@pytest.mark.parametrize("H,dtype", [(7168, "bf16"), (7168, "f32"), (4096, "f32"), (9000, "bf16"),
+                                     (16384, "bf16"), (104, "bf16"), (256, "f32")])
+@pytest.mark.parametrize("gate", [0, 1, 5, 300])
+def test_many_tokens_a_team(H, dtype, gate):
+    """Several tokens a team, so that places in shared memory are taken again."""
+    p = Problem(700 if H > 1000 else 20000, H, dtype, gate=gate, seed=H + gate)
+    p.check_forward()
+    p.check_backward()
+
+
+@pytest.mark.parametrize("T,H,dtype,K,add", [
+    (700, 2056, "bf16", 8, False), (500, 7168, "bf16", 8, True), (900, 1500, "f32", 5, True),
+    (500, 7168, "f32", 3, False), (400, 9000, "bf16", 2, True), (900, 2048, "bf16", 16, False),
+    (30000, 96, "bf16", 4, True)])
+def test_many_tokens_of_receive_rows_a_team(T, H, dtype, K, add):
+    Problem(T, H, dtype, K=K, E=24, add=add, drop=0.05, gate=0, seed=T).check_forward()
+
+
 def test_column_sums_of_very_many_tokens():
     """Units of more tokens than are added up in registers, with groups that
     end inside one."""
@@ -314,6 +332,29 @@ def test_two_backward_calls_at_once():
     torch.cuda.synchronize()
     for n, o in enumerate(outs):
         assert all(torch.equal(o[k], want[n % 2][k]) for k in o)
+
+
+def test_two_graphs_replayed_at_once():
+    """Each with its own workspace, on one handle."""
+    ps = [Problem(900, 1024, gate=200, seed=i) for i in range(2)]
+    ps[1].r = ps[0].r
+    saved = [p.saved() for p in ps]
+    want = [p.backward(s) for p, s in zip(ps, saved)]
+    graphs, outs = [], []
+    for p, s in zip(ps, saved):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(p.backward(s))
+        graphs.append(g)
+    streams = [torch.cuda.Stream() for _ in ps]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for g, st in zip(graphs, streams):
+            with torch.cuda.stream(st):
+                g.replay()
+    torch.cuda.synchronize()
+    for o, w in zip(outs, want):
+        assert all(torch.equal(o[k], w[k]) for k in w)
 
 
 def test_methods_give_the_same():
