@@ -656,6 +656,17 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kJoinWarps * 
 template <int LPT, int NV, bool SIGMOID>
 __global__ void __launch_bounds__(kBwdWarps * 32, 3) balance_bwd_kernel(BalArgs a) {
   constexpr int N = 4 * NV, TPW = 32 / LPT, U = NV < 3 ? 2 : 1;
+  // about the block's rows come into L2 while the kernel in front ends and the
+  // offsets are read
+  if (threadIdx.x == 0) {
+    const int64_t rows = (static_cast<int64_t>(a.T) - 1) / gridDim.x + 1;
+    const int64_t t = blockIdx.x * rows, n = min(rows, a.T - t);
+    if (n > 0) {
+      prefetch_l2(a.logits + t * a.E, min(n * a.E * 4, kAhead / 2));
+      if (a.base) prefetch_l2(a.base + t * a.E, min(n * a.E * 4, kAhead / 2));
+    }
+  }
+  grid_dependency_wait();
   __shared__ int soff[kOffBatch + 1];
   __shared__ int ired[96];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -897,8 +908,8 @@ cudaError_t launch_balance_bwd(const moe_handle* h, const float* logits, const i
                      : balance_bwd_kernel<lanes(), vecs(), false>;
     const int64_t blocks = (static_cast<int64_t>(T) + kBwdWarps * TPW - 1) / (kBwdWarps * TPW);
     const int64_t most = 3LL * h->num_sms;
-    k<<<static_cast<unsigned>(blocks < most ? blocks : most), kBwdWarps * 32, 0, s>>>(a);
-    return cudaGetLastError();
+    return launch_chained(k, dim3(static_cast<unsigned>(blocks < most ? blocks : most)),
+                          dim3(kBwdWarps * 32), 0, s, false, a);
   });
 }
 
