@@ -652,10 +652,16 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kJoinWarps * 
   }
 }
 
+// Blocks of the backward an SM: registers for four but with the widest rows, a token
+// a warp at a time.  Two tokens at a time on three blocks took 12.9 against 11.5 us
+// (DeepSeek-V3 shape, packed) and 4.2 against 3.6 (Qwen3-30B shape).
+template <int NV>
+constexpr int kBwdBlocks = NV < 4 ? 4 : 3;
+
 // Backward: a team of lanes a token, a warp's tokens in a row.
 template <int LPT, int NV, bool SIGMOID>
-__global__ void __launch_bounds__(kBwdWarps * 32, 3) balance_bwd_kernel(BalArgs a) {
-  constexpr int N = 4 * NV, TPW = 32 / LPT, U = NV < 3 ? 2 : 1;
+__global__ void __launch_bounds__(kBwdWarps * 32, kBwdBlocks<NV>) balance_bwd_kernel(BalArgs a) {
+  constexpr int N = 4 * NV, TPW = 32 / LPT;
   // about the block's rows come into L2 while the kernel in front ends and the
   // offsets are read
   if (threadIdx.x == 0) {
@@ -715,59 +721,48 @@ __global__ void __launch_bounds__(kBwdWarps * 32, 3) balance_bwd_kernel(BalArgs 
     factor = n > 0 ? g * seq_factor(a, n) : 0.0f;
   };
   bool entered = false;
-  for (int64_t tt = begin; tt < end; tt += U * TPW) {
-    float v[U][N], base[U][N], q[N];
+  for (int64_t tt = begin; tt < end; tt += TPW) {
+    float v[N], o[N], q[N];
+    const int64_t t64 = tt + team;
+    const bool live = t64 < end;
+    const size_t at = static_cast<size_t>(live ? t64 : begin) * a.E;
+    auto load = [&](float (&to)[N]) {
+      load_row<LPT, NV, float4>(a.logits + at, a.E, a.vec, live, tl, -kInf, to);
+    };
+    load(v);
+    if (a.base) {
+      load_base<LPT, NV>(a.base + at, a.E, a.vec, live, tl, o);
+    } else {
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int64_t t = tt + u * TPW + team;
-      const int64_t at = (t < end ? t : begin) * a.E;
-      load_row<LPT, NV, float4>(a.logits + at, a.E, a.vec, t < end, tl, -kInf, v[u]);
-      if (a.base) {
-        load_base<LPT, NV>(a.base + at, a.E, a.vec, t < end, tl, base[u]);
+      for (int i = 0; i < N; ++i) o[i] = 0.0f;
+    }
+    if (live && (!entered || t64 >= r.y)) {
+      enter(static_cast<int>(t64));
+      entered = true;
+    }
+    __syncwarp();
+    bool bad;
+    const float inv = probabilities<LPT, NV, SIGMOID, true>(v, q, live, bad, load);
+    if (bad && tl == 0) raise_flag(a.flags, MOE_DEVERR_NONFINITE);
+    float dot = 0.0f;
+#pragma unroll
+    for (int i = 0; i < N; ++i) dot = fmaf(v[i], live ? d[i] : 0.0f, dot);
+    dot = team_sum<LPT>(dot) * inv;
+    const float scale = factor * inv;
+    if (!live) continue;
+#pragma unroll
+    for (int i = 0; i < N; ++i) o[i] = fmaf(scale * (SIGMOID ? q[i] : v[i]), d[i] - dot, o[i]);
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int c = col_of<LPT>(tl, 4 * j);
+      if (a.vec) {
+        if (c < a.E)
+          *reinterpret_cast<float4*>(a.glogits + at + c) =
+              make_float4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
       } else {
 #pragma unroll
-        for (int i = 0; i < N; ++i) base[u][i] = 0.0f;
-      }
-    }
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int64_t t64 = tt + u * TPW + team;
-      const bool live = t64 < end;
-      const int t = static_cast<int>(t64);
-      if (live && (!entered || t >= r.y)) {
-        enter(t);
-        entered = true;
-      }
-      __syncwarp();
-      bool bad;
-      const float inv = probabilities<LPT, NV, SIGMOID, true>(
-          v[u], q, live, bad, [&](float (&to)[N]) {
-            load_row<LPT, NV, float4>(a.logits + (live ? t64 : begin) * a.E, a.E, a.vec, live, tl,
-                                      -kInf, to);
-          });
-      if (bad && tl == 0) raise_flag(a.flags, MOE_DEVERR_NONFINITE);
-      float dot = 0.0f;
-#pragma unroll
-      for (int i = 0; i < N; ++i) dot = fmaf(v[u][i], live ? d[i] : 0.0f, dot);
-      dot = team_sum<LPT>(dot) * inv;
-      const float scale = factor * inv;
-      if (!live) continue;
-      const size_t at = static_cast<size_t>(t) * a.E;
-#pragma unroll
-      for (int i = 0; i < N; ++i)
-        base[u][i] = fmaf(scale * (SIGMOID ? q[i] : v[u][i]), d[i] - dot, base[u][i]);
-#pragma unroll
-      for (int j = 0; j < NV; ++j) {
-        const int c = col_of<LPT>(tl, 4 * j);
-        const float* o = base[u] + 4 * j;
-        if (a.vec) {
-          if (c < a.E)
-            *reinterpret_cast<float4*>(a.glogits + at + c) = make_float4(o[0], o[1], o[2], o[3]);
-        } else {
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            if (c + i < a.E) a.glogits[at + c + i] = o[i];
-        }
+        for (int i = 0; i < 4; ++i)
+          if (c + i < a.E) a.glogits[at + c + i] = o[4 * j + i];
       }
     }
   }
@@ -907,7 +902,7 @@ cudaError_t launch_balance_bwd(const moe_handle* h, const float* logits, const i
     auto k = sigmoid ? balance_bwd_kernel<lanes(), vecs(), true>
                      : balance_bwd_kernel<lanes(), vecs(), false>;
     const int64_t blocks = (static_cast<int64_t>(T) + kBwdWarps * TPW - 1) / (kBwdWarps * TPW);
-    const int64_t most = 3LL * h->num_sms;
+    const int64_t most = static_cast<int64_t>(kBwdBlocks<vecs()>) * h->num_sms;
     return launch_chained(k, dim3(static_cast<unsigned>(blocks < most ? blocks : most)),
                           dim3(kBwdWarps * 32), 0, s, false, a);
   });
