@@ -18,10 +18,17 @@
 // them.  Every sum has a fixed order (counts are integers), so repeated calls
 // give the same bits.
 //
-// Both passes read the logits once and are bound by HBM at the largest sizes,
-// below some 20 MB by the chain of dependent loads around that: offsets, logits,
-// slots.  So offsets are read by all threads at once and searched in shared
-// memory, and a warp loads several tokens' logits before it works on the first.
+// Both passes read the logits once and are bound by HBM at the largest sizes, below
+// some 20 MB by the chain of dependent loads around that: offsets, logits, slots.  So
+// logits come into L2 before the offsets are known, offsets are read by all threads
+// at once and searched in shared memory, and a tile's fragments are worked on
+// together.
+//
+// us (replayed in a graph, logits from HBM; floor: the bytes at the copy rate): 131072
+// tokens x 512 experts 52.3 (40.8), the DeepSeek-V3 shape (16384 x 256, sigmoid) packed
+// in 9 sequences 14.7 (2.4): 1.2 offsets, 4.6 tiles, 1.5 their sums, 0.5 the hand-over to
+// the second kernel, 6 that one.  Backward of the latter, added to another gradient, 11.5
+// (6.9), of 8192 x 128 3.6 (1.3).
 #include <type_traits>
 
 #include "common.cuh"

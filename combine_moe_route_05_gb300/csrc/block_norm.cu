@@ -6,18 +6,25 @@
 //   res' = res_scale * res + gate * (c r_c (w_post + offset))
 //   x    = res' r_p (w_pre + offset),    r_v = 1 / sqrt(mean(v^2) + eps)
 //
-// One pass over the rows: a team of threads (a warp, or a block) holds a row in
-// registers, 16 elements a thread, and the two sums of squares are its only
-// exchange.  x is made from the sum before that is rounded; sums are fp32, each
-// output is rounded once.
+// One pass over the rows: a team of threads (8 to 32 lanes of a warp, or the warps of
+// a block, several teams to a block) holds a row in registers, 16 elements a thread,
+// and the two sums of squares are its only exchange.  x is made from the sum before
+// that is rounded; sums are fp32, each output is rounded once.
 //
 // Bound by HBM; what stands in its way are the two sums in a row's chain.  Each
 // thread therefore copies the vectors that it will need itself into shared memory
 // ahead of time (cp.async: no other thread waits for them), so loads go on while
-// the team waits for its sums, and its weights, in fp32 with their offset, stay
-// there too.  Arithmetic is on pairs of fp32 (one instruction for both), which
-// halves what the issue slots have to do: without it the backward took 52
-// instructions an element and ran at half of the copy rate.
+// the team waits for its sums, and the weights, in fp32 with their offset, stay
+// there too, once for all teams of a block.  Nothing else that a token needs (row
+// positions, scores, the norms' factors) is read in the token's own chain, and no
+// division is left in it.  Arithmetic is on pairs of fp32, one instruction for both.
+//
+// DeepSeek-V3 shape (16384 tokens of 7168, bf16), us against the 457 and 211 of the
+// bytes at the copy rate: the combine's sum of 8 rows with shared experts, both norms
+// and what the backward needs 738 as plain loads in registers, 672 with the copies
+// ahead, 458 with nothing read in the chain, 437 now; the backward 549, 302, 225, 216.
+// Token rows alone 150 (141), the backward of 8192 x 2048 with a gate row for 1300
+// tokens 41.8 (30.2), of which some 9 are the first rows' and the joins' latency.
 #include <mutex>
 
 #include "common.cuh"

@@ -552,9 +552,10 @@ moe_status moe_layer(const moe_handle* h, const moe_layer_args* args, int32_t T,
  *     Offsets that fall or lie outside [0,T] are flagged (MOE_DEVERR_BAD_LAYOUT)
  *     and the results unspecified.
  *   d_loss fp32 [1], d_cnt int32 [num_seqs, E], d_prob fp32 [num_seqs, E].
- * d_workspace: moe_balance_workspace_bytes(c, num_seqs) bytes (for any T),
- * 256-byte aligned, free after the call's work; calls that may overlap on the
- * GPU need one each.  The handle's layout is neither read nor changed.
+ * coef is finite in fp32; T > max_tokens is MOE_ERR_CAPACITY.  d_workspace:
+ * moe_balance_workspace_bytes(c, num_seqs) bytes (for any T), 256-byte aligned,
+ * free after the call's work; calls that may overlap on the GPU need one each.
+ * The handle's layout is neither read nor changed.
  */
 size_t moe_balance_workspace_bytes(const moe_config* c, int32_t num_seqs);
 
@@ -601,9 +602,10 @@ moe_status moe_balance_bwd(const moe_handle* h, const float* d_logits, const int
  *   d_res_out [T,H] (may be d_res), d_x [T,H] or NULL, and for the backward,
  *     each may be NULL: d_c [T,H] (may be d_add, or without gather d_y),
  *     d_rstd_post, d_rstd_pre [T] fp32.
- * All rows in `dtype`, H at most MOE_NORM_MAX_WIDTH; res_scale finite, eps > 0.
- * The square of a row's values must not overflow fp32 (|v| < 1e17).  Without gather the handle's layout is neither read
- * nor changed.
+ * All rows in `dtype`, H at most MOE_NORM_MAX_WIDTH; res_scale finite, eps > 0;
+ * T > max_tokens is MOE_ERR_CAPACITY.  A row's sum of squares must not overflow
+ * fp32 (|v| < 1e17 is enough); a row with NaN or infinity spoils no other.  Without
+ * gather the handle's layout is neither read nor changed.
  */
 #define MOE_NORM_MAX_WIDTH 16384
 
@@ -652,9 +654,10 @@ moe_status moe_block_norm(const moe_handle* h, const moe_block_norm_args* args, 
  *   Outputs, each may be NULL: d_gres [T,H] (may be d_gres_out), d_gy [T,H],
  *     d_ggate (as d_gate, in dtype), d_gw_post and d_gw_pre [H] fp32.
  * Sums over tokens are fp32 and in a fixed order: the same inputs give the same
- * bits.  d_workspace: moe_block_norm_workspace_bytes(h, T, H, gate_tokens)
- * bytes (which does not fall as T grows), 256-byte aligned, free after the
- * call's work; calls that may overlap on the GPU need one each.
+ * bits.  No other output may share memory with an input.  d_workspace:
+ * moe_block_norm_workspace_bytes(h, T, H, gate_tokens) bytes (which does not fall
+ * as T grows), 256-byte aligned, free after the call's work; calls that may overlap
+ * on the GPU need one each.
  */
 typedef struct moe_block_norm_bwd_args {
   const void* d_gres_out;
