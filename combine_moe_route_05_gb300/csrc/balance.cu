@@ -40,15 +40,15 @@ namespace {
 constexpr unsigned kFull = 0xffffffffu;
 constexpr int kWarps = 32;       // of a tile's block: one an SM
 constexpr int kThreads = kWarps * 32;
-constexpr int kMaxTiles = 256;
+constexpr int kMaxTiles = 160;
 constexpr int kFrags = 16;       // fragments that a tile works on at a time
 constexpr int kRows = kWarps + kFrags - 1;  // rows of sums: warp w's of fragment f is w + f
 constexpr int kBwdWarps = 8;     // of a block of the backward
 constexpr int kOffBatch = 2048;  // sequences whose offsets are kept in shared memory
 constexpr int kJoinWarps = 32;   // of a block of the second kernel
 constexpr int kCluster = 8;      // blocks of the second kernel
-constexpr int kFew = 16;         // sequences that it looks at one by one
-constexpr int kSlots = 5;        // slots that one of its warps loads at a time
+constexpr int kShare = kMaxTiles / kJoinWarps;  // tiles of one of its warps
+constexpr int kJoinRows = kJoinWarps + kMaxTiles;
 // Tokens a team sums in registers before it adds them to shared memory: bounds
 // the number of fp32 additions in a row however long a tile is.
 constexpr int kFlush = 64;
@@ -60,7 +60,6 @@ struct BalArgs {
   const int32_t* off;    // [S + 1] or NULL: one sequence, all T tokens
   int T, E, K, S;
   int tile, tiles;       // tokens of a tile, tiles
-  int chunks;            // groups of 128 experts
   int stride;            // of a slot: E rounded up to 4
   int vec;               // rows can be read 16 bytes at a time
   float coef;
@@ -72,7 +71,9 @@ struct BalArgs {
   float* slot_p;         // [2 * tiles, stride]
   int32_t* slot_c;       // [2 * tiles, stride]
   float* tile_loss;      // [tiles] of the sequences inside a tile
-  int32_t* tail;         // [tiles] the sequence that begins there and goes on, or -1
+  int4* spans;           // [tiles] {a fragment that began earlier, the sequence that begins
+                         // here and goes on or -1, its length, its last tile}
+  int32_t* full;         // [1] sequences that are not empty
   // backward
   const int32_t* bcnt;   // [S, E]
   const float* gloss;    // [1] or NULL: 1
@@ -344,6 +345,7 @@ struct Fragments {
   int length[kFrags];    // of the sequence
   int kind[kFrags];      // 0: the whole sequence; 1: it began in an earlier tile; 2: it goes on
   int next_seq, next_token;
+  int last_tile;         // of the last one's sequence
 };
 
 // Finds the next fragments of tokens [cursor, t1), from sequence s on, by one warp.
@@ -373,6 +375,7 @@ __device__ __forceinline__ void find_fragments(const BalArgs& a, const int* soff
         f->end[n] = end;
         f->length[n] = hi - lo;
         f->kind[n] = lo < t0 ? 1 : hi > t1 ? 2 : 0;
+        f->last_tile = (hi - 1) / a.tile;
       }
       cursor = end;
       if (++n == kFrags) done = k + 1;
@@ -430,7 +433,8 @@ __global__ void __launch_bounds__(kThreads, 1) balance_tile_kernel(BalArgs a) {
   }
   if (blockIdx.x == 0 && threadIdx.x == 0 && table.wrong) raise_flag(a.flags, MOE_DEVERR_BAD_LAYOUT);
   float loss = 0.0f;  // the thread's part
-  int tail = -1, next_seq = table.first, next_token = t0;
+  int4 span = make_int4(0, -1, 0, 0);
+  int next_seq = table.first, next_token = t0;
   while (next_seq < a.S && next_token < t1) {
     if (warp == 0) find_fragments(a, soff, next_seq, next_token, t0, t1, &frag);
     __syncthreads();
@@ -518,10 +522,24 @@ __global__ void __launch_bounds__(kThreads, 1) balance_tile_kernel(BalArgs a) {
         a.slot_c[at] = c;
       }
     }
-    if (frag.kind[nf - 1] == 2) tail = frag.seq[nf - 1];
+    if (frag.kind[0] == 1) span.x = 1;
+    if (frag.kind[nf - 1] == 2)
+      span = make_int4(span.x, frag.seq[nf - 1], frag.length[nf - 1], frag.last_tile);
     next_seq = frag.next_seq;
     next_token = frag.next_token;
     __syncthreads();  // stage, hist and frag are taken up again
+  }
+  if (gridDim.x > 1) {
+    // slots without a fragment: the second kernel asks for them as well, and lines
+    // that were written lately it finds in L2
+    for (int i = threadIdx.x; i < 2 * a.stride; i += kThreads) {
+      const bool head = i < a.stride;
+      if (head ? span.x == 0 : span.y < 0) {
+        const size_t at = static_cast<size_t>(2 * blockIdx.x) * a.stride + i;
+        a.slot_p[at] = 0.0f;
+        a.slot_c[at] = 0;
+      }
+    }
   }
   loss = block_sum(loss, red);
   if (threadIdx.x == 0) {
@@ -529,109 +547,144 @@ __global__ void __launch_bounds__(kThreads, 1) balance_tile_kernel(BalArgs a) {
       *a.loss = table.full > 0 ? a.coef * loss / table.full : 0.0f;
     } else {
       a.tile_loss[blockIdx.x] = loss;
-      a.tail[blockIdx.x] = tail;
+      a.spans[blockIdx.x] = span;
+      if (blockIdx.x == 0) *a.full = table.full;
     }
   }
 }
 
-// Sequences that span tiles.  A unit is 128 experts of one of them, four a lane:
-// `share` warps of a block add up its slots.  Units go round the cluster's blocks;
-// block 0 adds up the loss.
+// Sequences that span tiles: adds up their slots.  Each block of the cluster has 32 C
+// experts, C a lane, each warp kShare tiles at most, whose slots it asks for at once
+// with what the tiles noted down.  A warp's tiles hold runs of slots of one sequence
+// each; sequence f of those that span tiles has its run of warp w in row w + f, as
+// both rise with the tokens, and its sum is that of rows in a row.  Block 0 adds up
+// the loss.
+template <int C>
 __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kJoinWarps * 32)
-    balance_join_kernel(BalArgs a, int share) {
+    balance_join_kernel(BalArgs a) {
   asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
   grid_dependency_wait();
-  __shared__ float4 ps[kJoinWarps][32];
-  __shared__ int4 cs[kJoinWarps][32];
-  __shared__ int soff[kOffBatch + 1];
-  __shared__ int ired[96];
+  extern __shared__ float dyn[];
+  float* ps = dyn;                                                    // [kJoinRows][32 * C]
+  int* cs = reinterpret_cast<int*>(dyn + kJoinRows * 32 * C);         // the same
+  __shared__ int item_seq[kMaxTiles], item_length[kMaxTiles], item_first[kMaxTiles],
+      item_last[kMaxTiles];
   __shared__ float losses[kJoinWarps], block_loss[kCluster];
-  __shared__ int spans[kMaxTiles];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int rank = blockIdx.x;  // in the one cluster
-  // the tiles' own losses, and the sequences that go on from one
-  float loss = 0.0f;
-  if (rank == 0 && threadIdx.x < a.tiles) loss = __ldcg(a.tile_loss + threadIdx.x);
-  // of a few sequences each is looked at, of many those that go on from a tile
-  const bool few = a.S <= kFew;
-  const int tail = !few && threadIdx.x < a.tiles ? __ldcg(a.tail + threadIdx.x) : -1;
-  const Table table = read_table(a, 0, soff, ired);
-  int items = a.S;
-  if (!few) {  // one behind the other
-    const unsigned some = __ballot_sync(kFull, tail >= 0);
-    if (lane == 0) ired[warp] = __popc(some);
-    __syncthreads();
-    const int each = ired[lane];
-    const int before = __reduce_add_sync(kFull, lane < warp ? each : 0);
-    items = __reduce_add_sync(kFull, each);
-    if (tail >= 0) spans[before + __popc(some & lanemask_lt())] = tail;
-    __syncthreads();
+  const int per = (a.tiles + kJoinWarps - 1) / kJoinWarps;
+  const int first = warp * per;
+  const int col = (rank * 32 + lane) * C;
+  // everything is on its way together
+  float x[kShare][2][C];
+  int y[kShare][2][C];
+#pragma unroll
+  for (int i = 0; i < kShare; ++i) {
+    const bool real = i < per && first + i < a.tiles && col < a.E;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const size_t at = static_cast<size_t>(2 * (first + i) + h) * a.stride + col;
+      if (C == 2) {  // the row is padded to four
+        float2 p{0.0f, 0.0f};
+        int2 c{0, 0};
+        if (real) {
+          p = __ldcg(reinterpret_cast<const float2*>(a.slot_p + at));
+          c = __ldcg(reinterpret_cast<const int2*>(a.slot_c + at));
+        }
+        x[i][h][0] = p.x;
+        x[i][h][C - 1] = p.y;
+        y[i][h][0] = c.x;
+        y[i][h][C - 1] = c.y;
+      } else {
+        x[i][h][0] = real ? __ldcg(a.slot_p + at) : 0.0f;
+        y[i][h][0] = real ? __ldcg(a.slot_c + at) : 0;
+      }
+    }
   }
-  const int groups = kJoinWarps / share;  // units of a block at a time
-  const int units = items * a.chunks;
-  for (int n0 = rank * groups; n0 < units; n0 += kCluster * groups) {
-    const int n = n0 + warp / share;
-    int s = a.S, e = a.E;
-    if (n < units) {
-      s = few ? n / a.chunks : min(spans[n / a.chunks], a.S);
-      e = n % a.chunks * 128 + lane * 4;
-    }
-    int2 r = make_int2(0, 0);
-    if (s < a.S) r = a.S <= kOffBatch ? range_of(soff[s], soff[s + 1], a.T) : seq_range(a, s);
-    const int b0 = r.x / a.tile, b1 = r.y > r.x ? (r.y - 1) / a.tile : b0;
-    const bool real = b1 > b0 && e < a.E;
-    float4 p{0.0f, 0.0f, 0.0f, 0.0f};
-    int4 c{0, 0, 0, 0};
-    for (int b = b0 + warp % share; b <= b1 && real; b += kSlots * share) {
-      float4 x[kSlots];
-      int4 y[kSlots];
+  const int full = __ldcg(a.full);
+  float loss = rank == 0 && threadIdx.x < a.tiles ? __ldcg(a.tile_loss + threadIdx.x) : 0.0f;
+  // sequences that go on from a tile in front of the warp's, and from any
+  int f = -1, items = 0;
+  int tails[kShare];
 #pragma unroll
-      for (int i = 0; i < kSlots; ++i) {  // all on their way together
-        const int bi = b + i * share;
-        const size_t at = static_cast<size_t>(2 * bi + (bi == b0)) * a.stride + e;
-        x[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        y[i] = make_int4(0, 0, 0, 0);
-        if (bi <= b1) {
-          x[i] = __ldcg(reinterpret_cast<const float4*>(a.slot_p + at));
-          y[i] = __ldcg(reinterpret_cast<const int4*>(a.slot_c + at));
-        }
-      }
+  for (int i = 0; i < kShare; ++i)
+    tails[i] = i * 32 + lane < a.tiles ? __ldcg(&a.spans[i * 32 + lane].y) : -1;
 #pragma unroll
-      for (int i = 0; i < kSlots; ++i) {
-        p = make_float4(p.x + x[i].x, p.y + x[i].y, p.z + x[i].z, p.w + x[i].w);
-        c = make_int4(c.x + y[i].x, c.y + y[i].y, c.z + y[i].z, c.w + y[i].w);
+  for (int i = 0; i < kShare; ++i) {
+    items += __popc(__ballot_sync(kFull, tails[i] >= 0));
+    f += __popc(__ballot_sync(kFull, tails[i] >= 0 && i * 32 + lane < first));
+  }
+  float p[C];
+  int c[C];
+#pragma unroll
+  for (int k = 0; k < C; ++k) {
+    p[k] = 0.0f;
+    c[k] = 0;
+  }
+  bool some = false;
+  auto keep = [&]() {  // the run of sequence f
+    if (some && f >= 0)
+#pragma unroll
+      for (int k = 0; k < C; ++k) {
+        ps[(warp + f) * (32 * C) + lane * C + k] = p[k];
+        cs[(warp + f) * (32 * C) + lane * C + k] = c[k];
+      }
+  };
+#pragma unroll
+  for (int i = 0; i < kShare; ++i) {
+    if (i >= per || first + i >= a.tiles) break;
+    const int4 span = __ldcg(a.spans + first + i);
+    if (span.x) {
+#pragma unroll
+      for (int k = 0; k < C; ++k) {
+        p[k] += x[i][0][k];
+        c[k] += y[i][0][k];
+      }
+      some = true;
+    }
+    if (span.y >= 0) {
+      keep();
+      ++f;
+#pragma unroll
+      for (int k = 0; k < C; ++k) {
+        p[k] = x[i][1][k];
+        c[k] = y[i][1][k];
+      }
+      some = true;
+      if (lane == 0) {
+        item_seq[f] = span.y;
+        item_length[f] = span.z;
+        item_first[f] = warp;
+        item_last[f] = min(span.w / per, kJoinWarps - 1);
       }
     }
-    if (share > 1) {
-      __syncthreads();
-      ps[warp][lane] = p;
-      cs[warp][lane] = c;
-      __syncthreads();
-      if (warp % share == 0) {
+  }
+  keep();
+  __syncthreads();
+  for (int n = warp; n < items; n += kJoinWarps) {
+    const int s = item_seq[n], tokens = item_length[n];
+#pragma unroll
+    for (int k = 0; k < C; ++k) {
+      p[k] = 0.0f;
+      c[k] = 0;
+    }
 #pragma unroll 4
-        for (int w = 1; w < share; ++w) {
-          const float4 x = ps[warp + w][lane];
-          const int4 y = cs[warp + w][lane];
-          p = make_float4(p.x + x.x, p.y + x.y, p.z + x.z, p.w + x.w);
-          c = make_int4(c.x + y.x, c.y + y.y, c.z + y.z, c.w + y.w);
-        }
-      }
-    }
-    if (real && warp % share == 0) {
-      const int n_tokens = r.y - r.x;
-      const float pe[4] = {p.x, p.y, p.z, p.w}, per_token = 1.0f / n_tokens;
-      const int ce[4] = {c.x, c.y, c.z, c.w};
-      float val = 0.0f;
+    for (int w = item_first[n]; w <= item_last[n]; ++w)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        if (e + i >= a.E) break;
-        const size_t at = static_cast<size_t>(s) * a.E + e + i;
-        a.cnt[at] = ce[i];
-        if (a.prob) a.prob[at] = pe[i] * per_token;
-        val = fmaf(static_cast<float>(ce[i]), pe[i], val);
+      for (int k = 0; k < C; ++k) {
+        p[k] += ps[(w + n) * (32 * C) + lane * C + k];
+        c[k] += cs[(w + n) * (32 * C) + lane * C + k];
       }
-      loss = fmaf(val, seq_factor(a, n_tokens), loss);
-    }
+    float val = 0.0f;
+#pragma unroll
+    for (int k = 0; k < C; ++k)
+      if (col + k < a.E && s < a.S) {
+        const size_t at = static_cast<size_t>(s) * a.E + col + k;
+        a.cnt[at] = c[k];
+        if (a.prob) a.prob[at] = p[k] / tokens;
+        val = fmaf(static_cast<float>(c[k]), p[k], val);
+      }
+    loss = fmaf(val, seq_factor(a, tokens), loss);
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) loss += __shfl_xor_sync(kFull, loss, o);
@@ -646,7 +699,9 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kJoinWarps * 
   asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
   if (threadIdx.x == 0) {
     uint32_t to;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(to) : "r"(smem_addr(block_loss + rank)));
+    asm volatile("mapa.shared::cluster.u32 %0, %1, 0;"
+                 : "=r"(to)
+                 : "r"(smem_addr(block_loss + rank)));
     asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(to), "f"(loss) : "memory");
   }
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
@@ -655,7 +710,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kJoinWarps * 
     loss = 0.0f;
 #pragma unroll
     for (int b = 0; b < kCluster; ++b) loss += block_loss[b];
-    *a.loss = table.full > 0 ? a.coef * loss / table.full : 0.0f;
+    *a.loss = full > 0 ? a.coef * loss / full : 0.0f;
   }
 }
 
@@ -803,7 +858,6 @@ BalArgs bal_args(const moe_handle* h, const float* logits, int T, const int32_t*
   a.E = h->cfg.num_experts;
   a.K = h->cfg.top_k;
   a.S = S;
-  a.chunks = (a.E + 127) / 128;
   a.stride = (a.E + 3) / 4 * 4;
   a.coef = static_cast<float>(coef);
   a.flags = h->flags;
@@ -814,11 +868,17 @@ BalArgs bal_args(const moe_handle* h, const float* logits, int T, const int32_t*
 
 namespace {
 size_t tile_shared(int E) { return static_cast<size_t>(kRows + kFrags) * E * sizeof(float); }
+size_t join_shared(int C) { return static_cast<size_t>(kJoinRows) * 32 * C * 2 * sizeof(float); }
 }  // namespace
 
-// The tile kernels take more shared memory than the default: once for a device.
+// The forward's kernels take more shared memory than the default: once for a device.
 cudaError_t prepare_balance_kernels() {
-  cudaError_t e = cudaSuccess;
+  cudaError_t e = cudaFuncSetAttribute(balance_join_kernel<1>,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       static_cast<int>(join_shared(1)));
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(balance_join_kernel<2>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             static_cast<int>(join_shared(2)));
   for (int E : {8, 16, 32, 64, 128, 256, 384, 512}) {
     if (e != cudaSuccess) return e;
     const int bytes = static_cast<int>(tile_shared(E));
@@ -846,7 +906,8 @@ BalancePlan balance_plan(int E) {
   p.slot_p = take(slots * sizeof(float));
   p.slot_c = take(slots * sizeof(int32_t));
   p.tile_loss = take(kMaxTiles * sizeof(float));
-  p.tail = take(kMaxTiles * sizeof(int32_t));
+  p.spans = take(kMaxTiles * sizeof(int4));
+  p.full = take(sizeof(int32_t));
   p.total = o;
   return p;
 }
@@ -864,7 +925,8 @@ cudaError_t launch_balance(const moe_handle* h, const float* logits, const int32
   a.slot_p = reinterpret_cast<float*>(ws + p.slot_p);
   a.slot_c = reinterpret_cast<int32_t*>(ws + p.slot_c);
   a.tile_loss = reinterpret_cast<float*>(ws + p.tile_loss);
-  a.tail = reinterpret_cast<int32_t*>(ws + p.tail);
+  a.spans = reinterpret_cast<int4*>(ws + p.spans);
+  a.full = reinterpret_cast<int32_t*>(ws + p.full);
   a.vec = rows_vec(a.E, logits);
   // tiles of at least 32 tokens, one to an SM at most; one, and with it one
   // launch, where a block works through all logits in about a second launch's time
@@ -884,12 +946,9 @@ cudaError_t launch_balance(const moe_handle* h, const float* logits, const int32
     return launch_chained(k, dim3(a.tiles), dim3(kThreads), smem, s, false, a);
   });
   if (e != cudaSuccess || a.tiles == 1) return e;
-  // warps of a unit: as many as leave all units in one round
-  const int units = (S < a.tiles ? S : a.tiles) * a.chunks;
-  int share = 1;
-  while (share < kJoinWarps && 2 * share * units <= kCluster * kJoinWarps) share *= 2;
-  return launch_chained(balance_join_kernel, dim3(kCluster), dim3(32 * kJoinWarps), 0, s, false, a,
-                        share);
+  const bool two = a.E > 32 * kCluster;
+  return launch_chained(two ? balance_join_kernel<2> : balance_join_kernel<1>, dim3(kCluster),
+                        dim3(32 * kJoinWarps), join_shared(two ? 2 : 1), s, false, a);
 }
 
 cudaError_t launch_balance_bwd(const moe_handle* h, const float* logits, const int32_t* cnt, int T,

@@ -119,9 +119,9 @@ cudaError_t launch_layer(const moe_handle* h, const moe_layer_args& q, int T, vo
                          cudaStream_t s);
 
 // Workspace of the balance loss: byte offsets of the fragments' sums and counts,
-// the tiles' losses and the sequences that go on from them.
+// the tiles' losses, the sequences that go on from them and the number of sequences.
 struct BalancePlan {
-  size_t slot_p, slot_c, tile_loss, tail, total;
+  size_t slot_p, slot_c, tile_loss, spans, full, total;
 };
 BalancePlan balance_plan(int E);
 cudaError_t prepare_balance_kernels();
