@@ -25,9 +25,9 @@
 // together.
 //
 // us (replayed in a graph, logits from HBM; floor: the bytes at the copy rate): 131072
-// tokens x 512 experts 52.3 (40.8), the DeepSeek-V3 shape (16384 x 256, sigmoid) packed
-// in 9 sequences 14.7 (2.4): 1.2 offsets, 4.6 tiles, 1.5 their sums, 0.5 the hand-over to
-// the second kernel, 6 that one.  Backward of the latter, added to another gradient, 11.5
+// tokens x 512 experts 51.6 (40.8), the DeepSeek-V3 shape (16384 x 256, sigmoid) packed
+// in 9 sequences 13.3 (2.4): 1.2 offsets, 4.7 tiles, 1.5 their sums, 0.5 the hand-over to
+// the second kernel, 4 that one.  Backward of the latter, added to another gradient, 11.5
 // (6.9), of 8192 x 128 3.6 (1.3).
 #include <type_traits>
 
