@@ -1001,6 +1001,33 @@ cudaError_t allow_shared(K k) {
                               static_cast<int>(kShared));
 }
 
+// Resident blocks per SM of a forward kernel.  There are more kernels and sizes here
+// than the table of resident_blocks() holds.
+int forward_blocks(void (*kernel)(NormArgs), int threads, size_t shared) {
+  struct Entry {
+    void (*kernel)(NormArgs);
+    int threads;
+    size_t shared;
+    int per_sm;
+  };
+  static Entry table[64];
+  static int used = 0, next = 0;
+  static std::mutex mu;
+  std::lock_guard<std::mutex> lock(mu);
+  for (int i = 0; i < used; ++i)
+    if (table[i].kernel == kernel && table[i].threads == threads && table[i].shared == shared)
+      return table[i].per_sm;
+  int per_sm = 0;
+  if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, threads, shared) !=
+          cudaSuccess ||
+      per_sm < 1)
+    per_sm = 1;
+  table[next] = Entry{kernel, threads, shared, per_sm};
+  next = (next + 1) % 64;
+  if (used < 64) ++used;
+  return per_sm;
+}
+
 // A kernel, the tokens that it has under way, and its shared memory.
 template <typename A>
 struct Chosen {
@@ -1177,8 +1204,7 @@ cudaError_t launch_block_norm(const moe_handle* h, const moe_block_norm_args& q,
   const auto c = bf16 ? forward_kernel<__nv_bfloat16>(q.H, kmax, threads, rows, weights)
                       : forward_kernel<float>(q.H, kmax, threads, rows, weights);
   const long long most =
-      static_cast<long long>(h->num_sms) *
-      resident_blocks(reinterpret_cast<const void*>(c.kernel), threads, c.shared);
+      static_cast<long long>(h->num_sms) * forward_blocks(c.kernel, threads, c.shared);
   const int blocks = (T - 1) / a.teams + 1;
   const int grid = static_cast<int>(blocks < most ? blocks : most);
   a.units = grid * a.teams;

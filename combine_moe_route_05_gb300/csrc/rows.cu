@@ -583,7 +583,7 @@ int resident_blocks(const void* kernel, int threads, size_t smem) {
     size_t smem;
     int per_sm;
   };
-  static Entry cache[128];
+  static Entry cache[32];
   static int used = 0;
   static std::mutex mu;
   std::lock_guard<std::mutex> lock(mu);
@@ -594,7 +594,7 @@ int resident_blocks(const void* kernel, int threads, size_t smem) {
   if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, threads, smem) != cudaSuccess)
     per_sm = 1;
   if (per_sm < 1) per_sm = 1;
-  if (used < 128) cache[used++] = Entry{kernel, threads, smem, per_sm};
+  if (used < 32) cache[used++] = Entry{kernel, threads, smem, per_sm};
   return per_sm;
 }
 
