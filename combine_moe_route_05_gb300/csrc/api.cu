@@ -124,7 +124,7 @@ bool layer_sizes_ok(const moe_config* c, int32_t H, int32_t I, int32_t num_share
 
 // Sequences of a balance loss: their table, and the factor.
 bool balance_args_ok(const int32_t* off, int32_t S, double coef) {
-  if (S < 1 || (!off && S != 1) || !aligned(off, 4)) return false;
+  if (S < 1 || S > MOE_BALANCE_MAX_SEQS || (!off && S != 1) || !aligned(off, 4)) return false;
   return std::isfinite(static_cast<float>(coef));
 }
 
@@ -498,7 +498,7 @@ moe_status moe_layer(const moe_handle* h, const moe_layer_args* q, int32_t T, vo
 }
 
 size_t moe_balance_workspace_bytes(const moe_config* c, int32_t num_seqs) {
-  if (!config_valid(c) || num_seqs < 1) return 0;
+  if (!config_valid(c) || num_seqs < 1 || num_seqs > MOE_BALANCE_MAX_SEQS) return 0;
   return moe::balance_plan(c->num_experts).total;
 }
 

@@ -933,11 +933,10 @@ cudaError_t launch_balance(const moe_handle* h, const float* logits, const int32
   // (softmax: 256 tokens of 64 experts 5.8 us against 9.6, 512 of 64 7.4 against
   // 9.8, but 512 of 128 10.1 against 9.8)
   int tiles = h->num_sms < kMaxTiles ? h->num_sms : kMaxTiles;
-  if ((T + 31) / 32 < tiles) tiles = (T + 31) / 32;
+  if ((T - 1) / 32 + 1 < tiles) tiles = (T - 1) / 32 + 1;
   if (static_cast<int64_t>(T) * a.E <= 49152) tiles = 1;
-  if (tiles < 1) tiles = 1;
-  a.tile = T > 0 ? (T + tiles - 1) / tiles : 1;
-  a.tiles = T > 0 ? (T + a.tile - 1) / a.tile : 1;
+  a.tile = T > 0 ? (T - 1) / tiles + 1 : 1;
+  a.tiles = T > 0 ? (T - 1) / a.tile + 1 : 1;
   const size_t smem = tile_shared(a.E);
   const bool sigmoid = h->cfg.score_fn == MOE_SCORE_SIGMOID;
   cudaError_t e = with_team(a.E, [&](auto lanes, auto vecs) {

@@ -987,7 +987,7 @@ int team_threads(int H) { return H <= 128 ? 8 : H <= 256 ? 16 : (H + kWarpRow - 
 // Teams of a block for T tokens: as many as it holds, once there is one for every SM.
 int teams_of(int T, int H, int num_sms) {
   const int most = kTeamThreads / team_threads(H);
-  int n = (T + num_sms - 1) / num_sms;
+  int n = (T - 1) / num_sms + 1;
   n = most < 1 || n < 1 ? 1 : n < most ? n : most;
   const int per_warp = 32 / team_threads(H);  // whole warps
   return per_warp > 1 ? (n + per_warp - 1) / per_warp * per_warp : n;
@@ -1151,8 +1151,8 @@ namespace {
 // Units of the backward for T tokens, at least: the workspace of T serves fewer.
 int units_of(int T, int H, int num_sms, int* teams) {
   *teams = teams_of(T, H, num_sms);
-  const int blocks = (T + *teams - 1) / *teams;
-  return *teams * (blocks < 1 ? 1 : blocks < num_sms ? blocks : num_sms);
+  const int blocks = (T - 1) / *teams + 1;
+  return *teams * (blocks < num_sms ? blocks : num_sms);
 }
 }  // namespace
 

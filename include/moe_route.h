@@ -549,6 +549,7 @@ moe_status moe_layer(const moe_handle* h, const moe_layer_args* args, int32_t T,
  *   d_seq_off int32 [num_seqs + 1] on the device: sequence s is tokens
  *     d_seq_off[s] <= t < d_seq_off[s + 1]; NULL: one sequence of all T tokens
  *     (num_seqs = 1).  Tokens before the first or behind the last are not read.
+ *     num_seqs is at most MOE_BALANCE_MAX_SEQS.
  *     Offsets that fall or lie outside [0,T] are flagged (MOE_DEVERR_BAD_LAYOUT)
  *     and the results unspecified.
  *   d_loss fp32 [1], d_cnt int32 [num_seqs, E], d_prob fp32 [num_seqs, E].
@@ -557,6 +558,8 @@ moe_status moe_layer(const moe_handle* h, const moe_layer_args* args, int32_t T,
  * free after the call's work; calls that may overlap on the GPU need one each.
  * The handle's layout is neither read nor changed.
  */
+#define MOE_BALANCE_MAX_SEQS (1 << 30)
+
 size_t moe_balance_workspace_bytes(const moe_config* c, int32_t num_seqs);
 
 moe_status moe_balance(const moe_handle* h, const float* d_logits, const int32_t* d_idx, int32_t T,

@@ -157,6 +157,16 @@ def test_sizes_and_null_handles_are_refused_without_a_gpu():
     assert L.moe_block_norm_bwd(None, ctypes.byref(b), 4, A, 1 << 30, None) == moe.MOE_ERR_INVALID
 
 
+def test_sequences_of_a_balance_loss_are_limited():
+    """The kernels count sequences in steps of a grid, in 32 bits."""
+    import combine_moe_route_05_gb300 as moe
+    cfg = moe.make_config(64, 4, 1, 128)
+    most = 1 << 30
+    assert moe.moe_balance_workspace_bytes(cfg, most) > 0
+    for S in (most + 1, 2 ** 31 - 1, -1):
+        assert moe.moe_balance_workspace_bytes(cfg, S) == 0
+
+
 def test_structs_match_the_header():
     """Field order and types of the binding's structs are the header's."""
     import os

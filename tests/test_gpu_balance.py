@@ -402,3 +402,18 @@ def test_refusals():
             call()
     torch.cuda.synchronize()
     assert moe.moe_read_device_status(h) == 0
+
+
+def test_too_many_sequences_are_refused():
+    p = Problem(64, 8, 2, "softmax")
+    h, L = p.r.h, moe.lib()
+    l, i, o = to_dev(p.logits), to_dev(p.idx), to_dev(p.off)
+    loss, gl = torch.zeros(1, device=dev()), torch.zeros(64, 8, device=dev())
+    cnt = torch.zeros(1, 8, dtype=torch.int32, device=dev())
+    ws = moe.balance_workspace(h, 1)
+    for S in ((1 << 30) + 1, 2 ** 31 - 1):
+        assert L.moe_balance(h.ptr, l.data_ptr(), i.data_ptr(), 64, o.data_ptr(), S, 1.0,
+                             loss.data_ptr(), cnt.data_ptr(), None, ws.data_ptr(), ws.numel(),
+                             None) == moe.MOE_ERR_INVALID
+        assert L.moe_balance_bwd(h.ptr, l.data_ptr(), cnt.data_ptr(), 64, o.data_ptr(), S, 1.0,
+                                 None, None, gl.data_ptr(), None) == moe.MOE_ERR_INVALID
