@@ -928,13 +928,14 @@ cudaError_t launch_balance(const moe_handle* h, const float* logits, const int32
   a.spans = reinterpret_cast<int4*>(ws + p.spans);
   a.full = reinterpret_cast<int32_t*>(ws + p.full);
   a.vec = rows_vec(a.E, logits);
-  // tiles of at least 32 tokens, one to an SM at most; one, and with it one
-  // launch, where a block works through all logits in about a second launch's time
-  // (softmax: 256 tokens of 64 experts 5.8 us against 9.6, 512 of 64 7.4 against
-  // 9.8, but 512 of 128 10.1 against 9.8)
+  // tiles of at least 32 tokens, one to an SM at most; one, and with it one launch,
+  // where a block works through all tokens in less than a second launch's time: a
+  // token costs it as much as 8 logits and its own (us, softmax, against two launches:
+  // 1536 tokens of 8 experts 5.9 and 8.1, 6144 of 8 11.2 and 8.9, 384 of 64 7.4 and
+  // 8.5, 768 of 64 9.3 and 8.6, 12288 of 4 17.8 and 8.9)
   int tiles = h->num_sms < kMaxTiles ? h->num_sms : kMaxTiles;
   if ((T - 1) / 32 + 1 < tiles) tiles = (T - 1) / 32 + 1;
-  if (static_cast<int64_t>(T) * a.E <= 49152) tiles = 1;
+  if (static_cast<int64_t>(T) * (a.E + 8) <= 45056) tiles = 1;
   a.tile = T > 0 ? (T - 1) / tiles + 1 : 1;
   a.tiles = T > 0 ? (T - 1) / a.tile + 1 : 1;
   const size_t smem = tile_shared(a.E);
