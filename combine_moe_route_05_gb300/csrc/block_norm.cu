@@ -583,12 +583,15 @@ enum GateKind { kNoGate, kGateRows, kGateGroups };
 // AHEAD as in the forward.  With room for one token alone, its vectors are asked for
 // in two parts, each as soon as that of the token before is used up (fp32 rows of
 // 7168: 98.6 -> 65.6 us for 2048 tokens); with more, at the token's end (sooner,
-// between its two sums, took 232 instead of 222 us at the DeepSeek-V3 shape).
+// between its two sums, took 232 instead of 222 us at the DeepSeek-V3 shape).  -1: as
+// 0, and the group's gate row, for which there is no room beside its product with
+// w_post, is read again at the group's end (fp32 rows of more than 14336).
 template <typename Elt, GateKind GATE, bool WARP, int MAXT, int AHEAD>
 __global__ void __launch_bounds__(MAXT, 1) block_norm_bwd_kernel(NormBwdArgs a) {
   using PT = PairTraits<Elt>;
   constexpr int P = PT::P, N = 2 * P, V = kEpt / N, ROWS = GATE == kGateRows ? 5 : 4;
   constexpr bool PARTS = AHEAD == 1;
+  constexpr bool KEPT_GATE = AHEAD >= 0;  // of a group
   enum { GRes, Gx, ResOut, C, Gate };
   __shared__ __align__(16) float red[kRed];
   extern __shared__ __align__(16) uint8_t shared[];
@@ -601,7 +604,7 @@ __global__ void __launch_bounds__(MAXT, 1) block_norm_bwd_kernel(NormBwdArgs a) 
   const uint32_t wpre = wpost + kWeightSlots * wb;
   // of a group: the gate's row, and its product with w_post
   const uint32_t gate_row = smem_addr(shared) + threadIdx.x * 16 + 2 * kWeightSlots * wb;
-  const uint32_t gate_w = gate_row + V * sb;
+  const uint32_t gate_w = gate_row + (KEPT_GATE ? V * sb : 0);
   const uint32_t ring = GATE == kGateGroups ? gate_w + kWeightSlots * sb : gate_row;
   bool in[V];    // vectors inside the row, and where
   int at[V];
@@ -688,7 +691,7 @@ __global__ void __launch_bounds__(MAXT, 1) block_norm_bwd_kernel(NormBwdArgs a) 
         if (a.gx) r_pre = __ldg(a.rstd_pre + t + 1);
         if (a.w_post) r_post = __ldg(a.rstd_post + t + 1);
       }
-      if (AHEAD > 0) wait_copies<PARTS ? 1 : AHEAD - 1>();
+      if constexpr (AHEAD > 0) wait_copies<PARTS ? 1 : AHEAD - 1>();
       F2 D[V][P], h[V][P];
       if (a.gx) {
         F2 s = 0;
@@ -747,7 +750,7 @@ __global__ void __launch_bounds__(MAXT, 1) block_norm_bwd_kernel(NormBwdArgs a) 
           }
           F2 g[P], w[P];
           PT::to(x, g);
-          st_shared(gate_row + i * sb, x);
+          if (KEPT_GATE) st_shared(gate_row + i * sb, x);
           if (a.w_post) {
             kept_weights<N>(wpost, wb, i, w);
 #pragma unroll
@@ -815,7 +818,7 @@ __global__ void __launch_bounds__(MAXT, 1) block_norm_bwd_kernel(NormBwdArgs a) 
         for (int i = 0; i < V; ++i)
           if (in[i]) st_vec(a.gy + row + at[i], PT::from(D[i]));
       }
-      if (AHEAD > 0) {
+      if constexpr (AHEAD > 0) {
         if (end - t > AHEAD) fetch(!PARTS, true, row + AHEAD * a.row_bytes, stage);
         commit_copies();
         stage += token;
@@ -831,7 +834,10 @@ __global__ void __launch_bounds__(MAXT, 1) block_norm_bwd_kernel(NormBwdArgs a) 
           for (int i = 0; i < V; ++i) {
             if (a.w_post) {
               F2 g[P], w[P];
-              PT::to(ld_shared(gate_row + i * sb), g);
+              Vec16 x{};
+              if (KEPT_GATE) x = ld_shared(gate_row + i * sb);
+              else if (in[i]) x = ld_vec(a.gate + group * a.row_bytes + at[i]);
+              PT::to(x, g);
               kept_weights<N>(wpost, wb, i, w);
 #pragma unroll
               for (int j = 0; j < P; ++j) {
@@ -1072,8 +1078,10 @@ Chosen<NormArgs> forward_kernel(int H, int kmax, int threads, int rows, int weig
                      : forward_kernel<Elt, 16>(H, kept, token, kShared);
 }
 
+// `gate`: bytes of a group's gate row among `kept`; with them the widest rows need
+// more than a block has, and do without.
 template <typename Elt, GateKind GATE, bool WARP, int MAXT>
-Chosen<NormBwdArgs> backward_within(size_t kept, size_t token, size_t most) {
+Chosen<NormBwdArgs> backward_within(size_t kept, size_t gate, size_t token, size_t most) {
   if constexpr (MAXT < 1024) {
     if (kept + 3 * token <= most)
       return {block_norm_bwd_kernel<Elt, GATE, WARP, MAXT, 3>, 3, kept + 3 * token};
@@ -1082,22 +1090,36 @@ Chosen<NormBwdArgs> backward_within(size_t kept, size_t token, size_t most) {
   }
   if (kept + token <= most)
     return {block_norm_bwd_kernel<Elt, GATE, WARP, MAXT, 1>, 1, kept + token};
+  if constexpr (GATE == kGateGroups && MAXT == 1024 && sizeof(Elt) == 4) {
+    // the widest rows: both weights and the product alone fit
+    static_assert(static_cast<size_t>(MAXT) * 16 * 3 * kWeightSlots <= kShared,
+                  "a block's weights and its gate's product with them");
+    if (kept > most) return {block_norm_bwd_kernel<Elt, GATE, WARP, MAXT, -1>, -1, kept - gate};
+  } else {
+    // both weights, and with groups a gate row and its product with one
+    static_assert(static_cast<size_t>(MAXT) *
+                          (16 * 2 * kWeightSlots +
+                           (GATE == kGateGroups ? kEpt * (sizeof(Elt) + sizeof(float)) : 0)) <=
+                      kShared,
+                  "what a block keeps");
+  }
   return {block_norm_bwd_kernel<Elt, GATE, WARP, MAXT, 0>, 0, kept};
 }
 template <typename Elt, GateKind GATE>
-Chosen<NormBwdArgs> backward_fitting(int H, size_t kept, size_t token, size_t most) {
-  return one_warp(H) ? backward_within<Elt, GATE, true, kTeamThreads>(kept, token, most)
+Chosen<NormBwdArgs> backward_fitting(int H, size_t kept, size_t gate, size_t token, size_t most) {
+  return one_warp(H) ? backward_within<Elt, GATE, true, kTeamThreads>(kept, gate, token, most)
          : team_threads(H) <= kTeamThreads
-             ? backward_within<Elt, GATE, false, kTeamThreads>(kept, token, most)
-             : backward_within<Elt, GATE, false, 1024>(kept, token, most);
+             ? backward_within<Elt, GATE, false, kTeamThreads>(kept, gate, token, most)
+             : backward_within<Elt, GATE, false, 1024>(kept, gate, token, most);
 }
 template <typename Elt, GateKind GATE>
 Chosen<NormBwdArgs> backward_kernel(int H, int threads) {
   size_t kept = kept_bytes(H, 2);
+  const size_t row = GATE == kGateGroups ? token_bytes<Elt>(threads, 1) : 0;
   if (GATE == kGateGroups)  // a gate row and 16 fp32 a thread
-    kept += token_bytes<Elt>(threads, 1) + static_cast<size_t>(threads) * kEpt * sizeof(float);
+    kept += row + static_cast<size_t>(threads) * kEpt * sizeof(float);
   auto c = backward_fitting<Elt, GATE>(
-      H, kept, token_bytes<Elt>(threads, GATE == kGateRows ? 5 : 4), kShared);
+      H, kept, row, token_bytes<Elt>(threads, GATE == kGateRows ? 5 : 4), kShared);
   // the teams' sums meet there as well
   const size_t meet = kept + static_cast<size_t>(threads) * kEpt * sizeof(float);
   if (threads > team_threads(H) && c.shared < meet) c.shared = meet;
@@ -1117,15 +1139,17 @@ cudaError_t allow_all() {
   auto allow = [&](const auto& c) {
     if (e == cudaSuccess) e = allow_shared(c.kernel);
   };
-  for (int H : {kWarpRow, kTeamThreads * kEpt, 1024 * kEpt})
+  for (int H : {kWarpRow, kTeamThreads * kEpt, 1024 * kEpt}) {
+    allow(backward_fitting<Elt, kGateGroups>(H, 1, 0, 1, 0));  // not for the gate row either
     for (size_t fit = 0; fit <= 3; ++fit) {  // tokens that there is room for
       allow(forward_kernel<Elt, 1>(H, 0, 1, fit));
       allow(forward_kernel<Elt, 8>(H, 0, 1, fit));
       allow(forward_kernel<Elt, 16>(H, 0, 1, fit));
-      allow(backward_fitting<Elt, kNoGate>(H, 0, 1, fit));
-      allow(backward_fitting<Elt, kGateRows>(H, 0, 1, fit));
-      allow(backward_fitting<Elt, kGateGroups>(H, 0, 1, fit));
+      allow(backward_fitting<Elt, kNoGate>(H, 0, 0, 1, fit));
+      allow(backward_fitting<Elt, kGateRows>(H, 0, 0, 1, fit));
+      allow(backward_fitting<Elt, kGateGroups>(H, 0, 0, 1, fit));
     }
+  }
   return e;
 }
 

@@ -545,3 +545,14 @@ def test_a_training_step_of_a_block(score, pad):
     for got, name in ((gres0, "res"), (gwr, "wr"), (gw0, "w0"), (gwpost, "wpost"), (gw1, "w1"),
                       (ggate, "gate")):
         close(got, P[name].grad, name)
+
+
+@pytest.mark.parametrize("post", [True, False])
+@pytest.mark.parametrize("gate", [2, 5, 10 ** 6])
+@pytest.mark.parametrize("T,H", [(3, 14340), (330, 14336), (330, 14340), (330, 16384)])
+def test_widest_fp32_rows_with_a_gate_of_groups(T, H, gate, post):
+    """Weights, the gate's row and its product with them do not all fit into a
+    block's shared memory from 14340 on."""
+    p = Problem(T, H, "f32", "f32", gate=gate, post=post, seed=H + gate)
+    p.check_forward()
+    p.check_backward()
