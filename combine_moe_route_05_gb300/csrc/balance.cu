@@ -201,7 +201,7 @@ __device__ __forceinline__ float probabilities(float (&v)[4 * NV], float (&q)[4 
     for (int i = 0; i < N; ++i) {
       m = fmaxf(m, v[i]);
       const float e = exp_fast(-v[i]), s = reciprocal(1.0f + e);
-      if (GRAD) q[i] = s * (fminf(e, 1e30f) * s);  // 1 - s = e s
+      if (GRAD) q[i] = s * fminf(e * s, 1.0f);  // 1 - s = e s; 1 where e is infinite (inf * 0)
       v[i] = s;
       z += s;
     }

@@ -417,3 +417,22 @@ def test_too_many_sequences_are_refused():
                              None) == moe.MOE_ERR_INVALID
         assert L.moe_balance_bwd(h.ptr, l.data_ptr(), cnt.data_ptr(), 64, o.data_ptr(), S, 1.0,
                                  None, None, gl.data_ptr(), None) == moe.MOE_ERR_INVALID
+
+
+@pytest.mark.parametrize("E", [8, 24, 256])
+@pytest.mark.parametrize("top", [0.0, -15.0, 30.0])
+def test_slopes_of_sigmoids_far_below_the_rows_largest(top, E):
+    """One expert at `top`, the others at -69 to -87: their slope is their sigmoid
+    itself, within the bound of every other logit.  coef keeps the gradient above
+    fp32's smallest normal value."""
+    p = Problem(6, E, 2, "sigmoid", seed=E)
+    g = np.random.default_rng(E)
+    p.logits[:] = g.uniform(-87.0, -69.0, p.logits.shape)
+    p.logits[np.arange(6), g.integers(0, E, 6)] = top
+    cnt = to_dev(g.integers(0, 7, (1, E)).astype(np.int32))
+    got = to_host(p.backward(cnt, coef=1e6)).astype(np.float64)
+    want, bound = ref.balance_bwd(p.logits, to_host(cnt), p.off, 2, "sigmoid", 1e6)
+    assert (np.abs(want) > 1e3 * ref.TINY).mean() > 0.5
+    bad = ~(np.abs(got - want) <= bound + ref.TINY)
+    assert not bad.any(), "%d of %d out of bound, worst ratio %.3g" % (
+        bad.sum(), bad.size, (np.abs(got - want) / (bound + ref.TINY)).max())
