@@ -6,9 +6,9 @@
 // S' the sequences that are not empty.  With the counts constant,
 //   dloss/dl_tj = coef / S' * E / (K n_s^2) * q_tj (c_sj - sum_e c_se p_te),
 // q = p for softmax, sigma (1 - sigma) / sum(sigma) for sigmoid.  Since p sums
-// to 1, a constant can be taken off the counts: the backward takes the mean
-// count off as an integer, exactly, so that the difference of two near-equal
-// sums of counts never loses digits.
+// to 1, a constant can be taken off the counts: the backward takes about
+// their mean off as an integer, exactly, so that the gradient of an even router is made of
+// small differences, not of near-equal sums of counts.
 //
 // Forward: tokens are cut into equal tiles, one block each.  A tile's part of a
 // sequence is a fragment.  A sequence inside one tile is finished there; the
@@ -756,6 +756,8 @@ __global__ void __launch_bounds__(kBwdWarps * 32, kBwdBlocks<NV>) balance_bwd_ke
   if (begin >= end) return;
   int2 r = make_int2(0, 0);
   float d[N], factor = 0.0f;  // counts less their mean; the sequence's factor
+  const unsigned mates = kFull >> (32 - LPT) << team * LPT;  // the team's lanes
+  const float inv_e = 1.0f / static_cast<float>(a.E);
   // the sequence of token t, for tokens in order: most often the next one
   int s = -1;
   auto enter = [&](int t) {
@@ -777,7 +779,18 @@ __global__ void __launch_bounds__(kBwdWarps * 32, kBwdBlocks<NV>) balance_bwd_ke
     int c[N];
     load_row<LPT, NV, int4>(a.bcnt + static_cast<size_t>(s) * a.E, a.E, a.vec, true, tl, 0, c);
     const int n = r.y - r.x;
-    const int mean = static_cast<int>(static_cast<int64_t>(a.K) * n / a.E);
+    // their mean as they are, since entries without an expert are not in them; a
+    // team enters together, and max_tokens * K fits into 31 bits
+    unsigned sum = 0;
+#pragma unroll
+    for (int i = 0; i < N; ++i) sum += c[i];
+    if (LPT == 32) {
+      sum = __reduce_add_sync(kFull, sum);
+    } else {
+#pragma unroll
+      for (int o = LPT / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(mates, sum, o);
+    }
+    const int mean = __float2int_rn(static_cast<float>(sum) * inv_e);
 #pragma unroll
     for (int i = 0; i < N; ++i) d[i] = static_cast<float>(c[i] - mean);
     factor = n > 0 ? g * seq_factor(a, n) : 0.0f;

@@ -419,6 +419,25 @@ def test_too_many_sequences_are_refused():
                                  None, None, gl.data_ptr(), None) == moe.MOE_ERR_INVALID
 
 
+def gradient_of_one_sequence(logits, cnt, T, K, score, coef):
+    """(gradient, bound) of some tokens of one sequence of T, whatever its counts.
+    A constant m may be taken off the counts, as p sums to 1: with d = c - m the
+    gradient is B q (d - sum p d).  A relative error r of p and q makes one of at
+    most r B q (|d| + sum p |d|) of it, and so do the additions: the bound of
+    block_ref.balance_bwd, whose m is K T / E.  The counts' own mean, as here, is
+    that if no entry was dropped; where some were, or where the counts are any
+    numbers, another m would leave a part of |m| in d and in the error."""
+    E = logits.shape[1]
+    p, q, _ = ref.probabilities(logits, score)
+    c = cnt.astype(np.float64)
+    d = c - np.rint(c.mean())
+    B = coef * E / (K * float(T) ** 2)
+    want = B * q * (d - (p * d).sum(1, keepdims=True))
+    away = np.abs(d) + (p * np.abs(d)).sum(1, keepdims=True)
+    rel = 2 * ref.probability_error(logits, score) + (16 + ref.TREE) * ref.U32
+    return want, abs(B) * q * away * rel
+
+
 @pytest.mark.parametrize("E", [8, 24, 256])
 @pytest.mark.parametrize("top", [0.0, -15.0, 30.0])
 def test_slopes_of_sigmoids_far_below_the_rows_largest(top, E):
@@ -431,8 +450,28 @@ def test_slopes_of_sigmoids_far_below_the_rows_largest(top, E):
     p.logits[np.arange(6), g.integers(0, E, 6)] = top
     cnt = to_dev(g.integers(0, 7, (1, E)).astype(np.int32))
     got = to_host(p.backward(cnt, coef=1e6)).astype(np.float64)
-    want, bound = ref.balance_bwd(p.logits, to_host(cnt), p.off, 2, "sigmoid", 1e6)
+    want, bound = gradient_of_one_sequence(p.logits, to_host(cnt)[0], 6, 2, "sigmoid", 1e6)
     assert (np.abs(want) > 1e3 * ref.TINY).mean() > 0.5
     bad = ~(np.abs(got - want) <= bound + ref.TINY)
     assert not bad.any(), "%d of %d out of bound, worst ratio %.3g" % (
         bad.sum(), bad.size, (np.abs(got - want) / (bound + ref.TINY)).max())
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("T,E,K", [(400000, 8, 2), (400000, 100, 16), (100000, 384, 16)])
+def test_gradient_of_even_counts_with_dropped_entries(T, E, K, score):
+    """A long sequence whose counts differ by some tens, 30% of its entries dropped:
+    the gradient, which is made of those differences, keeps their digits."""
+    r = moe.MoeRouter(E, K, 1, T, score_fn=score)
+    g = torch.Generator(device="cuda").manual_seed(E)
+    logits = torch.randn(T, E, generator=g, device="cuda")
+    even = K * T * 7 // (E * 10)
+    cnt = (even + torch.randint(-20, 21, (1, E), generator=g, device="cuda")).to(torch.int32)
+    glogits = torch.empty_like(logits)
+    moe.moe_balance_bwd(r.h, logits, cnt, glogits, coef=1.0)
+    for rows in (slice(0, 1000), slice(T - 1000, T)):
+        l, got = to_host(logits[rows]), to_host(glogits[rows]).astype(np.float64)
+        want, bound = gradient_of_one_sequence(l, to_host(cnt)[0], T, K, score, 1.0)
+        bad = ~(np.abs(got - want) <= bound + ref.TINY)
+        assert not bad.any(), "%d of %d out of bound, worst ratio %.3g" % (
+            bad.sum(), bad.size, (np.abs(got - want) / (bound + ref.TINY)).max())
