@@ -823,7 +823,7 @@ __global__ void __launch_bounds__(kBwdWarps * 32, kBwdBlocks<NV>) balance_bwd_ke
 #pragma unroll
     for (int i = 0; i < N; ++i) dot = fmaf(v[i], live ? d[i] : 0.0f, dot);
     dot = team_sum<LPT>(dot) * inv;
-    const float scale = factor * inv;
+    const float scale = inv > 0.0f ? factor * inv : 0.0f;  // an infinite factor, too
     if (!live) continue;
 #pragma unroll
     for (int i = 0; i < N; ++i) o[i] = fmaf(scale * (SIGMOID ? q[i] : v[i]), d[i] - dot, o[i]);

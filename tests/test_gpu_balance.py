@@ -475,3 +475,21 @@ def test_gradient_of_even_counts_with_dropped_entries(T, E, K, score):
         bad = ~(np.abs(got - want) <= bound + ref.TINY)
         assert not bad.any(), "%d of %d out of bound, worst ratio %.3g" % (
             bad.sum(), bad.size, (np.abs(got - want) / (bound + ref.TINY)).max())
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("gloss", [np.inf, -np.inf, np.nan])
+def test_tokens_without_probabilities_get_the_base_whatever_the_gradient(gloss, score):
+    """A scaled loss whose gradient overflowed spoils the tokens that have a part in
+    the loss, no others."""
+    p = Problem(300, 24, 2, score, seed=5)
+    p.logits[30:40] = -np.inf
+    p.logits[7, 5] = np.nan
+    p.logits[299, 23] = np.inf
+    none = np.zeros(300, bool)
+    none[[7, 299]] = none[30:40] = True
+    _, cnt, _ = p.forward()
+    for in_place in (False, True):
+        got = to_host(p.backward(cnt, gloss=gloss, base=p.base, in_place=in_place))
+        assert np.array_equal(got[none], p.base[none])
+        assert not np.isfinite(got[~none]).any()
