@@ -3,6 +3,7 @@
 // is made here, before anything is launched; a failed check launches nothing.
 #include <cmath>
 #include <cstdint>
+#include <mutex>
 #include <new>
 
 #include "internal.h"
@@ -148,6 +149,23 @@ bool on_handle_device(const moe_handle* h) {
 
 namespace moe {
 bool valid_config(const moe_config* c) { return config_valid(c); }
+
+cudaError_t allow_shared_at_launch(const moe_handle* h, const void* kernel, size_t bytes) {
+  struct Entry {
+    const void* kernel;
+    int device;
+  };
+  static Entry done[512];
+  static int used = 0;
+  static std::mutex mu;
+  std::lock_guard<std::mutex> lock(mu);
+  for (int i = 0; i < used; ++i)
+    if (done[i].kernel == kernel && done[i].device == h->device) return cudaSuccess;
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             static_cast<int>(bytes));
+  if (e == cudaSuccess && used < 512) done[used++] = Entry{kernel, h->device};
+  return e;
+}
 }  // namespace moe
 
 extern "C" {
@@ -186,8 +204,6 @@ moe_status moe_handle_create(const moe_config* c, void* d_workspace, size_t work
   if (moe::prepare_layout_kernels() != cudaSuccess) return MOE_ERR_CUDA;
   if (moe::prepare_w2_kernel() != cudaSuccess) return MOE_ERR_CUDA;
   if (moe::prepare_layer_kernels() != cudaSuccess) return MOE_ERR_CUDA;
-  if (moe::prepare_balance_kernels() != cudaSuccess) return MOE_ERR_CUDA;
-  if (moe::prepare_block_norm_kernels() != cudaSuccess) return MOE_ERR_CUDA;
 
   uint8_t* ws = static_cast<uint8_t*>(d_workspace);
   if (cudaMemset(ws, 0, p.S + sizeof(int32_t)) != cudaSuccess) return MOE_ERR_CUDA;

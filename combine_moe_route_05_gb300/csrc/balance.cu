@@ -884,29 +884,6 @@ size_t tile_shared(int E) { return static_cast<size_t>(kRows + kFrags) * E * siz
 size_t join_shared(int C) { return static_cast<size_t>(kJoinRows) * 32 * C * 2 * sizeof(float); }
 }  // namespace
 
-// The forward's kernels take more shared memory than the default: once for a device.
-cudaError_t prepare_balance_kernels() {
-  cudaError_t e = cudaFuncSetAttribute(balance_join_kernel<1>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       static_cast<int>(join_shared(1)));
-  if (e == cudaSuccess)
-    e = cudaFuncSetAttribute(balance_join_kernel<2>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             static_cast<int>(join_shared(2)));
-  for (int E : {8, 16, 32, 64, 128, 256, 384, 512}) {
-    if (e != cudaSuccess) return e;
-    const int bytes = static_cast<int>(tile_shared(E));
-    e = with_team(E, [&](auto lanes, auto vecs) {
-      cudaError_t r = cudaFuncSetAttribute(balance_tile_kernel<lanes(), vecs(), false>,
-                                           cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-      if (r == cudaSuccess)
-        r = cudaFuncSetAttribute(balance_tile_kernel<lanes(), vecs(), true>,
-                                 cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-      return r;
-    });
-  }
-  return e;
-}
-
 BalancePlan balance_plan(int E) {
   BalancePlan p{};
   size_t o = 0;
@@ -956,12 +933,18 @@ cudaError_t launch_balance(const moe_handle* h, const float* logits, const int32
   cudaError_t e = with_team(a.E, [&](auto lanes, auto vecs) {
     auto k = sigmoid ? balance_tile_kernel<lanes(), vecs(), true>
                      : balance_tile_kernel<lanes(), vecs(), false>;
+    const cudaError_t r = allow_shared_at_launch(h, reinterpret_cast<const void*>(k),
+                                                 tile_shared(MOE_MAX_EXPERTS));
+    if (r != cudaSuccess) return r;
     return launch_chained(k, dim3(a.tiles), dim3(kThreads), smem, s, false, a);
   });
   if (e != cudaSuccess || a.tiles == 1) return e;
   const bool two = a.E > 32 * kCluster;
-  return launch_chained(two ? balance_join_kernel<2> : balance_join_kernel<1>, dim3(kCluster),
-                        dim3(32 * kJoinWarps), join_shared(two ? 2 : 1), s, false, a);
+  auto join = two ? balance_join_kernel<2> : balance_join_kernel<1>;
+  const size_t join_smem = join_shared(two ? 2 : 1);
+  e = allow_shared_at_launch(h, reinterpret_cast<const void*>(join), join_smem);
+  if (e != cudaSuccess) return e;
+  return launch_chained(join, dim3(kCluster), dim3(32 * kJoinWarps), join_smem, s, false, a);
 }
 
 cudaError_t launch_balance_bwd(const moe_handle* h, const float* logits, const int32_t* cnt, int T,

@@ -999,14 +999,6 @@ int teams_of(int T, int H, int num_sms) {
   return per_warp > 1 ? (n + per_warp - 1) / per_warp * per_warp : n;
 }
 
-// Largest dynamic shared memory for a kernel that takes more than the default.
-template <typename K>
-cudaError_t allow_shared(K k) {
-  return cudaFuncSetAttribute(reinterpret_cast<const void*>(k),
-                              cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              static_cast<int>(kShared));
-}
-
 // Resident blocks per SM of a forward kernel.  There are more kernels and sizes here
 // than the table of resident_blocks() holds.
 int forward_blocks(void (*kernel)(NormArgs), int threads, size_t shared) {
@@ -1132,46 +1124,6 @@ Chosen<NormBwdArgs> backward_kernel(GateKind gate, int H, int threads) {
                              : backward_kernel<Elt, kGateGroups>(H, threads);
 }
 
-// Shared memory for every kernel that the choices above can make.
-template <typename Elt>
-cudaError_t allow_all() {
-  cudaError_t e = cudaSuccess;
-  auto allow = [&](const auto& c) {
-    if (e == cudaSuccess) e = allow_shared(c.kernel);
-  };
-  for (int H : {kWarpRow, kTeamThreads * kEpt, 1024 * kEpt}) {
-    allow(backward_fitting<Elt, kGateGroups>(H, 1, 0, 1, 0));  // not for the gate row either
-    for (size_t fit = 0; fit <= 3; ++fit) {  // tokens that there is room for
-      allow(forward_kernel<Elt, 1>(H, 0, 1, fit));
-      allow(forward_kernel<Elt, 8>(H, 0, 1, fit));
-      allow(forward_kernel<Elt, 16>(H, 0, 1, fit));
-      allow(backward_fitting<Elt, kNoGate>(H, 0, 0, 1, fit));
-      allow(backward_fitting<Elt, kGateRows>(H, 0, 0, 1, fit));
-      allow(backward_fitting<Elt, kGateGroups>(H, 0, 0, 1, fit));
-    }
-  }
-  return e;
-}
-
-}  // namespace
-
-// Once for a device: the first call of a process loads the kernels.
-cudaError_t prepare_block_norm_kernels() {
-  static std::mutex mu;
-  static uint64_t done[4];  // a bit a device
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  std::lock_guard<std::mutex> lock(mu);
-  uint64_t* word = dev < 256 ? done + dev / 64 : nullptr;
-  if (word && (*word >> (dev % 64) & 1)) return cudaSuccess;
-  e = allow_all<__nv_bfloat16>();
-  if (e == cudaSuccess) e = allow_all<float>();
-  if (e == cudaSuccess && word) *word |= uint64_t{1} << (dev % 64);
-  return e;
-}
-
-namespace {
 // Units of the backward for T tokens, at least: the workspace of T serves fewer.
 int units_of(int T, int H, int num_sms, int* teams) {
   *teams = teams_of(T, H, num_sms);
@@ -1227,6 +1179,9 @@ cudaError_t launch_block_norm(const moe_handle* h, const moe_block_norm_args& q,
   const int weights = (a.w_post != nullptr) + (a.w_pre != nullptr);
   const auto c = bf16 ? forward_kernel<__nv_bfloat16>(q.H, kmax, threads, rows, weights)
                       : forward_kernel<float>(q.H, kmax, threads, rows, weights);
+  const cudaError_t e =
+      allow_shared_at_launch(h, reinterpret_cast<const void*>(c.kernel), kShared);
+  if (e != cudaSuccess) return e;
   const long long most =
       static_cast<long long>(h->num_sms) * forward_blocks(c.kernel, threads, c.shared);
   const int blocks = (T - 1) / a.teams + 1;
@@ -1278,8 +1233,9 @@ cudaError_t launch_block_norm_bwd(const moe_handle* h, const moe_block_norm_bwd_
   const auto k = bf16 ? backward_kernel<__nv_bfloat16>(gate, q.H, threads)
                       : backward_kernel<float>(gate, q.H, threads);
   if (T > 0) {
-    const cudaError_t e =
-        launch_chained(k.kernel, dim3(a.blocks), dim3(threads), k.shared, s, false, a);
+    cudaError_t e = allow_shared_at_launch(h, reinterpret_cast<const void*>(k.kernel), kShared);
+    if (e == cudaSuccess)
+      e = launch_chained(k.kernel, dim3(a.blocks), dim3(threads), k.shared, s, false, a);
     if (e != cudaSuccess) return e;
   }
   const bool spans = a.ggate && a.gate_tokens > 1 && a.chunk % a.gate_tokens != 0;
