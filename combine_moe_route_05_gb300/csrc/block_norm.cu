@@ -1043,14 +1043,38 @@ size_t token_bytes(int threads, int rows) {
   return static_cast<size_t>(threads) * kEpt * sizeof(Elt) * rows;
 }
 
-// The kernel with the most tokens under way whose shared memory fits into `most`.
-template <typename Elt, int KMAX, bool WARP, int MAXT>
+// Kernels are made for rows of one warp, for those of up to 512 threads, where a block
+// holds as many teams, and for wider ones, whose narrowest has 544.  With a class's
+// most and least bytes of what a block keeps and of a token's rows, a kernel is left
+// out where one with more tokens under way fits any of its rows, or where it fits none.
+struct Bytes {
+  size_t kept, token;
+  constexpr bool fit(int tokens) const { return kept + tokens * token <= kShared; }
+};
+template <typename Elt>
+constexpr Bytes class_bytes(int team, int threads, int weights, int rows, bool groups) {
+  const size_t t = threads, row = kEpt * sizeof(Elt);
+  return {static_cast<size_t>(team) * 16 * kWeightSlots * weights +
+              (groups ? t * (row + kEpt * sizeof(float)) : 0),
+          t * row * rows};
+}
+constexpr int kWideThreads = kTeamThreads + 32;
+
+// The kernel with the most tokens under way, AHEAD at most, whose shared memory fits
+// into `most`.
+template <typename Elt, int KMAX, bool WARP, int MAXT, int AHEAD = KMAX == 1 && MAXT < 1024 ? 2 : 1>
 Chosen<NormArgs> forward_within(size_t kept, size_t token, size_t most) {
-  if constexpr (KMAX == 1 && MAXT < 1024)
-    if (kept + 2 * token <= most)
-      return {block_norm_kernel<Elt, KMAX, WARP, MAXT, 2>, 2, kept + 2 * token};
-  if (kept + token <= most) return {block_norm_kernel<Elt, KMAX, WARP, MAXT, 1>, 1, kept + token};
-  return {block_norm_kernel<Elt, KMAX, WARP, MAXT, 0>, 0, kept};
+  constexpr auto largest = class_bytes<Elt>(WARP ? 32 : MAXT, MAXT, 2, KMAX + 3, false);
+  constexpr auto least =
+      class_bytes<Elt>(0, MAXT == 1024 ? kWideThreads : 8, 0, KMAX == 16 ? 10 : 1, false);
+  if constexpr (AHEAD == 0 || (AHEAD == 1 && largest.fit(1))) {
+    return {block_norm_kernel<Elt, KMAX, WARP, MAXT, AHEAD>, AHEAD, kept + AHEAD * token};
+  } else {
+    if constexpr (least.fit(AHEAD))
+      if (kept + AHEAD * token <= most)
+        return {block_norm_kernel<Elt, KMAX, WARP, MAXT, AHEAD>, AHEAD, kept + AHEAD * token};
+    return forward_within<Elt, KMAX, WARP, MAXT, AHEAD - 1>(kept, token, most);
+  }
 }
 template <typename Elt, int KMAX>
 Chosen<NormArgs> forward_kernel(int H, size_t kept, size_t token, size_t most) {
@@ -1072,37 +1096,33 @@ Chosen<NormArgs> forward_kernel(int H, int kmax, int threads, int rows, int weig
 
 // `gate`: bytes of a group's gate row among `kept`; with them the widest rows need
 // more than a block has, and do without.
-template <typename Elt, GateKind GATE, bool WARP, int MAXT>
-Chosen<NormBwdArgs> backward_within(size_t kept, size_t gate, size_t token, size_t most) {
-  if constexpr (MAXT < 1024) {
-    if (kept + 3 * token <= most)
-      return {block_norm_bwd_kernel<Elt, GATE, WARP, MAXT, 3>, 3, kept + 3 * token};
-    if (kept + 2 * token <= most)
-      return {block_norm_bwd_kernel<Elt, GATE, WARP, MAXT, 2>, 2, kept + 2 * token};
-  }
-  if (kept + token <= most)
-    return {block_norm_bwd_kernel<Elt, GATE, WARP, MAXT, 1>, 1, kept + token};
-  if constexpr (GATE == kGateGroups && MAXT == 1024 && sizeof(Elt) == 4) {
-    // the widest rows: both weights and the product alone fit
-    static_assert(static_cast<size_t>(MAXT) * 16 * 3 * kWeightSlots <= kShared,
-                  "a block's weights and its gate's product with them");
-    if (kept > most) return {block_norm_bwd_kernel<Elt, GATE, WARP, MAXT, -1>, -1, kept - gate};
+template <typename Elt, GateKind GATE, bool WARP, int MAXT, int AHEAD = MAXT < 1024 ? 3 : 1>
+Chosen<NormBwdArgs> backward_within(size_t kept, size_t gate, size_t token) {
+  constexpr int rows = GATE == kGateRows ? 5 : 4;
+  constexpr bool groups = GATE == kGateGroups;
+  constexpr auto largest = class_bytes<Elt>(WARP ? 32 : MAXT, MAXT, 2, rows, groups);
+  constexpr auto least = MAXT == 1024
+                             ? class_bytes<Elt>(kWideThreads, kWideThreads, 2, rows, groups)
+                             : class_bytes<Elt>(8, 8, 2, rows, groups);
+  if constexpr (AHEAD < 0) {
+    static_assert(groups && largest.kept - MAXT * kEpt * sizeof(Elt) <= kShared,
+                  "both weights and the gate's product with one");
+    return {block_norm_bwd_kernel<Elt, GATE, WARP, MAXT, AHEAD>, AHEAD, kept - gate};
+  } else if constexpr (largest.fit(AHEAD)) {
+    return {block_norm_bwd_kernel<Elt, GATE, WARP, MAXT, AHEAD>, AHEAD, kept + AHEAD * token};
   } else {
-    // both weights, and with groups a gate row and its product with one
-    static_assert(static_cast<size_t>(MAXT) *
-                          (16 * 2 * kWeightSlots +
-                           (GATE == kGateGroups ? kEpt * (sizeof(Elt) + sizeof(float)) : 0)) <=
-                      kShared,
-                  "what a block keeps");
+    if constexpr (least.fit(AHEAD))
+      if (kept + AHEAD * token <= kShared)
+        return {block_norm_bwd_kernel<Elt, GATE, WARP, MAXT, AHEAD>, AHEAD, kept + AHEAD * token};
+    return backward_within<Elt, GATE, WARP, MAXT, AHEAD - 1>(kept, gate, token);
   }
-  return {block_norm_bwd_kernel<Elt, GATE, WARP, MAXT, 0>, 0, kept};
 }
 template <typename Elt, GateKind GATE>
-Chosen<NormBwdArgs> backward_fitting(int H, size_t kept, size_t gate, size_t token, size_t most) {
-  return one_warp(H) ? backward_within<Elt, GATE, true, kTeamThreads>(kept, gate, token, most)
+Chosen<NormBwdArgs> backward_fitting(int H, size_t kept, size_t gate, size_t token) {
+  return one_warp(H) ? backward_within<Elt, GATE, true, kTeamThreads>(kept, gate, token)
          : team_threads(H) <= kTeamThreads
-             ? backward_within<Elt, GATE, false, kTeamThreads>(kept, gate, token, most)
-             : backward_within<Elt, GATE, false, 1024>(kept, gate, token, most);
+             ? backward_within<Elt, GATE, false, kTeamThreads>(kept, gate, token)
+             : backward_within<Elt, GATE, false, 1024>(kept, gate, token);
 }
 template <typename Elt, GateKind GATE>
 Chosen<NormBwdArgs> backward_kernel(int H, int threads) {
@@ -1111,7 +1131,7 @@ Chosen<NormBwdArgs> backward_kernel(int H, int threads) {
   if (GATE == kGateGroups)  // a gate row and 16 fp32 a thread
     kept += row + static_cast<size_t>(threads) * kEpt * sizeof(float);
   auto c = backward_fitting<Elt, GATE>(
-      H, kept, row, token_bytes<Elt>(threads, GATE == kGateRows ? 5 : 4), kShared);
+      H, kept, row, token_bytes<Elt>(threads, GATE == kGateRows ? 5 : 4));
   // the teams' sums meet there as well
   const size_t meet = kept + static_cast<size_t>(threads) * kEpt * sizeof(float);
   if (threads > team_threads(H) && c.shared < meet) c.shared = meet;
