@@ -556,3 +556,42 @@ def test_widest_fp32_rows_with_a_gate_of_groups(T, H, gate, post):
     p = Problem(T, H, "f32", "f32", gate=gate, post=post, seed=H + gate)
     p.check_forward()
     p.check_backward()
+
+
+@pytest.mark.parametrize("T,H,dtype", [(70, 96, "f32"), (700, 2056, "bf16"), (40, 9000, "bf16")])
+def test_the_kept_sum_in_place_of_what_is_added_or_of_the_block(T, H, dtype):
+    for K, add in ((3, True), (0, True), (0, False)):
+        p = Problem(T, H, dtype, K=K, add=add, gate=9)
+        want = p.forward()
+        for name in ("add",) * add + ("y",) * (K == 0):
+            kept = getattr(p, name)
+            setattr(p, name, kept.clone())
+            o = {k: torch.empty_like(v) for k, v in want.items()}
+            o["c"] = getattr(p, name)
+            moe.moe_block_norm(p.r.h, p.res, y=p.y, gather=K > 0, cw=p.cw, add=p.add, eps=EPS, **o,
+                               **p.shared())
+            assert all(torch.equal(o[k], want[k]) for k in o), name
+            setattr(p, name, kept)
+
+
+@pytest.mark.parametrize("gate", [0, 1, 7, 300])
+@pytest.mark.parametrize("T,H,dtype", [(300, 96, "bf16"), (300, 1036, "f32"), (300, 16384, "f32")])
+def test_each_output_alone(T, H, dtype, gate):
+    p = Problem(T, H, dtype, gate=gate)
+    want = p.saved()
+    o = dict.fromkeys(want)
+    o["res_out"] = torch.empty_like(p.res)
+    for alone in ("res_out", "x", "c", "rstd_post", "rstd_pre"):
+        q = dict(o, **{alone: torch.empty_like(want[alone])})
+        if alone == "rstd_pre":
+            q["x"] = torch.empty_like(want["x"])
+        kw = p.shared()
+        if q["x"] is None:
+            kw["w_pre"] = None
+        moe.moe_block_norm(p.r.h, p.res, y=p.y, eps=EPS, **q, **kw)
+        assert all(torch.equal(v, want[k]) for k, v in q.items() if v is not None), alone
+    grads = p.backward(want)
+    for alone in grads:
+        if grads[alone] is not None:
+            got = p.backward(want, dict(dict.fromkeys(grads), **{alone: torch.empty_like(grads[alone])}))
+            assert torch.equal(got[alone], grads[alone]), alone
