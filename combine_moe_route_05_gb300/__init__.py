@@ -920,7 +920,8 @@ class MoeRouter:
                    stream=None):
         """The norms around a block (see moe_block_norm): (res_out, x, saved).
         res_out is None without y, x without w_pre; saved (None without `save`):
-        what block_norm_bwd needs, a dict."""
+        what block_norm_bwd needs, a dict.  It holds y itself where nothing was summed
+        or added, and res itself without y: not to be written over until then."""
         T = res.shape[0]
         with torch.cuda.stream(stream):
             res_out = torch.empty_like(res) if y is not None else None

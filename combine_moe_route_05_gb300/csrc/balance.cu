@@ -27,8 +27,8 @@
 // us (replayed in a graph, logits from HBM; floor: the bytes at the copy rate): 131072
 // tokens x 512 experts 51.6 (40.8), the DeepSeek-V3 shape (16384 x 256, sigmoid) packed
 // in 9 sequences 13.3 (2.4): 1.2 offsets, 4.7 tiles, 1.5 their sums, 0.5 the hand-over to
-// the second kernel, 4 that one.  Backward of the latter, added to another gradient, 11.5
-// (6.9), of 8192 x 128 3.6 (1.3).
+// the second kernel, 4 that one.  Backward of the latter, added to another gradient, 11.6
+// (6.9), of 8192 x 128 3.7 (1.3).
 #include <type_traits>
 
 #include "common.cuh"
@@ -49,8 +49,9 @@ constexpr int kJoinWarps = 32;   // of a block of the second kernel
 constexpr int kCluster = 8;      // blocks of the second kernel
 constexpr int kShare = kMaxTiles / kJoinWarps;  // tiles of one of its warps
 constexpr int kJoinRows = kJoinWarps + kMaxTiles;
-// Tokens a team sums in registers before it adds them to shared memory: bounds
-// the number of fp32 additions in a row however long a tile is.
+// Tokens a team sums in registers before it adds them to shared memory.  A sum then
+// has 64 + T / (64 * warps of the grid * teams of a warp) + 70 fp32 additions in a row:
+// 135 for 131072 tokens of 512 experts, under 1100 for any logits that fit into 284 GB.
 constexpr int kFlush = 64;
 constexpr float kInf = __builtin_huge_valf();
 
@@ -184,7 +185,7 @@ __device__ __forceinline__ float exponentials(float (&v)[N], bool& infinite) {
 // Turns a team's logits v into v = p * z and, for the backward of sigmoids, q =
 // (see the top) * z, and returns 1 / z.  A logit of -inf is an expert that is
 // masked out: p = q = 0.  A row without any other is 0, and so is one with a NaN
-// or +inf, which returns `bad`.  exp is the fast one: its error, 2 + |x| ulp, falls
+// or +inf, which returns `bad`.  exp is the fast one: its error, 2 + 1.2 |x| ulp, falls
 // for the softmax on values that are e^x of the row's largest.  `again` loads v
 // once more, for a row (`live`) whose sigmoids are all far below 1: those are e^l
 // to 1e-9, and normalised from the row's largest they cannot vanish together.
@@ -714,9 +715,11 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kJoinWarps * 
   }
 }
 
-// Blocks of the backward an SM: registers for four but with the widest rows, a token
-// a warp at a time.  Two tokens at a time on three blocks took 12.9 against 11.5 us
-// (DeepSeek-V3 shape, packed) and 4.2 against 3.6 (Qwen3-30B shape).
+// Blocks of the backward an SM: four but with the widest rows, a token a warp at a
+// time.  Two tokens at a time on three blocks took 12.9 against 11.5 us (DeepSeek-V3
+// shape, packed) and 4.2 against 3.6 (Qwen3-30B shape).  The 64 registers of four blocks
+// (80 of three) are short for sigmoids: 28 bytes spill at 9 to 128 experts, 84 with three
+// vectors a lane (257 to 384), where three blocks have not been tried, 96 with four.
 template <int NV>
 constexpr int kBwdBlocks = NV < 4 ? 4 : 3;
 
@@ -922,7 +925,10 @@ cudaError_t launch_balance(const moe_handle* h, const float* logits, const int32
   // where a block works through all tokens in less than a second launch's time: a
   // token costs it as much as 8 logits and its own (us, softmax, against two launches:
   // 1536 tokens of 8 experts 5.9 and 8.1, 6144 of 8 11.2 and 8.9, 384 of 64 7.4 and
-  // 8.5, 768 of 64 9.3 and 8.6, 12288 of 4 17.8 and 8.9)
+  // 8.5, 768 of 64 9.3 and 8.6, 12288 of 4 17.8 and 8.9).  These are of one sequence; the
+  // rule counts neither sequences nor the score, and the one block works on 16 sequences
+  // at a time, 11 us each time: 2800 tokens of 8 take 8 us in one sequence, 43 in 64,
+  // 1970 in 2800
   int tiles = h->num_sms < kMaxTiles ? h->num_sms : kMaxTiles;
   if ((T - 1) / 32 + 1 < tiles) tiles = (T - 1) / 32 + 1;
   if (static_cast<int64_t>(T) * (a.E + 8) <= 45056) tiles = 1;

@@ -539,7 +539,9 @@ moe_status moe_layer(const moe_handle* h, const moe_layer_args* args, int32_t T,
  * over the tokens t of s; S' = sequences that are not empty (a loss of 0 if
  * there is none).  p is over all E experts, whatever groups, renorm, scale and
  * bias the routing has.  fp32, sums in a fixed order: the same inputs give the
- * same bits.
+ * same bits.  e^x is the fast one, off by up to 2 + 1.2 |x| units in the last place (2^-23
+ * of its value): x is a logit's distance from its row's largest (softmax), or the
+ * logit itself (sigmoid).
  *   d_logits [T,E] fp32, d_idx [T,K] int32 as in moe_route_topk.  An entry of
  *     -1 is no expert; any other index outside [0,E) (MOE_DEVERR_BAD_EXPERT) and
  *     a token's repeated expert (MOE_DEVERR_DUP_EXPERT) are flagged and not
@@ -575,7 +577,8 @@ moe_status moe_balance(const moe_handle* h, const float* d_logits, const int32_t
  * d_cnt is the forward's.  d_gloss fp32 [1] on the device (the gradient of the
  * loss; NULL: 1), d_base [T,E] fp32 (a gradient to add to, for example that of
  * moe_route_bwd; NULL: 0), which may be d_glogits.  Rows of tokens outside the
- * sequences are not written.  Tokens without p (see above) get d_base alone.
+ * sequences are not written.  Tokens without p (see above) get d_base alone, also of
+ * a *d_gloss that is not finite.
  */
 moe_status moe_balance_bwd(const moe_handle* h, const float* d_logits, const int32_t* d_cnt,
                            int32_t T, const int32_t* d_seq_off, int32_t num_seqs, double coef,
